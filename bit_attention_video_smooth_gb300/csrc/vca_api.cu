@@ -19,6 +19,34 @@ bool shape_ok(int B, int H, int N, int d) {
     return BH <= 65535 && BH * N <= (static_cast<int64_t>(1) << 31) - 1;   // BH is a grid y extent
 }
 
+bool aligned4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+// The cache's sizes and pointers; `view` gets them in the kernels' form.
+bool cache_ok(const vca_cache *c, vca::CacheView *view) {
+    const int64_t most = (static_cast<int64_t>(1) << 31) - 1;
+    if (!c || c->d != 128 || c->pages < 1 || c->H < 1 || c->B < 1 || c->cols < 1) return false;
+    if (static_cast<int64_t>(c->B) * c->H > 65535 || static_cast<int64_t>(c->cols) * 128 > most) return false;
+    if (static_cast<int64_t>(c->pages) * c->H > most / 128) return false;
+    if (!c->k8 || !c->v8 || !aligned16(c->k8) || !aligned16(c->v8)) return false;
+    const void *ptrs[] = {c->sk, c->sv, c->table, c->len};
+    for (const void *p : ptrs)
+        if (!p || !aligned4(p)) return false;
+    *view = vca::CacheView{c->k8, c->v8, c->sk, c->sv, c->table, c->len, c->pages, c->H, c->B, c->cols};
+    return true;
+}
+bool rows_ok(const uint16_t *p, int64_t tok, int64_t head) {
+    return p && aligned16(p) && (tok & 7) == 0 && (head & 7) == 0;
+}
+bool query_sizes_ok(int T, int Hq, int H) {
+    return T >= 0 && Hq >= 1 && H >= 1 && Hq % H == 0 && static_cast<int64_t>(T) * Hq <= (static_cast<int64_t>(1) << 31) - 1;
+}
+bool scores_ok(int causal, float softmax_scale, float softcap) {
+    return (causal == 0 || causal == 1) && std::isfinite(softmax_scale) && std::isfinite(softcap) && softcap >= 0.0f;
+}
+float scale_or_default(float softmax_scale) {
+    return softmax_scale > 0.0f ? softmax_scale : static_cast<float>(1.0 / std::sqrt(128.0));
+}
+
 int from_cuda(cudaError_t e) { return e == cudaSuccess ? VCA_OK : VCA_ERR_CUDA; }
 
 }  // namespace
@@ -125,6 +153,73 @@ int vca_attention(const uint8_t *q8, const float *sq, const uint8_t *k8, const f
     a.wait_limit_ns = g_wait_limit_ns;
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
     return from_cuda(vmode == VCA_V_NVFP4 ? vca::launch_attention_nvfp4(a, st) : vca::launch_attention(a, st));
+}
+
+size_t vca_cache_workspace_bytes(int op, int T, int Hq, int H, int B, int cols) {
+    if (!query_sizes_ok(T, Hq, H) || T < 1 || B < 1 || cols < 1 || static_cast<int64_t>(B) * H > 65535 ||
+        static_cast<int64_t>(cols) * 128 > (static_cast<int64_t>(1) << 31) - 1)
+        return 0;
+    switch (op) {
+        case VCA_OP_CACHE_ATTENTION: return vca::cache_attention_workspace(T, Hq, H, B, cols);
+        case VCA_OP_CACHE_WEIGH: return vca::cache_weigh_workspace(T, Hq, H, B, cols);
+        default: return 0;
+    }
+}
+
+int vca_cache_append(const vca_cache *cache, const uint16_t *K, int64_t k_token, int64_t k_head, const uint16_t *V,
+                     int64_t v_token, int64_t v_head, const int32_t *start, int T, int32_t *dev_status, void *stream) {
+    vca::CacheView c;
+    if (!cache_ok(cache, &c) || T < 0 || !start || !aligned4(start) || !aligned4(dev_status)) return VCA_ERR_INVALID_ARG;
+    if (T == 0) return VCA_OK;
+    if (!rows_ok(K, k_token, k_head) || !rows_ok(V, v_token, v_head)) return VCA_ERR_INVALID_ARG;
+    return from_cuda(vca::launch_cache_append(c, vca::CacheRows{K, k_token, k_head}, vca::CacheRows{V, v_token, v_head},
+                                              start, T, dev_status, static_cast<cudaStream_t>(stream)));
+}
+
+int vca_cache_attention(const vca_cache *cache, const uint16_t *Q, int64_t q_token, int64_t q_head,
+                        const int32_t *start, int T, int Hq, int causal, float softmax_scale, float softcap,
+                        uint16_t *O, float *lse, void *ws, size_t ws_bytes, int32_t *dev_status, void *stream) {
+    vca::CacheView c;
+    if (!cache_ok(cache, &c) || !query_sizes_ok(T, Hq, c.H) || !scores_ok(causal, softmax_scale, softcap))
+        return VCA_ERR_INVALID_ARG;
+    if (!start || !aligned4(start) || !aligned4(lse) || !aligned4(dev_status)) return VCA_ERR_INVALID_ARG;
+    if (T == 0) return VCA_OK;
+    if (!rows_ok(Q, q_token, q_head) || !O || !aligned16(O)) return VCA_ERR_INVALID_ARG;
+    const size_t need = vca::cache_attention_workspace(T, Hq, c.H, c.B, c.cols);
+    if (need && (!ws || ws_bytes < need || !aligned16(ws))) return VCA_ERR_WORKSPACE;
+    vca::CacheAttnArgs a{c, vca::CacheRows{Q, q_token, q_head}, start, T, Hq, causal, scale_or_default(softmax_scale),
+                         softcap, O, lse, ws, dev_status, g_wait_limit_ns};
+    return from_cuda(vca::launch_cache_attention(a, static_cast<cudaStream_t>(stream)));
+}
+
+int vca_cache_weigh(const vca_cache *cache, const uint16_t *Q, int64_t q_token, int64_t q_head, const int32_t *start,
+                    int T, int Hq, int causal, float softmax_scale, float softcap, const float *lse, float *weight,
+                    void *ws, size_t ws_bytes, int32_t *dev_status, void *stream) {
+    vca::CacheView c;
+    if (!cache_ok(cache, &c) || !query_sizes_ok(T, Hq, c.H) || !scores_ok(causal, softmax_scale, softcap))
+        return VCA_ERR_INVALID_ARG;
+    if (!start || !aligned4(start) || !aligned4(dev_status)) return VCA_ERR_INVALID_ARG;
+    if (T == 0) return VCA_OK;
+    if (!rows_ok(Q, q_token, q_head) || !lse || !aligned4(lse) || !weight || !aligned16(weight)) return VCA_ERR_INVALID_ARG;
+    const size_t need = vca::cache_weigh_workspace(T, Hq, c.H, c.B, c.cols);
+    if (need && (!ws || ws_bytes < need || !aligned16(ws))) return VCA_ERR_WORKSPACE;
+    vca::CacheWeighArgs a{c, vca::CacheRows{Q, q_token, q_head}, start, T, Hq, causal, scale_or_default(softmax_scale),
+                          softcap, lse, weight, ws, dev_status, g_wait_limit_ns};
+    return from_cuda(vca::launch_cache_weigh(a, static_cast<cudaStream_t>(stream)));
+}
+
+int vca_cache_evict(const vca_cache *cache, float *weight, const int32_t *dst_table, int dst_cols, int budget,
+                    int recent, int32_t *new_len, int32_t *kept, int32_t *dev_status, void *stream) {
+    vca::CacheView c;
+    if (!cache_ok(cache, &c) || budget < 1 || recent < 0 || recent > budget || dst_cols < 1 ||
+        static_cast<int64_t>(dst_cols) * 128 < budget)
+        return VCA_ERR_INVALID_ARG;
+    if (!weight || !aligned16(weight) || !aligned4(dev_status)) return VCA_ERR_INVALID_ARG;
+    const void *ptrs[] = {dst_table, new_len, kept};
+    for (const void *p : ptrs)
+        if (!p || !aligned4(p)) return VCA_ERR_INVALID_ARG;
+    return from_cuda(vca::launch_cache_evict(c, weight, dst_table, dst_cols, budget, recent, new_len, kept, dev_status,
+                                             static_cast<cudaStream_t>(stream)));
 }
 
 int vca_expcast_codes(const float *s_raw, const float *c, const float *m, int64_t n, uint8_t *out, void *stream) {

@@ -1,0 +1,351 @@
+// vca_cache.cu -- writing the 8-bit cache: new K/V rows into pages (append) and
+// the tokens that stay after an eviction into fresh pages (evict).
+//
+// A page of one head has one scale s, a power of two with max|x| <= 448 s, so
+// x / s is exact and an E4M3 code keeps its significant bits when the scale
+// grows: only values that become subnormal round again.
+#include "vca_cache.cuh"
+
+namespace vca {
+
+namespace {
+
+using namespace cache;
+
+constexpr int kThreads = 256;
+constexpr int kRowsPerPass = kThreads / 16;         // 16 threads a row, 8 channels each
+constexpr int kPasses = kBlk / kRowsPerPass;
+
+// Eight codes of eight fp32 values times inv (a power of two: exact above the
+// subnormal codes).
+__device__ __forceinline__ uint2 encode8(const float (&x)[8], float inv) {
+    float y[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) y[i] = scaled_or_nan(x[i], inv);
+    return make_uint2(e4m3x4(y[0], y[1], y[2], y[3]), e4m3x4(y[4], y[5], y[6], y[7]));
+}
+// The values of eight codes at scale s: exact, the smallest (2^-9 2^-120) as a
+// subnormal.
+__device__ __forceinline__ void decode8(const uint2 &w, float s, float (&x)[8]) {
+    float a[4], b[4];
+    e4m3x4_decode(w.x, a);
+    e4m3x4_decode(w.y, b);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        x[i] = __fmul_rn(a[i], s);
+        x[4 + i] = __fmul_rn(b[i], s);
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Append: one CTA per (page that gets new rows, head, K or V)
+// ---------------------------------------------------------------------------
+struct AppendParams {
+    CacheView c;
+    CacheRows k, v;
+    const int32_t *start;
+    int T;
+    int32_t *dev_status;
+};
+
+__global__ void __launch_bounds__(kThreads) append_kernel(const AppendParams p) {
+    __shared__ int s_at[4];                 // sequence, page column, its first new row (of the call), page
+    __shared__ uint32_t red[kThreads / 32];
+    const int lane = threadIdx.x & 31;
+    if (threadIdx.x < 32) {
+        // the blockIdx.x-th page that gets new rows, counted over the sequences in order
+        int before = 0, found = -1;
+        const bool reports = blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0;
+        if (lane == 0) s_at[0] = -1;
+        for (int b0 = 0; b0 < p.c.B && (found < 0 || reports); b0 += 32) {
+            const int b = b0 + lane;
+            int cnt = 0, first = 0;
+            Seq s{0, 0, 0, false};
+            if (b < p.c.B) {
+                s = load_seq(p.c, p.start, p.T, b);
+                if (s.n > s.len) s.bad = true;      // the cache's length counts the new rows
+                if (reports && s.bad) report(p.dev_status, kErrInvalid);
+                first = s.len - s.n;
+                if (!s.bad && s.n > 0) cnt = (s.len - 1) / kBlk - first / kBlk + 1;
+            }
+            int incl = cnt;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int y = __shfl_up_sync(0xffffffffu, incl, o);
+                if (lane >= o) incl += y;
+            }
+            const int j = static_cast<int>(blockIdx.x) - before - (incl - cnt);
+            if (found < 0 && j >= 0 && j < cnt) {
+                const int col = first / kBlk + j;
+                s_at[1] = col;
+                s_at[2] = s.row0 - first;           // row of slot t: t + s_at[2]
+                s_at[3] = first;
+                s_at[0] = b;
+            }
+            found = __ballot_sync(0xffffffffu, j >= 0 && j < cnt) != 0 ? 1 : found;
+            before += __shfl_sync(0xffffffffu, incl, 31);
+        }
+    }
+    __syncthreads();
+    const int b = s_at[0];
+    if (b < 0) return;
+    const int col = s_at[1], shift = s_at[2], first = s_at[3], h = blockIdx.y;
+    const int page = load_page(p.c, b, col, p.dev_status);
+    if (page < 0) return;
+    const bool is_v = blockIdx.z != 0;
+    const CacheRows x = is_v ? p.v : p.k;
+    uint8_t *codes = (is_v ? p.c.v8 : p.c.k8) + (static_cast<int64_t>(page) * p.c.H + h) * (kBlk * kD);
+    float *scale = (is_v ? p.c.sv : p.c.sk) + static_cast<int64_t>(page) * p.c.H + h;
+    const int lo = max(first - col * kBlk, 0), hi = min(p.c.len[b] - col * kBlk, kBlk);   // new slots of this page
+    const int r = threadIdx.x >> 4, ch = (threadIdx.x & 15) * 8;
+
+    uint4 v[kPasses];
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < kPasses; ++i) {
+        const int slot = r + i * kRowsPerPass;
+        v[i] = make_uint4(0, 0, 0, 0);
+        if (slot >= lo && slot < hi)
+            v[i] = *reinterpret_cast<const uint4 *>(x.p + (col * kBlk + slot + shift) * x.tok + h * x.head + ch);
+    }
+#pragma unroll
+    for (int i = 0; i < kPasses; ++i) m = max(m, amax_bf16x8(v[i]));
+    const float s_old = lo > 0 ? *scale : 0.0f;
+    const uint32_t sb = max(scale_bits(block_max<kThreads>(m, red)), __float_as_uint(s_old) & 0x7f800000u);
+    const float inv = pow2_inverse(sb);
+    if (threadIdx.x == 0) *scale = __uint_as_float(sb);
+#pragma unroll
+    for (int i = 0; i < kPasses; ++i) {
+        const int slot = r + i * kRowsPerPass;
+        if (slot < lo || slot >= hi) continue;
+        float f[8];
+        const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            f[2 * e] = __uint_as_float(w[e] << 16);
+            f[2 * e + 1] = __uint_as_float(w[e] & 0xffff0000u);
+        }
+        *reinterpret_cast<uint2 *>(codes + slot * kD + ch) = encode8(f, inv);
+    }
+    // the scale grew: the codes that were there move with it
+    if (lo > 0 && __uint_as_float(sb) != s_old) {
+        for (int slot = r; slot < lo; slot += kRowsPerPass) {
+            uint2 *at = reinterpret_cast<uint2 *>(codes + slot * kD + ch);
+            float f[8];
+            decode8(*at, s_old, f);
+            *at = encode8(f, inv);
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Evict
+// ---------------------------------------------------------------------------
+struct EvictParams {
+    CacheView c;
+    float *weight;
+    const int32_t *dst;
+    int dst_cols, budget, recent;
+    int32_t *new_len, *kept, *dev_status;
+};
+
+// Unsigned keys in the order of the weights; NaN counts as the lowest, -0 as 0.
+__device__ __forceinline__ uint32_t weight_key(float w) {
+    uint32_t u = __float_as_uint(w);
+    if ((u & 0x7fffffffu) > 0x7f800000u) u = 0xff800000u;
+    if (u == 0x80000000u) u = 0u;
+    return (u >> 31) ? ~u : (u | 0x80000000u);
+}
+
+constexpr int kSelThreads = 1024;
+
+// One CTA per (sequence, head): the key of the last weight that stays, by a
+// radix select over four bytes, then the slots that stay, in order.
+__global__ void __launch_bounds__(kSelThreads) select_kernel(const EvictParams p) {
+    __shared__ int hist[256];
+    __shared__ int s_bin, s_left;
+    __shared__ int wsum[2][kSelThreads / 32];
+    const int h = blockIdx.x, b = blockIdx.y, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    int len = p.c.len[b];
+    if (len < 0 || len > static_cast<int64_t>(p.c.cols) * kBlk) {
+        if (tid == 0) report(p.dev_status, kErrInvalid);
+        len = 0;
+    }
+    const int stay = min(len, p.budget), recent = min(min(len, p.recent), stay);
+    if (h == 0 && tid == 0) p.new_len[b] = stay;
+    const int older = len - recent, want = stay - recent;
+    int32_t *kept = p.kept + (static_cast<int64_t>(b) * p.c.H + h) * p.budget;
+    for (int j = tid; j < recent; j += kSelThreads) kept[want + j] = older + j;
+    if (want == 0) return;
+    auto key_of = [&](int t) -> uint32_t {
+        const int page = p.c.table[static_cast<int64_t>(b) * p.c.cols + t / kBlk];
+        if (page < 0 || page >= p.c.pages) {
+            report(p.dev_status, kErrInvalid);
+            return 0u;
+        }
+        return weight_key(p.weight[(static_cast<int64_t>(page) * p.c.H + h) * kBlk + t % kBlk]);
+    };
+    uint32_t prefix = 0, mask = 0;
+    int left = want;               // how many of those whose key starts with `prefix` stay
+    for (int shift = 24; shift >= 0; shift -= 8) {
+        if (tid < 256) hist[tid] = 0;
+        __syncthreads();
+        for (int t = tid; t < older; t += kSelThreads) {
+            const uint32_t k = key_of(t);
+            if ((k & mask) == prefix) atomicAdd(&hist[(k >> shift) & 255], 1);
+        }
+        __syncthreads();
+        if (warp == 0) {
+            // bins from the top: lane i holds bins 255 - 8 i .. 248 - 8 i
+            int c[8], s = 0;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) s += c[e] = hist[255 - 8 * lane - e];
+            int incl = s;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int y = __shfl_up_sync(0xffffffffu, incl, o);
+                if (lane >= o) incl += y;
+            }
+            int above = incl - s;
+            if (above < left && left <= incl) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    if (above < left && left <= above + c[e]) {
+                        s_bin = 255 - 8 * lane - e;
+                        s_left = left - above;
+                    }
+                    above += c[e];
+                }
+            }
+        }
+        __syncthreads();
+        prefix |= static_cast<uint32_t>(s_bin) << shift;
+        mask |= 255u << shift;
+        left = s_left;
+        __syncthreads();
+    }
+    // keys above `prefix` stay, and the first `left` of those equal to it
+    int done = 0, ties = 0;
+    for (int t0 = 0; t0 < older; t0 += kSelThreads) {
+        const int t = t0 + tid;
+        const uint32_t k = t < older ? key_of(t) : 0u;
+        const bool gt = t < older && k > prefix, eq = t < older && k == prefix;
+        const uint32_t bg = __ballot_sync(0xffffffffu, gt), be = __ballot_sync(0xffffffffu, eq);
+        if (lane == 0) {
+            wsum[0][warp] = __popc(bg);
+            wsum[1][warp] = __popc(be);
+        }
+        __syncthreads();
+        int g0 = 0, e0 = 0, gt_all = 0, eq_all = 0;
+        for (int i = 0; i < kSelThreads / 32; ++i) {
+            const int a = wsum[0][i], c = wsum[1][i];
+            if (i < warp) {
+                g0 += a;
+                e0 += c;
+            }
+            gt_all += a;
+            eq_all += c;
+        }
+        const uint32_t below = (1u << lane) - 1u;
+        g0 += __popc(bg & below);
+        e0 += __popc(be & below);
+        // kept so far: everything above, plus the ties among the first `left`
+        const int tie = ties + e0;
+        if (gt || (eq && tie < left)) kept[done + g0 + min(tie, left) - min(ties, left)] = t;
+        done += gt_all + min(ties + eq_all, left) - min(ties, left);
+        ties += eq_all;
+        __syncthreads();
+    }
+}
+
+// One CTA per (page that is written, head, K or V) of a sequence.
+__global__ void __launch_bounds__(kThreads) move_kernel(const EvictParams p) {
+    __shared__ uint32_t red[kThreads / 32];
+    __shared__ int s_page[kBlk], s_slot[kBlk];
+    const int col = blockIdx.x, b = blockIdx.y / p.c.H, h = blockIdx.y % p.c.H;
+    const bool is_v = blockIdx.z != 0;
+    const int stay = p.new_len[b];
+    const int rows = min(stay - col * kBlk, kBlk);
+    if (rows <= 0) return;
+    const int page = p.dst[static_cast<int64_t>(b) * p.dst_cols + col];
+    if (page < 0 || page >= p.c.pages) {
+        report(p.dev_status, kErrInvalid);
+        return;
+    }
+    const int32_t *kept = p.kept + (static_cast<int64_t>(b) * p.c.H + h) * p.budget + col * kBlk;
+    if (threadIdx.x < kBlk) {
+        int from = -1, t = 0;
+        if (threadIdx.x < rows) {
+            t = kept[threadIdx.x];
+            from = load_page(p.c, b, t / kBlk, p.dev_status);
+        }
+        s_page[threadIdx.x] = from;
+        s_slot[threadIdx.x] = t % kBlk;
+        if (!is_v && from >= 0)
+            p.weight[(static_cast<int64_t>(page) * p.c.H + h) * kBlk + threadIdx.x] =
+                p.weight[(static_cast<int64_t>(from) * p.c.H + h) * kBlk + t % kBlk];
+    }
+    __syncthreads();
+    uint8_t *codes = is_v ? p.c.v8 : p.c.k8;
+    float *scale = is_v ? p.c.sv : p.c.sk;
+    const int r = threadIdx.x >> 4, ch = (threadIdx.x & 15) * 8;
+    uint2 v[kPasses];
+    float s[kPasses];
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < kPasses; ++i) {
+        const int j = r + i * kRowsPerPass, from = s_page[j];
+        v[i] = make_uint2(0, 0);
+        s[i] = 0.0f;
+        if (from >= 0) {
+            const int64_t tile = static_cast<int64_t>(from) * p.c.H + h;
+            v[i] = *reinterpret_cast<const uint2 *>(codes + (tile * kBlk + s_slot[j]) * kD + ch);
+            s[i] = scale[tile];
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < kPasses; ++i) {
+        float f[8];
+        decode8(v[i], s[i], f);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const uint32_t u = __float_as_uint(f[e]) & 0x7fffffffu;
+            if (u < 0x7f800000u) m = max(m, u);
+        }
+    }
+    const uint32_t sb = scale_bits(block_max<kThreads>(m, red));
+    const float inv = pow2_inverse(sb);
+    const int64_t to = static_cast<int64_t>(page) * p.c.H + h;
+    if (threadIdx.x == 0) scale[to] = __uint_as_float(sb);
+#pragma unroll
+    for (int i = 0; i < kPasses; ++i) {
+        const int j = r + i * kRowsPerPass;
+        if (s_page[j] < 0) continue;
+        float f[8];
+        decode8(v[i], s[i], f);
+        *reinterpret_cast<uint2 *>(codes + (to * kBlk + j) * kD + ch) = encode8(f, inv);
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_cache_append(const CacheView &c, const CacheRows &k, const CacheRows &v, const int32_t *start, int T,
+                                int32_t *dev_status, cudaStream_t st) {
+    // n rows touch at most n pages and at most (n - 1) / 128 + 2
+    const int64_t bound = static_cast<int64_t>(T) / kBlk + 2ll * c.B;
+    const AppendParams p{c, k, v, start, T, dev_status};
+    append_kernel<<<dim3(static_cast<unsigned>(bound < T ? bound : T), c.H, 2), kThreads, 0, st>>>(p);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_cache_evict(const CacheView &c, float *weight, const int32_t *dst_table, int dst_cols, int budget,
+                               int recent, int32_t *new_len, int32_t *kept, int32_t *dev_status, cudaStream_t st) {
+    const EvictParams p{c, weight, dst_table, dst_cols, budget, recent, new_len, kept, dev_status};
+    select_kernel<<<dim3(c.H, c.B), kSelThreads, 0, st>>>(p);
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    move_kernel<<<dim3((budget + kBlk - 1) / kBlk, c.B * c.H, 2), kThreads, 0, st>>>(p);
+    return cudaGetLastError();
+}
+
+}  // namespace vca

@@ -1,0 +1,113 @@
+// vca_cache.cuh -- what the kernels of the 8-bit cache share: the view of the
+// cache, the place of a sequence's new rows, and the page scales.
+//
+// Cache: E4M3 codes [pages][H][128][128] with one fp32 scale per (page, head),
+// a power of two; table[b][j] names the page of tokens 128 j .. 128 j + 127 of
+// sequence b, len[b] counts its tokens, the current call's new ones included.
+// Device-side values are never trusted: every index read from table, len or
+// start is checked before it is used, and a bad one is reported in dev_status.
+#pragma once
+
+#include <cuda_fp16.h>
+
+#include "vca_device.cuh"
+#include "vca_internal.h"
+
+namespace vca {
+namespace cache {
+
+constexpr int kErrInvalid = 1;       // mirrors VCA_ERR_INVALID_ARG
+constexpr uint32_t kScaleExpMin = 127 - 120;   // biased exponent of the smallest page scale, 2^-120
+
+__device__ __forceinline__ void report(int32_t *dev_status, int code) {
+    if (dev_status) atomicExch(dev_status, code);
+}
+
+// Rows and length of sequence b: its new rows are [row0, row0 + n) of the T
+// rows of the call, `len` its tokens.  bad: start or len out of range (the
+// sequence then counts as having no new rows).
+struct Seq {
+    int row0, n, len;
+    bool bad;
+};
+__device__ __forceinline__ Seq load_seq(const CacheView &c, const int32_t *start, int T, int b) {
+    Seq s;
+    const int lo = start[b], hi = start[b + 1];
+    s.len = c.len[b];
+    s.bad = lo < 0 || hi < lo || hi > T || s.len < 0 || s.len > static_cast<int64_t>(c.cols) * kBlk;
+    s.row0 = lo;
+    s.n = s.bad ? 0 : hi - lo;
+    return s;
+}
+
+// Page of tokens 128 col .. 128 col + 127 of sequence b, or -1 (reported).
+__device__ __forceinline__ int load_page(const CacheView &c, int b, int col, int32_t *dev_status) {
+    const int page = c.table[static_cast<int64_t>(b) * c.cols + col];
+    if (page < 0 || page >= c.pages) {
+        report(dev_status, kErrInvalid);
+        return -1;
+    }
+    return page;
+}
+
+// fp32 bits of the smallest power of two s >= 2^-120 with amax <= 448 s; `bits`
+// are amax's (finite, >= 0).  448 = 1.75 * 2^8, so the exponent is the amax's
+// less 8, or less 7 where its mantissa is above 1.75.
+__device__ __forceinline__ uint32_t scale_bits(uint32_t bits) {
+    const int e = static_cast<int>(bits >> 23) - ((bits & 0x7fffffu) > 0x600000u ? 7 : 8);
+    return static_cast<uint32_t>(max(e, static_cast<int>(kScaleExpMin))) << 23;
+}
+// 1 / s of a power of two s in [2^-120, 2^120].
+__device__ __forceinline__ float pow2_inverse(uint32_t sbits) { return __uint_as_float((254u << 23) - sbits); }
+
+// Four E4M3 codes -> fp32 (exact).
+__device__ __forceinline__ void e4m3x4_decode(uint32_t w, float (&f)[4]) {
+    uint32_t lo, hi;
+    asm("{\n\t.reg .b16 a, b;\n\t"
+        "mov.b32 {a, b}, %2;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %0, a;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+        : "=r"(lo), "=r"(hi)
+        : "r"(w));
+    const float2 x = __half22float2(*reinterpret_cast<const __half2 *>(&lo));
+    const float2 y = __half22float2(*reinterpret_cast<const __half2 *>(&hi));
+    f[0] = x.x;
+    f[1] = x.y;
+    f[2] = y.x;
+    f[3] = y.y;
+}
+
+// Largest finite magnitude among eight bf16 values (as fp32 bits).
+__device__ __forceinline__ uint32_t amax_bf16x8(const uint4 &v) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t lo = (w[i] & 0x7fffu) << 16, hi = w[i] & 0x7fff0000u;
+        if (lo < 0x7f800000u) m = max(m, lo);
+        if (hi < 0x7f800000u) m = max(m, hi);
+    }
+    return m;
+}
+
+// x * inv with what is not finite turned into NaN (E4M3 has no infinity, and
+// a conversion that saturates would hide one).
+__device__ __forceinline__ float scaled_or_nan(float x, float inv) {
+    return (__float_as_uint(x) & 0x7f800000u) == 0x7f800000u ? __uint_as_float(0x7fc00000u) : __fmul_rn(x, inv);
+}
+
+// Largest of `v` over a block of kThreads threads, in every thread; `red` holds
+// kThreads / 32 words.
+template <int kThreads>
+__device__ __forceinline__ uint32_t block_max(uint32_t v, uint32_t *red) {
+    v = __reduce_max_sync(0xffffffffu, v);
+    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
+    __syncthreads();
+    uint32_t m = red[0];
+#pragma unroll
+    for (int i = 1; i < kThreads / 32; ++i) m = max(m, red[i]);
+    return m;
+}
+
+}  // namespace cache
+}  // namespace vca

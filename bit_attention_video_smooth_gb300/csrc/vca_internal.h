@@ -46,6 +46,50 @@ struct AttentionArgs {
 cudaError_t launch_attention(const AttentionArgs &a, cudaStream_t st);         // E4M3 residual V
 cudaError_t launch_attention_nvfp4(const AttentionArgs &a, cudaStream_t st);   // NVFP4 residual V and P
 
+// The 8-bit cache (vca_cache of include/vca.h; d = 128, pages of 128 tokens).
+struct CacheView {
+    uint8_t *k8, *v8;
+    float *sk, *sv;
+    const int32_t *table, *len;
+    int pages, H, B, cols;
+};
+struct CacheRows {                     // bf16 rows [T][heads][128] with element strides
+    const uint16_t *p;
+    int64_t tok, head;
+};
+struct CacheAttnArgs {
+    CacheView c;
+    CacheRows q;
+    const int32_t *start;
+    int T, Hq, causal;
+    float scale, softcap;
+    uint16_t *O;                       // [T][Hq][128]
+    float *lse;                        // [T][Hq] or null
+    void *ws;
+    int32_t *dev_status;
+    uint64_t wait_limit_ns;
+};
+struct CacheWeighArgs {
+    CacheView c;
+    CacheRows q;
+    const int32_t *start;
+    int T, Hq, causal;
+    float scale, softcap;
+    const float *lse;                  // [T][Hq]
+    float *weight;                     // [pages][H][128]
+    void *ws;
+    int32_t *dev_status;
+    uint64_t wait_limit_ns;
+};
+cudaError_t launch_cache_append(const CacheView &c, const CacheRows &k, const CacheRows &v, const int32_t *start, int T,
+                                int32_t *dev_status, cudaStream_t st);
+size_t cache_attention_workspace(int T, int Hq, int H, int B, int cols);
+cudaError_t launch_cache_attention(const CacheAttnArgs &a, cudaStream_t st);
+size_t cache_weigh_workspace(int T, int Hq, int H, int B, int cols);
+cudaError_t launch_cache_weigh(const CacheWeighArgs &a, cudaStream_t st);
+cudaError_t launch_cache_evict(const CacheView &c, float *weight, const int32_t *dst_table, int dst_cols, int budget,
+                               int recent, int32_t *new_len, int32_t *kept, int32_t *dev_status, cudaStream_t st);
+
 cudaError_t launch_expcast_codes(const float *s_raw, const float *c, const float *m, int64_t n, uint8_t *out,
                                  cudaStream_t st);
 cudaError_t launch_e4m3_encode_bits(uint32_t start, int64_t n, uint8_t *out, cudaStream_t st);

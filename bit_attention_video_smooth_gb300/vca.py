@@ -21,11 +21,14 @@ LIB_PATH = os.path.join(_HERE, "_build", "libvca.so")
 VCA_OK, VCA_ERR_INVALID_ARG, VCA_ERR_UNSUPPORTED, VCA_ERR_CUDA, VCA_ERR_TIMEOUT, VCA_ERR_WORKSPACE = range(6)
 VCA_V_E4M3, VCA_V_NVFP4 = 0, 1
 VCA_OP_GROUP, VCA_OP_PREP, VCA_OP_ATTENTION, VCA_OP_PREP_KSMOOTH = 0, 1, 2, 3
+VCA_OP_CACHE_ATTENTION, VCA_OP_CACHE_WEIGH = 4, 5
 
 # Entry points declared in include/vca.h (the ABI test checks they are exported).
 EXPORTS = ("vca_status_string", "vca_version", "vca_workspace_bytes", "vca_group", "vca_prep_quant",
            "vca_attention", "vca_expcast_codes", "vca_e4m3_encode_bits", "vca_selftest_timeout",
-           "vca_set_wait_limit_ns", "vca_prep_quant_noalloc", "vca_prep_quant_ex")
+           "vca_set_wait_limit_ns", "vca_prep_quant_noalloc", "vca_prep_quant_ex",
+           "vca_cache_workspace_bytes", "vca_cache_append", "vca_cache_attention", "vca_cache_weigh",
+           "vca_cache_evict")
 
 if not os.path.exists(LIB_PATH):
     raise ImportError(f"libvca.so is not built ({LIB_PATH}); run __graft_entry__.build() -- "
@@ -33,6 +36,14 @@ if not os.path.exists(LIB_PATH):
 
 _lib = ctypes.CDLL(LIB_PATH)
 _P, _I, _I64, _F, _SZ = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_float, ctypes.c_size_t
+
+
+class _CacheStruct(ctypes.Structure):
+    _fields_ = [(n, _P) for n in ("k8", "v8", "sk", "sv", "table", "len")] + \
+        [(n, _I) for n in ("pages", "H", "d", "B", "cols")]
+
+
+_C = ctypes.POINTER(_CacheStruct)
 _SIGS = {
     "vca_status_string": (ctypes.c_char_p, [_I]),
     "vca_version": (_I, []),
@@ -47,6 +58,11 @@ _SIGS = {
     "vca_prep_quant_noalloc": (_I, [_P, _P, _P, _P, _I, _I, _I, _I, _I, _P, _P, _P, _P, _P, _P, _P, _P, _P]),
     "vca_prep_quant_ex": (_I, [_P, _P, _P, _P, _I, _I, _I, _I, _I, ctypes.c_uint32, _P, _P, _P, _P, _P, _P, _P, _P,
                                _P, _SZ, _P]),
+    "vca_cache_workspace_bytes": (_SZ, [_I] * 6),
+    "vca_cache_append": (_I, [_C, _P, _I64, _I64, _P, _I64, _I64, _P, _I, _P, _P]),
+    "vca_cache_attention": (_I, [_C, _P, _I64, _I64, _P, _I, _I, _I, _F, _F, _P, _P, _P, _SZ, _P, _P]),
+    "vca_cache_weigh": (_I, [_C, _P, _I64, _I64, _P, _I, _I, _I, _F, _F, _P, _P, _P, _SZ, _P, _P]),
+    "vca_cache_evict": (_I, [_C, _P, _P, _I, _I, _I, _P, _P, _P, _P]),
 }
 for _name, (_res, _args) in _SIGS.items():
     _fn = getattr(_lib, _name)
@@ -320,3 +336,195 @@ def vc_attention(Q, K, V, k: int = 64, iters: int = 8, expcast: bool = True, vmo
     p = prep_quant(Q, K, V, g.perm, vmode)
     O = attention(p, B, H, N, expcast=expcast, softmax_scale=softmax_scale)
     return O, g, p
+
+
+# ---------------------------------------------------------------------------
+# The 8-bit cache (layouts and formulas: include/vca.h)
+# ---------------------------------------------------------------------------
+@dataclass
+class Cache:
+    """Pages of E4M3 keys and values with one power-of-two scale per page and
+    head, and the sequences that own them.  `length` counts each sequence's
+    tokens with the new ones of the next call included."""
+    k8: torch.Tensor        # uint8 [pages, H, 128, 128]
+    v8: torch.Tensor
+    sk: torch.Tensor        # float32 [pages, H]
+    sv: torch.Tensor
+    table: torch.Tensor     # int32 [B, cols]
+    length: torch.Tensor    # int32 [B]
+
+
+def alloc_cache(pages: int, H: int, B: int, cols: int, device="cuda") -> Cache:
+    """An empty cache: every length 0, every table entry -1."""
+    return Cache(torch.zeros((pages, H, 128, 128), dtype=torch.uint8, device=device),
+                 torch.zeros((pages, H, 128, 128), dtype=torch.uint8, device=device),
+                 torch.full((pages, H), 2.0 ** -120, dtype=torch.float32, device=device),
+                 torch.full((pages, H), 2.0 ** -120, dtype=torch.float32, device=device),
+                 torch.full((B, cols), -1, dtype=torch.int32, device=device),
+                 torch.zeros((B,), dtype=torch.int32, device=device))
+
+
+def vca_cache_workspace_bytes(op: int, T: int, Hq: int, H: int, B: int, cols: int) -> int:
+    return int(_lib.vca_cache_workspace_bytes(op, T, Hq, H, B, cols))
+
+
+def _typed(where, name, t, dtype, shape):
+    if t.dtype != dtype or t.shape != shape:
+        raise ValueError(f"{where}: {name} must be {dtype} {tuple(shape)}, got {t.dtype} {tuple(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{where}: {name} must be contiguous")
+
+
+def _cache_call(where, cache: Cache, rows, others, start=None):
+    """Checks a call's tensors and returns the C struct and the device: every
+    tensor of the types and shapes of include/vca.h, all on one CUDA device.
+    `rows` are (name, tensor, heads) of [T, heads, 128] bf16 with contiguous
+    channels, `others` (name, tensor, dtype, shape) or None tensors."""
+    k8, table = cache.k8, cache.table
+    if k8.dim() != 4 or table.dim() != 2:
+        raise ValueError(f"{where}: k8 must be [pages, H, 128, 128] and table [B, cols]")
+    (pages, H), (B, cols) = k8.shape[:2], table.shape
+    for name, t in (("k8", k8), ("v8", cache.v8)):
+        _typed(where, name, t, torch.uint8, (pages, H, 128, 128))
+    for name, t in (("sk", cache.sk), ("sv", cache.sv)):
+        _typed(where, name, t, torch.float32, (pages, H))
+    _typed(where, "table", table, torch.int32, (B, cols))
+    _typed(where, "length", cache.length, torch.int32, (B,))
+    seen = [("k8", k8), ("v8", cache.v8), ("sk", cache.sk), ("sv", cache.sv), ("table", table),
+            ("length", cache.length)]
+    if start is not None:
+        _typed(where, "start", start, torch.int32, (B + 1,))
+        seen.append(("start", start))
+    T = None
+    for name, t, heads in rows:
+        if t.dtype != torch.bfloat16 or t.dim() != 3 or t.shape[1] != heads or t.shape[2] != 128:
+            raise ValueError(f"{where}: {name} must be bfloat16 [T, {heads}, 128], got {t.dtype} {tuple(t.shape)}")
+        if t.stride(2) != 1:
+            raise ValueError(f"{where}: the channels of {name} must be contiguous")
+        if T is not None and t.shape[0] != T:
+            raise ValueError(f"{where}: {name} has {t.shape[0]} rows, not {T}")
+        T = t.shape[0]
+        seen.append((name, t))
+    for name, t, dtype, shape in others:
+        if t is not None:
+            if shape is not None:
+                _typed(where, name, t, dtype, shape)
+            elif not t.is_contiguous():
+                raise ValueError(f"{where}: {name} must be contiguous")
+            seen.append((name, t))
+    dev = k8.device
+    for name, t in seen:
+        if not t.is_cuda:
+            raise ValueError(f"{where}: {name} is not a CUDA tensor")
+        if t.device != dev:
+            raise ValueError(f"{where}: tensors on several devices: {name} on {t.device}, k8 on {dev}")
+    s = _CacheStruct(k8.data_ptr(), cache.v8.data_ptr(), cache.sk.data_ptr(), cache.sv.data_ptr(), table.data_ptr(),
+                     cache.length.data_ptr(), pages, H, 128, B, cols)
+    return s, dev
+
+
+def _launch(where, dev, fn, *args, stream=None):
+    """fn(*args, stream) with `dev` current, on its current stream unless one is given."""
+    if stream is None:
+        stream = torch.cuda.current_stream(dev)
+    if torch.cuda.current_device() == dev.index:
+        st = fn(*args, stream.cuda_stream)
+    else:
+        with torch.cuda.device(dev):
+            st = fn(*args, stream.cuda_stream)
+    _check(st, where)
+
+
+def _at(t: Optional[torch.Tensor]):
+    return None if t is None else t.data_ptr()
+
+
+def vca_cache_append(cache: Cache, K, V, start, dev_status=None, stream=None) -> None:
+    H = cache.k8.shape[1] if cache.k8.dim() == 4 else 0
+    s, dev = _cache_call("vca_cache_append", cache, (("K", K, H), ("V", V, H)),
+                         (("dev_status", dev_status, torch.int32, (1,)),), start)
+    _launch("vca_cache_append", dev, _lib.vca_cache_append, s, K.data_ptr(), K.stride(0), K.stride(1), V.data_ptr(),
+            V.stride(0), V.stride(1), start.data_ptr(), K.shape[0], _at(dev_status), stream=stream)
+
+
+def vca_cache_attention(cache: Cache, Q, start, causal: int, softmax_scale: float, softcap: float, O, lse, ws,
+                        dev_status=None, stream=None) -> None:
+    T, Hq = (Q.shape[0], Q.shape[1]) if Q.dim() == 3 else (0, 0)
+    s, dev = _cache_call("vca_cache_attention", cache, (("Q", Q, Hq),),
+                         (("O", O, torch.bfloat16, (T, Hq, 128)), ("lse", lse, torch.float32, (T, Hq)),
+                          ("ws", ws, None, None), ("dev_status", dev_status, torch.int32, (1,))), start)
+    _launch("vca_cache_attention", dev, _lib.vca_cache_attention, s, Q.data_ptr(), Q.stride(0), Q.stride(1),
+            start.data_ptr(), T, Hq, int(causal), softmax_scale, softcap, O.data_ptr(), _at(lse), _at(ws),
+            0 if ws is None else ws.numel() * ws.element_size(), _at(dev_status), stream=stream)
+
+
+def vca_cache_weigh(cache: Cache, Q, start, causal: int, softmax_scale: float, softcap: float, lse, weight, ws,
+                    dev_status=None, stream=None) -> None:
+    T, Hq = (Q.shape[0], Q.shape[1]) if Q.dim() == 3 else (0, 0)
+    s, dev = _cache_call("vca_cache_weigh", cache, (("Q", Q, Hq),),
+                         (("lse", lse, torch.float32, (T, Hq)),
+                          ("weight", weight, torch.float32, (*cache.k8.shape[:2], 128)),
+                          ("ws", ws, None, None), ("dev_status", dev_status, torch.int32, (1,))), start)
+    _launch("vca_cache_weigh", dev, _lib.vca_cache_weigh, s, Q.data_ptr(), Q.stride(0), Q.stride(1), start.data_ptr(),
+            T, Hq, int(causal), softmax_scale, softcap, lse.data_ptr(), weight.data_ptr(), _at(ws),
+            0 if ws is None else ws.numel() * ws.element_size(), _at(dev_status), stream=stream)
+
+
+def vca_cache_evict(cache: Cache, weight, dst_table, budget: int, recent: int, new_len, kept, dev_status=None,
+                    stream=None) -> None:
+    if dst_table.dim() != 2:
+        raise ValueError("vca_cache_evict: dst_table must be [B, dst_cols]")
+    B, H = cache.length.shape[0], cache.k8.shape[1]
+    s, dev = _cache_call("vca_cache_evict", cache, (),
+                         (("weight", weight, torch.float32, (*cache.k8.shape[:2], 128)),
+                          ("dst_table", dst_table, torch.int32, (B, dst_table.shape[1])),
+                          ("new_len", new_len, torch.int32, (B,)), ("kept", kept, torch.int32, (B, H, budget)),
+                          ("dev_status", dev_status, torch.int32, (1,))))
+    _launch("vca_cache_evict", dev, _lib.vca_cache_evict, s, weight.data_ptr(), dst_table.data_ptr(),
+            dst_table.shape[1], budget, recent, new_len.data_ptr(), kept.data_ptr(), _at(dev_status), stream=stream)
+
+
+def _cache_ws(op, cache: Cache, Q, ws):
+    if ws is not None:
+        return ws
+    need = vca_cache_workspace_bytes(op, Q.shape[0], Q.shape[1], cache.k8.shape[1], *cache.table.shape)
+    return torch.empty(need, dtype=torch.uint8, device=cache.k8.device) if need else None
+
+
+def cache_append(cache: Cache, K, V, start, dev_status=None) -> None:
+    """Quantises the new rows K, V [T, H, 128] into the cache's pages; sequence b
+    owns the rows start[b] .. start[b+1] - 1, its newest tokens."""
+    vca_cache_append(cache, K, V, start, dev_status)
+
+
+def cache_attention(cache: Cache, Q, start, causal: bool = True, softmax_scale: float = 0.0, softcap: float = 0.0,
+                    out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
+                    ws: Optional[torch.Tensor] = None, dev_status: Optional[torch.Tensor] = None):
+    """Attention of Q [T, Hq, 128] over the cache.  Returns (O [T, Hq, 128], lse [T, Hq])."""
+    O = out if out is not None else torch.empty(Q.shape, dtype=torch.bfloat16, device=Q.device)
+    lse = lse if lse is not None else torch.empty(Q.shape[:2], dtype=torch.float32, device=Q.device)
+    vca_cache_attention(cache, Q, start, causal, softmax_scale, softcap, O, lse,
+                        _cache_ws(VCA_OP_CACHE_ATTENTION, cache, Q, ws), dev_status)
+    return O, lse
+
+
+def cache_weigh(cache: Cache, Q, start, lse, weight, causal: bool = True, softmax_scale: float = 0.0,
+                softcap: float = 0.0, ws: Optional[torch.Tensor] = None,
+                dev_status: Optional[torch.Tensor] = None) -> None:
+    """Adds to weight [pages, H, 128] the attention that each cached token gets
+    from Q; lse is cache_attention's."""
+    vca_cache_weigh(cache, Q, start, causal, softmax_scale, softcap, lse, weight,
+                    _cache_ws(VCA_OP_CACHE_WEIGH, cache, Q, ws), dev_status)
+
+
+def cache_evict(cache: Cache, weight, dst_table, budget: int, recent: int, kept: Optional[torch.Tensor] = None,
+                dev_status: Optional[torch.Tensor] = None):
+    """Cuts every sequence to `budget` tokens per head into the pages of
+    dst_table.  Returns (new_len [B], kept [B, H, budget]); the cut sequences are
+    Cache(k8, v8, sk, sv, dst_table, new_len)."""
+    B, H = cache.length.shape[0], cache.k8.shape[1]
+    new_len = torch.empty((B,), dtype=torch.int32, device=cache.k8.device)
+    if kept is None:
+        kept = torch.full((B, H, budget), -1, dtype=torch.int32, device=cache.k8.device)
+    vca_cache_evict(cache, weight, dst_table, budget, recent, new_len, kept, dev_status)
+    return new_len, kept

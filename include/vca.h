@@ -65,7 +65,10 @@ typedef enum {
 
 typedef enum { VCA_V_E4M3 = 0, VCA_V_NVFP4 = 1 } vca_vmode;
 /* VCA_OP_PREP_KSMOOTH: the prep's workspace when VCA_PREP_K_SMOOTH is set. */
-typedef enum { VCA_OP_GROUP = 0, VCA_OP_PREP = 1, VCA_OP_ATTENTION = 2, VCA_OP_PREP_KSMOOTH = 3 } vca_op;
+typedef enum {
+    VCA_OP_GROUP = 0, VCA_OP_PREP = 1, VCA_OP_ATTENTION = 2, VCA_OP_PREP_KSMOOTH = 3,
+    VCA_OP_CACHE_ATTENTION = 4, VCA_OP_CACHE_WEIGH = 5   /* vca_cache_workspace_bytes */
+} vca_op;
 
 /* Human-readable name of a vca_status value (static string, never NULL). */
 const char *vca_status_string(int status);
@@ -236,6 +239,112 @@ int vca_selftest_timeout(int32_t *dev_status, uint64_t limit_ns, void *stream);
 
 /* Upper bound on every bounded device wait, in nanoseconds (default 2e9). */
 void vca_set_wait_limit_ns(uint64_t limit_ns);
+
+/*
+ * The 8-bit cache: keys and values of a growing sequence kept as E4M3 in pages
+ * of 128 tokens (the method's hardware block) with one scale per page and head,
+ * for models that produce a video chunk by chunk, or a sequence token by token,
+ * and attend to what came before.  The paper has no counterpart to it.
+ *
+ *   k8, v8   E4M3 bytes [pages][H][128][d]
+ *   sk, sv   fp32 [pages][H], powers of two >= 2^-120: a value is code * scale
+ *   table    int32 [B][cols]: the page of tokens 128 j .. 128 j + 127 of
+ *            sequence b; entries behind its last page are never read
+ *   len      int32 [B]: the tokens each sequence holds, the new ones of the
+ *            current call included
+ *
+ * The struct lies in host memory and is read during the call; every pointer in
+ * it is a device pointer (k8 and v8 16-byte aligned, the others 4-byte).
+ * Sizes: d = 128, pages, H, B, cols >= 1, B*H <= 65,535, pages*H*128 <= 2^31 - 1,
+ * cols*128 <= 2^31 - 1; codes are addressed with 64 bits.  Sequences may share
+ * pages that no call writes.
+ *
+ * A call's rows (K, V, Q) are bf16 [T][heads][d]: `start`, int32 [B + 1] on the
+ * device, cuts them: rows start[b] .. start[b+1] - 1, n of them (0 allowed),
+ * are sequence b's newest tokens, row i at slot len - n + i.  Rows behind
+ * start[B] belong to nobody and their outputs are left as they are.  The
+ * distance from token to token and from head to head is given in elements
+ * (multiples of 8; the d channels lie together), so views of a fused
+ * projection need no copy.  T = 0 returns VCA_OK and launches nothing.
+ *
+ * What lies on the device is checked there: a sequence whose start or len is
+ * out of range (start not rising within 0 .. T, len above cols*128) counts as
+ * having no rows, a page outside 0 .. pages - 1 as holding no tokens, and
+ * dev_status (optional, device int32) is set to VCA_ERR_INVALID_ARG, or to
+ * VCA_ERR_TIMEOUT if a bounded wait ran out; it is left untouched otherwise.
+ * Calls keep nothing between them: a workspace may be used by any call that
+ * does not overlap with this one, and the calls can be captured into a graph.
+ */
+typedef struct {
+    uint8_t *k8, *v8;
+    float *sk, *sv;
+    const int32_t *table, *len;
+    int pages, H, d, B, cols;
+} vca_cache;
+
+/* Scratch bytes for VCA_OP_CACHE_ATTENTION or VCA_OP_CACHE_WEIGH of T rows with
+ * Hq query heads over H KV heads, B sequences and `cols` table columns (0 if
+ * none, and for invalid sizes). */
+size_t vca_cache_workspace_bytes(int op, int T, int Hq, int H, int B, int cols);
+
+/*
+ * vca_cache_append -- quantises new K and V rows [T][H][d] into the cache.  Per
+ * page and head with new rows X: s = the smallest power of two >= 2^-120 with
+ * max |X| <= 448 s, or the page's scale if that is larger and the page already
+ * held tokens; sk (sv) = s; code = E4M3_rne(x / s).  x / s is exact.  Where s
+ * grew, the codes already there become E4M3_rne(value / s): only values that
+ * turn subnormal lose bits.  NaN and infinities become the NaN code and do not
+ * enter the maximum.  Slots that are not new and not rescaled stay as they are.
+ * A sequence with n > len is invalid.  No page may be written twice in a call.
+ */
+int vca_cache_append(const vca_cache *cache, const uint16_t *K, int64_t k_token, int64_t k_head, const uint16_t *V,
+                     int64_t v_token, int64_t v_head, const int32_t *start, int T, int32_t *dev_status, void *stream);
+
+/*
+ * vca_cache_attention -- attention of the rows Q [T][Hq][d] over the cache;
+ * query heads h*G .. h*G + G - 1 read KV head h, G = Hq / H:
+ *   s_ij = softmax_scale q_i . (k_j sk);  with softcap > 0: softcap tanh(s_ij / softcap)
+ *   j visible to row i: j < len, and with causal = 1: j <= len - n + i
+ *   O_i = sum_j softmax_j(s_ij) v_j sv,  lse_i = ln sum_j exp(s_ij)
+ * A row that sees nothing gets O = 0 and lse = -inf.  softmax_scale <= 0 selects
+ * 1/sqrt(d).  O is bf16 [T][Hq][d] and lse fp32 [T][Hq] (may be NULL), both
+ * contiguous.  Products are exact, sums and statistics fp32; the probabilities
+ * enter the second product as fp16.  A slot behind len may hold any bytes; a
+ * NaN among the values of a sequence may reach every row of that sequence.
+ * Equal calls give equal bits.
+ */
+int vca_cache_attention(const vca_cache *cache, const uint16_t *Q, int64_t q_token, int64_t q_head,
+                        const int32_t *start, int T, int Hq, int causal, float softmax_scale, float softcap,
+                        uint16_t *O, float *lse, void *ws, size_t ws_bytes, int32_t *dev_status, void *stream);
+
+/*
+ * vca_cache_weigh -- adds to weight, fp32 [pages][H][128], what each cached token
+ * received from the rows Q: weight[page][h][slot] += sum over the rows i and the
+ * G query heads of KV head h, where the token is visible, of exp(s_ij - lse_i),
+ * with s, visibility and lse [T][Hq] those of vca_cache_attention.  Sequences
+ * that share a page add to it in any order.
+ */
+int vca_cache_weigh(const vca_cache *cache, const uint16_t *Q, int64_t q_token, int64_t q_head, const int32_t *start,
+                    int T, int Hq, int causal, float softmax_scale, float softcap, const float *lse, float *weight,
+                    void *ws, size_t ws_bytes, int32_t *dev_status, void *stream);
+
+/*
+ * vca_cache_evict -- cuts every sequence to its min(len, budget) most useful
+ * tokens, for each KV head on its own, into fresh pages.  The newest
+ * min(recent, len) tokens stay; of the others those with the largest weight
+ * (NaN counts as -inf, ties go to the lower slot).  What stays keeps its order;
+ * kept int32 [B][H][budget] names the slots (entries behind the last one are
+ * left as they are), new_len int32 [B] their number.  dst_table [B][dst_cols]
+ * names the pages to write, in the same pool: ceil(new_len / 128) of each row
+ * are read, each named once and none a page that `table` names (the cached
+ * pages are only read, so they may be shared with other sequences).  A written
+ * page gets the scale of its own values, as in vca_cache_append; weights move
+ * with their tokens.  Requires budget >= 1, 0 <= recent <= budget,
+ * dst_cols*128 >= budget.  `len` is the cache's as always; afterwards the
+ * sequence is the cache with dst_table and new_len.
+ */
+int vca_cache_evict(const vca_cache *cache, float *weight, const int32_t *dst_table, int dst_cols, int budget,
+                    int recent, int32_t *new_len, int32_t *kept, int32_t *dev_status, void *stream);
 
 #ifdef __cplusplus
 }
