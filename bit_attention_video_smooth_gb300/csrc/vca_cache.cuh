@@ -109,5 +109,61 @@ __device__ __forceinline__ uint32_t block_max(uint32_t v, uint32_t *red) {
     return m;
 }
 
+// What the kernels that score query rows against cached keys get.
+struct AttnParams {
+    CacheView c;
+    CacheRows q;
+    const int32_t *start;
+    int T, Hq, G, causal;
+    float scale_log2;      // softmax_scale log2(e)
+    float cap_in;          // 2 log2(e) softmax_scale / cap: tanh(x) = 1 - 2 / (1 + 2^(2 log2(e) x))
+    float cap_out;         // cap log2(e), 0: no cap
+    uint16_t *O;
+    float *lse;
+    float *part;
+    int32_t *dev_status;
+    uint64_t limit_ns;
+};
+
+inline AttnParams attn_params(const CacheView &c, const CacheRows &q, const int32_t *start, int T, int Hq, int causal,
+                              float scale, float softcap, int32_t *dev_status, uint64_t limit_ns) {
+    AttnParams p{};
+    p.c = c;
+    p.q = q;
+    p.start = start;
+    p.T = T;
+    p.Hq = Hq;
+    p.G = Hq / c.H;
+    p.causal = causal;
+    const double log2e = 1.4426950408889634;
+    p.scale_log2 = static_cast<float>(scale * log2e);
+    p.cap_in = softcap > 0.0f ? static_cast<float>(2.0 * log2e * scale / softcap) : 0.0f;
+    p.cap_out = softcap > 0.0f ? static_cast<float>(softcap * log2e) : 0.0f;
+    p.dev_status = dev_status;
+    p.limit_ns = limit_ns;
+    return p;
+}
+
+// Query row r of a (sequence, KV head) is token r / G of the sequence's new
+// ones in query head h G + r % G.  It sees the keys [0, seen_by_row).
+__device__ __forceinline__ int seen_by_row(const AttnParams &p, const Seq &s, int r) {
+    return p.causal ? max(0, s.len - s.n + r / p.G + 1) : s.len;
+}
+__device__ __forceinline__ const uint16_t *query_row(const AttnParams &p, const Seq &s, int h, int r) {
+    return p.q.p + (s.row0 + r / p.G) * p.q.tok + (h * p.G + r % p.G) * p.q.head;
+}
+// Place of the row among the outputs [T][Hq].
+__device__ __forceinline__ int64_t out_row(const AttnParams &p, const Seq &s, int h, int r) {
+    return static_cast<int64_t>(s.row0 + r / p.G) * p.Hq + h * p.G + r % p.G;
+}
+
+// Score in log2 units from the raw product: x = S * f with f = c (no cap) or
+// the cap's inner factor.
+__device__ __forceinline__ float scored(float s, float f, float cap_out) {
+    const float x = __fmul_rn(s, f);
+    if (cap_out == 0.0f) return x;
+    return cap_out * (1.0f - __fdividef(2.0f, 1.0f + ex2_approx(x)));
+}
+
 }  // namespace cache
 }  // namespace vca

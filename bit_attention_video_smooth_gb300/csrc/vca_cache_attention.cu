@@ -50,21 +50,6 @@ constexpr uint32_t kOffBar = kOffScale + kStages * 8;
 constexpr uint32_t kSmem = kOffBar + 2 * kStages * 8 + 16 + 1024;
 static_assert(kSmem <= 232448, "shared memory budget");
 
-struct Params {
-    CacheView c;
-    CacheRows q;
-    const int32_t *start;
-    int T, Hq, G, causal;
-    float scale_log2;      // softmax_scale log2(e)
-    float cap_in;          // 2 log2(e) softmax_scale / cap: tanh(x) = 1 - 2 / (1 + 2^(2 log2(e) x))
-    float cap_out;         // cap log2(e), 0: no cap
-    uint16_t *O;
-    float *lse;
-    float *part;
-    int32_t *dev_status;
-    uint64_t limit_ns;
-};
-
 // ---------------------------------------------------------------------------
 // The list of units
 // ---------------------------------------------------------------------------
@@ -74,14 +59,14 @@ struct Shape {
     Seq s;
     int tiles, pages;
 };
-__device__ __forceinline__ Shape shape_of(const Params &p, int b) {
+__device__ __forceinline__ Shape shape_of(const AttnParams &p, int b) {
     Shape x;
     x.s = load_seq(p.c, p.start, p.T, b);
     x.tiles = static_cast<int>((static_cast<int64_t>(x.s.n) * p.G + kRows - 1) / kRows);
     x.pages = x.s.bad ? 0 : max(1, (x.s.len + kBlk - 1) / kBlk);
     return x;
 }
-__device__ __forceinline__ int64_t units_of(const Params &p, const Shape &x) {
+__device__ __forceinline__ int64_t units_of(const AttnParams &p, const Shape &x) {
     return static_cast<int64_t>(x.tiles) * x.pages * p.c.H;
 }
 
@@ -96,7 +81,7 @@ __device__ __forceinline__ int64_t warp_incl_scan(int64_t v) {
 }
 
 // Units of all sequences (a warp's work).
-__device__ int64_t count_units(const Params &p) {
+__device__ int64_t count_units(const AttnParams &p) {
     int64_t all = 0;
     for (int b0 = 0; b0 < p.c.B; b0 += 32) {
         const int b = b0 + static_cast<int>(threadIdx.x & 31);
@@ -113,7 +98,7 @@ __device__ __forceinline__ int64_t share_of(int64_t all, int ctas) {
 }
 
 // Where unit u lies: sequence, and the unit's place among the sequence's.
-__device__ void find_unit(const Params &p, int64_t u, int &b_out, int64_t &local) {
+__device__ void find_unit(const AttnParams &p, int64_t u, int &b_out, int64_t &local) {
     int64_t before = 0;
     const int lane = threadIdx.x & 31;
     for (int b0 = 0; b0 < p.c.B; b0 += 32) {
@@ -138,7 +123,7 @@ struct Walk {
     int b, h, tile, page;      // the next unit
     int64_t left;              // units left in the share
     Shape x;
-    __device__ void begin(const Params &p, int b_, int64_t local, int64_t units) {
+    __device__ void begin(const AttnParams &p, int b_, int64_t local, int64_t units) {
         b = b_;
         left = units;
         if (b < p.c.B) {
@@ -151,7 +136,7 @@ struct Walk {
     }
     // Pages of the current tile in this share.
     __device__ int run() const { return static_cast<int>(left < x.pages - page ? left : x.pages - page); }
-    __device__ void next(const Params &p, int done) {
+    __device__ void next(const AttnParams &p, int done) {
         left -= done;
         page += done;
         if (page < x.pages) return;
@@ -167,11 +152,6 @@ struct Walk {
         } while (x.tiles == 0 || x.pages == 0);
     }
 };
-
-// Keys that the rows of a tile may see: [0, seen) by at least one row.
-__device__ __forceinline__ int seen_by_row(const Params &p, const Seq &s, int r) {
-    return p.causal ? max(0, s.len - s.n + r / p.G + 1) : s.len;
-}
 
 // ---------------------------------------------------------------------------
 // The products
@@ -198,18 +178,10 @@ __device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
 }
 __device__ __forceinline__ uint4 lds128(const unsigned char *p) { return *reinterpret_cast<const uint4 *>(p); }
 
-// Score in log2 units from the raw product: x = S * f with f = c (no cap) or
-// the cap's inner factor.
-__device__ __forceinline__ float scored(float s, float f, float cap_out) {
-    const float x = __fmul_rn(s, f);
-    if (cap_out == 0.0f) return x;
-    return cap_out * (1.0f - __fdividef(2.0f, 1.0f + ex2_approx(x)));
-}
-
 // The 32 channels t * 32 .. t * 32 + 31 of one query row as fp16 pairs, scaled
 // by a power of two; returns the factor's inverse.  All four threads of a quad
 // hold a quarter of the same row.
-__device__ __forceinline__ float load_q(const Params &p, const Seq &s, int h, int r, int t, uint32_t (&q)[16]) {
+__device__ __forceinline__ float load_q(const AttnParams &p, const Seq &s, int h, int r, int t, uint32_t (&q)[16]) {
     uint4 v[4];
     const bool real = r < s.n * p.G;
 #pragma unroll
@@ -238,7 +210,7 @@ __device__ __forceinline__ float load_q(const Params &p, const Seq &s, int h, in
 }
 
 __global__ void __launch_bounds__(kThreads, 1)
-    decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, const Params p) {
+    decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, const AttnParams p) {
     extern __shared__ unsigned char smem_raw[];
     unsigned char *smem =
         reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -518,7 +490,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // Joins the partials of the tile that straddles the end of CTA blockIdx.x's
 // share and begins in it.  One thread per (row, eight channels).
-__global__ void __launch_bounds__(256) combine_kernel(const Params p, int ctas) {
+__global__ void __launch_bounds__(256) combine_kernel(const AttnParams p, int ctas) {
     const int64_t all = count_units(p), share = share_of(all, ctas);
     const int64_t u0 = share * blockIdx.x, u1 = u0 + share;
     if (u1 >= all) return;                   // nothing behind this share
@@ -574,7 +546,7 @@ __global__ void __launch_bounds__(256) combine_kernel(const Params p, int ctas) 
 // One CTA per (page column, sequence, KV head), one thread per key; the query
 // rows in tiles of 16 as fp32 in shared memory.
 constexpr int kWeighThreads = kBlk;
-__global__ void __launch_bounds__(kWeighThreads) weigh_kernel(const Params p, const float *__restrict__ lse, float *weight) {
+__global__ void __launch_bounds__(kWeighThreads) weigh_kernel(const AttnParams p, const float *__restrict__ lse, float *weight) {
     __shared__ float4 sQ[kRows][kD / 4];
     __shared__ float sLse[kRows];
     __shared__ int sSeen[kRows];
@@ -625,25 +597,6 @@ __global__ void __launch_bounds__(kWeighThreads) weigh_kernel(const Params p, co
     if (key < s.len) atomicAdd(weight + tile * kBlk + tid, w);
 }
 
-Params params_of(const CacheView &c, const CacheRows &q, const int32_t *start, int T, int Hq, int causal, float scale,
-                 float softcap, int32_t *dev_status, uint64_t limit_ns) {
-    Params p{};
-    p.c = c;
-    p.q = q;
-    p.start = start;
-    p.T = T;
-    p.Hq = Hq;
-    p.G = Hq / c.H;
-    p.causal = causal;
-    const double log2e = 1.4426950408889634;
-    p.scale_log2 = static_cast<float>(scale * log2e);
-    p.cap_in = softcap > 0.0f ? static_cast<float>(2.0 * log2e * scale / softcap) : 0.0f;
-    p.cap_out = softcap > 0.0f ? static_cast<float>(softcap * log2e) : 0.0f;
-    p.dev_status = dev_status;
-    p.limit_ns = limit_ns;
-    return p;
-}
-
 // CTAs of the decode kernel: one per SM, fewer where there cannot be work for all.
 int decode_ctas(int T, int Hq, int H, int B, int cols) {
     const int64_t G = Hq / H;
@@ -653,18 +606,24 @@ int decode_ctas(int T, int Hq, int H, int B, int cols) {
     return static_cast<int>(most < 152 ? (most < 1 ? 1 : most) : 152);
 }
 
+// More than one tile of 16 rows a sequence and KV head on average: the tensor
+// core kernel's tiles of 128 rows.
+bool many_rows(int T, int Hq, int H, int B) { return static_cast<int64_t>(T) * (Hq / H) > static_cast<int64_t>(kRows) * B; }
+
 }  // namespace
 
 size_t cache_attention_workspace(int T, int Hq, int H, int B, int cols) {
+    if (many_rows(T, Hq, H, B)) return cache_chunk_workspace(T, Hq, H, B, cols);
     return static_cast<size_t>(decode_ctas(T, Hq, H, B, cols)) * 2 * kPartFloats * sizeof(float);
 }
 size_t cache_weigh_workspace(int, int, int, int, int) { return 0; }
 
 cudaError_t launch_cache_attention(const CacheAttnArgs &a, cudaStream_t st) {
+    if (many_rows(a.T, a.Hq, a.c.H, a.c.B)) return launch_cache_chunk(a, st);
     CUtensorMap mk, mv;
     const uint64_t rows = static_cast<uint64_t>(a.c.pages) * a.c.H * kBlk;
     if (!attn::make_tile_map(&mk, a.c.k8, rows) || !attn::make_tile_map(&mv, a.c.v8, rows)) return cudaErrorInvalidValue;
-    Params p = params_of(a.c, a.q, a.start, a.T, a.Hq, a.causal, a.scale, a.softcap, a.dev_status, a.wait_limit_ns);
+    AttnParams p = attn_params(a.c, a.q, a.start, a.T, a.Hq, a.causal, a.scale, a.softcap, a.dev_status, a.wait_limit_ns);
     p.O = a.O;
     p.lse = a.lse;
     p.part = static_cast<float *>(a.ws);
@@ -679,7 +638,7 @@ cudaError_t launch_cache_attention(const CacheAttnArgs &a, cudaStream_t st) {
 }
 
 cudaError_t launch_cache_weigh(const CacheWeighArgs &a, cudaStream_t st) {
-    const Params p = params_of(a.c, a.q, a.start, a.T, a.Hq, a.causal, a.scale, a.softcap, a.dev_status, a.wait_limit_ns);
+    const AttnParams p = attn_params(a.c, a.q, a.start, a.T, a.Hq, a.causal, a.scale, a.softcap, a.dev_status, a.wait_limit_ns);
     weigh_kernel<<<dim3(a.c.cols, a.c.B * a.c.H), kWeighThreads, 0, st>>>(p, a.lse, a.weight);
     return cudaGetLastError();
 }

@@ -85,6 +85,8 @@ cudaError_t launch_cache_append(const CacheView &c, const CacheRows &k, const Ca
                                 int32_t *dev_status, cudaStream_t st);
 size_t cache_attention_workspace(int T, int Hq, int H, int B, int cols);
 cudaError_t launch_cache_attention(const CacheAttnArgs &a, cudaStream_t st);
+size_t cache_chunk_workspace(int T, int Hq, int H, int B, int cols);              // many rows
+cudaError_t launch_cache_chunk(const CacheAttnArgs &a, cudaStream_t st);
 size_t cache_weigh_workspace(int T, int Hq, int H, int B, int cols);
 cudaError_t launch_cache_weigh(const CacheWeighArgs &a, cudaStream_t st);
 cudaError_t launch_cache_evict(const CacheView &c, float *weight, const int32_t *dst_table, int dst_cols, int budget,
