@@ -540,63 +540,6 @@ __global__ void __launch_bounds__(256) combine_kernel(const AttnParams p, int ct
     if (p.lse && ch == 0) p.lse[at] = Mu * 0.6931471805599453f + logf(L);
 }
 
-// ---------------------------------------------------------------------------
-// The weight each cached token received
-// ---------------------------------------------------------------------------
-// One CTA per (page column, sequence, KV head), one thread per key; the query
-// rows in tiles of 16 as fp32 in shared memory.
-constexpr int kWeighThreads = kBlk;
-__global__ void __launch_bounds__(kWeighThreads) weigh_kernel(const AttnParams p, const float *__restrict__ lse, float *weight) {
-    __shared__ float4 sQ[kRows][kD / 4];
-    __shared__ float sLse[kRows];
-    __shared__ int sSeen[kRows];
-    const int col = blockIdx.x, b = blockIdx.y / p.c.H, h = blockIdx.y % p.c.H, tid = threadIdx.x;
-    const Seq s = load_seq(p.c, p.start, p.T, b);
-    if (s.bad && col == 0 && h == 0 && tid == 0) report(p.dev_status, kErrInvalid);
-    if (s.n == 0 || col * kBlk >= s.len) return;
-    const int page = load_page(p.c, b, col, p.dev_status);
-    if (page < 0) return;
-    const int64_t tile = static_cast<int64_t>(page) * p.c.H + h;
-    const uint32_t *codes = reinterpret_cast<const uint32_t *>(p.c.k8 + (tile * kBlk + tid) * kD);
-    const float f = (p.cap_out != 0.0f ? p.cap_in : p.scale_log2) * p.c.sk[tile];
-    const int key = col * kBlk + tid, R = s.n * p.G;
-    float w = 0.0f;
-    for (int r0 = 0; r0 < R; r0 += kRows) {
-        __syncthreads();
-        for (int i = tid; i < kRows * kD / 4; i += kWeighThreads) {
-            const int r = r0 + i / (kD / 4), ch = i % (kD / 4) * 4;
-            float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-            if (r < R) {
-                const uint2 u = *reinterpret_cast<const uint2 *>(p.q.p + (s.row0 + r / p.G) * p.q.tok +
-                                                                 (h * p.G + r % p.G) * p.q.head + ch);
-                x = make_float4(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xffff0000u),
-                                __uint_as_float(u.y << 16), __uint_as_float(u.y & 0xffff0000u));
-            }
-            sQ[i / (kD / 4)][i % (kD / 4)] = x;
-        }
-        if (tid < kRows) {
-            const int r = r0 + tid;
-            sLse[tid] = r < R ? lse[static_cast<int64_t>(s.row0 + r / p.G) * p.Hq + h * p.G + r % p.G] : 0.0f;
-            sSeen[tid] = r < R ? min(seen_by_row(p, s, r), s.len) : 0;
-        }
-        __syncthreads();
-        float acc[kRows] = {};
-        for (int c = 0; c < kD / 4; ++c) {
-            float k[4];
-            e4m3x4_decode(codes[c], k);
-#pragma unroll
-            for (int r = 0; r < kRows; ++r) {
-                const float4 q = sQ[r][c];
-                acc[r] = fmaf(q.x, k[0], fmaf(q.y, k[1], fmaf(q.z, k[2], fmaf(q.w, k[3], acc[r]))));
-            }
-        }
-#pragma unroll
-        for (int r = 0; r < kRows; ++r)
-            if (key < sSeen[r]) w += ex2_approx(scored(acc[r], f, p.cap_out) - sLse[r] * 1.4426950408889634f);
-    }
-    if (key < s.len) atomicAdd(weight + tile * kBlk + tid, w);
-}
-
 // CTAs of the decode kernel: one per SM, fewer where there cannot be work for all.
 int decode_ctas(int T, int Hq, int H, int B, int cols) {
     const int64_t G = Hq / H;
@@ -616,7 +559,6 @@ size_t cache_attention_workspace(int T, int Hq, int H, int B, int cols) {
     if (many_rows(T, Hq, H, B)) return cache_chunk_workspace(T, Hq, H, B, cols);
     return static_cast<size_t>(decode_ctas(T, Hq, H, B, cols)) * 2 * kPartFloats * sizeof(float);
 }
-size_t cache_weigh_workspace(int, int, int, int, int) { return 0; }
 
 cudaError_t launch_cache_attention(const CacheAttnArgs &a, cudaStream_t st) {
     if (many_rows(a.T, a.Hq, a.c.H, a.c.B)) return launch_cache_chunk(a, st);
@@ -634,12 +576,6 @@ cudaError_t launch_cache_attention(const CacheAttnArgs &a, cudaStream_t st) {
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     combine_kernel<<<ctas, 256, 0, st>>>(p, ctas);
-    return cudaGetLastError();
-}
-
-cudaError_t launch_cache_weigh(const CacheWeighArgs &a, cudaStream_t st) {
-    const AttnParams p = attn_params(a.c, a.q, a.start, a.T, a.Hq, a.causal, a.scale, a.softcap, a.dev_status, a.wait_limit_ns);
-    weigh_kernel<<<dim3(a.c.cols, a.c.B * a.c.H), kWeighThreads, 0, st>>>(p, a.lse, a.weight);
     return cudaGetLastError();
 }
 

@@ -1,0 +1,635 @@
+// vca_cache_weigh.cu -- the attention weight that each cached token receives:
+//   weight[key] += sum over the rows r that see it of 2^(x(r, key) - lse(r) log2 e),
+// x the score in log2 units, as vca_cache_attention.cu has it.
+//
+// The scores come from the tensor core with keys as rows: S^T = K Q^T, K's E4M3
+// codes straight from TMA, so a thread owns one key and adds its row of S^T up in
+// registers; no sum crosses threads.  A query row is hi + lo E4M3 with a factor
+// per 32 channels, as in vca_cache_chunk.cu, here the B operand.  A first kernel
+// writes every tile of N query rows (16 where sequences have few, else 128) as
+// an image of what the second one wants in shared memory: the two code
+// matrices, their factors, and for each row its score factor and lse.
+//
+// The second kernel runs one CTA per SM over an equal share of the (sequence,
+// KV head, page) list.  Up to four pages of a head stay in shared memory while the
+// head's tiles stream past them: a page is read once, and a tile once for four
+// pages.  Few rows are bound by reading K (128 B a token) and the weights; many
+// by the tensor core's two FP8 products, 2 x 2 rows keys d flops.
+// Warps: 0 producer, 1 MMA issuer, 2-9 sums (two sets of four that take the
+// unit's even and odd pages).  Every wait is bounded, as in vca_attention.cu.
+#include "vca_attention_common.cuh"
+#include "vca_cache.cuh"
+
+namespace vca {
+
+namespace {
+
+using namespace attn;
+using namespace cache;
+
+constexpr uint32_t kTile = kBlk * kD;
+constexpr int kKP = 4;                       // pages of a unit
+constexpr int kKStages = 8, kSlots = 16;
+constexpr int kThreads = 320;
+
+// A tile of N rows as it lies in the workspace and in shared memory: hi, lo
+// codes [N][128], swizzled; the factors of hi and of lo, 32 rows of 16 bytes each
+// (row i: rows i, i + 32, i + 64, i + 96); per two rows their factors and -lse;
+// and how many keys each row sees.
+template <int N>
+struct Image {
+    static constexpr uint32_t lo = N * kD, sf = 2 * N * kD, consts = sf + 1024, seen = consts + 8 * N, bytes = seen + 4 * N;
+    static constexpr uint32_t stride = (bytes + 1023) / 1024 * 1024;
+};
+
+template <int N>
+struct Layout {
+    static constexpr int qstages = N == 128 ? 2 : 4, sbufs = N == 128 ? 3 : 8;
+    static constexpr uint32_t tmem_sfa = sbufs * N, tmem_sfb = tmem_sfa + 4, tmem_cols = N == 128 ? 512 : 256;
+    static constexpr uint32_t offQ = kKStages * kTile, offSlot = offQ + qstages * Image<N>::stride, offBar = offSlot + kSlots * 8;
+    static constexpr int bars = 2 * kKStages + 2 * qstages + 2 * sbufs + 1;
+    static constexpr uint32_t offMisc = offBar + bars * 8, smem = offMisc + 16 + 1024;
+    static_assert(smem <= 232448, "shared memory budget");
+    static_assert(tmem_sfb + 8 * qstages <= tmem_cols, "TMEM plan");
+};
+
+struct WeighParams {
+    AttnParams a;
+    const float *lse;
+    float *weight;
+    uint8_t *images;
+    int tiles;           // images of one head at most
+};
+
+// A sequence's rows and pages.
+struct Work {
+    Seq s;
+    int tiles, pages;
+};
+template <int N>
+__device__ __forceinline__ Work work_of(const AttnParams &p, int b) {
+    Work w;
+    w.s = load_seq(p.c, p.start, p.T, b);
+    w.tiles = static_cast<int>((static_cast<int64_t>(w.s.n) * p.G + N - 1) / N);
+    w.pages = w.s.bad || w.tiles == 0 ? 0 : (w.s.len + kBlk - 1) / kBlk;
+    return w;
+}
+// The first tile with a row that sees a page: with x = 128 page - (len - n), a
+// causal row sees it when its token is at least the x-th new one.
+template <int N>
+__device__ __forceinline__ int first_tile(const AttnParams &p, const Seq &s, int page) {
+    if (!p.causal) return 0;
+    const int64_t x = static_cast<int64_t>(page) * kBlk - (s.len - s.n);
+    return x <= 0 ? 0 : static_cast<int>(x * p.G / N);
+}
+
+__device__ __forceinline__ int64_t scan64(int64_t v) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t y = __shfl_up_sync(0xffffffffu, v, o);
+        if (lane >= o) v += y;
+    }
+    return v;
+}
+
+// Tiles that the pages [0, upto) of one head take, or with `find` >= 0 the first
+// page before which at least `find` tiles lie.  A warp's work.
+template <int N>
+__device__ int64_t head_cost(const AttnParams &p, const Work &w, int64_t find, int &page) {
+    if (!p.causal || N == 16) {
+        // few rows: the last page alone may be seen by fewer tiles
+        if (find >= 0) page = w.tiles ? static_cast<int>((find + w.tiles - 1) / w.tiles) : 0;
+        return static_cast<int64_t>(w.tiles) * w.pages;
+    }
+    int64_t sum = 0;
+    for (int j0 = 0; j0 < w.pages; j0 += 32) {
+        const int j = j0 + static_cast<int>(threadIdx.x & 31);
+        const int64_t c = j < w.pages ? w.tiles - first_tile<N>(p, w.s, j) : 0;
+        const int64_t incl = scan64(c) + sum;
+        if (find >= 0) {
+            const uint32_t hit = __ballot_sync(0xffffffffu, j < w.pages && incl - c >= find);
+            if (hit) {
+                page = j0 + __ffs(hit) - 1;
+                return 0;
+            }
+        }
+        sum = __shfl_sync(0xffffffffu, incl, 31);
+    }
+    page = w.pages;
+    return sum;
+}
+
+// Place in the list of (sequence, head, page).
+struct Place {
+    int64_t linear;      // pages before it
+    int b, at, tile0;    // its sequence, its place among the sequence's H * pages, the tiles of the sequences before
+};
+// The first place before which at least `pos` tiles of work lie: 32 sequences
+// at a time, one per lane, or one by one where their pages cost differently.
+template <int N>
+__device__ Place find_place(const AttnParams &p, int64_t pos) {
+    Place r{0, 0, 0, 0};
+    const bool even = !p.causal || N == 16;
+    const int lane = threadIdx.x & 31, step = even ? 32 : 1;
+    int page = 0;
+    for (int b0 = 0; b0 < p.c.B; b0 += step) {
+        const int mine = b0 + (even ? lane : 0);
+        Work w{};
+        int64_t c = 0;
+        if (mine < p.c.B) {
+            w = work_of<N>(p, mine);
+            c = head_cost<N>(p, w, -1, page);
+        }
+        const bool counts = mine < p.c.B && (even || lane == 0);
+        const int64_t cost = counts ? c * p.c.H : 0, pages = counts ? static_cast<int64_t>(p.c.H) * w.pages : 0;
+        const int64_t tiles = counts ? w.tiles : 0;
+        const int64_t ci = scan64(cost), pi = scan64(pages), ti = scan64(tiles);
+        const uint32_t hit = __ballot_sync(0xffffffffu, counts && pos < ci);
+        if (hit) {
+            const int l = __ffs(hit) - 1;
+            r.b = b0 + l;
+            r.tile0 += static_cast<int>(__shfl_sync(0xffffffffu, ti - tiles, l));
+            r.linear += __shfl_sync(0xffffffffu, pi - pages, l);
+            const int64_t rest = pos - __shfl_sync(0xffffffffu, ci - cost, l);
+            w = work_of<N>(p, r.b);
+            c = __shfl_sync(0xffffffffu, c, l);
+            const int64_t h = rest / c;
+            head_cost<N>(p, w, rest - h * c, page);
+            r.at = static_cast<int>(h * w.pages + page);
+            r.linear += r.at;
+            if (r.at == p.c.H * w.pages) {
+                r.tile0 += w.tiles;
+                ++r.b;
+                r.at = 0;
+            }
+            return r;
+        }
+        pos -= __shfl_sync(0xffffffffu, ci, 31);
+        r.linear += __shfl_sync(0xffffffffu, pi, 31);
+        r.tile0 += static_cast<int>(__shfl_sync(0xffffffffu, ti, 31));
+    }
+    r.b = p.c.B;
+    return r;
+}
+template <int N>
+__device__ int64_t all_work(const AttnParams &p) {
+    int64_t sum = 0;
+    int page;
+    if (!p.causal || N == 16) {
+        for (int b = threadIdx.x & 31; b < p.c.B; b += 32) {
+            const Work w = work_of<N>(p, b);
+            sum += static_cast<int64_t>(w.tiles) * w.pages;
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    } else {
+        for (int b = 0; b < p.c.B; ++b) sum += head_cost<N>(p, work_of<N>(p, b), -1, page);
+    }
+    return sum * p.c.H;
+}
+
+// A CTA's walk over its share, up to kKP pages of one head at a time.
+template <int N>
+struct Walk {
+    int64_t left;
+    int b, h, page, tile0;       // tile0: the sequence's first image
+    Work w;
+    __device__ void begin(const AttnParams &p, const Place &from, int64_t pages) {
+        left = pages;
+        b = from.b;
+        tile0 = from.tile0;
+        w = work_of<N>(p, b);
+        skip(p);
+        h = from.at / w.pages;
+        page = from.at - h * w.pages;
+    }
+    __device__ void skip(const AttnParams &p) {
+        while (w.pages == 0 && b + 1 < p.c.B) {
+            tile0 += w.tiles;
+            w = work_of<N>(p, ++b);
+        }
+    }
+    __device__ int count() const { return static_cast<int>(min(left, static_cast<int64_t>(min(kKP, w.pages - page)))); }
+    __device__ void next(const AttnParams &p, int done) {
+        left -= done;
+        page += done;
+        if (page < w.pages || left <= 0) return;
+        page = 0;
+        if (++h < p.c.H) return;
+        h = 0;
+        tile0 += w.tiles;
+        w = work_of<N>(p, ++b);
+        skip(p);
+    }
+};
+
+// ---------------------------------------------------------------------------
+// The images
+// ---------------------------------------------------------------------------
+// One CTA per (tile, head): 16 threads a row, 8 channels each.
+template <int N>
+__global__ void __launch_bounds__(256) image_kernel(const WeighParams wp) {
+    const AttnParams &p = wp.a;
+    const int h = blockIdx.y, lane16 = threadIdx.x & 15;
+    // the tile's sequence
+    int b = 0, rest = blockIdx.x;
+    {
+        const int lane = threadIdx.x & 31;
+        int before = 0;
+        bool found = false;
+        for (int b0 = 0; b0 < p.c.B && !found; b0 += 32) {
+            const int t = b0 + lane < p.c.B ? work_of<N>(p, b0 + lane).tiles : 0;
+            if (blockIdx.x == 0 && h == 0 && b0 + lane < p.c.B && load_seq(p.c, p.start, p.T, b0 + lane).bad)
+                report(p.dev_status, kErrInvalid);
+            int incl = t;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int y = __shfl_up_sync(0xffffffffu, incl, o);
+                if (lane >= o) incl += y;
+            }
+            const uint32_t hit = __ballot_sync(0xffffffffu, static_cast<int>(blockIdx.x) < before + incl);
+            if (hit) {
+                const int l = __ffs(hit) - 1;
+                b = b0 + l;
+                rest = blockIdx.x - before - __shfl_sync(0xffffffffu, incl - t, l);
+                found = true;
+            }
+            before += __shfl_sync(0xffffffffu, incl, 31);
+        }
+        if (!found) return;
+    }
+    const Seq s = load_seq(p.c, p.start, p.T, b);
+    const int R = s.n * p.G;
+    uint8_t *img = wp.images + (static_cast<int64_t>(h) * wp.tiles + blockIdx.x) * Image<N>::stride;
+    uint8_t *sf = img + Image<N>::sf;
+    if (N < 32) {
+        // rows that do not exist have factor words too
+        for (int i = threadIdx.x; i < 256; i += 256) reinterpret_cast<uint32_t *>(sf)[i] = 0x7f7f7f7fu;
+        __syncthreads();
+    }
+    for (int n = threadIdx.x >> 4; n < N; n += 16) {
+        const int r = rest * N + n;
+        const bool real = r < R;
+        const int seen = real ? min(seen_by_row(p, s, r), s.len) : 0;
+        uint4 v = make_uint4(0, 0, 0, 0);
+        if (real) v = *reinterpret_cast<const uint4 *>(query_row(p, s, h, r) + 8 * lane16);
+        uint32_t m = amax_bf16x8(v);
+        m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+        m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
+        const int e = max(static_cast<int>(m >> 23) - 127 - 7, -100);
+        int E = max(e, __shfl_xor_sync(0xffffffffu, e, 4));
+        E = max(E, __shfl_xor_sync(0xffffffffu, E, 8));
+        const float down = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+        float x[8];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            x[2 * k] = scaled_or_nan(__uint_as_float(w[k] << 16), down);
+            x[2 * k + 1] = scaled_or_nan(__uint_as_float(w[k] & 0xffff0000u), down);
+        }
+        uint2 hi, lo;
+        float d[4];
+        hi.x = e4m3x4(x[0], x[1], x[2], x[3]);
+        hi.y = e4m3x4(x[4], x[5], x[6], x[7]);
+        e4m3x4_decode(hi.x, d);
+        lo.x = e4m3x4(32.0f * (x[0] - d[0]), 32.0f * (x[1] - d[1]), 32.0f * (x[2] - d[2]), 32.0f * (x[3] - d[3]));
+        e4m3x4_decode(hi.y, d);
+        lo.y = e4m3x4(32.0f * (x[4] - d[0]), 32.0f * (x[5] - d[1]), 32.0f * (x[6] - d[2]), 32.0f * (x[7] - d[3]));
+        const uint32_t at = sw128_offset(n, lane16 >> 1) + 8 * (lane16 & 1);
+        *reinterpret_cast<uint2 *>(img + at) = hi;
+        *reinterpret_cast<uint2 *>(img + Image<N>::lo + at) = lo;
+        if ((lane16 & 3) == 0) {
+            const int byte = max(127 + e - E, 6);
+            uint8_t *q = sf + (n & 31) * 16 + (n >> 5) * 4 + (lane16 >> 2);
+            q[0] = static_cast<uint8_t>(byte);
+            q[512] = static_cast<uint8_t>(byte - 5);
+        }
+        if (lane16 == 0) {
+            // a row that sees nothing adds nothing: 2^(0 S - inf)
+            float *c = reinterpret_cast<float *>(img + Image<N>::consts) + (n >> 1) * 4 + (n & 1);
+            const float two_e = __uint_as_float(static_cast<uint32_t>(127 + E) << 23);
+            c[0] = seen > 0 ? two_e * (p.cap_out != 0.0f ? p.cap_in : p.scale_log2) : 0.0f;
+            c[2] = seen > 0 ? -1.4426950408889634f * wp.lse[out_row(p, s, h, r)] : __int_as_float(0xff800000);
+            reinterpret_cast<int *>(img + Image<N>::seen)[n] = seen;
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------
+// The sums
+// ---------------------------------------------------------------------------
+// Instruction descriptor of the block-scaled FP8 MMA, B's factor byte `sf` of its word, A's byte 0.
+__host__ __device__ constexpr uint32_t make_idesc_mxf8_b(int M, int N, uint32_t sf) {
+    return (sf << 4) | (static_cast<uint32_t>(N >> 3) << 17) | (1u << 23) | (static_cast<uint32_t>(M >> 4) << 24);
+}
+__device__ __forceinline__ void mma_mxf8_ss(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                            uint32_t sfa_tmem, uint32_t sfb_tmem, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], [%5], p;\n\t}\n"
+        ::"r"(d_tmem), "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sfa_tmem), "r"(sfb_tmem), "r"(accumulate)
+        : "memory");
+}
+// A plain matrix of 16-byte rows one after another, 32 rows into TMEM columns
+// taddr .. taddr + 3 of every lane quarter, before the MMAs issued after it.
+__device__ __forceinline__ void copy_factors(uint32_t taddr, uint32_t saddr) {
+    uint64_t d = static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4) | (1ull << 16) | (static_cast<uint64_t>(128 >> 4) << 32) | (1ull << 46);
+    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(d) : "memory");
+}
+
+template <int N, bool kCap>
+__global__ void __launch_bounds__(kThreads, 1)
+    weigh_kernel(const __grid_constant__ CUtensorMap tmK, const WeighParams wp) {
+    using L = Layout<N>;
+    extern __shared__ unsigned char smem_raw[];
+    unsigned char *smem =
+        reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint64_t *k_full = reinterpret_cast<uint64_t *>(smem + L::offBar), *k_empty = k_full + kKStages;
+    uint64_t *q_full = k_empty + kKStages, *q_empty = q_full + L::qstages;
+    uint64_t *s_full = q_empty + L::qstages, *s_empty = s_full + L::sbufs, *drain = s_empty + L::sbufs;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + L::offMisc);
+    int *abort_flag = reinterpret_cast<int *>(smem + L::offMisc + 4);
+    float2 *sSlot = reinterpret_cast<float2 *>(smem + L::offSlot);      // page (bits), its scale
+    const AttnParams &p = wp.a;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+    const int64_t all = all_work<N>(p), share = (all + gridDim.x - 1) / gridDim.x;
+    if (share * blockIdx.x >= all) return;
+    const Place from = find_place<N>(p, share * blockIdx.x);
+    const Place to = find_place<N>(p, min(all, share * (blockIdx.x + 1)));
+    if (to.linear <= from.linear) return;
+    Walk<N> wk;
+    wk.begin(p, from, to.linear - from.linear);
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kKStages; ++s) {
+            mbar_init(k_full + s, 1);
+            mbar_init(k_empty + s, 1);
+        }
+        for (int s = 0; s < L::qstages; ++s) {
+            mbar_init(q_full + s, 1);
+            mbar_init(q_empty + s, 1 + 8);       // the MMA's commit, the sum warps
+        }
+        for (int s = 0; s < L::sbufs; ++s) {
+            mbar_init(s_full + s, 2);            // the MMA's commit, the issuer itself
+            mbar_init(s_empty + s, 4);
+        }
+        mbar_init(drain, 1);
+        *abort_flag = 0;
+        mbar_fence_init();
+    }
+    if (warp == 1) {
+        tmem_alloc(tmem_slot, L::tmem_cols);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    // A's factors are 1 everywhere
+    if (warp >= 2 && warp < 6) {
+        asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1,%1,%1,%1};" ::"r"(
+                         tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + L::tmem_sfa), "r"(0x7f7f7f7fu) : "memory");
+        tmem_st_wait();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+
+    if (warp == 0) {
+        // ------------------------------------------------------------ producer
+        bool ok = true;
+        int kn = 0, qn = 0;      // pages and tiles issued
+        while (ok && wk.left > 0) {
+            const int kp = wk.count();
+            int page = -1;
+            float sk = 0.0f;
+            if (lane < kp) {
+                page = load_page(p.c, wk.b, wk.page + lane, p.dev_status);
+                if (page >= 0) sk = p.c.sk[static_cast<int64_t>(page) * p.c.H + wk.h];
+            }
+            for (int j = 0; ok && j < kp; ++j) {
+                const int pg = __shfl_sync(0xffffffffu, page, j), st = kn % kKStages;
+                const float ks = __shfl_sync(0xffffffffu, sk, j);
+                if (kn >= kKStages) ok = mbar_wait(k_empty + st, (kn / kKStages - 1) & 1, abort_flag, p.limit_ns);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
+                if (lane == 0) {
+                    sSlot[kn % kSlots] = make_float2(__int_as_float(pg), ks);
+                    if (pg >= 0) {
+                        mbar_expect_tx(k_full + st, kTile);
+                        tma_load_2d(smem + st * kTile, &tmK, k_full + st, 0, (pg * p.c.H + wk.h) * kBlk);
+                    } else {
+                        mbar_arrive(k_full + st);
+                    }
+                }
+                ++kn;
+            }
+            for (int t = first_tile<N>(p, wk.w.s, wk.page); ok && t < wk.w.tiles; ++t) {
+                const int st = qn % L::qstages;
+                if (qn >= L::qstages) ok = mbar_wait(q_empty + st, (qn / L::qstages - 1) & 1, abort_flag, p.limit_ns);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
+                if (lane == 0) {
+                    mbar_expect_tx(q_full + st, Image<N>::bytes);
+                    bulk_load(smem + L::offQ + st * Image<N>::stride,
+                              wp.images + (static_cast<int64_t>(wk.h) * wp.tiles + wk.tile0 + t) * Image<N>::stride,
+                              Image<N>::bytes, q_full + st);
+                }
+                ++qn;
+            }
+            if (ok) wk.next(p, kp);
+        }
+        // every copy issued has landed before the CTA can exit
+        if (lane == 0) {
+            for (int k = max(0, kn - kKStages); k < kn; ++k) drain_wait(k_full + k % kKStages, (k / kKStages) & 1, p.limit_ns);
+            for (int k = max(0, qn - L::qstages); k < qn; ++k)
+                drain_wait(q_full + k % L::qstages, (k / L::qstages) & 1, p.limit_ns);
+        }
+    } else if (warp == 1) {
+        // ------------------------------------------------------------ MMA issuer
+        if (lane == 0) {
+            const uint32_t sbase = smem_u32(smem);
+            bool ok = true;
+            int kn = 0, qn = 0, sn = 0;
+            while (ok && wk.left > 0) {
+                const int kp = wk.count();
+                int landed = 0;
+                for (int t = first_tile<N>(p, wk.w.s, wk.page); ok && t < wk.w.tiles; ++t, ++qn) {
+                    const int qs = qn % L::qstages;
+                    ok = mbar_wait_spin(q_full + qs, (qn / L::qstages) & 1, abort_flag, p.limit_ns);
+                    if (!ok) break;
+                    const uint32_t img = sbase + L::offQ + qs * Image<N>::stride, tsf = tmem + L::tmem_sfb + 8 * qs;
+                    copy_factors(tsf, img + Image<N>::sf);
+                    copy_factors(tsf + 4, img + Image<N>::sf + 512);
+                    const uint64_t dh = sdesc_k_sw128(img), dl = sdesc_k_sw128(img + Image<N>::lo);
+                    for (int j = 0; ok && j < kp; ++j) {
+                        if (t < first_tile<N>(p, wk.w.s, wk.page + j)) break;      // nor does a later page see it
+                        const int st = (kn + j) % kKStages, sb = sn % L::sbufs;
+                        if (j >= landed) {
+                            ok = mbar_wait_spin(k_full + st, ((kn + j) / kKStages) & 1, abort_flag, p.limit_ns);
+                            landed = j + 1;
+                        }
+                        if (ok && sn >= L::sbufs) ok = mbar_wait_spin(s_empty + sb, (sn / L::sbufs - 1) & 1, abort_flag, p.limit_ns);
+                        if (!ok) break;
+                        tc_fence_after();
+                        const uint64_t dk = sdesc_k_sw128(sbase + st * kTile);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            mma_mxf8_ss(tmem + sb * N, dk + 2 * i, dh + 2 * i, make_idesc_mxf8_b(128, N, i), tmem + L::tmem_sfa,
+                                        tsf, i > 0);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            mma_mxf8_ss(tmem + sb * N, dk + 2 * i, dl + 2 * i, make_idesc_mxf8_b(128, N, i), tmem + L::tmem_sfa,
+                                        tsf + 4, 1u);
+                        if (t + 1 == wk.w.tiles) tc_commit(k_empty + st);
+                        tc_commit(s_full + sb);
+                        mbar_arrive(s_full + sb);
+                        ++sn;
+                    }
+                    if (ok) tc_commit(q_empty + qs);
+                }
+                kn += kp;
+                if (ok) wk.next(p, kp);
+            }
+            tc_commit(drain);
+            drain_wait(drain, 0, p.limit_ns);
+        }
+    } else {
+        // ------------------------------------------------------------ sums
+        const int set = (warp - 2) >> 2, quarter = warp & 3, row = quarter * 32 + lane;
+        const uint32_t tl = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
+        bool ok = true;
+        int kn = 0, qn = 0, sn = 0;
+        while (ok && wk.left > 0) {
+            const int kp = wk.count();
+            float acc[kKP / 2] = {};
+            int page[kKP / 2] = {-1, -1};
+            for (int t = first_tile<N>(p, wk.w.s, wk.page); ok && t < wk.w.tiles; ++t, ++qn) {
+                const int qs = qn % L::qstages;
+                ok = __all_sync(0xffffffffu, mbar_wait(q_full + qs, (qn / L::qstages) & 1, abort_flag, p.limit_ns));
+                if (!ok) break;
+                const unsigned char *img = smem + L::offQ + qs * Image<N>::stride;
+                const ulonglong2 *consts = reinterpret_cast<const ulonglong2 *>(img + Image<N>::consts);
+                const int *seen = reinterpret_cast<const int *>(img + Image<N>::seen);
+                const int all_see = seen_by_row(p, wk.w.s, t * N);
+#pragma unroll
+                for (int j = 0; j < kKP; ++j) {
+                    if (!ok || j >= kp || t < first_tile<N>(p, wk.w.s, wk.page + j)) break;
+                    const int sb = sn % L::sbufs, phase = (sn / L::sbufs) & 1;
+                    ++sn;
+                    if ((j & 1) != set) continue;
+                    ok = __all_sync(0xffffffffu, mbar_wait(s_full + sb, phase, abort_flag, p.limit_ns));
+                    if (!ok) break;
+                    tc_fence_after();
+                    const float2 slot = sSlot[(kn + j) % kSlots];      // rewritten once its page's S is given back
+                    page[j >> 1] = __float_as_int(slot.x);
+                    const float sk = slot.y;
+                    const uint64_t sk2 = pk2(__float_as_uint(sk), __float_as_uint(sk));
+                    const int key = (wk.page + j) * kBlk + row;
+                    const bool edge = (wk.page + j + 1) * kBlk > all_see;
+                    uint64_t sum2 = 0;
+#pragma unroll 1
+                    for (int c = 0; c < N; c += 32) {
+                        uint32_t X[32];
+                        if constexpr (N == 16) {
+                            float unused;
+                            VCA_TMEM_LDMAX16(tl + sb * N, X, unused);
+                        } else {
+                            VCA_TMEM_LD32(tl + sb * N + c, X);
+                        }
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int k = 0; k < (N == 16 ? 8 : 16); ++k) {
+                            const ulonglong2 cc = consts[c / 2 + k];     // two rows' factors, their -lse
+                            const uint64_t s2 = mul2(pk2(X[2 * k], X[2 * k + 1]), sk2);
+                            float a, b;
+                            if constexpr (kCap) {
+                                float u, v, lu, lv;
+                                upk2(mul2(s2, cc.x), u, v);
+                                upk2(cc.y, lu, lv);
+                                a = capped(u, p.cap_out) + lu;
+                                b = capped(v, p.cap_out) + lv;
+                            } else {
+                                upk2(fma2(s2, cc.x, cc.y), a, b);
+                            }
+                            a = ex2_approx(a);
+                            b = ex2_approx(b);
+                            if (edge) {
+                                if (key >= seen[c + 2 * k]) a = 0.0f;
+                                if (key >= seen[c + 2 * k + 1]) b = 0.0f;
+                            }
+                            sum2 = add2(sum2, pk2(__float_as_uint(a), __float_as_uint(b)));
+                        }
+                    }
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(s_empty + sb);
+                    float a, b;
+                    upk2(sum2, a, b);
+                    acc[j >> 1] += a + b;
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(q_empty + qs);
+            }
+            if (!ok) break;
+#pragma unroll
+            for (int i = 0; i < kKP / 2; ++i) {
+                if (page[i] >= 0 && (wk.page + 2 * i + set) * kBlk + row < wk.w.s.len)
+                    atomicAdd(wp.weight + (static_cast<int64_t>(page[i]) * p.c.H + wk.h) * kBlk + row, acc[i]);
+            }
+            kn += kp;
+            wk.next(p, kp);
+        }
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem, L::tmem_cols);
+    }
+    if (threadIdx.x == 0 && *reinterpret_cast<volatile int *>(abort_flag)) report(p.dev_status, kErrTimeout);
+}
+
+// Tiles of 16 rows where a sequence and KV head have no more than that on average.
+bool few_rows(int T, int Hq, int H, int B) { return static_cast<int64_t>(T) * (Hq / H) <= 16ll * B; }
+int64_t tiles_at_most(int T, int Hq, int H, int B) {
+    return static_cast<int64_t>(T) * (Hq / H) / (few_rows(T, Hq, H, B) ? 16 : 128) + (B < T ? B : T);
+}
+
+template <int N>
+cudaError_t launch(const CacheWeighArgs &a, const WeighParams &wp, cudaStream_t st) {
+    CUtensorMap mk;
+    if (!make_tile_map(&mk, a.c.k8, static_cast<uint64_t>(a.c.pages) * a.c.H * kBlk)) return cudaErrorInvalidValue;
+    const auto kernel = a.softcap > 0.0f ? weigh_kernel<N, true> : weigh_kernel<N, false>;
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Layout<N>::smem);
+    if (e != cudaSuccess) return e;
+    image_kernel<N><<<dim3(wp.tiles, a.c.H), 256, 0, st>>>(wp);
+    e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    const int64_t pages = static_cast<int64_t>(a.c.cols) * a.c.B * a.c.H;
+    kernel<<<static_cast<unsigned>(pages < 152 ? pages : 152), kThreads, Layout<N>::smem, st>>>(mk, wp);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+size_t cache_weigh_workspace(int T, int Hq, int H, int B, int cols) {
+    (void)cols;
+    return static_cast<size_t>(tiles_at_most(T, Hq, H, B)) * H *
+           (few_rows(T, Hq, H, B) ? Image<16>::stride : Image<128>::stride);
+}
+
+cudaError_t launch_cache_weigh(const CacheWeighArgs &a, cudaStream_t st) {
+    WeighParams wp;
+    wp.a = attn_params(a.c, a.q, a.start, a.T, a.Hq, a.causal, a.scale, a.softcap, a.dev_status, a.wait_limit_ns);
+    wp.lse = a.lse;
+    wp.weight = a.weight;
+    wp.images = static_cast<uint8_t *>(a.ws);
+    wp.tiles = static_cast<int>(tiles_at_most(a.T, a.Hq, a.c.H, a.c.B));
+    return few_rows(a.T, a.Hq, a.c.H, a.c.B) ? launch<16>(a, wp, st) : launch<128>(a, wp, st);
+}
+
+}  // namespace vca
