@@ -7,7 +7,7 @@
 //   lse = ln 2 (m + log2 l), m the running maximum.
 //
 // The query rows of one (sequence, KV head) -- its new tokens times the G query
-// heads that share the KV head -- are cut into tiles of 16.  The work is the
+// heads that share the KV head -- are cut into tiles of 8 or 16.  The work is the
 // list of all (sequence, KV head, tile, page) units in that order; each CTA
 // takes an equal share of consecutive units, whatever the sequences' lengths,
 // and writes an (O, m, l) partial where a tile's pages are shared between CTAs;
@@ -15,10 +15,16 @@
 // give equal bits.
 //
 // One producer warp keeps a ring of pages (K and V tile, 16 KB each, one TMA
-// load per tile) full across tile borders.  Eight consumer warps take 16 keys of
-// every page each, with a running maximum, sum and O of their own, which they
-// merge at a tile's end: no barrier but the ring's in between.  Both products
-// are m16n8k16 MMAs on fp16: an E4M3 code is exact in fp16, and so is a bf16
+// load per tile) full across tile borders; their table entries and scales are
+// loaded two batches ahead, since a load under full traffic takes longer than a
+// page.  Eight consumer warps take 16 keys of every page each, with a running
+// maximum, sum and O of their own, which they merge at a tile's end: no barrier
+// but the ring's in between.
+//
+// Both products are m16n8k16 MMAs on fp16 with the long side as rows, so that
+// eight query rows fill a tile: S^T = K Q^T (16 keys x 8 rows), then O^T = V^T P^T
+// (16 channels x 8 rows), P^T being S^T's registers after an 8 x 8 transpose.  The
+// codes are the A operands: an E4M3 code is exact in fp16, and so is a bf16
 // query row after a power-of-two scaling that puts its largest element at 2^13
 // (elements below 2^-30 of it lose bits); P is rounded to fp16 (2^-12
 // relative), while l sums the unrounded values.
@@ -31,24 +37,27 @@ namespace {
 
 using namespace cache;
 
-constexpr int kRows = 16;                       // query rows of a tile
 constexpr int kWarps = 8;                       // consumer warps
 constexpr int kThreads = 32 * (kWarps + 1);
 constexpr int kKeys = kBlk / kWarps;            // keys of a page per warp
-constexpr int kStages = 4;
 constexpr uint32_t kTile = kBlk * kD;           // bytes of one K or V tile
 constexpr int kSmallest = 2;                    // units a CTA takes at least
 
-// One partial: O [16][128], m [16], l [16].
-constexpr int kPartFloats = kRows * kD + 2 * kRows;
+// One partial of a tile of `rows` rows: O [rows][128], m [rows], l [rows].
+__host__ __device__ constexpr int part_floats(int rows) { return rows * kD + 2 * rows; }
 
-constexpr uint32_t kOffRing = 0;
-constexpr uint32_t kOffMerge = kOffRing + kStages * 2 * kTile;       // fp32 [8][16][128]
-constexpr uint32_t kOffML = kOffMerge + kWarps * kRows * kD * 4;     // fp32 [8][16] m, [8][16] l
-constexpr uint32_t kOffScale = kOffML + 2 * kWarps * kRows * 4;      // fp32 [stages][2]
-constexpr uint32_t kOffBar = kOffScale + kStages * 8;
-constexpr uint32_t kSmem = kOffBar + 2 * kStages * 8 + 16 + 1024;
-static_assert(kSmem <= 232448, "shared memory budget");
+// Shared memory: the ring, the warps' O, m and l of a tile of kRows rows, the
+// pages' scales, barriers.  Eight rows leave room for a longer ring.
+template <int kRows>
+struct Smem {
+    static constexpr int stages = kRows == 8 ? 5 : 4;
+    static constexpr uint32_t merge = stages * 2 * kTile;               // fp32 [8][rows][128]
+    static constexpr uint32_t ml = merge + kWarps * kRows * kD * 4;     // fp32 [8][rows] m, [8][rows] l
+    static constexpr uint32_t scale = ml + 2 * kWarps * kRows * 4;      // fp32 [stages][2]
+    static constexpr uint32_t bar = scale + stages * 8;
+    static constexpr uint32_t bytes = bar + 2 * stages * 8 + 16 + 1024;
+    static_assert(bytes <= 232448, "shared memory budget");
+};
 
 // ---------------------------------------------------------------------------
 // The list of units
@@ -59,6 +68,7 @@ struct Shape {
     Seq s;
     int tiles, pages;
 };
+template <int kRows>
 __device__ __forceinline__ Shape shape_of(const AttnParams &p, int b) {
     Shape x;
     x.s = load_seq(p.c, p.start, p.T, b);
@@ -81,11 +91,12 @@ __device__ __forceinline__ int64_t warp_incl_scan(int64_t v) {
 }
 
 // Units of all sequences (a warp's work).
+template <int kRows>
 __device__ int64_t count_units(const AttnParams &p) {
     int64_t all = 0;
     for (int b0 = 0; b0 < p.c.B; b0 += 32) {
         const int b = b0 + static_cast<int>(threadIdx.x & 31);
-        int64_t v = b < p.c.B ? units_of(p, shape_of(p, b)) : 0;
+        int64_t v = b < p.c.B ? units_of(p, shape_of<kRows>(p, b)) : 0;
         all += __shfl_sync(0xffffffffu, warp_incl_scan(v), 31);
     }
     return all;
@@ -98,12 +109,13 @@ __device__ __forceinline__ int64_t share_of(int64_t all, int ctas) {
 }
 
 // Where unit u lies: sequence, and the unit's place among the sequence's.
+template <int kRows>
 __device__ void find_unit(const AttnParams &p, int64_t u, int &b_out, int64_t &local) {
     int64_t before = 0;
     const int lane = threadIdx.x & 31;
     for (int b0 = 0; b0 < p.c.B; b0 += 32) {
         const int b = b0 + lane;
-        const int64_t v = b < p.c.B ? units_of(p, shape_of(p, b)) : 0;
+        const int64_t v = b < p.c.B ? units_of(p, shape_of<kRows>(p, b)) : 0;
         const int64_t incl = warp_incl_scan(v) + before;
         const uint32_t hit = __ballot_sync(0xffffffffu, u < incl);
         if (hit) {
@@ -119,6 +131,7 @@ __device__ void find_unit(const AttnParams &p, int64_t u, int &b_out, int64_t &l
 }
 
 // A CTA's walk over its units, one (sequence, head, tile) at a time.
+template <int kRows>
 struct Walk {
     int b, h, tile, page;      // the next unit
     int64_t left;              // units left in the share
@@ -127,7 +140,7 @@ struct Walk {
         b = b_;
         left = units;
         if (b < p.c.B) {
-            x = shape_of(p, b);
+            x = shape_of<kRows>(p, b);
             h = static_cast<int>(local / (static_cast<int64_t>(x.tiles) * x.pages));
             const int64_t r = local - static_cast<int64_t>(h) * x.tiles * x.pages;
             tile = static_cast<int>(r / x.pages);
@@ -148,7 +161,7 @@ struct Walk {
         do {
             ++b;
             if (b >= p.c.B) return;
-            x = shape_of(p, b);
+            x = shape_of<kRows>(p, b);
         } while (x.tiles == 0 || x.pages == 0);
     }
 };
@@ -178,6 +191,13 @@ __device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
 }
 __device__ __forceinline__ uint4 lds128(const unsigned char *p) { return *reinterpret_cast<const uint4 *>(p); }
 
+// 8 x 8 transpose of 16-bit elements held as an MMA fragment.
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+    uint32_t d;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(x));
+    return d;
+}
+
 // The 32 channels t * 32 .. t * 32 + 31 of one query row as fp16 pairs, scaled
 // by a power of two; returns the factor's inverse.  All four threads of a quad
 // hold a quarter of the same row.
@@ -187,9 +207,9 @@ __device__ __forceinline__ float load_q(const AttnParams &p, const Seq &s, int h
 #pragma unroll
     for (int i = 0; i < 4; ++i) v[i] = make_uint4(0, 0, 0, 0);
     if (real) {
-        const uint16_t *at = p.q.p + (s.row0 + r / p.G) * p.q.tok + (h * p.G + r % p.G) * p.q.head + t * 32;
+        const uint4 *at = reinterpret_cast<const uint4 *>(query_row(p, s, h, r) + t * 32);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) v[i] = reinterpret_cast<const uint4 *>(at)[i];
+        for (int i = 0; i < 4; ++i) v[i] = at[i];
     }
     uint32_t m = 0;
 #pragma unroll
@@ -209,14 +229,71 @@ __device__ __forceinline__ float load_q(const AttnParams &p, const Seq &s, int h
     return __uint_as_float(static_cast<uint32_t>(127 - 13 + e) << 23);
 }
 
+// The pages of a share and their scales, in order, for a whole warp: three
+// batches of up to 32 pages of one tile, one page per lane -- the one being
+// used, one whose scales are being loaded, one whose table entries are.
+template <int kRows>
+struct Feed {
+    Walk<kRows> ahead;
+    int page[3], count[3], head[3], used;
+    float sk[2], sv[2];
+    __device__ void begin(const AttnParams &p, const Walk<kRows> &w) {
+        ahead = w;
+        used = 0;
+#pragma unroll
+        for (int i = 0; i < 3; ++i) fetch(p, i);
+        scales(p, 0);
+        scales(p, 1);
+    }
+    __device__ void fetch(const AttnParams &p, int i) {
+        page[i] = -1;
+        count[i] = head[i] = 0;
+        if (ahead.left <= 0) return;
+        count[i] = min(32, ahead.run());
+        head[i] = ahead.h;
+        const int lane = threadIdx.x & 31;
+        if (lane < count[i] && ahead.x.s.len > 0) page[i] = load_page(p.c, ahead.b, ahead.page + lane, p.dev_status);
+        ahead.next(p, count[i]);
+    }
+    __device__ void scales(const AttnParams &p, int i) {
+        const int64_t at = static_cast<int64_t>(page[i]) * p.c.H + head[i];
+        sk[i] = page[i] >= 0 ? p.c.sk[at] : -1.0f;      // -1: no page
+        sv[i] = page[i] >= 0 ? p.c.sv[at] : 0.0f;
+    }
+    // The next page: its tile's first row of codes (negative: no page) and its scales.
+    __device__ void take(const AttnParams &p, int &y, float &ks, float &vs) {
+        if (used == count[0]) {
+            used = 0;
+            page[0] = page[1];
+            count[0] = count[1];
+            head[0] = head[1];
+            sk[0] = sk[1];
+            sv[0] = sv[1];
+            page[1] = page[2];
+            count[1] = count[2];
+            head[1] = head[2];
+            scales(p, 1);
+            fetch(p, 2);
+        }
+        const int pg = __shfl_sync(0xffffffffu, page[0], used);
+        y = pg < 0 ? -1 : (pg * p.c.H + head[0]) * kBlk;
+        ks = __shfl_sync(0xffffffffu, sk[0], used);
+        vs = __shfl_sync(0xffffffffu, sv[0], used);
+        ++used;
+    }
+};
+
+template <int kRows>
 __global__ void __launch_bounds__(kThreads, 1)
     decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, const AttnParams p) {
+    constexpr int NT = kRows / 8;               // groups of eight query rows
+    constexpr int kStages = Smem<kRows>::stages;
     extern __shared__ unsigned char smem_raw[];
     unsigned char *smem =
         reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    uint64_t *full = reinterpret_cast<uint64_t *>(smem + kOffBar), *empty = full + kStages;
+    uint64_t *full = reinterpret_cast<uint64_t *>(smem + Smem<kRows>::bar), *empty = full + kStages;
     int *abort_flag = reinterpret_cast<int *>(empty + kStages);
-    float *sScale = reinterpret_cast<float *>(smem + kOffScale);
+    float *sScale = reinterpret_cast<float *>(smem + Smem<kRows>::scale);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
     if (threadIdx.x == 0) {
@@ -228,7 +305,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_fence_init();
     }
     __syncthreads();
-    const int64_t all = count_units(p), share = share_of(all, gridDim.x);
+    const int64_t all = count_units<kRows>(p), share = share_of(all, gridDim.x);
     const int64_t u0 = share * blockIdx.x, u1 = min(all, u0 + share);
     if (blockIdx.x == 0 && warp == 0)
         for (int b = lane; b < p.c.B; b += 32)
@@ -236,54 +313,41 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (u0 >= u1) return;
     int b0;
     int64_t local;
-    find_unit(p, u0, b0, local);
-    Walk w;
+    find_unit<kRows>(p, u0, b0, local);
+    Walk<kRows> w;
     w.begin(p, b0, local, u1 - u0);
 
     if (warp == kWarps) {
         // ------------------------------------------------------------ producer
-        int stage = 0, round = 0, armed = 0;
+        int stage = 0, round = 0;
+        const int units = static_cast<int>(u1 - u0);
+        int armed = 0;
         bool ok = true;
-        while (ok && w.left > 0) {
-            const int run = w.run();
-            for (int i0 = 0; ok && i0 < run; i0 += 32) {
-                // the next 32 pages and their scales, one per lane
-                int page = -1;
-                float sk = 0.0f, sv = 0.0f;
-                if (i0 + lane < run && w.x.s.len > 0) {
-                    page = load_page(p.c, w.b, w.page + i0 + lane, p.dev_status);
-                    if (page >= 0) {
-                        sk = p.c.sk[static_cast<int64_t>(page) * p.c.H + w.h];
-                        sv = p.c.sv[static_cast<int64_t>(page) * p.c.H + w.h];
-                    }
-                }
-                for (int i = 0; i < 32 && i0 + i < run; ++i) {
-                    const int pg = __shfl_sync(0xffffffffu, page, i);
-                    const float ks = __shfl_sync(0xffffffffu, sk, i), vs = __shfl_sync(0xffffffffu, sv, i);
-                    if (round > 0) ok = mbar_wait(empty + stage, (round - 1) & 1, abort_flag, p.limit_ns);
-                    ok = __all_sync(0xffffffffu, ok);
-                    if (!ok) break;
-                    if (lane == 0) {
-                        sScale[2 * stage] = pg >= 0 ? ks : -1.0f;     // -1: no page
-                        sScale[2 * stage + 1] = vs;
-                        if (pg >= 0) {
-                            unsigned char *at = smem + kOffRing + stage * 2 * kTile;
-                            const int y = (pg * p.c.H + w.h) * kBlk;
-                            mbar_expect_tx(full + stage, 2 * kTile);
-                            tma_load_2d(at, &tmK, full + stage, 0, y);
-                            tma_load_2d(at + kTile, &tmV, full + stage, 0, y);
-                        } else {
-                            mbar_arrive(full + stage);
-                        }
-                    }
-                    armed = round * kStages + stage + 1;
-                    if (++stage == kStages) {
-                        stage = 0;
-                        ++round;
-                    }
+        Feed<kRows> feed;
+        feed.begin(p, w);
+        for (int i = 0; i < units; ++i) {
+            int y;
+            float ks, vs;
+            feed.take(p, y, ks, vs);
+            if (round > 0) ok = mbar_wait(empty + stage, (round - 1) & 1, abort_flag, p.limit_ns);
+            if (!__all_sync(0xffffffffu, ok)) break;
+            if (lane == 0) {
+                sScale[2 * stage] = ks;
+                sScale[2 * stage + 1] = vs;
+                if (y >= 0) {
+                    unsigned char *at = smem + stage * 2 * kTile;
+                    mbar_expect_tx(full + stage, 2 * kTile);
+                    tma_load_2d(at, &tmK, full + stage, 0, y);
+                    tma_load_2d(at + kTile, &tmV, full + stage, 0, y);
+                } else {
+                    mbar_arrive(full + stage);
                 }
             }
-            if (ok) w.next(p, run);
+            armed = i + 1;
+            if (++stage == kStages) {
+                stage = 0;
+                ++round;
+            }
         }
         // every copy issued has landed before the CTA can exit
         if (lane == 0)
@@ -291,9 +355,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 attn::drain_wait(full + k % kStages, (k / kStages) & 1, p.limit_ns);
     } else {
         // ------------------------------------------------------------ consumers
+        // fragments: g and t are the row (key, channel or query row) and the pair of a quad
         const int g = lane >> 2, t = lane & 3;
-        float *sMerge = reinterpret_cast<float *>(smem + kOffMerge);
-        float *sM = reinterpret_cast<float *>(smem + kOffML), *sL = sM + kWarps * kRows;
+        float *sMerge = reinterpret_cast<float *>(smem + Smem<kRows>::merge);
+        float *sM = reinterpret_cast<float *>(smem + Smem<kRows>::ml), *sL = sM + kWarps * kRows;
         int stage = 0, round = 0;
         bool ok = true;
         const float kNegInf = __int_as_float(0xff800000);
@@ -301,23 +366,32 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int run = w.run();
             const Seq s = w.x.s;
             const int R = s.n * p.G, r0 = w.tile * kRows;
-            uint32_t q[2][16];
-            float f[2];
-            int seen[2];
+            // Q: the B operand, row 8 n + g; this thread's scores are of the rows 8 n + 2 t and + 1
+            uint32_t q[NT][16];
+            float f[NT][2], m[NT][2], l[NT][2];
+            int seen[NT][2];
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const int r = r0 + g + 8 * i;
-                const float down = load_q(p, s, w.h, r, t, q[i]);
-                f[i] = __fmul_rn(p.cap_out != 0.0f ? p.cap_in : p.scale_log2, down);
-                seen[i] = r < R ? seen_by_row(p, s, r) : 0;
+            for (int n = 0; n < NT; ++n) {
+                const float down = load_q(p, s, w.h, r0 + 8 * n + g, t, q[n]);
+                const float fg = __fmul_rn(p.cap_out != 0.0f ? p.cap_in : p.scale_log2, down);
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int r = r0 + 8 * n + 2 * t + e;
+                    f[n][e] = __shfl_sync(0xffffffffu, fg, (2 * t + e) * 4);
+                    seen[n][e] = r < R ? seen_by_row(p, s, r) : 0;
+                    m[n][e] = kNegInf;
+                    l[n][e] = 0.0f;
+                }
             }
             const int all_see = seen_by_row(p, s, r0);      // keys below this are seen by every row of the tile
-            float m[2] = {kNegInf, kNegInf}, l[2] = {0.0f, 0.0f};
-            float o[16][4];
+            // O^T: channel 16 g + 2 j (elements 0, 1) and 16 g + 2 j + 1 (2, 3) of the rows 2 t, 2 t + 1
+            float o[NT][8][4];
 #pragma unroll
-            for (int j = 0; j < 16; ++j)
+            for (int n = 0; n < NT; ++n)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) o[j][e] = 0.0f;
+                for (int j = 0; j < 8; ++j)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) o[n][j][e] = 0.0f;
 
             for (int i = 0; i < run; ++i) {
                 if (ok) ok = mbar_wait(full + stage, round & 1, abort_flag, p.limit_ns);
@@ -325,83 +399,88 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (!ok) break;
                 const float sk = sScale[2 * stage], sv = sScale[2 * stage + 1];
                 const int key0 = (w.page + i) * kBlk + kKeys * warp;
-                const bool edge = key0 + kKeys > all_see;
-                // the last page's slots behind the last token may hold anything
-                const bool tail = key0 + kKeys > s.len;
                 if (sk >= 0.0f && key0 < s.len) {
-                    const unsigned char *sK = smem + kOffRing + stage * 2 * kTile, *sV = sK + kTile;
-                    float S[2][4];
+                    const unsigned char *sK = smem + stage * 2 * kTile, *sV = sK + kTile;
+                    float S[NT][4];
 #pragma unroll
-                    for (int j = 0; j < 2; ++j) {
-                        const int key = kKeys * warp + 8 * j + g;
-                        uint32_t kw[8];
-                        *reinterpret_cast<uint4 *>(kw) = lds128(sK + sw128_offset(key, 2 * t));
-                        *reinterpret_cast<uint4 *>(kw + 4) = lds128(sK + sw128_offset(key, 2 * t + 1));
+                    for (int n = 0; n < NT; ++n)
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) S[j][e] = 0.0f;
+                        for (int e = 0; e < 4; ++e) S[n][e] = 0.0f;
+                    // K: keys g and g + 8; the four codes of a word are channels 32 t + 4 k .. + 3
 #pragma unroll
-                        for (int k = 0; k < 8; ++k) {
-                            uint32_t lo, hi;
-                            codes_to_half(kw[k], lo, hi);
-                            const uint32_t a[4] = {q[0][2 * k], q[1][2 * k], q[0][2 * k + 1], q[1][2 * k + 1]};
-                            mma16816(S[j], a, lo, hi);
+                    for (int half = 0; half < 2; ++half) {
+                        uint32_t ka[4], kb[4];
+                        *reinterpret_cast<uint4 *>(ka) = lds128(sK + sw128_offset(kKeys * warp + g, 2 * t + half));
+                        *reinterpret_cast<uint4 *>(kb) = lds128(sK + sw128_offset(kKeys * warp + 8 + g, 2 * t + half));
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            uint32_t a[4];
+                            codes_to_half(ka[k], a[0], a[2]);
+                            codes_to_half(kb[k], a[1], a[3]);
+#pragma unroll
+                            for (int n = 0; n < NT; ++n) mma16816(S[n], a, q[n][8 * half + 2 * k], q[n][8 * half + 2 * k + 1]);
                         }
                     }
                     uint32_t vw[4][4];
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const int tok = kKeys * warp + 2 * t + (k & 1) + 8 * (k >> 1);
-                        uint4 x = lds128(sV + sw128_offset(tok, g));
-                        if (tail && (w.page + i) * kBlk + tok >= s.len) x = make_uint4(0, 0, 0, 0);
-                        *reinterpret_cast<uint4 *>(vw[k]) = x;
-                    }
-                    // scores in log2 units, the running maximum, P
-                    float mx[2] = {m[0], m[1]};
+                    for (int k = 0; k < 4; ++k)
+                        *reinterpret_cast<uint4 *>(vw[k]) =
+                            lds128(sV + sw128_offset(kKeys * warp + 2 * t + (k & 1) + 8 * (k >> 1), g));
+                    // the last page's slots behind the last token may hold anything
+                    if (key0 + kKeys > s.len) {
 #pragma unroll
-                    for (int j = 0; j < 2; ++j)
+                        for (int k = 0; k < 4; ++k)
+                            if (key0 + 2 * t + (k & 1) + 8 * (k >> 1) >= s.len)
+                                vw[k][0] = vw[k][1] = vw[k][2] = vw[k][3] = 0u;
+                    }
+                    // scores in log2 units, the running maximum, P; element e: key g + 8 (e >> 1), row 2 t + (e & 1)
+                    const bool edge = key0 + kKeys > all_see;
+                    uint32_t pb[NT][2];
+                    float alpha[NT][2];
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) {
+                        float mx[2] = {m[n][0], m[n][1]};
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
-                            float x = scored(S[j][e], f[e >> 1] * sk, p.cap_out);
-                            if (edge && key0 + 8 * j + 2 * t + (e & 1) >= seen[e >> 1]) x = kNegInf;
-                            S[j][e] = x;
-                            mx[e >> 1] = fmaxf(mx[e >> 1], x);
+                            float x = scored(S[n][e], f[n][e & 1] * sk, p.cap_out);
+                            if (edge && key0 + g + 8 * (e >> 1) >= seen[n][e & 1]) x = kNegInf;
+                            S[n][e] = x;
+                            mx[e & 1] = fmaxf(mx[e & 1], x);
                         }
-                    float alpha[2], mu[2];
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], 1));
-                        mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], 2));
-                        mu[e] = mx[e] == kNegInf ? 0.0f : mx[e];      // a row that sees nothing yet
-                        alpha[e] = ex2_approx(m[e] - mu[e]);
-                        l[e] *= alpha[e];
-                        m[e] = mx[e];
+                        for (int e = 0; e < 2; ++e) {
+                            mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], 4));
+                            mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], 8));
+                            mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], 16));
+                            const float mu = mx[e] == kNegInf ? 0.0f : mx[e];      // a row that sees nothing yet
+                            alpha[n][e] = ex2_approx(m[n][e] - mu);
+                            m[n][e] = mx[e];
+                            S[n][e] = ex2_approx(S[n][e] - mu);
+                            S[n][e + 2] = ex2_approx(S[n][e + 2] - mu);
+                            l[n][e] = fmaf(l[n][e], alpha[n][e], S[n][e] + S[n][e + 2]);
+                        }
+                        pb[n][0] = transpose8x8(pack_half2(S[n][0], S[n][1]));
+                        pb[n][1] = transpose8x8(pack_half2(S[n][2], S[n][3]));
                     }
-#pragma unroll
-                    for (int j = 0; j < 2; ++j)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            S[j][e] = ex2_approx(S[j][e] - mu[e >> 1]);
-                            l[e >> 1] += S[j][e];
-                        }
-                    const uint32_t a[4] = {pack_half2(S[0][0], S[0][1]), pack_half2(S[0][2], S[0][3]),
-                                           pack_half2(S[1][0], S[1][1]), pack_half2(S[1][2], S[1][3])};
                     // this page's P V in the codes' units, then O = O alpha + sv (P V): the page
                     // scales may differ by any power of two
+                    const uint64_t sv2 = pk2(__float_as_uint(sv), __float_as_uint(sv));
 #pragma unroll
-                    for (int n = 0; n < 16; n += 2) {
-                        const uint32_t sel = (n & 2) ? 0x7362u : 0x5140u;
-                        const uint32_t b01 = prmt(vw[0][n >> 2], vw[1][n >> 2], sel);
-                        const uint32_t b89 = prmt(vw[2][n >> 2], vw[3][n >> 2], sel);
-                        uint32_t x0, x1, y0, y1;
-                        codes_to_half(b01, x0, x1);
-                        codes_to_half(b89, y0, y1);
-                        float d0[4] = {0.0f, 0.0f, 0.0f, 0.0f}, d1[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-                        mma16816(d0, a, x0, y0);
-                        mma16816(d1, a, x1, y1);
+                    for (int j = 0; j < 8; ++j) {
+                        const uint32_t sel = (j & 1) ? 0x7362u : 0x5140u;
+                        uint32_t a[4];
+                        codes_to_half(prmt(vw[0][j >> 1], vw[1][j >> 1], sel), a[0], a[1]);
+                        codes_to_half(prmt(vw[2][j >> 1], vw[3][j >> 1], sel), a[2], a[3]);
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            o[n][e] = fmaf(d0[e], sv, o[n][e] * alpha[e >> 1]);
-                            o[n + 1][e] = fmaf(d1[e], sv, o[n + 1][e] * alpha[e >> 1]);
+                        for (int n = 0; n < NT; ++n) {
+                            float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                            mma16816(d, a, pb[n][0], pb[n][1]);
+                            const uint64_t al = pk2(__float_as_uint(alpha[n][0]), __float_as_uint(alpha[n][1]));
+#pragma unroll
+                            for (int e = 0; e < 4; e += 2)
+                                upk2(fma2(pk2(__float_as_uint(d[e]), __float_as_uint(d[e + 1])), sv2,
+                                          mul2(pk2(__float_as_uint(o[n][j][e]), __float_as_uint(o[n][j][e + 1])), al)),
+                                     o[n][j][e], o[n][j][e + 1]);
                         }
                     }
                 }
@@ -414,66 +493,66 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             // ---- the warps' (O, m, l) merged: each writes its own, all add them up
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                l[e] += __shfl_xor_sync(0xffffffffu, l[e], 1);
-                l[e] += __shfl_xor_sync(0xffffffffu, l[e], 2);
-                if (t == 0) {
-                    sM[warp * kRows + g + 8 * e] = m[e];
-                    sL[warp * kRows + g + 8 * e] = l[e];
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    l[n][e] += __shfl_xor_sync(0xffffffffu, l[n][e], 4);
+                    l[n][e] += __shfl_xor_sync(0xffffffffu, l[n][e], 8);
+                    l[n][e] += __shfl_xor_sync(0xffffffffu, l[n][e], 16);
+                    const int r = 8 * n + 2 * t + e;
+                    if (g == 0) {
+                        sM[warp * kRows + r] = m[n][e];
+                        sL[warp * kRows + r] = l[n][e];
+                    }
+                    float4 *at = reinterpret_cast<float4 *>(sMerge + (warp * kRows + r) * kD + 16 * g);
+#pragma unroll
+                    for (int j = 0; j < 8; j += 2)
+                        at[j / 2] = make_float4(o[n][j][e], o[n][j][e + 2], o[n][j + 1][e], o[n][j + 1][e + 2]);
                 }
-            }
-            // column 16 g' + n of the row: the n-th tile's column g', here g' = 2 t + (e & 1)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                float *at = sMerge + (warp * kRows + g + 8 * (e >> 1)) * kD + 16 * (2 * t + (e & 1));
-#pragma unroll
-                for (int n = 0; n < 16; n += 4)
-                    *reinterpret_cast<float4 *>(at + n) = make_float4(o[n][e], o[n + 1][e], o[n + 2][e], o[n + 3][e]);
-            }
             ok = attn::bar_and(ok, 1, 32 * kWarps);
             if (!ok) break;
             {
-                const int r = threadIdx.x >> 4, ch = (threadIdx.x & 15) * 8;     // row, eight channels
+                constexpr int kCh = kRows * kD / (32 * kWarps);      // channels a thread adds up
+                const int r = threadIdx.x / (kD / kCh), ch = threadIdx.x % (kD / kCh) * kCh;
                 float M = kNegInf;
 #pragma unroll
                 for (int i = 0; i < kWarps; ++i) M = fmaxf(M, sM[i * kRows + r]);
                 const float Mu = M == kNegInf ? 0.0f : M;
-                float L = 0.0f, acc[8] = {};
+                float L = 0.0f, acc[kCh] = {};
 #pragma unroll
                 for (int i = 0; i < kWarps; ++i) {
                     const float k = ex2_approx(sM[i * kRows + r] - Mu);
                     L = fmaf(sL[i * kRows + r], k, L);
                     const float4 *at = reinterpret_cast<const float4 *>(sMerge + (i * kRows + r) * kD + ch);
-                    const float4 x = at[0], y = at[1];
-                    acc[0] = fmaf(x.x, k, acc[0]);
-                    acc[1] = fmaf(x.y, k, acc[1]);
-                    acc[2] = fmaf(x.z, k, acc[2]);
-                    acc[3] = fmaf(x.w, k, acc[3]);
-                    acc[4] = fmaf(y.x, k, acc[4]);
-                    acc[5] = fmaf(y.y, k, acc[5]);
-                    acc[6] = fmaf(y.z, k, acc[6]);
-                    acc[7] = fmaf(y.w, k, acc[7]);
+#pragma unroll
+                    for (int c = 0; c < kCh / 4; ++c) {
+                        const float4 x = at[c];
+                        acc[4 * c] = fmaf(x.x, k, acc[4 * c]);
+                        acc[4 * c + 1] = fmaf(x.y, k, acc[4 * c + 1]);
+                        acc[4 * c + 2] = fmaf(x.z, k, acc[4 * c + 2]);
+                        acc[4 * c + 3] = fmaf(x.w, k, acc[4 * c + 3]);
+                    }
                 }
                 const int row = r0 + r;
                 if (run == w.x.pages) {
                     // the whole tile: the output itself
                     if (row < R) {
-                        const int64_t at = static_cast<int64_t>(s.row0 + row / p.G) * p.Hq + w.h * p.G + row % p.G;
+                        const int64_t at = out_row(p, s, w.h, row);
                         const float inv = L > 0.0f || L != L ? 1.0f / L : 0.0f;
-                        uint4 y;
-                        y.x = pack_bf16x2(acc[0] * inv, acc[1] * inv);
-                        y.y = pack_bf16x2(acc[2] * inv, acc[3] * inv);
-                        y.z = pack_bf16x2(acc[4] * inv, acc[5] * inv);
-                        y.w = pack_bf16x2(acc[6] * inv, acc[7] * inv);
-                        *reinterpret_cast<uint4 *>(p.O + at * kD + ch) = y;
+#pragma unroll
+                        for (int c = 0; c < kCh / 4; ++c)
+                            *reinterpret_cast<uint2 *>(p.O + at * kD + ch + 4 * c) =
+                                make_uint2(pack_bf16x2(acc[4 * c] * inv, acc[4 * c + 1] * inv),
+                                           pack_bf16x2(acc[4 * c + 2] * inv, acc[4 * c + 3] * inv));
                         if (p.lse && ch == 0) p.lse[at] = Mu * 0.6931471805599453f + logf(L);
                     }
                 } else {
                     // a share of it: slot 0 where the CTA's share begins in this tile, else slot 1
-                    float *part = p.part + (static_cast<int64_t>(blockIdx.x) * 2 + (w.left == u1 - u0 ? 0 : 1)) * kPartFloats;
-                    float4 *at = reinterpret_cast<float4 *>(part + r * kD + ch);
-                    at[0] = make_float4(acc[0], acc[1], acc[2], acc[3]);
-                    at[1] = make_float4(acc[4], acc[5], acc[6], acc[7]);
+                    float *part = p.part + (static_cast<int64_t>(blockIdx.x) * 2 + (w.left == u1 - u0 ? 0 : 1)) * part_floats(kRows);
+#pragma unroll
+                    for (int c = 0; c < kCh / 4; ++c)
+                        *reinterpret_cast<float4 *>(part + r * kD + ch + 4 * c) =
+                            make_float4(acc[4 * c], acc[4 * c + 1], acc[4 * c + 2], acc[4 * c + 3]);
                     if (ch == 0) {
                         part[kRows * kD + r] = M;
                         part[kRows * kD + kRows + r] = L;
@@ -490,14 +569,15 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // Joins the partials of the tile that straddles the end of CTA blockIdx.x's
 // share and begins in it.  One thread per (row, eight channels).
-__global__ void __launch_bounds__(256) combine_kernel(const AttnParams p, int ctas) {
-    const int64_t all = count_units(p), share = share_of(all, ctas);
+template <int kRows>
+__global__ void __launch_bounds__(16 * kRows) combine_kernel(const AttnParams p, int ctas) {
+    const int64_t all = count_units<kRows>(p), share = share_of(all, ctas);
     const int64_t u0 = share * blockIdx.x, u1 = u0 + share;
     if (u1 >= all) return;                   // nothing behind this share
     int b;
     int64_t local;
-    find_unit(p, u1 - 1, b, local);
-    Walk w;
+    find_unit<kRows>(p, u1 - 1, b, local);
+    Walk<kRows> w;
     w.begin(p, b, local, 1);
     if (w.page + 1 == w.x.pages) return;     // its tile ends with the share
     const int64_t begin = u1 - 1 - w.page, end = begin + w.x.pages;
@@ -508,7 +588,7 @@ __global__ void __launch_bounds__(256) combine_kernel(const AttnParams p, int ct
     const int last = static_cast<int>((end - 1) / share);
     const float kNegInf = __int_as_float(0xff800000);
     auto part_of = [&](int c) {
-        return p.part + (static_cast<int64_t>(c) * 2 + (c == static_cast<int>(blockIdx.x) && begin > u0 ? 1 : 0)) * kPartFloats;
+        return p.part + (static_cast<int64_t>(c) * 2 + (c == static_cast<int>(blockIdx.x) && begin > u0 ? 1 : 0)) * part_floats(kRows);
     };
     float M = kNegInf;
     for (int c = blockIdx.x; c <= last; ++c) M = fmaxf(M, part_of(c)[kRows * kD + r]);
@@ -529,7 +609,7 @@ __global__ void __launch_bounds__(256) combine_kernel(const AttnParams p, int ct
         acc[6] = fmaf(y.z, k, acc[6]);
         acc[7] = fmaf(y.w, k, acc[7]);
     }
-    const int64_t at = static_cast<int64_t>(s.row0 + row / p.G) * p.Hq + w.h * p.G + row % p.G;
+    const int64_t at = out_row(p, s, w.h, row);
     const float inv = L > 0.0f || L != L ? 1.0f / L : 0.0f;
     uint4 y;
     y.x = pack_bf16x2(acc[0] * inv, acc[1] * inv);
@@ -540,10 +620,13 @@ __global__ void __launch_bounds__(256) combine_kernel(const AttnParams p, int ct
     if (p.lse && ch == 0) p.lse[at] = Mu * 0.6931471805599453f + logf(L);
 }
 
+// Rows of a tile: eight where every sequence can have no more on average.
+int tile_rows(int T, int Hq, int H, int B) { return static_cast<int64_t>(T) * (Hq / H) > 8ll * B ? 16 : 8; }
+
 // CTAs of the decode kernel: one per SM, fewer where there cannot be work for all.
 int decode_ctas(int T, int Hq, int H, int B, int cols) {
     const int64_t G = Hq / H;
-    const int64_t tiles = static_cast<int64_t>(T) * G / kRows + (B < T ? B : T);   // of one head, at most
+    const int64_t tiles = static_cast<int64_t>(T) * G / tile_rows(T, Hq, H, B) + (B < T ? B : T);   // of one head, at most
     const int64_t units = tiles * H * (cols > 0 ? cols : 1);
     const int64_t most = (units + kSmallest - 1) / kSmallest;
     return static_cast<int>(most < 152 ? (most < 1 ? 1 : most) : 152);
@@ -551,13 +634,24 @@ int decode_ctas(int T, int Hq, int H, int B, int cols) {
 
 // More than one tile of 16 rows a sequence and KV head on average: the tensor
 // core kernel's tiles of 128 rows.
-bool many_rows(int T, int Hq, int H, int B) { return static_cast<int64_t>(T) * (Hq / H) > static_cast<int64_t>(kRows) * B; }
+bool many_rows(int T, int Hq, int H, int B) { return static_cast<int64_t>(T) * (Hq / H) > 16ll * B; }
+
+template <int kRows>
+cudaError_t launch_decode(const CUtensorMap &mk, const CUtensorMap &mv, const AttnParams &p, int ctas, cudaStream_t st) {
+    cudaError_t e = cudaFuncSetAttribute(decode_kernel<kRows>, cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<kRows>::bytes);
+    if (e != cudaSuccess) return e;
+    decode_kernel<kRows><<<ctas, kThreads, Smem<kRows>::bytes, st>>>(mk, mv, p);
+    e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    combine_kernel<kRows><<<ctas, 16 * kRows, 0, st>>>(p, ctas);
+    return cudaGetLastError();
+}
 
 }  // namespace
 
 size_t cache_attention_workspace(int T, int Hq, int H, int B, int cols) {
     if (many_rows(T, Hq, H, B)) return cache_chunk_workspace(T, Hq, H, B, cols);
-    return static_cast<size_t>(decode_ctas(T, Hq, H, B, cols)) * 2 * kPartFloats * sizeof(float);
+    return static_cast<size_t>(decode_ctas(T, Hq, H, B, cols)) * 2 * part_floats(tile_rows(T, Hq, H, B)) * sizeof(float);
 }
 
 cudaError_t launch_cache_attention(const CacheAttnArgs &a, cudaStream_t st) {
@@ -570,13 +664,8 @@ cudaError_t launch_cache_attention(const CacheAttnArgs &a, cudaStream_t st) {
     p.lse = a.lse;
     p.part = static_cast<float *>(a.ws);
     const int ctas = decode_ctas(a.T, a.Hq, a.c.H, a.c.B, a.c.cols);
-    cudaError_t e = cudaFuncSetAttribute(decode_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
-    if (e != cudaSuccess) return e;
-    decode_kernel<<<ctas, kThreads, kSmem, st>>>(mk, mv, p);
-    e = cudaGetLastError();
-    if (e != cudaSuccess) return e;
-    combine_kernel<<<ctas, 256, 0, st>>>(p, ctas);
-    return cudaGetLastError();
+    return tile_rows(a.T, a.Hq, a.c.H, a.c.B) == 8 ? launch_decode<8>(mk, mv, p, ctas, st)
+                                                   : launch_decode<16>(mk, mv, p, ctas, st);
 }
 
 }  // namespace vca

@@ -11,8 +11,8 @@
 //           into a ring of slots
 //   1       the MMA issuer, one thread: QK(b+2) after PV(b), in that order, so
 //           P(b), which lies over S(b) in TMEM, is read before it is overwritten
-//   4-7     V codes -> fp16 in shared memory, a page ahead of PV (two buffers)
-//   8-15    softmax, one thread per row and page: warps w and w + 4 share a TMEM
+//   2-5     V codes -> fp16 in shared memory, a page ahead of PV (two buffers)
+//   6-13    softmax, one thread per row and page: warps w and w + 4 share a TMEM
 //           lane quarter and take alternate pages; the reference maximum is
 //           handed from page to page and moves only when a page's maximum
 //           exceeds it by 8 (then O is rescaled in TMEM)
@@ -39,8 +39,8 @@ using namespace cache;
 
 constexpr int kRows = 128;
 constexpr int kKStages = 3, kVStages = 3, kWStages = 2, kSlots = 16;
-constexpr int kConvWarps = 4, kConvWarp0 = 4, kSoftWarp0 = 8;
-constexpr int kThreads = 512;
+constexpr int kConvWarps = 4, kConvWarp0 = 2, kSoftWarp0 = 6;
+constexpr int kThreads = 32 * (kSoftWarp0 + kSoftmaxWarps);
 constexpr uint32_t kTile = kBlk * kD;            // E4M3 tile
 constexpr uint32_t kWTile = 2 * kTile;           // fp16 tile, two panels of 64 channels
 constexpr uint32_t kPanel = kTile;
@@ -250,8 +250,8 @@ __device__ __forceinline__ float rcp_approx(float x) {
 struct PageScore {
     float c, bias;       // no cap: p = 2^(S c + bias); cap: p = 2^(r t + bias), r = 1 / (1 + 2^(S c))
     float t;             // -2 cap log2(e)
-    int lim;             // columns that the row sees
-    bool edge;
+    int lim;             // columns that the row sees (cap)
+    bool edge;           // some row of the warp sees fewer than all (cap)
 };
 
 // 32 raw scores -> 16 words of fp16 pairs; the unrounded probabilities add to l2.
@@ -274,13 +274,62 @@ __device__ __forceinline__ void probabilities(const uint32_t (&X)[32], const Pag
         }
         a = ex2_approx(a);
         b = ex2_approx(b);
-        if (s.edge) {
-            if (col0 + 2 * k >= s.lim) a = 0.0f;
-            if (col0 + 2 * k + 1 >= s.lim) b = 0.0f;
+        if constexpr (kCap) {
+            if (s.edge) {
+                if (col0 + 2 * k >= s.lim) a = 0.0f;
+                if (col0 + 2 * k + 1 >= s.lim) b = 0.0f;
+            }
         }
         l2 = add2(l2, pk2(__float_as_uint(a), __float_as_uint(b)));
         W[k] = pack_half2(a, b);
     }
+}
+
+// A warp's 32 rows of V codes as fp16 times a power of two, rows from `live` on
+// as zeros.  Eight lanes a row, one 16-byte chunk of codes each: two 16-byte
+// chunks of fp16, the second first in the upper panel, so that a quarter warp's
+// stores fall into different banks.
+template <bool kPlain>
+__device__ __forceinline__ void convert_rows(const unsigned char *src, unsigned char *dst, int part, float factor, int live) {
+    const int lane = threadIdx.x & 31, c = lane & 7, up = c >> 2, oc = 2 * (c & 3);
+    const __half2 f = __float2half2_rn(factor);
+    dst += up * kPanel;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const int r = part * 32 + 4 * i + (lane >> 3);
+        const uint4 v = *reinterpret_cast<const uint4 *>(src + sw128_offset(r, c));
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+        uint32_t o[8];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\t"
+                "cvt.rn.f16x2.e4m3x2 %1, b;\n\t}" : "=r"(o[2 * k]), "=r"(o[2 * k + 1]) : "r"(w[k]));
+            if constexpr (!kPlain) {
+                const __half2 x = __hmul2(*reinterpret_cast<__half2 *>(&o[2 * k]), f);
+                const __half2 y = __hmul2(*reinterpret_cast<__half2 *>(&o[2 * k + 1]), f);
+                o[2 * k] = r < live ? *reinterpret_cast<const uint32_t *>(&x) : 0u;
+                o[2 * k + 1] = r < live ? *reinterpret_cast<const uint32_t *>(&y) : 0u;
+            }
+        }
+        const uint4 lo = make_uint4(o[0], o[1], o[2], o[3]), hi = make_uint4(o[4], o[5], o[6], o[7]);
+        *reinterpret_cast<uint4 *>(dst + sw128_offset(r, oc + up)) = up ? hi : lo;
+        *reinterpret_cast<uint4 *>(dst + sw128_offset(r, oc + 1 - up)) = up ? lo : hi;
+    }
+}
+
+// The scores of keys that the row does not see, columns lim and up, become -inf
+// in TMEM: the pages' common path then needs no masks.
+__device__ __forceinline__ void mask_scores(uint32_t tS, int lim) {
+#pragma unroll 1
+    for (int i = 0; i < kBlk; i += 32) {
+        uint32_t X[32];
+        VCA_TMEM_LD32(tS + i, X);
+        tmem_ld_wait();
+#pragma unroll
+        for (int e = 0; e < 32; ++e) X[e] = i + e < lim ? X[e] : 0xff800000u;
+        VCA_TMEM_ST32(tS + i, X);
+    }
+    tmem_st_wait();
 }
 
 template <bool kCap>
@@ -460,42 +509,19 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     } else if (warp >= kConvWarp0 && warp < kConvWarp0 + kConvWarps) {
         // ------------------------------------------------------------ V codes -> fp16
-        // eight lanes a row, one 16-byte chunk of codes each: two 16-byte chunks of
-        // fp16, the second first in the upper panel, so that a quarter warp's
-        // stores fall into different banks
-        const int c = lane & 7, up = c >> 2;
         for (int j = 0; j < nb; ++j) {
             const int vt = j % kVStages, wt = j % kWStages;
             bool ok = mbar_wait(v_full + vt, (j / kVStages) & 1, abort_flag, p.limit_ns);
             if (ok && j >= kWStages) ok = mbar_wait(w_empty + wt, (j / kWStages - 1) & 1, abort_flag, p.limit_ns);
             if (!__all_sync(0xffffffffu, ok)) break;
             const float4 slot = sSlot[j % kSlots];
-            const __half2 f = __float2half2_rn(slot.y);
             const unsigned char *src = smem + kOffV + vt * kTile;
-            unsigned char *dst = smem + kOffW + wt * kWTile + up * kPanel;
+            unsigned char *dst = smem + kOffW + wt * kWTile;
             const int live = slot.x < 0.0f ? 0 : it.s.len - (it.page0 + j) * kBlk;    // rows behind the last token hold anything
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const int r = (warp - kConvWarp0) * 32 + 4 * i + (lane >> 3);
-                const uint4 v = *reinterpret_cast<const uint4 *>(src + sw128_offset(r, c));
-                const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-                uint32_t o[8];
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    uint32_t lo, hi;
-                    asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\t"
-                        "cvt.rn.f16x2.e4m3x2 %1, b;\n\t}" : "=r"(lo), "=r"(hi) : "r"(w[k]));
-                    const __half2 x = __hmul2(*reinterpret_cast<__half2 *>(&lo), f);
-                    const __half2 y = __hmul2(*reinterpret_cast<__half2 *>(&hi), f);
-                    o[2 * k] = r < live ? *reinterpret_cast<const uint32_t *>(&x) : 0u;
-                    o[2 * k + 1] = r < live ? *reinterpret_cast<const uint32_t *>(&y) : 0u;
-                }
-                const uint4 first = up ? make_uint4(o[4], o[5], o[6], o[7]) : make_uint4(o[0], o[1], o[2], o[3]);
-                const uint4 second = up ? make_uint4(o[0], o[1], o[2], o[3]) : make_uint4(o[4], o[5], o[6], o[7]);
-                const int oc = 2 * (c & 3);
-                *reinterpret_cast<uint4 *>(dst + sw128_offset(r, oc + up)) = first;
-                *reinterpret_cast<uint4 *>(dst + sw128_offset(r, oc + 1 - up)) = second;
-            }
+            if (slot.y == 1.0f && live >= kBlk)
+                convert_rows<true>(src, dst, warp - kConvWarp0, 1.0f, kBlk);
+            else
+                convert_rows<false>(src, dst, warp - kConvWarp0, slot.y, live);
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) {
@@ -545,29 +571,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                 slot = sSlot[b % kSlots];
                 s.lim = slot.x < 0.0f ? 0 : seen - (it.page0 + b) * kBlk;
                 s.edge = __any_sync(0xffffffffu, s.lim < kBlk);
+                if (s.edge) mask_scores(tS, s.lim);
                 float m0, m1, m2, m3;
                 VCA_TMEM_LDMAX32(tS + 64, X0, m2);
                 VCA_TMEM_LDMAX32(tS + 96, X1, m3);
                 tmem_ld_wait();
-                if (s.edge) {
-                    m2 = m3 = kNegInf;
-#pragma unroll
-                    for (int e = 0; e < 32; ++e) {
-                        if (64 + e < s.lim) m2 = fmaxf(m2, __uint_as_float(X0[e]));
-                        if (96 + e < s.lim) m3 = fmaxf(m3, __uint_as_float(X1[e]));
-                    }
-                }
                 VCA_TMEM_LDMAX32(tS, X0, m0);
                 VCA_TMEM_LDMAX32(tS + 32, X1, m1);
                 tmem_ld_wait();
-                if (s.edge) {
-                    m0 = m1 = kNegInf;
-#pragma unroll
-                    for (int e = 0; e < 32; ++e) {
-                        if (e < s.lim) m0 = fmaxf(m0, __uint_as_float(X0[e]));
-                        if (32 + e < s.lim) m1 = fmaxf(m1, __uint_as_float(X1[e]));
-                    }
-                }
                 pm = fmaxf(fmaxf(m0, m1), fmaxf(m2, m3));
             }
             // the reference maximum after page b - 1 from the partner, after page b
@@ -578,7 +589,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 m_in = sMX[(par ^ 1) * kRows + row];
             }
             const bool valid = ok && !(m_in != m_in);
-            s.c = __fmul_rn(f, slot.x);
+            s.c = fmaxf(__fmul_rn(f, slot.x), 0x1p-126f);      // above 0, so that -inf stays -inf
             s.t = -2.0f * p.cap_out;
             float bm = kNegInf;
             if (pm != kNegInf)

@@ -224,6 +224,55 @@ struct Walk {
     }
 };
 
+// The pages of a share and their scales, in order, for a whole warp: three
+// batches of up to 32 pages of one head, one page per lane -- the one being
+// used, one whose scales are being loaded, one whose table entries are.
+template <int N>
+struct Feed {
+    Walk<N> ahead;
+    int page[3], count[3], head[3], used;
+    float sk[2];
+    __device__ void begin(const AttnParams &p, const Walk<N> &w) {
+        ahead = w;
+        used = 0;
+#pragma unroll
+        for (int i = 0; i < 3; ++i) fetch(p, i);
+        sk[0] = scale(p, 0);
+        sk[1] = scale(p, 1);
+    }
+    // The next batch's table entries.
+    __device__ void fetch(const AttnParams &p, int i) {
+        page[i] = -1;
+        count[i] = 0;
+        if (ahead.left <= 0) return;
+        count[i] = static_cast<int>(min(ahead.left, static_cast<int64_t>(min(32, ahead.w.pages - ahead.page))));
+        head[i] = ahead.h;
+        const int lane = threadIdx.x & 31;
+        if (lane < count[i]) page[i] = load_page(p.c, ahead.b, ahead.page + lane, p.dev_status);
+        ahead.next(p, count[i]);
+    }
+    __device__ float scale(const AttnParams &p, int i) const {
+        return page[i] >= 0 ? p.c.sk[static_cast<int64_t>(page[i]) * p.c.H + head[i]] : 0.0f;
+    }
+    __device__ void take(const AttnParams &p, int &pg, float &ks) {
+        if (used == count[0]) {
+            used = 0;
+            page[0] = page[1];
+            count[0] = count[1];
+            head[0] = head[1];
+            sk[0] = sk[1];
+            page[1] = page[2];
+            count[1] = count[2];
+            head[1] = head[2];
+            sk[1] = scale(p, 1);
+            fetch(p, 2);
+        }
+        pg = __shfl_sync(0xffffffffu, page[0], used);
+        ks = __shfl_sync(0xffffffffu, sk[0], used);
+        ++used;
+    }
+};
+
 // ---------------------------------------------------------------------------
 // The images
 // ---------------------------------------------------------------------------
@@ -338,6 +387,63 @@ __device__ __forceinline__ void copy_factors(uint32_t taddr, uint32_t saddr) {
     asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(d) : "memory");
 }
 
+// Adds 2^(S f + (-lse)) over kCols of a key's rows; consts and seen at the first of them.
+template <int kCols, bool kCap, bool kEdge>
+__device__ __forceinline__ uint64_t sum_cols(const uint32_t *X, uint64_t sk2, const ulonglong2 *consts, const int *seen,
+                                             int key, float cap_out, uint64_t sum2) {
+#pragma unroll
+    for (int k = 0; k < kCols / 2; ++k) {
+        const ulonglong2 cc = consts[k];     // two rows' factors, their -lse
+        const uint64_t s2 = mul2(pk2(X[2 * k], X[2 * k + 1]), sk2);
+        float a, b;
+        if constexpr (kCap) {
+            float u, v, lu, lv;
+            upk2(mul2(s2, cc.x), u, v);
+            upk2(cc.y, lu, lv);
+            a = capped(u, cap_out) + lu;
+            b = capped(v, cap_out) + lv;
+        } else {
+            upk2(fma2(s2, cc.x, cc.y), a, b);
+        }
+        a = ex2_approx(a);
+        b = ex2_approx(b);
+        if constexpr (kEdge) {
+            if (key >= seen[2 * k]) a = 0.0f;
+            if (key >= seen[2 * k + 1]) b = 0.0f;
+        }
+        sum2 = add2(sum2, pk2(__float_as_uint(a), __float_as_uint(b)));
+    }
+    return sum2;
+}
+
+// A key's sum over the N rows of S^T at tS.
+template <int N, bool kCap, bool kEdge>
+__device__ __forceinline__ uint64_t sum_row(uint32_t tS, uint64_t sk2, const ulonglong2 *consts, const int *seen, int key,
+                                            float cap_out) {
+    uint32_t X0[32];
+    uint64_t sum2 = 0;
+    if constexpr (N == 16) {
+        float unused;
+        VCA_TMEM_LDMAX16(tS, X0, unused);
+        tmem_ld_wait();
+        return sum_cols<16, kCap, kEdge>(X0, sk2, consts, seen, key, cap_out, sum2);
+    } else {
+        uint32_t X1[32];
+        VCA_TMEM_LD32(tS, X0);
+        tmem_ld_wait();
+#pragma unroll 1
+        for (int c = 0; c < N; c += 64) {
+            VCA_TMEM_LD32(tS + c + 32, X1);
+            sum2 = sum_cols<32, kCap, kEdge>(X0, sk2, consts + c / 2, seen + c, key, cap_out, sum2);
+            tmem_ld_wait();
+            if (c + 64 < N) VCA_TMEM_LD32(tS + c + 64, X0);
+            sum2 = sum_cols<32, kCap, kEdge>(X1, sk2, consts + c / 2 + 16, seen + c + 32, key, cap_out, sum2);
+            tmem_ld_wait();
+        }
+        return sum2;
+    }
+}
+
 template <int N, bool kCap>
 __global__ void __launch_bounds__(kThreads, 1)
     weigh_kernel(const __grid_constant__ CUtensorMap tmK, const WeighParams wp) {
@@ -401,17 +507,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         // ------------------------------------------------------------ producer
         bool ok = true;
         int kn = 0, qn = 0;      // pages and tiles issued
+        // pages and scales come 32 at a time, one per lane, two batches ahead: a
+        // load under full traffic takes longer than a unit's pages
+        Feed<N> feed;
+        feed.begin(p, wk);
         while (ok && wk.left > 0) {
             const int kp = wk.count();
-            int page = -1;
-            float sk = 0.0f;
-            if (lane < kp) {
-                page = load_page(p.c, wk.b, wk.page + lane, p.dev_status);
-                if (page >= 0) sk = p.c.sk[static_cast<int64_t>(page) * p.c.H + wk.h];
-            }
             for (int j = 0; ok && j < kp; ++j) {
-                const int pg = __shfl_sync(0xffffffffu, page, j), st = kn % kKStages;
-                const float ks = __shfl_sync(0xffffffffu, sk, j);
+                int pg;
+                float ks;
+                feed.take(p, pg, ks);
+                const int st = kn % kKStages;
                 if (kn >= kKStages) ok = mbar_wait(k_empty + st, (kn / kKStages - 1) & 1, abort_flag, p.limit_ns);
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
@@ -529,40 +635,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const uint64_t sk2 = pk2(__float_as_uint(sk), __float_as_uint(sk));
                     const int key = (wk.page + j) * kBlk + row;
                     const bool edge = (wk.page + j + 1) * kBlk > all_see;
-                    uint64_t sum2 = 0;
-#pragma unroll 1
-                    for (int c = 0; c < N; c += 32) {
-                        uint32_t X[32];
-                        if constexpr (N == 16) {
-                            float unused;
-                            VCA_TMEM_LDMAX16(tl + sb * N, X, unused);
-                        } else {
-                            VCA_TMEM_LD32(tl + sb * N + c, X);
-                        }
-                        tmem_ld_wait();
-#pragma unroll
-                        for (int k = 0; k < (N == 16 ? 8 : 16); ++k) {
-                            const ulonglong2 cc = consts[c / 2 + k];     // two rows' factors, their -lse
-                            const uint64_t s2 = mul2(pk2(X[2 * k], X[2 * k + 1]), sk2);
-                            float a, b;
-                            if constexpr (kCap) {
-                                float u, v, lu, lv;
-                                upk2(mul2(s2, cc.x), u, v);
-                                upk2(cc.y, lu, lv);
-                                a = capped(u, p.cap_out) + lu;
-                                b = capped(v, p.cap_out) + lv;
-                            } else {
-                                upk2(fma2(s2, cc.x, cc.y), a, b);
-                            }
-                            a = ex2_approx(a);
-                            b = ex2_approx(b);
-                            if (edge) {
-                                if (key >= seen[c + 2 * k]) a = 0.0f;
-                                if (key >= seen[c + 2 * k + 1]) b = 0.0f;
-                            }
-                            sum2 = add2(sum2, pk2(__float_as_uint(a), __float_as_uint(b)));
-                        }
-                    }
+                    const uint64_t sum2 = edge ? sum_row<N, kCap, true>(tl + sb * N, sk2, consts, seen, key, p.cap_out)
+                                               : sum_row<N, kCap, false>(tl + sb * N, sk2, consts, seen, key, p.cap_out);
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(s_empty + sb);
