@@ -8,15 +8,14 @@
 // per 32 channels, as in vca_cache_chunk.cu, here the B operand.  A first kernel
 // writes every tile of N query rows (16 where sequences have few, else 128) as
 // an image of what the second one wants in shared memory: the two code
-// matrices, their factors, and for each row its score factor and lse.
+// matrices, their factors, and for each row its lse.
 //
 // The second kernel runs one CTA per SM over an equal share of the (sequence,
 // KV head, page) list.  Up to four pages of a head stay in shared memory while the
 // head's tiles stream past them: a page is read once, and a tile once for four
 // pages.  Few rows are bound by reading K (128 B a token) and the weights; many
 // by the tensor core's two FP8 products, 2 x 2 rows keys d flops.
-// Warps: 0 producer, 1 MMA issuer, 2-9 sums (two sets of four that take the
-// unit's even and odd pages).  Every wait is bounded, as in vca_attention.cu.
+// Warps: 0 producer, 1 MMA issuer, 2-9 sums (two sets of four).  Every wait is bounded, as in vca_attention.cu.
 #include "vca_attention_common.cuh"
 #include "vca_cache.cuh"
 
@@ -30,23 +29,29 @@ using namespace cache;
 constexpr uint32_t kTile = kBlk * kD;
 constexpr int kKP = 4;                       // pages of a unit
 constexpr int kKStages = 8, kSlots = 16;
-constexpr int kThreads = 320;
+constexpr int kSets = 2;                     // sets of four sum warps
+constexpr int kThreads = 32 * (2 + 4 * kSets);
+constexpr uint32_t kBarSums = 1;             // named barrier of the sum warps
 
 // A tile of N rows as it lies in the workspace and in shared memory: hi, lo
 // codes [N][128], swizzled; the factors of hi and of lo, 32 rows of 16 bytes each
-// (row i: rows i, i + 32, i + 64, i + 96); per two rows their factors and -lse;
-// and how many keys each row sees.
+// (row i: rows i, i + 32, i + 64, i + 96; for N = 16 in the first of the two: row
+// i the factors of hi i, row 16 + i those of lo i); -lse log2 e of each row; and
+// how many keys it sees.
 template <int N>
 struct Image {
-    static constexpr uint32_t lo = N * kD, sf = 2 * N * kD, consts = sf + 1024, seen = consts + 8 * N, bytes = seen + 4 * N;
+    static constexpr uint32_t lo = N * kD, sf = 2 * N * kD, consts = sf + 1024, seen = consts + 4 * N, bytes = seen + 4 * N;
     static constexpr uint32_t stride = (bytes + 1023) / 1024 * 1024;
 };
 
+// S^T takes a column per row; of 16 rows, two: hi and lo are then one product of
+// 32 columns, since issuing an MMA costs the same for few columns as for many.
 template <int N>
 struct Layout {
-    static constexpr int qstages = N == 128 ? 2 : 4, sbufs = N == 128 ? 3 : 8;
-    static constexpr uint32_t tmem_sfa = sbufs * N, tmem_sfb = tmem_sfa + 4, tmem_cols = N == 128 ? 512 : 256;
-    static constexpr uint32_t offQ = kKStages * kTile, offSlot = offQ + qstages * Image<N>::stride, offBar = offSlot + kSlots * 8;
+    static constexpr int qstages = N == 128 ? 2 : 4, cols = N == 128 ? 128 : 32, sbufs = N == 128 ? 3 : 8;
+    static constexpr uint32_t tmem_sfa = sbufs * cols, tmem_sfb = tmem_sfa + 4, tmem_cols = 512;
+    static constexpr uint32_t offQ = kKStages * kTile, offSlot = offQ + qstages * Image<N>::stride;
+    static constexpr uint32_t offSum = offSlot + kSlots * 8, offBar = offSum + 2 * kKP * kBlk * 4;   // fp32 [2][pages][128]
     static constexpr int bars = 2 * kKStages + 2 * qstages + 2 * sbufs + 1;
     static constexpr uint32_t offMisc = offBar + bars * 8, smem = offMisc + 16 + 1024;
     static_assert(smem <= 232448, "shared memory budget");
@@ -312,9 +317,9 @@ __global__ void __launch_bounds__(256) image_kernel(const WeighParams wp) {
     const int R = s.n * p.G;
     uint8_t *img = wp.images + (static_cast<int64_t>(h) * wp.tiles + blockIdx.x) * Image<N>::stride;
     uint8_t *sf = img + Image<N>::sf;
-    if (N < 32) {
-        // rows that do not exist have factor words too
-        for (int i = threadIdx.x; i < 256; i += 256) reinterpret_cast<uint32_t *>(sf)[i] = 0x7f7f7f7fu;
+    if (N == 16) {
+        // the columns of TMEM that no row takes get factors too
+        reinterpret_cast<uint32_t *>(sf)[threadIdx.x] = 0x7f7f7f7fu;
         __syncthreads();
     }
     for (int n = threadIdx.x >> 4; n < N; n += 16) {
@@ -327,8 +332,6 @@ __global__ void __launch_bounds__(256) image_kernel(const WeighParams wp) {
         m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
         m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
         const int e = max(static_cast<int>(m >> 23) - 127 - 7, -100);
-        int E = max(e, __shfl_xor_sync(0xffffffffu, e, 4));
-        E = max(E, __shfl_xor_sync(0xffffffffu, E, 8));
         const float down = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
         const uint32_t w[4] = {v.x, v.y, v.z, v.w};
         float x[8];
@@ -349,17 +352,15 @@ __global__ void __launch_bounds__(256) image_kernel(const WeighParams wp) {
         *reinterpret_cast<uint2 *>(img + at) = hi;
         *reinterpret_cast<uint2 *>(img + Image<N>::lo + at) = lo;
         if ((lane16 & 3) == 0) {
-            const int byte = max(127 + e - E, 6);
+            const int byte = 127 + e;       // 27 .. 247
             uint8_t *q = sf + (n & 31) * 16 + (n >> 5) * 4 + (lane16 >> 2);
             q[0] = static_cast<uint8_t>(byte);
-            q[512] = static_cast<uint8_t>(byte - 5);
+            q[N == 16 ? 256 : 512] = static_cast<uint8_t>(byte - 5);
         }
         if (lane16 == 0) {
-            // a row that sees nothing adds nothing: 2^(0 S - inf)
-            float *c = reinterpret_cast<float *>(img + Image<N>::consts) + (n >> 1) * 4 + (n & 1);
-            const float two_e = __uint_as_float(static_cast<uint32_t>(127 + E) << 23);
-            c[0] = seen > 0 ? two_e * (p.cap_out != 0.0f ? p.cap_in : p.scale_log2) : 0.0f;
-            c[2] = seen > 0 ? -1.4426950408889634f * wp.lse[out_row(p, s, h, r)] : __int_as_float(0xff800000);
+            // a row that sees nothing adds nothing: 2^(S c - inf)
+            reinterpret_cast<float *>(img + Image<N>::consts)[n] =
+                seen > 0 ? -1.4426950408889634f * wp.lse[out_row(p, s, h, r)] : __int_as_float(0xff800000);
             reinterpret_cast<int *>(img + Image<N>::seen)[n] = seen;
         }
     }
@@ -387,23 +388,22 @@ __device__ __forceinline__ void copy_factors(uint32_t taddr, uint32_t saddr) {
     asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(d) : "memory");
 }
 
-// Adds 2^(S f + (-lse)) over kCols of a key's rows; consts and seen at the first of them.
+// The sum of 2^(S c + (-lse)) over 32 rows of S^T at tS; `lse` their -lse as pairs.
 template <int kCols, bool kCap, bool kEdge>
-__device__ __forceinline__ uint64_t sum_cols(const uint32_t *X, uint64_t sk2, const ulonglong2 *consts, const int *seen,
-                                             int key, float cap_out, uint64_t sum2) {
+__device__ __forceinline__ uint64_t sum_cols(const uint32_t *X, float c, const uint64_t *lse, const int *seen, int key,
+                                             float cap_out, uint64_t sum2) {
+    const uint64_t c2 = pk2(__float_as_uint(c), __float_as_uint(c));
 #pragma unroll
     for (int k = 0; k < kCols / 2; ++k) {
-        const ulonglong2 cc = consts[k];     // two rows' factors, their -lse
-        const uint64_t s2 = mul2(pk2(X[2 * k], X[2 * k + 1]), sk2);
         float a, b;
         if constexpr (kCap) {
             float u, v, lu, lv;
-            upk2(mul2(s2, cc.x), u, v);
-            upk2(cc.y, lu, lv);
+            upk2(mul2(pk2(X[2 * k], X[2 * k + 1]), c2), u, v);
+            upk2(lse[k], lu, lv);
             a = capped(u, cap_out) + lu;
             b = capped(v, cap_out) + lv;
         } else {
-            upk2(fma2(s2, cc.x, cc.y), a, b);
+            upk2(fma2(pk2(X[2 * k], X[2 * k + 1]), c2, lse[k]), a, b);
         }
         a = ex2_approx(a);
         b = ex2_approx(b);
@@ -416,32 +416,28 @@ __device__ __forceinline__ uint64_t sum_cols(const uint32_t *X, uint64_t sk2, co
     return sum2;
 }
 
-// A key's sum over the N rows of S^T at tS.
+// A key's sum over the rows whose -lse this thread holds, S^T's first of them at tS.
 template <int N, bool kCap, bool kEdge>
-__device__ __forceinline__ uint64_t sum_row(uint32_t tS, uint64_t sk2, const ulonglong2 *consts, const int *seen, int key,
-                                            float cap_out) {
+__device__ __forceinline__ float sum_row(uint32_t tS, float c, const uint64_t *lse, const int *seen, int key, float cap_out) {
     uint32_t X0[32];
     uint64_t sum2 = 0;
+    VCA_TMEM_LD32(tS, X0);
     if constexpr (N == 16) {
-        float unused;
-        VCA_TMEM_LDMAX16(tS, X0, unused);
         tmem_ld_wait();
-        return sum_cols<16, kCap, kEdge>(X0, sk2, consts, seen, key, cap_out, sum2);
+#pragma unroll
+        for (int k = 0; k < 16; ++k) X0[k] = __float_as_uint(__fadd_rn(__uint_as_float(X0[k]), __uint_as_float(X0[16 + k])));
+        sum2 = sum_cols<16, kCap, kEdge>(X0, c, lse, seen, key, cap_out, sum2);
     } else {
         uint32_t X1[32];
-        VCA_TMEM_LD32(tS, X0);
         tmem_ld_wait();
-#pragma unroll 1
-        for (int c = 0; c < N; c += 64) {
-            VCA_TMEM_LD32(tS + c + 32, X1);
-            sum2 = sum_cols<32, kCap, kEdge>(X0, sk2, consts + c / 2, seen + c, key, cap_out, sum2);
-            tmem_ld_wait();
-            if (c + 64 < N) VCA_TMEM_LD32(tS + c + 64, X0);
-            sum2 = sum_cols<32, kCap, kEdge>(X1, sk2, consts + c / 2 + 16, seen + c + 32, key, cap_out, sum2);
-            tmem_ld_wait();
-        }
-        return sum2;
+        VCA_TMEM_LD32(tS + 32, X1);
+        sum2 = sum_cols<32, kCap, kEdge>(X0, c, lse, seen, key, cap_out, sum2);
+        tmem_ld_wait();
+        sum2 = sum_cols<32, kCap, kEdge>(X1, c, lse + 16, seen + 32, key, cap_out, sum2);
     }
+    float a, b;
+    upk2(sum2, a, b);
+    return a + b;
 }
 
 template <int N, bool kCap>
@@ -475,11 +471,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         for (int s = 0; s < L::qstages; ++s) {
             mbar_init(q_full + s, 1);
-            mbar_init(q_empty + s, 1 + 8);       // the MMA's commit, the sum warps
+            mbar_init(q_empty + s, 1 + 4 * kSets);       // the MMA's commit, the sum warps
         }
         for (int s = 0; s < L::sbufs; ++s) {
             mbar_init(s_full + s, 2);            // the MMA's commit, the issuer itself
-            mbar_init(s_empty + s, 4);
+            mbar_init(s_empty + s, N == 128 ? 4 * kSets : 4);
         }
         mbar_init(drain, 1);
         *abort_flag = 0;
@@ -568,7 +564,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (!ok) break;
                     const uint32_t img = sbase + L::offQ + qs * Image<N>::stride, tsf = tmem + L::tmem_sfb + 8 * qs;
                     copy_factors(tsf, img + Image<N>::sf);
-                    copy_factors(tsf + 4, img + Image<N>::sf + 512);
+                    if constexpr (N == 128) copy_factors(tsf + 4, img + Image<N>::sf + 512);
                     const uint64_t dh = sdesc_k_sw128(img), dl = sdesc_k_sw128(img + Image<N>::lo);
                     for (int j = 0; ok && j < kp; ++j) {
                         if (t < first_tile<N>(p, wk.w.s, wk.page + j)) break;      // nor does a later page see it
@@ -583,12 +579,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                         const uint64_t dk = sdesc_k_sw128(sbase + st * kTile);
 #pragma unroll
                         for (int i = 0; i < 4; ++i)
-                            mma_mxf8_ss(tmem + sb * N, dk + 2 * i, dh + 2 * i, make_idesc_mxf8_b(128, N, i), tmem + L::tmem_sfa,
-                                        tsf, i > 0);
+                            mma_mxf8_ss(tmem + sb * L::cols, dk + 2 * i, dh + 2 * i, make_idesc_mxf8_b(128, L::cols, i),
+                                        tmem + L::tmem_sfa, tsf, i > 0);
+                        if constexpr (N == 128) {
 #pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            mma_mxf8_ss(tmem + sb * N, dk + 2 * i, dl + 2 * i, make_idesc_mxf8_b(128, N, i), tmem + L::tmem_sfa,
-                                        tsf + 4, 1u);
+                            for (int i = 0; i < 4; ++i)
+                                mma_mxf8_ss(tmem + sb * L::cols, dk + 2 * i, dl + 2 * i, make_idesc_mxf8_b(128, L::cols, i),
+                                            tmem + L::tmem_sfa, tsf + 4, 1u);
+                        }
                         if (t + 1 == wk.w.tiles) tc_commit(k_empty + st);
                         tc_commit(s_full + sb);
                         mbar_arrive(s_full + sb);
@@ -604,54 +602,77 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     } else {
         // ------------------------------------------------------------ sums
+        // 128 rows: each set takes half of every page's rows, whose -lse it keeps in
+        // registers for the unit's pages (read from shared memory by every page they
+        // take more of its bandwidth than the products do); 16 rows: every other page
         const int set = (warp - 2) >> 2, quarter = warp & 3, row = quarter * 32 + lane;
-        const uint32_t tl = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
+        constexpr int kCols = N == 128 ? 64 : 16;
+        const int col0 = N == 128 ? 64 * set : 0;
+        const uint32_t tl = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + col0;
+        const float c0 = kCap ? p.cap_in : p.scale_log2;
+        float *sSum = reinterpret_cast<float *>(smem + L::offSum);
         bool ok = true;
-        int kn = 0, qn = 0, sn = 0;
+        int kn = 0, qn = 0, sn = 0, un = 0;
         while (ok && wk.left > 0) {
             const int kp = wk.count();
-            float acc[kKP / 2] = {};
-            int page[kKP / 2] = {-1, -1};
+            float acc[kKP] = {};
+            int page[kKP] = {-1, -1, -1, -1};
             for (int t = first_tile<N>(p, wk.w.s, wk.page); ok && t < wk.w.tiles; ++t, ++qn) {
                 const int qs = qn % L::qstages;
                 ok = __all_sync(0xffffffffu, mbar_wait(q_full + qs, (qn / L::qstages) & 1, abort_flag, p.limit_ns));
                 if (!ok) break;
                 const unsigned char *img = smem + L::offQ + qs * Image<N>::stride;
-                const ulonglong2 *consts = reinterpret_cast<const ulonglong2 *>(img + Image<N>::consts);
-                const int *seen = reinterpret_cast<const int *>(img + Image<N>::seen);
+                const int *seen = reinterpret_cast<const int *>(img + Image<N>::seen) + col0;
                 const int all_see = seen_by_row(p, wk.w.s, t * N);
+                uint64_t lse[kCols / 2];
+#pragma unroll
+                for (int k = 0; k < kCols / 4; ++k) {
+                    const ulonglong2 x = reinterpret_cast<const ulonglong2 *>(img + Image<N>::consts)[col0 / 4 + k];
+                    lse[2 * k] = x.x;
+                    lse[2 * k + 1] = x.y;
+                }
 #pragma unroll
                 for (int j = 0; j < kKP; ++j) {
                     if (!ok || j >= kp || t < first_tile<N>(p, wk.w.s, wk.page + j)) break;
                     const int sb = sn % L::sbufs, phase = (sn / L::sbufs) & 1;
                     ++sn;
-                    if ((j & 1) != set) continue;
+                    if (N == 16 && (j & 1) != set) continue;
                     ok = __all_sync(0xffffffffu, mbar_wait(s_full + sb, phase, abort_flag, p.limit_ns));
                     if (!ok) break;
                     tc_fence_after();
                     const float2 slot = sSlot[(kn + j) % kSlots];      // rewritten once its page's S is given back
-                    page[j >> 1] = __float_as_int(slot.x);
-                    const float sk = slot.y;
-                    const uint64_t sk2 = pk2(__float_as_uint(sk), __float_as_uint(sk));
+                    page[j] = __float_as_int(slot.x);
                     const int key = (wk.page + j) * kBlk + row;
-                    const bool edge = (wk.page + j + 1) * kBlk > all_see;
-                    const uint64_t sum2 = edge ? sum_row<N, kCap, true>(tl + sb * N, sk2, consts, seen, key, p.cap_out)
-                                               : sum_row<N, kCap, false>(tl + sb * N, sk2, consts, seen, key, p.cap_out);
+                    const uint32_t tS = tl + sb * L::cols;
+                    acc[j] += (wk.page + j + 1) * kBlk > all_see
+                                  ? sum_row<N, kCap, true>(tS, c0 * slot.y, lse, seen, key, p.cap_out)
+                                  : sum_row<N, kCap, false>(tS, c0 * slot.y, lse, seen, key, p.cap_out);
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(s_empty + sb);
-                    float a, b;
-                    upk2(sum2, a, b);
-                    acc[j >> 1] += a + b;
                 }
                 __syncwarp();
                 if (lane == 0) mbar_arrive(q_empty + qs);
             }
-            if (!ok) break;
+            if constexpr (N == 128) {
+                // the second set's sums to the first, in buffers by turns: a buffer is
+                // written again only behind the barrier after the one its reads precede
+                float *buf = sSum + (un & 1) * kKP * kBlk;
+                if (set == 1)
 #pragma unroll
-            for (int i = 0; i < kKP / 2; ++i) {
-                if (page[i] >= 0 && (wk.page + 2 * i + set) * kBlk + row < wk.w.s.len)
-                    atomicAdd(wp.weight + (static_cast<int64_t>(page[i]) * p.c.H + wk.h) * kBlk + row, acc[i]);
+                    for (int j = 0; j < kKP; ++j) buf[j * kBlk + row] = acc[j];
+                ok = bar_and(ok, kBarSums, 32 * 4 * kSets);
+                if (set == 0)
+#pragma unroll
+                    for (int j = 0; j < kKP; ++j) acc[j] += buf[j * kBlk + row];
+                ++un;
+            }
+            if (!ok) break;
+            if (N == 16 || set == 0) {
+#pragma unroll
+                for (int j = 0; j < kKP; ++j)
+                    if (page[j] >= 0 && (wk.page + j) * kBlk + row < wk.w.s.len)
+                        atomicAdd(wp.weight + (static_cast<int64_t>(page[j]) * p.c.H + wk.h) * kBlk + row, acc[j]);
             }
             kn += kp;
             wk.next(p, kp);
