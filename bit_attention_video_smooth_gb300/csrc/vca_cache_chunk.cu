@@ -9,10 +9,11 @@
 // kernel joins the parts).  Warps:
 //   0       TMA producer: K and V tiles into rings of three, each page's scales
 //           into a ring of slots
-//   1       the MMA issuer, one thread: QK(b+2) after PV(b), in that order, so
-//           P(b), which lies over S(b) in TMEM, is read before it is overwritten
-//   2-5     V codes -> fp16 in shared memory, a page ahead of PV (two buffers)
-//   6-13    softmax, one thread per row and page: warps w and w + 4 share a TMEM
+//   1, 2    MMA issuers, one thread each, QK and PV: issuing an MMA costs more than
+//           the tensor core takes for it.  QK(b+2) waits for PV(b), which reads
+//           P(b), lying over S(b) in TMEM; PV(b+1) fills that wait
+//   4-7     V codes -> fp16 in shared memory, a page ahead of PV (two buffers)
+//   8-15    softmax, one thread per row and page: warps w and w + 4 share a TMEM
 //           lane quarter and take alternate pages; the reference maximum is
 //           handed from page to page and moves only when a page's maximum
 //           exceeds it by 8 (then O is rescaled in TMEM)
@@ -39,7 +40,7 @@ using namespace cache;
 
 constexpr int kRows = 128;
 constexpr int kKStages = 3, kVStages = 3, kWStages = 2, kSlots = 16;
-constexpr int kConvWarps = 4, kConvWarp0 = 2, kSoftWarp0 = 6;
+constexpr int kConvWarps = 4, kConvWarp0 = 4, kSoftWarp0 = 8;
 constexpr int kThreads = 32 * (kSoftWarp0 + kSoftmaxWarps);
 constexpr uint32_t kTile = kBlk * kD;            // E4M3 tile
 constexpr uint32_t kWTile = 2 * kTile;           // fp16 tile, two panels of 64 channels
@@ -56,7 +57,7 @@ constexpr uint32_t kOffL = kOffMX + 2 * kRows * 4;               // fp32 [2][128
 constexpr uint32_t kOffF = kOffL + 4 * kRows * 4;                // fp32 [128] the rows' factors
 constexpr uint32_t kOffBar = kOffF + kRows * 4;
 constexpr uint32_t kBarQuery = kBarHand0 + 8;                    // + quarter: the factors handed over
-constexpr int kNumBars = 1 + 2 * kKStages + 2 * kVStages + 2 * kWStages + 2 + 2 + 2 + 1;
+constexpr int kNumBars = 1 + 2 * kKStages + 2 * kVStages + 2 * kWStages + 2 + 2 + 2 + 2;
 constexpr uint32_t kOffMisc = kOffBar + kNumBars * 8;
 constexpr uint32_t kSmem = kOffMisc + 16 + 1024;
 static_assert(kSmem <= 232448, "shared memory budget");
@@ -381,6 +382,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(pv_done + i, 1);
         }
         mbar_init(drain, 1);
+        mbar_init(drain + 1, 1);
         *abort_flag = 0;
         mbar_fence_init();
     }
@@ -464,48 +466,60 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int j = max(0, vk - kVStages); j < vk; ++j) drain_wait(v_full + j % kVStages, (j / kVStages) & 1, p.limit_ns);
         }
     } else if (warp == 1) {
-        // ------------------------------------------------------------ MMA issuer
+        // ------------------------------------------------------------ QK issuer
         if (lane == 0) {
-            const uint32_t sbase = smem_u32(smem);
-            auto qk = [&](int b) -> bool {
-                const int st = b % kKStages;
-                if (!mbar_wait_spin(k_full + st, (b / kKStages) & 1, abort_flag, p.limit_ns)) return false;
-                tc_fence_after();
-                const uint64_t dk = sdesc_k_sw128(sbase + kOffK + st * kTile);
-                const uint32_t d = tmem + kTmemS + 128 * (b & 1);
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    mma_mxf8_ts(d, tmem + kTmemQ + 8 * i, dk + 2 * i, make_idesc_mxf8(128, 128, i), tmem + kTmemSFA,
-                                tmem + kTmemSFB, i > 0);
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    mma_mxf8_ts(d, tmem + kTmemQ + 32 + 8 * i, dk + 2 * i, make_idesc_mxf8(128, 128, i), tmem + kTmemSFA + 4,
-                                tmem + kTmemSFB, 1u);
-                tc_commit(k_empty + st);
-                tc_commit(s_full + (b & 1));
-                mbar_arrive(s_full + (b & 1));
-                return true;
-            };
-            constexpr uint32_t idesc_pv = make_idesc(128, 128, 0, 0, 0, 1);
+            const uint32_t tq = tmem + kTmemQ, sfa = tmem + kTmemSFA, sfb = tmem + kTmemSFB;
+            const uint64_t dk0 = sdesc_k_sw128(smem_u32(smem) + kOffK);
+            int st = 0;
+            uint32_t kphase = 0, pphase = 0;
             bool ok = mbar_wait(q_full, 0, abort_flag, p.limit_ns);
-            for (int b = 0; ok && b < 2 && b < nb; ++b) ok = qk(b);
             for (int b = 0; ok && b < nb; ++b) {
-                const int wt = b % kWStages;
-                ok = mbar_wait_spin(w_full + wt, (b / kWStages) & 1, abort_flag, p.limit_ns) &&
-                     mbar_wait_spin(p_full + (b & 1), (b >> 1) & 1, abort_flag, p.limit_ns);
+                const int sb = b & 1;
+                ok = mbar_wait_spin(k_full + st, kphase, abort_flag, p.limit_ns);
+                if (ok && b >= 2) ok = mbar_wait_spin(pv_done + sb, pphase, abort_flag, p.limit_ns);
                 if (!ok) break;
                 tc_fence_after();
-                const uint64_t dv = sdesc_mn_sw128(sbase + kOffW + wt * kWTile, kPanel);
-                const uint32_t a = tmem + kTmemS + 128 * (b & 1);
+                const uint64_t dk = dk0 + static_cast<uint32_t>(st) * (kTile >> 4);
+                const uint32_t d = tmem + kTmemS + 128 * sb;
 #pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    mma_f16_ts(tmem + kTmemO, a + 8 * i, dv + (2048 >> 4) * i, idesc_pv, (b > 0 || i > 0) ? 1u : 0u);
-                tc_commit(w_empty + wt);
-                tc_commit(pv_done + (b & 1));
-                if (b + 2 < nb) ok = qk(b + 2);
+                for (int i = 0; i < 4; ++i) mma_mxf8_ts(d, tq + 8 * i, dk + 2 * i, make_idesc_mxf8(128, 128, i), sfa, sfb, i > 0);
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    mma_mxf8_ts(d, tq + 32 + 8 * i, dk + 2 * i, make_idesc_mxf8(128, 128, i), sfa + 4, sfb, 1u);
+                tc_commit(s_full + sb);
+                mbar_arrive(s_full + sb);
+                tc_commit(k_empty + st);
+                if (++st == kKStages) {
+                    st = 0;
+                    kphase ^= 1;
+                }
+                if (b >= 2) pphase ^= sb;
             }
             tc_commit(drain);
             drain_wait(drain, 0, p.limit_ns);
+        }
+    } else if (warp == 2) {
+        // ------------------------------------------------------------ PV issuer
+        if (lane == 0) {
+            constexpr uint32_t idesc = make_idesc(128, 128, 0, 0, 0, 1);
+            const uint64_t dv0 = sdesc_mn_sw128(smem_u32(smem) + kOffW, kPanel);
+            bool ok = true;
+            for (int b = 0; b < nb; ++b) {
+                const int wt = b % kWStages, sb = b & 1;
+                ok = mbar_wait_spin(w_full + wt, (b / kWStages) & 1, abort_flag, p.limit_ns) &&
+                     mbar_wait_spin(p_full + sb, (b >> 1) & 1, abort_flag, p.limit_ns);
+                if (!ok) break;
+                tc_fence_after();
+                const uint64_t dv = dv0 + static_cast<uint32_t>(wt) * (kWTile >> 4);
+                const uint32_t a = tmem + kTmemS + 128 * sb;
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    mma_f16_ts(tmem + kTmemO, a + 8 * i, dv + (2048 >> 4) * i, idesc, (b > 0 || i > 0) ? 1u : 0u);
+                tc_commit(pv_done + sb);
+                tc_commit(w_empty + wt);
+            }
+            tc_commit(drain + 1);
+            drain_wait(drain + 1, 0, p.limit_ns);
         }
     } else if (warp >= kConvWarp0 && warp < kConvWarp0 + kConvWarps) {
         // ------------------------------------------------------------ V codes -> fp16

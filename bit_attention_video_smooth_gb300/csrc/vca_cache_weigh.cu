@@ -15,7 +15,7 @@
 // head's tiles stream past them: a page is read once, and a tile once for four
 // pages.  Few rows are bound by reading K (128 B a token) and the weights; many
 // by the tensor core's two FP8 products, 2 x 2 rows keys d flops.
-// Warps: 0 producer, 1 MMA issuer, 2-9 sums (two sets of four).  Every wait is bounded, as in vca_attention.cu.
+// Warps: 0 producer, 1-2 MMA issuers, 3-10 sums (two sets of four).  Every wait is bounded, as in vca_attention.cu.
 #include "vca_attention_common.cuh"
 #include "vca_cache.cuh"
 
@@ -30,7 +30,8 @@ constexpr uint32_t kTile = kBlk * kD;
 constexpr int kKP = 4;                       // pages of a unit
 constexpr int kKStages = 8, kSlots = 16;
 constexpr int kSets = 2;                     // sets of four sum warps
-constexpr int kThreads = 32 * (2 + 4 * kSets);
+constexpr int kIssuers = 2;                  // MMA issuers, for the even and the odd pages of a unit
+constexpr int kThreads = 32 * (1 + kIssuers + 4 * kSets);
 constexpr uint32_t kBarSums = 1;             // named barrier of the sum warps
 
 // A tile of N rows as it lies in the workspace and in shared memory: hi, lo
@@ -52,10 +53,10 @@ struct Layout {
     static constexpr uint32_t tmem_sfa = sbufs * cols, tmem_sfb = tmem_sfa + 4, tmem_cols = 512;
     static constexpr uint32_t offQ = kKStages * kTile, offSlot = offQ + qstages * Image<N>::stride;
     static constexpr uint32_t offSum = offSlot + kSlots * 8, offBar = offSum + 2 * kKP * kBlk * 4;   // fp32 [2][pages][128]
-    static constexpr int bars = 2 * kKStages + 2 * qstages + 2 * sbufs + 1;
+    static constexpr int bars = 2 * kKStages + 2 * qstages + 2 * sbufs + kIssuers;
     static constexpr uint32_t offMisc = offBar + bars * 8, smem = offMisc + 16 + 1024;
     static_assert(smem <= 232448, "shared memory budget");
-    static_assert(tmem_sfb + 8 * qstages <= tmem_cols, "TMEM plan");
+    static_assert(tmem_sfb + 8 * qstages * kIssuers <= tmem_cols, "TMEM plan");
 };
 
 struct WeighParams {
@@ -86,6 +87,14 @@ __device__ __forceinline__ int first_tile(const AttnParams &p, const Seq &s, int
     if (!p.causal) return 0;
     const int64_t x = static_cast<int64_t>(page) * kBlk - (s.len - s.n);
     return x <= 0 ? 0 : static_cast<int>(x * p.G / N);
+}
+
+// How many of `count` pages from `page` on the rows of a tile see.
+template <int N>
+__device__ __forceinline__ int pages_seen(const AttnParams &p, const Seq &s, int tile, int page, int count) {
+    if (!p.causal) return count;
+    const int last = min(s.n * p.G, (tile + 1) * N) - 1;
+    return min(count, (min(seen_by_row(p, s, last), s.len) + kBlk - 1) / kBlk - page);
 }
 
 __device__ __forceinline__ int64_t scan64(int64_t v) {
@@ -471,13 +480,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         for (int s = 0; s < L::qstages; ++s) {
             mbar_init(q_full + s, 1);
-            mbar_init(q_empty + s, 1 + 4 * kSets);       // the MMA's commit, the sum warps
+            mbar_init(q_empty + s, kIssuers + 4 * kSets);       // the MMAs' commits, the sum warps
         }
         for (int s = 0; s < L::sbufs; ++s) {
             mbar_init(s_full + s, 2);            // the MMA's commit, the issuer itself
             mbar_init(s_empty + s, N == 128 ? 4 * kSets : 4);
         }
-        mbar_init(drain, 1);
+        for (int i = 0; i < kIssuers; ++i) mbar_init(drain + i, 1);
         *abort_flag = 0;
         mbar_fence_init();
     }
@@ -490,7 +499,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
     // A's factors are 1 everywhere
-    if (warp >= 2 && warp < 6) {
+    if (warp > kIssuers && warp <= kIssuers + 4) {
         asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1,%1,%1,%1};" ::"r"(
                          tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + L::tmem_sfa), "r"(0x7f7f7f7fu) : "memory");
         tmem_st_wait();
@@ -549,70 +558,81 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int k = max(0, qn - L::qstages); k < qn; ++k)
                 drain_wait(q_full + k % L::qstages, (k / L::qstages) & 1, p.limit_ns);
         }
-    } else if (warp == 1) {
-        // ------------------------------------------------------------ MMA issuer
+    } else if (warp <= kIssuers) {
+        // ------------------------------------------------------------ MMA issuers
+        // one thread each: issuing costs more than the tensor core takes
         if (lane == 0) {
-            const uint32_t sbase = smem_u32(smem);
+            const int odd = warp - 1;
+            const uint32_t sbase = smem_u32(smem), tsfa = tmem + L::tmem_sfa;
             bool ok = true;
-            int kn = 0, qn = 0, sn = 0;
+            int kn = 0, qs = 0, sb = 0;
+            uint32_t qphase = 0, sphase = 1;       // a buffer's first use waits for nothing
             while (ok && wk.left > 0) {
                 const int kp = wk.count();
                 int landed = 0;
-                for (int t = first_tile<N>(p, wk.w.s, wk.page); ok && t < wk.w.tiles; ++t, ++qn) {
-                    const int qs = qn % L::qstages;
-                    ok = mbar_wait_spin(q_full + qs, (qn / L::qstages) & 1, abort_flag, p.limit_ns);
+                for (int t = first_tile<N>(p, wk.w.s, wk.page); ok && t < wk.w.tiles; ++t) {
+                    const int np = pages_seen<N>(p, wk.w.s, t, wk.page, kp);
+                    ok = mbar_wait_spin(q_full + qs, qphase, abort_flag, p.limit_ns);
                     if (!ok) break;
-                    const uint32_t img = sbase + L::offQ + qs * Image<N>::stride, tsf = tmem + L::tmem_sfb + 8 * qs;
+                    const uint32_t img = sbase + L::offQ + qs * Image<N>::stride, tsf = tmem + L::tmem_sfb + 8 * (2 * qs + odd);
                     copy_factors(tsf, img + Image<N>::sf);
                     if constexpr (N == 128) copy_factors(tsf + 4, img + Image<N>::sf + 512);
                     const uint64_t dh = sdesc_k_sw128(img), dl = sdesc_k_sw128(img + Image<N>::lo);
-                    for (int j = 0; ok && j < kp; ++j) {
-                        if (t < first_tile<N>(p, wk.w.s, wk.page + j)) break;      // nor does a later page see it
-                        const int st = (kn + j) % kKStages, sb = sn % L::sbufs;
-                        if (j >= landed) {
-                            ok = mbar_wait_spin(k_full + st, ((kn + j) / kKStages) & 1, abort_flag, p.limit_ns);
-                            landed = j + 1;
-                        }
-                        if (ok && sn >= L::sbufs) ok = mbar_wait_spin(s_empty + sb, (sn / L::sbufs - 1) & 1, abort_flag, p.limit_ns);
-                        if (!ok) break;
-                        tc_fence_after();
-                        const uint64_t dk = sdesc_k_sw128(sbase + st * kTile);
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            mma_mxf8_ss(tmem + sb * L::cols, dk + 2 * i, dh + 2 * i, make_idesc_mxf8_b(128, L::cols, i),
-                                        tmem + L::tmem_sfa, tsf, i > 0);
-                        if constexpr (N == 128) {
+                    for (int j = 0; j < np; ++j) {
+                        if ((j & 1) == odd) {
+                            const int st = (kn + j) % kKStages;
+                            if (j >= landed) {
+                                ok = mbar_wait_spin(k_full + st, ((kn + j) / kKStages) & 1, abort_flag, p.limit_ns);
+                                landed = j + 1;
+                            }
+                            ok = ok && mbar_wait_spin(s_empty + sb, sphase, abort_flag, p.limit_ns);
+                            if (!ok) break;
+                            tc_fence_after();
+                            const uint64_t dk = sdesc_k_sw128(sbase + st * kTile);
+                            const uint32_t d = tmem + sb * L::cols;
 #pragma unroll
                             for (int i = 0; i < 4; ++i)
-                                mma_mxf8_ss(tmem + sb * L::cols, dk + 2 * i, dl + 2 * i, make_idesc_mxf8_b(128, L::cols, i),
-                                            tmem + L::tmem_sfa, tsf + 4, 1u);
+                                mma_mxf8_ss(d, dk + 2 * i, dh + 2 * i, make_idesc_mxf8_b(128, L::cols, i), tsfa, tsf, i > 0);
+                            if constexpr (N == 128) {
+#pragma unroll
+                                for (int i = 0; i < 4; ++i)
+                                    mma_mxf8_ss(d, dk + 2 * i, dl + 2 * i, make_idesc_mxf8_b(128, L::cols, i), tsfa, tsf + 4, 1u);
+                            }
+                            tc_commit(s_full + sb);
+                            mbar_arrive(s_full + sb);
+                            if (t + 1 == wk.w.tiles) tc_commit(k_empty + st);
                         }
-                        if (t + 1 == wk.w.tiles) tc_commit(k_empty + st);
-                        tc_commit(s_full + sb);
-                        mbar_arrive(s_full + sb);
-                        ++sn;
+                        if (++sb == L::sbufs) {
+                            sb = 0;
+                            sphase ^= 1;
+                        }
                     }
                     if (ok) tc_commit(q_empty + qs);
+                    if (++qs == L::qstages) {
+                        qs = 0;
+                        qphase ^= 1;
+                    }
                 }
                 kn += kp;
                 if (ok) wk.next(p, kp);
             }
-            tc_commit(drain);
-            drain_wait(drain, 0, p.limit_ns);
+            tc_commit(drain + odd);
+            drain_wait(drain + odd, 0, p.limit_ns);
         }
     } else {
         // ------------------------------------------------------------ sums
         // 128 rows: each set takes half of every page's rows, whose -lse it keeps in
         // registers for the unit's pages (read from shared memory by every page they
         // take more of its bandwidth than the products do); 16 rows: every other page
-        const int set = (warp - 2) >> 2, quarter = warp & 3, row = quarter * 32 + lane;
+        const int set = (warp - 1 - kIssuers) >> 2, quarter = warp & 3, row = quarter * 32 + lane;
         constexpr int kCols = N == 128 ? 64 : 16;
         const int col0 = N == 128 ? 64 * set : 0;
         const uint32_t tl = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + col0;
         const float c0 = kCap ? p.cap_in : p.scale_log2;
         float *sSum = reinterpret_cast<float *>(smem + L::offSum);
         bool ok = true;
-        int kn = 0, qn = 0, sn = 0, un = 0;
+        int kn = 0, qn = 0, un = 0, next_sb = 0;
+        uint32_t next_phase = 0;
         while (ok && wk.left > 0) {
             const int kp = wk.count();
             float acc[kKP] = {};
@@ -623,7 +643,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (!ok) break;
                 const unsigned char *img = smem + L::offQ + qs * Image<N>::stride;
                 const int *seen = reinterpret_cast<const int *>(img + Image<N>::seen) + col0;
-                const int all_see = seen_by_row(p, wk.w.s, t * N);
+                const int all_see = seen_by_row(p, wk.w.s, t * N), np = pages_seen<N>(p, wk.w.s, t, wk.page, kp);
                 uint64_t lse[kCols / 2];
 #pragma unroll
                 for (int k = 0; k < kCols / 4; ++k) {
@@ -633,9 +653,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
 #pragma unroll
                 for (int j = 0; j < kKP; ++j) {
-                    if (!ok || j >= kp || t < first_tile<N>(p, wk.w.s, wk.page + j)) break;
-                    const int sb = sn % L::sbufs, phase = (sn / L::sbufs) & 1;
-                    ++sn;
+                    if (!ok || j >= np) break;
+                    const int sb = next_sb;
+                    const uint32_t phase = next_phase;
+                    if (++next_sb == L::sbufs) {
+                        next_sb = 0;
+                        next_phase ^= 1;
+                    }
                     if (N == 16 && (j & 1) != set) continue;
                     ok = __all_sync(0xffffffffu, mbar_wait(s_full + sb, phase, abort_flag, p.limit_ns));
                     if (!ok) break;
