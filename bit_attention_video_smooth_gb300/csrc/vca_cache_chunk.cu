@@ -13,10 +13,11 @@
 //           the tensor core takes for it.  QK(b+2) waits for PV(b), which reads
 //           P(b), lying over S(b) in TMEM; PV(b+1) fills that wait
 //   4-7     V codes -> fp16 in shared memory, a page ahead of PV (two buffers)
-//   8-15    softmax, one thread per row and page: warps w and w + 4 share a TMEM
-//           lane quarter and take alternate pages; the reference maximum is
-//           handed from page to page and moves only when a page's maximum
-//           exceeds it by 8 (then O is rescaled in TMEM)
+//   8-15    softmax, two threads per row, 64 scores of every page each, which stay in
+//           registers from the maximum to the probabilities; warps w and w + 4
+//           share a TMEM lane quarter and tell each other their half's maximum.
+//           The reference maximum moves only when a page's exceeds it by 8 (then O
+//           is rescaled in TMEM)
 // QK: E4M3 codes of K straight from TMA.  A bf16 query element has 8 significant
 // bits and an E4M3 code 4, so q = hi + lo: per 32 channels a power of two puts
 // the largest element in [2^7, 2^8), hi = E4M3(q), lo = E4M3(32 (q - hi)), and
@@ -52,11 +53,11 @@ constexpr uint32_t kOffK = 0;
 constexpr uint32_t kOffV = kOffK + kKStages * kTile;
 constexpr uint32_t kOffW = kOffV + kVStages * kTile;
 constexpr uint32_t kOffSlot = kOffW + kWStages * kWTile;         // float4 [kSlots]: sk, V factor, O factor, reference scale
-constexpr uint32_t kOffMX = kOffSlot + kSlots * 16;              // fp32 [2][128] reference maximum handed on
-constexpr uint32_t kOffL = kOffMX + 2 * kRows * 4;               // fp32 [2][128] partial l, [2][128] its maximum
-constexpr uint32_t kOffF = kOffL + 4 * kRows * 4;                // fp32 [128] the rows' factors
+constexpr uint32_t kOffMX = kOffSlot + kSlots * 16;              // fp32 [2][2][128] the halves' maxima, by turns
+constexpr uint32_t kOffL = kOffMX + 4 * kRows * 4;               // fp32 [2][128] the halves' l
+constexpr uint32_t kOffF = kOffL + 2 * kRows * 4;                // fp32 [128] the rows' factors
 constexpr uint32_t kOffBar = kOffF + kRows * 4;
-constexpr uint32_t kBarQuery = kBarHand0 + 8;                    // + quarter: the factors handed over
+constexpr uint32_t kBarPair = 2;                                 // + quarter: the two warps of a row's halves
 constexpr int kNumBars = 1 + 2 * kKStages + 2 * kVStages + 2 * kWStages + 2 + 2 + 2 + 2;
 constexpr uint32_t kOffMisc = kOffBar + kNumBars * 8;
 constexpr uint32_t kSmem = kOffMisc + 16 + 1024;
@@ -251,8 +252,8 @@ __device__ __forceinline__ float rcp_approx(float x) {
 struct PageScore {
     float c, bias;       // no cap: p = 2^(S c + bias); cap: p = 2^(r t + bias), r = 1 / (1 + 2^(S c))
     float t;             // -2 cap log2(e)
-    int lim;             // columns that the row sees (cap)
-    bool edge;           // some row of the warp sees fewer than all (cap)
+    int lim;             // how many of the thread's 64 columns the row sees
+    bool edge;           // some row of the warp does not see all
 };
 
 // 32 raw scores -> 16 words of fp16 pairs; the unrounded probabilities add to l2.
@@ -287,9 +288,10 @@ __device__ __forceinline__ void probabilities(const uint32_t (&X)[32], const Pag
 }
 
 // A warp's 32 rows of V codes as fp16 times a power of two, rows from `live` on
-// as zeros.  Eight lanes a row, one 16-byte chunk of codes each: two 16-byte
-// chunks of fp16, the second first in the upper panel, so that a quarter warp's
-// stores fall into different banks.
+// as zeros.  A lane takes a 16-byte chunk of codes to two 16-byte chunks of fp16,
+// lanes 0-3 of eight the lower 64 channels of one row, lanes 4-7 the upper ones of
+// its neighbour: by the swizzle a quarter warp's accesses then fall into
+// different banks.
 template <bool kPlain>
 __device__ __forceinline__ void convert_rows(const unsigned char *src, unsigned char *dst, int part, float factor, int live) {
     const int lane = threadIdx.x & 31, c = lane & 7, up = c >> 2, oc = 2 * (c & 3);
@@ -297,7 +299,7 @@ __device__ __forceinline__ void convert_rows(const unsigned char *src, unsigned 
     dst += up * kPanel;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        const int r = part * 32 + 4 * i + (lane >> 3);
+        const int r = part * 32 + 8 * (i >> 1) + 2 * (lane >> 3) + ((i & 1) ? 1 - up : up);
         const uint4 v = *reinterpret_cast<const uint4 *>(src + sw128_offset(r, c));
         const uint32_t w[4] = {v.x, v.y, v.z, v.w};
         uint32_t o[8];
@@ -312,25 +314,21 @@ __device__ __forceinline__ void convert_rows(const unsigned char *src, unsigned 
                 o[2 * k + 1] = r < live ? *reinterpret_cast<const uint32_t *>(&y) : 0u;
             }
         }
-        const uint4 lo = make_uint4(o[0], o[1], o[2], o[3]), hi = make_uint4(o[4], o[5], o[6], o[7]);
-        *reinterpret_cast<uint4 *>(dst + sw128_offset(r, oc + up)) = up ? hi : lo;
-        *reinterpret_cast<uint4 *>(dst + sw128_offset(r, oc + 1 - up)) = up ? lo : hi;
+        *reinterpret_cast<uint4 *>(dst + sw128_offset(r, oc)) = make_uint4(o[0], o[1], o[2], o[3]);
+        *reinterpret_cast<uint4 *>(dst + sw128_offset(r, oc + 1)) = make_uint4(o[4], o[5], o[6], o[7]);
     }
 }
 
-// The scores of keys that the row does not see, columns lim and up, become -inf
-// in TMEM: the pages' common path then needs no masks.
-__device__ __forceinline__ void mask_scores(uint32_t tS, int lim) {
-#pragma unroll 1
-    for (int i = 0; i < kBlk; i += 32) {
-        uint32_t X[32];
-        VCA_TMEM_LD32(tS + i, X);
-        tmem_ld_wait();
+// Scores of keys that the row does not see, columns col0 + lim and up, become
+// -inf; returns the largest of the others.
+__device__ __forceinline__ float mask_scores(uint32_t (&X)[32], int col0, int lim) {
+    float m = __int_as_float(0xff800000);
 #pragma unroll
-        for (int e = 0; e < 32; ++e) X[e] = i + e < lim ? X[e] : 0xff800000u;
-        VCA_TMEM_ST32(tS + i, X);
+    for (int e = 0; e < 32; ++e) {
+        if (col0 + e >= lim) X[e] = 0xff800000u;
+        m = fmaxf(m, __uint_as_float(X[e]));
     }
-    tmem_st_wait();
+    return m;
 }
 
 template <bool kCap>
@@ -348,7 +346,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     int *abort_flag = reinterpret_cast<int *>(smem + kOffMisc + 4);
     float4 *sSlot = reinterpret_cast<float4 *>(smem + kOffSlot);
     float *sMX = reinterpret_cast<float *>(smem + kOffMX);
-    float *sL = reinterpret_cast<float *>(smem + kOffL), *sLM = sL + 2 * kRows;
+    float *sL = reinterpret_cast<float *>(smem + kOffL);
     float *sF = reinterpret_cast<float *>(smem + kOffF);
 
     const AttnParams &p = cp.a;
@@ -378,7 +376,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(s_full + i, 2);      // the MMA's commit and the issuer itself
-            mbar_init(p_full + i, 4);
+            mbar_init(p_full + i, kSoftmaxWarps);
             mbar_init(pv_done + i, 1);
         }
         mbar_init(drain, 1);
@@ -545,153 +543,129 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     } else if (warp >= kSoftWarp0) {
         // ------------------------------------------------------------ softmax
-        const int quarter = warp & 3, par = (warp - kSoftWarp0) >> 2, row = quarter * 32 + lane;
-        const uint32_t bar_out = kBarHand0 + 2 * quarter + par, bar_in = kBarHand0 + 2 * quarter + (par ^ 1);
+        const int quarter = warp & 3, half = (warp - kSoftWarp0) >> 2, row = quarter * 32 + lane;
+        const uint32_t bar_pair = kBarPair + quarter;
         const uint32_t tl = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
         const float kNegInf = __int_as_float(0xff800000);
         const int r = r0 + row;
         const bool real = r < R;
         float f;      // raw score -> log2 units (or the cap's inner argument), but for the page's scale
-        {
-            const uint16_t *at = real ? query_row(p, it.s, h, r) : nullptr;
-            if (par == 0) {
-                f = store_query(tl, quarter, at);
-                tmem_st_wait();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(q_full);
-                sF[row] = f;
-                bar_arrive_release(kBarQuery + quarter, 64);
-            } else {
-                bar_sync(kBarQuery + quarter, 64);
-                f = sF[row];
-            }
-            f *= kCap ? p.cap_in : p.scale_log2;
+        if (half == 0) {
+            f = store_query(tl, quarter, real ? query_row(p, it.s, h, r) : nullptr);
+            tmem_st_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(q_full);
+            sF[row] = f;
         }
-        const int seen = real ? min(seen_by_row(p, it.s, r), it.s.len) : it.s.len;
+        bar_sync(bar_pair, 64);
+        if (half == 1) f = sF[row];
+        f *= kCap ? p.cap_in : p.scale_log2;
+        const int seen = (real ? min(seen_by_row(p, it.s, r), it.s.len) : it.s.len) - it.page0 * kBlk - 64 * half;
+        PageScore s;
+        s.t = -2.0f * p.cap_out;
         float m = kNegInf, l = 0.0f;
         bool ok = true;
-        for (int b = par; b < nb; b += 2) {
-            if (ok) ok = __all_sync(0xffffffffu, mbar_wait(s_full + par, (b >> 1) & 1, abort_flag, p.limit_ns));
-            const uint32_t tS = tl + kTmemS + 128 * par;
+        for (int b = 0; b < nb; ++b) {
+            const int sb = b & 1;
+            if (ok) ok = __all_sync(0xffffffffu, mbar_wait(s_full + sb, (b >> 1) & 1, abort_flag, p.limit_ns));
+            const uint32_t tS = tl + kTmemS + 128 * sb;
             uint32_t X0[32], X1[32];
-            float pm = kNegInf;
-            PageScore s;
+            float bm = kNegInf;
             float4 slot = make_float4(0.0f, 0.0f, 1.0f, 1.0f);
-            s.lim = 0;
             s.edge = false;
             if (ok) {
                 tc_fence_after();
+                float m0, m1;
+                VCA_TMEM_LDMAX32(tS + 64 * half, X0, m0);
+                VCA_TMEM_LDMAX32(tS + 64 * half + 32, X1, m1);
                 slot = sSlot[b % kSlots];
-                s.lim = slot.x < 0.0f ? 0 : seen - (it.page0 + b) * kBlk;
-                s.edge = __any_sync(0xffffffffu, s.lim < kBlk);
-                if (s.edge) mask_scores(tS, s.lim);
-                float m0, m1, m2, m3;
-                VCA_TMEM_LDMAX32(tS + 64, X0, m2);
-                VCA_TMEM_LDMAX32(tS + 96, X1, m3);
+                s.lim = slot.x < 0.0f ? 0 : seen - b * kBlk;
+                s.edge = __any_sync(0xffffffffu, s.lim < 64);
+                s.c = fmaxf(__fmul_rn(f, slot.x), 0x1p-126f);      // above 0, so that -inf stays -inf
                 tmem_ld_wait();
-                VCA_TMEM_LDMAX32(tS, X0, m0);
-                VCA_TMEM_LDMAX32(tS + 32, X1, m1);
-                tmem_ld_wait();
-                pm = fmaxf(fmaxf(m0, m1), fmaxf(m2, m3));
+                if (s.edge) {
+                    m0 = mask_scores(X0, 0, s.lim);
+                    m1 = mask_scores(X1, 32, s.lim);
+                }
+                const float pm = fmaxf(m0, m1);
+                if (pm != kNegInf)
+                    bm = kCap ? fmaf(rcp_approx(1.0f + ex2_approx(pm * s.c)), s.t, p.cap_out) : __fmul_rn(pm, s.c);
             }
-            // the reference maximum after page b - 1 from the partner, after page b
-            // handed on; NaN marks a partner that gave up
-            float m_in = kNegInf;
-            if (b >= 1) {
-                bar_sync(bar_in, 64);
-                m_in = sMX[(par ^ 1) * kRows + row];
-            }
-            const bool valid = ok && !(m_in != m_in);
-            s.c = fmaxf(__fmul_rn(f, slot.x), 0x1p-126f);      // above 0, so that -inf stays -inf
-            s.t = -2.0f * p.cap_out;
-            float bm = kNegInf;
-            if (pm != kNegInf)
-                bm = kCap ? fmaf(rcp_approx(1.0f + ex2_approx(pm * s.c)), s.t, p.cap_out) : __fmul_rn(pm, s.c);
-            const bool moved = valid && bm > __fadd_rn(m_in, kLazyTau);
-            const float m_new = moved ? bm : m_in;
-            if (b + 1 < nb) {
-                sMX[par * kRows + row] = valid ? m_new : __int_as_float(0x7fc00000);
-                bar_arrive_release(bar_out, 64);
-            }
-            if (!__all_sync(0xffffffffu, valid)) {
+            // the row's maximum over both halves; NaN: the other half gave up.  Both
+            // halves have read their scores when they meet, so P may be written over
+            // them.  Buffers by turns: the next page's barrier separates this read
+            // from the write after it
+            float *mx = sMX + sb * 2 * kRows;
+            mx[half * kRows + row] = ok ? bm : __int_as_float(0x7fc00000);
+            bar_sync(bar_pair, 64);
+            const float other = mx[(half ^ 1) * kRows + row];
+            if (!__all_sync(0xffffffffu, ok && !(other != other))) {
                 ok = false;
                 break;
             }
-            const float mu = m_new == kNegInf ? 0.0f : m_new;      // a row that sees nothing yet
+            const float top = fmaxf(bm, other);
+            const bool moved = top > __fadd_rn(m, kLazyTau);
+            const float m_in = m;
+            if (moved) {
+                l = __fmul_rn(l, ex2_approx(__fsub_rn(m, top)));
+                m = top;
+            }
+            const float mu = m == kNegInf ? 0.0f : m;      // a row that sees nothing yet
             s.bias = kCap ? p.cap_out - mu : -mu;
-            if (m != m_new) l = __fmul_rn(l, ex2_approx(__fsub_rn(m, m_new)));
-            m = m_new;
             uint64_t l2 = pk2(__float_as_uint(l), 0u);
-            // P over S: columns 16 i .. 16 i + 15 from scores 32 i .. 32 i + 31, all of them read by then
-            const uint32_t tP = tS;
             uint32_t W[16];
             probabilities<kCap>(X0, s, 0, l2, W);
-            VCA_TMEM_LD32(tS + 64, X0);
-            VCA_TMEM_ST16(tP, W);
+            VCA_TMEM_ST16(tS + 32 * half, W);
             probabilities<kCap>(X1, s, 32, l2, W);
-            tmem_ld_wait();
-            VCA_TMEM_LD32(tS + 96, X1);
-            VCA_TMEM_ST16(tP + 16, W);
-            probabilities<kCap>(X0, s, 64, l2, W);
-            VCA_TMEM_ST16(tP + 32, W);
-            tmem_ld_wait();
-            probabilities<kCap>(X1, s, 96, l2, W);
-            VCA_TMEM_ST16(tP + 48, W);
+            VCA_TMEM_ST16(tS + 32 * half + 16, W);
             {
                 float a, c;
                 upk2(l2, a, c);
                 l = __fadd_rn(a, c);
             }
-            // O after PV(b - 1) to the new reference maximum and reference scale
-            const float alpha = b > 0 ? (moved ? ex2_approx(__fsub_rn(m_in, m_new)) : 1.0f) * slot.z : 1.0f;
+            // this half's channels of O after PV(b - 1) to the new reference maximum and scale
+            const float alpha = b > 0 ? (moved ? ex2_approx(__fsub_rn(m_in, m)) : 1.0f) * slot.z : 1.0f;
             if (__any_sync(0xffffffffu, alpha != 1.0f)) {
-                ok = __all_sync(0xffffffffu, mbar_wait(pv_done + (par ^ 1), ((b - 1) >> 1) & 1, abort_flag, p.limit_ns));
+                ok = __all_sync(0xffffffffu, mbar_wait(pv_done + (sb ^ 1), ((b - 1) >> 1) & 1, abort_flag, p.limit_ns));
                 if (ok) {
                     tc_fence_after();
 #pragma unroll 1
-                    for (int i = 0; i < kD / 32; ++i) {
+                    for (int i = 0; i < 2; ++i) {
                         uint32_t o[32];
-                        VCA_TMEM_LD32(tl + kTmemO + 32 * i, o);
+                        VCA_TMEM_LD32(tl + kTmemO + 64 * half + 32 * i, o);
                         tmem_ld_wait();
 #pragma unroll
                         for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__fmul_rn(__uint_as_float(o[e]), alpha));
-                        VCA_TMEM_ST32(tl + kTmemO + 32 * i, o);
+                        VCA_TMEM_ST32(tl + kTmemO + 64 * half + 32 * i, o);
                     }
                 }
             }
-            // a thread that gave up here still hands a NaN on at its next page
+            // a thread that gave up here tells the other half at the next page
             if (ok) {
                 tmem_st_wait();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(p_full + par);
+                if (lane == 0) mbar_arrive(p_full + sb);
             }
         }
         // ------------------------------------------------------------ epilogue
-        // this thread's last page lb: PV(lb) complete (PV(lb - 2) was when S(lb) came)
-        const int lb = ((nb - 1) & 1) == par ? nb - 1 : nb - 2;
-        if (ok && lb >= 0) ok = __all_sync(0xffffffffu, mbar_wait(pv_done + par, (lb >> 1) & 1, abort_flag, p.limit_ns));
-        sL[par * kRows + row] = l;
-        sLM[par * kRows + row] = lb >= 0 ? m : kNegInf;
+        // PV(nb - 1) complete (PV(nb - 3) was when S(nb - 1) came)
+        if (ok)
+            ok = __all_sync(0xffffffffu, mbar_wait(pv_done + ((nb - 1) & 1), ((nb - 1) >> 1) & 1, abort_flag, p.limit_ns));
+        sL[half * kRows + row] = l;
         ok = bar_and(ok, kBarSoftmax, 32 * kSoftmaxWarps);
         if (ok) {
             tc_fence_after();
-            const float M = sLM[((nb - 1) & 1) * kRows + row], Mu = M == kNegInf ? 0.0f : M;
-            float L = 0.0f;
-#pragma unroll
-            for (int q = 0; q < 2; ++q) {
-                const float mq = sLM[q * kRows + row];
-                if (mq != kNegInf) L = fmaf(sL[q * kRows + row], mq == M ? 1.0f : ex2_approx(__fsub_rn(mq, M)), L);
-            }
+            const float M = m, Mu = M == kNegInf ? 0.0f : M, L = __fadd_rn(sL[row], sL[kRows + row]);
             const float ref = sSlot[(nb - 1) % kSlots].w;
             if (it.parts == 1) {
                 const float inv = L > 0.0f || L != L ? 1.0f / L : 0.0f;
-                uint16_t *orow = real ? p.O + out_row(p, it.s, h, r) * kD + 64 * par : nullptr;
+                uint16_t *orow = real ? p.O + out_row(p, it.s, h, r) * kD + 64 * half : nullptr;
 #pragma unroll 1
                 for (int i = 0; i < 2; ++i) {
                     uint32_t o[32], w[16];
-                    VCA_TMEM_LD32(tl + kTmemO + 64 * par + 32 * i, o);
+                    VCA_TMEM_LD32(tl + kTmemO + 64 * half + 32 * i, o);
                     tmem_ld_wait();
 #pragma unroll
                     for (int e = 0; e < 16; ++e)
@@ -703,23 +677,23 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 make_uint4(w[4 * e], w[4 * e + 1], w[4 * e + 2], w[4 * e + 3]);
                     }
                 }
-                if (real && par == 0 && p.lse) p.lse[out_row(p, it.s, h, r)] = Mu * 0.6931471805599453f + logf(L);
+                if (real && half == 0 && p.lse) p.lse[out_row(p, it.s, h, r)] = Mu * 0.6931471805599453f + logf(L);
             } else {
                 float *part = p.part + (static_cast<int64_t>(h) * gridDim.x + it.slot) * kPartFloats;
 #pragma unroll 1
                 for (int i = 0; i < 2; ++i) {
                     uint32_t o[32];
-                    VCA_TMEM_LD32(tl + kTmemO + 64 * par + 32 * i, o);
+                    VCA_TMEM_LD32(tl + kTmemO + 64 * half + 32 * i, o);
                     tmem_ld_wait();
                     if (real) {
-                        float4 *at = reinterpret_cast<float4 *>(part + row * kD + 64 * par + 32 * i);
+                        float4 *at = reinterpret_cast<float4 *>(part + row * kD + 64 * half + 32 * i);
 #pragma unroll
                         for (int e = 0; e < 8; ++e)
                             at[e] = make_float4(__uint_as_float(o[4 * e]) * ref, __uint_as_float(o[4 * e + 1]) * ref,
                                                 __uint_as_float(o[4 * e + 2]) * ref, __uint_as_float(o[4 * e + 3]) * ref);
                     }
                 }
-                if (par == 0) {
+                if (half == 0) {
                     part[kRows * kD + row] = M;
                     part[kRows * kD + kRows + row] = L;
                 }
