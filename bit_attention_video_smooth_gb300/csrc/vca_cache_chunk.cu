@@ -568,39 +568,41 @@ __global__ void __launch_bounds__(kThreads, 1)
         bool ok = true;
         for (int b = 0; b < nb; ++b) {
             const int sb = b & 1;
+            float *mx = sMX + sb * 2 * kRows;
             if (ok) ok = __all_sync(0xffffffffu, mbar_wait(s_full + sb, (b >> 1) & 1, abort_flag, p.limit_ns));
+            if (!ok) {
+                // the other half learns of it where they meet
+                mx[half * kRows + row] = __int_as_float(0x7fc00000);
+                bar_sync(bar_pair, 64);
+                break;
+            }
             const uint32_t tS = tl + kTmemS + 128 * sb;
             uint32_t X0[32], X1[32];
             float bm = kNegInf;
-            float4 slot = make_float4(0.0f, 0.0f, 1.0f, 1.0f);
-            s.edge = false;
-            if (ok) {
-                tc_fence_after();
-                float m0, m1;
-                VCA_TMEM_LDMAX32(tS + 64 * half, X0, m0);
-                VCA_TMEM_LDMAX32(tS + 64 * half + 32, X1, m1);
-                slot = sSlot[b % kSlots];
-                s.lim = slot.x < 0.0f ? 0 : seen - b * kBlk;
-                s.edge = __any_sync(0xffffffffu, s.lim < 64);
-                s.c = fmaxf(__fmul_rn(f, slot.x), 0x1p-126f);      // above 0, so that -inf stays -inf
-                tmem_ld_wait();
-                if (s.edge) {
-                    m0 = mask_scores(X0, 0, s.lim);
-                    m1 = mask_scores(X1, 32, s.lim);
-                }
-                const float pm = fmaxf(m0, m1);
-                if (pm != kNegInf)
-                    bm = kCap ? fmaf(rcp_approx(1.0f + ex2_approx(pm * s.c)), s.t, p.cap_out) : __fmul_rn(pm, s.c);
+            tc_fence_after();
+            float m0, m1;
+            VCA_TMEM_LDMAX32(tS + 64 * half, X0, m0);
+            VCA_TMEM_LDMAX32(tS + 64 * half + 32, X1, m1);
+            const float4 slot = sSlot[b % kSlots];
+            s.lim = slot.x < 0.0f ? 0 : seen - b * kBlk;
+            s.edge = __any_sync(0xffffffffu, s.lim < 64);
+            s.c = fmaxf(__fmul_rn(f, slot.x), 0x1p-126f);      // above 0, so that -inf stays -inf
+            tmem_ld_wait();
+            if (s.edge) {
+                m0 = mask_scores(X0, 0, s.lim);
+                m1 = mask_scores(X1, 32, s.lim);
             }
+            const float pm = fmaxf(m0, m1);
+            if (pm != kNegInf)
+                bm = kCap ? fmaf(rcp_approx(1.0f + ex2_approx(pm * s.c)), s.t, p.cap_out) : __fmul_rn(pm, s.c);
             // the row's maximum over both halves; NaN: the other half gave up.  Both
             // halves have read their scores when they meet, so P may be written over
             // them.  Buffers by turns: the next page's barrier separates this read
             // from the write after it
-            float *mx = sMX + sb * 2 * kRows;
-            mx[half * kRows + row] = ok ? bm : __int_as_float(0x7fc00000);
+            mx[half * kRows + row] = bm;
             bar_sync(bar_pair, 64);
             const float other = mx[(half ^ 1) * kRows + row];
-            if (!__all_sync(0xffffffffu, ok && !(other != other))) {
+            if (__any_sync(0xffffffffu, other != other)) {
                 ok = false;
                 break;
             }
