@@ -5,14 +5,17 @@
 // One CTA takes 128 query rows of a (sequence, KV head) -- rows i G + g: the G
 // query heads that share the KV head are rows of one tile, so its codes are
 // read once for all of them -- and a run of the pages they see: all of them, or
-// an even part where there are too few tiles to fill the GPU (then a second
-// kernel joins the parts).  Warps:
+// an even part where there are too few tiles to fill the GPU (then a last
+// kernel joins the parts).  A first kernel lays out every tile's queries as the
+// product wants them, so that a CTA only copies them, and lists the CTAs' work.
+// Warps:
 //   0       TMA producer: K and V tiles into rings of three, each page's scales
 //           into a ring of slots
 //   1, 2    MMA issuers, one thread each, QK and PV: issuing an MMA costs more than
 //           the tensor core takes for it.  QK(b+2) waits for PV(b), which reads
 //           P(b), lying over S(b) in TMEM; PV(b+1) fills that wait
-//   4-7     V codes -> fp16 in shared memory, a page ahead of PV (two buffers)
+//   4-7     the queries into TMEM, then V codes -> fp16 in shared memory, a page
+//           ahead of PV (two buffers)
 //   8-15    softmax, two threads per row, 64 scores of every page each, which stay in
 //           registers from the maximum to the probabilities; warps w and w + 4
 //           share a TMEM lane quarter and tell each other their half's maximum.
@@ -55,8 +58,7 @@ constexpr uint32_t kOffW = kOffV + kVStages * kTile;
 constexpr uint32_t kOffSlot = kOffW + kWStages * kWTile;         // float4 [kSlots]: sk, V factor, O factor, reference scale
 constexpr uint32_t kOffMX = kOffSlot + kSlots * 16;              // fp32 [2][2][128] the halves' maxima, by turns
 constexpr uint32_t kOffL = kOffMX + 4 * kRows * 4;               // fp32 [2][128] the halves' l
-constexpr uint32_t kOffF = kOffL + 2 * kRows * 4;                // fp32 [128] the rows' factors
-constexpr uint32_t kOffBar = kOffF + kRows * 4;
+constexpr uint32_t kOffBar = kOffL + 2 * kRows * 4;
 constexpr uint32_t kBarPair = 2;                                 // + quarter: the two warps of a row's halves
 constexpr int kNumBars = 1 + 2 * kKStages + 2 * kVStages + 2 * kWStages + 2 + 2 + 2 + 2;
 constexpr uint32_t kOffMisc = kOffBar + kNumBars * 8;
@@ -66,13 +68,30 @@ static_assert(kSmem <= 232448, "shared memory budget");
 constexpr int kPartFloats = kRows * kD + 2 * kRows;   // O, m, l of a part
 constexpr int kSmallest = 4;                          // pages of a part at least
 
-struct ChunkParams {
-    AttnParams a;
-    int split;         // 0: a CTA takes all pages of a tile; otherwise how many CTAs the pages should keep busy
+// What one CTA does: pages [page0, page0 + pages) of a tile, as one of `parts`
+// parts, `slot` its place among the parts of its head, `image` its tile's among
+// the tiles.  pages = 0: nothing.
+struct alignas(16) Item {
+    int b, tile, page0, pages, parts, slot, image, pad;
+    Seq s;
 };
 
+struct ChunkParams {
+    AttnParams a;
+    Item *items;         // [items] of every head alike
+    int *first;          // [tiles] a tile's first item, where tiles are cut
+    uint8_t *images;     // [heads of a launch][tiles][kImage]
+    int h0;              // the launch's first head
+    int tiles, grid;     // tiles and items of a head at most
+    int split;           // CTAs that parts of tiles should fill; 0: tiles are not cut
+};
+
+// A tile's queries: hi, then lo codes, each as eight 16-byte columns of 128 rows,
+// then the words of their factors.
+constexpr int kImage = 2 * kTile + 2 * kRows * 4;
+
 // ---------------------------------------------------------------------------
-// Tiles and their parts
+// Tiles
 // ---------------------------------------------------------------------------
 __device__ __forceinline__ int tiles_of(const AttnParams &p, const Seq &s) {
     return static_cast<int>((static_cast<int64_t>(s.n) * p.G + kRows - 1) / kRows);
@@ -82,8 +101,6 @@ __device__ __forceinline__ int pages_of(const AttnParams &p, const Seq &s, int t
     const int last = min(static_cast<int64_t>(s.n) * p.G, (static_cast<int64_t>(tile) + 1) * kRows) - 1;
     return max(1, (min(seen_by_row(p, s, last), s.len) + kBlk - 1) / kBlk);
 }
-__device__ __forceinline__ int parts_of(int pages, int share) { return share > 0 ? (pages + share - 1) / share : 1; }
-
 __device__ __forceinline__ int warp_scan(int v) {
     const int lane = threadIdx.x & 31;
 #pragma unroll
@@ -93,80 +110,154 @@ __device__ __forceinline__ int warp_scan(int v) {
     }
     return v;
 }
-
-// Pages of a part: an even share of all the tiles' pages of all heads (a warp's work).
-__device__ int share_of(const ChunkParams &cp) {
-    if (cp.split == 0) return 0;
-    const AttnParams &p = cp.a;
-    int64_t all = 0;
-    for (int b = threadIdx.x & 31; b < p.c.B; b += 32) {
-        const Seq s = load_seq(p.c, p.start, p.T, b);
-        const int tiles = tiles_of(p, s);
-        for (int t = 0; t < tiles; ++t) all += pages_of(p, s, t);
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) all += __shfl_xor_sync(0xffffffffu, all, o);
-    return max(kSmallest, static_cast<int>((all * p.c.H + cp.split - 1) / cp.split));
-}
-
-// A tile, and one of its parts: pages [page0, page0 + pages).
-struct Item {
-    int b, tile, part, parts, page0, pages, slot;   // slot: the part's place among all parts of its head
-    Seq s;
-};
-
-// The index-th part of a head (by_tile: the index-th tile, its part 0); false behind the last one.
-__device__ bool find_item(const ChunkParams &cp, int share, int index, bool by_tile, Item &it) {
-    const AttnParams &p = cp.a;
+// The index-th tile of a head: its sequence and place there (a warp's work).
+__device__ bool find_tile(const AttnParams &p, int index, int &b, int &tile) {
     const int lane = threadIdx.x & 31;
-    int before = 0, slots = 0;
+    int before = 0;
     for (int b0 = 0; b0 < p.c.B; b0 += 32) {
-        Seq mine{0, 0, 0, false};
-        int cnt = 0, parts = 0;
-        if (b0 + lane < p.c.B) {
-            mine = load_seq(p.c, p.start, p.T, b0 + lane);
-            const int tiles = tiles_of(p, mine);
-            if (share == 0) {
-                parts = tiles;
-            } else {
-                for (int t = 0; t < tiles; ++t) parts += parts_of(pages_of(p, mine, t), share);
-            }
-            cnt = by_tile ? tiles : parts;
-        }
-        const int incl = warp_scan(cnt) + before;
-        const int pincl = warp_scan(parts) + slots;
+        const int t = b0 + lane < p.c.B ? tiles_of(p, load_seq(p.c, p.start, p.T, b0 + lane)) : 0;
+        const int incl = warp_scan(t) + before;
         const uint32_t hit = __ballot_sync(0xffffffffu, index < incl);
         if (hit) {
             const int l = __ffs(hit) - 1;
-            it.b = b0 + l;
-            int rest = index - __shfl_sync(0xffffffffu, incl - cnt, l);
-            it.slot = __shfl_sync(0xffffffffu, pincl - parts, l);
-            it.s = load_seq(p.c, p.start, p.T, it.b);
-            for (int t = 0;; ++t) {
-                int q;
-                if (share == 0 && !by_tile) {
-                    t = rest;      // one part each: straight to the tile
-                    it.slot += rest;
-                    rest = 0;
-                }
-                it.tile = t;
-                it.pages = pages_of(p, it.s, t);
-                q = it.parts = parts_of(it.pages, share);
-                if (by_tile ? rest == 0 : rest < q) break;
-                rest -= by_tile ? 1 : q;
-                it.slot += q;
-            }
-            it.part = by_tile ? 0 : rest;
-            it.slot += it.part;
-            const int all = it.pages;
-            it.page0 = static_cast<int>(static_cast<int64_t>(all) * it.part / it.parts);
-            it.pages = static_cast<int>(static_cast<int64_t>(all) * (it.part + 1) / it.parts) - it.page0;
+            b = b0 + l;
+            tile = index - __shfl_sync(0xffffffffu, incl - t, l);
             return true;
         }
         before = __shfl_sync(0xffffffffu, incl, 31);
-        slots = __shfl_sync(0xffffffffu, pincl, 31);
     }
     return false;
+}
+
+// The list of work where tiles are cut (fewer than kCutMost of them in a head):
+// into parts of at most `share` pages, the least for which all heads' parts
+// fit cp.split CTAs.
+constexpr int kCutMost = 2 * 152, kPlanThreads = 512;
+__device__ void plan_parts(const ChunkParams &cp) {
+    __shared__ int sB[kCutMost], sTile[kCutMost], sParts[kCutMost], sSum[kPlanThreads / 32], sTiles;
+    const AttnParams &p = cp.a;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    if (warp == 0) {
+        int before = 0;
+        for (int b0 = 0; b0 < p.c.B; b0 += 32) {
+            const int n = b0 + lane < p.c.B ? tiles_of(p, load_seq(p.c, p.start, p.T, b0 + lane)) : 0;
+            const int incl = warp_scan(n) + before;
+            for (int t = 0; t < n; ++t) {
+                sB[incl - n + t] = b0 + lane;
+                sTile[incl - n + t] = t;
+            }
+            before = __shfl_sync(0xffffffffu, incl, 31);
+        }
+        if (lane == 0) sTiles = before;
+    }
+    __syncthreads();
+    const int tiles = sTiles;
+    Seq s{0, 0, 0, false};
+    int pages = 0;
+    if (tid < tiles) {
+        s = load_seq(p.c, p.start, p.T, sB[tid]);
+        pages = pages_of(p, s, sTile[tid]);
+    }
+    auto block_sum = [&](int v) {
+        v = __reduce_add_sync(0xffffffffu, v);
+        __syncthreads();
+        if (lane == 0) sSum[warp] = v;
+        __syncthreads();
+        int sum = 0;
+        for (int i = 0; i < kPlanThreads / 32; ++i) sum += sSum[i];
+        return sum;
+    };
+    int lo = kSmallest, hi = max(kSmallest, p.c.cols);      // the share lies in [lo, hi]
+    while (lo < hi) {
+        const int mid = lo + (hi - lo) / 2;
+        if (static_cast<int64_t>(block_sum((pages + mid - 1) / mid)) * p.c.H <= cp.split)
+            hi = mid;
+        else
+            lo = mid + 1;
+    }
+    const int parts = (pages + lo - 1) / lo;
+    if (tid < tiles) sParts[tid] = parts;
+    __syncthreads();
+    int slot = 0, total = 0;
+    for (int t = 0; t < tiles; ++t) {
+        if (t < tid) slot += sParts[t];
+        total += sParts[t];
+    }
+    if (tid < tiles) {
+        cp.first[tid] = slot;
+        for (int i = 0; i < parts; ++i) {
+            const int from = static_cast<int>(static_cast<int64_t>(pages) * i / parts);
+            const int to = static_cast<int>(static_cast<int64_t>(pages) * (i + 1) / parts);
+            cp.items[slot + i] = Item{sB[tid], sTile[tid], from, to - from, parts, slot + i, tid, 0, s};
+        }
+    }
+    for (int i = total + tid; i < cp.grid; i += kPlanThreads) cp.items[i].pages = 0;
+    for (int i = tiles + tid; i < cp.tiles; i += kPlanThreads) cp.first[i] = -1;
+}
+
+// One CTA per (tile, head), one thread per row and 32 channels: a query row split
+// as hi + lo, with factors that carry the whole power of two, so that a score is
+// the product times softmax_scale alone; and the list of work.
+__global__ void __launch_bounds__(kPlanThreads) queries_kernel(const ChunkParams cp) {
+    const AttnParams &p = cp.a;
+    const int h = cp.h0 + blockIdx.y, row = threadIdx.x & (kRows - 1), g = threadIdx.x / kRows;
+    if (blockIdx.x == 0 && h == 0)
+        for (int b = threadIdx.x; b < p.c.B; b += kPlanThreads)
+            if (load_seq(p.c, p.start, p.T, b).bad) report(p.dev_status, kErrInvalid);
+    int b = 0, tile = 0;
+    const bool found = find_tile(p, blockIdx.x, b, tile);
+    Seq s{0, 0, 0, false};
+    if (found) s = load_seq(p.c, p.start, p.T, b);
+    if (cp.split == 0 && blockIdx.y == 0 && threadIdx.x == 0) {
+        const int i = static_cast<int>(blockIdx.x);
+        cp.items[i] = Item{b, tile, 0, found ? pages_of(p, s, tile) : 0, 1, i, i, 0, s};
+    }
+    if (found) {
+        uint8_t *img = cp.images + (static_cast<int64_t>(blockIdx.y) * cp.tiles + blockIdx.x) * kImage;
+        const int r = tile * kRows + row;
+        uint4 v[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = make_uint4(0, 0, 0, 0);
+        if (r < s.n * p.G) {
+            const uint4 *at = reinterpret_cast<const uint4 *>(query_row(p, s, h, r) + 32 * g);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[i] = at[i];
+        }
+        uint32_t m = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) m = max(m, amax_bf16x8(v[i]));
+        const int e = max(static_cast<int>(m >> 23) - 127 - 7, -100);      // q 2^-e in [2^7, 2^8)
+        const float down = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+        uint32_t hi[8], lo[8];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                float x[4], d[4];
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                    x[2 * q] = scaled_or_nan(__uint_as_float(w[2 * k + q] << 16), down);
+                    x[2 * q + 1] = scaled_or_nan(__uint_as_float(w[2 * k + q] & 0xffff0000u), down);
+                }
+                hi[2 * i + k] = e4m3x4(x[0], x[1], x[2], x[3]);
+                e4m3x4_decode(hi[2 * i + k], d);
+#pragma unroll
+                for (int q = 0; q < 4; ++q) x[q] = 32.0f * (x[q] - d[q]);
+                lo[2 * i + k] = e4m3x4(x[0], x[1], x[2], x[3]);
+            }
+        }
+        uint4 *to = reinterpret_cast<uint4 *>(img) + row;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            to[(2 * g + i) * kRows] = make_uint4(hi[4 * i], hi[4 * i + 1], hi[4 * i + 2], hi[4 * i + 3]);
+            to[(8 + 2 * g + i) * kRows] = make_uint4(lo[4 * i], lo[4 * i + 1], lo[4 * i + 2], lo[4 * i + 3]);
+        }
+        uint8_t *sf = img + 2 * kTile + 4 * row + g;
+        sf[0] = static_cast<uint8_t>(127 + e);          // 27 .. 247
+        sf[4 * kRows] = static_cast<uint8_t>(127 + e - 5);
+    }
+    if (cp.split && blockIdx.x == 0 && h == 0) plan_parts(cp);
 }
 
 // ---------------------------------------------------------------------------
@@ -184,57 +275,6 @@ __device__ __forceinline__ void mma_mxf8_ts(uint32_t d_tmem, uint32_t a_tmem, ui
         "tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], [%1], %2, %3, [%4], [%5], p;\n\t}\n"
         ::"r"(d_tmem), "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(sfa_tmem), "r"(sfb_tmem), "r"(accumulate)
         : "memory");
-}
-
-// One query row split as hi + lo into TMEM with its factors; returns 2^E, the
-// row's largest group factor, which the scores are multiplied by.
-__device__ __forceinline__ float store_query(uint32_t tl, int quarter, const uint16_t *row) {
-    uint32_t sfh = 0, sfl = 0;
-    int e[4], E = -100;
-    uint4 v[16];
-#pragma unroll
-    for (int i = 0; i < 16; ++i) v[i] = row ? reinterpret_cast<const uint4 *>(row)[i] : make_uint4(0, 0, 0, 0);
-#pragma unroll
-    for (int g = 0; g < 4; ++g) {
-        uint32_t m = 0;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) m = max(m, amax_bf16x8(v[4 * g + i]));
-        e[g] = max(static_cast<int>(m >> 23) - 127 - 7, -100);    // q 2^-e in [2^7, 2^8)
-        E = max(E, e[g]);
-    }
-#pragma unroll
-    for (int g = 0; g < 4; ++g) {
-        const float down = __uint_as_float(static_cast<uint32_t>(127 - e[g]) << 23);
-        uint32_t hi[8], lo[8];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const uint32_t w[4] = {v[4 * g + i].x, v[4 * g + i].y, v[4 * g + i].z, v[4 * g + i].w};
-            float x[8];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                x[2 * k] = __uint_as_float(w[k] << 16) * down;
-                x[2 * k + 1] = __uint_as_float(w[k] & 0xffff0000u) * down;
-            }
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                float d[4];
-                hi[2 * i + k] = e4m3x4(scaled_or_nan(x[4 * k], 1.0f), scaled_or_nan(x[4 * k + 1], 1.0f),
-                                       scaled_or_nan(x[4 * k + 2], 1.0f), scaled_or_nan(x[4 * k + 3], 1.0f));
-                e4m3x4_decode(hi[2 * i + k], d);
-                lo[2 * i + k] = e4m3x4(32.0f * (x[4 * k] - d[0]), 32.0f * (x[4 * k + 1] - d[1]),
-                                       32.0f * (x[4 * k + 2] - d[2]), 32.0f * (x[4 * k + 3] - d[3]));
-            }
-        }
-        VCA_TMEM_ST8(tl + kTmemQ + 8 * g, hi);
-        VCA_TMEM_ST8(tl + kTmemQ + 32 + 8 * g, lo);
-        sfh |= static_cast<uint32_t>(max(127 + e[g] - E, 6)) << (8 * g);
-        sfl |= static_cast<uint32_t>(max(127 + e[g] - E, 6) - 5) << (8 * g);
-    }
-    // row m's factor words lie in lane m, column m / 32; B's factors are 1 everywhere
-    asm volatile("tcgen05.st.sync.aligned.32x32b.x1.b32 [%0], {%1};" ::"r"(tl + kTmemSFA + quarter), "r"(sfh) : "memory");
-    asm volatile("tcgen05.st.sync.aligned.32x32b.x1.b32 [%0], {%1};" ::"r"(tl + kTmemSFA + 4 + quarter), "r"(sfl) : "memory");
-    asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1,%1,%1,%1};" ::"r"(tl + kTmemSFB), "r"(0x7f7f7f7fu) : "memory");
-    return __uint_as_float(static_cast<uint32_t>(127 + E) << 23);
 }
 
 __device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
@@ -347,21 +387,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     float4 *sSlot = reinterpret_cast<float4 *>(smem + kOffSlot);
     float *sMX = reinterpret_cast<float *>(smem + kOffMX);
     float *sL = reinterpret_cast<float *>(smem + kOffL);
-    float *sF = reinterpret_cast<float *>(smem + kOffF);
 
     const AttnParams &p = cp.a;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, h = blockIdx.y;
-    if (blockIdx.x == 0 && h == 0 && warp == 0)
-        for (int b = lane; b < p.c.B; b += 32)
-            if (load_seq(p.c, p.start, p.T, b).bad) report(p.dev_status, kErrInvalid);
-    Item it;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, h = cp.h0 + blockIdx.y;
     // the last tiles of a causal sequence see the most pages: they go first
-    const int share = share_of(cp);
-    if (!find_item(cp, share, static_cast<int>(gridDim.x - 1 - blockIdx.x), false, it)) return;
+    const Item it = cp.items[gridDim.x - 1 - blockIdx.x];
+    if (it.pages == 0) return;
     const int nb = it.pages, r0 = it.tile * kRows, R = it.s.n * p.G;
 
     if (threadIdx.x == 0) {
-        mbar_init(q_full, 4);
+        mbar_init(q_full, kConvWarps);
         for (int s = 0; s < kKStages; ++s) {
             mbar_init(k_full + s, 1);
             mbar_init(k_empty + s, 1);
@@ -520,7 +555,30 @@ __global__ void __launch_bounds__(kThreads, 1)
             drain_wait(drain + 1, 0, p.limit_ns);
         }
     } else if (warp >= kConvWarp0 && warp < kConvWarp0 + kConvWarps) {
-        // ------------------------------------------------------------ V codes -> fp16
+        // ------------------------------------------------------------ queries, V codes -> fp16
+        {
+            const int quarter = warp & 3, row = quarter * 32 + lane;
+            const uint32_t tl = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
+            const uint8_t *img = cp.images + (static_cast<int64_t>(blockIdx.y) * cp.tiles + it.image) * kImage;
+            const uint32_t *sf = reinterpret_cast<const uint32_t *>(img + 2 * kTile) + row;
+            const uint32_t sfh = sf[0], sfl = sf[kRows];
+#pragma unroll
+            for (int part = 0; part < 2; ++part) {
+                uint32_t w[32];
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    *reinterpret_cast<uint4 *>(w + 4 * i) = reinterpret_cast<const uint4 *>(img)[(8 * part + i) * kRows + row];
+                VCA_TMEM_ST32(tl + kTmemQ + 32 * part, w);
+            }
+            // row m's factor words lie in lane m, column m / 32; B's factors are 1 everywhere
+            asm volatile("tcgen05.st.sync.aligned.32x32b.x1.b32 [%0], {%1};" ::"r"(tl + kTmemSFA + quarter), "r"(sfh) : "memory");
+            asm volatile("tcgen05.st.sync.aligned.32x32b.x1.b32 [%0], {%1};" ::"r"(tl + kTmemSFA + 4 + quarter), "r"(sfl) : "memory");
+            asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1,%1,%1,%1};" ::"r"(tl + kTmemSFB), "r"(0x7f7f7f7fu) : "memory");
+            tmem_st_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(q_full);
+        }
         for (int j = 0; j < nb; ++j) {
             const int vt = j % kVStages, wt = j % kWStages;
             bool ok = mbar_wait(v_full + vt, (j / kVStages) & 1, abort_flag, p.limit_ns);
@@ -549,18 +607,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float kNegInf = __int_as_float(0xff800000);
         const int r = r0 + row;
         const bool real = r < R;
-        float f;      // raw score -> log2 units (or the cap's inner argument), but for the page's scale
-        if (half == 0) {
-            f = store_query(tl, quarter, real ? query_row(p, it.s, h, r) : nullptr);
-            tmem_st_wait();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(q_full);
-            sF[row] = f;
-        }
-        bar_sync(bar_pair, 64);
-        if (half == 1) f = sF[row];
-        f *= kCap ? p.cap_in : p.scale_log2;
+        // raw score -> log2 units (or the cap's inner argument), but for the page's scale
+        const float f = kCap ? p.cap_in : p.scale_log2;
         const int seen = (real ? min(seen_by_row(p, it.s, r), it.s.len) : it.s.len) - it.page0 * kBlk - 64 * half;
         PageScore s;
         s.t = -2.0f * p.cap_out;
@@ -713,13 +761,15 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // Joins the parts of a tile: one CTA per (tile, head, 16 rows).
-__global__ void __launch_bounds__(256) join_kernel(const ChunkParams cp, int slots) {
+__global__ void __launch_bounds__(256) join_kernel(const ChunkParams cp) {
     const AttnParams &p = cp.a;
-    Item it;
-    if (!find_item(cp, share_of(cp), blockIdx.x, true, it) || it.parts == 1) return;
+    const int first = cp.first[blockIdx.x];
+    if (first < 0) return;
+    const Item it = cp.items[first];
+    if (it.parts == 1) return;
     const int h = blockIdx.y, row = 16 * blockIdx.z + (threadIdx.x >> 4), ch = (threadIdx.x & 15) * 8, r = it.tile * kRows + row;
     if (r >= it.s.n * p.G) return;
-    const float *part = p.part + (static_cast<int64_t>(h) * slots + it.slot) * kPartFloats;
+    const float *part = p.part + (static_cast<int64_t>(h) * cp.grid + it.slot) * kPartFloats;
     float M = __int_as_float(0xff800000);
     for (int c = 0; c < it.parts; ++c) M = fmaxf(M, part[c * static_cast<int64_t>(kPartFloats) + kRows * kD + row]);
     const float Mu = M == __int_as_float(0xff800000) ? 0.0f : M;
@@ -750,45 +800,64 @@ __global__ void __launch_bounds__(256) join_kernel(const ChunkParams cp, int slo
     if (p.lse && ch == 0) p.lse[at] = Mu * 0.6931471805599453f + logf(L);
 }
 
-// Tiles of one head at most, and whether their pages are cut into parts: with
-// two tiles for every SM the last wave costs little.
+// Sizes of a call, and whether tiles are cut: where there are fewer than two for
+// every SM, whose last wave would leave most of them idle.
 struct Plan {
     int64_t tiles;
-    int split, grid;
+    int split, grid, heads;      // heads: of one launch
+    size_t off_first, off_images, off_parts, bytes;
 };
 Plan plan_of(int T, int Hq, int H, int B, int cols) {
     Plan q;
     q.tiles = static_cast<int64_t>(T) * (Hq / H) / kRows + (B < T ? B : T);
-    q.split = q.tiles * H < 2 * 152 && cols > kSmallest ? 152 : 0;
-    q.grid = static_cast<int>(q.tiles + (q.split ? q.split / H + 1 : 0));
+    q.split = q.tiles * H < kCutMost && cols > kSmallest ? 152 : 0;
+    // cut tiles number at most one CTA's parts each, or what fits the CTAs
+    q.grid = static_cast<int>(q.split && q.tiles < q.split / H ? q.split / H : q.tiles);
+    q.off_first = sizeof(Item) * q.grid;
+    q.off_images = (q.off_first + 4 * static_cast<size_t>(q.tiles) + 1023) / 1024 * 1024;
+    // images of some heads at a time: enough tiles for many waves, and a bound on the workspace
+    const int64_t fit = (64ll << 20) / (q.tiles * kImage);
+    q.heads = static_cast<int>(fit < 1 ? 1 : fit < H ? fit : H);
+    q.off_parts = q.off_images + static_cast<size_t>(q.tiles) * q.heads * kImage;
+    q.bytes = q.off_parts + (q.split ? static_cast<size_t>(q.grid) * H * kPartFloats * sizeof(float) : 0);
     return q;
 }
 
 }  // namespace
 
-size_t cache_chunk_workspace(int T, int Hq, int H, int B, int cols) {
-    const Plan q = plan_of(T, Hq, H, B, cols);
-    return q.split ? static_cast<size_t>(q.grid) * H * kPartFloats * sizeof(float) : 0;
-}
+size_t cache_chunk_workspace(int T, int Hq, int H, int B, int cols) { return plan_of(T, Hq, H, B, cols).bytes; }
 
 cudaError_t launch_cache_chunk(const CacheAttnArgs &a, cudaStream_t st) {
     CUtensorMap mk, mv;
     const uint64_t rows = static_cast<uint64_t>(a.c.pages) * a.c.H * kBlk;
     if (!make_tile_map(&mk, a.c.k8, rows) || !make_tile_map(&mv, a.c.v8, rows)) return cudaErrorInvalidValue;
     const Plan q = plan_of(a.T, a.Hq, a.c.H, a.c.B, a.c.cols);
+    uint8_t *ws = static_cast<uint8_t *>(a.ws);
     ChunkParams cp;
     cp.a = attn_params(a.c, a.q, a.start, a.T, a.Hq, a.causal, a.scale, a.softcap, a.dev_status, a.wait_limit_ns);
     cp.a.O = a.O;
     cp.a.lse = a.lse;
-    cp.a.part = static_cast<float *>(a.ws);
+    cp.a.part = reinterpret_cast<float *>(ws + q.off_parts);
+    cp.items = reinterpret_cast<Item *>(ws);
+    cp.first = reinterpret_cast<int *>(ws + q.off_first);
+    cp.images = ws + q.off_images;
+    cp.tiles = static_cast<int>(q.tiles);
+    cp.grid = q.grid;
     cp.split = q.split;
     const auto kernel = a.softcap > 0.0f ? chunk_kernel<true> : chunk_kernel<false>;
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
     if (e != cudaSuccess) return e;
-    kernel<<<dim3(q.grid, a.c.H), kThreads, kSmem, st>>>(mk, mv, cp);
-    e = cudaGetLastError();
-    if (e != cudaSuccess || !q.split) return e;
-    join_kernel<<<dim3(static_cast<unsigned>(q.tiles), a.c.H, kRows / 16), 256, 0, st>>>(cp, q.grid);
+    for (cp.h0 = 0; cp.h0 < a.c.H; cp.h0 += q.heads) {
+        const int heads = a.c.H - cp.h0 < q.heads ? a.c.H - cp.h0 : q.heads;
+        queries_kernel<<<dim3(cp.tiles, heads), kPlanThreads, 0, st>>>(cp);
+        e = cudaGetLastError();
+        if (e != cudaSuccess) return e;
+        kernel<<<dim3(q.grid, heads), kThreads, kSmem, st>>>(mk, mv, cp);
+        e = cudaGetLastError();
+        if (e != cudaSuccess) return e;
+    }
+    if (!q.split) return cudaSuccess;      // cut tiles are few: one launch had all heads
+    join_kernel<<<dim3(cp.tiles, a.c.H, kRows / 16), 256, 0, st>>>(cp);
     return cudaGetLastError();
 }
 
