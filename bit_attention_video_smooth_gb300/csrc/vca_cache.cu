@@ -157,27 +157,59 @@ __device__ __forceinline__ uint32_t weight_key(float w) {
     return (u >> 31) ? ~u : (u | 0x80000000u);
 }
 
-constexpr int kSelThreads = 1024;
+constexpr int kSelThreads = 512;
+constexpr int kSelKeys = 40960;         // keys that a CTA can keep in shared memory
+constexpr int kClusterTokens = 4096;    // longer sequences take a cluster for each head
 
-// One CTA per (sequence, head): the key of the last weight that stays, by a
-// radix select over four bytes, then the slots that stay, in order.
-__global__ void __launch_bounds__(kSelThreads) select_kernel(const EvictParams p) {
-    __shared__ int hist[256];
-    __shared__ int s_bin, s_left;
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
+}
+// A word of another CTA's shared memory.
+__device__ __forceinline__ int cluster_read(const int *p, uint32_t rank) {
+    uint32_t at;
+    int v;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_u32(p)), "r"(rank));
+    asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(at) : "memory");
+    return v;
+}
+
+// A cluster of kCluster CTAs per (sequence, head), each over an equal run of the
+// older slots: the key of the last weight that stays by a radix select over four
+// bytes (the CTAs' histograms are added through distributed shared memory), then
+// the slots that stay, in order.  Each weight is read once, unless a CTA's run
+// does not fit its shared memory.
+template <int kCluster>
+__global__ void __launch_bounds__(kSelThreads) select_kernel(const EvictParams p, int keep) {
+    extern __shared__ uint32_t sKeys[];
+    __shared__ int hist[2][256], s_bin, s_left, counts[2];
     __shared__ int wsum[2][kSelThreads / 32];
-    const int h = blockIdx.x, b = blockIdx.y, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int rank = kCluster > 1 ? static_cast<int>(cluster_rank()) : 0;
+    const int h = blockIdx.x / kCluster, b = blockIdx.y, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    let_next_start();
     int len = p.c.len[b];
     if (len < 0 || len > static_cast<int64_t>(p.c.cols) * kBlk) {
         if (tid == 0) report(p.dev_status, kErrInvalid);
         len = 0;
     }
     const int stay = min(len, p.budget), recent = min(min(len, p.recent), stay);
-    if (h == 0 && tid == 0) p.new_len[b] = stay;
+    if (h == 0 && tid == 0 && rank == 0) p.new_len[b] = stay;
     const int older = len - recent, want = stay - recent;
     int32_t *kept = p.kept + (static_cast<int64_t>(b) * p.c.H + h) * p.budget;
-    for (int j = tid; j < recent; j += kSelThreads) kept[want + j] = older + j;
+    for (int j = rank * kSelThreads + tid; j < recent; j += kCluster * kSelThreads) kept[want + j] = older + j;
+    if (want == older) {
+        // all of them stay
+        for (int j = rank * kSelThreads + tid; j < want; j += kCluster * kSelThreads) kept[j] = j;
+        return;
+    }
     if (want == 0) return;
-    auto key_of = [&](int t) -> uint32_t {
+    const int run = (older + kCluster * 32 - 1) / (kCluster * 32) * 32;      // a multiple of a warp's
+    const int t0 = min(older, rank * run), n = min(older, t0 + run) - t0;
+    auto load_key = [&](int t) -> uint32_t {
         const int page = p.c.table[static_cast<int64_t>(b) * p.c.cols + t / kBlk];
         if (page < 0 || page >= p.c.pages) {
             report(p.dev_status, kErrInvalid);
@@ -185,21 +217,35 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const EvictParams p
         }
         return weight_key(p.weight[(static_cast<int64_t>(page) * p.c.H + h) * kBlk + t % kBlk]);
     };
+    const bool kept_keys = n <= keep;
+    auto key_of = [&](int i) -> uint32_t { return kept_keys ? sKeys[i] : load_key(t0 + i); };
+    if (kept_keys) {
+#pragma unroll 4
+        for (int i = tid; i < n; i += kSelThreads) sKeys[i] = load_key(t0 + i);
+    }
+    if (tid < 256) hist[0][tid] = 0;
+    __syncthreads();
     uint32_t prefix = 0, mask = 0;
     int left = want;               // how many of those whose key starts with `prefix` stay
-    for (int shift = 24; shift >= 0; shift -= 8) {
-        if (tid < 256) hist[tid] = 0;
-        __syncthreads();
-        for (int t = tid; t < older; t += kSelThreads) {
-            const uint32_t k = key_of(t);
-            if ((k & mask) == prefix) atomicAdd(&hist[(k >> shift) & 255], 1);
+    for (int pass = 0; pass < 4; ++pass) {
+        const int shift = 24 - 8 * pass;
+        int *mine = hist[pass & 1];
+        for (int i = tid; i < n; i += kSelThreads) {
+            const uint32_t k = key_of(i);
+            if ((k & mask) == prefix) atomicAdd(&mine[(k >> shift) & 255], 1);
         }
         __syncthreads();
+        if constexpr (kCluster > 1) cluster_sync();
         if (warp == 0) {
             // bins from the top: lane i holds bins 255 - 8 i .. 248 - 8 i
-            int c[8], s = 0;
+            int c[8] = {}, s = 0;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) s += c[e] = hist[255 - 8 * lane - e];
+            for (int r = 0; r < kCluster; ++r)
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    c[e] += kCluster > 1 ? cluster_read(&mine[255 - 8 * lane - e], r) : mine[255 - 8 * lane - e];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) s += c[e];
             int incl = s;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
@@ -218,91 +264,111 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const EvictParams p
                 }
             }
         }
+        // the other histogram, which every CTA of the cluster has read by now
+        if (tid < 256) hist[(pass & 1) ^ 1][tid] = 0;
         __syncthreads();
         prefix |= static_cast<uint32_t>(s_bin) << shift;
         mask |= 255u << shift;
         left = s_left;
-        __syncthreads();
     }
-    // keys above `prefix` stay, and the first `left` of those equal to it
-    int done = 0, ties = 0;
-    for (int t0 = 0; t0 < older; t0 += kSelThreads) {
-        const int t = t0 + tid;
-        const uint32_t k = t < older ? key_of(t) : 0u;
-        const bool gt = t < older && k > prefix, eq = t < older && k == prefix;
-        const uint32_t bg = __ballot_sync(0xffffffffu, gt), be = __ballot_sync(0xffffffffu, eq);
-        if (lane == 0) {
-            wsum[0][warp] = __popc(bg);
-            wsum[1][warp] = __popc(be);
+    // keys above `prefix` stay, and the first `left` of those equal to it.  A warp
+    // takes a run of its own: counts first, then places
+    const int per = (n + kSelThreads - 1) / kSelThreads * 32;       // slots of a warp
+    const int w0 = min(n, warp * per), w1 = min(n, w0 + per);
+    int gt = 0, eq = 0;
+    for (int i = w0 + lane; i < w1; i += 32) {
+        const uint32_t k = key_of(i);
+        gt += k > prefix;
+        eq += k == prefix;
+    }
+    gt = __reduce_add_sync(0xffffffffu, gt);
+    eq = __reduce_add_sync(0xffffffffu, eq);
+    if (lane == 0) {
+        wsum[0][warp] = gt;
+        wsum[1][warp] = eq;
+    }
+    __syncthreads();
+    int g0 = 0, e0 = 0, g_all = 0, e_all = 0;      // before this warp, and of the CTA
+    for (int i = 0; i < kSelThreads / 32; ++i) {
+        const int x = wsum[0][i], y = wsum[1][i];
+        if (i < warp) {
+            g0 += x;
+            e0 += y;
+        }
+        g_all += x;
+        e_all += y;
+    }
+    if constexpr (kCluster > 1) {
+        if (tid == 0) {
+            counts[0] = g_all;
+            counts[1] = e_all;
         }
         __syncthreads();
-        int g0 = 0, e0 = 0, gt_all = 0, eq_all = 0;
-        for (int i = 0; i < kSelThreads / 32; ++i) {
-            const int a = wsum[0][i], c = wsum[1][i];
-            if (i < warp) {
-                g0 += a;
-                e0 += c;
-            }
-            gt_all += a;
-            eq_all += c;
+        cluster_sync();
+        for (int r = 0; r < rank; ++r) {
+            g0 += cluster_read(&counts[0], r);
+            e0 += cluster_read(&counts[1], r);
         }
-        const uint32_t below = (1u << lane) - 1u;
-        g0 += __popc(bg & below);
-        e0 += __popc(be & below);
-        // kept so far: everything above, plus the ties among the first `left`
-        const int tie = ties + e0;
-        if (gt || (eq && tie < left)) kept[done + g0 + min(tie, left) - min(ties, left)] = t;
-        done += gt_all + min(ties + eq_all, left) - min(ties, left);
-        ties += eq_all;
-        __syncthreads();
+        cluster_sync();      // no CTA leaves while another reads its counts
+    }
+    const uint32_t below = (1u << lane) - 1u;
+    for (int i = w0; i < w1; i += 32) {
+        const bool there = i + lane < w1;
+        const uint32_t k = there ? key_of(i + lane) : 0u;
+        const uint32_t bg = __ballot_sync(0xffffffffu, there && k > prefix), be = __ballot_sync(0xffffffffu, there && k == prefix);
+        const int tie = e0 + __popc(be & below);      // ties before this slot
+        if (there && (k > prefix || (k == prefix && tie < left))) kept[g0 + __popc(bg & below) + min(tie, left)] = t0 + i + lane;
+        g0 += __popc(bg);
+        e0 += __popc(be);
     }
 }
 
-// One CTA per (page that is written, head, K or V) of a sequence.
-__global__ void __launch_bounds__(kThreads) move_kernel(const EvictParams p) {
-    __shared__ uint32_t red[kThreads / 32];
-    __shared__ int s_page[kBlk], s_slot[kBlk];
-    const int col = blockIdx.x, b = blockIdx.y / p.c.H, h = blockIdx.y % p.c.H;
-    const bool is_v = blockIdx.z != 0;
-    const int stay = p.new_len[b];
-    const int rows = min(stay - col * kBlk, kBlk);
-    if (rows <= 0) return;
+// One CTA per (page that is written, head): K by the first 256 threads, V by the others.
+__global__ void __launch_bounds__(2 * kThreads) move_kernel(const EvictParams p) {
+    __shared__ uint32_t red[2][kThreads / 32];
+    __shared__ int s_row[kBlk];         // place of the token's row of codes in the pool, in tiles of 128; -1: none
+    __shared__ int s_slot[kBlk];
+    const int col = blockIdx.x, h = blockIdx.y, b = blockIdx.z, tid = threadIdx.x;
+    const bool is_v = tid >= kThreads;
+    const int32_t *kept = p.kept + (static_cast<int64_t>(b) * p.c.H + h) * p.budget + col * kBlk;
     const int page = p.dst[static_cast<int64_t>(b) * p.dst_cols + col];
+    wait_for_results();
+    const int rows = min(p.new_len[b] - col * kBlk, kBlk);
+    if (rows <= 0) return;
     if (page < 0 || page >= p.c.pages) {
-        report(p.dev_status, kErrInvalid);
+        if (tid == 0) report(p.dev_status, kErrInvalid);
         return;
     }
-    const int32_t *kept = p.kept + (static_cast<int64_t>(b) * p.c.H + h) * p.budget + col * kBlk;
-    if (threadIdx.x < kBlk) {
+    const int to = page * p.c.H + h;
+    if (tid < kBlk) {
         int from = -1, t = 0;
-        if (threadIdx.x < rows) {
-            t = kept[threadIdx.x];
+        if (tid < rows) {
+            t = kept[tid];
             from = load_page(p.c, b, t / kBlk, p.dev_status);
+            if (from >= 0) from = from * p.c.H + h;
         }
-        s_page[threadIdx.x] = from;
-        s_slot[threadIdx.x] = t % kBlk;
-        if (!is_v && from >= 0)
-            p.weight[(static_cast<int64_t>(page) * p.c.H + h) * kBlk + threadIdx.x] =
-                p.weight[(static_cast<int64_t>(from) * p.c.H + h) * kBlk + t % kBlk];
+        s_row[tid] = from;
+        s_slot[tid] = t % kBlk;
     }
     __syncthreads();
-    uint8_t *codes = is_v ? p.c.v8 : p.c.k8;
-    float *scale = is_v ? p.c.sv : p.c.sk;
-    const int r = threadIdx.x >> 4, ch = (threadIdx.x & 15) * 8;
+    const uint8_t *codes = is_v ? p.c.v8 : p.c.k8;
+    const float *scale = is_v ? p.c.sv : p.c.sk;
+    const int r = (tid >> 4) & 15, ch = (tid & 15) * 8;
     uint2 v[kPasses];
     float s[kPasses];
     uint32_t m = 0;
 #pragma unroll
     for (int i = 0; i < kPasses; ++i) {
-        const int j = r + i * kRowsPerPass, from = s_page[j];
+        const int j = r + i * kRowsPerPass, from = s_row[j];
         v[i] = make_uint2(0, 0);
         s[i] = 0.0f;
         if (from >= 0) {
-            const int64_t tile = static_cast<int64_t>(from) * p.c.H + h;
-            v[i] = *reinterpret_cast<const uint2 *>(codes + (tile * kBlk + s_slot[j]) * kD + ch);
-            s[i] = scale[tile];
+            v[i] = *reinterpret_cast<const uint2 *>(codes + (static_cast<int64_t>(from) * kBlk + s_slot[j]) * kD + ch);
+            s[i] = scale[from];
         }
     }
+    if (tid < kBlk && s_row[tid] >= 0)
+        p.weight[static_cast<int64_t>(to) * kBlk + tid] = p.weight[static_cast<int64_t>(s_row[tid]) * kBlk + s_slot[tid]];
 #pragma unroll
     for (int i = 0; i < kPasses; ++i) {
         float f[8];
@@ -313,17 +379,23 @@ __global__ void __launch_bounds__(kThreads) move_kernel(const EvictParams p) {
             if (u < 0x7f800000u) m = max(m, u);
         }
     }
-    const uint32_t sb = scale_bits(block_max<kThreads>(m, red));
+    m = __reduce_max_sync(0xffffffffu, m);
+    if ((tid & 31) == 0) red[is_v][(tid >> 5) & 7] = m;
+    __syncthreads();
+    m = 0;
+#pragma unroll
+    for (int i = 0; i < kThreads / 32; ++i) m = max(m, red[is_v][i]);
+    const uint32_t sb = scale_bits(m);
     const float inv = pow2_inverse(sb);
-    const int64_t to = static_cast<int64_t>(page) * p.c.H + h;
-    if (threadIdx.x == 0) scale[to] = __uint_as_float(sb);
+    if ((tid & (kThreads - 1)) == 0) (is_v ? p.c.sv : p.c.sk)[to] = __uint_as_float(sb);
+    uint8_t *out = (is_v ? p.c.v8 : p.c.k8) + static_cast<int64_t>(to) * kBlk * kD;
 #pragma unroll
     for (int i = 0; i < kPasses; ++i) {
         const int j = r + i * kRowsPerPass;
-        if (s_page[j] < 0) continue;
+        if (s_row[j] < 0) continue;
         float f[8];
         decode8(v[i], s[i], f);
-        *reinterpret_cast<uint2 *>(codes + (to * kBlk + j) * kD + ch) = encode8(f, inv);
+        *reinterpret_cast<uint2 *>(out + j * kD + ch) = encode8(f, inv);
     }
 }
 
@@ -341,11 +413,27 @@ cudaError_t launch_cache_append(const CacheView &c, const CacheRows &k, const Ca
 cudaError_t launch_cache_evict(const CacheView &c, float *weight, const int32_t *dst_table, int dst_cols, int budget,
                                int recent, int32_t *new_len, int32_t *kept, int32_t *dev_status, cudaStream_t st) {
     const EvictParams p{c, weight, dst_table, dst_cols, budget, recent, new_len, kept, dev_status};
-    select_kernel<<<dim3(c.H, c.B), kSelThreads, 0, st>>>(p);
-    cudaError_t e = cudaGetLastError();
+    const int64_t tokens = static_cast<int64_t>(c.cols) * kBlk;      // of a sequence, at most
+    const int parts = tokens > kClusterTokens ? 8 : 1;
+    const int64_t run = (tokens + parts - 1) / parts + 32;
+    const int keep = static_cast<int>(run < kSelKeys ? run : kSelKeys);
+    const auto kernel = parts == 8 ? select_kernel<8> : select_kernel<1>;
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSelKeys * 4);
     if (e != cudaSuccess) return e;
-    move_kernel<<<dim3((budget + kBlk - 1) / kBlk, c.B * c.H, 2), kThreads, 0, st>>>(p);
-    return cudaGetLastError();
+    cudaLaunchAttribute at;
+    at.id = cudaLaunchAttributeClusterDimension;
+    at.val.clusterDim.x = parts;
+    at.val.clusterDim.y = at.val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(c.H * parts, c.B);
+    cfg.blockDim = dim3(kSelThreads);
+    cfg.dynamicSmemBytes = static_cast<size_t>(keep) * 4;
+    cfg.stream = st;
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, kernel, p, keep);
+    if (e != cudaSuccess) return e;
+    return launch_after(move_kernel, dim3((budget + kBlk - 1) / kBlk, c.H, c.B), 2 * kThreads, 0, st, p);
 }
 
 }  // namespace vca

@@ -121,6 +121,7 @@ struct AttnParams {
     uint16_t *O;
     float *lse;
     float *part;
+    int whole;             // decode kernel: every CTA takes one whole tile
     int32_t *dev_status;
     uint64_t limit_ns;
 };
@@ -157,6 +158,25 @@ __device__ __forceinline__ int64_t out_row(const AttnParams &p, const Seq &s, in
     return static_cast<int64_t>(s.row0 + r / p.G) * p.Hq + h * p.G + r % p.G;
 }
 
+// A kernel that follows another of the same call may start while that one runs
+// (launch_after) and waits here for its results; the first lets it start.
+__device__ __forceinline__ void wait_for_results() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+template <typename... Params, typename... Args>
+cudaError_t launch_after(void (*kernel)(Params...), dim3 grid, int threads, size_t smem, cudaStream_t st, Args... args) {
+    cudaLaunchAttribute at;
+    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t c{};
+    c.gridDim = grid;
+    c.blockDim = dim3(threads);
+    c.dynamicSmemBytes = smem;
+    c.stream = st;
+    c.attrs = &at;
+    c.numAttrs = 1;
+    return cudaLaunchKernelEx(&c, kernel, Params(args)...);
+}
+
 // The capped score cap tanh(y) in log2 units, y = u ln 2 / 2: tanh(y) =
 // 1 - 2 / (1 + 2^u), which cancels where u is small; below |u| = 1.6 an odd
 // polynomial in u instead, fitted to 3.5e-8 relative (2^-22 with its roundings).
@@ -166,6 +186,13 @@ __device__ __forceinline__ float capped(float u, float cap_out) {
                          3.4657359e-01f);
     const float far = 1.0f - __fdividef(2.0f, 1.0f + ex2_approx(u));
     return cap_out * (fabsf(u) <= 1.6f ? u * q : far);
+}
+
+// The same where |u| <= 1.6 is known.
+__device__ __forceinline__ float capped_near(float u, float cap_out) {
+    const float w = u * u;
+    return cap_out * u *
+           fmaf(fmaf(fmaf(fmaf(1.1715225e-06f, w, -3.1559721e-05f), w, 6.6592207e-04f), w, -1.3875789e-02f), w, 3.4657359e-01f);
 }
 
 // Score in log2 units from the raw product: x = S * f with f = c (no cap) or

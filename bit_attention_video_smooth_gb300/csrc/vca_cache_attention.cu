@@ -7,19 +7,21 @@
 //   lse = ln 2 (m + log2 l), m the running maximum.
 //
 // The query rows of one (sequence, KV head) -- its new tokens times the G query
-// heads that share the KV head -- are cut into tiles of 8 or 16.  The work is the
+// heads that share the KV head -- are cut into tiles of 8 or 32.  The work is the
 // list of all (sequence, KV head, tile, page) units in that order; each CTA
 // takes an equal share of consecutive units, whatever the sequences' lengths,
 // and writes an (O, m, l) partial where a tile's pages are shared between CTAs;
 // a second kernel joins those.  The order of the sums is fixed, so equal calls
-// give equal bits.
+// give equal bits.  Short caches of few tiles are not cut: a CTA for each tile
+// is done before a second kernel would be.
 //
 // One producer warp keeps a ring of pages (K and V tile, 16 KB each, one TMA
 // load per tile) full across tile borders; their table entries and scales are
 // loaded two batches ahead, since a load under full traffic takes longer than a
-// page.  Eight consumer warps take 16 keys of every page each, with a running
-// maximum, sum and O of their own, which they merge at a tile's end: no barrier
-// but the ring's in between.
+// page.  Eight consumer warps take 16 keys of every page each (32 keys and half of
+// the rows where a tile has more than 16), with a running maximum, sum and O of
+// their own, which they merge at a tile's end: no barrier but the ring's in
+// between.
 //
 // Both products are m16n8k16 MMAs on fp16 with the long side as rows, so that
 // eight query rows fill a tile: S^T = K Q^T (16 keys x 8 rows), then O^T = V^T P^T
@@ -39,21 +41,22 @@ using namespace cache;
 
 constexpr int kWarps = 8;                       // consumer warps
 constexpr int kThreads = 32 * (kWarps + 1);
-constexpr int kKeys = kBlk / kWarps;            // keys of a page per warp
 constexpr uint32_t kTile = kBlk * kD;           // bytes of one K or V tile
 constexpr int kSmallest = 2;                    // units a CTA takes at least
 
 // One partial of a tile of `rows` rows: O [rows][128], m [rows], l [rows].
 __host__ __device__ constexpr int part_floats(int rows) { return rows * kD + 2 * rows; }
 
-// Shared memory: the ring, the warps' O, m and l of a tile of kRows rows, the
-// pages' scales, barriers.  Eight rows leave room for a longer ring.
+// Shared memory: the ring, the warps' O, m and l (of 16 rows at most), the pages'
+// scales, barriers.  Eight rows leave room for a longer ring.
 template <int kRows>
 struct Smem {
+    static constexpr int rows = kRows == 8 ? 8 : 16;                    // of a warp
     static constexpr int stages = kRows == 8 ? 5 : 4;
     static constexpr uint32_t merge = stages * 2 * kTile;               // fp32 [8][rows][128]
-    static constexpr uint32_t ml = merge + kWarps * kRows * kD * 4;     // fp32 [8][rows] m, [8][rows] l
-    static constexpr uint32_t scale = ml + 2 * kWarps * kRows * 4;      // fp32 [stages][2]
+    static constexpr uint32_t ml = merge + kWarps * rows * kD * 4;      // fp32 [8][rows] m, [8][rows] l
+    static constexpr uint32_t query = ml + 2 * kWarps * rows * 4;       // the warps' Q fragments of 16 rows: uint2 [8][2][8][32]
+    static constexpr uint32_t scale = query + (rows == 16 ? kWarps * 4096 : 0);      // fp32 [stages][2]
     static constexpr uint32_t bar = scale + stages * 8;
     static constexpr uint32_t bytes = bar + 2 * stages * 8 + 16 + 1024;
     static_assert(bytes <= 232448, "shared memory budget");
@@ -77,7 +80,7 @@ __device__ __forceinline__ Shape shape_of(const AttnParams &p, int b) {
     return x;
 }
 __device__ __forceinline__ int64_t units_of(const AttnParams &p, const Shape &x) {
-    return static_cast<int64_t>(x.tiles) * x.pages * p.c.H;
+    return static_cast<int64_t>(x.tiles) * (p.whole ? min(x.pages, 1) : x.pages) * p.c.H;
 }
 
 __device__ __forceinline__ int64_t warp_incl_scan(int64_t v) {
@@ -103,9 +106,9 @@ __device__ int64_t count_units(const AttnParams &p) {
 }
 
 // The share of every CTA.
-__device__ __forceinline__ int64_t share_of(int64_t all, int ctas) {
+__device__ __forceinline__ int64_t share_of(const AttnParams &p, int64_t all, int ctas) {
     const int64_t s = (all + ctas - 1) / ctas;
-    return s < kSmallest ? kSmallest : s;
+    return p.whole ? 1 : s < kSmallest ? kSmallest : s;
 }
 
 // Where unit u lies: sequence, and the unit's place among the sequence's.
@@ -141,6 +144,13 @@ struct Walk {
         left = units;
         if (b < p.c.B) {
             x = shape_of<kRows>(p, b);
+            if (p.whole) {
+                h = static_cast<int>(local / x.tiles);
+                tile = static_cast<int>(local - static_cast<int64_t>(h) * x.tiles);
+                page = 0;
+                left = x.pages;
+                return;
+            }
             h = static_cast<int>(local / (static_cast<int64_t>(x.tiles) * x.pages));
             const int64_t r = local - static_cast<int64_t>(h) * x.tiles * x.pages;
             tile = static_cast<int>(r / x.pages);
@@ -286,14 +296,16 @@ struct Feed {
 template <int kRows>
 __global__ void __launch_bounds__(kThreads, 1)
     decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, const AttnParams p) {
-    constexpr int NT = kRows / 8;               // groups of eight query rows
-    constexpr int kStages = Smem<kRows>::stages;
+    using L = Smem<kRows>;
+    constexpr int NT = L::rows / 8;             // groups of eight query rows of a warp
+    constexpr int KS = kRows == 8 ? 1 : 2;      // groups of 16 keys of a page, at most
+    constexpr int kStages = L::stages;
     extern __shared__ unsigned char smem_raw[];
     unsigned char *smem =
         reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    uint64_t *full = reinterpret_cast<uint64_t *>(smem + Smem<kRows>::bar), *empty = full + kStages;
+    uint64_t *full = reinterpret_cast<uint64_t *>(smem + L::bar), *empty = full + kStages;
     int *abort_flag = reinterpret_cast<int *>(empty + kStages);
-    float *sScale = reinterpret_cast<float *>(smem + Smem<kRows>::scale);
+    float *sScale = reinterpret_cast<float *>(smem + L::scale);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
     if (threadIdx.x == 0) {
@@ -305,7 +317,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_fence_init();
     }
     __syncthreads();
-    const int64_t all = count_units<kRows>(p), share = share_of(all, gridDim.x);
+    let_next_start();
+    const int64_t all = count_units<kRows>(p), share = share_of(p, all, gridDim.x);
     const int64_t u0 = share * blockIdx.x, u1 = min(all, u0 + share);
     if (blockIdx.x == 0 && warp == 0)
         for (int b = lane; b < p.c.B; b += 32)
@@ -320,12 +333,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == kWarps) {
         // ------------------------------------------------------------ producer
         int stage = 0, round = 0;
-        const int units = static_cast<int>(u1 - u0);
+        const int64_t units = w.left;
         int armed = 0;
         bool ok = true;
         Feed<kRows> feed;
         feed.begin(p, w);
-        for (int i = 0; i < units; ++i) {
+        for (int64_t i = 0; i < units; ++i) {
             int y;
             float ks, vs;
             feed.take(p, y, ks, vs);
@@ -343,7 +356,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     mbar_arrive(full + stage);
                 }
             }
-            armed = i + 1;
+            ++armed;
             if (++stage == kStages) {
                 stage = 0;
                 ++round;
@@ -357,8 +370,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         // ------------------------------------------------------------ consumers
         // fragments: g and t are the row (key, channel or query row) and the pair of a quad
         const int g = lane >> 2, t = lane & 3;
-        float *sMerge = reinterpret_cast<float *>(smem + Smem<kRows>::merge);
-        float *sM = reinterpret_cast<float *>(smem + Smem<kRows>::ml), *sL = sM + kWarps * kRows;
+        float *sMerge = reinterpret_cast<float *>(smem + L::merge);
+        float *sM = reinterpret_cast<float *>(smem + L::ml), *sL = sM + kWarps * L::rows;
+        const int64_t u_left = w.left;
         int stage = 0, round = 0;
         bool ok = true;
         const float kNegInf = __int_as_float(0xff800000);
@@ -366,24 +380,39 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int run = w.run();
             const Seq s = w.x.s;
             const int R = s.n * p.G, r0 = w.tile * kRows;
+            // the tile's rows in one or two groups of 16; the warp's begin at rw
+            const int groups = KS == 2 && R - r0 > 16 ? 2 : 1, rw = r0 + (groups == 2 ? (warp & 1) * 16 : 0);
+            const int kKeys = 16 * groups, key_base = groups == 2 ? (warp >> 1) * 32 : warp * 16;
             // Q: the B operand, row 8 n + g; this thread's scores are of the rows 8 n + 2 t and + 1
-            uint32_t q[NT][16];
+            // (in registers for eight rows; 16 leave no room, so each warp keeps a copy in shared memory)
+            uint32_t q[NT == 1 ? 16 : 1];
+            uint2 *sQ = reinterpret_cast<uint2 *>(smem + L::query) + warp * 512 + lane;
             float f[NT][2], m[NT][2], l[NT][2];
             int seen[NT][2];
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
-                const float down = load_q(p, s, w.h, r0 + 8 * n + g, t, q[n]);
+                uint32_t row[16];
+                const float down = load_q(p, s, w.h, rw + 8 * n + g, t, row);
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    if constexpr (NT == 1) {
+                        q[2 * k] = row[2 * k];
+                        q[2 * k + 1] = row[2 * k + 1];
+                    } else {
+                        sQ[(n * 8 + k) * 32] = make_uint2(row[2 * k], row[2 * k + 1]);      // read by this thread alone
+                    }
+                }
                 const float fg = __fmul_rn(p.cap_out != 0.0f ? p.cap_in : p.scale_log2, down);
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    const int r = r0 + 8 * n + 2 * t + e;
+                    const int r = rw + 8 * n + 2 * t + e;
                     f[n][e] = __shfl_sync(0xffffffffu, fg, (2 * t + e) * 4);
                     seen[n][e] = r < R ? seen_by_row(p, s, r) : 0;
                     m[n][e] = kNegInf;
                     l[n][e] = 0.0f;
                 }
             }
-            const int all_see = seen_by_row(p, s, r0);      // keys below this are seen by every row of the tile
+            const int all_see = seen_by_row(p, s, rw);      // keys below this are seen by every row of the warp
             // O^T: channel 16 g + 2 j (elements 0, 1) and 16 g + 2 j + 1 (2, 3) of the rows 2 t, 2 t + 1
             float o[NT][8][4];
 #pragma unroll
@@ -398,89 +427,160 @@ __global__ void __launch_bounds__(kThreads, 1)
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
                 const float sk = sScale[2 * stage], sv = sScale[2 * stage + 1];
-                const int key0 = (w.page + i) * kBlk + kKeys * warp;
+                const int key0 = (w.page + i) * kBlk + key_base;
                 if (sk >= 0.0f && key0 < s.len) {
                     const unsigned char *sK = smem + stage * 2 * kTile, *sV = sK + kTile;
-                    float S[NT][4];
+                    float S[KS][NT][4];
 #pragma unroll
-                    for (int n = 0; n < NT; ++n)
+                    for (int c = 0; c < KS; ++c) {
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) S[n][e] = 0.0f;
-                    // K: keys g and g + 8; the four codes of a word are channels 32 t + 4 k .. + 3
+                        for (int n = 0; n < NT; ++n)
 #pragma unroll
-                    for (int half = 0; half < 2; ++half) {
-                        uint32_t ka[4], kb[4];
-                        *reinterpret_cast<uint4 *>(ka) = lds128(sK + sw128_offset(kKeys * warp + g, 2 * t + half));
-                        *reinterpret_cast<uint4 *>(kb) = lds128(sK + sw128_offset(kKeys * warp + 8 + g, 2 * t + half));
+                            for (int e = 0; e < 4; ++e) S[c][n][e] = c < groups ? 0.0f : kNegInf;
+                        if (c >= groups) continue;
+                        // K: keys g and g + 8; the four codes of a word are channels 32 t + 4 k .. + 3
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            uint32_t a[4];
-                            codes_to_half(ka[k], a[0], a[2]);
-                            codes_to_half(kb[k], a[1], a[3]);
+                        for (int half = 0; half < 2; ++half) {
+                            uint32_t ka[4], kb[4];
+                            const int k0 = key_base + 16 * c + g;
+                            *reinterpret_cast<uint4 *>(ka) = lds128(sK + sw128_offset(k0, 2 * t + half));
+                            *reinterpret_cast<uint4 *>(kb) = lds128(sK + sw128_offset(k0 + 8, 2 * t + half));
 #pragma unroll
-                            for (int n = 0; n < NT; ++n) mma16816(S[n], a, q[n][8 * half + 2 * k], q[n][8 * half + 2 * k + 1]);
+                            for (int k = 0; k < 4; ++k) {
+                                uint32_t a[4];
+                                codes_to_half(ka[k], a[0], a[2]);
+                                codes_to_half(kb[k], a[1], a[3]);
+#pragma unroll
+                                for (int n = 0; n < NT; ++n) {
+                                    if constexpr (NT == 1) {
+                                        mma16816(S[c][n], a, q[8 * half + 2 * k], q[8 * half + 2 * k + 1]);
+                                    } else {
+                                        const uint2 x = sQ[(n * 8 + 4 * half + k) * 32];
+                                        mma16816(S[c][n], a, x.x, x.y);
+                                    }
+                                }
+                            }
                         }
                     }
-                    uint32_t vw[4][4];
+                    // scores in log2 units; element e: key 16 c + g + 8 (e >> 1), row 2 t + (e & 1)
+                    if (p.cap_out == 0.0f) {
 #pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        *reinterpret_cast<uint4 *>(vw[k]) =
-                            lds128(sV + sw128_offset(kKeys * warp + 2 * t + (k & 1) + 8 * (k >> 1), g));
-                    // the last page's slots behind the last token may hold anything
-                    if (key0 + kKeys > s.len) {
+                        for (int n = 0; n < NT; ++n) {
+                            const float f0 = f[n][0] * sk, f1 = f[n][1] * sk;
 #pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            if (key0 + 2 * t + (k & 1) + 8 * (k >> 1) >= s.len)
-                                vw[k][0] = vw[k][1] = vw[k][2] = vw[k][3] = 0u;
+                            for (int c = 0; c < KS; ++c)
+                                if (c < groups)
+#pragma unroll
+                                    for (int e = 0; e < 4; ++e) S[c][n][e] *= (e & 1) ? f1 : f0;
+                        }
+                    } else {
+                        float far = 0.0f;
+#pragma unroll
+                        for (int n = 0; n < NT; ++n) {
+                            const float f0 = f[n][0] * sk, f1 = f[n][1] * sk;
+#pragma unroll
+                            for (int c = 0; c < KS; ++c)
+                                if (c < groups)
+#pragma unroll
+                                    for (int e = 0; e < 4; ++e) {
+                                        S[c][n][e] *= (e & 1) ? f1 : f0;
+                                        far = fmaxf(far, fabsf(S[c][n][e]));
+                                    }
+                        }
+                        if (__all_sync(0xffffffffu, far <= 1.6f)) {
+#pragma unroll
+                            for (int c = 0; c < KS; ++c)
+                                if (c < groups)
+#pragma unroll
+                                    for (int n = 0; n < NT; ++n)
+#pragma unroll
+                                        for (int e = 0; e < 4; ++e) S[c][n][e] = capped_near(S[c][n][e], p.cap_out);
+                        } else {
+#pragma unroll
+                            for (int c = 0; c < KS; ++c)
+                                if (c < groups)
+#pragma unroll
+                                    for (int n = 0; n < NT; ++n)
+#pragma unroll
+                                        for (int e = 0; e < 4; ++e) S[c][n][e] = capped(S[c][n][e], p.cap_out);
+                        }
                     }
-                    // scores in log2 units, the running maximum, P; element e: key g + 8 (e >> 1), row 2 t + (e & 1)
-                    const bool edge = key0 + kKeys > all_see;
-                    uint32_t pb[NT][2];
+                    if (key0 + kKeys > all_see) {
+#pragma unroll
+                        for (int c = 0; c < KS; ++c)
+#pragma unroll
+                            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                                for (int e = 0; e < 4; ++e)
+                                    if (key0 + 16 * c + g + 8 * (e >> 1) >= seen[n][e & 1]) S[c][n][e] = kNegInf;
+                    }
+                    // the running maximum, P
+                    uint32_t pb[KS][NT][2];
                     float alpha[NT][2];
 #pragma unroll
                     for (int n = 0; n < NT; ++n) {
-                        float mx[2] = {m[n][0], m[n][1]};
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            float x = scored(S[n][e], f[n][e & 1] * sk, p.cap_out);
-                            if (edge && key0 + g + 8 * (e >> 1) >= seen[n][e & 1]) x = kNegInf;
-                            S[n][e] = x;
-                            mx[e & 1] = fmaxf(mx[e & 1], x);
-                        }
 #pragma unroll
                         for (int e = 0; e < 2; ++e) {
-                            mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], 4));
-                            mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], 8));
-                            mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], 16));
-                            const float mu = mx[e] == kNegInf ? 0.0f : mx[e];      // a row that sees nothing yet
+                            float mx = m[n][e];
+#pragma unroll
+                            for (int c = 0; c < KS; ++c) mx = fmaxf(mx, fmaxf(S[c][n][e], S[c][n][e + 2]));
+                            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
+                            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
+                            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+                            const float mu = mx == kNegInf ? 0.0f : mx;      // a row that sees nothing yet
                             alpha[n][e] = ex2_approx(m[n][e] - mu);
-                            m[n][e] = mx[e];
-                            S[n][e] = ex2_approx(S[n][e] - mu);
-                            S[n][e + 2] = ex2_approx(S[n][e + 2] - mu);
-                            l[n][e] = fmaf(l[n][e], alpha[n][e], S[n][e] + S[n][e + 2]);
+                            m[n][e] = mx;
+                            l[n][e] *= alpha[n][e];
+#pragma unroll
+                            for (int c = 0; c < KS; ++c) {
+                                S[c][n][e] = ex2_approx(S[c][n][e] - mu);
+                                S[c][n][e + 2] = ex2_approx(S[c][n][e + 2] - mu);
+                                l[n][e] += S[c][n][e] + S[c][n][e + 2];
+                            }
                         }
-                        pb[n][0] = transpose8x8(pack_half2(S[n][0], S[n][1]));
-                        pb[n][1] = transpose8x8(pack_half2(S[n][2], S[n][3]));
+#pragma unroll
+                        for (int c = 0; c < KS; ++c) {
+                            pb[c][n][0] = transpose8x8(pack_half2(S[c][n][0], S[c][n][1]));
+                            pb[c][n][1] = transpose8x8(pack_half2(S[c][n][2], S[c][n][3]));
+                        }
                     }
                     // this page's P V in the codes' units, then O = O alpha + sv (P V): the page
                     // scales may differ by any power of two
                     const uint64_t sv2 = pk2(__float_as_uint(sv), __float_as_uint(sv));
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        const uint32_t sel = (j & 1) ? 0x7362u : 0x5140u;
-                        uint32_t a[4];
-                        codes_to_half(prmt(vw[0][j >> 1], vw[1][j >> 1], sel), a[0], a[1]);
-                        codes_to_half(prmt(vw[2][j >> 1], vw[3][j >> 1], sel), a[2], a[3]);
+                    for (int c = 0; c < KS; ++c) {
+                        if (c >= groups) break;
+                        uint32_t vw[4][4];
 #pragma unroll
-                        for (int n = 0; n < NT; ++n) {
-                            float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-                            mma16816(d, a, pb[n][0], pb[n][1]);
-                            const uint64_t al = pk2(__float_as_uint(alpha[n][0]), __float_as_uint(alpha[n][1]));
+                        for (int k = 0; k < 4; ++k)
+                            *reinterpret_cast<uint4 *>(vw[k]) =
+                                lds128(sV + sw128_offset(key_base + 16 * c + 2 * t + (k & 1) + 8 * (k >> 1), g));
+                        // the last page's slots behind the last token may hold anything
+                        if (key0 + kKeys > s.len) {
 #pragma unroll
-                            for (int e = 0; e < 4; e += 2)
-                                upk2(fma2(pk2(__float_as_uint(d[e]), __float_as_uint(d[e + 1])), sv2,
-                                          mul2(pk2(__float_as_uint(o[n][j][e]), __float_as_uint(o[n][j][e + 1])), al)),
-                                     o[n][j][e], o[n][j][e + 1]);
+                            for (int k = 0; k < 4; ++k)
+                                if (key0 + 16 * c + 2 * t + (k & 1) + 8 * (k >> 1) >= s.len)
+                                    vw[k][0] = vw[k][1] = vw[k][2] = vw[k][3] = 0u;
+                        }
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) {
+                            const uint32_t sel = (j & 1) ? 0x7362u : 0x5140u;
+                            uint32_t a[4];
+                            codes_to_half(prmt(vw[0][j >> 1], vw[1][j >> 1], sel), a[0], a[1]);
+                            codes_to_half(prmt(vw[2][j >> 1], vw[3][j >> 1], sel), a[2], a[3]);
+#pragma unroll
+                            for (int n = 0; n < NT; ++n) {
+                                float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                                mma16816(d, a, pb[c][n][0], pb[c][n][1]);
+                                const uint64_t al = pk2(__float_as_uint(alpha[n][0]), __float_as_uint(alpha[n][1]));
+#pragma unroll
+                                for (int e = 0; e < 4; e += 2) {
+                                    uint64_t old = pk2(__float_as_uint(o[n][j][e]), __float_as_uint(o[n][j][e + 1]));
+                                    if (c == 0) old = mul2(old, al);
+                                    upk2(fma2(pk2(__float_as_uint(d[e]), __float_as_uint(d[e + 1])), sv2, old), o[n][j][e],
+                                         o[n][j][e + 1]);
+                                }
+                            }
                         }
                     }
                 }
@@ -501,10 +601,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                     l[n][e] += __shfl_xor_sync(0xffffffffu, l[n][e], 16);
                     const int r = 8 * n + 2 * t + e;
                     if (g == 0) {
-                        sM[warp * kRows + r] = m[n][e];
-                        sL[warp * kRows + r] = l[n][e];
+                        sM[warp * L::rows + r] = m[n][e];
+                        sL[warp * L::rows + r] = l[n][e];
                     }
-                    float4 *at = reinterpret_cast<float4 *>(sMerge + (warp * kRows + r) * kD + 16 * g);
+                    float4 *at = reinterpret_cast<float4 *>(sMerge + (warp * L::rows + r) * kD + 16 * g);
 #pragma unroll
                     for (int j = 0; j < 8; j += 2)
                         at[j / 2] = make_float4(o[n][j][e], o[n][j][e + 2], o[n][j + 1][e], o[n][j + 1][e + 2]);
@@ -515,15 +615,19 @@ __global__ void __launch_bounds__(kThreads, 1)
                 constexpr int kCh = kRows * kD / (32 * kWarps);      // channels a thread adds up
                 const int r = threadIdx.x / (kD / kCh), ch = threadIdx.x % (kD / kCh) * kCh;
                 float M = kNegInf;
+                // row r of key group i: 16 rows a warp, the warps of a key group side by side
+                const int step = kRows == 8 ? 8 : 16 * groups, key_groups = kWarps / groups, from = r & (step - 1);
 #pragma unroll
-                for (int i = 0; i < kWarps; ++i) M = fmaxf(M, sM[i * kRows + r]);
+                for (int i = 0; i < kWarps; ++i)
+                    if (i < key_groups) M = fmaxf(M, sM[i * step + from]);
                 const float Mu = M == kNegInf ? 0.0f : M;
-                float L = 0.0f, acc[kCh] = {};
+                float sum = 0.0f, acc[kCh] = {};
 #pragma unroll
                 for (int i = 0; i < kWarps; ++i) {
-                    const float k = ex2_approx(sM[i * kRows + r] - Mu);
-                    L = fmaf(sL[i * kRows + r], k, L);
-                    const float4 *at = reinterpret_cast<const float4 *>(sMerge + (i * kRows + r) * kD + ch);
+                    if (i >= key_groups) break;
+                    const float k = ex2_approx(sM[i * step + from] - Mu);
+                    sum = fmaf(sL[i * step + from], k, sum);
+                    const float4 *at = reinterpret_cast<const float4 *>(sMerge + (i * step + from) * kD + ch);
 #pragma unroll
                     for (int c = 0; c < kCh / 4; ++c) {
                         const float4 x = at[c];
@@ -534,28 +638,30 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
                 const int row = r0 + r;
-                if (run == w.x.pages) {
+                if (KS == 2 && groups == 1 && r >= 16) {
+                    // no such rows
+                } else if (run == w.x.pages) {
                     // the whole tile: the output itself
                     if (row < R) {
                         const int64_t at = out_row(p, s, w.h, row);
-                        const float inv = L > 0.0f || L != L ? 1.0f / L : 0.0f;
+                        const float inv = sum > 0.0f || sum != sum ? 1.0f / sum : 0.0f;
 #pragma unroll
                         for (int c = 0; c < kCh / 4; ++c)
                             *reinterpret_cast<uint2 *>(p.O + at * kD + ch + 4 * c) =
                                 make_uint2(pack_bf16x2(acc[4 * c] * inv, acc[4 * c + 1] * inv),
                                            pack_bf16x2(acc[4 * c + 2] * inv, acc[4 * c + 3] * inv));
-                        if (p.lse && ch == 0) p.lse[at] = Mu * 0.6931471805599453f + logf(L);
+                        if (p.lse && ch == 0) p.lse[at] = Mu * 0.6931471805599453f + logf(sum);
                     }
                 } else {
                     // a share of it: slot 0 where the CTA's share begins in this tile, else slot 1
-                    float *part = p.part + (static_cast<int64_t>(blockIdx.x) * 2 + (w.left == u1 - u0 ? 0 : 1)) * part_floats(kRows);
+                    float *part = p.part + (static_cast<int64_t>(blockIdx.x) * 2 + (w.left == u_left ? 0 : 1)) * part_floats(kRows);
 #pragma unroll
                     for (int c = 0; c < kCh / 4; ++c)
                         *reinterpret_cast<float4 *>(part + r * kD + ch + 4 * c) =
                             make_float4(acc[4 * c], acc[4 * c + 1], acc[4 * c + 2], acc[4 * c + 3]);
                     if (ch == 0) {
                         part[kRows * kD + r] = M;
-                        part[kRows * kD + kRows + r] = L;
+                        part[kRows * kD + kRows + r] = sum;
                     }
                 }
             }
@@ -571,7 +677,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 // share and begins in it.  One thread per (row, eight channels).
 template <int kRows>
 __global__ void __launch_bounds__(16 * kRows) combine_kernel(const AttnParams p, int ctas) {
-    const int64_t all = count_units<kRows>(p), share = share_of(all, ctas);
+    const int64_t all = count_units<kRows>(p), share = share_of(p, all, ctas);
     const int64_t u0 = share * blockIdx.x, u1 = u0 + share;
     if (u1 >= all) return;                   // nothing behind this share
     int b;
@@ -587,13 +693,16 @@ __global__ void __launch_bounds__(16 * kRows) combine_kernel(const AttnParams p,
     if (row >= s.n * p.G) return;
     const int last = static_cast<int>((end - 1) / share);
     const float kNegInf = __int_as_float(0xff800000);
+    wait_for_results();
     auto part_of = [&](int c) {
         return p.part + (static_cast<int64_t>(c) * 2 + (c == static_cast<int>(blockIdx.x) && begin > u0 ? 1 : 0)) * part_floats(kRows);
     };
     float M = kNegInf;
+#pragma unroll 4
     for (int c = blockIdx.x; c <= last; ++c) M = fmaxf(M, part_of(c)[kRows * kD + r]);
     const float Mu = M == kNegInf ? 0.0f : M;
     float L = 0.0f, acc[8] = {};
+#pragma unroll 4
     for (int c = blockIdx.x; c <= last; ++c) {
         const float *part = part_of(c);
         const float k = ex2_approx(part[kRows * kD + r] - Mu);
@@ -620,21 +729,28 @@ __global__ void __launch_bounds__(16 * kRows) combine_kernel(const AttnParams p,
     if (p.lse && ch == 0) p.lse[at] = Mu * 0.6931471805599453f + logf(L);
 }
 
-// Rows of a tile: eight where every sequence can have no more on average.
-int tile_rows(int T, int Hq, int H, int B) { return static_cast<int64_t>(T) * (Hq / H) > 8ll * B ? 16 : 8; }
+// Rows of a tile: eight where a sequence has no more on average.
+int tile_rows(int T, int Hq, int H, int B) { return static_cast<int64_t>(T) * (Hq / H) <= 8ll * B ? 8 : 32; }
 
-// CTAs of the decode kernel: one per SM, fewer where there cannot be work for all.
-int decode_ctas(int T, int Hq, int H, int B, int cols) {
+// CTAs of the decode kernel: one per SM, fewer where there cannot be work for
+// all; or one for each tile where caches are of at most kWholePages pages and
+// tiles few.
+constexpr int kWholePages = 8;
+struct Grid {
+    int ctas;
+    bool whole;
+};
+Grid grid_of(int T, int Hq, int H, int B, int cols) {
     const int64_t G = Hq / H;
-    const int64_t tiles = static_cast<int64_t>(T) * G / tile_rows(T, Hq, H, B) + (B < T ? B : T);   // of one head, at most
-    const int64_t units = tiles * H * (cols > 0 ? cols : 1);
-    const int64_t most = (units + kSmallest - 1) / kSmallest;
-    return static_cast<int>(most < 152 ? (most < 1 ? 1 : most) : 152);
+    const int64_t tiles = (static_cast<int64_t>(T) * G / tile_rows(T, Hq, H, B) + (B < T ? B : T)) * H;   // at most
+    if (cols <= kWholePages && tiles <= 2 * 152) return {static_cast<int>(tiles), true};
+    const int64_t most = (tiles * cols + kSmallest - 1) / kSmallest;
+    return {static_cast<int>(most < 152 ? most : 152), false};
 }
 
-// More than one tile of 16 rows a sequence and KV head on average: the tensor
-// core kernel's tiles of 128 rows.
-bool many_rows(int T, int Hq, int H, int B) { return static_cast<int64_t>(T) * (Hq / H) > 16ll * B; }
+// More than 32 rows a sequence and KV head on average: the tensor core kernel's
+// tiles of 128 rows.
+bool many_rows(int T, int Hq, int H, int B) { return static_cast<int64_t>(T) * (Hq / H) > 32ll * B; }
 
 template <int kRows>
 cudaError_t launch_decode(const CUtensorMap &mk, const CUtensorMap &mv, const AttnParams &p, int ctas, cudaStream_t st) {
@@ -642,16 +758,16 @@ cudaError_t launch_decode(const CUtensorMap &mk, const CUtensorMap &mv, const At
     if (e != cudaSuccess) return e;
     decode_kernel<kRows><<<ctas, kThreads, Smem<kRows>::bytes, st>>>(mk, mv, p);
     e = cudaGetLastError();
-    if (e != cudaSuccess) return e;
-    combine_kernel<kRows><<<ctas, 16 * kRows, 0, st>>>(p, ctas);
-    return cudaGetLastError();
+    if (e != cudaSuccess || p.whole) return e;
+    return launch_after(combine_kernel<kRows>, dim3(ctas), 16 * kRows, 0, st, p, ctas);
 }
 
 }  // namespace
 
 size_t cache_attention_workspace(int T, int Hq, int H, int B, int cols) {
     if (many_rows(T, Hq, H, B)) return cache_chunk_workspace(T, Hq, H, B, cols);
-    return static_cast<size_t>(decode_ctas(T, Hq, H, B, cols)) * 2 * part_floats(tile_rows(T, Hq, H, B)) * sizeof(float);
+    const Grid g = grid_of(T, Hq, H, B, cols);
+    return static_cast<size_t>(g.ctas) * 2 * part_floats(tile_rows(T, Hq, H, B)) * sizeof(float);
 }
 
 cudaError_t launch_cache_attention(const CacheAttnArgs &a, cudaStream_t st) {
@@ -663,9 +779,10 @@ cudaError_t launch_cache_attention(const CacheAttnArgs &a, cudaStream_t st) {
     p.O = a.O;
     p.lse = a.lse;
     p.part = static_cast<float *>(a.ws);
-    const int ctas = decode_ctas(a.T, a.Hq, a.c.H, a.c.B, a.c.cols);
-    return tile_rows(a.T, a.Hq, a.c.H, a.c.B) == 8 ? launch_decode<8>(mk, mv, p, ctas, st)
-                                                   : launch_decode<16>(mk, mv, p, ctas, st);
+    const Grid g = grid_of(a.T, a.Hq, a.c.H, a.c.B, a.c.cols);
+    p.whole = g.whole;
+    return tile_rows(a.T, a.Hq, a.c.H, a.c.B) == 8 ? launch_decode<8>(mk, mv, p, g.ctas, st)
+                                                   : launch_decode<32>(mk, mv, p, g.ctas, st);
 }
 
 }  // namespace vca

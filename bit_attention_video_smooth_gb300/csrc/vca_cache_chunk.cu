@@ -199,6 +199,7 @@ __device__ void plan_parts(const ChunkParams &cp) {
 // as hi + lo, with factors that carry the whole power of two, so that a score is
 // the product times softmax_scale alone; and the list of work.
 __global__ void __launch_bounds__(kPlanThreads) queries_kernel(const ChunkParams cp) {
+    let_next_start();
     const AttnParams &p = cp.a;
     const int h = cp.h0 + blockIdx.y, row = threadIdx.x & (kRows - 1), g = threadIdx.x / kRows;
     if (blockIdx.x == 0 && h == 0)
@@ -390,6 +391,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     const AttnParams &p = cp.a;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, h = cp.h0 + blockIdx.y;
+    let_next_start();
+    wait_for_results();
     // the last tiles of a causal sequence see the most pages: they go first
     const Item it = cp.items[gridDim.x - 1 - blockIdx.x];
     if (it.pages == 0) return;
@@ -763,6 +766,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 // Joins the parts of a tile: one CTA per (tile, head, 16 rows).
 __global__ void __launch_bounds__(256) join_kernel(const ChunkParams cp) {
     const AttnParams &p = cp.a;
+    wait_for_results();
     const int first = cp.first[blockIdx.x];
     if (first < 0) return;
     const Item it = cp.items[first];
@@ -852,13 +856,11 @@ cudaError_t launch_cache_chunk(const CacheAttnArgs &a, cudaStream_t st) {
         queries_kernel<<<dim3(cp.tiles, heads), kPlanThreads, 0, st>>>(cp);
         e = cudaGetLastError();
         if (e != cudaSuccess) return e;
-        kernel<<<dim3(q.grid, heads), kThreads, kSmem, st>>>(mk, mv, cp);
-        e = cudaGetLastError();
+        e = launch_after(kernel, dim3(q.grid, heads), kThreads, kSmem, st, mk, mv, cp);
         if (e != cudaSuccess) return e;
     }
     if (!q.split) return cudaSuccess;      // cut tiles are few: one launch had all heads
-    join_kernel<<<dim3(cp.tiles, a.c.H, kRows / 16), 256, 0, st>>>(cp);
-    return cudaGetLastError();
+    return launch_after(join_kernel, dim3(cp.tiles, a.c.H, kRows / 16), 256, 0, st, cp);
 }
 
 }  // namespace vca

@@ -293,6 +293,7 @@ struct Feed {
 // One CTA per (tile, head): 16 threads a row, 8 channels each.
 template <int N>
 __global__ void __launch_bounds__(256) image_kernel(const WeighParams wp) {
+    let_next_start();
     const AttnParams &p = wp.a;
     const int h = blockIdx.y, lane16 = threadIdx.x & 15;
     // the tile's sequence
@@ -507,6 +508,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    wait_for_results();
 
     if (warp == 0) {
         // ------------------------------------------------------------ producer
@@ -729,8 +731,7 @@ cudaError_t launch(const CacheWeighArgs &a, const WeighParams &wp, cudaStream_t 
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     const int64_t pages = static_cast<int64_t>(a.c.cols) * a.c.B * a.c.H;
-    kernel<<<static_cast<unsigned>(pages < 152 ? pages : 152), kThreads, Layout<N>::smem, st>>>(mk, wp);
-    return cudaGetLastError();
+    return launch_after(kernel, dim3(static_cast<unsigned>(pages < 152 ? pages : 152)), kThreads, Layout<N>::smem, st, mk, wp);
 }
 
 }  // namespace

@@ -379,60 +379,56 @@ def _cache_call(where, cache: Cache, rows, others, start=None):
     """Checks a call's tensors and returns the C struct and the device: every
     tensor of the types and shapes of include/vca.h, all on one CUDA device.
     `rows` are (name, tensor, heads) of [T, heads, 128] bf16 with contiguous
-    channels, `others` (name, tensor, dtype, shape) or None tensors."""
-    k8, table = cache.k8, cache.table
+    channels, `others` (name, tensor, dtype, shape), the tensor or the shape
+    None where there is nothing to check."""
+    k8, v8, sk, sv, table, length = cache.k8, cache.v8, cache.sk, cache.sv, cache.table, cache.length
     if k8.dim() != 4 or table.dim() != 2:
         raise ValueError(f"{where}: k8 must be [pages, H, 128, 128] and table [B, cols]")
-    (pages, H), (B, cols) = k8.shape[:2], table.shape
-    for name, t in (("k8", k8), ("v8", cache.v8)):
-        _typed(where, name, t, torch.uint8, (pages, H, 128, 128))
-    for name, t in (("sk", cache.sk), ("sv", cache.sv)):
-        _typed(where, name, t, torch.float32, (pages, H))
-    _typed(where, "table", table, torch.int32, (B, cols))
-    _typed(where, "length", cache.length, torch.int32, (B,))
-    seen = [("k8", k8), ("v8", cache.v8), ("sk", cache.sk), ("sv", cache.sv), ("table", table),
-            ("length", cache.length)]
+    pages, H = k8.shape[:2]
+    B, cols = table.shape
+    codes, scales = (pages, H, 128, 128), (pages, H)
+    seen = [("k8", k8, torch.uint8, codes), ("v8", v8, torch.uint8, codes), ("sk", sk, torch.float32, scales),
+            ("sv", sv, torch.float32, scales), ("table", table, torch.int32, (B, cols)),
+            ("length", length, torch.int32, (B,))]
     if start is not None:
-        _typed(where, "start", start, torch.int32, (B + 1,))
-        seen.append(("start", start))
+        seen.append(("start", start, torch.int32, (B + 1,)))
+    seen += [x for x in others if x[1] is not None]
+    for name, t, dtype, shape in seen:
+        if shape is not None:
+            _typed(where, name, t, dtype, shape)
+        elif not t.is_contiguous():
+            raise ValueError(f"{where}: {name} must be contiguous")
     T = None
     for name, t, heads in rows:
-        if t.dtype != torch.bfloat16 or t.dim() != 3 or t.shape[1] != heads or t.shape[2] != 128:
-            raise ValueError(f"{where}: {name} must be bfloat16 [T, {heads}, 128], got {t.dtype} {tuple(t.shape)}")
+        shape = t.shape
+        if t.dtype != torch.bfloat16 or len(shape) != 3 or shape[1] != heads or shape[2] != 128:
+            raise ValueError(f"{where}: {name} must be bfloat16 [T, {heads}, 128], got {t.dtype} {tuple(shape)}")
         if t.stride(2) != 1:
             raise ValueError(f"{where}: the channels of {name} must be contiguous")
-        if T is not None and t.shape[0] != T:
-            raise ValueError(f"{where}: {name} has {t.shape[0]} rows, not {T}")
-        T = t.shape[0]
-        seen.append((name, t))
-    for name, t, dtype, shape in others:
-        if t is not None:
-            if shape is not None:
-                _typed(where, name, t, dtype, shape)
-            elif not t.is_contiguous():
-                raise ValueError(f"{where}: {name} must be contiguous")
-            seen.append((name, t))
+        if T is not None and shape[0] != T:
+            raise ValueError(f"{where}: {name} has {shape[0]} rows, not {T}")
+        T = shape[0]
     dev = k8.device
-    for name, t in seen:
-        if not t.is_cuda:
-            raise ValueError(f"{where}: {name} is not a CUDA tensor")
-        if t.device != dev:
+    for name, t, *_ in seen + list(rows):
+        if t.device != dev or not t.is_cuda:
+            if not t.is_cuda:
+                raise ValueError(f"{where}: {name} is not a CUDA tensor")
             raise ValueError(f"{where}: tensors on several devices: {name} on {t.device}, k8 on {dev}")
-    s = _CacheStruct(k8.data_ptr(), cache.v8.data_ptr(), cache.sk.data_ptr(), cache.sv.data_ptr(), table.data_ptr(),
-                     cache.length.data_ptr(), pages, H, 128, B, cols)
+    s = _CacheStruct(k8.data_ptr(), v8.data_ptr(), sk.data_ptr(), sv.data_ptr(), table.data_ptr(), length.data_ptr(),
+                     pages, H, 128, B, cols)
     return s, dev
 
 
 def _launch(where, dev, fn, *args, stream=None):
     """fn(*args, stream) with `dev` current, on its current stream unless one is given."""
-    if stream is None:
-        stream = torch.cuda.current_stream(dev)
+    raw = torch._C._cuda_getCurrentRawStream(dev.index) if stream is None else stream.cuda_stream
     if torch.cuda.current_device() == dev.index:
-        st = fn(*args, stream.cuda_stream)
+        st = fn(*args, raw)
     else:
         with torch.cuda.device(dev):
-            st = fn(*args, stream.cuda_stream)
-    _check(st, where)
+            st = fn(*args, raw)
+    if st != VCA_OK:
+        _check(st, where)
 
 
 def _at(t: Optional[torch.Tensor]):
