@@ -48,7 +48,7 @@ struct AppendParams {
     int32_t *dev_status;
 };
 
-__global__ void __launch_bounds__(kThreads) append_kernel(const AppendParams p) {
+__global__ void __launch_bounds__(kThreads, 4) append_kernel(const AppendParams p) {
     __shared__ int s_at[4];                 // sequence, page column, its first new row (of the call), page
     __shared__ uint32_t red[kThreads / 32];
     const int lane = threadIdx.x & 31;
@@ -157,9 +157,9 @@ __device__ __forceinline__ uint32_t weight_key(float w) {
     return (u >> 31) ? ~u : (u | 0x80000000u);
 }
 
-constexpr int kSelThreads = 512;
+constexpr int kSelThreads = 1024;
 constexpr int kSelKeys = 40960;         // keys that a CTA can keep in shared memory
-constexpr int kClusterTokens = 4096;    // longer sequences take a cluster for each head
+constexpr int kCluster4Tokens = 16384;  // longer sequences take a cluster of four CTAs for each head
 
 __device__ __forceinline__ uint32_t cluster_rank() {
     uint32_t r;
@@ -182,11 +182,14 @@ __device__ __forceinline__ int cluster_read(const int *p, uint32_t rank) {
 // older slots: the key of the last weight that stays by a radix select over four
 // bytes (the CTAs' histograms are added through distributed shared memory), then
 // the slots that stay, in order.  Each weight is read once, unless a CTA's run
-// does not fit its shared memory.
+// does not fit its shared memory.  Weights crowd into few bins (their first byte
+// is most of the exponent, and many are 0), and equal lanes' atomics take turns:
+// eight copies of the histogram, in different banks, cut the turns by eight.
 template <int kCluster>
 __global__ void __launch_bounds__(kSelThreads) select_kernel(const EvictParams p, int keep) {
     extern __shared__ uint32_t sKeys[];
-    __shared__ int hist[2][256], s_bin, s_left, counts[2];
+    constexpr int kCopy = 257;
+    __shared__ int copies[8 * kCopy], hist[2][256], total[256], s_bin, s_left, counts[2];
     __shared__ int wsum[2][kSelThreads / 32];
     const int rank = kCluster > 1 ? static_cast<int>(cluster_rank()) : 0;
     const int h = blockIdx.x / kCluster, b = blockIdx.y, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -209,8 +212,9 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const EvictParams p
     if (want == 0) return;
     const int run = (older + kCluster * 32 - 1) / (kCluster * 32) * 32;      // a multiple of a warp's
     const int t0 = min(older, rank * run), n = min(older, t0 + run) - t0;
-    auto load_key = [&](int t) -> uint32_t {
-        const int page = p.c.table[static_cast<int64_t>(b) * p.c.cols + t / kBlk];
+    // the key of slot t of the run; a page that does not exist counts as the lowest weights
+    auto load_key = [&](int i) -> uint32_t {
+        const int t = t0 + i, page = p.c.table[static_cast<int64_t>(b) * p.c.cols + t / kBlk];
         if (page < 0 || page >= p.c.pages) {
             report(p.dev_status, kErrInvalid);
             return 0u;
@@ -218,12 +222,34 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const EvictParams p
         return weight_key(p.weight[(static_cast<int64_t>(page) * p.c.H + h) * kBlk + t % kBlk]);
     };
     const bool kept_keys = n <= keep;
-    auto key_of = [&](int i) -> uint32_t { return kept_keys ? sKeys[i] : load_key(t0 + i); };
+    auto key_of = [&](int i) -> uint32_t { return kept_keys ? sKeys[i] : load_key(i); };
     if (kept_keys) {
-#pragma unroll 4
-        for (int i = tid; i < n; i += kSelThreads) sKeys[i] = load_key(t0 + i);
+        // eight at once: the table entries' loads side by side, then the weights'
+        for (int i0 = tid; i0 < n; i0 += 8 * kSelThreads) {
+            int page[8];
+            float w[8];
+            bool bad = false;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                const int i = i0 + k * kSelThreads;
+                page[k] = i < n ? p.c.table[static_cast<int64_t>(b) * p.c.cols + (t0 + i) / kBlk] : 0;
+            }
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                const int i = i0 + k * kSelThreads;
+                const bool there = page[k] >= 0 && page[k] < p.c.pages;
+                bad |= !there;
+                if (i < n && there) w[k] = p.weight[(static_cast<int64_t>(page[k]) * p.c.H + h) * kBlk + (t0 + i) % kBlk];
+            }
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                const int i = i0 + k * kSelThreads;
+                if (i < n) sKeys[i] = page[k] >= 0 && page[k] < p.c.pages ? weight_key(w[k]) : 0u;
+            }
+            if (bad) report(p.dev_status, kErrInvalid);
+        }
     }
-    if (tid < 256) hist[0][tid] = 0;
+    for (int i = tid; i < 8 * kCopy; i += kSelThreads) copies[i] = 0;
     __syncthreads();
     uint32_t prefix = 0, mask = 0;
     int left = want;               // how many of those whose key starts with `prefix` stay
@@ -232,20 +258,35 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const EvictParams p
         int *mine = hist[pass & 1];
         for (int i = tid; i < n; i += kSelThreads) {
             const uint32_t k = key_of(i);
-            if ((k & mask) == prefix) atomicAdd(&mine[(k >> shift) & 255], 1);
+            if ((k & mask) == prefix) atomicAdd(&copies[(lane & 7) * kCopy + ((k >> shift) & 255)], 1);
+        }
+        __syncthreads();
+        if (tid < 256) {
+            int sum = 0;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                sum += copies[i * kCopy + tid];
+                copies[i * kCopy + tid] = 0;
+            }
+            mine[tid] = sum;
         }
         __syncthreads();
         if constexpr (kCluster > 1) cluster_sync();
+        if constexpr (kCluster > 1) {
+            if (tid < 256) {
+                int sum = 0;
+#pragma unroll
+                for (int r = 0; r < kCluster; ++r) sum += cluster_read(&mine[tid], r);
+                total[tid] = sum;
+            }
+            __syncthreads();
+        }
         if (warp == 0) {
             // bins from the top: lane i holds bins 255 - 8 i .. 248 - 8 i
-            int c[8] = {}, s = 0;
+            const int *bins = kCluster > 1 ? total : mine;
+            int c[8], s = 0;
 #pragma unroll
-            for (int r = 0; r < kCluster; ++r)
-#pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    c[e] += kCluster > 1 ? cluster_read(&mine[255 - 8 * lane - e], r) : mine[255 - 8 * lane - e];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) s += c[e];
+            for (int e = 0; e < 8; ++e) s += c[e] = bins[255 - 8 * lane - e];
             int incl = s;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
@@ -264,8 +305,7 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const EvictParams p
                 }
             }
         }
-        // the other histogram, which every CTA of the cluster has read by now
-        if (tid < 256) hist[(pass & 1) ^ 1][tid] = 0;
+        // the next pass writes the other histogram, which every CTA of the cluster has read by now
         __syncthreads();
         prefix |= static_cast<uint32_t>(s_bin) << shift;
         mask |= 255u << shift;
@@ -323,11 +363,24 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const EvictParams p
     }
 }
 
+// The largest magnitude among eight codes, NaN apart.
+__device__ __forceinline__ uint32_t top_code(const uint2 &w) {
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const uint32_t x = (i ? w.y : w.x) & 0x7f7f7f7fu;
+        m = __vmaxu4(m, x & ~(((x + 0x01010101u) & 0x80808080u) - (((x + 0x01010101u) & 0x80808080u) >> 7)));
+    }
+    m = __vmaxu4(m, m >> 16);
+    return max(m & 0xffu, (m >> 8) & 0xffu);
+}
+
 // One CTA per (page that is written, head): K by the first 256 threads, V by the others.
-__global__ void __launch_bounds__(2 * kThreads) move_kernel(const EvictParams p) {
+__global__ void __launch_bounds__(2 * kThreads, 3) move_kernel(const EvictParams p) {
     __shared__ uint32_t red[2][kThreads / 32];
     __shared__ int s_row[kBlk];         // place of the token's row of codes in the pool, in tiles of 128; -1: none
     __shared__ int s_slot[kBlk];
+    __shared__ float s_scale[2][kBlk];
     const int col = blockIdx.x, h = blockIdx.y, b = blockIdx.z, tid = threadIdx.x;
     const bool is_v = tid >= kThreads;
     const int32_t *kept = p.kept + (static_cast<int64_t>(b) * p.c.H + h) * p.budget + col * kBlk;
@@ -340,44 +393,39 @@ __global__ void __launch_bounds__(2 * kThreads) move_kernel(const EvictParams p)
         return;
     }
     const int to = page * p.c.H + h;
-    if (tid < kBlk) {
+    if (tid < 2 * kBlk) {
+        const int j = tid & (kBlk - 1);
         int from = -1, t = 0;
-        if (tid < rows) {
-            t = kept[tid];
+        if (j < rows) {
+            t = kept[j];
             from = load_page(p.c, b, t / kBlk, p.dev_status);
             if (from >= 0) from = from * p.c.H + h;
         }
-        s_row[tid] = from;
-        s_slot[tid] = t % kBlk;
+        s_scale[tid / kBlk][j] = from >= 0 ? (tid < kBlk ? p.c.sk : p.c.sv)[from] : 0.0f;
+        if (tid < kBlk) {
+            s_row[j] = from;
+            s_slot[j] = t % kBlk;
+            if (from >= 0)
+                p.weight[static_cast<int64_t>(to) * kBlk + j] = p.weight[static_cast<int64_t>(from) * kBlk + t % kBlk];
+        }
     }
     __syncthreads();
     const uint8_t *codes = is_v ? p.c.v8 : p.c.k8;
-    const float *scale = is_v ? p.c.sv : p.c.sk;
+    const float *s = s_scale[is_v];
     const int r = (tid >> 4) & 15, ch = (tid & 15) * 8;
     uint2 v[kPasses];
-    float s[kPasses];
     uint32_t m = 0;
 #pragma unroll
     for (int i = 0; i < kPasses; ++i) {
         const int j = r + i * kRowsPerPass, from = s_row[j];
         v[i] = make_uint2(0, 0);
-        s[i] = 0.0f;
-        if (from >= 0) {
-            v[i] = *reinterpret_cast<const uint2 *>(codes + (static_cast<int64_t>(from) * kBlk + s_slot[j]) * kD + ch);
-            s[i] = scale[from];
-        }
+        if (from >= 0) v[i] = *reinterpret_cast<const uint2 *>(codes + (static_cast<int64_t>(from) * kBlk + s_slot[j]) * kD + ch);
     }
-    if (tid < kBlk && s_row[tid] >= 0)
-        p.weight[static_cast<int64_t>(to) * kBlk + tid] = p.weight[static_cast<int64_t>(s_row[tid]) * kBlk + s_slot[tid]];
+    // the largest value of a row: magnitudes of codes are in the order of their bits (NaN apart)
 #pragma unroll
     for (int i = 0; i < kPasses; ++i) {
-        float f[8];
-        decode8(v[i], s[i], f);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const uint32_t u = __float_as_uint(f[e]) & 0x7fffffffu;
-            if (u < 0x7f800000u) m = max(m, u);
-        }
+        const float top = __fmul_rn(e4m3_to_f32(top_code(v[i])), s[r + i * kRowsPerPass]);
+        m = max(m, __float_as_uint(top));
     }
     m = __reduce_max_sync(0xffffffffu, m);
     if ((tid & 31) == 0) red[is_v][(tid >> 5) & 7] = m;
@@ -393,9 +441,12 @@ __global__ void __launch_bounds__(2 * kThreads) move_kernel(const EvictParams p)
     for (int i = 0; i < kPasses; ++i) {
         const int j = r + i * kRowsPerPass;
         if (s_row[j] < 0) continue;
-        float f[8];
-        decode8(v[i], s[i], f);
-        *reinterpret_cast<uint2 *>(out + j * kD + ch) = encode8(f, inv);
+        if (__float_as_uint(s[j]) != sb) {
+            float f[8];
+            decode8(v[i], s[j], f);
+            v[i] = encode8(f, inv);
+        }
+        *reinterpret_cast<uint2 *>(out + j * kD + ch) = v[i];
     }
 }
 
@@ -414,10 +465,10 @@ cudaError_t launch_cache_evict(const CacheView &c, float *weight, const int32_t 
                                int recent, int32_t *new_len, int32_t *kept, int32_t *dev_status, cudaStream_t st) {
     const EvictParams p{c, weight, dst_table, dst_cols, budget, recent, new_len, kept, dev_status};
     const int64_t tokens = static_cast<int64_t>(c.cols) * kBlk;      // of a sequence, at most
-    const int parts = tokens > kClusterTokens ? 8 : 1;
+    const int parts = tokens > kCluster4Tokens ? 4 : 1;
     const int64_t run = (tokens + parts - 1) / parts + 32;
     const int keep = static_cast<int>(run < kSelKeys ? run : kSelKeys);
-    const auto kernel = parts == 8 ? select_kernel<8> : select_kernel<1>;
+    const auto kernel = parts == 4 ? select_kernel<4> : select_kernel<1>;
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSelKeys * 4);
     if (e != cudaSuccess) return e;
     cudaLaunchAttribute at;

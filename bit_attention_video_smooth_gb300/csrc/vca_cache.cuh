@@ -188,13 +188,6 @@ __device__ __forceinline__ float capped(float u, float cap_out) {
     return cap_out * (fabsf(u) <= 1.6f ? u * q : far);
 }
 
-// The same where |u| <= 1.6 is known.
-__device__ __forceinline__ float capped_near(float u, float cap_out) {
-    const float w = u * u;
-    return cap_out * u *
-           fmaf(fmaf(fmaf(fmaf(1.1715225e-06f, w, -3.1559721e-05f), w, 6.6592207e-04f), w, -1.3875789e-02f), w, 3.4657359e-01f);
-}
-
 // Score in log2 units from the raw product: x = S * f with f = c (no cap) or
 // the cap's inner factor.
 __device__ __forceinline__ float scored(float s, float f, float cap_out) {

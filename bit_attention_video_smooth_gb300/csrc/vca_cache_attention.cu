@@ -7,7 +7,7 @@
 //   lse = ln 2 (m + log2 l), m the running maximum.
 //
 // The query rows of one (sequence, KV head) -- its new tokens times the G query
-// heads that share the KV head -- are cut into tiles of 8 or 32.  The work is the
+// heads that share the KV head -- are cut into tiles of 8.  The work is the
 // list of all (sequence, KV head, tile, page) units in that order; each CTA
 // takes an equal share of consecutive units, whatever the sequences' lengths,
 // and writes an (O, m, l) partial where a tile's pages are shared between CTAs;
@@ -18,10 +18,10 @@
 // One producer warp keeps a ring of pages (K and V tile, 16 KB each, one TMA
 // load per tile) full across tile borders; their table entries and scales are
 // loaded two batches ahead, since a load under full traffic takes longer than a
-// page.  Eight consumer warps take 16 keys of every page each (32 keys and half of
-// the rows where a tile has more than 16), with a running maximum, sum and O of
-// their own, which they merge at a tile's end: no barrier but the ring's in
-// between.
+// page.  Eight consumer warps take 16 keys of every page each, with a running
+// maximum, sum and O of their own, which they merge at a tile's end: no barrier
+// but the ring's in between.  (Sixteen rows of a tile, by two such MMAs a
+// fragment, took 1.6 times as long as eight, and the tensor core's kernel less.)
 //
 // Both products are m16n8k16 MMAs on fp16 with the long side as rows, so that
 // eight query rows fill a tile: S^T = K Q^T (16 keys x 8 rows), then O^T = V^T P^T
@@ -44,23 +44,18 @@ constexpr int kThreads = 32 * (kWarps + 1);
 constexpr uint32_t kTile = kBlk * kD;           // bytes of one K or V tile
 constexpr int kSmallest = 2;                    // units a CTA takes at least
 
-// One partial of a tile of `rows` rows: O [rows][128], m [rows], l [rows].
-__host__ __device__ constexpr int part_floats(int rows) { return rows * kD + 2 * rows; }
+constexpr int kRows = 8;                        // query rows of a tile
+constexpr int kKeys = kBlk / kWarps;            // keys of a page per warp
+constexpr int kStages = 5;
+constexpr int kPartFloats = kRows * kD + 2 * kRows;      // O, m and l of a part of a tile
 
-// Shared memory: the ring, the warps' O, m and l (of 16 rows at most), the pages'
-// scales, barriers.  Eight rows leave room for a longer ring.
-template <int kRows>
-struct Smem {
-    static constexpr int rows = kRows == 8 ? 8 : 16;                    // of a warp
-    static constexpr int stages = kRows == 8 ? 5 : 4;
-    static constexpr uint32_t merge = stages * 2 * kTile;               // fp32 [8][rows][128]
-    static constexpr uint32_t ml = merge + kWarps * rows * kD * 4;      // fp32 [8][rows] m, [8][rows] l
-    static constexpr uint32_t query = ml + 2 * kWarps * rows * 4;       // the warps' Q fragments of 16 rows: uint2 [8][2][8][32]
-    static constexpr uint32_t scale = query + (rows == 16 ? kWarps * 4096 : 0);      // fp32 [stages][2]
-    static constexpr uint32_t bar = scale + stages * 8;
-    static constexpr uint32_t bytes = bar + 2 * stages * 8 + 16 + 1024;
-    static_assert(bytes <= 232448, "shared memory budget");
-};
+// Shared memory: the ring, the warps' O, m and l, the pages' scales, barriers.
+constexpr uint32_t kOffMerge = kStages * 2 * kTile;                  // fp32 [8][8][128]
+constexpr uint32_t kOffML = kOffMerge + kWarps * kRows * kD * 4;     // fp32 [8][8] m, [8][8] l
+constexpr uint32_t kOffScale = kOffML + 2 * kWarps * kRows * 4;      // fp32 [stages][2]
+constexpr uint32_t kOffBar = kOffScale + kStages * 8;
+constexpr uint32_t kSmem = kOffBar + 2 * kStages * 8 + 16 + 1024;
+static_assert(kSmem <= 232448, "shared memory budget");
 
 // ---------------------------------------------------------------------------
 // The list of units
@@ -71,7 +66,6 @@ struct Shape {
     Seq s;
     int tiles, pages;
 };
-template <int kRows>
 __device__ __forceinline__ Shape shape_of(const AttnParams &p, int b) {
     Shape x;
     x.s = load_seq(p.c, p.start, p.T, b);
@@ -94,12 +88,11 @@ __device__ __forceinline__ int64_t warp_incl_scan(int64_t v) {
 }
 
 // Units of all sequences (a warp's work).
-template <int kRows>
 __device__ int64_t count_units(const AttnParams &p) {
     int64_t all = 0;
     for (int b0 = 0; b0 < p.c.B; b0 += 32) {
         const int b = b0 + static_cast<int>(threadIdx.x & 31);
-        int64_t v = b < p.c.B ? units_of(p, shape_of<kRows>(p, b)) : 0;
+        int64_t v = b < p.c.B ? units_of(p, shape_of(p, b)) : 0;
         all += __shfl_sync(0xffffffffu, warp_incl_scan(v), 31);
     }
     return all;
@@ -112,13 +105,12 @@ __device__ __forceinline__ int64_t share_of(const AttnParams &p, int64_t all, in
 }
 
 // Where unit u lies: sequence, and the unit's place among the sequence's.
-template <int kRows>
 __device__ void find_unit(const AttnParams &p, int64_t u, int &b_out, int64_t &local) {
     int64_t before = 0;
     const int lane = threadIdx.x & 31;
     for (int b0 = 0; b0 < p.c.B; b0 += 32) {
         const int b = b0 + lane;
-        const int64_t v = b < p.c.B ? units_of(p, shape_of<kRows>(p, b)) : 0;
+        const int64_t v = b < p.c.B ? units_of(p, shape_of(p, b)) : 0;
         const int64_t incl = warp_incl_scan(v) + before;
         const uint32_t hit = __ballot_sync(0xffffffffu, u < incl);
         if (hit) {
@@ -134,7 +126,6 @@ __device__ void find_unit(const AttnParams &p, int64_t u, int &b_out, int64_t &l
 }
 
 // A CTA's walk over its units, one (sequence, head, tile) at a time.
-template <int kRows>
 struct Walk {
     int b, h, tile, page;      // the next unit
     int64_t left;              // units left in the share
@@ -143,7 +134,7 @@ struct Walk {
         b = b_;
         left = units;
         if (b < p.c.B) {
-            x = shape_of<kRows>(p, b);
+            x = shape_of(p, b);
             if (p.whole) {
                 h = static_cast<int>(local / x.tiles);
                 tile = static_cast<int>(local - static_cast<int64_t>(h) * x.tiles);
@@ -171,7 +162,7 @@ struct Walk {
         do {
             ++b;
             if (b >= p.c.B) return;
-            x = shape_of<kRows>(p, b);
+            x = shape_of(p, b);
         } while (x.tiles == 0 || x.pages == 0);
     }
 };
@@ -242,12 +233,12 @@ __device__ __forceinline__ float load_q(const AttnParams &p, const Seq &s, int h
 // The pages of a share and their scales, in order, for a whole warp: three
 // batches of up to 32 pages of one tile, one page per lane -- the one being
 // used, one whose scales are being loaded, one whose table entries are.
-template <int kRows>
 struct Feed {
-    Walk<kRows> ahead;
+    Walk ahead;
     int page[3], count[3], head[3], used;
+    bool real[3];
     float sk[2], sv[2];
-    __device__ void begin(const AttnParams &p, const Walk<kRows> &w) {
+    __device__ void begin(const AttnParams &p, const Walk &w) {
         ahead = w;
         used = 0;
 #pragma unroll
@@ -258,14 +249,22 @@ struct Feed {
     __device__ void fetch(const AttnParams &p, int i) {
         page[i] = -1;
         count[i] = head[i] = 0;
+        real[i] = false;
         if (ahead.left <= 0) return;
         count[i] = min(32, ahead.run());
         head[i] = ahead.h;
         const int lane = threadIdx.x & 31;
-        if (lane < count[i] && ahead.x.s.len > 0) page[i] = load_page(p.c, ahead.b, ahead.page + lane, p.dev_status);
+        // checked when its scales are fetched: the load is not waited for here
+        if (lane < count[i] && ahead.x.s.len > 0)
+            page[i] = p.c.table[static_cast<int64_t>(ahead.b) * p.c.cols + ahead.page + lane];
+        real[i] = lane < count[i] && ahead.x.s.len > 0;
         ahead.next(p, count[i]);
     }
     __device__ void scales(const AttnParams &p, int i) {
+        if (page[i] < 0 || page[i] >= p.c.pages) {
+            if (real[i]) report(p.dev_status, kErrInvalid);
+            page[i] = -1;
+        }
         const int64_t at = static_cast<int64_t>(page[i]) * p.c.H + head[i];
         sk[i] = page[i] >= 0 ? p.c.sk[at] : -1.0f;      // -1: no page
         sv[i] = page[i] >= 0 ? p.c.sv[at] : 0.0f;
@@ -282,6 +281,7 @@ struct Feed {
             page[1] = page[2];
             count[1] = count[2];
             head[1] = head[2];
+            real[1] = real[2];
             scales(p, 1);
             fetch(p, 2);
         }
@@ -293,19 +293,14 @@ struct Feed {
     }
 };
 
-template <int kRows>
 __global__ void __launch_bounds__(kThreads, 1)
     decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, const AttnParams p) {
-    using L = Smem<kRows>;
-    constexpr int NT = L::rows / 8;             // groups of eight query rows of a warp
-    constexpr int KS = kRows == 8 ? 1 : 2;      // groups of 16 keys of a page, at most
-    constexpr int kStages = L::stages;
     extern __shared__ unsigned char smem_raw[];
     unsigned char *smem =
         reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    uint64_t *full = reinterpret_cast<uint64_t *>(smem + L::bar), *empty = full + kStages;
+    uint64_t *full = reinterpret_cast<uint64_t *>(smem + kOffBar), *empty = full + kStages;
     int *abort_flag = reinterpret_cast<int *>(empty + kStages);
-    float *sScale = reinterpret_cast<float *>(smem + L::scale);
+    float *sScale = reinterpret_cast<float *>(smem + kOffScale);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
     if (threadIdx.x == 0) {
@@ -318,7 +313,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     __syncthreads();
     let_next_start();
-    const int64_t all = count_units<kRows>(p), share = share_of(p, all, gridDim.x);
+    const int64_t all = count_units(p), share = share_of(p, all, gridDim.x);
     const int64_t u0 = share * blockIdx.x, u1 = min(all, u0 + share);
     if (blockIdx.x == 0 && warp == 0)
         for (int b = lane; b < p.c.B; b += 32)
@@ -326,8 +321,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (u0 >= u1) return;
     int b0;
     int64_t local;
-    find_unit<kRows>(p, u0, b0, local);
-    Walk<kRows> w;
+    find_unit(p, u0, b0, local);
+    Walk w;
     w.begin(p, b0, local, u1 - u0);
 
     if (warp == kWarps) {
@@ -336,7 +331,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int64_t units = w.left;
         int armed = 0;
         bool ok = true;
-        Feed<kRows> feed;
+        Feed feed;
         feed.begin(p, w);
         for (int64_t i = 0; i < units; ++i) {
             int y;
@@ -370,8 +365,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         // ------------------------------------------------------------ consumers
         // fragments: g and t are the row (key, channel or query row) and the pair of a quad
         const int g = lane >> 2, t = lane & 3;
-        float *sMerge = reinterpret_cast<float *>(smem + L::merge);
-        float *sM = reinterpret_cast<float *>(smem + L::ml), *sL = sM + kWarps * L::rows;
+        float *sMerge = reinterpret_cast<float *>(smem + kOffMerge);
+        float *sM = reinterpret_cast<float *>(smem + kOffML), *sL = sM + kWarps * kRows;
         const int64_t u_left = w.left;
         int stage = 0, round = 0;
         bool ok = true;
@@ -380,208 +375,103 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int run = w.run();
             const Seq s = w.x.s;
             const int R = s.n * p.G, r0 = w.tile * kRows;
-            // the tile's rows in one or two groups of 16; the warp's begin at rw
-            const int groups = KS == 2 && R - r0 > 16 ? 2 : 1, rw = r0 + (groups == 2 ? (warp & 1) * 16 : 0);
-            const int kKeys = 16 * groups, key_base = groups == 2 ? (warp >> 1) * 32 : warp * 16;
-            // Q: the B operand, row 8 n + g; this thread's scores are of the rows 8 n + 2 t and + 1
-            // (in registers for eight rows; 16 leave no room, so each warp keeps a copy in shared memory)
-            uint32_t q[NT == 1 ? 16 : 1];
-            uint2 *sQ = reinterpret_cast<uint2 *>(smem + L::query) + warp * 512 + lane;
-            float f[NT][2], m[NT][2], l[NT][2];
-            int seen[NT][2];
+            // Q: the B operand, row g; this thread's scores are of the rows 2 t and 2 t + 1
+            uint32_t q[16];
+            float f[2], m[2], l[2];
+            int seen[2];
+            const float down = load_q(p, s, w.h, r0 + g, t, q);
+            const float fg = __fmul_rn(p.cap_out != 0.0f ? p.cap_in : p.scale_log2, down);
 #pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                uint32_t row[16];
-                const float down = load_q(p, s, w.h, rw + 8 * n + g, t, row);
-#pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    if constexpr (NT == 1) {
-                        q[2 * k] = row[2 * k];
-                        q[2 * k + 1] = row[2 * k + 1];
-                    } else {
-                        sQ[(n * 8 + k) * 32] = make_uint2(row[2 * k], row[2 * k + 1]);      // read by this thread alone
-                    }
-                }
-                const float fg = __fmul_rn(p.cap_out != 0.0f ? p.cap_in : p.scale_log2, down);
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const int r = rw + 8 * n + 2 * t + e;
-                    f[n][e] = __shfl_sync(0xffffffffu, fg, (2 * t + e) * 4);
-                    seen[n][e] = r < R ? seen_by_row(p, s, r) : 0;
-                    m[n][e] = kNegInf;
-                    l[n][e] = 0.0f;
-                }
+            for (int e = 0; e < 2; ++e) {
+                const int r = r0 + 2 * t + e;
+                f[e] = __shfl_sync(0xffffffffu, fg, (2 * t + e) * 4);
+                seen[e] = r < R ? seen_by_row(p, s, r) : 0;
+                m[e] = kNegInf;
+                l[e] = 0.0f;
             }
-            const int all_see = seen_by_row(p, s, rw);      // keys below this are seen by every row of the warp
+            const int all_see = seen_by_row(p, s, r0);      // keys below this are seen by every row of the tile
             // O^T: channel 16 g + 2 j (elements 0, 1) and 16 g + 2 j + 1 (2, 3) of the rows 2 t, 2 t + 1
-            float o[NT][8][4];
+            float o[8][4];
 #pragma unroll
-            for (int n = 0; n < NT; ++n)
+            for (int j = 0; j < 8; ++j)
 #pragma unroll
-                for (int j = 0; j < 8; ++j)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) o[n][j][e] = 0.0f;
+                for (int e = 0; e < 4; ++e) o[j][e] = 0.0f;
 
             for (int i = 0; i < run; ++i) {
                 if (ok) ok = mbar_wait(full + stage, round & 1, abort_flag, p.limit_ns);
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
                 const float sk = sScale[2 * stage], sv = sScale[2 * stage + 1];
-                const int key0 = (w.page + i) * kBlk + key_base;
+                const int key0 = (w.page + i) * kBlk + kKeys * warp;
                 if (sk >= 0.0f && key0 < s.len) {
                     const unsigned char *sK = smem + stage * 2 * kTile, *sV = sK + kTile;
-                    float S[KS][NT][4];
+                    float S[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                    // K: keys g and g + 8; the four codes of a word are channels 32 t + 4 k .. + 3
 #pragma unroll
-                    for (int c = 0; c < KS; ++c) {
+                    for (int half = 0; half < 2; ++half) {
+                        uint32_t ka[4], kb[4];
+                        *reinterpret_cast<uint4 *>(ka) = lds128(sK + sw128_offset(kKeys * warp + g, 2 * t + half));
+                        *reinterpret_cast<uint4 *>(kb) = lds128(sK + sw128_offset(kKeys * warp + 8 + g, 2 * t + half));
 #pragma unroll
-                        for (int n = 0; n < NT; ++n)
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) S[c][n][e] = c < groups ? 0.0f : kNegInf;
-                        if (c >= groups) continue;
-                        // K: keys g and g + 8; the four codes of a word are channels 32 t + 4 k .. + 3
-#pragma unroll
-                        for (int half = 0; half < 2; ++half) {
-                            uint32_t ka[4], kb[4];
-                            const int k0 = key_base + 16 * c + g;
-                            *reinterpret_cast<uint4 *>(ka) = lds128(sK + sw128_offset(k0, 2 * t + half));
-                            *reinterpret_cast<uint4 *>(kb) = lds128(sK + sw128_offset(k0 + 8, 2 * t + half));
-#pragma unroll
-                            for (int k = 0; k < 4; ++k) {
-                                uint32_t a[4];
-                                codes_to_half(ka[k], a[0], a[2]);
-                                codes_to_half(kb[k], a[1], a[3]);
-#pragma unroll
-                                for (int n = 0; n < NT; ++n) {
-                                    if constexpr (NT == 1) {
-                                        mma16816(S[c][n], a, q[8 * half + 2 * k], q[8 * half + 2 * k + 1]);
-                                    } else {
-                                        const uint2 x = sQ[(n * 8 + 4 * half + k) * 32];
-                                        mma16816(S[c][n], a, x.x, x.y);
-                                    }
-                                }
-                            }
+                        for (int k = 0; k < 4; ++k) {
+                            uint32_t a[4];
+                            codes_to_half(ka[k], a[0], a[2]);
+                            codes_to_half(kb[k], a[1], a[3]);
+                            mma16816(S, a, q[8 * half + 2 * k], q[8 * half + 2 * k + 1]);
                         }
                     }
-                    // scores in log2 units; element e: key 16 c + g + 8 (e >> 1), row 2 t + (e & 1)
-                    if (p.cap_out == 0.0f) {
+                    uint32_t vw[4][4];
 #pragma unroll
-                        for (int n = 0; n < NT; ++n) {
-                            const float f0 = f[n][0] * sk, f1 = f[n][1] * sk;
+                    for (int k = 0; k < 4; ++k)
+                        *reinterpret_cast<uint4 *>(vw[k]) =
+                            lds128(sV + sw128_offset(kKeys * warp + 2 * t + (k & 1) + 8 * (k >> 1), g));
+                    // the last page's slots behind the last token may hold anything
+                    if (key0 + kKeys > s.len) {
 #pragma unroll
-                            for (int c = 0; c < KS; ++c)
-                                if (c < groups)
-#pragma unroll
-                                    for (int e = 0; e < 4; ++e) S[c][n][e] *= (e & 1) ? f1 : f0;
-                        }
-                    } else {
-                        float far = 0.0f;
-#pragma unroll
-                        for (int n = 0; n < NT; ++n) {
-                            const float f0 = f[n][0] * sk, f1 = f[n][1] * sk;
-#pragma unroll
-                            for (int c = 0; c < KS; ++c)
-                                if (c < groups)
-#pragma unroll
-                                    for (int e = 0; e < 4; ++e) {
-                                        S[c][n][e] *= (e & 1) ? f1 : f0;
-                                        far = fmaxf(far, fabsf(S[c][n][e]));
-                                    }
-                        }
-                        if (__all_sync(0xffffffffu, far <= 1.6f)) {
-#pragma unroll
-                            for (int c = 0; c < KS; ++c)
-                                if (c < groups)
-#pragma unroll
-                                    for (int n = 0; n < NT; ++n)
-#pragma unroll
-                                        for (int e = 0; e < 4; ++e) S[c][n][e] = capped_near(S[c][n][e], p.cap_out);
-                        } else {
-#pragma unroll
-                            for (int c = 0; c < KS; ++c)
-                                if (c < groups)
-#pragma unroll
-                                    for (int n = 0; n < NT; ++n)
-#pragma unroll
-                                        for (int e = 0; e < 4; ++e) S[c][n][e] = capped(S[c][n][e], p.cap_out);
-                        }
+                        for (int k = 0; k < 4; ++k)
+                            if (key0 + 2 * t + (k & 1) + 8 * (k >> 1) >= s.len)
+                                vw[k][0] = vw[k][1] = vw[k][2] = vw[k][3] = 0u;
                     }
-                    if (key0 + kKeys > all_see) {
+                    // scores in log2 units, the running maximum, P; element e: key g + 8 (e >> 1), row 2 t + (e & 1)
+                    const bool edge = key0 + kKeys > all_see;
+                    float alpha[2], mx[2] = {m[0], m[1]};
 #pragma unroll
-                        for (int c = 0; c < KS; ++c)
-#pragma unroll
-                            for (int n = 0; n < NT; ++n)
-#pragma unroll
-                                for (int e = 0; e < 4; ++e)
-                                    if (key0 + 16 * c + g + 8 * (e >> 1) >= seen[n][e & 1]) S[c][n][e] = kNegInf;
+                    for (int e = 0; e < 4; ++e) {
+                        float x = scored(S[e], f[e & 1] * sk, p.cap_out);
+                        if (edge && key0 + g + 8 * (e >> 1) >= seen[e & 1]) x = kNegInf;
+                        S[e] = x;
+                        mx[e & 1] = fmaxf(mx[e & 1], x);
                     }
-                    // the running maximum, P
-                    uint32_t pb[KS][NT][2];
-                    float alpha[NT][2];
 #pragma unroll
-                    for (int n = 0; n < NT; ++n) {
-#pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            float mx = m[n][e];
-#pragma unroll
-                            for (int c = 0; c < KS; ++c) mx = fmaxf(mx, fmaxf(S[c][n][e], S[c][n][e + 2]));
-                            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
-                            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
-                            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-                            const float mu = mx == kNegInf ? 0.0f : mx;      // a row that sees nothing yet
-                            alpha[n][e] = ex2_approx(m[n][e] - mu);
-                            m[n][e] = mx;
-                            l[n][e] *= alpha[n][e];
-#pragma unroll
-                            for (int c = 0; c < KS; ++c) {
-                                S[c][n][e] = ex2_approx(S[c][n][e] - mu);
-                                S[c][n][e + 2] = ex2_approx(S[c][n][e + 2] - mu);
-                                l[n][e] += S[c][n][e] + S[c][n][e + 2];
-                            }
-                        }
-#pragma unroll
-                        for (int c = 0; c < KS; ++c) {
-                            pb[c][n][0] = transpose8x8(pack_half2(S[c][n][0], S[c][n][1]));
-                            pb[c][n][1] = transpose8x8(pack_half2(S[c][n][2], S[c][n][3]));
-                        }
+                    for (int e = 0; e < 2; ++e) {
+                        mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], 4));
+                        mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], 8));
+                        mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], 16));
+                        const float mu = mx[e] == kNegInf ? 0.0f : mx[e];      // a row that sees nothing yet
+                        alpha[e] = ex2_approx(m[e] - mu);
+                        m[e] = mx[e];
+                        S[e] = ex2_approx(S[e] - mu);
+                        S[e + 2] = ex2_approx(S[e + 2] - mu);
+                        l[e] = fmaf(l[e], alpha[e], S[e] + S[e + 2]);
                     }
+                    const uint32_t p0 = transpose8x8(pack_half2(S[0], S[1])), p1 = transpose8x8(pack_half2(S[2], S[3]));
                     // this page's P V in the codes' units, then O = O alpha + sv (P V): the page
                     // scales may differ by any power of two
                     const uint64_t sv2 = pk2(__float_as_uint(sv), __float_as_uint(sv));
+                    const uint64_t al = pk2(__float_as_uint(alpha[0]), __float_as_uint(alpha[1]));
 #pragma unroll
-                    for (int c = 0; c < KS; ++c) {
-                        if (c >= groups) break;
-                        uint32_t vw[4][4];
+                    for (int j = 0; j < 8; ++j) {
+                        const uint32_t sel = (j & 1) ? 0x7362u : 0x5140u;
+                        uint32_t a[4];
+                        codes_to_half(prmt(vw[0][j >> 1], vw[1][j >> 1], sel), a[0], a[1]);
+                        codes_to_half(prmt(vw[2][j >> 1], vw[3][j >> 1], sel), a[2], a[3]);
+                        float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                        mma16816(d, a, p0, p1);
 #pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            *reinterpret_cast<uint4 *>(vw[k]) =
-                                lds128(sV + sw128_offset(key_base + 16 * c + 2 * t + (k & 1) + 8 * (k >> 1), g));
-                        // the last page's slots behind the last token may hold anything
-                        if (key0 + kKeys > s.len) {
-#pragma unroll
-                            for (int k = 0; k < 4; ++k)
-                                if (key0 + 16 * c + 2 * t + (k & 1) + 8 * (k >> 1) >= s.len)
-                                    vw[k][0] = vw[k][1] = vw[k][2] = vw[k][3] = 0u;
-                        }
-#pragma unroll
-                        for (int j = 0; j < 8; ++j) {
-                            const uint32_t sel = (j & 1) ? 0x7362u : 0x5140u;
-                            uint32_t a[4];
-                            codes_to_half(prmt(vw[0][j >> 1], vw[1][j >> 1], sel), a[0], a[1]);
-                            codes_to_half(prmt(vw[2][j >> 1], vw[3][j >> 1], sel), a[2], a[3]);
-#pragma unroll
-                            for (int n = 0; n < NT; ++n) {
-                                float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-                                mma16816(d, a, pb[c][n][0], pb[c][n][1]);
-                                const uint64_t al = pk2(__float_as_uint(alpha[n][0]), __float_as_uint(alpha[n][1]));
-#pragma unroll
-                                for (int e = 0; e < 4; e += 2) {
-                                    uint64_t old = pk2(__float_as_uint(o[n][j][e]), __float_as_uint(o[n][j][e + 1]));
-                                    if (c == 0) old = mul2(old, al);
-                                    upk2(fma2(pk2(__float_as_uint(d[e]), __float_as_uint(d[e + 1])), sv2, old), o[n][j][e],
-                                         o[n][j][e + 1]);
-                                }
-                            }
-                        }
+                        for (int e = 0; e < 4; e += 2)
+                            upk2(fma2(pk2(__float_as_uint(d[e]), __float_as_uint(d[e + 1])), sv2,
+                                      mul2(pk2(__float_as_uint(o[j][e]), __float_as_uint(o[j][e + 1])), al)),
+                                 o[j][e], o[j][e + 1]);
                     }
                 }
                 __syncwarp();
@@ -593,72 +483,52 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             // ---- the warps' (O, m, l) merged: each writes its own, all add them up
 #pragma unroll
-            for (int n = 0; n < NT; ++n)
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    l[n][e] += __shfl_xor_sync(0xffffffffu, l[n][e], 4);
-                    l[n][e] += __shfl_xor_sync(0xffffffffu, l[n][e], 8);
-                    l[n][e] += __shfl_xor_sync(0xffffffffu, l[n][e], 16);
-                    const int r = 8 * n + 2 * t + e;
-                    if (g == 0) {
-                        sM[warp * L::rows + r] = m[n][e];
-                        sL[warp * L::rows + r] = l[n][e];
-                    }
-                    float4 *at = reinterpret_cast<float4 *>(sMerge + (warp * L::rows + r) * kD + 16 * g);
-#pragma unroll
-                    for (int j = 0; j < 8; j += 2)
-                        at[j / 2] = make_float4(o[n][j][e], o[n][j][e + 2], o[n][j + 1][e], o[n][j + 1][e + 2]);
+            for (int e = 0; e < 2; ++e) {
+                l[e] += __shfl_xor_sync(0xffffffffu, l[e], 4);
+                l[e] += __shfl_xor_sync(0xffffffffu, l[e], 8);
+                l[e] += __shfl_xor_sync(0xffffffffu, l[e], 16);
+                const int r = 2 * t + e;
+                if (g == 0) {
+                    sM[warp * kRows + r] = m[e];
+                    sL[warp * kRows + r] = l[e];
                 }
+                float4 *at = reinterpret_cast<float4 *>(sMerge + (warp * kRows + r) * kD + 16 * g);
+#pragma unroll
+                for (int j = 0; j < 8; j += 2) at[j / 2] = make_float4(o[j][e], o[j][e + 2], o[j + 1][e], o[j + 1][e + 2]);
+            }
             ok = attn::bar_and(ok, 1, 32 * kWarps);
             if (!ok) break;
             {
-                constexpr int kCh = kRows * kD / (32 * kWarps);      // channels a thread adds up
-                const int r = threadIdx.x / (kD / kCh), ch = threadIdx.x % (kD / kCh) * kCh;
+                const int r = threadIdx.x >> 5, ch = lane * 4;      // row, four channels
                 float M = kNegInf;
-                // row r of key group i: 16 rows a warp, the warps of a key group side by side
-                const int step = kRows == 8 ? 8 : 16 * groups, key_groups = kWarps / groups, from = r & (step - 1);
 #pragma unroll
-                for (int i = 0; i < kWarps; ++i)
-                    if (i < key_groups) M = fmaxf(M, sM[i * step + from]);
+                for (int i = 0; i < kWarps; ++i) M = fmaxf(M, sM[i * kRows + r]);
                 const float Mu = M == kNegInf ? 0.0f : M;
-                float sum = 0.0f, acc[kCh] = {};
+                float sum = 0.0f, acc[4] = {};
 #pragma unroll
                 for (int i = 0; i < kWarps; ++i) {
-                    if (i >= key_groups) break;
-                    const float k = ex2_approx(sM[i * step + from] - Mu);
-                    sum = fmaf(sL[i * step + from], k, sum);
-                    const float4 *at = reinterpret_cast<const float4 *>(sMerge + (i * step + from) * kD + ch);
-#pragma unroll
-                    for (int c = 0; c < kCh / 4; ++c) {
-                        const float4 x = at[c];
-                        acc[4 * c] = fmaf(x.x, k, acc[4 * c]);
-                        acc[4 * c + 1] = fmaf(x.y, k, acc[4 * c + 1]);
-                        acc[4 * c + 2] = fmaf(x.z, k, acc[4 * c + 2]);
-                        acc[4 * c + 3] = fmaf(x.w, k, acc[4 * c + 3]);
-                    }
+                    const float k = ex2_approx(sM[i * kRows + r] - Mu);
+                    sum = fmaf(sL[i * kRows + r], k, sum);
+                    const float4 x = *reinterpret_cast<const float4 *>(sMerge + (i * kRows + r) * kD + ch);
+                    acc[0] = fmaf(x.x, k, acc[0]);
+                    acc[1] = fmaf(x.y, k, acc[1]);
+                    acc[2] = fmaf(x.z, k, acc[2]);
+                    acc[3] = fmaf(x.w, k, acc[3]);
                 }
                 const int row = r0 + r;
-                if (KS == 2 && groups == 1 && r >= 16) {
-                    // no such rows
-                } else if (run == w.x.pages) {
+                if (run == w.x.pages) {
                     // the whole tile: the output itself
                     if (row < R) {
                         const int64_t at = out_row(p, s, w.h, row);
                         const float inv = sum > 0.0f || sum != sum ? 1.0f / sum : 0.0f;
-#pragma unroll
-                        for (int c = 0; c < kCh / 4; ++c)
-                            *reinterpret_cast<uint2 *>(p.O + at * kD + ch + 4 * c) =
-                                make_uint2(pack_bf16x2(acc[4 * c] * inv, acc[4 * c + 1] * inv),
-                                           pack_bf16x2(acc[4 * c + 2] * inv, acc[4 * c + 3] * inv));
+                        *reinterpret_cast<uint2 *>(p.O + at * kD + ch) =
+                            make_uint2(pack_bf16x2(acc[0] * inv, acc[1] * inv), pack_bf16x2(acc[2] * inv, acc[3] * inv));
                         if (p.lse && ch == 0) p.lse[at] = Mu * 0.6931471805599453f + logf(sum);
                     }
                 } else {
                     // a share of it: slot 0 where the CTA's share begins in this tile, else slot 1
-                    float *part = p.part + (static_cast<int64_t>(blockIdx.x) * 2 + (w.left == u_left ? 0 : 1)) * part_floats(kRows);
-#pragma unroll
-                    for (int c = 0; c < kCh / 4; ++c)
-                        *reinterpret_cast<float4 *>(part + r * kD + ch + 4 * c) =
-                            make_float4(acc[4 * c], acc[4 * c + 1], acc[4 * c + 2], acc[4 * c + 3]);
+                    float *part = p.part + (static_cast<int64_t>(blockIdx.x) * 2 + (w.left == u_left ? 0 : 1)) * kPartFloats;
+                    *reinterpret_cast<float4 *>(part + r * kD + ch) = make_float4(acc[0], acc[1], acc[2], acc[3]);
                     if (ch == 0) {
                         part[kRows * kD + r] = M;
                         part[kRows * kD + kRows + r] = sum;
@@ -675,15 +545,14 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // Joins the partials of the tile that straddles the end of CTA blockIdx.x's
 // share and begins in it.  One thread per (row, eight channels).
-template <int kRows>
 __global__ void __launch_bounds__(16 * kRows) combine_kernel(const AttnParams p, int ctas) {
-    const int64_t all = count_units<kRows>(p), share = share_of(p, all, ctas);
+    const int64_t all = count_units(p), share = share_of(p, all, ctas);
     const int64_t u0 = share * blockIdx.x, u1 = u0 + share;
     if (u1 >= all) return;                   // nothing behind this share
     int b;
     int64_t local;
-    find_unit<kRows>(p, u1 - 1, b, local);
-    Walk<kRows> w;
+    find_unit(p, u1 - 1, b, local);
+    Walk w;
     w.begin(p, b, local, 1);
     if (w.page + 1 == w.x.pages) return;     // its tile ends with the share
     const int64_t begin = u1 - 1 - w.page, end = begin + w.x.pages;
@@ -695,7 +564,7 @@ __global__ void __launch_bounds__(16 * kRows) combine_kernel(const AttnParams p,
     const float kNegInf = __int_as_float(0xff800000);
     wait_for_results();
     auto part_of = [&](int c) {
-        return p.part + (static_cast<int64_t>(c) * 2 + (c == static_cast<int>(blockIdx.x) && begin > u0 ? 1 : 0)) * part_floats(kRows);
+        return p.part + (static_cast<int64_t>(c) * 2 + (c == static_cast<int>(blockIdx.x) && begin > u0 ? 1 : 0)) * kPartFloats;
     };
     float M = kNegInf;
 #pragma unroll 4
@@ -729,9 +598,6 @@ __global__ void __launch_bounds__(16 * kRows) combine_kernel(const AttnParams p,
     if (p.lse && ch == 0) p.lse[at] = Mu * 0.6931471805599453f + logf(L);
 }
 
-// Rows of a tile: eight where a sequence has no more on average.
-int tile_rows(int T, int Hq, int H, int B) { return static_cast<int64_t>(T) * (Hq / H) <= 8ll * B ? 8 : 32; }
-
 // CTAs of the decode kernel: one per SM, fewer where there cannot be work for
 // all; or one for each tile where caches are of at most kWholePages pages and
 // tiles few.
@@ -742,32 +608,22 @@ struct Grid {
 };
 Grid grid_of(int T, int Hq, int H, int B, int cols) {
     const int64_t G = Hq / H;
-    const int64_t tiles = (static_cast<int64_t>(T) * G / tile_rows(T, Hq, H, B) + (B < T ? B : T)) * H;   // at most
+    const int64_t tiles = (static_cast<int64_t>(T) * G / kRows + (B < T ? B : T)) * H;   // at most
     if (cols <= kWholePages && tiles <= 2 * 152) return {static_cast<int>(tiles), true};
     const int64_t most = (tiles * cols + kSmallest - 1) / kSmallest;
     return {static_cast<int>(most < 152 ? most : 152), false};
 }
 
-// More than 32 rows a sequence and KV head on average: the tensor core kernel's
-// tiles of 128 rows.
-bool many_rows(int T, int Hq, int H, int B) { return static_cast<int64_t>(T) * (Hq / H) > 32ll * B; }
-
-template <int kRows>
-cudaError_t launch_decode(const CUtensorMap &mk, const CUtensorMap &mv, const AttnParams &p, int ctas, cudaStream_t st) {
-    cudaError_t e = cudaFuncSetAttribute(decode_kernel<kRows>, cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<kRows>::bytes);
-    if (e != cudaSuccess) return e;
-    decode_kernel<kRows><<<ctas, kThreads, Smem<kRows>::bytes, st>>>(mk, mv, p);
-    e = cudaGetLastError();
-    if (e != cudaSuccess || p.whole) return e;
-    return launch_after(combine_kernel<kRows>, dim3(ctas), 16 * kRows, 0, st, p, ctas);
-}
+// More than a tile of rows a sequence and KV head on average: the tensor core
+// kernel's tiles of 128 rows.
+bool many_rows(int T, int Hq, int H, int B) { return static_cast<int64_t>(T) * (Hq / H) > static_cast<int64_t>(kRows) * B; }
 
 }  // namespace
 
 size_t cache_attention_workspace(int T, int Hq, int H, int B, int cols) {
     if (many_rows(T, Hq, H, B)) return cache_chunk_workspace(T, Hq, H, B, cols);
     const Grid g = grid_of(T, Hq, H, B, cols);
-    return static_cast<size_t>(g.ctas) * 2 * part_floats(tile_rows(T, Hq, H, B)) * sizeof(float);
+    return static_cast<size_t>(g.ctas) * 2 * kPartFloats * sizeof(float);
 }
 
 cudaError_t launch_cache_attention(const CacheAttnArgs &a, cudaStream_t st) {
@@ -781,8 +637,12 @@ cudaError_t launch_cache_attention(const CacheAttnArgs &a, cudaStream_t st) {
     p.part = static_cast<float *>(a.ws);
     const Grid g = grid_of(a.T, a.Hq, a.c.H, a.c.B, a.c.cols);
     p.whole = g.whole;
-    return tile_rows(a.T, a.Hq, a.c.H, a.c.B) == 8 ? launch_decode<8>(mk, mv, p, g.ctas, st)
-                                                   : launch_decode<32>(mk, mv, p, g.ctas, st);
+    cudaError_t e = cudaFuncSetAttribute(decode_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    if (e != cudaSuccess) return e;
+    decode_kernel<<<g.ctas, kThreads, kSmem, st>>>(mk, mv, p);
+    e = cudaGetLastError();
+    if (e != cudaSuccess || p.whole) return e;
+    return launch_after(combine_kernel, dim3(g.ctas), 16 * kRows, 0, st, p, g.ctas);
 }
 
 }  // namespace vca

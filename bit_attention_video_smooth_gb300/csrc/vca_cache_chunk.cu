@@ -167,10 +167,14 @@ __device__ void plan_parts(const ChunkParams &cp) {
         for (int i = 0; i < kPlanThreads / 32; ++i) sum += sSum[i];
         return sum;
     };
-    int lo = kSmallest, hi = max(kSmallest, p.c.cols);      // the share lies in [lo, hi]
+    // with W pages in all, sum ceil(pages / share) lies between W / share and W / share + tiles
+    const int slots = max(1, cp.split / p.c.H);
+    const int64_t W = 256ll * block_sum(pages >> 8) + block_sum(pages & 255);      // 2^24 pages a tile at most
+    int lo = max(kSmallest, static_cast<int>((W + slots - 1) / slots));
+    int hi = slots > tiles ? max(lo, static_cast<int>((W + slots - tiles - 1) / (slots - tiles))) : max(lo, p.c.cols);
     while (lo < hi) {
         const int mid = lo + (hi - lo) / 2;
-        if (static_cast<int64_t>(block_sum((pages + mid - 1) / mid)) * p.c.H <= cp.split)
+        if (block_sum((pages + mid - 1) / mid) <= slots)
             hi = mid;
         else
             lo = mid + 1;
