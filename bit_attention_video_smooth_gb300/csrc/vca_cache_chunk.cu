@@ -111,16 +111,21 @@ __device__ __forceinline__ int warp_scan(int v) {
     return v;
 }
 // The index-th tile of a head: its sequence and place there (a warp's work).
-__device__ bool find_tile(const AttnParams &p, int index, int &b, int &tile) {
+__device__ bool find_tile(const AttnParams &p, int index, int &b, int &tile, Seq &s) {
     const int lane = threadIdx.x & 31;
     int before = 0;
     for (int b0 = 0; b0 < p.c.B; b0 += 32) {
-        const int t = b0 + lane < p.c.B ? tiles_of(p, load_seq(p.c, p.start, p.T, b0 + lane)) : 0;
-        const int incl = warp_scan(t) + before;
+        Seq mine{0, 0, 0, false};
+        if (b0 + lane < p.c.B) mine = load_seq(p.c, p.start, p.T, b0 + lane);
+        const int t = tiles_of(p, mine), incl = warp_scan(t) + before;
         const uint32_t hit = __ballot_sync(0xffffffffu, index < incl);
         if (hit) {
             const int l = __ffs(hit) - 1;
             b = b0 + l;
+            s.row0 = __shfl_sync(0xffffffffu, mine.row0, l);
+            s.n = __shfl_sync(0xffffffffu, mine.n, l);
+            s.len = __shfl_sync(0xffffffffu, mine.len, l);
+            s.bad = false;
             tile = index - __shfl_sync(0xffffffffu, incl - t, l);
             return true;
         }
@@ -202,7 +207,7 @@ __device__ void plan_parts(const ChunkParams &cp) {
 // One CTA per (tile, head), one thread per row and 32 channels: a query row split
 // as hi + lo, with factors that carry the whole power of two, so that a score is
 // the product times softmax_scale alone; and the list of work.
-__global__ void __launch_bounds__(kPlanThreads) queries_kernel(const ChunkParams cp) {
+__global__ void __launch_bounds__(kPlanThreads, 3) queries_kernel(const ChunkParams cp) {
     let_next_start();
     const AttnParams &p = cp.a;
     const int h = cp.h0 + blockIdx.y, row = threadIdx.x & (kRows - 1), g = threadIdx.x / kRows;
@@ -210,9 +215,8 @@ __global__ void __launch_bounds__(kPlanThreads) queries_kernel(const ChunkParams
         for (int b = threadIdx.x; b < p.c.B; b += kPlanThreads)
             if (load_seq(p.c, p.start, p.T, b).bad) report(p.dev_status, kErrInvalid);
     int b = 0, tile = 0;
-    const bool found = find_tile(p, blockIdx.x, b, tile);
     Seq s{0, 0, 0, false};
-    if (found) s = load_seq(p.c, p.start, p.T, b);
+    const bool found = find_tile(p, blockIdx.x, b, tile, s);
     if (cp.split == 0 && blockIdx.y == 0 && threadIdx.x == 0) {
         const int i = static_cast<int>(blockIdx.x);
         cp.items[i] = Item{b, tile, 0, found ? pages_of(p, s, tile) : 0, 1, i, i, 0, s};
@@ -291,6 +295,16 @@ __device__ __forceinline__ float rcp_approx(float x) {
     float y;
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
+}
+
+// Contiguous shared -> global copy of `bytes` (a multiple of 16, both addresses
+// 16-byte aligned), and the wait for this thread's.
+__device__ __forceinline__ void bulk_store(void *gmem, const void *smem, uint32_t bytes) {
+    asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(reinterpret_cast<uint64_t>(gmem)),
+                 "r"(smem_u32(smem)), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void bulk_store_wait() {
+    asm volatile("cp.async.bulk.commit_group;\n\tcp.async.bulk.wait_group 0;" ::: "memory");
 }
 
 // What a softmax thread needs for one page's probabilities.
@@ -716,44 +730,50 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc_fence_after();
             const float M = m, Mu = M == kNegInf ? 0.0f : M, L = __fadd_rn(sL[row], sL[kRows + row]);
             const float ref = sSlot[(nb - 1) % kSlots].w;
-            if (it.parts == 1) {
-                const float inv = L > 0.0f || L != L ? 1.0f / L : 0.0f;
-                uint16_t *orow = real ? p.O + out_row(p, it.s, h, r) * kD + 64 * half : nullptr;
+            // rows to shared memory (the K and V rings, free by now), then one bulk copy a
+            // row: a thread's own stores, a row each, would take a cycle for every sector
+            const uint32_t pitch = it.parts == 1 ? kD * 2 + 16 : kD * 4 + 16;      // 16 more: the rows' banks differ
+            unsigned char *line = smem + row * pitch;
+            const float scale = it.parts == 1 ? (L > 0.0f || L != L ? __fdividef(1.0f, L) : 0.0f) * ref : ref;
 #pragma unroll 1
-                for (int i = 0; i < 2; ++i) {
-                    uint32_t o[32], w[16];
-                    VCA_TMEM_LD32(tl + kTmemO + 64 * half + 32 * i, o);
-                    tmem_ld_wait();
+            for (int i = 0; i < 2; ++i) {
+                uint32_t o[32];
+                VCA_TMEM_LD32(tl + kTmemO + 64 * half + 32 * i, o);
+                tmem_ld_wait();
 #pragma unroll
-                    for (int e = 0; e < 16; ++e)
-                        w[e] = pack_bf16x2(__uint_as_float(o[2 * e]) * inv * ref, __uint_as_float(o[2 * e + 1]) * inv * ref);
-                    if (real) {
+                for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * scale);
+                if (it.parts == 1) {
+                    uint4 *to = reinterpret_cast<uint4 *>(line + 2 * (64 * half + 32 * i));
 #pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            reinterpret_cast<uint4 *>(orow + 32 * i)[e] =
-                                make_uint4(w[4 * e], w[4 * e + 1], w[4 * e + 2], w[4 * e + 3]);
+                    for (int e = 0; e < 4; ++e) {
+                        uint32_t w[4];
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            w[k] = pack_bf16x2(__uint_as_float(o[8 * e + 2 * k]), __uint_as_float(o[8 * e + 2 * k + 1]));
+                        to[e] = make_uint4(w[0], w[1], w[2], w[3]);
                     }
-                }
-                if (real && half == 0 && p.lse) p.lse[out_row(p, it.s, h, r)] = Mu * 0.6931471805599453f + logf(L);
-            } else {
-                float *part = p.part + (static_cast<int64_t>(h) * gridDim.x + it.slot) * kPartFloats;
-#pragma unroll 1
-                for (int i = 0; i < 2; ++i) {
-                    uint32_t o[32];
-                    VCA_TMEM_LD32(tl + kTmemO + 64 * half + 32 * i, o);
-                    tmem_ld_wait();
-                    if (real) {
-                        float4 *at = reinterpret_cast<float4 *>(part + row * kD + 64 * half + 32 * i);
+                } else {
+                    uint4 *to = reinterpret_cast<uint4 *>(line + 4 * (64 * half + 32 * i));
 #pragma unroll
-                        for (int e = 0; e < 8; ++e)
-                            at[e] = make_float4(__uint_as_float(o[4 * e]) * ref, __uint_as_float(o[4 * e + 1]) * ref,
-                                                __uint_as_float(o[4 * e + 2]) * ref, __uint_as_float(o[4 * e + 3]) * ref);
-                    }
+                    for (int e = 0; e < 8; ++e) to[e] = make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
                 }
-                if (half == 0) {
+            }
+            fence_proxy_async_smem();
+            bar_sync(bar_pair, 64);      // both halves of the row are there
+            if (half == 0) {
+                if (it.parts == 1) {
+                    if (real) {
+                        const int64_t at = out_row(p, it.s, h, r);
+                        bulk_store(p.O + at * kD, line, kD * 2);
+                        if (p.lse) p.lse[at] = Mu * 0.6931471805599453f + logf(L);
+                    }
+                } else {
+                    float *part = p.part + (static_cast<int64_t>(h) * cp.grid + it.slot) * kPartFloats;
+                    if (real) bulk_store(part + row * kD, line, kD * 4);
                     part[kRows * kD + row] = M;
                     part[kRows * kD + kRows + row] = L;
                 }
+                bulk_store_wait();
             }
         }
     }
