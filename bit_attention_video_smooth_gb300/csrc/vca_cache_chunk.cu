@@ -204,13 +204,14 @@ __device__ void plan_parts(const ChunkParams &cp) {
     for (int i = tiles + tid; i < cp.tiles; i += kPlanThreads) cp.first[i] = -1;
 }
 
-// One CTA per (tile, head), one thread per row and 32 channels: a query row split
-// as hi + lo, with factors that carry the whole power of two, so that a score is
-// the product times softmax_scale alone; and the list of work.
+// One CTA per (tile, head), 16 threads per row, 8 channels each (a warp then reads
+// two whole rows and writes whole sectors of the image): a query row split as hi +
+// lo, with factors that carry the whole power of two, so that a score is the
+// product times softmax_scale alone; and the list of work.
 __global__ void __launch_bounds__(kPlanThreads, 3) queries_kernel(const ChunkParams cp) {
     let_next_start();
     const AttnParams &p = cp.a;
-    const int h = cp.h0 + blockIdx.y, row = threadIdx.x & (kRows - 1), g = threadIdx.x / kRows;
+    const int h = cp.h0 + blockIdx.y;
     if (blockIdx.x == 0 && h == 0)
         for (int b = threadIdx.x; b < p.c.B; b += kPlanThreads)
             if (load_seq(p.c, p.start, p.T, b).bad) report(p.dev_status, kErrInvalid);
@@ -223,48 +224,48 @@ __global__ void __launch_bounds__(kPlanThreads, 3) queries_kernel(const ChunkPar
     }
     if (found) {
         uint8_t *img = cp.images + (static_cast<int64_t>(blockIdx.y) * cp.tiles + blockIdx.x) * kImage;
-        const int r = tile * kRows + row;
-        uint4 v[4];
+        const int lane16 = threadIdx.x & 15, row0 = threadIdx.x >> 4;
+        constexpr int kStep = kPlanThreads / 16;
+        uint4 v[kRows / kStep];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) v[i] = make_uint4(0, 0, 0, 0);
-        if (r < s.n * p.G) {
-            const uint4 *at = reinterpret_cast<const uint4 *>(query_row(p, s, h, r) + 32 * g);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) v[i] = at[i];
+        for (int i = 0; i < kRows / kStep; ++i) {
+            const int r = tile * kRows + row0 + i * kStep;
+            v[i] = make_uint4(0, 0, 0, 0);
+            if (r < s.n * p.G) v[i] = reinterpret_cast<const uint4 *>(query_row(p, s, h, r))[lane16];
         }
-        uint32_t m = 0;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) m = max(m, amax_bf16x8(v[i]));
-        const int e = max(static_cast<int>(m >> 23) - 127 - 7, -100);      // q 2^-e in [2^7, 2^8)
-        const float down = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
-        uint32_t hi[8], lo[8];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < kRows / kStep; ++i) {
+            const int row = row0 + i * kStep;
+            uint32_t m = amax_bf16x8(v[i]);      // of the four threads that share 32 channels
+            m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+            m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
+            const int e = max(static_cast<int>(m >> 23) - 127 - 7, -100);      // q 2^-e in [2^7, 2^8)
+            const float down = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
             const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+            float x[8], d[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                x[2 * k] = scaled_or_nan(__uint_as_float(w[k] << 16), down);
+                x[2 * k + 1] = scaled_or_nan(__uint_as_float(w[k] & 0xffff0000u), down);
+            }
+            uint32_t hi[2], lo[2];
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
-                float x[4], d[4];
+                hi[k] = e4m3x4(x[4 * k], x[4 * k + 1], x[4 * k + 2], x[4 * k + 3]);
+                e4m3x4_decode(hi[k], d);
 #pragma unroll
-                for (int q = 0; q < 2; ++q) {
-                    x[2 * q] = scaled_or_nan(__uint_as_float(w[2 * k + q] << 16), down);
-                    x[2 * q + 1] = scaled_or_nan(__uint_as_float(w[2 * k + q] & 0xffff0000u), down);
-                }
-                hi[2 * i + k] = e4m3x4(x[0], x[1], x[2], x[3]);
-                e4m3x4_decode(hi[2 * i + k], d);
-#pragma unroll
-                for (int q = 0; q < 4; ++q) x[q] = 32.0f * (x[q] - d[q]);
-                lo[2 * i + k] = e4m3x4(x[0], x[1], x[2], x[3]);
+                for (int q = 0; q < 4; ++q) d[q] = 32.0f * (x[4 * k + q] - d[q]);
+                lo[k] = e4m3x4(d[0], d[1], d[2], d[3]);
+            }
+            uint2 *to = reinterpret_cast<uint2 *>(img + ((lane16 >> 1) * kRows + row) * 16 + (lane16 & 1) * 8);
+            to[0] = make_uint2(hi[0], hi[1]);
+            to[kTile / 8] = make_uint2(lo[0], lo[1]);
+            if ((lane16 & 3) == 0) {
+                uint8_t *sf = img + 2 * kTile + 4 * row + (lane16 >> 2);
+                sf[0] = static_cast<uint8_t>(127 + e);          // 27 .. 247
+                sf[4 * kRows] = static_cast<uint8_t>(127 + e - 5);
             }
         }
-        uint4 *to = reinterpret_cast<uint4 *>(img) + row;
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            to[(2 * g + i) * kRows] = make_uint4(hi[4 * i], hi[4 * i + 1], hi[4 * i + 2], hi[4 * i + 3]);
-            to[(8 + 2 * g + i) * kRows] = make_uint4(lo[4 * i], lo[4 * i + 1], lo[4 * i + 2], lo[4 * i + 3]);
-        }
-        uint8_t *sf = img + 2 * kTile + 4 * row + g;
-        sf[0] = static_cast<uint8_t>(127 + e);          // 27 .. 247
-        sf[4 * kRows] = static_cast<uint8_t>(127 + e - 5);
     }
     if (cp.split && blockIdx.x == 0 && h == 0) plan_parts(cp);
 }
@@ -529,8 +530,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             bool ok = mbar_wait(q_full, 0, abort_flag, p.limit_ns);
             for (int b = 0; ok && b < nb; ++b) {
                 const int sb = b & 1;
-                ok = mbar_wait_spin(k_full + st, kphase, abort_flag, p.limit_ns);
-                if (ok && b >= 2) ok = mbar_wait_spin(pv_done + sb, pphase, abort_flag, p.limit_ns);
+                ok = mbar_wait(k_full + st, kphase, abort_flag, p.limit_ns);
+                if (ok && b >= 2) ok = mbar_wait(pv_done + sb, pphase, abort_flag, p.limit_ns);
                 if (!ok) break;
                 tc_fence_after();
                 const uint64_t dk = dk0 + static_cast<uint32_t>(st) * (kTile >> 4);
@@ -560,8 +561,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             bool ok = true;
             for (int b = 0; b < nb; ++b) {
                 const int wt = b % kWStages, sb = b & 1;
-                ok = mbar_wait_spin(w_full + wt, (b / kWStages) & 1, abort_flag, p.limit_ns) &&
-                     mbar_wait_spin(p_full + sb, (b >> 1) & 1, abort_flag, p.limit_ns);
+                ok = mbar_wait(w_full + wt, (b / kWStages) & 1, abort_flag, p.limit_ns) &&
+                     mbar_wait(p_full + sb, (b >> 1) & 1, abort_flag, p.limit_ns);
                 if (!ok) break;
                 tc_fence_after();
                 const uint64_t dv = dv0 + static_cast<uint32_t>(wt) * (kWTile >> 4);
@@ -631,9 +632,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         // raw score -> log2 units (or the cap's inner argument), but for the page's scale
         const float f = kCap ? p.cap_in : p.scale_log2;
         const int seen = (real ? min(seen_by_row(p, it.s, r), it.s.len) : it.s.len) - it.page0 * kBlk - 64 * half;
+        // pages before this one every row of the warp sees in full
+        const int full = __reduce_min_sync(0xffffffffu, seen) / 64 / 2;
         PageScore s;
         s.t = -2.0f * p.cap_out;
-        float m = kNegInf, l = 0.0f;
+        s.bias = kCap ? p.cap_out : 0.0f;
+        float m = kNegInf;
+        uint64_t l2 = 0;
         bool ok = true;
         for (int b = 0; b < nb; ++b) {
             const int sb = b & 1;
@@ -647,59 +652,47 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             const uint32_t tS = tl + kTmemS + 128 * sb;
             uint32_t X0[32], X1[32];
-            float bm = kNegInf;
             tc_fence_after();
             float m0, m1;
             VCA_TMEM_LDMAX32(tS + 64 * half, X0, m0);
             VCA_TMEM_LDMAX32(tS + 64 * half + 32, X1, m1);
             const float4 slot = sSlot[b % kSlots];
-            s.lim = slot.x < 0.0f ? 0 : seen - b * kBlk;
-            s.edge = __any_sync(0xffffffffu, s.lim < 64);
+            s.edge = b >= full || slot.x < 0.0f;
             s.c = fmaxf(__fmul_rn(f, slot.x), 0x1p-126f);      // above 0, so that -inf stays -inf
             tmem_ld_wait();
             if (s.edge) {
+                s.lim = slot.x < 0.0f ? 0 : seen - b * kBlk;
                 m0 = mask_scores(X0, 0, s.lim);
                 m1 = mask_scores(X1, 32, s.lim);
             }
-            const float pm = fmaxf(m0, m1);
-            if (pm != kNegInf)
-                bm = kCap ? fmaf(rcp_approx(1.0f + ex2_approx(pm * s.c)), s.t, p.cap_out) : __fmul_rn(pm, s.c);
+            const float pm = fmaxf(m0, m1) * s.c;
+            const float bm = kCap ? fmaf(rcp_approx(1.0f + ex2_approx(pm)), s.t, p.cap_out) : pm;
             // the row's maximum over both halves; NaN: the other half gave up.  Both
             // halves have read their scores when they meet, so P may be written over
             // them.  Buffers by turns: the next page's barrier separates this read
             // from the write after it
             mx[half * kRows + row] = bm;
             bar_sync(bar_pair, 64);
-            const float other = mx[(half ^ 1) * kRows + row];
-            if (__any_sync(0xffffffffu, other != other)) {
-                ok = false;
-                break;
-            }
-            const float top = fmaxf(bm, other);
-            const bool moved = top > __fadd_rn(m, kLazyTau);
-            const float m_in = m;
-            if (moved) {
-                l = __fmul_rn(l, ex2_approx(__fsub_rn(m, top)));
-                m = top;
-            }
-            const float mu = m == kNegInf ? 0.0f : m;      // a row that sees nothing yet
-            s.bias = kCap ? p.cap_out - mu : -mu;
-            uint64_t l2 = pk2(__float_as_uint(l), 0u);
-            uint32_t W[16];
-            probabilities<kCap>(X0, s, 0, l2, W);
-            VCA_TMEM_ST16(tS + 32 * half, W);
-            probabilities<kCap>(X1, s, 32, l2, W);
-            VCA_TMEM_ST16(tS + 32 * half + 16, W);
-            {
-                float a, c;
-                upk2(l2, a, c);
-                l = __fadd_rn(a, c);
-            }
-            // this half's channels of O after PV(b - 1) to the new reference maximum and scale
-            const float alpha = b > 0 ? (moved ? ex2_approx(__fsub_rn(m_in, m)) : 1.0f) * slot.z : 1.0f;
-            if (__any_sync(0xffffffffu, alpha != 1.0f)) {
-                ok = __all_sync(0xffffffffu, mbar_wait(pv_done + (sb ^ 1), ((b - 1) >> 1) & 1, abort_flag, p.limit_ns));
-                if (ok) {
+            const float other = mx[(half ^ 1) * kRows + row], most = __fadd_rn(m, kLazyTau);
+            // mostly neither the reference maximum nor the reference scale moves
+            if (__any_sync(0xffffffffu, !(bm <= most) || !(other <= most) || slot.z != 1.0f)) {
+                if (__any_sync(0xffffffffu, other != other)) {
+                    ok = false;
+                    break;
+                }
+                const float top = fmaxf(bm, other);
+                float alpha = slot.z;
+                if (top > most) {
+                    const float down = ex2_approx(__fsub_rn(m, top));
+                    l2 = mul2(l2, pk2(__float_as_uint(down), __float_as_uint(down)));
+                    alpha *= down;
+                    m = top;
+                    s.bias = kCap ? p.cap_out - m : -m;
+                }
+                if (b > 0) {
+                    // this half's channels of O, after PV(b - 1), to the new references
+                    ok = __all_sync(0xffffffffu, mbar_wait(pv_done + (sb ^ 1), ((b - 1) >> 1) & 1, abort_flag, p.limit_ns));
+                    if (!ok) continue;      // the other half learns of it where they meet next
                     tc_fence_after();
 #pragma unroll 1
                     for (int i = 0; i < 2; ++i) {
@@ -712,13 +705,21 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
             }
-            // a thread that gave up here tells the other half at the next page
-            if (ok) {
-                tmem_st_wait();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(p_full + sb);
-            }
+            uint32_t W[16];
+            probabilities<kCap>(X0, s, 0, l2, W);
+            VCA_TMEM_ST16(tS + 32 * half, W);
+            probabilities<kCap>(X1, s, 32, l2, W);
+            VCA_TMEM_ST16(tS + 32 * half + 16, W);
+            tmem_st_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(p_full + sb);
+        }
+        float l;
+        {
+            float a, c;
+            upk2(l2, a, c);
+            l = __fadd_rn(a, c);
         }
         // ------------------------------------------------------------ epilogue
         // PV(nb - 1) complete (PV(nb - 3) was when S(nb - 1) came)
