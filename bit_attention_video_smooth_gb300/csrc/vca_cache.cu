@@ -17,11 +17,15 @@ constexpr int kRowsPerPass = kThreads / 16;         // 16 threads a row, 8 chann
 constexpr int kPasses = kBlk / kRowsPerPass;
 
 // Eight codes of eight fp32 values times inv (a power of two: exact above the
-// subnormal codes).
-__device__ __forceinline__ uint2 encode8(const float (&x)[8], float inv) {
+// subnormal codes); `odd`: some may not be finite.
+__device__ __forceinline__ uint2 encode8(const float (&x)[8], float inv, bool odd) {
     float y[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) y[i] = scaled_or_nan(x[i], inv);
+    for (int i = 0; i < 8; ++i) y[i] = __fmul_rn(x[i], inv);
+    if (odd) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) y[i] = scaled_or_nan(x[i], inv);
+    }
     return make_uint2(e4m3x4(y[0], y[1], y[2], y[3]), e4m3x4(y[4], y[5], y[6], y[7]));
 }
 // The values of eight codes at scale s: exact, the smallest (2^-9 2^-120) as a
@@ -101,6 +105,7 @@ __global__ void __launch_bounds__(kThreads, 4) append_kernel(const AppendParams 
 
     uint4 v[kPasses];
     uint32_t m = 0;
+    bool odd = false;
 #pragma unroll
     for (int i = 0; i < kPasses; ++i) {
         const int slot = r + i * kRowsPerPass;
@@ -109,7 +114,7 @@ __global__ void __launch_bounds__(kThreads, 4) append_kernel(const AppendParams 
             v[i] = *reinterpret_cast<const uint4 *>(x.p + (col * kBlk + slot + shift) * x.tok + h * x.head + ch);
     }
 #pragma unroll
-    for (int i = 0; i < kPasses; ++i) m = max(m, amax_bf16x8(v[i]));
+    for (int i = 0; i < kPasses; ++i) m = max(m, amax_bf16x8(v[i], odd));
     const float s_old = lo > 0 ? *scale : 0.0f;
     const uint32_t sb = max(scale_bits(block_max<kThreads>(m, red)), __float_as_uint(s_old) & 0x7f800000u);
     const float inv = pow2_inverse(sb);
@@ -125,7 +130,7 @@ __global__ void __launch_bounds__(kThreads, 4) append_kernel(const AppendParams 
             f[2 * e] = __uint_as_float(w[e] << 16);
             f[2 * e + 1] = __uint_as_float(w[e] & 0xffff0000u);
         }
-        *reinterpret_cast<uint2 *>(codes + slot * kD + ch) = encode8(f, inv);
+        *reinterpret_cast<uint2 *>(codes + slot * kD + ch) = encode8(f, inv, odd);
     }
     // the scale grew: the codes that were there move with it
     if (lo > 0 && __uint_as_float(sb) != s_old) {
@@ -133,7 +138,7 @@ __global__ void __launch_bounds__(kThreads, 4) append_kernel(const AppendParams 
             uint2 *at = reinterpret_cast<uint2 *>(codes + slot * kD + ch);
             float f[8];
             decode8(*at, s_old, f);
-            *at = encode8(f, inv);
+            *at = encode8(f, inv, false);      // a NaN code stays one
         }
     }
 }
@@ -444,7 +449,7 @@ __global__ void __launch_bounds__(2 * kThreads, 3) move_kernel(const EvictParams
         if (__float_as_uint(s[j]) != sb) {
             float f[8];
             decode8(v[i], s[j], f);
-            v[i] = encode8(f, inv);
+            v[i] = encode8(f, inv, false);     // a NaN code stays one
         }
         *reinterpret_cast<uint2 *>(out + j * kD + ch) = v[i];
     }

@@ -77,9 +77,14 @@ __device__ __forceinline__ void e4m3x4_decode(uint32_t w, float (&f)[4]) {
     f[3] = y.y;
 }
 
-// Largest finite magnitude among eight bf16 values (as fp32 bits).
-__device__ __forceinline__ uint32_t amax_bf16x8(const uint4 &v) {
+// Largest finite magnitude among eight bf16 values (as fp32 bits); `odd` is set
+// where some are not finite.
+__device__ __forceinline__ uint32_t amax_bf16x8(const uint4 &v, bool &odd) {
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    uint32_t a = __vmaxu2(__vmaxu2(w[0] & 0x7fff7fffu, w[1] & 0x7fff7fffu), __vmaxu2(w[2] & 0x7fff7fffu, w[3] & 0x7fff7fffu));
+    a = max(a & 0xffffu, a >> 16) << 16;
+    if (a < 0x7f800000u) return a;
+    odd = true;
     uint32_t m = 0;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {

@@ -213,8 +213,9 @@ __device__ __forceinline__ float load_q(const AttnParams &p, const Seq &s, int h
         for (int i = 0; i < 4; ++i) v[i] = at[i];
     }
     uint32_t m = 0;
+    bool odd = false;      // an infinity or NaN is one in fp16 too
 #pragma unroll
-    for (int i = 0; i < 4; ++i) m = max(m, amax_bf16x8(v[i]));
+    for (int i = 0; i < 4; ++i) m = max(m, amax_bf16x8(v[i], odd));
     m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
     m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
     // 2^(13 - e), e the largest element's exponent, kept where both it and its inverse are normal

@@ -236,7 +236,8 @@ __global__ void __launch_bounds__(kPlanThreads, 3) queries_kernel(const ChunkPar
 #pragma unroll
         for (int i = 0; i < kRows / kStep; ++i) {
             const int row = row0 + i * kStep;
-            uint32_t m = amax_bf16x8(v[i]);      // of the four threads that share 32 channels
+            bool odd = false;
+            uint32_t m = amax_bf16x8(v[i], odd);      // of the four threads that share 32 channels
             m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
             m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
             const int e = max(static_cast<int>(m >> 23) - 127 - 7, -100);      // q 2^-e in [2^7, 2^8)
@@ -245,8 +246,12 @@ __global__ void __launch_bounds__(kPlanThreads, 3) queries_kernel(const ChunkPar
             float x[8], d[4];
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-                x[2 * k] = scaled_or_nan(__uint_as_float(w[k] << 16), down);
-                x[2 * k + 1] = scaled_or_nan(__uint_as_float(w[k] & 0xffff0000u), down);
+                x[2 * k] = __uint_as_float(w[k] << 16) * down;
+                x[2 * k + 1] = __uint_as_float(w[k] & 0xffff0000u) * down;
+            }
+            if (odd) {      // the conversion would turn an infinity into a number
+#pragma unroll
+                for (int k = 0; k < 8; ++k) x[k] = scaled_or_nan(x[k], 1.0f);
             }
             uint32_t hi[2], lo[2];
 #pragma unroll

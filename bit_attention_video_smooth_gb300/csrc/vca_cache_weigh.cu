@@ -338,7 +338,8 @@ __global__ void __launch_bounds__(256) image_kernel(const WeighParams wp) {
         const int seen = real ? min(seen_by_row(p, s, r), s.len) : 0;
         uint4 v = make_uint4(0, 0, 0, 0);
         if (real) v = *reinterpret_cast<const uint4 *>(query_row(p, s, h, r) + 8 * lane16);
-        uint32_t m = amax_bf16x8(v);
+        bool odd = false;
+        uint32_t m = amax_bf16x8(v, odd);
         m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
         m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
         const int e = max(static_cast<int>(m >> 23) - 127 - 7, -100);
@@ -347,8 +348,12 @@ __global__ void __launch_bounds__(256) image_kernel(const WeighParams wp) {
         float x[8];
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-            x[2 * k] = scaled_or_nan(__uint_as_float(w[k] << 16), down);
-            x[2 * k + 1] = scaled_or_nan(__uint_as_float(w[k] & 0xffff0000u), down);
+            x[2 * k] = __uint_as_float(w[k] << 16) * down;
+            x[2 * k + 1] = __uint_as_float(w[k] & 0xffff0000u) * down;
+        }
+        if (odd) {      // the conversion would turn an infinity into a number
+#pragma unroll
+            for (int k = 0; k < 8; ++k) x[k] = scaled_or_nan(x[k], 1.0f);
         }
         uint2 hi, lo;
         float d[4];
