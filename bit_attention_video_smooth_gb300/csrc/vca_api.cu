@@ -40,11 +40,14 @@ bool rows_ok(const uint16_t *p, int64_t tok, int64_t head) {
 bool query_sizes_ok(int T, int Hq, int H) {
     return T >= 0 && Hq >= 1 && H >= 1 && Hq % H == 0 && static_cast<int64_t>(T) * Hq <= (static_cast<int64_t>(1) << 31) - 1;
 }
-bool scores_ok(int causal, float softmax_scale, float softcap) {
-    return (causal == 0 || causal == 1) && std::isfinite(softmax_scale) && std::isfinite(softcap) && softcap >= 0.0f;
-}
 float scale_or_default(float softmax_scale) {
     return softmax_scale > 0.0f ? softmax_scale : static_cast<float>(1.0 / std::sqrt(128.0));
+}
+// The kernels scale by softmax_scale / softcap and by softcap, times 2 log2(e): a factor 4 to fp32's largest.
+bool scores_ok(int causal, float softmax_scale, float softcap) {
+    if ((causal != 0 && causal != 1) || !std::isfinite(softmax_scale) || !std::isfinite(softcap) || softcap < 0.0f) return false;
+    const double most = 8.5e37;
+    return softcap == 0.0f || (softcap < most && static_cast<double>(scale_or_default(softmax_scale)) / softcap < most);
 }
 
 int from_cuda(cudaError_t e) { return e == cudaSuccess ? VCA_OK : VCA_ERR_CUDA; }

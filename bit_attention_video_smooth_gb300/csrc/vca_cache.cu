@@ -61,17 +61,14 @@ __global__ void __launch_bounds__(kThreads, 4) append_kernel(const AppendParams 
         int before = 0, found = -1;
         const bool reports = blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0;
         if (lane == 0) s_at[0] = -1;
-        for (int b0 = 0; b0 < p.c.B && (found < 0 || reports); b0 += 32) {
+        bool more = true;
+        for (int b0 = 0; more && (found < 0 || reports); b0 += 32) {
             const int b = b0 + lane;
-            int cnt = 0, first = 0;
-            Seq s{0, 0, 0, false};
-            if (b < p.c.B) {
-                s = load_seq(p.c, p.start, p.T, b);
-                if (s.n > s.len) s.bad = true;      // the cache's length counts the new rows
-                if (reports && s.bad) report(p.dev_status, kErrInvalid);
-                first = s.len - s.n;
-                if (!s.bad && s.n > 0) cnt = (s.len - 1) / kBlk - first / kBlk + 1;
-            }
+            Seq s;
+            more = load_seqs(p.c, p.start, p.T, b0, s);
+            if (s.n > s.len) s.bad = true;      // the cache's length counts the new rows
+            if (reports && s.bad) report(p.dev_status, kErrInvalid);
+            const int first = s.len - s.n, cnt = s.bad || s.n == 0 ? 0 : (s.len - 1) / kBlk - first / kBlk + 1;
             int incl = cnt;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {

@@ -25,19 +25,34 @@ __device__ __forceinline__ void report(int32_t *dev_status, int code) {
 
 // Rows and length of sequence b: its new rows are [row0, row0 + n) of the T
 // rows of the call, `len` its tokens.  bad: start or len out of range (the
-// sequence then counts as having no new rows).
+// sequence then counts as having no new rows); falls: start is.
 struct Seq {
     int row0, n, len;
-    bool bad;
+    bool bad, falls;
 };
 __device__ __forceinline__ Seq load_seq(const CacheView &c, const int32_t *start, int T, int b) {
     Seq s;
     const int lo = start[b], hi = start[b + 1];
     s.len = c.len[b];
-    s.bad = lo < 0 || hi < lo || hi > T || s.len < 0 || s.len > static_cast<int64_t>(c.cols) * kBlk;
+    s.falls = lo < 0 || hi < lo || hi > T;
+    s.bad = s.falls || s.len < 0 || s.len > static_cast<int64_t>(c.cols) * kBlk;
     s.row0 = lo;
     s.n = s.bad ? 0 : hi - lo;
     return s;
+}
+// The sequences b0 .. b0 + 31, one per lane of a warp; returns whether more
+// follow.  Lists of work end at the first sequence whose start falls: the
+// rows of those before it are disjoint, so that no list outgrows T rows.
+__device__ __forceinline__ bool load_seqs(const CacheView &c, const int32_t *start, int T, int b0, Seq &s) {
+    const int lane = threadIdx.x & 31;
+    s = Seq{0, 0, 0, false, false};
+    if (b0 + lane < c.B) s = load_seq(c, start, T, b0 + lane);
+    const uint32_t falls = __ballot_sync(0xffffffffu, s.falls);
+    if (falls & ((1u << lane) - 1u)) {
+        s.n = 0;
+        s.bad = true;
+    }
+    return falls == 0 && b0 + 32 < c.B;
 }
 
 // Page of tokens 128 col .. 128 col + 127 of sequence b, or -1 (reported).
@@ -182,15 +197,48 @@ cudaError_t launch_after(void (*kernel)(Params...), dim3 grid, int threads, size
     return cudaLaunchKernelEx(&c, kernel, Params(args)...);
 }
 
-// The capped score cap tanh(y) in log2 units, y = u ln 2 / 2: tanh(y) =
-// 1 - 2 / (1 + 2^u), which cancels where u is small; below |u| = 1.6 an odd
-// polynomial in u instead, fitted to 3.5e-8 relative (2^-22 with its roundings).
-__device__ __forceinline__ float capped(float u, float cap_out) {
+// tanh(u ln 2 / 2) = 1 - 2 / (1 + 2^u), which cancels where u is small; below
+// |u| = 1.6 an odd polynomial in u instead, fitted to 3.5e-8 relative (2^-22
+// with its roundings).
+constexpr float kTanhNear = 1.6f;
+constexpr float kT0 = 3.4657359e-01f, kT1 = -1.3875789e-02f, kT2 = 6.6592207e-04f, kT3 = -3.1559721e-05f, kT4 = 1.1715225e-06f;
+__device__ __forceinline__ float tanh_half(float u) {
     const float w = u * u;
-    const float q = fmaf(fmaf(fmaf(fmaf(1.1715225e-06f, w, -3.1559721e-05f), w, 6.6592207e-04f), w, -1.3875789e-02f), w,
-                         3.4657359e-01f);
-    const float far = 1.0f - __fdividef(2.0f, 1.0f + ex2_approx(u));
-    return cap_out * (fabsf(u) <= 1.6f ? u * q : far);
+    const float q = fmaf(fmaf(fmaf(fmaf(kT4, w, kT3), w, kT2), w, kT1), w, kT0);
+    const float far = 1.0f - __fdividef(2.0f, 1.0f + ex2_approx(fabsf(u)));
+    return fabsf(u) <= kTanhNear ? u * q : copysignf(far, u);
+}
+// The capped score in log2 units, cap_out tanh.
+__device__ __forceinline__ float capped(float u, float cap_out) { return cap_out * tanh_half(u); }
+
+// tanh_half(X c) in place for kN raw scores of every lane of a warp.  Scores are
+// mostly well below the cap: then the polynomial alone, in pairs, which needs no
+// reciprocal and no power of two (with those, whose units run at a quarter of
+// the multiply-adds' rate or less, they bound the kernels that cap).
+template <int kN>
+__device__ __forceinline__ void tanh_scores(uint32_t (&X)[kN], float c) {
+    float top = 0.0f;
+#pragma unroll
+    for (int k = 0; k < kN; k += 2)
+        top = fmaxf(top, fmaxf(fabsf(__uint_as_float(X[k])), fabsf(__uint_as_float(X[k + 1]))));
+    if (__any_sync(0xffffffffu, top * c > kTanhNear)) {
+#pragma unroll
+        for (int k = 0; k < kN; ++k) X[k] = __float_as_uint(tanh_half(__uint_as_float(X[k]) * c));
+        return;
+    }
+    auto both = [](float x) { return pk2(__float_as_uint(x), __float_as_uint(x)); };
+#pragma unroll
+    for (int k = 0; k < kN; k += 2) {
+        const uint64_t u = mul2(pk2(X[k], X[k + 1]), both(c)), w = mul2(u, u);
+        uint64_t q = fma2(both(kT4), w, both(kT3));
+        q = fma2(q, w, both(kT2));
+        q = fma2(q, w, both(kT1));
+        q = fma2(q, w, both(kT0));
+        float a, b;
+        upk2(mul2(u, q), a, b);
+        X[k] = __float_as_uint(a);
+        X[k + 1] = __float_as_uint(b);
+    }
 }
 
 // Score in log2 units from the raw product: x = S * f with f = c (no cap) or

@@ -66,9 +66,9 @@ struct Shape {
     Seq s;
     int tiles, pages;
 };
-__device__ __forceinline__ Shape shape_of(const AttnParams &p, int b) {
+__device__ __forceinline__ Shape shape_of(const AttnParams &p, const Seq &s) {
     Shape x;
-    x.s = load_seq(p.c, p.start, p.T, b);
+    x.s = s;
     x.tiles = static_cast<int>((static_cast<int64_t>(x.s.n) * p.G + kRows - 1) / kRows);
     x.pages = x.s.bad ? 0 : max(1, (x.s.len + kBlk - 1) / kBlk);
     return x;
@@ -90,10 +90,11 @@ __device__ __forceinline__ int64_t warp_incl_scan(int64_t v) {
 // Units of all sequences (a warp's work).
 __device__ int64_t count_units(const AttnParams &p) {
     int64_t all = 0;
-    for (int b0 = 0; b0 < p.c.B; b0 += 32) {
-        const int b = b0 + static_cast<int>(threadIdx.x & 31);
-        int64_t v = b < p.c.B ? units_of(p, shape_of(p, b)) : 0;
-        all += __shfl_sync(0xffffffffu, warp_incl_scan(v), 31);
+    bool more = true;
+    for (int b0 = 0; more; b0 += 32) {
+        Seq s;
+        more = load_seqs(p.c, p.start, p.T, b0, s);
+        all += __shfl_sync(0xffffffffu, warp_incl_scan(units_of(p, shape_of(p, s))), 31);
     }
     return all;
 }
@@ -107,10 +108,11 @@ __device__ __forceinline__ int64_t share_of(const AttnParams &p, int64_t all, in
 // Where unit u lies: sequence, and the unit's place among the sequence's.
 __device__ void find_unit(const AttnParams &p, int64_t u, int &b_out, int64_t &local) {
     int64_t before = 0;
-    const int lane = threadIdx.x & 31;
-    for (int b0 = 0; b0 < p.c.B; b0 += 32) {
-        const int b = b0 + lane;
-        const int64_t v = b < p.c.B ? units_of(p, shape_of(p, b)) : 0;
+    bool more = true;
+    for (int b0 = 0; more; b0 += 32) {
+        Seq s;
+        more = load_seqs(p.c, p.start, p.T, b0, s);
+        const int64_t v = units_of(p, shape_of(p, s));
         const int64_t incl = warp_incl_scan(v) + before;
         const uint32_t hit = __ballot_sync(0xffffffffu, u < incl);
         if (hit) {
@@ -134,7 +136,7 @@ struct Walk {
         b = b_;
         left = units;
         if (b < p.c.B) {
-            x = shape_of(p, b);
+            x = shape_of(p, load_seq(p.c, p.start, p.T, b));
             if (p.whole) {
                 h = static_cast<int>(local / x.tiles);
                 tile = static_cast<int>(local - static_cast<int64_t>(h) * x.tiles);
@@ -162,7 +164,7 @@ struct Walk {
         do {
             ++b;
             if (b >= p.c.B) return;
-            x = shape_of(p, b);
+            x = shape_of(p, load_seq(p.c, p.start, p.T, b));
         } while (x.tiles == 0 || x.pages == 0);
     }
 };
@@ -549,18 +551,19 @@ __global__ void __launch_bounds__(kThreads, 1)
 __global__ void __launch_bounds__(16 * kRows) combine_kernel(const AttnParams p, int ctas) {
     const int64_t all = count_units(p), share = share_of(p, all, ctas);
     const int64_t u0 = share * blockIdx.x, u1 = u0 + share;
-    if (u1 >= all) return;                   // nothing behind this share
+    // whoever returns here waits too: the call's end is the end of all its kernels
+    if (u1 >= all) return wait_for_results();                   // nothing behind this share
     int b;
     int64_t local;
     find_unit(p, u1 - 1, b, local);
     Walk w;
     w.begin(p, b, local, 1);
-    if (w.page + 1 == w.x.pages) return;     // its tile ends with the share
+    if (w.page + 1 == w.x.pages) return wait_for_results();     // its tile ends with the share
     const int64_t begin = u1 - 1 - w.page, end = begin + w.x.pages;
-    if (begin < u0) return;                  // it began in an earlier share
+    if (begin < u0) return wait_for_results();                  // it began in an earlier share
     const int r = threadIdx.x >> 4, ch = (threadIdx.x & 15) * 8, row = w.tile * kRows + r;
     const Seq s = w.x.s;
-    if (row >= s.n * p.G) return;
+    if (row >= s.n * p.G) return wait_for_results();
     const int last = static_cast<int>((end - 1) / share);
     const float kNegInf = __int_as_float(0xff800000);
     wait_for_results();

@@ -72,7 +72,7 @@ constexpr int kSmallest = 4;                          // pages of a part at leas
 // parts, `slot` its place among the parts of its head, `image` its tile's among
 // the tiles.  pages = 0: nothing.
 struct alignas(16) Item {
-    int b, tile, page0, pages, parts, slot, image, pad;
+    int b, tile, page0, pages, parts, slot, image;
     Seq s;
 };
 
@@ -112,11 +112,11 @@ __device__ __forceinline__ int warp_scan(int v) {
 }
 // The index-th tile of a head: its sequence and place there (a warp's work).
 __device__ bool find_tile(const AttnParams &p, int index, int &b, int &tile, Seq &s) {
-    const int lane = threadIdx.x & 31;
     int before = 0;
-    for (int b0 = 0; b0 < p.c.B; b0 += 32) {
-        Seq mine{0, 0, 0, false};
-        if (b0 + lane < p.c.B) mine = load_seq(p.c, p.start, p.T, b0 + lane);
+    bool more = true;
+    for (int b0 = 0; more; b0 += 32) {
+        Seq mine;
+        more = load_seqs(p.c, p.start, p.T, b0, mine);
         const int t = tiles_of(p, mine), incl = warp_scan(t) + before;
         const uint32_t hit = __ballot_sync(0xffffffffu, index < incl);
         if (hit) {
@@ -125,7 +125,6 @@ __device__ bool find_tile(const AttnParams &p, int index, int &b, int &tile, Seq
             s.row0 = __shfl_sync(0xffffffffu, mine.row0, l);
             s.n = __shfl_sync(0xffffffffu, mine.n, l);
             s.len = __shfl_sync(0xffffffffu, mine.len, l);
-            s.bad = false;
             tile = index - __shfl_sync(0xffffffffu, incl - t, l);
             return true;
         }
@@ -144,8 +143,11 @@ __device__ void plan_parts(const ChunkParams &cp) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     if (warp == 0) {
         int before = 0;
-        for (int b0 = 0; b0 < p.c.B; b0 += 32) {
-            const int n = b0 + lane < p.c.B ? tiles_of(p, load_seq(p.c, p.start, p.T, b0 + lane)) : 0;
+        bool more = true;
+        for (int b0 = 0; more; b0 += 32) {
+            Seq s;
+            more = load_seqs(p.c, p.start, p.T, b0, s);
+            const int n = tiles_of(p, s);
             const int incl = warp_scan(n) + before;
             for (int t = 0; t < n; ++t) {
                 sB[incl - n + t] = b0 + lane;
@@ -157,7 +159,7 @@ __device__ void plan_parts(const ChunkParams &cp) {
     }
     __syncthreads();
     const int tiles = sTiles;
-    Seq s{0, 0, 0, false};
+    Seq s{0, 0, 0, false, false};
     int pages = 0;
     if (tid < tiles) {
         s = load_seq(p.c, p.start, p.T, sB[tid]);
@@ -197,7 +199,7 @@ __device__ void plan_parts(const ChunkParams &cp) {
         for (int i = 0; i < parts; ++i) {
             const int from = static_cast<int>(static_cast<int64_t>(pages) * i / parts);
             const int to = static_cast<int>(static_cast<int64_t>(pages) * (i + 1) / parts);
-            cp.items[slot + i] = Item{sB[tid], sTile[tid], from, to - from, parts, slot + i, tid, 0, s};
+            cp.items[slot + i] = Item{sB[tid], sTile[tid], from, to - from, parts, slot + i, tid, s};
         }
     }
     for (int i = total + tid; i < cp.grid; i += kPlanThreads) cp.items[i].pages = 0;
@@ -216,11 +218,11 @@ __global__ void __launch_bounds__(kPlanThreads, 3) queries_kernel(const ChunkPar
         for (int b = threadIdx.x; b < p.c.B; b += kPlanThreads)
             if (load_seq(p.c, p.start, p.T, b).bad) report(p.dev_status, kErrInvalid);
     int b = 0, tile = 0;
-    Seq s{0, 0, 0, false};
+    Seq s{0, 0, 0, false, false};
     const bool found = find_tile(p, blockIdx.x, b, tile, s);
     if (cp.split == 0 && blockIdx.y == 0 && threadIdx.x == 0) {
         const int i = static_cast<int>(blockIdx.x);
-        cp.items[i] = Item{b, tile, 0, found ? pages_of(p, s, tile) : 0, 1, i, i, 0, s};
+        cp.items[i] = Item{b, tile, 0, found ? pages_of(p, s, tile) : 0, 1, i, i, s};
     }
     if (found) {
         uint8_t *img = cp.images + (static_cast<int64_t>(blockIdx.y) * cp.tiles + blockIdx.x) * kImage;
@@ -297,11 +299,6 @@ __device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
     asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
     return d;
 }
-__device__ __forceinline__ float rcp_approx(float x) {
-    float y;
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
 
 // Contiguous shared -> global copy of `bytes` (a multiple of 16, both addresses
 // 16-byte aligned), and the wait for this thread's.
@@ -315,30 +312,24 @@ __device__ __forceinline__ void bulk_store_wait() {
 
 // What a softmax thread needs for one page's probabilities.
 struct PageScore {
-    float c, bias;       // no cap: p = 2^(S c + bias); cap: p = 2^(r t + bias), r = 1 / (1 + 2^(S c))
-    float t;             // -2 cap log2(e)
+    float c, bias;       // no cap: p = 2^(S c + bias); cap: p = 2^(cap tanh_half(S c) + bias)
+    float cap;           // cap log2(e)
     int lim;             // how many of the thread's 64 columns the row sees
     bool edge;           // some row of the warp does not see all
 };
 
 // 32 raw scores -> 16 words of fp16 pairs; the unrounded probabilities add to l2.
 template <bool kCap>
-__device__ __forceinline__ void probabilities(const uint32_t (&X)[32], const PageScore &s, int col0, uint64_t &l2,
+__device__ __forceinline__ void probabilities(uint32_t (&X)[32], const PageScore &s, int col0, uint64_t &l2,
                                               uint32_t (&W)[16]) {
-    const uint64_t c2 = pk2(__float_as_uint(s.c), __float_as_uint(s.c));
+    if constexpr (kCap) tanh_scores(X, s.c);
+    const float c = kCap ? s.cap : s.c;
+    const uint64_t c2 = pk2(__float_as_uint(c), __float_as_uint(c));
     const uint64_t b2 = pk2(__float_as_uint(s.bias), __float_as_uint(s.bias));
 #pragma unroll
     for (int k = 0; k < 16; ++k) {
         float a, b;
-        if constexpr (kCap) {
-            upk2(mul2(pk2(X[2 * k], X[2 * k + 1]), c2), a, b);
-            a = rcp_approx(1.0f + ex2_approx(a));
-            b = rcp_approx(1.0f + ex2_approx(b));
-            const uint64_t t2 = pk2(__float_as_uint(s.t), __float_as_uint(s.t));
-            upk2(fma2(pk2(__float_as_uint(a), __float_as_uint(b)), t2, b2), a, b);
-        } else {
-            upk2(fma2(pk2(X[2 * k], X[2 * k + 1]), c2, b2), a, b);
-        }
+        upk2(fma2(pk2(X[2 * k], X[2 * k + 1]), c2, b2), a, b);
         a = ex2_approx(a);
         b = ex2_approx(b);
         if constexpr (kCap) {
@@ -385,13 +376,14 @@ __device__ __forceinline__ void convert_rows(const unsigned char *src, unsigned 
 }
 
 // Scores of keys that the row does not see, columns col0 + lim and up, become
-// -inf; returns the largest of the others.
+// -inf (0 where a cap follows); returns the largest of the others.
+template <bool kCap>
 __device__ __forceinline__ float mask_scores(uint32_t (&X)[32], int col0, int lim) {
     float m = __int_as_float(0xff800000);
 #pragma unroll
     for (int e = 0; e < 32; ++e) {
-        if (col0 + e >= lim) X[e] = 0xff800000u;
-        m = fmaxf(m, __uint_as_float(X[e]));
+        if (col0 + e < lim) m = fmaxf(m, __uint_as_float(X[e]));
+        else X[e] = kCap ? 0u : 0xff800000u;
     }
     return m;
 }
@@ -640,8 +632,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         // pages before this one every row of the warp sees in full
         const int full = __reduce_min_sync(0xffffffffu, seen) / 64 / 2;
         PageScore s;
-        s.t = -2.0f * p.cap_out;
-        s.bias = kCap ? p.cap_out : 0.0f;
+        s.cap = p.cap_out;
+        s.bias = 0.0f;
         float m = kNegInf;
         uint64_t l2 = 0;
         bool ok = true;
@@ -667,11 +659,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             tmem_ld_wait();
             if (s.edge) {
                 s.lim = slot.x < 0.0f ? 0 : seen - b * kBlk;
-                m0 = mask_scores(X0, 0, s.lim);
-                m1 = mask_scores(X1, 32, s.lim);
+                m0 = mask_scores<kCap>(X0, 0, s.lim);
+                m1 = mask_scores<kCap>(X1, 32, s.lim);
             }
             const float pm = fmaxf(m0, m1) * s.c;
-            const float bm = kCap ? fmaf(rcp_approx(1.0f + ex2_approx(pm)), s.t, p.cap_out) : pm;
+            const float pc = kCap ? capped(pm, p.cap_out) : pm;
+            const float bm = pc != pc ? kNegInf : pc;      // NaN scores reach O by their probabilities
             // the row's maximum over both halves; NaN: the other half gave up.  Both
             // halves have read their scores when they meet, so P may be written over
             // them.  Buffers by turns: the next page's barrier separates this read
@@ -692,7 +685,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     l2 = mul2(l2, pk2(__float_as_uint(down), __float_as_uint(down)));
                     alpha *= down;
                     m = top;
-                    s.bias = kCap ? p.cap_out - m : -m;
+                    s.bias = -m;
                 }
                 if (b > 0) {
                     // this half's channels of O, after PV(b - 1), to the new references

@@ -15,7 +15,8 @@
 // head's tiles stream past them: a page is read once, and a tile once for four
 // pages.  Few rows are bound by reading K (128 B a token) and the weights; many
 // by the tensor core's two FP8 products, 2 x 2 rows keys d flops.
-// Warps: 0 producer, 1-2 MMA issuers, 3-10 sums (two sets of four).  Every wait is bounded, as in vca_attention.cu.
+// Warps: 0 producer, 1-2 MMA issuers, 3-10 sums (two sets of four).  Every wait is
+// bounded, as in vca_attention.cu.
 #include "vca_attention_common.cuh"
 #include "vca_cache.cuh"
 
@@ -73,12 +74,16 @@ struct Work {
     int tiles, pages;
 };
 template <int N>
-__device__ __forceinline__ Work work_of(const AttnParams &p, int b) {
+__device__ __forceinline__ Work work_of(const AttnParams &p, const Seq &s) {
     Work w;
-    w.s = load_seq(p.c, p.start, p.T, b);
+    w.s = s;
     w.tiles = static_cast<int>((static_cast<int64_t>(w.s.n) * p.G + N - 1) / N);
     w.pages = w.s.bad || w.tiles == 0 ? 0 : (w.s.len + kBlk - 1) / kBlk;
     return w;
+}
+template <int N>
+__device__ __forceinline__ Work work_of(const AttnParams &p, int b) {
+    return work_of<N>(p, load_seq(p.c, p.start, p.T, b));
 }
 // The first tile with a row that sees a page: with x = 128 page - (len - n), a
 // causal row sees it when its token is at least the x-th new one.
@@ -137,25 +142,29 @@ __device__ int64_t head_cost(const AttnParams &p, const Work &w, int64_t find, i
 // Place in the list of (sequence, head, page).
 struct Place {
     int64_t linear;      // pages before it
-    int b, at, tile0;    // its sequence, its place among the sequence's H * pages, the tiles of the sequences before
+    int64_t at;          // its place among its sequence's H * pages
+    int b, tile0;        // the sequence, the tiles of those before
 };
 // The first place before which at least `pos` tiles of work lie: 32 sequences
 // at a time, one per lane, or one by one where their pages cost differently.
 template <int N>
 __device__ Place find_place(const AttnParams &p, int64_t pos) {
-    Place r{0, 0, 0, 0};
+    Place r{};
     const bool even = !p.causal || N == 16;
     const int lane = threadIdx.x & 31, step = even ? 32 : 1;
     int page = 0;
-    for (int b0 = 0; b0 < p.c.B; b0 += step) {
-        const int mine = b0 + (even ? lane : 0);
-        Work w{};
-        int64_t c = 0;
-        if (mine < p.c.B) {
-            w = work_of<N>(p, mine);
-            c = head_cost<N>(p, w, -1, page);
+    bool more = true;
+    for (int b0 = 0; more; b0 += step) {
+        Seq s;
+        if (even) {
+            more = load_seqs(p.c, p.start, p.T, b0, s);
+        } else {
+            s = load_seq(p.c, p.start, p.T, b0);
+            more = !s.falls && b0 + 1 < p.c.B;
         }
-        const bool counts = mine < p.c.B && (even || lane == 0);
+        Work w = work_of<N>(p, s);
+        int64_t c = head_cost<N>(p, w, -1, page);
+        const bool counts = even || lane == 0;
         const int64_t cost = counts ? c * p.c.H : 0, pages = counts ? static_cast<int64_t>(p.c.H) * w.pages : 0;
         const int64_t tiles = counts ? w.tiles : 0;
         const int64_t ci = scan64(cost), pi = scan64(pages), ti = scan64(tiles);
@@ -170,9 +179,9 @@ __device__ Place find_place(const AttnParams &p, int64_t pos) {
             c = __shfl_sync(0xffffffffu, c, l);
             const int64_t h = rest / c;
             head_cost<N>(p, w, rest - h * c, page);
-            r.at = static_cast<int>(h * w.pages + page);
+            r.at = h * w.pages + page;
             r.linear += r.at;
-            if (r.at == p.c.H * w.pages) {
+            if (r.at == static_cast<int64_t>(p.c.H) * w.pages) {
                 r.tile0 += w.tiles;
                 ++r.b;
                 r.at = 0;
@@ -190,15 +199,22 @@ template <int N>
 __device__ int64_t all_work(const AttnParams &p) {
     int64_t sum = 0;
     int page;
+    bool more = true;
     if (!p.causal || N == 16) {
-        for (int b = threadIdx.x & 31; b < p.c.B; b += 32) {
-            const Work w = work_of<N>(p, b);
+        for (int b0 = 0; more; b0 += 32) {
+            Seq s;
+            more = load_seqs(p.c, p.start, p.T, b0, s);
+            const Work w = work_of<N>(p, s);
             sum += static_cast<int64_t>(w.tiles) * w.pages;
         }
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
     } else {
-        for (int b = 0; b < p.c.B; ++b) sum += head_cost<N>(p, work_of<N>(p, b), -1, page);
+        for (int b = 0; more; ++b) {
+            const Work w = work_of<N>(p, b);
+            sum += head_cost<N>(p, w, -1, page);
+            more = !w.s.falls && b + 1 < p.c.B;
+        }
     }
     return sum * p.c.H;
 }
@@ -215,8 +231,8 @@ struct Walk {
         tile0 = from.tile0;
         w = work_of<N>(p, b);
         skip(p);
-        h = from.at / w.pages;
-        page = from.at - h * w.pages;
+        h = static_cast<int>(from.at / w.pages);
+        page = static_cast<int>(from.at - static_cast<int64_t>(h) * w.pages);
     }
     __device__ void skip(const AttnParams &p) {
         while (w.pages == 0 && b + 1 < p.c.B) {
@@ -301,11 +317,14 @@ __global__ void __launch_bounds__(256) image_kernel(const WeighParams wp) {
     {
         const int lane = threadIdx.x & 31;
         int before = 0;
-        bool found = false;
-        for (int b0 = 0; b0 < p.c.B && !found; b0 += 32) {
-            const int t = b0 + lane < p.c.B ? work_of<N>(p, b0 + lane).tiles : 0;
-            if (blockIdx.x == 0 && h == 0 && b0 + lane < p.c.B && load_seq(p.c, p.start, p.T, b0 + lane).bad)
-                report(p.dev_status, kErrInvalid);
+        bool found = false, more = true;
+        if (blockIdx.x == 0 && h == 0)
+            for (int i = threadIdx.x; i < p.c.B; i += 256)
+                if (load_seq(p.c, p.start, p.T, i).bad) report(p.dev_status, kErrInvalid);
+        for (int b0 = 0; more && !found; b0 += 32) {
+            Seq s;
+            more = load_seqs(p.c, p.start, p.T, b0, s);
+            const int t = work_of<N>(p, s).tiles;
             int incl = t;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
@@ -403,23 +422,20 @@ __device__ __forceinline__ void copy_factors(uint32_t taddr, uint32_t saddr) {
     asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(d) : "memory");
 }
 
-// The sum of 2^(S c + (-lse)) over 32 rows of S^T at tS; `lse` their -lse as pairs.
+// The sum of 2^(S c + (-lse)) over kCols rows of S^T, S capped first where there
+// is a cap; `lse` their -lse as pairs.
 template <int kCols, bool kCap, bool kEdge>
-__device__ __forceinline__ uint64_t sum_cols(const uint32_t *X, float c, const uint64_t *lse, const int *seen, int key,
+__device__ __forceinline__ uint64_t sum_cols(uint32_t (&X)[kCols], float c, const uint64_t *lse, const int *seen, int key,
                                              float cap_out, uint64_t sum2) {
+    if constexpr (kCap) {
+        tanh_scores(X, c);
+        c = cap_out;
+    }
     const uint64_t c2 = pk2(__float_as_uint(c), __float_as_uint(c));
 #pragma unroll
     for (int k = 0; k < kCols / 2; ++k) {
         float a, b;
-        if constexpr (kCap) {
-            float u, v, lu, lv;
-            upk2(mul2(pk2(X[2 * k], X[2 * k + 1]), c2), u, v);
-            upk2(lse[k], lu, lv);
-            a = capped(u, cap_out) + lu;
-            b = capped(v, cap_out) + lv;
-        } else {
-            upk2(fma2(pk2(X[2 * k], X[2 * k + 1]), c2, lse[k]), a, b);
-        }
+        upk2(fma2(pk2(X[2 * k], X[2 * k + 1]), c2, lse[k]), a, b);
         a = ex2_approx(a);
         b = ex2_approx(b);
         if constexpr (kEdge) {
@@ -439,14 +455,16 @@ __device__ __forceinline__ float sum_row(uint32_t tS, float c, const uint64_t *l
     VCA_TMEM_LD32(tS, X0);
     if constexpr (N == 16) {
         tmem_ld_wait();
+        uint32_t X[16];
 #pragma unroll
-        for (int k = 0; k < 16; ++k) X0[k] = __float_as_uint(__fadd_rn(__uint_as_float(X0[k]), __uint_as_float(X0[16 + k])));
-        sum2 = sum_cols<16, kCap, kEdge>(X0, c, lse, seen, key, cap_out, sum2);
+        for (int k = 0; k < 16; ++k) X[k] = __float_as_uint(__fadd_rn(__uint_as_float(X0[k]), __uint_as_float(X0[16 + k])));
+        sum2 = sum_cols<16, kCap, kEdge>(X, c, lse, seen, key, cap_out, sum2);
     } else {
         uint32_t X1[32];
         tmem_ld_wait();
-        VCA_TMEM_LD32(tS + 32, X1);
+        if constexpr (!kCap) VCA_TMEM_LD32(tS + 32, X1);      // (a cap has no registers left for it)
         sum2 = sum_cols<32, kCap, kEdge>(X0, c, lse, seen, key, cap_out, sum2);
+        if constexpr (kCap) VCA_TMEM_LD32(tS + 32, X1);
         tmem_ld_wait();
         sum2 = sum_cols<32, kCap, kEdge>(X1, c, lse + 16, seen + 32, key, cap_out, sum2);
     }
@@ -472,10 +490,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
     const int64_t all = all_work<N>(p), share = (all + gridDim.x - 1) / gridDim.x;
-    if (share * blockIdx.x >= all) return;
+    // whoever returns here waits too: the call's end is the end of both kernels
+    if (share * blockIdx.x >= all) return wait_for_results();
     const Place from = find_place<N>(p, share * blockIdx.x);
     const Place to = find_place<N>(p, min(all, share * (blockIdx.x + 1)));
-    if (to.linear <= from.linear) return;
+    if (to.linear <= from.linear) return wait_for_results();
     Walk<N> wk;
     wk.begin(p, from, to.linear - from.linear);
 

@@ -459,7 +459,7 @@ def vca_cache_weigh(cache: Cache, Q, start, causal: int, softmax_scale: float, s
     T, Hq = (Q.shape[0], Q.shape[1]) if Q.dim() == 3 else (0, 0)
     s, dev = _cache_call("vca_cache_weigh", cache, (("Q", Q, Hq),),
                          (("lse", lse, torch.float32, (T, Hq)),
-                          ("weight", weight, torch.float32, (*cache.k8.shape[:2], 128)),
+                          ("weight", weight, torch.float32, (*cache.sk.shape, 128)),
                           ("ws", ws, None, None), ("dev_status", dev_status, torch.int32, (1,))), start)
     _launch("vca_cache_weigh", dev, _lib.vca_cache_weigh, s, Q.data_ptr(), Q.stride(0), Q.stride(1), start.data_ptr(),
             T, Hq, int(causal), softmax_scale, softcap, lse.data_ptr(), weight.data_ptr(), _at(ws),
@@ -470,11 +470,11 @@ def vca_cache_evict(cache: Cache, weight, dst_table, budget: int, recent: int, n
                     stream=None) -> None:
     if dst_table.dim() != 2:
         raise ValueError("vca_cache_evict: dst_table must be [B, dst_cols]")
-    B, H = cache.length.shape[0], cache.k8.shape[1]
+    B, H = cache.table.shape[:1], cache.sk.shape[1:]
     s, dev = _cache_call("vca_cache_evict", cache, (),
-                         (("weight", weight, torch.float32, (*cache.k8.shape[:2], 128)),
-                          ("dst_table", dst_table, torch.int32, (B, dst_table.shape[1])),
-                          ("new_len", new_len, torch.int32, (B,)), ("kept", kept, torch.int32, (B, H, budget)),
+                         (("weight", weight, torch.float32, (*cache.sk.shape, 128)),
+                          ("dst_table", dst_table, torch.int32, (*B, dst_table.shape[1])),
+                          ("new_len", new_len, torch.int32, B), ("kept", kept, torch.int32, (*B, *H, budget)),
                           ("dev_status", dev_status, torch.int32, (1,))))
     _launch("vca_cache_evict", dev, _lib.vca_cache_evict, s, weight.data_ptr(), dst_table.data_ptr(),
             dst_table.shape[1], budget, recent, new_len.data_ptr(), kept.data_ptr(), _at(dev_status), stream=stream)

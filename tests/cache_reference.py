@@ -116,8 +116,8 @@ def attention(c, Q, causal=True, softcap=0.0, scale=None):
     The score: products are exact, 128 of them and the accumulator are added in
     fp32, each addition off by at most 2^-23 of what it holds (a tensor core may
     truncate): 2^-16 of the sum of magnitudes; the scale factors' and exp2's
-    roundings 2^-20 more of the probability, a cap its own rounding of 1 - tanh,
-    2^-20 of the cap.  A probability is off by twice that (its own score and the
+    roundings 2^-20 more of the probability, a cap's tanh 2^-20 of the capped score,
+    which is at most the cap and at most the sum of magnitudes.  A probability is off by twice that (its own score and the
     largest one's) and by its rounding to fp16: 2^-11, or 2^-25 absolute.  O
     rounds to bf16: 2^-8."""
     T, Hq = Q.shape[:2]
@@ -140,7 +140,7 @@ def attention(c, Q, causal=True, softcap=0.0, scale=None):
                 z = torch.logsumexp(s, -1)
                 p = torch.exp(s - torch.where(torch.isinf(z), 0.0, z)[..., None])
                 top = mag.amax(-1)
-            es = 2.0 ** -16 * top + 2.0 ** -20 * (1.0 + softcap)
+            es = 2.0 ** -16 * top + 2.0 ** -20 * (1.0 + top.clamp(max=softcap))
             sl = slice(h * G, (h + 1) * G)
             o[lo:hi, sl] = p @ v
             lse[lo:hi, sl] = z
@@ -168,7 +168,7 @@ def weigh(c, Q, lse, weight, causal=True, softcap=0.0, scale=None):
             s, mag = seq_scores(c, Q, b, h, G, causal, softcap, scale)
             z = lse[lo:hi, h * G:(h + 1) * G].double()[..., None]
             x = torch.where(s > -math.inf, torch.exp(s - z), 0.0)
-            off = 2.0 ** -16 * mag + 2.0 ** -20 * (1.0 + softcap) + 2.0 ** -22 * (s.abs().nan_to_num(0, 0, 0) + z.abs().nan_to_num(0, 0, 0))
+            off = 2.0 ** -16 * mag + 2.0 ** -20 * (1.0 + mag.clamp(max=softcap)) + 2.0 ** -22 * (s.abs().nan_to_num(0, 0, 0) + z.abs().nan_to_num(0, 0, 0))
             for t, y in ((w, x.sum((0, 1))), (e, (x * off).sum((0, 1)) + 2.0 ** -22 * x.sum((0, 1)))):
                 flat = t[p, h].reshape(-1)
                 flat[:m] += y

@@ -153,3 +153,28 @@ def test_reference_attention_is_a_softmax():
     v = torch.stack([R.seq_values(c, 0, h // 2, c.v8, c.sv) for h in range(4)])
     ref = torch.nn.functional.scaled_dot_product_attention(Q[:70].double().transpose(0, 1), k, v, is_causal=True)
     assert torch.allclose(o[:70].transpose(0, 1), ref, rtol=1e-10, atol=1e-10) and bool((eo >= 0).all())
+
+
+def test_caps_beyond_fp32_are_refused(V):
+    """softcap and softmax_scale / softcap have to be fp32 numbers after a factor of 4."""
+    s = _struct(V)
+    for cap in (1e-40, 3e38):
+        assert _attend(V, s, cap=cap) == INVALID and _weigh(V, s, cap=cap) == INVALID
+    assert _attend(V, s, scale=1e30, cap=1e-10) == INVALID
+    # in range: on to the next check
+    assert _attend(V, s, cap=1e-30, ws=None) == WORKSPACE and _attend(V, s, cap=1e30, ws=None) == WORKSPACE
+
+
+def test_a_pool_of_another_rank_is_named(V):
+    c = _host_cache(V)
+    flat = V.Cache(c.k8.view(6, -1), c.v8, c.sk, c.sv, c.table, c.length)
+    start = torch.zeros(3, dtype=torch.int32)
+    K, Q = R.rows(4, 2, 1), R.rows(4, 6, 2)
+    w, dst = torch.zeros(6, 2, 128), torch.zeros((2, 2), dtype=torch.int32)
+    kept = torch.zeros((2, 2, 200), dtype=torch.int32)
+    for call in (lambda: V.vca_cache_append(flat, K, K, start),
+                 lambda: V.vca_cache_attention(flat, Q, start, 1, 0.0, 0.0, Q, None, None),
+                 lambda: V.vca_cache_weigh(flat, Q, start, 1, 0.0, 0.0, torch.zeros(4, 6), w, None),
+                 lambda: V.vca_cache_evict(flat, w, dst, 200, 10, torch.zeros(2, dtype=torch.int32), kept)):
+        with pytest.raises(ValueError, match="k8 must be"):
+            call()

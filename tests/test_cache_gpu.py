@@ -392,3 +392,289 @@ def test_capture_and_replay(V):
         _within(lse, z, el, "lse")
         w, e = R.weigh(c, Q.cpu(), lse.cpu(), torch.zeros(weight.shape))
         _within(weight, w, e, "weight")
+
+
+@pytest.mark.parametrize("news", [1, 30])
+def test_starts_that_fall_end_the_list(V, news):
+    """Every second sequence's start falls and the others claim every row: the
+    rows of those before the first fall are right, the rest counts as none,
+    whatever number of rows the list would come to."""
+    B, H, Hq = 70, 2, 4
+    T = B * news
+    c = R.make_case([200] * 2, [T, 0], H, seed=81)
+    c.table = c.table[:1].repeat(B, 1)
+    c.length = c.length[:1].repeat(B)
+    good = c.clone()
+    good.start = torch.tensor([0] + [T] * B, dtype=torch.int32)
+    c.start = torch.tensor([T * (b & 1) for b in range(B + 1)], dtype=torch.int32)
+    Q = R.rows(T, Hq, seed=82)
+    o, z, eo, el = R.attention(good, Q, causal=False)
+    cache, start = c.on(V)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    out, lse = V.cache_attention(cache, Q.cuda(), start, causal=False, dev_status=status)
+    torch.cuda.synchronize()
+    assert int(status) == V.VCA_ERR_INVALID_ARG
+    _within(out, o, eo, "O")
+    _within(lse, z, el, "lse")
+    for causal in (False, True):
+        _, z, _, _ = R.attention(good, Q, causal=causal)
+        w, e = R.weigh(good, Q, z.float(), torch.zeros((*c.sk.shape, 128)), causal=causal)
+        weight = torch.zeros((*c.sk.shape, 128), device="cuda")
+        status.zero_()
+        V.cache_weigh(cache, Q.cuda(), start, z.float().cuda(), weight, causal=causal, dev_status=status)
+        torch.cuda.synchronize()
+        assert int(status) == V.VCA_ERR_INVALID_ARG
+        _within(weight, w, e, "weight")
+    K = R.rows(T, H, seed=83)
+    before = cache.k8.clone()
+    status.zero_()
+    V.cache_append(cache, K.cuda(), K.cuda(), start, dev_status=status)
+    torch.cuda.synchronize()
+    assert int(status) == V.VCA_ERR_INVALID_ARG
+    if T > 200:      # more rows than tokens: sequence 0 is invalid too
+        assert torch.equal(cache.k8, before)
+    else:
+        R.append(good, K, K)
+        _same_codes(cache.k8, good.k8)
+
+
+@pytest.mark.parametrize("news", [1, 20])
+def test_many_sequences(V, news):
+    """More than 32 sequences; one of the last has a bad length and only it suffers."""
+    B, H, Hq = 75, 2, 4
+    lens = [20 + (37 * b) % 300 for b in range(B)]
+    c = R.make_case(lens, [news] * B, H, seed=84)
+    Q = R.rows(B * news, Hq, seed=85)
+    _check_attention(V, c, Q, causal=True)
+    _, z, _, _ = R.attention(c, Q)
+    for bad in (False, True):
+        d, keep = c.clone(), c.clone()
+        if bad:
+            d.length[70] = 1 << 20
+            keep.length[70] = 0
+        w, e = R.weigh(keep, Q, z.float(), torch.zeros((*c.sk.shape, 128)))
+        cache, start = d.on(V)
+        weight = torch.zeros((*c.sk.shape, 128), device="cuda")
+        status = torch.zeros(1, dtype=torch.int32, device="cuda")
+        V.cache_weigh(cache, Q.cuda(), start, z.float().cuda(), weight, dev_status=status)
+        torch.cuda.synchronize()
+        assert int(status) == (V.VCA_ERR_INVALID_ARG if bad else 0)
+        _within(weight, w, e, "weight")
+
+
+@pytest.mark.parametrize("name", ["five to a head", "a chunk", "wide rows"])
+@pytest.mark.parametrize("softcap", [1e-3, 4.0, 1000.0, 1e6, 1e30])
+def test_caps_of_any_size(V, name, softcap):
+    lens, news, Hq, H = BATCHES[name]
+    c = R.make_case(lens, news, H, seed=11)
+    Q = R.rows(sum(news), Hq, seed=86)
+    _, lse = _check_attention(V, c, Q, causal=True, softcap=softcap)
+    w, e = R.weigh(c, Q, lse.cpu(), torch.zeros((*c.sk.shape, 128)), softcap=softcap)
+    cache, start = c.on(V)
+    weight = torch.zeros((*c.sk.shape, 128), device="cuda")
+    V.cache_weigh(cache, Q.cuda(), start, lse, weight, softcap=softcap)
+    _within(weight, w, e, "weight")
+
+
+def test_heads_in_rounds(V):
+    """So many rows that the queries of all heads are not laid out at once."""
+    H, n = 16, 16100
+    c = R.make_case([64], [n], H, seed=87)
+    _check_attention(V, c, R.rows(n, H, seed=88), causal=False)
+
+
+def test_queries_that_are_not_finite(V):
+    """A NaN or an infinity in a row stays in that row."""
+    for news in ([1, 1], [70, 60]):
+        c = R.make_case([200, 300], news, 2, seed=89)
+        Q = R.rows(sum(news), 4, seed=90)
+        o, z, eo, el = R.attention(c, Q)
+        Q[0, 1, 5], Q[-1, 3, 100], Q[-1, 2, 0] = math.nan, math.inf, -math.inf
+        cache, start = c.on(V)
+        out, lse = V.cache_attention(cache, Q.cuda(), start)
+        bad = torch.zeros(Q.shape[:2], dtype=torch.bool)
+        bad[0, 1] = bad[-1, 3] = bad[-1, 2] = True
+        assert bool(torch.isnan(out.cpu()[bad]).all())
+        _within(out.cpu()[~bad], o[~bad], eo[~bad], "O")
+        _within(lse.cpu()[~bad], z[~bad], el[~bad], "lse")
+
+
+def test_empty_caches(V):
+    """Rows of sequences without tokens: O = 0, lse = -inf, nothing weighed."""
+    for news in ([1, 2], [40, 90]):
+        c = R.make_case([0, 0], news, 2, seed=91)
+        Q = R.rows(sum(news), 4, seed=92)
+        out, lse = _check_attention(V, c, Q, causal=False)
+        assert bool((out == 0).all()) and bool((lse == -math.inf).all())
+        cache, start = c.on(V)
+        weight = torch.full((*c.sk.shape, 128), 0.5, device="cuda")
+        V.cache_weigh(cache, Q.cuda(), start, lse, weight, causal=False)
+        kept = torch.full((2, 2, 5), -1, dtype=torch.int32, device="cuda")
+        new_len, _ = V.cache_evict(cache, weight, torch.zeros((2, 1), dtype=torch.int32, device="cuda"), 5, 2, kept=kept)
+        assert bool((weight == 0.5).all()) and bool((new_len == 0).all()) and bool((kept == -1).all())
+
+
+def test_shared_pages(V):
+    """Two sequences with a common prompt read the same pages; their weights add up."""
+    for news in ([1, 1], [50, 70]):
+        c = R.make_case([400, 390], news, 2, seed=93)
+        c.table[1, :2] = c.table[0, :2]
+        Q = R.rows(sum(news), 4, seed=94)
+        _, lse = _check_attention(V, c, Q, causal=True)
+        w, e = R.weigh(c, Q, lse.cpu(), torch.zeros((*c.sk.shape, 128)))
+        cache, start = c.on(V)
+        weight = torch.zeros((*c.sk.shape, 128), device="cuda")
+        V.cache_weigh(cache, Q.cuda(), start, lse, weight)
+        _within(weight, w, e, "weight")
+
+
+def test_pages_that_repeat_in_a_long_table(V):
+    """A table may name a page many times: more tokens than the pool holds."""
+    c = R.make_case([300], [1], 1, seed=95)
+    c.table = c.table[:, :2].repeat(1, 700)
+    c.length[0] = 1400 * 128 - 5
+    _check_attention(V, c, R.rows(1, 2, seed=96))
+    c.start[1] = 12
+    _check_attention(V, c, R.rows(12, 2, seed=97))
+
+
+@pytest.mark.parametrize("len_,budget,recent", [(20000, 900, 100), (170000, 300, 40), (170000, 200, 0)])
+def test_evict_of_long_sequences(V, len_, budget, recent):
+    """Several CTAs to a head, and runs that a CTA's shared memory does not hold."""
+    cols = -(-budget // 128)
+    c = R.make_case([len_, 700], [0, 0], 1, seed=98, spare=2 * cols)
+    used = set(c.table[c.table >= 0].tolist())
+    free = [p for p in range(len(c.sk)) if p not in used]
+    dst = torch.tensor(free[:2 * cols], dtype=torch.int32).view(2, cols)
+    g = torch.Generator().manual_seed(99)
+    weight = torch.rand((*c.sk.shape, 128), generator=g)
+    if recent == 0:
+        weight = (weight * 4).floor()      # mostly ties
+    kept = torch.full((2, 1, budget), -1, dtype=torch.int32)
+    cache, _ = c.on(V)
+    got_w, got_kept = weight.cuda(), kept.cuda()
+    new_len, _ = V.cache_evict(cache, got_w, dst.cuda(), budget, recent, kept=got_kept)
+    torch.cuda.synchronize()
+    ref_len = R.evict(c, weight, dst, budget, recent, kept)
+    assert torch.equal(new_len.cpu(), ref_len) and torch.equal(got_kept.cpu(), kept)
+    _same_codes(cache.k8, c.k8)
+    _same_codes(cache.v8, c.v8)
+    assert torch.equal(cache.sk.cpu(), c.sk) and torch.equal(got_w.cpu(), weight)
+
+
+def test_a_pool_beyond_32_bits(V):
+    """Pages whose codes lie more than 4 GB into the pool."""
+    c = R.make_case([330, 140], [10, 3], 1, seed=100, spare=4)
+    small, far = len(c.sk), 270000
+    cache, start = c.on(V)
+
+    def wide(x):
+        y = torch.zeros((far + small, *x.shape[1:]), dtype=x.dtype, device="cuda")
+        y[far:] = x
+        return y
+
+    table = torch.where(cache.table >= 0, cache.table + far, cache.table)
+    big = V.Cache(wide(cache.k8), wide(cache.v8), wide(cache.sk), wide(cache.sv), table, cache.length)
+    K, W, Q = R.rows(13, 1, 101), R.rows(13, 1, 102), R.rows(13, 2, 103)
+    V.cache_append(big, K.cuda(), W.cuda(), start)
+    R.append(c, K, W)
+    _same_codes(big.k8[far:], c.k8)
+    _same_codes(big.v8[far:], c.v8)
+    for rows in ([0, 10, 13], [0, 2, 3]):
+        c.start = torch.tensor(rows, dtype=torch.int32)
+        o, z, eo, el = R.attention(c, Q[:rows[2]])
+        out, lse = V.cache_attention(big, Q[:rows[2]].cuda(), c.start.cuda())
+        _within(out, o, eo, "O")
+        weight = torch.zeros((*big.sk.shape, 128), device="cuda")
+        V.cache_weigh(big, Q[:rows[2]].cuda(), c.start.cuda(), lse, weight)
+        w, e = R.weigh(c, Q[:rows[2]], lse.cpu(), torch.zeros((*c.sk.shape, 128)))
+        _within(weight[far:], w, e, "weight")
+    used = set(c.table[c.table >= 0].tolist())
+    dst = torch.tensor([p for p in range(small) if p not in used][:4], dtype=torch.int32).view(2, 2)
+    kept = torch.full((2, 1, 130), -1, dtype=torch.int32)
+    _, got_kept = V.cache_evict(big, weight, dst.cuda() + far, 130, 20)
+    w = weight[far:].cpu()
+    R.evict(c, w, dst, 130, 20, kept)
+    assert torch.equal(got_kept.cpu(), kept)
+    _same_codes(big.k8[far:], c.k8)
+    assert torch.equal(big.sv[far:].cpu(), c.sv)
+
+
+@pytest.mark.parametrize("news", [[1, 1, 1], [90, 40, 70]])
+def test_two_streams_at_once(V, news):
+    """Calls that overlap, each with a workspace of its own, do not disturb one another."""
+    cases = [R.make_case([9000, 300, 1200], news, 2, seed=s) for s in (104, 105)]
+    Q = [R.rows(sum(news), 8, seed=s).cuda() for s in (106, 107)]
+    on = [c.on(V) for c in cases]
+    alone = [V.cache_attention(cache, q, start) for (cache, start), q in zip(on, Q)]
+    weights = [torch.zeros((*c.sk.shape, 128), device="cuda") for c in cases]
+    for (cache, start), q, (_, lse), w in zip(on, Q, alone, weights):
+        V.cache_weigh(cache, q, start, lse, w)
+    streams = [torch.cuda.Stream() for _ in cases]
+    got, gw = [[] for _ in cases], [[] for _ in cases]
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for i, st in enumerate(streams):
+            with torch.cuda.stream(st):
+                cache, start = on[i]
+                got[i].append(V.cache_attention(cache, Q[i], start))
+                gw[i].append(torch.zeros_like(weights[i]))
+                V.cache_weigh(cache, Q[i], start, got[i][-1][1], gw[i][-1])
+    torch.cuda.synchronize()
+    for i in range(len(cases)):
+        for out, lse in got[i]:
+            assert torch.equal(out, alone[i][0]) and torch.equal(lse, alone[i][1])
+        for w in gw[i]:
+            assert torch.equal(w, weights[i])
+
+
+def test_an_eviction_replayed(V):
+    """A captured eviction replays with other lengths and weights."""
+    H, budget, recent = 2, 200, 30
+    c = R.make_case([700, 150], [0, 0], H, seed=108, spare=4)
+    used = set(c.table[c.table >= 0].tolist())
+    dst = torch.tensor([p for p in range(len(c.sk)) if p not in used][:4], dtype=torch.int32).view(2, 2)
+    cache, _ = c.on(V)
+    weight, got_dst = torch.zeros((*c.sk.shape, 128), device="cuda"), dst.cuda()
+    new_len = torch.empty(2, dtype=torch.int32, device="cuda")
+    kept = torch.empty((2, H, budget), dtype=torch.int32, device="cuda")
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        V.vca_cache_evict(cache, weight, got_dst, budget, recent, new_len, kept)
+    for i, lens in enumerate(([700, 150], [333, 1])):
+        w = torch.rand(weight.shape, generator=torch.Generator().manual_seed(109 + i))
+        c.length = torch.tensor(lens, dtype=torch.int32)
+        cache.length.copy_(c.length)
+        weight.copy_(w)
+        kept.fill_(-1)
+        graph.replay()
+        torch.cuda.synchronize()
+        ref = torch.full((2, H, budget), -1, dtype=torch.int32)
+        assert torch.equal(new_len.cpu(), R.evict(c, w, dst, budget, recent, ref))
+        assert torch.equal(kept.cpu(), ref)
+        _same_codes(cache.k8, c.k8)
+        assert torch.equal(weight.cpu(), w)
+
+
+@pytest.mark.parametrize("causal", [True, False])
+def test_pages_of_nan(V, causal):
+    """Whole pages of NaN keys: the call ends, and only rows that see them are NaN."""
+    for news in ([1, 1], [70, 200]):
+        c = R.make_case([500, 300], news, 2, seed=111)
+        Q = R.rows(sum(news), 4, seed=112)
+        o, z, eo, el = R.attention(c, Q, causal=causal)
+        c.k8[c.table[0, 1].long()] = 0x7F
+        n0 = news[0]
+        for cap in (0.0, 20.0):
+            cache, start = c.on(V)
+            out, lse = V.cache_attention(cache, Q.cuda(), start, causal=causal, softcap=cap)
+            assert bool(torch.isnan(out[:n0]).all()) and bool(torch.isnan(lse[:n0]).all())
+            if cap == 0.0:
+                _within(out[n0:], o[n0:], eo[n0:], "O")
+                _within(lse[n0:], z[n0:], el[n0:], "lse")
+            weight = torch.zeros((*c.sk.shape, 128), device="cuda")
+            V.cache_weigh(cache, Q.cuda(), start, z.float().cuda(), weight, causal=causal, softcap=cap)
+            page = c.table[0, 1].long()
+            assert bool(torch.isnan(weight[page]).all())
+            weight[page] = 0
+            assert bool(torch.isfinite(weight).all())
