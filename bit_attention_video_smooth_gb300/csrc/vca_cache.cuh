@@ -211,31 +211,42 @@ __device__ __forceinline__ float tanh_half(float u) {
 // The capped score in log2 units, cap_out tanh.
 __device__ __forceinline__ float capped(float u, float cap_out) { return cap_out * tanh_half(u); }
 
-// tanh_half(X c) in place for kN raw scores of every lane of a warp.  Scores are
-// mostly well below the cap: then the polynomial alone, in pairs, which needs no
-// reciprocal and no power of two (with those, whose units run at a quarter of
-// the multiply-adds' rate or less, they bound the kernels that cap).
-template <int kN>
-__device__ __forceinline__ void tanh_scores(uint32_t (&X)[kN], float c) {
-    float top = 0.0f;
+// 32 columns of TMEM and, in `m`, the largest magnitude among them, NaN apart.
+#define VCA_TMEM_LDTOP32(taddr, r, m)                                                                             \
+    asm volatile(                                                                                                 \
+        "tcgen05.ld.red.sync.aligned.32x32b.x32.max.abs.f32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,"  \
+        "%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, %32, [%33];"                       \
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),         \
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),   \
+          "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), \
+          "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31]), \
+          "=f"(m)                                                                                                 \
+        : "r"(taddr))
+
+// X = cap_out tanh_half(X c) + add in place for kN raw scores of every lane of a
+// warp; add(k): the terms of X[k], X[k + 1].  Scores are mostly well below the cap
+// (`near`: |X| c <= kTanhNear in all lanes): then the polynomial alone, in
+// pairs, without reciprocals and powers of two.
+template <int kN, typename Add>
+__device__ __forceinline__ void cap_scores(uint32_t (&X)[kN], float c, float cap_out, bool near, const Add &add) {
+    if (!near) {
 #pragma unroll
-    for (int k = 0; k < kN; k += 2)
-        top = fmaxf(top, fmaxf(fabsf(__uint_as_float(X[k])), fabsf(__uint_as_float(X[k + 1]))));
-    if (__any_sync(0xffffffffu, top * c > kTanhNear)) {
-#pragma unroll
-        for (int k = 0; k < kN; ++k) X[k] = __float_as_uint(tanh_half(__uint_as_float(X[k]) * c));
+        for (int k = 0; k < kN; k += 2) {
+            float a, b;
+            upk2(add(k), a, b);
+            X[k] = __float_as_uint(fmaf(tanh_half(__uint_as_float(X[k]) * c), cap_out, a));
+            X[k + 1] = __float_as_uint(fmaf(tanh_half(__uint_as_float(X[k + 1]) * c), cap_out, b));
+        }
         return;
     }
     auto both = [](float x) { return pk2(__float_as_uint(x), __float_as_uint(x)); };
+    const uint64_t t0 = both(cap_out * kT0), t1 = both(cap_out * kT1), t2 = both(cap_out * kT2), t3 = both(cap_out * kT3),
+                   t4 = both(cap_out * kT4);
 #pragma unroll
     for (int k = 0; k < kN; k += 2) {
         const uint64_t u = mul2(pk2(X[k], X[k + 1]), both(c)), w = mul2(u, u);
-        uint64_t q = fma2(both(kT4), w, both(kT3));
-        q = fma2(q, w, both(kT2));
-        q = fma2(q, w, both(kT1));
-        q = fma2(q, w, both(kT0));
         float a, b;
-        upk2(mul2(u, q), a, b);
+        upk2(fma2(u, fma2(fma2(fma2(fma2(t4, w, t3), w, t2), w, t1), w, t0), add(k)), a, b);
         X[k] = __float_as_uint(a);
         X[k + 1] = __float_as_uint(b);
     }

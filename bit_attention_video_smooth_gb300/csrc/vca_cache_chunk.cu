@@ -314,6 +314,7 @@ __device__ __forceinline__ void bulk_store_wait() {
 struct PageScore {
     float c, bias;       // no cap: p = 2^(S c + bias); cap: p = 2^(cap tanh_half(S c) + bias)
     float cap;           // cap log2(e)
+    bool near;           // the polynomial of the cap's tanh will do for the warp
     int lim;             // how many of the thread's 64 columns the row sees
     bool edge;           // some row of the warp does not see all
 };
@@ -322,14 +323,13 @@ struct PageScore {
 template <bool kCap>
 __device__ __forceinline__ void probabilities(uint32_t (&X)[32], const PageScore &s, int col0, uint64_t &l2,
                                               uint32_t (&W)[16]) {
-    if constexpr (kCap) tanh_scores(X, s.c);
-    const float c = kCap ? s.cap : s.c;
-    const uint64_t c2 = pk2(__float_as_uint(c), __float_as_uint(c));
+    const uint64_t c2 = pk2(__float_as_uint(s.c), __float_as_uint(s.c));
     const uint64_t b2 = pk2(__float_as_uint(s.bias), __float_as_uint(s.bias));
+    if constexpr (kCap) cap_scores(X, s.c, s.cap, s.near, [&](int) { return b2; });
 #pragma unroll
     for (int k = 0; k < 16; ++k) {
-        float a, b;
-        upk2(fma2(pk2(X[2 * k], X[2 * k + 1]), c2, b2), a, b);
+        float a = __uint_as_float(X[2 * k]), b = __uint_as_float(X[2 * k + 1]);
+        if constexpr (!kCap) upk2(fma2(pk2(X[2 * k], X[2 * k + 1]), c2, b2), a, b);
         a = ex2_approx(a);
         b = ex2_approx(b);
         if constexpr (kCap) {
@@ -651,11 +651,18 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint32_t X0[32], X1[32];
             tc_fence_after();
             float m0, m1;
-            VCA_TMEM_LDMAX32(tS + 64 * half, X0, m0);
-            VCA_TMEM_LDMAX32(tS + 64 * half + 32, X1, m1);
             const float4 slot = sSlot[b % kSlots];
             s.edge = b >= full || slot.x < 0.0f;
             s.c = fmaxf(__fmul_rn(f, slot.x), 0x1p-126f);      // above 0, so that -inf stays -inf
+            if constexpr (kCap) {
+                // loaded twice: the load's own maximum is cheaper than the thread's
+                VCA_TMEM_LDTOP32(tS + 64 * half, X0, m0);
+                VCA_TMEM_LDTOP32(tS + 64 * half + 32, X1, m1);
+                tmem_ld_wait();
+                s.near = __all_sync(0xffffffffu, fmaxf(m0, m1) * s.c <= kTanhNear);
+            }
+            VCA_TMEM_LDMAX32(tS + 64 * half, X0, m0);
+            VCA_TMEM_LDMAX32(tS + 64 * half + 32, X1, m1);
             tmem_ld_wait();
             if (s.edge) {
                 s.lim = slot.x < 0.0f ? 0 : seen - b * kBlk;

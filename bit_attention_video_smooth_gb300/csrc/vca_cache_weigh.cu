@@ -422,20 +422,17 @@ __device__ __forceinline__ void copy_factors(uint32_t taddr, uint32_t saddr) {
     asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(d) : "memory");
 }
 
-// The sum of 2^(S c + (-lse)) over kCols rows of S^T, S capped first where there
-// is a cap; `lse` their -lse as pairs.
+// The sum of 2^(S c + (-lse)) over kCols rows of S^T, S, none of them larger than
+// `top`, capped first where there is a cap; `lse` their -lse as pairs.
 template <int kCols, bool kCap, bool kEdge>
 __device__ __forceinline__ uint64_t sum_cols(uint32_t (&X)[kCols], float c, const uint64_t *lse, const int *seen, int key,
-                                             float cap_out, uint64_t sum2) {
-    if constexpr (kCap) {
-        tanh_scores(X, c);
-        c = cap_out;
-    }
+                                             float cap_out, float top, uint64_t sum2) {
+    if constexpr (kCap) cap_scores(X, c, cap_out, __all_sync(0xffffffffu, top * c <= kTanhNear), [&](int k) { return lse[k / 2]; });
     const uint64_t c2 = pk2(__float_as_uint(c), __float_as_uint(c));
 #pragma unroll
     for (int k = 0; k < kCols / 2; ++k) {
-        float a, b;
-        upk2(fma2(pk2(X[2 * k], X[2 * k + 1]), c2, lse[k]), a, b);
+        float a = __uint_as_float(X[2 * k]), b = __uint_as_float(X[2 * k + 1]);
+        if constexpr (!kCap) upk2(fma2(pk2(X[2 * k], X[2 * k + 1]), c2, lse[k]), a, b);
         a = ex2_approx(a);
         b = ex2_approx(b);
         if constexpr (kEdge) {
@@ -452,21 +449,25 @@ template <int N, bool kCap, bool kEdge>
 __device__ __forceinline__ float sum_row(uint32_t tS, float c, const uint64_t *lse, const int *seen, int key, float cap_out) {
     uint32_t X0[32];
     uint64_t sum2 = 0;
-    VCA_TMEM_LD32(tS, X0);
+    float top = 0.0f;
+    if constexpr (kCap)
+        VCA_TMEM_LDTOP32(tS, X0, top);
+    else
+        VCA_TMEM_LD32(tS, X0);
     if constexpr (N == 16) {
         tmem_ld_wait();
         uint32_t X[16];
 #pragma unroll
         for (int k = 0; k < 16; ++k) X[k] = __float_as_uint(__fadd_rn(__uint_as_float(X0[k]), __uint_as_float(X0[16 + k])));
-        sum2 = sum_cols<16, kCap, kEdge>(X, c, lse, seen, key, cap_out, sum2);
+        sum2 = sum_cols<16, kCap, kEdge>(X, c, lse, seen, key, cap_out, 2.0f * top, sum2);
     } else {
         uint32_t X1[32];
         tmem_ld_wait();
         if constexpr (!kCap) VCA_TMEM_LD32(tS + 32, X1);      // (a cap has no registers left for it)
-        sum2 = sum_cols<32, kCap, kEdge>(X0, c, lse, seen, key, cap_out, sum2);
-        if constexpr (kCap) VCA_TMEM_LD32(tS + 32, X1);
+        sum2 = sum_cols<32, kCap, kEdge>(X0, c, lse, seen, key, cap_out, top, sum2);
+        if constexpr (kCap) VCA_TMEM_LDTOP32(tS + 32, X1, top);
         tmem_ld_wait();
-        sum2 = sum_cols<32, kCap, kEdge>(X1, c, lse + 16, seen + 32, key, cap_out, sum2);
+        sum2 = sum_cols<32, kCap, kEdge>(X1, c, lse + 16, seen + 32, key, cap_out, top, sum2);
     }
     float a, b;
     upk2(sum2, a, b);
