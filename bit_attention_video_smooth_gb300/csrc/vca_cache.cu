@@ -161,7 +161,6 @@ __device__ __forceinline__ uint32_t weight_key(float w) {
 
 constexpr int kSelThreads = 1024;
 constexpr int kSelKeys = 40960;         // keys that a CTA can keep in shared memory
-constexpr int kCluster4Tokens = 16384;  // longer sequences take a cluster of four CTAs for each head
 
 __device__ __forceinline__ uint32_t cluster_rank() {
     uint32_t r;
@@ -467,7 +466,11 @@ cudaError_t launch_cache_evict(const CacheView &c, float *weight, const int32_t 
                                int recent, int32_t *new_len, int32_t *kept, int32_t *dev_status, cudaStream_t st) {
     const EvictParams p{c, weight, dst_table, dst_cols, budget, recent, new_len, kept, dev_status};
     const int64_t tokens = static_cast<int64_t>(c.cols) * kBlk;      // of a sequence, at most
-    const int parts = tokens > kCluster4Tokens ? 4 : 1;
+    // a cluster of four CTAs for each head where one CTA would not hold the keys, or
+    // where they are many and all clusters run at once (a CTA fills an SM): 2 x 8
+    // heads of 32,000 tokens 23 us against 39, of 8,000 18 against 17; 16 x 8 heads of
+    // 32,000 tokens 88 against 58, of 64,000 (past kSelKeys) 118 against 210
+    const int parts = tokens > kSelKeys || (tokens > 12288 && 4ll * c.B * c.H <= 152) ? 4 : 1;
     const int64_t run = (tokens + parts - 1) / parts + 32;
     const int keep = static_cast<int>(run < kSelKeys ? run : kSelKeys);
     const auto kernel = parts == 4 ? select_kernel<4> : select_kernel<1>;

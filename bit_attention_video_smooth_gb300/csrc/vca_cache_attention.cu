@@ -605,7 +605,7 @@ __global__ void __launch_bounds__(16 * kRows) combine_kernel(const AttnParams p,
 // CTAs of the decode kernel: one per SM, fewer where there cannot be work for
 // all; or one for each tile where caches are of at most kWholePages pages and
 // tiles few.
-constexpr int kWholePages = 8;
+constexpr int kWholePages = 6;
 struct Grid {
     int ctas;
     bool whole;

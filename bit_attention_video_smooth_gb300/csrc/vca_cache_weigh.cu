@@ -29,7 +29,7 @@ using namespace cache;
 
 constexpr uint32_t kTile = kBlk * kD;
 constexpr int kKP = 4;                       // pages of a unit
-constexpr int kKStages = 8, kSlots = 16;
+constexpr int kKStages = 8, kSlots = 32;
 constexpr int kSets = 2;                     // sets of four sum warps
 constexpr int kIssuers = 2;                  // MMA issuers, for the even and the odd pages of a unit
 constexpr int kThreads = 32 * (1 + kIssuers + 4 * kSets);
@@ -58,6 +58,16 @@ struct Layout {
     static constexpr uint32_t offMisc = offBar + bars * 8, smem = offMisc + 16 + 1024;
     static_assert(smem <= 232448, "shared memory budget");
     static_assert(tmem_sfb + 8 * qstages * kIssuers <= tmem_cols, "TMEM plan");
+    // The producer lists a unit's pages once every reader has left the unit qstages before the last one
+    static_assert(kSlots >= (qstages + 1) * kKP, "page slots");
+    // S^T buffers: of 16 rows every issuer and its set of sum warps have a ring of
+    // their own; of 128 one ring serves both issuers, and one may come to a buffer
+    // before the other has used it.  It has waited for its page two before, or else
+    // for the tile's q_full, which tells that the tile qstages before is summed up: at
+    // most max(sbufs + 1, (qstages - 1) kKP + 1) uses are not, which must be fewer than
+    // two rounds for the barrier's parity to be unambiguous.
+    static constexpr int ring = N == 128 ? sbufs : sbufs / kIssuers;
+    static_assert(N == 16 || (sbufs + 1 < 2 * ring && (qstages - 1) * kKP + 1 < 2 * ring), "S^T buffers");
 };
 
 struct WeighParams {
@@ -85,13 +95,19 @@ template <int N>
 __device__ __forceinline__ Work work_of(const AttnParams &p, int b) {
     return work_of<N>(p, load_seq(p.c, p.start, p.T, b));
 }
-// The first tile with a row that sees a page: with x = 128 page - (len - n), a
-// causal row sees it when its token is at least the x-th new one.
+// The first tile with a row that sees page j: with c = len - n, a causal row sees
+// it when its token is at least the (128 j - c)-th new one, so its row at least
+// G (128 j - c) and its tile floor of that by N = 128 j G / N - ceil(c G / N).
+template <int N>
+__device__ __forceinline__ int64_t hidden_tiles(const AttnParams &p, const Seq &s) {      // ceil(c G / N)
+    const int64_t r = static_cast<int64_t>(s.len - s.n) * p.G;
+    return r >= 0 ? (r + N - 1) / N : -(-r / N);
+}
 template <int N>
 __device__ __forceinline__ int first_tile(const AttnParams &p, const Seq &s, int page) {
     if (!p.causal) return 0;
-    const int64_t x = static_cast<int64_t>(page) * kBlk - (s.len - s.n);
-    return x <= 0 ? 0 : static_cast<int>(x * p.G / N);
+    const int64_t t = static_cast<int64_t>(page) * (kBlk / N) * p.G - hidden_tiles<N>(p, s);
+    return static_cast<int>(t > 0 ? t : 0);
 }
 
 // How many of `count` pages from `page` on the rows of a tile see.
@@ -112,32 +128,37 @@ __device__ __forceinline__ int64_t scan64(int64_t v) {
     return v;
 }
 
-// Tiles that the pages [0, upto) of one head take, or with `find` >= 0 the first
-// page before which at least `find` tiles lie.  A warp's work.
+// Tiles of work in the pages [0, upto) of one head: upto * tiles less what
+// first_tile leaves out, an arithmetic series.  Of few rows all tiles count for
+// every page: but for the last pages they do.
 template <int N>
-__device__ int64_t head_cost(const AttnParams &p, const Work &w, int64_t find, int &page) {
-    if (!p.causal || N == 16) {
-        // few rows: the last page alone may be seen by fewer tiles
-        if (find >= 0) page = w.tiles ? static_cast<int>((find + w.tiles - 1) / w.tiles) : 0;
-        return static_cast<int64_t>(w.tiles) * w.pages;
+struct Cost {
+    int64_t tiles, hidden, from;      // from: the first page that leaves some out
+    int G;
+    bool even;
+    __device__ Cost(const AttnParams &p, const Work &w) : tiles(w.tiles), hidden(0), from(0), G(p.G), even(N == 16 || !p.causal) {
+        if (even) return;
+        hidden = hidden_tiles<N>(p, w.s);
+        from = hidden >= 0 ? hidden / G + 1 : 0;
     }
-    int64_t sum = 0;
-    for (int j0 = 0; j0 < w.pages; j0 += 32) {
-        const int j = j0 + static_cast<int>(threadIdx.x & 31);
-        const int64_t c = j < w.pages ? w.tiles - first_tile<N>(p, w.s, j) : 0;
-        const int64_t incl = scan64(c) + sum;
-        if (find >= 0) {
-            const uint32_t hit = __ballot_sync(0xffffffffu, j < w.pages && incl - c >= find);
-            if (hit) {
-                page = j0 + __ffs(hit) - 1;
-                return 0;
-            }
+    __device__ int64_t before(int64_t upto) const {
+        const int64_t m = even ? 0 : upto - from;
+        return upto * tiles - (m > 0 ? G * (m * (from + upto - 1) / 2) - hidden * m : 0);
+    }
+    // The first page before which at least `find` tiles lie.
+    __device__ int page_at(int64_t find, int pages) const {
+        if (even) return static_cast<int>((find + tiles - 1) / tiles);
+        int lo = 0, hi = pages;
+        while (lo < hi) {
+            const int mid = lo + (hi - lo) / 2;
+            if (before(mid) >= find)
+                hi = mid;
+            else
+                lo = mid + 1;
         }
-        sum = __shfl_sync(0xffffffffu, incl, 31);
+        return lo;
     }
-    page = w.pages;
-    return sum;
-}
+};
 
 // Place in the list of (sequence, head, page).
 struct Place {
@@ -145,30 +166,19 @@ struct Place {
     int64_t at;          // its place among its sequence's H * pages
     int b, tile0;        // the sequence, the tiles of those before
 };
-// The first place before which at least `pos` tiles of work lie: 32 sequences
-// at a time, one per lane, or one by one where their pages cost differently.
+// The first place before which at least `pos` tiles of work lie (a warp's work).
 template <int N>
 __device__ Place find_place(const AttnParams &p, int64_t pos) {
     Place r{};
-    const bool even = !p.causal || N == 16;
-    const int lane = threadIdx.x & 31, step = even ? 32 : 1;
-    int page = 0;
     bool more = true;
-    for (int b0 = 0; more; b0 += step) {
+    for (int b0 = 0; more; b0 += 32) {
         Seq s;
-        if (even) {
-            more = load_seqs(p.c, p.start, p.T, b0, s);
-        } else {
-            s = load_seq(p.c, p.start, p.T, b0);
-            more = !s.falls && b0 + 1 < p.c.B;
-        }
+        more = load_seqs(p.c, p.start, p.T, b0, s);
         Work w = work_of<N>(p, s);
-        int64_t c = head_cost<N>(p, w, -1, page);
-        const bool counts = even || lane == 0;
-        const int64_t cost = counts ? c * p.c.H : 0, pages = counts ? static_cast<int64_t>(p.c.H) * w.pages : 0;
-        const int64_t tiles = counts ? w.tiles : 0;
+        const int64_t cost = Cost<N>(p, w).before(w.pages) * p.c.H, pages = static_cast<int64_t>(p.c.H) * w.pages;
+        const int64_t tiles = w.tiles;
         const int64_t ci = scan64(cost), pi = scan64(pages), ti = scan64(tiles);
-        const uint32_t hit = __ballot_sync(0xffffffffu, counts && pos < ci);
+        const uint32_t hit = __ballot_sync(0xffffffffu, pos < ci);
         if (hit) {
             const int l = __ffs(hit) - 1;
             r.b = b0 + l;
@@ -176,10 +186,9 @@ __device__ Place find_place(const AttnParams &p, int64_t pos) {
             r.linear += __shfl_sync(0xffffffffu, pi - pages, l);
             const int64_t rest = pos - __shfl_sync(0xffffffffu, ci - cost, l);
             w = work_of<N>(p, r.b);
-            c = __shfl_sync(0xffffffffu, c, l);
-            const int64_t h = rest / c;
-            head_cost<N>(p, w, rest - h * c, page);
-            r.at = h * w.pages + page;
+            const Cost<N> head(p, w);
+            const int64_t one = head.before(w.pages), h = rest / one;
+            r.at = h * w.pages + head.page_at(rest - h * one, w.pages);
             r.linear += r.at;
             if (r.at == static_cast<int64_t>(p.c.H) * w.pages) {
                 r.tile0 += w.tiles;
@@ -198,24 +207,15 @@ __device__ Place find_place(const AttnParams &p, int64_t pos) {
 template <int N>
 __device__ int64_t all_work(const AttnParams &p) {
     int64_t sum = 0;
-    int page;
     bool more = true;
-    if (!p.causal || N == 16) {
-        for (int b0 = 0; more; b0 += 32) {
-            Seq s;
-            more = load_seqs(p.c, p.start, p.T, b0, s);
-            const Work w = work_of<N>(p, s);
-            sum += static_cast<int64_t>(w.tiles) * w.pages;
-        }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    } else {
-        for (int b = 0; more; ++b) {
-            const Work w = work_of<N>(p, b);
-            sum += head_cost<N>(p, w, -1, page);
-            more = !w.s.falls && b + 1 < p.c.B;
-        }
+    for (int b0 = 0; more; b0 += 32) {
+        Seq s;
+        more = load_seqs(p.c, p.start, p.T, b0, s);
+        const Work w = work_of<N>(p, s);
+        sum += Cost<N>(p, w).before(w.pages);
     }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
     return sum * p.c.H;
 }
 
@@ -589,7 +589,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // ------------------------------------------------------------ MMA issuers
         // one thread each: issuing costs more than the tensor core takes
         if (lane == 0) {
-            const int odd = warp - 1;
+            const int odd = warp - 1, sb0 = N == 128 ? 0 : odd * L::ring;
             const uint32_t sbase = smem_u32(smem), tsfa = tmem + L::tmem_sfa;
             bool ok = true;
             int kn = 0, qs = 0, sb = 0;
@@ -606,17 +606,18 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if constexpr (N == 128) copy_factors(tsf + 4, img + Image<N>::sf + 512);
                     const uint64_t dh = sdesc_k_sw128(img), dl = sdesc_k_sw128(img + Image<N>::lo);
                     for (int j = 0; j < np; ++j) {
-                        if ((j & 1) == odd) {
+                        const bool mine = (j & 1) == odd;
+                        if (mine) {
                             const int st = (kn + j) % kKStages;
                             if (j >= landed) {
                                 ok = mbar_wait_spin(k_full + st, ((kn + j) / kKStages) & 1, abort_flag, p.limit_ns);
                                 landed = j + 1;
                             }
-                            ok = ok && mbar_wait_spin(s_empty + sb, sphase, abort_flag, p.limit_ns);
+                            ok = ok && mbar_wait_spin(s_empty + sb0 + sb, sphase, abort_flag, p.limit_ns);
                             if (!ok) break;
                             tc_fence_after();
                             const uint64_t dk = sdesc_k_sw128(sbase + st * kTile);
-                            const uint32_t d = tmem + sb * L::cols;
+                            const uint32_t d = tmem + (sb0 + sb) * L::cols;
 #pragma unroll
                             for (int i = 0; i < 4; ++i)
                                 mma_mxf8_ss(d, dk + 2 * i, dh + 2 * i, make_idesc_mxf8_b(128, L::cols, i), tsfa, tsf, i > 0);
@@ -625,11 +626,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 for (int i = 0; i < 4; ++i)
                                     mma_mxf8_ss(d, dk + 2 * i, dl + 2 * i, make_idesc_mxf8_b(128, L::cols, i), tsfa, tsf + 4, 1u);
                             }
-                            tc_commit(s_full + sb);
-                            mbar_arrive(s_full + sb);
+                            tc_commit(s_full + sb0 + sb);
+                            mbar_arrive(s_full + sb0 + sb);
                             if (t + 1 == wk.w.tiles) tc_commit(k_empty + st);
                         }
-                        if (++sb == L::sbufs) {
+                        if ((N == 128 || mine) && ++sb == L::ring) {
                             sb = 0;
                             sphase ^= 1;
                         }
@@ -653,7 +654,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // take more of its bandwidth than the products do); 16 rows: every other page
         const int set = (warp - 1 - kIssuers) >> 2, quarter = warp & 3, row = quarter * 32 + lane;
         constexpr int kCols = N == 128 ? 64 : 16;
-        const int col0 = N == 128 ? 64 * set : 0;
+        const int col0 = N == 128 ? 64 * set : 0, sb0 = N == 128 ? 0 : set * L::ring;
         const uint32_t tl = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + col0;
         const float c0 = kCap ? p.cap_in : p.scale_log2;
         float *sSum = reinterpret_cast<float *>(smem + L::offSum);
@@ -681,13 +682,13 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                 for (int j = 0; j < kKP; ++j) {
                     if (!ok || j >= np) break;
-                    const int sb = next_sb;
+                    if (N == 16 && (j & 1) != set) continue;
+                    const int sb = sb0 + next_sb;
                     const uint32_t phase = next_phase;
-                    if (++next_sb == L::sbufs) {
+                    if (++next_sb == L::ring) {
                         next_sb = 0;
                         next_phase ^= 1;
                     }
-                    if (N == 16 && (j & 1) != set) continue;
                     ok = __all_sync(0xffffffffu, mbar_wait(s_full + sb, phase, abort_flag, p.limit_ns));
                     if (!ok) break;
                     tc_fence_after();
@@ -739,8 +740,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (threadIdx.x == 0 && *reinterpret_cast<volatile int *>(abort_flag)) report(p.dev_status, kErrTimeout);
 }
 
-// Tiles of 16 rows where a sequence and KV head have no more than that on average.
-bool few_rows(int T, int Hq, int H, int B) { return static_cast<int64_t>(T) * (Hq / H) <= 16ll * B; }
+// Tiles of 16 rows where a sequence and KV head have at most 32 on average: a
+// tile of 128 takes the products of 128 rows however many it has.  16 x 8 heads of
+// 8,000 tokens, 16 rows each: 34 us against 56; 32 rows 54 against 57; 48 rows
+// 73 against 58.
+bool few_rows(int T, int Hq, int H, int B) { return static_cast<int64_t>(T) * (Hq / H) <= 32ll * B; }
 int64_t tiles_at_most(int T, int Hq, int H, int B) {
     return static_cast<int64_t>(T) * (Hq / H) / (few_rows(T, Hq, H, B) ? 16 : 128) + (B < T ? B : T);
 }

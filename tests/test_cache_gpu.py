@@ -678,3 +678,23 @@ def test_pages_of_nan(V, causal):
             assert bool(torch.isnan(weight[page]).all())
             weight[page] = 0
             assert bool(torch.isfinite(weight).all())
+
+
+@pytest.mark.parametrize("pages", [1, 3, 8, 19])
+def test_weights_of_ragged_rows(V, pages):
+    """Few rows on average, several hundred of some sequences: many tiles of 16 rows to a page."""
+    for news in ([12] * 4 + [1] * 12, [60] + [1] * 15, [30, 2, 30] + [1] * 13):
+        lens = [pages * 128 - 11 * (b % 7) for b in range(16)]
+        c = R.make_case(lens, news, 2, seed=113)
+        Q = R.rows(sum(news), 16, seed=114)
+        for causal in (True, False):
+            _, z, _, _ = R.attention(c, Q, causal=causal)
+            w, e = R.weigh(c, Q, z.float(), torch.zeros((*c.sk.shape, 128)), causal=causal)
+            cache, start = c.on(V)
+            for _ in range(5):
+                status = torch.zeros(1, dtype=torch.int32, device="cuda")
+                weight = torch.zeros((*c.sk.shape, 128), device="cuda")
+                V.cache_weigh(cache, Q.cuda(), start, z.float().cuda(), weight, causal=causal, dev_status=status)
+                torch.cuda.synchronize()
+                assert int(status) == 0
+                _within(weight, w, e, "weight")
