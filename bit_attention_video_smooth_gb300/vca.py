@@ -375,12 +375,12 @@ def _typed(where, name, t, dtype, shape):
         raise ValueError(f"{where}: {name} must be contiguous")
 
 
-def _cache_call(where, cache: Cache, rows, others, start=None):
+def _cache_call(where, cache: Cache, rows, others, start=None, ws=None):
     """Checks a call's tensors and returns the C struct and the device: every
     tensor of the types and shapes of include/vca.h, all on one CUDA device.
     `rows` are (name, tensor, heads) of [T, heads, 128] bf16 with contiguous
-    channels, `others` (name, tensor, dtype, shape), the tensor or the shape
-    None where there is nothing to check."""
+    channels, `others` (name, tensor, dtype, shape), the tensor None where it is
+    not given; `ws` is a workspace or None."""
     k8, v8, sk, sv, table, length = cache.k8, cache.v8, cache.sk, cache.sv, cache.table, cache.length
     if k8.dim() != 4 or table.dim() != 2:
         raise ValueError(f"{where}: k8 must be [pages, H, 128, 128] and table [B, cols]")
@@ -393,11 +393,27 @@ def _cache_call(where, cache: Cache, rows, others, start=None):
     if start is not None:
         seen.append(("start", start, torch.int32, (B + 1,)))
     seen += [x for x in others if x[1] is not None]
+    # a launch of a few microseconds waits for these checks: all at once, and by name only where one fails
+    dev = k8.get_device()
+    ok = dev >= 0 and (ws is None or (ws.get_device() == dev and ws.is_contiguous()))
+    for _, t, dtype, shape in seen:
+        ok = ok and t.dtype is dtype and t.shape == shape and t.get_device() == dev and t.is_contiguous()
+    T = rows[0][1].shape[0] if rows and rows[0][1].dim() else 0
+    for _, t, heads in rows:
+        ok = ok and t.dtype is torch.bfloat16 and t.shape == (T, heads, 128) and t.stride(2) == 1 and t.get_device() == dev
+    if not ok:
+        _refuse(where, k8, seen, rows, ws)
+    s = _CacheStruct(k8.data_ptr(), v8.data_ptr(), sk.data_ptr(), sv.data_ptr(), table.data_ptr(), length.data_ptr(),
+                     pages, H, 128, B, cols)
+    return s, dev
+
+
+def _refuse(where, k8, seen, rows, ws):
+    """Names the first tensor of a call that is not as it must be."""
     for name, t, dtype, shape in seen:
-        if shape is not None:
-            _typed(where, name, t, dtype, shape)
-        elif not t.is_contiguous():
-            raise ValueError(f"{where}: {name} must be contiguous")
+        _typed(where, name, t, dtype, shape)
+    if ws is not None and not ws.is_contiguous():
+        raise ValueError(f"{where}: ws must be contiguous")
     T = None
     for name, t, heads in rows:
         shape = t.shape
@@ -408,21 +424,19 @@ def _cache_call(where, cache: Cache, rows, others, start=None):
         if T is not None and shape[0] != T:
             raise ValueError(f"{where}: {name} has {shape[0]} rows, not {T}")
         T = shape[0]
-    dev = k8.device
-    for name, t, *_ in seen + list(rows):
-        if t.device != dev or not t.is_cuda:
-            if not t.is_cuda:
-                raise ValueError(f"{where}: {name} is not a CUDA tensor")
-            raise ValueError(f"{where}: tensors on several devices: {name} on {t.device}, k8 on {dev}")
-    s = _CacheStruct(k8.data_ptr(), v8.data_ptr(), sk.data_ptr(), sv.data_ptr(), table.data_ptr(), length.data_ptr(),
-                     pages, H, 128, B, cols)
-    return s, dev
+    named = [x[:2] for x in (*seen, *rows)] + ([("ws", ws)] if ws is not None else [])
+    for name, t in named:
+        if not t.is_cuda:
+            raise ValueError(f"{where}: {name} is not a CUDA tensor")
+        if t.device != k8.device:
+            raise ValueError(f"{where}: tensors on several devices: {name} on {t.device}, k8 on {k8.device}")
+    raise ValueError(f"{where}: tensors that do not fit together")
 
 
 def _launch(where, dev, fn, *args, stream=None):
-    """fn(*args, stream) with `dev` current, on its current stream unless one is given."""
-    raw = torch._C._cuda_getCurrentRawStream(dev.index) if stream is None else stream.cuda_stream
-    if torch.cuda.current_device() == dev.index:
+    """fn(*args, stream) with device `dev` current, on its current stream unless one is given."""
+    raw = torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+    if torch._C._cuda_getDevice() == dev:
         st = fn(*args, raw)
     else:
         with torch.cuda.device(dev):
@@ -448,7 +462,7 @@ def vca_cache_attention(cache: Cache, Q, start, causal: int, softmax_scale: floa
     T, Hq = (Q.shape[0], Q.shape[1]) if Q.dim() == 3 else (0, 0)
     s, dev = _cache_call("vca_cache_attention", cache, (("Q", Q, Hq),),
                          (("O", O, torch.bfloat16, (T, Hq, 128)), ("lse", lse, torch.float32, (T, Hq)),
-                          ("ws", ws, None, None), ("dev_status", dev_status, torch.int32, (1,))), start)
+                          ("dev_status", dev_status, torch.int32, (1,))), start, ws)
     _launch("vca_cache_attention", dev, _lib.vca_cache_attention, s, Q.data_ptr(), Q.stride(0), Q.stride(1),
             start.data_ptr(), T, Hq, int(causal), softmax_scale, softcap, O.data_ptr(), _at(lse), _at(ws),
             0 if ws is None else ws.numel() * ws.element_size(), _at(dev_status), stream=stream)
@@ -460,7 +474,7 @@ def vca_cache_weigh(cache: Cache, Q, start, causal: int, softmax_scale: float, s
     s, dev = _cache_call("vca_cache_weigh", cache, (("Q", Q, Hq),),
                          (("lse", lse, torch.float32, (T, Hq)),
                           ("weight", weight, torch.float32, (*cache.sk.shape, 128)),
-                          ("ws", ws, None, None), ("dev_status", dev_status, torch.int32, (1,))), start)
+                          ("dev_status", dev_status, torch.int32, (1,))), start, ws)
     _launch("vca_cache_weigh", dev, _lib.vca_cache_weigh, s, Q.data_ptr(), Q.stride(0), Q.stride(1), start.data_ptr(),
             T, Hq, int(causal), softmax_scale, softcap, lse.data_ptr(), weight.data_ptr(), _at(ws),
             0 if ws is None else ws.numel() * ws.element_size(), _at(dev_status), stream=stream)
