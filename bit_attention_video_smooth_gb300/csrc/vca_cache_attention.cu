@@ -20,8 +20,7 @@
 // loaded two batches ahead, since a load under full traffic takes longer than a
 // page.  Eight consumer warps take 16 keys of every page each, with a running
 // maximum, sum and O of their own, which they merge at a tile's end: no barrier
-// but the ring's in between.  (Sixteen rows of a tile, by two such MMAs a
-// fragment, took 1.6 times as long as eight, and the tensor core's kernel less.)
+// but the ring's in between.
 //
 // Both products are m16n8k16 MMAs on fp16 with the long side as rows, so that
 // eight query rows fill a tile: S^T = K Q^T (16 keys x 8 rows), then O^T = V^T P^T
@@ -30,6 +29,11 @@
 // query row after a power-of-two scaling that puts its largest element at 2^13
 // (elements below 2^-30 of it lose bits); P is rounded to fp16 (2^-12
 // relative), while l sums the unrounded values.
+//
+// One token for each of 32 sequences of up to 32,768 tokens, 40 heads over 8: 190
+// us, 6.4 TB/s (0.94 of a copy); for one of 131,072 tokens with 40 KV heads 207 us,
+// 6.5 TB/s.  A tile's issue slots are 37 % used, so that capped scores cost
+// 9 us of the 190 more.
 #include "vca_attention_common.cuh"
 #include "vca_cache.cuh"
 
@@ -604,7 +608,8 @@ __global__ void __launch_bounds__(16 * kRows) combine_kernel(const AttnParams p,
 
 // CTAs of the decode kernel: one per SM, fewer where there cannot be work for
 // all; or one for each tile where caches are of at most kWholePages pages and
-// tiles few.
+// tiles few.  8 heads of one sequence: 500 tokens 7.3 us whole, 7.9 cut; 1,000
+// tokens 9.5 whole, 8.5 cut; of eight sequences 7.3 and 8.7, 9.7 and 9.8.
 constexpr int kWholePages = 6;
 struct Grid {
     int ctas;
@@ -619,7 +624,9 @@ Grid grid_of(int T, int Hq, int H, int B, int cols) {
 }
 
 // More than a tile of rows a sequence and KV head on average: the tensor core
-// kernel's tiles of 128 rows.
+// kernel's tiles of 128 rows.  16 x 8 heads of 8,000 tokens: 8 rows 50 us here, 70
+// there; 16 rows 88 here, 70 there; 32 rows 159 and 72.  (Tiles of 16 rows, by
+// two MMAs a fragment, took 1.6 times as long as tiles of eight.)
 bool many_rows(int T, int Hq, int H, int B) { return static_cast<int64_t>(T) * (Hq / H) > static_cast<int64_t>(kRows) * B; }
 
 }  // namespace

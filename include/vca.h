@@ -267,13 +267,16 @@ void vca_set_wait_limit_ns(uint64_t limit_ns);
  * (multiples of 8; the d channels lie together), so views of a fused
  * projection need no copy.  T = 0 returns VCA_OK and launches nothing.
  *
- * What lies on the device is checked there: a sequence whose start or len is
- * out of range (start not rising within 0 .. T, len above cols*128) counts as
- * having no rows, a page outside 0 .. pages - 1 as holding no tokens, and
- * dev_status (optional, device int32) is set to VCA_ERR_INVALID_ARG, or to
- * VCA_ERR_TIMEOUT if a bounded wait ran out; it is left untouched otherwise.
+ * What lies on the device is checked there: a sequence whose len is out of
+ * range (above cols*128 or negative) counts as having no rows, and so do a
+ * sequence whose start is (not rising within 0 .. T) and all sequences behind it;
+ * a page outside 0 .. pages - 1 counts as holding no tokens; and dev_status
+ * (optional, device int32) is set to VCA_ERR_INVALID_ARG, or to VCA_ERR_TIMEOUT if
+ * a bounded wait ran out; it is left untouched otherwise.  Scales are trusted to
+ * be powers of two.
  * Calls keep nothing between them: a workspace may be used by any call that
  * does not overlap with this one, and the calls can be captured into a graph.
+ * Outputs and workspace must not overlap the inputs.
  */
 typedef struct {
     uint8_t *k8, *v8;
@@ -283,8 +286,8 @@ typedef struct {
 } vca_cache;
 
 /* Scratch bytes for VCA_OP_CACHE_ATTENTION or VCA_OP_CACHE_WEIGH of T rows with
- * Hq query heads over H KV heads, B sequences and `cols` table columns (0 if
- * none, and for invalid sizes). */
+ * Hq query heads over H KV heads, B sequences and `cols` table columns (0 for
+ * invalid sizes).  The workspace is 16-byte aligned; nothing has to be in it. */
 size_t vca_cache_workspace_bytes(int op, int T, int Hq, int H, int B, int cols);
 
 /*
@@ -307,11 +310,15 @@ int vca_cache_append(const vca_cache *cache, const uint16_t *K, int64_t k_token,
  *   j visible to row i: j < len, and with causal = 1: j <= len - n + i
  *   O_i = sum_j softmax_j(s_ij) v_j sv,  lse_i = ln sum_j exp(s_ij)
  * A row that sees nothing gets O = 0 and lse = -inf.  softmax_scale <= 0 selects
- * 1/sqrt(d).  O is bf16 [T][Hq][d] and lse fp32 [T][Hq] (may be NULL), both
- * contiguous.  Products are exact, sums and statistics fp32; the probabilities
- * enter the second product as fp16.  A slot behind len may hold any bytes; a
- * NaN among the values of a sequence may reach every row of that sequence.
- * Equal calls give equal bits.
+ * 1/sqrt(d); softcap = 0 caps nothing, and softcap and softmax_scale / softcap have
+ * to be below 8.5e37.  O is bf16 [T][Hq][d] and lse fp32 [T][Hq] (may be NULL), both
+ * contiguous.  The products are exact but for query elements far below the
+ * largest of their row (2^-30 of it) or of their 32 channels (2^-15, off by 2^-22 of
+ * the largest, where a sequence has many rows); sums and statistics are fp32, the
+ * probabilities enter the second product as fp16 (2^-12 relative, nothing below
+ * 2^-25 of the row's largest).  A slot behind len may hold any bytes; a NaN among
+ * the values of a sequence may reach every row of that sequence, one in a query
+ * row, or an infinity, only that row.  Equal calls give equal bits.
  */
 int vca_cache_attention(const vca_cache *cache, const uint16_t *Q, int64_t q_token, int64_t q_head,
                         const int32_t *start, int T, int Hq, int causal, float softmax_scale, float softcap,
@@ -321,8 +328,9 @@ int vca_cache_attention(const vca_cache *cache, const uint16_t *Q, int64_t q_tok
  * vca_cache_weigh -- adds to weight, fp32 [pages][H][128], what each cached token
  * received from the rows Q: weight[page][h][slot] += sum over the rows i and the
  * G query heads of KV head h, where the token is visible, of exp(s_ij - lse_i),
- * with s, visibility and lse [T][Hq] those of vca_cache_attention.  Sequences
- * that share a page add to it in any order.
+ * with s, visibility and lse [T][Hq] those of vca_cache_attention.  A key's sum
+ * over the rows of one sequence has a fixed order and is added once (weight is
+ * 16-byte aligned); sequences that share a page add to it in any order.
  */
 int vca_cache_weigh(const vca_cache *cache, const uint16_t *Q, int64_t q_token, int64_t q_head, const int32_t *start,
                     int T, int Hq, int causal, float softmax_scale, float softcap, const float *lse, float *weight,
