@@ -211,7 +211,7 @@ __device__ __forceinline__ float tanh_half(float u) {
 // The capped score in log2 units, cap_out tanh.
 __device__ __forceinline__ float capped(float u, float cap_out) { return cap_out * tanh_half(u); }
 
-// 32 columns of TMEM and, in `m`, the largest magnitude among them, NaN apart.
+// 32 (16) columns of TMEM and, in `m`, the largest magnitude among them, NaN apart.
 #define VCA_TMEM_LDTOP32(taddr, r, m)                                                                             \
     asm volatile(                                                                                                 \
         "tcgen05.ld.red.sync.aligned.32x32b.x32.max.abs.f32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,"  \
@@ -220,6 +220,15 @@ __device__ __forceinline__ float capped(float u, float cap_out) { return cap_out
           "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),   \
           "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), \
           "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31]), \
+          "=f"(m)                                                                                                 \
+        : "r"(taddr))
+
+#define VCA_TMEM_LDTOP16(taddr, r, m)                                                                             \
+    asm volatile(                                                                                                 \
+        "tcgen05.ld.red.sync.aligned.32x32b.x16.max.abs.f32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,"  \
+        "%15}, %16, [%17];"                                                                                       \
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),         \
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),   \
           "=f"(m)                                                                                                 \
         : "r"(taddr))
 

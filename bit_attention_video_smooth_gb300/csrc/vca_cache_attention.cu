@@ -624,9 +624,9 @@ Grid grid_of(int T, int Hq, int H, int B, int cols) {
 }
 
 // More than a tile of rows a sequence and KV head on average: the tensor core
-// kernel's tiles of 128 rows.  16 x 8 heads of 8,000 tokens: 8 rows 50 us here, 70
-// there; 16 rows 88 here, 70 there; 32 rows 159 and 72.  (Tiles of 16 rows, by
-// two MMAs a fragment, took 1.6 times as long as tiles of eight.)
+// kernel.  16 x 8 heads of 8,000 tokens: 8 rows 50 us here, 66 there; 16 rows 88
+// here, 67 there; 32 rows 159 and 68.  (Tiles of 16 rows, by two MMAs a fragment,
+// took 1.6 times as long as tiles of eight.)
 bool many_rows(int T, int Hq, int H, int B) { return static_cast<int64_t>(T) * (Hq / H) > static_cast<int64_t>(kRows) * B; }
 
 }  // namespace

@@ -2,8 +2,8 @@
 // chunk of frames, a prompt), bound by the tensor cores: 4 rows keys d flops.
 // The mathematics is vca_cache_attention.cu's.
 //
-// One CTA takes 128 query rows of a (sequence, KV head) -- rows i G + g: the G
-// query heads that share the KV head are rows of one tile, so its codes are
+// One CTA takes a tile of 128 query rows of a (sequence, KV head) -- rows i G + g:
+// the G query heads that share the KV head are rows of one tile, so its codes are
 // read once for all of them -- and a run of the pages they see: all of them, or
 // an even part where there are too few tiles to fill the GPU (then a last
 // kernel joins the parts).  A first kernel lays out every tile's queries as the
@@ -28,6 +28,11 @@
 // brings the factors back: exact for elements above 2^-15 of the largest of
 // their 32, off by less than 2^-22 of it below.  Two FP8 products cost what one
 // 16-bit product does, and K needs no conversion (V's is 10 % of the time).
+// Few rows (tiles of N = 32): the 128 rows of the product are four copies of the
+// tile's, and each copy takes the probabilities of a quarter of every page's
+// keys, the other keys' being zeros to it: its warps then have 16 scores a thread
+// instead of 64, and none of them idles.  The copies have statistics and O of
+// their own, which are put together at the end like parts of a tile.
 // PV: P as fp16 (TMEM) times V as fp16: exact codes times a power of two, the
 // page's scale relative to a reference scale that moves, with O, only when a
 // page's lies outside [2^-15, 2^7] of it.
@@ -42,7 +47,8 @@
 // Measured and not kept: P in columns of its own, with Q's lo in shared memory
 // (1,030 us); one persistent CTA per SM with equal runs of pages (1,016; prompts
 // 513); probabilities before the halves' maxima meet (1,236); one issuer (1,066
-// against 988 at the time).
+// against 988 at the time).  Few rows: 8 sequences of up to 16,383 tokens, 5 rows
+// each, 40 heads over 8, capped: 63 us (92 in tiles of 128), 2.7 TB/s.
 #include "vca_attention_common.cuh"
 #include "vca_cache.cuh"
 
@@ -53,7 +59,7 @@ namespace {
 using namespace attn;
 using namespace cache;
 
-constexpr int kRows = 128;
+constexpr int kLanes = 128;                      // rows of an MMA
 constexpr int kKStages = 3, kVStages = 3, kWStages = 2, kSlots = 16;
 constexpr int kConvWarps = 4, kConvWarp0 = 4, kSoftWarp0 = 8;
 constexpr int kThreads = 32 * (kSoftWarp0 + kSoftmaxWarps);
@@ -68,15 +74,17 @@ constexpr uint32_t kOffV = kOffK + kKStages * kTile;
 constexpr uint32_t kOffW = kOffV + kVStages * kTile;
 constexpr uint32_t kOffSlot = kOffW + kWStages * kWTile;         // float4 [kSlots]: sk, V factor, O factor, reference scale
 constexpr uint32_t kOffMX = kOffSlot + kSlots * 16;              // fp32 [2][2][128] the halves' maxima, by turns
-constexpr uint32_t kOffL = kOffMX + 4 * kRows * 4;               // fp32 [2][128] the halves' l
-constexpr uint32_t kOffBar = kOffL + 2 * kRows * 4;
+constexpr uint32_t kOffL = kOffMX + 4 * kLanes * 4;              // fp32 [2][128] the halves' l
+constexpr uint32_t kOffBar = kOffL + 2 * kLanes * 4;
 constexpr uint32_t kBarPair = 2;                                 // + quarter: the two warps of a row's halves
 constexpr int kNumBars = 1 + 2 * kKStages + 2 * kVStages + 2 * kWStages + 2 + 2 + 2 + 2;
 constexpr uint32_t kOffMisc = kOffBar + kNumBars * 8;
 constexpr uint32_t kSmem = kOffMisc + 16 + 1024;
 static_assert(kSmem <= 232448, "shared memory budget");
 
-constexpr int kPartFloats = kRows * kD + 2 * kRows;   // O, m, l of a part
+// Of N rows: O, m, l of a part
+template <int N>
+constexpr int kPartFloats = N * kD + 2 * N;
 constexpr int kSmallest = 4;                          // pages of a part at least
 
 // What one CTA does: pages [page0, page0 + pages) of a tile, as one of `parts`
@@ -97,19 +105,22 @@ struct ChunkParams {
     int split;           // CTAs that parts of tiles should fill; 0: tiles are not cut
 };
 
-// A tile's queries: hi, then lo codes, each as eight 16-byte columns of 128 rows,
+// A tile's queries: hi, then lo codes, each as eight 16-byte columns of N rows,
 // then the words of their factors.
-constexpr int kImage = 2 * kTile + 2 * kRows * 4;
+template <int N>
+constexpr int kImage = 2 * N * kD + 2 * N * 4;
 
 // ---------------------------------------------------------------------------
 // Tiles
 // ---------------------------------------------------------------------------
+template <int N>
 __device__ __forceinline__ int tiles_of(const AttnParams &p, const Seq &s) {
-    return static_cast<int>((static_cast<int64_t>(s.n) * p.G + kRows - 1) / kRows);
+    return static_cast<int>((static_cast<int64_t>(s.n) * p.G + N - 1) / N);
 }
 // Pages that the rows of a tile see; a tile that sees nothing has one, so that its rows are written.
+template <int N>
 __device__ __forceinline__ int pages_of(const AttnParams &p, const Seq &s, int tile) {
-    const int last = min(static_cast<int64_t>(s.n) * p.G, (static_cast<int64_t>(tile) + 1) * kRows) - 1;
+    const int last = min(static_cast<int64_t>(s.n) * p.G, (static_cast<int64_t>(tile) + 1) * N) - 1;
     return max(1, (min(seen_by_row(p, s, last), s.len) + kBlk - 1) / kBlk);
 }
 __device__ __forceinline__ int warp_scan(int v) {
@@ -122,13 +133,14 @@ __device__ __forceinline__ int warp_scan(int v) {
     return v;
 }
 // The index-th tile of a head: its sequence and place there (a warp's work).
+template <int N>
 __device__ bool find_tile(const AttnParams &p, int index, int &b, int &tile, Seq &s) {
     int before = 0;
     bool more = true;
     for (int b0 = 0; more; b0 += 32) {
         Seq mine;
         more = load_seqs(p.c, p.start, p.T, b0, mine);
-        const int t = tiles_of(p, mine), incl = warp_scan(t) + before;
+        const int t = tiles_of<N>(p, mine), incl = warp_scan(t) + before;
         const uint32_t hit = __ballot_sync(0xffffffffu, index < incl);
         if (hit) {
             const int l = __ffs(hit) - 1;
@@ -148,6 +160,7 @@ __device__ bool find_tile(const AttnParams &p, int index, int &b, int &tile, Seq
 // heads): into parts of at most `share` pages, the least for which all heads'
 // parts fit cp.split CTAs.
 constexpr int kCutMost = 2 * 152, kPlanThreads = 512;
+template <int N>
 __device__ void plan_parts(const ChunkParams &cp) {
     __shared__ int sB[kCutMost], sTile[kCutMost], sParts[kCutMost], sSum[kPlanThreads / 32], sTiles;
     const AttnParams &p = cp.a;
@@ -158,7 +171,7 @@ __device__ void plan_parts(const ChunkParams &cp) {
         for (int b0 = 0; more; b0 += 32) {
             Seq s;
             more = load_seqs(p.c, p.start, p.T, b0, s);
-            const int n = tiles_of(p, s);
+            const int n = tiles_of<N>(p, s);
             const int incl = warp_scan(n) + before;
             for (int t = 0; t < n; ++t) {
                 sB[incl - n + t] = b0 + lane;
@@ -174,7 +187,7 @@ __device__ void plan_parts(const ChunkParams &cp) {
     int pages = 0;
     if (tid < tiles) {
         s = load_seq(p.c, p.start, p.T, sB[tid]);
-        pages = pages_of(p, s, sTile[tid]);
+        pages = pages_of<N>(p, s, sTile[tid]);
     }
     auto block_sum = [&](int v) {
         v = __reduce_add_sync(0xffffffffu, v);
@@ -221,6 +234,7 @@ __device__ void plan_parts(const ChunkParams &cp) {
 // two whole rows and writes whole sectors of the image): a query row split as hi +
 // lo, with factors that carry the whole power of two, so that a score is the
 // product times softmax_scale alone; and the list of work.
+template <int N>
 __global__ void __launch_bounds__(kPlanThreads, 3) queries_kernel(const ChunkParams cp) {
     let_next_start();
     const AttnParams &p = cp.a;
@@ -230,24 +244,24 @@ __global__ void __launch_bounds__(kPlanThreads, 3) queries_kernel(const ChunkPar
             if (load_seq(p.c, p.start, p.T, b).bad) report(p.dev_status, kErrInvalid);
     int b = 0, tile = 0;
     Seq s{0, 0, 0, false, false};
-    const bool found = find_tile(p, blockIdx.x, b, tile, s);
+    const bool found = find_tile<N>(p, blockIdx.x, b, tile, s);
     if (cp.split == 0 && blockIdx.y == 0 && threadIdx.x == 0) {
         const int i = static_cast<int>(blockIdx.x);
-        cp.items[i] = Item{b, tile, 0, found ? pages_of(p, s, tile) : 0, 1, i, i, s};
+        cp.items[i] = Item{b, tile, 0, found ? pages_of<N>(p, s, tile) : 0, 1, i, i, s};
     }
     if (found) {
-        uint8_t *img = cp.images + (static_cast<int64_t>(blockIdx.y) * cp.tiles + blockIdx.x) * kImage;
+        uint8_t *img = cp.images + (static_cast<int64_t>(blockIdx.y) * cp.tiles + blockIdx.x) * kImage<N>;
         const int lane16 = threadIdx.x & 15, row0 = threadIdx.x >> 4;
         constexpr int kStep = kPlanThreads / 16;
-        uint4 v[kRows / kStep];
+        uint4 v[N / kStep];
 #pragma unroll
-        for (int i = 0; i < kRows / kStep; ++i) {
-            const int r = tile * kRows + row0 + i * kStep;
+        for (int i = 0; i < N / kStep; ++i) {
+            const int r = tile * N + row0 + i * kStep;
             v[i] = make_uint4(0, 0, 0, 0);
             if (r < s.n * p.G) v[i] = reinterpret_cast<const uint4 *>(query_row(p, s, h, r))[lane16];
         }
 #pragma unroll
-        for (int i = 0; i < kRows / kStep; ++i) {
+        for (int i = 0; i < N / kStep; ++i) {
             const int row = row0 + i * kStep;
             bool odd = false;
             uint32_t m = amax_bf16x8(v[i], odd);      // of the four threads that share 32 channels
@@ -275,17 +289,17 @@ __global__ void __launch_bounds__(kPlanThreads, 3) queries_kernel(const ChunkPar
                 for (int q = 0; q < 4; ++q) d[q] = 32.0f * (x[4 * k + q] - d[q]);
                 lo[k] = e4m3x4(d[0], d[1], d[2], d[3]);
             }
-            uint2 *to = reinterpret_cast<uint2 *>(img + ((lane16 >> 1) * kRows + row) * 16 + (lane16 & 1) * 8);
+            uint2 *to = reinterpret_cast<uint2 *>(img + ((lane16 >> 1) * N + row) * 16 + (lane16 & 1) * 8);
             to[0] = make_uint2(hi[0], hi[1]);
-            to[kTile / 8] = make_uint2(lo[0], lo[1]);
+            to[N * kD / 8] = make_uint2(lo[0], lo[1]);
             if ((lane16 & 3) == 0) {
-                uint8_t *sf = img + 2 * kTile + 4 * row + (lane16 >> 2);
+                uint8_t *sf = img + 2 * N * kD + 4 * row + (lane16 >> 2);
                 sf[0] = static_cast<uint8_t>(127 + e);          // 27 .. 247
-                sf[4 * kRows] = static_cast<uint8_t>(127 + e - 5);
+                sf[4 * N] = static_cast<uint8_t>(127 + e - 5);
             }
         }
     }
-    if (cp.split && blockIdx.x == 0 && h == 0) plan_parts(cp);
+    if (cp.split && blockIdx.x == 0 && h == 0) plan_parts<N>(cp);
 }
 
 // ---------------------------------------------------------------------------
@@ -326,19 +340,19 @@ struct PageScore {
     float c, bias;       // no cap: p = 2^(S c + bias); cap: p = 2^(cap tanh_half(S c) + bias)
     float cap;           // cap log2(e)
     bool near;           // the polynomial of the cap's tanh will do for the warp
-    int lim;             // how many of the thread's 64 columns the row sees
+    int lim;             // how many of the thread's columns the row sees
     bool edge;           // some row of the warp does not see all
 };
 
-// 32 raw scores -> 16 words of fp16 pairs; the unrounded probabilities add to l2.
-template <bool kCap>
-__device__ __forceinline__ void probabilities(uint32_t (&X)[32], const PageScore &s, int col0, uint64_t &l2,
-                                              uint32_t (&W)[16]) {
+// kN raw scores -> words of fp16 pairs; the unrounded probabilities add to l2.
+template <bool kCap, int kN>
+__device__ __forceinline__ void probabilities(uint32_t (&X)[kN], const PageScore &s, int col0, uint64_t &l2,
+                                              uint32_t (&W)[kN / 2]) {
     const uint64_t c2 = pk2(__float_as_uint(s.c), __float_as_uint(s.c));
     const uint64_t b2 = pk2(__float_as_uint(s.bias), __float_as_uint(s.bias));
     if constexpr (kCap) cap_scores(X, s.c, s.cap, s.near, [&](int) { return b2; });
 #pragma unroll
-    for (int k = 0; k < 16; ++k) {
+    for (int k = 0; k < kN / 2; ++k) {
         float a = __uint_as_float(X[2 * k]), b = __uint_as_float(X[2 * k + 1]);
         if constexpr (!kCap) upk2(fma2(pk2(X[2 * k], X[2 * k + 1]), c2, b2), a, b);
         a = ex2_approx(a);
@@ -388,18 +402,31 @@ __device__ __forceinline__ void convert_rows(const unsigned char *src, unsigned 
 
 // Scores of keys that the row does not see, columns col0 + lim and up, become
 // -inf (0 where a cap follows); returns the largest of the others.
-template <bool kCap>
-__device__ __forceinline__ float mask_scores(uint32_t (&X)[32], int col0, int lim) {
+template <bool kCap, int kN>
+__device__ __forceinline__ float mask_scores(uint32_t (&X)[kN], int col0, int lim) {
     float m = __int_as_float(0xff800000);
 #pragma unroll
-    for (int e = 0; e < 32; ++e) {
+    for (int e = 0; e < kN; ++e) {
         if (col0 + e < lim) m = fmaxf(m, __uint_as_float(X[e]));
         else X[e] = kCap ? 0u : 0xff800000u;
     }
     return m;
 }
 
-template <bool kCap>
+// kN raw scores and the largest of them, or with kTop the largest magnitude.
+template <bool kTop, int kN>
+__device__ __forceinline__ void load_scores(uint32_t taddr, uint32_t (&X)[kN], float &m) {
+    if constexpr (kN == 32 && kTop)
+        VCA_TMEM_LDTOP32(taddr, X, m);
+    else if constexpr (kN == 32)
+        VCA_TMEM_LDMAX32(taddr, X, m);
+    else if constexpr (kTop)
+        VCA_TMEM_LDTOP16(taddr, X, m);
+    else
+        VCA_TMEM_LDMAX16(taddr, X, m);
+}
+
+template <int N, bool kCap>
 __global__ void __launch_bounds__(kThreads, 1)
     chunk_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, const ChunkParams cp) {
     extern __shared__ unsigned char smem_raw[];
@@ -423,7 +450,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // the last tiles of a causal sequence see the most pages: they go first
     const Item it = cp.items[gridDim.x - 1 - blockIdx.x];
     if (it.pages == 0) return;
-    const int nb = it.pages, r0 = it.tile * kRows, R = it.s.n * p.G;
+    const int nb = it.pages, r0 = it.tile * N, R = it.s.n * p.G;
 
     if (threadIdx.x == 0) {
         mbar_init(q_full, kConvWarps);
@@ -587,17 +614,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (warp >= kConvWarp0 && warp < kConvWarp0 + kConvWarps) {
         // ------------------------------------------------------------ queries, V codes -> fp16
         {
-            const int quarter = warp & 3, row = quarter * 32 + lane;
+            const int quarter = warp & 3, row = N == 128 ? quarter * 32 + lane : lane;
             const uint32_t tl = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
-            const uint8_t *img = cp.images + (static_cast<int64_t>(blockIdx.y) * cp.tiles + it.image) * kImage;
-            const uint32_t *sf = reinterpret_cast<const uint32_t *>(img + 2 * kTile) + row;
-            const uint32_t sfh = sf[0], sfl = sf[kRows];
+            const uint8_t *img = cp.images + (static_cast<int64_t>(blockIdx.y) * cp.tiles + it.image) * kImage<N>;
+            const uint32_t *sf = reinterpret_cast<const uint32_t *>(img + 2 * N * kD) + row;
+            const uint32_t sfh = sf[0], sfl = sf[N];
 #pragma unroll
             for (int part = 0; part < 2; ++part) {
                 uint32_t w[32];
 #pragma unroll
                 for (int i = 0; i < 8; ++i)
-                    *reinterpret_cast<uint4 *>(w + 4 * i) = reinterpret_cast<const uint4 *>(img)[(8 * part + i) * kRows + row];
+                    *reinterpret_cast<uint4 *>(w + 4 * i) = reinterpret_cast<const uint4 *>(img)[(8 * part + i) * N + row];
                 VCA_TMEM_ST32(tl + kTmemQ + 32 * part, w);
             }
             // row m's factor words lie in lane m, column m / 32; B's factors are 1 everywhere
@@ -631,7 +658,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     } else if (warp >= kSoftWarp0) {
         // ------------------------------------------------------------ softmax
-        const int quarter = warp & 3, half = (warp - kSoftWarp0) >> 2, row = quarter * 32 + lane;
+        const int quarter = warp & 3, half = (warp - kSoftWarp0) >> 2, at_lane = quarter * 32 + lane;
+        const int row = N == 128 ? at_lane : lane, col0 = N == 128 ? 64 * half : 32 * quarter + 16 * half;
+        constexpr int kCols = N == 128 ? 64 : 16, kLoad = N == 128 ? 32 : 16;      // a thread's columns, at a time
         const uint32_t bar_pair = kBarPair + quarter;
         const uint32_t tl = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
         const float kNegInf = __int_as_float(0xff800000);
@@ -639,9 +668,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool real = r < R;
         // raw score -> log2 units (or the cap's inner argument), but for the page's scale
         const float f = kCap ? p.cap_in : p.scale_log2;
-        const int seen = (real ? min(seen_by_row(p, it.s, r), it.s.len) : it.s.len) - it.page0 * kBlk - 64 * half;
-        // pages before this one every row of the warp sees in full
-        const int full = __reduce_min_sync(0xffffffffu, seen) / 64 / 2;
+        const int seen = (real ? min(seen_by_row(p, it.s, r), it.s.len) : it.s.len) - it.page0 * kBlk - col0;
+        // the warp's columns of pages before this one every row sees
+        const int full = (__reduce_min_sync(0xffffffffu, seen) + kBlk - kCols) >> 7;
         PageScore s;
         s.cap = p.cap_out;
         s.bias = 0.0f;
@@ -650,35 +679,35 @@ __global__ void __launch_bounds__(kThreads, 1)
         bool ok = true;
         for (int b = 0; b < nb; ++b) {
             const int sb = b & 1;
-            float *mx = sMX + sb * 2 * kRows;
+            float *mx = sMX + sb * 2 * kLanes;
             if (ok) ok = __all_sync(0xffffffffu, mbar_wait(s_full + sb, (b >> 1) & 1, abort_flag, p.limit_ns));
             if (!ok) {
                 // the other half learns of it where they meet
-                mx[half * kRows + row] = __int_as_float(0x7fc00000);
+                mx[half * kLanes + at_lane] = __int_as_float(0x7fc00000);
                 bar_sync(bar_pair, 64);
                 break;
             }
             const uint32_t tS = tl + kTmemS + 128 * sb;
-            uint32_t X0[32], X1[32];
+            uint32_t X0[kLoad], X1[kLoad];      // X1: of 128 rows
             tc_fence_after();
-            float m0, m1;
+            float m0, m1 = kNegInf;
             const float4 slot = sSlot[b % kSlots];
             s.edge = b >= full || slot.x < 0.0f;
             s.c = fmaxf(__fmul_rn(f, slot.x), 0x1p-126f);      // above 0, so that -inf stays -inf
             if constexpr (kCap) {
                 // loaded twice: the load's own maximum is cheaper than the thread's
-                VCA_TMEM_LDTOP32(tS + 64 * half, X0, m0);
-                VCA_TMEM_LDTOP32(tS + 64 * half + 32, X1, m1);
+                load_scores<true>(tS + col0, X0, m0);
+                if constexpr (N == 128) load_scores<true>(tS + col0 + 32, X1, m1);
                 tmem_ld_wait();
                 s.near = __all_sync(0xffffffffu, fmaxf(m0, m1) * s.c <= kTanhNear);
             }
-            VCA_TMEM_LDMAX32(tS + 64 * half, X0, m0);
-            VCA_TMEM_LDMAX32(tS + 64 * half + 32, X1, m1);
+            load_scores<false>(tS + col0, X0, m0);
+            if constexpr (N == 128) load_scores<false>(tS + col0 + 32, X1, m1);
             tmem_ld_wait();
             if (s.edge) {
                 s.lim = slot.x < 0.0f ? 0 : seen - b * kBlk;
                 m0 = mask_scores<kCap>(X0, 0, s.lim);
-                m1 = mask_scores<kCap>(X1, 32, s.lim);
+                if constexpr (N == 128) m1 = mask_scores<kCap>(X1, 32, s.lim);
             }
             const float pm = fmaxf(m0, m1) * s.c;
             const float pc = kCap ? capped(pm, p.cap_out) : pm;
@@ -687,9 +716,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             // halves have read their scores when they meet, so P may be written over
             // them.  Buffers by turns: the next page's barrier separates this read
             // from the write after it
-            mx[half * kRows + row] = bm;
+            mx[half * kLanes + at_lane] = bm;
             bar_sync(bar_pair, 64);
-            const float other = mx[(half ^ 1) * kRows + row], most = __fadd_rn(m, kLazyTau);
+            const float other = mx[(half ^ 1) * kLanes + at_lane], most = __fadd_rn(m, kLazyTau);
             // mostly neither the reference maximum nor the reference scale moves
             if (__any_sync(0xffffffffu, !(bm <= most) || !(other <= most) || slot.z != 1.0f)) {
                 if (__any_sync(0xffffffffu, other != other)) {
@@ -721,11 +750,22 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
             }
-            uint32_t W[16];
+            uint32_t W[kLoad / 2];
             probabilities<kCap>(X0, s, 0, l2, W);
-            VCA_TMEM_ST16(tS + 32 * half, W);
-            probabilities<kCap>(X1, s, 32, l2, W);
-            VCA_TMEM_ST16(tS + 32 * half + 16, W);
+            if constexpr (N == 128) {
+                VCA_TMEM_ST16(tS + 32 * half, W);
+                probabilities<kCap>(X1, s, 32, l2, W);
+                VCA_TMEM_ST16(tS + 32 * half + 16, W);
+            } else {
+                // the lane quarter's own keys; the other quarters' are not this copy's
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    uint32_t Y[8];
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) Y[k] = q == quarter ? W[k] : 0u;
+                    VCA_TMEM_ST8(tS + 16 * q + 8 * half, Y);
+                }
+            }
             tmem_st_wait();
             tc_fence_before();
             __syncwarp();
@@ -741,17 +781,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         // PV(nb - 1) complete (PV(nb - 3) was when S(nb - 1) came)
         if (ok)
             ok = __all_sync(0xffffffffu, mbar_wait(pv_done + ((nb - 1) & 1), ((nb - 1) >> 1) & 1, abort_flag, p.limit_ns));
-        sL[half * kRows + row] = l;
+        sL[half * kLanes + at_lane] = l;
         ok = bar_and(ok, kBarSoftmax, 32 * kSoftmaxWarps);
         if (ok) {
             tc_fence_after();
-            const float M = m, Mu = M == kNegInf ? 0.0f : M, L = __fadd_rn(sL[row], sL[kRows + row]);
+            const float M = m, Mu = M == kNegInf ? 0.0f : M, L = __fadd_rn(sL[at_lane], sL[kLanes + at_lane]);
             const float ref = sSlot[(nb - 1) % kSlots].w;
             // rows to shared memory (the K and V rings, free by now), then one bulk copy a
             // row: a thread's own stores, a row each, would take a cycle for every sector
-            const uint32_t pitch = it.parts == 1 ? kD * 2 + 16 : kD * 4 + 16;      // 16 more: the rows' banks differ
-            unsigned char *line = smem + row * pitch;
-            const float scale = it.parts == 1 ? (L > 0.0f || L != L ? __fdividef(1.0f, L) : 0.0f) * ref : ref;
+            const bool final = N == 128 && it.parts == 1;
+            const uint32_t pitch = final ? kD * 2 + 16 : kD * 4 + 16;      // 16 more: the rows' banks differ
+            unsigned char *line = smem + at_lane * pitch;
+            const float scale = final ? (L > 0.0f || L != L ? __fdividef(1.0f, L) : 0.0f) * ref : ref;
 #pragma unroll 1
             for (int i = 0; i < 2; ++i) {
                 uint32_t o[32];
@@ -759,7 +800,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tmem_ld_wait();
 #pragma unroll
                 for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * scale);
-                if (it.parts == 1) {
+                if (final) {
                     uint4 *to = reinterpret_cast<uint4 *>(line + 2 * (64 * half + 32 * i));
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
@@ -775,22 +816,70 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int e = 0; e < 8; ++e) to[e] = make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
                 }
             }
-            fence_proxy_async_smem();
-            bar_sync(bar_pair, 64);      // both halves of the row are there
-            if (half == 0) {
-                if (it.parts == 1) {
-                    if (real) {
-                        const int64_t at = out_row(p, it.s, h, r);
-                        bulk_store(p.O + at * kD, line, kD * 2);
-                        if (p.lse) p.lse[at] = Mu * 0.6931471805599453f + logf(L);
+            float *part = p.part + (static_cast<int64_t>(h) * cp.grid + it.slot) * kPartFloats<N>;
+            if constexpr (N == 32) {
+                // the four copies of a row, each over its quarter of the keys, put together
+                if (half == 0) sMX[at_lane] = M;
+                bar_sync(kBarSoftmax, 32 * kSoftmaxWarps);
+                const int i = (threadIdx.x - 32 * kSoftWarp0) >> 3, ch = (threadIdx.x & 7) * 16, ri = r0 + i;
+                float top = kNegInf;
+#pragma unroll
+                for (int q = 0; q < 4; ++q) top = fmaxf(top, sMX[32 * q + i]);
+                const float tu = top == kNegInf ? 0.0f : top;
+                float sum = 0.0f, acc[16] = {};
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const int from = 32 * q + i;
+                    const float k = ex2_approx(sMX[from] - tu);
+                    sum = fmaf(__fadd_rn(sL[from], sL[kLanes + from]), k, sum);
+                    const float4 *o = reinterpret_cast<const float4 *>(smem + from * pitch + 4 * ch);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const float4 x = o[e];
+                        acc[4 * e] = fmaf(x.x, k, acc[4 * e]);
+                        acc[4 * e + 1] = fmaf(x.y, k, acc[4 * e + 1]);
+                        acc[4 * e + 2] = fmaf(x.z, k, acc[4 * e + 2]);
+                        acc[4 * e + 3] = fmaf(x.w, k, acc[4 * e + 3]);
                     }
-                } else {
-                    float *part = p.part + (static_cast<int64_t>(h) * cp.grid + it.slot) * kPartFloats;
-                    if (real) bulk_store(part + row * kD, line, kD * 4);
-                    part[kRows * kD + row] = M;
-                    part[kRows * kD + kRows + row] = L;
                 }
-                bulk_store_wait();
+                if (it.parts > 1) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        reinterpret_cast<float4 *>(part + i * kD + ch)[e] =
+                            make_float4(acc[4 * e], acc[4 * e + 1], acc[4 * e + 2], acc[4 * e + 3]);
+                    if (ch == 0) {
+                        part[N * kD + i] = top;
+                        part[N * kD + N + i] = sum;
+                    }
+                } else if (ri < R) {
+                    const int64_t at = out_row(p, it.s, h, ri);
+                    const float inv = sum > 0.0f || sum != sum ? __fdividef(1.0f, sum) : 0.0f;
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        uint32_t w[4];
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) w[k] = pack_bf16x2(acc[8 * e + 2 * k] * inv, acc[8 * e + 2 * k + 1] * inv);
+                        reinterpret_cast<uint4 *>(p.O + at * kD + ch)[e] = make_uint4(w[0], w[1], w[2], w[3]);
+                    }
+                    if (p.lse && ch == 0) p.lse[at] = tu * 0.6931471805599453f + logf(sum);
+                }
+            } else {
+                fence_proxy_async_smem();
+                bar_sync(bar_pair, 64);      // both halves of the row are there
+                if (half == 0) {
+                    if (it.parts == 1) {
+                        if (real) {
+                            const int64_t at = out_row(p, it.s, h, r);
+                            bulk_store(p.O + at * kD, line, kD * 2);
+                            if (p.lse) p.lse[at] = Mu * 0.6931471805599453f + logf(L);
+                        }
+                    } else {
+                        if (real) bulk_store(part + row * kD, line, kD * 4);
+                        part[N * kD + row] = M;
+                        part[N * kD + N + row] = L;
+                    }
+                    bulk_store_wait();
+                }
             }
         }
     }
@@ -805,6 +894,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // Joins the parts of a tile: one CTA per (tile, head, 16 rows).
+template <int N>
 __global__ void __launch_bounds__(256) join_kernel(const ChunkParams cp) {
     const AttnParams &p = cp.a;
     wait_for_results();
@@ -812,17 +902,17 @@ __global__ void __launch_bounds__(256) join_kernel(const ChunkParams cp) {
     if (first < 0) return;
     const Item it = cp.items[first];
     if (it.parts == 1) return;
-    const int h = blockIdx.y, row = 16 * blockIdx.z + (threadIdx.x >> 4), ch = (threadIdx.x & 15) * 8, r = it.tile * kRows + row;
+    const int h = blockIdx.y, row = 16 * blockIdx.z + (threadIdx.x >> 4), ch = (threadIdx.x & 15) * 8, r = it.tile * N + row;
     if (r >= it.s.n * p.G) return;
-    const float *part = p.part + (static_cast<int64_t>(h) * cp.grid + it.slot) * kPartFloats;
+    const float *part = p.part + (static_cast<int64_t>(h) * cp.grid + it.slot) * kPartFloats<N>;
     float M = __int_as_float(0xff800000);
-    for (int c = 0; c < it.parts; ++c) M = fmaxf(M, part[c * static_cast<int64_t>(kPartFloats) + kRows * kD + row]);
+    for (int c = 0; c < it.parts; ++c) M = fmaxf(M, part[c * static_cast<int64_t>(kPartFloats<N>) + N * kD + row]);
     const float Mu = M == __int_as_float(0xff800000) ? 0.0f : M;
     float L = 0.0f, acc[8] = {};
     for (int c = 0; c < it.parts; ++c) {
-        const float *q = part + c * static_cast<int64_t>(kPartFloats);
-        const float k = ex2_approx(q[kRows * kD + row] - Mu);
-        L = fmaf(q[kRows * kD + kRows + row], k, L);
+        const float *q = part + c * static_cast<int64_t>(kPartFloats<N>);
+        const float k = ex2_approx(q[N * kD + row] - Mu);
+        L = fmaf(q[N * kD + N + row], k, L);
         const float4 *at = reinterpret_cast<const float4 *>(q + row * kD + ch);
         const float4 x = at[0], y = at[1];
         acc[0] = fmaf(x.x, k, acc[0]);
@@ -847,38 +937,41 @@ __global__ void __launch_bounds__(256) join_kernel(const ChunkParams cp) {
 
 // Sizes of a call, and whether tiles are cut: where there can be fewer than two
 // for every SM (the sequences' own number is known on the device alone, which
-// cuts none if they fill the SMs).  64 tiles of 25 rows over 16,383 tokens: 92 us
-// cut, 218 whole.
+// cuts none if they fill the SMs).  64 tiles of 25 rows over 16,383 tokens, in
+// tiles of 128: 92 us cut, 218 whole.
 struct Plan {
     int64_t tiles;
     int split, grid, heads;      // heads: of one launch
     size_t off_first, off_images, off_parts, bytes;
 };
+template <int N>
 Plan plan_of(int T, int Hq, int H, int B, int cols) {
     Plan q;
-    q.tiles = static_cast<int64_t>(T) * (Hq / H) / kRows + (B < T ? B : T);
+    q.tiles = static_cast<int64_t>(T) * (Hq / H) / N + (B < T ? B : T);
     q.split = q.tiles * H < kCutMost && cols > kSmallest ? 152 : 0;
     // cut tiles number at most one CTA's parts each, or what fits the CTAs
     q.grid = static_cast<int>(q.split && q.tiles < q.split / H ? q.split / H : q.tiles);
     q.off_first = sizeof(Item) * q.grid;
     q.off_images = (q.off_first + 4 * static_cast<size_t>(q.tiles) + 1023) / 1024 * 1024;
     // images of some heads at a time: enough tiles for many waves, and a bound on the workspace
-    const int64_t fit = (64ll << 20) / (q.tiles * kImage);
+    const int64_t fit = (64ll << 20) / (q.tiles * kImage<N>);
     q.heads = static_cast<int>(fit < 1 ? 1 : fit < H ? fit : H);
-    q.off_parts = q.off_images + static_cast<size_t>(q.tiles) * q.heads * kImage;
-    q.bytes = q.off_parts + (q.split ? static_cast<size_t>(q.grid) * H * kPartFloats * sizeof(float) : 0);
+    q.off_parts = q.off_images + static_cast<size_t>(q.tiles) * q.heads * kImage<N>;
+    q.bytes = q.off_parts + (q.split ? static_cast<size_t>(q.grid) * H * kPartFloats<N> * sizeof(float) : 0);
     return q;
 }
 
-}  // namespace
+// Tiles of 32 rows where a sequence and KV head have no more than that on average.
+// 16 x 8 heads of 8,000 tokens: 16 rows 67 us in tiles of 32, 70 in tiles of 128; 32
+// rows 68 and 72, with a cap 77 and 124; 40 rows 119 and 72, with a cap 136 and 123.
+bool few_rows(int T, int Hq, int H, int B) { return static_cast<int64_t>(T) * (Hq / H) <= 32ll * B; }
 
-size_t cache_chunk_workspace(int T, int Hq, int H, int B, int cols) { return plan_of(T, Hq, H, B, cols).bytes; }
-
-cudaError_t launch_cache_chunk(const CacheAttnArgs &a, cudaStream_t st) {
+template <int N>
+cudaError_t launch(const CacheAttnArgs &a, cudaStream_t st) {
     CUtensorMap mk, mv;
     const uint64_t rows = static_cast<uint64_t>(a.c.pages) * a.c.H * kBlk;
     if (!make_tile_map(&mk, a.c.k8, rows) || !make_tile_map(&mv, a.c.v8, rows)) return cudaErrorInvalidValue;
-    const Plan q = plan_of(a.T, a.Hq, a.c.H, a.c.B, a.c.cols);
+    const Plan q = plan_of<N>(a.T, a.Hq, a.c.H, a.c.B, a.c.cols);
     uint8_t *ws = static_cast<uint8_t *>(a.ws);
     ChunkParams cp;
     cp.a = attn_params(a.c, a.q, a.start, a.T, a.Hq, a.causal, a.scale, a.softcap, a.dev_status, a.wait_limit_ns);
@@ -891,19 +984,29 @@ cudaError_t launch_cache_chunk(const CacheAttnArgs &a, cudaStream_t st) {
     cp.tiles = static_cast<int>(q.tiles);
     cp.grid = q.grid;
     cp.split = q.split;
-    const auto kernel = a.softcap > 0.0f ? chunk_kernel<true> : chunk_kernel<false>;
+    const auto kernel = a.softcap > 0.0f ? chunk_kernel<N, true> : chunk_kernel<N, false>;
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
     if (e != cudaSuccess) return e;
     for (cp.h0 = 0; cp.h0 < a.c.H; cp.h0 += q.heads) {
         const int heads = a.c.H - cp.h0 < q.heads ? a.c.H - cp.h0 : q.heads;
-        queries_kernel<<<dim3(cp.tiles, heads), kPlanThreads, 0, st>>>(cp);
+        queries_kernel<N><<<dim3(cp.tiles, heads), kPlanThreads, 0, st>>>(cp);
         e = cudaGetLastError();
         if (e != cudaSuccess) return e;
         e = launch_after(kernel, dim3(q.grid, heads), kThreads, kSmem, st, mk, mv, cp);
         if (e != cudaSuccess) return e;
     }
     if (!q.split) return cudaSuccess;      // cut tiles are few: one launch had all heads
-    return launch_after(join_kernel, dim3(cp.tiles, a.c.H, kRows / 16), 256, 0, st, cp);
+    return launch_after(join_kernel<N>, dim3(cp.tiles, a.c.H, N / 16), 256, 0, st, cp);
+}
+
+}  // namespace
+
+size_t cache_chunk_workspace(int T, int Hq, int H, int B, int cols) {
+    return few_rows(T, Hq, H, B) ? plan_of<32>(T, Hq, H, B, cols).bytes : plan_of<128>(T, Hq, H, B, cols).bytes;
+}
+
+cudaError_t launch_cache_chunk(const CacheAttnArgs &a, cudaStream_t st) {
+    return few_rows(a.T, a.Hq, a.c.H, a.c.B) ? launch<32>(a, st) : launch<128>(a, st);
 }
 
 }  // namespace vca

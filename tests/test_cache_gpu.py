@@ -698,3 +698,47 @@ def test_weights_of_ragged_rows(V, pages):
                 torch.cuda.synchronize()
                 assert int(status) == 0
                 _within(weight, w, e, "weight")
+
+
+# between a tile of eight rows and one of 128: lengths, new rows, query heads, KV heads
+MIDDLE = {
+    "nine rows": ([700], [9], 1, 1),
+    "a full tile": ([1500, 129], [8, 8], 8, 2),
+    "five tokens": ([9000, 40, 1300], [5, 5, 5], 20, 4),
+    "one much longer": ([800, 300, 90, 700, 128, 256], [40, 1, 1, 2, 1, 1], 6, 2),
+    "long": ([30011], [7], 8, 2),
+    "many short": ([130 + 7 * b for b in range(80)], [3] * 80, 16, 4),
+    "in front of the cache": ([2, 300], [6, 6], 8, 2),
+}
+
+
+@pytest.mark.parametrize("softcap", [0.0, 30.0, 0.5])
+@pytest.mark.parametrize("name", MIDDLE)
+def test_attention_of_middle_rows(V, name, softcap):
+    lens, news, Hq, H = MIDDLE[name]
+    c = R.make_case(lens, news, H, seed=115)
+    for causal in (True, False):
+        first = _check_attention(V, c, R.rows(sum(news), Hq, seed=116), causal=causal, softcap=softcap)
+        again = _check_attention(V, c, R.rows(sum(news), Hq, seed=116), causal=causal, softcap=softcap)
+        assert torch.equal(first[0], again[0]) and torch.equal(first[1], again[1])
+
+
+def test_middle_rows_of_nan_and_far_scales(V):
+    c = R.make_case([900, 500], [7, 4], 1, seed=117)
+    for j, e in enumerate([-6, -30, -7, -120, -3, -60, 10, -6]):
+        p = int(c.table[0, j])
+        c.sv[p] = 2.0 ** e
+        if e == -120:
+            c.v8[p] = 0
+        c.sk[p] = 2.0 ** -7
+    Q = R.rows(11, 3, seed=118)
+    _check_attention(V, c, Q, causal=True)
+    o, z, eo, el = R.attention(c, Q)
+    Q[2, 1, 5], Q[9, 0, 7] = math.nan, math.inf
+    cache, start = c.on(V)
+    out, lse = V.cache_attention(cache, Q.cuda(), start)
+    bad = torch.zeros(Q.shape[:2], dtype=torch.bool)
+    bad[2, 1] = bad[9, 0] = True
+    assert bool(torch.isnan(out.cpu()[bad]).all())
+    _within(out.cpu()[~bad], o[~bad], eo[~bad], "O")
+    _within(lse.cpu()[~bad], z[~bad], el[~bad], "lse")
