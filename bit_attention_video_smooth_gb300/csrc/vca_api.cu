@@ -221,6 +221,8 @@ int vca_cache_evict(const vca_cache *cache, float *weight, const int32_t *dst_ta
     const void *ptrs[] = {dst_table, new_len, kept};
     for (const void *p : ptrs)
         if (!p || !aligned4(p)) return VCA_ERR_INVALID_ARG;
+    // read by other heads' CTAs while they are written
+    if (new_len == c.len || dst_table == c.table) return VCA_ERR_INVALID_ARG;
     return from_cuda(vca::launch_cache_evict(c, weight, dst_table, dst_cols, budget, recent, new_len, kept, dev_status,
                                              static_cast<cudaStream_t>(stream)));
 }

@@ -348,7 +348,8 @@ int vca_cache_weigh(const vca_cache *cache, const uint16_t *Q, int64_t q_token, 
  * pages are only read, so they may be shared with other sequences).  A written
  * page gets the scale of its own values, as in vca_cache_append; weights move
  * with their tokens.  Requires budget >= 1, 0 <= recent <= budget,
- * dst_cols*128 >= budget.  `len` is the cache's as always; afterwards the
+ * dst_cols*128 >= budget; new_len and dst_table are not the cache's own len and
+ * table (refused).  `len` is the cache's as always; afterwards the
  * sequence is the cache with dst_table and new_len.
  */
 int vca_cache_evict(const vca_cache *cache, float *weight, const int32_t *dst_table, int dst_cols, int budget,

@@ -39,7 +39,7 @@ def _weigh(V, s, Q=FAKE, T=3, Hq=4, causal=1, cap=0.0, lse=FAKE, weight=FAKE):
     return V._lib.vca_cache_weigh(s, Q, 512, 128, FAKE, T, Hq, causal, 0.0, cap, lse, weight, FAKE, 1 << 40, None, None)
 
 
-def _evict(V, s, weight=FAKE, dst=FAKE, dst_cols=2, budget=200, recent=10, new_len=FAKE, kept=FAKE):
+def _evict(V, s, weight=FAKE, dst=2 * FAKE, dst_cols=2, budget=200, recent=10, new_len=3 * FAKE, kept=FAKE):
     return V._lib.vca_cache_evict(s, weight, dst, dst_cols, budget, recent, new_len, kept, None, None)
 
 
@@ -178,3 +178,8 @@ def test_a_pool_of_another_rank_is_named(V):
                  lambda: V.vca_cache_evict(flat, w, dst, 200, 10, torch.zeros(2, dtype=torch.int32), kept)):
         with pytest.raises(ValueError, match="k8 must be"):
             call()
+
+
+def test_an_eviction_in_place_is_refused(V):
+    s = _struct(V)
+    assert _evict(V, s, new_len=FAKE) == INVALID and _evict(V, s, dst=FAKE) == INVALID

@@ -742,3 +742,54 @@ def test_middle_rows_of_nan_and_far_scales(V):
     assert bool(torch.isnan(out.cpu()[bad]).all())
     _within(out.cpu()[~bad], o[~bad], eo[~bad], "O")
     _within(lse.cpu()[~bad], z[~bad], el[~bad], "lse")
+
+
+def test_a_stream_that_is_named(V):
+    """The entries with a stream argument run there, whatever the current stream is."""
+    c = R.make_case([300, 90], [5, 6], 2, seed=119, spare=5)
+    K, Q = R.rows(11, 2, 120), R.rows(11, 4, 121)
+    cache, start = c.on(V)
+    side = torch.cuda.Stream()
+    Kd, Qd = K.cuda(), Q.cuda()
+    out, lse = torch.empty((11, 4, 128), dtype=torch.bfloat16, device="cuda"), torch.empty((11, 4), device="cuda")
+    weight = torch.zeros((*c.sk.shape, 128), device="cuda")
+    ws = torch.empty(max(V.vca_cache_workspace_bytes(op, 11, 4, 2, *c.table.shape)
+                         for op in (V.VCA_OP_CACHE_ATTENTION, V.VCA_OP_CACHE_WEIGH)), dtype=torch.uint8, device="cuda")
+    used = set(c.table[c.table >= 0].tolist())
+    dst = torch.tensor([p for p in range(len(c.sk)) if p not in used][:4], dtype=torch.int32).view(2, 2)
+    dd = dst.cuda()
+    new_len, kept = torch.empty(2, dtype=torch.int32, device="cuda"), torch.full((2, 2, 200), -1, dtype=torch.int32, device="cuda")
+    busy = torch.randn((4096, 4096), device="cuda")
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        for _ in range(20):
+            busy = busy @ busy * 1e-2      # the calls must wait for this on `side`
+        V.vca_cache_append(cache, Kd, Kd, start, stream=side)
+    V.vca_cache_attention(cache, Qd, start, 1, 0.0, 0.0, out, lse, ws, stream=side)
+    V.vca_cache_weigh(cache, Qd, start, 1, 0.0, 0.0, lse, weight, ws, stream=side)
+    V.vca_cache_evict(cache, weight, dd, 200, 20, new_len, kept, stream=side)
+    side.synchronize()
+    R.append(c, K, K)
+    o, z, eo, el = R.attention(c, Q)
+    _within(out, o, eo, "O")
+    _within(lse, z, el, "lse")
+    got = weight.cpu()
+    w, e = R.weigh(c, Q, lse.cpu(), torch.zeros(got.shape))
+    for b in range(2):
+        for p in c.table[b, :-(-int(c.length[b]) // 128)].tolist():
+            _within(got[p], w[p], e[p], "weight")
+    ref = torch.full((2, 2, 200), -1, dtype=torch.int32)
+    assert torch.equal(new_len.cpu(), R.evict(c, got.clone(), dst, 200, 20, ref)) and torch.equal(kept.cpu(), ref)
+    _same_codes(cache.k8, c.k8)
+
+
+def test_calls_without_rows(V):
+    c = R.make_case([300], [0], 2, seed=122)
+    cache, start = c.on(V)
+    K, Q = R.rows(0, 2, 1).cuda(), R.rows(0, 4, 1).cuda()
+    before = cache.k8.clone()
+    V.cache_append(cache, K, K, start)
+    out, lse = V.cache_attention(cache, Q, start)
+    weight = torch.zeros((*c.sk.shape, 128), device="cuda")
+    V.cache_weigh(cache, Q, start, lse, weight)
+    assert out.shape == (0, 4, 128) and lse.shape == (0, 4) and not bool(weight.any()) and torch.equal(cache.k8, before)
