@@ -793,3 +793,28 @@ def test_calls_without_rows(V):
     weight = torch.zeros((*c.sk.shape, 128), device="cuda")
     V.cache_weigh(cache, Q, start, lse, weight)
     assert out.shape == (0, 4, 128) and lse.shape == (0, 4) and not bool(weight.any()) and torch.equal(cache.k8, before)
+
+
+def test_middle_rows_beside_bad_sequences(V):
+    """A bad page or length of one sequence leaves the others right, and rows behind the last stay."""
+    news = [6, 6, 6]
+    c = R.make_case([200, 140, 300], news, 2, seed=123, cols=3)
+    Q = R.rows(sum(news) + 2, 4, seed=124)
+    o, z, eo, el = R.attention(c, Q)
+    for kind in ("page", "length"):
+        d = c.clone()
+        if kind == "page":
+            d.table[1, 0] = 1 << 30
+        else:
+            d.length[1] = -7
+        cache, start = d.on(V)
+        status = torch.zeros(1, dtype=torch.int32, device="cuda")
+        out = torch.full((20, 4, 128), 7.0, dtype=torch.bfloat16, device="cuda")
+        lse = torch.full((20, 4), 7.0, device="cuda")
+        V.cache_attention(cache, Q.cuda(), start, out=out, lse=lse, dev_status=status)
+        torch.cuda.synchronize()
+        assert int(status) == V.VCA_ERR_INVALID_ARG, kind
+        assert bool((out[18:] == 7).all()) and bool((lse[18:] == 7).all())
+        for sl in (slice(0, 6), slice(12, 18)):
+            _within(out[sl], o[sl], eo[sl], f"O ({kind})")
+            _within(lse[sl], z[sl], el[sl], f"lse ({kind})")
