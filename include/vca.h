@@ -316,9 +316,11 @@ int vca_cache_append(const vca_cache *cache, const uint16_t *K, int64_t k_token,
  * largest of their row (2^-30 of it) or of their 32 channels (2^-15, off by 2^-22 of
  * the largest, where a sequence has many rows); sums and statistics are fp32, the
  * probabilities enter the second product as fp16 (2^-12 relative, nothing below
- * 2^-25 of the row's largest).  A slot behind len may hold any bytes; a NaN among
- * the values of a sequence may reach every row of that sequence, one in a query
- * row, or an infinity, only that row.  Equal calls give equal bits.
+ * 2^-25 of the row's largest); where a sequence has many rows, values of pages
+ * whose sv is below 2^-95 of the sequence's largest lose bits and count as 0
+ * below 2^-104.  A slot behind len may hold any bytes; a NaN among the values of a
+ * sequence may reach every row of that sequence, one in a query row, or an
+ * infinity, only that row.  Equal calls give equal bits.
  */
 int vca_cache_attention(const vca_cache *cache, const uint16_t *Q, int64_t q_token, int64_t q_head,
                         const int32_t *start, int T, int Hq, int causal, float softmax_scale, float softcap,

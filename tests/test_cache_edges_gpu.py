@@ -1,0 +1,53 @@
+"""The 8-bit cache at the edges of what its documentation allows: page scales
+that fall again and again, against the 64-bit reference (cache_reference.py)."""
+import math
+
+import pytest
+import torch
+
+import cache_reference as R
+from test_cache_gpu import _check_attention
+
+pytestmark = pytest.mark.gpu
+
+# new rows of a sequence, sequences, KV heads: a token, tiles of 32 rows and of 128,
+# cut into parts of pages (few tiles) and whole (too many tiles to be cut)
+FORMS = {"a token": (1, 1, 2), "32 rows, cut": (20, 1, 2), "32 rows, whole": (20, 8, 24), "128 rows, cut": (130, 1, 2),
+         "128 rows, whole": (130, 8, 20)}
+Z = None      # a page of zeros, which append gives the scale 2^-120
+FALLS = {
+    "two zeros at the end": [-6] * 10 + [Z, Z],
+    "three zeros in the middle": [-6] * 5 + [Z] * 3 + [-6] * 4,
+    "ten zeros": [-6] * 4 + [Z] * 10 + [-6, -7],
+    "zeros first": [Z, Z, -6, -6, Z, Z, -7, -6],
+    "down and up": [-6, -6, Z, Z, -6, -5, Z, Z, 3, -6, Z, Z],
+    "steps": [-6] * 6 + [-40, -75, -110, -120] + [-7, -6],
+    "small ones at the end": [-6] * 4 + [-30, -60, -90, -118],
+}
+
+
+def _case_of_scales(scales, news, B, H, seed):
+    """B sequences over the same pages; V of one sign, so that O grows with every token."""
+    c = R.make_case([128 * len(scales) - 3], [0], H, seed=seed)
+    g = torch.Generator().manual_seed(seed + 1)
+    for j, e in enumerate(scales):
+        p = int(c.table[0, j])
+        v = torch.randn((H, 128, 128), generator=g).abs() * 32 + 256
+        c.v8[p] = 0 if e is Z else v.clamp(max=448).to(torch.float8_e4m3fn).view(torch.uint8)
+        c.sv[p] = 2.0 ** (-120 if e is Z else e)
+    c.v8[int(c.table[0, -1]), :, 125:] = 0x7F      # behind the last token
+    c.table, c.length = c.table.repeat(B, 1), c.length.repeat(B)
+    c.start = torch.arange(B + 1, dtype=torch.int32) * news
+    return c
+
+
+@pytest.mark.parametrize("softcap", [0.0, 20.0])
+@pytest.mark.parametrize("name", FALLS)
+@pytest.mark.parametrize("form", FORMS)
+def test_scales_that_fall_again(V, form, name, softcap):
+    """O is summed in units that follow the pages' scales down: it stays finite
+    however often they fall, with weights spread over every token."""
+    news, B, H = FORMS[form]
+    c = _case_of_scales(FALLS[name], news, B, H, seed=201)
+    Q = (R.rows(news * B, H, seed=202).float() * 0.05).to(torch.bfloat16)
+    _check_attention(V, c, Q, causal=B == 1, softcap=softcap)
