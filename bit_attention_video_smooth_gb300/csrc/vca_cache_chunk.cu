@@ -796,14 +796,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             const bool final = N == 128 && it.parts == 1;
             const uint32_t pitch = final ? kD * 2 + 16 : kD * 4 + 16;      // 16 more: the rows' banks differ
             unsigned char *line = smem + at_lane * pitch;
-            const float scale = final ? (L > 0.0f || L != L ? __fdividef(1.0f, L) : 0.0f) * ref : ref;
+            const float inv = !final ? 1.0f : L > 0.0f || L != L ? 1.0f / L : 0.0f;
 #pragma unroll 1
             for (int i = 0; i < 2; ++i) {
                 uint32_t o[32];
                 VCA_TMEM_LD32(tl + kTmemO + 64 * half + 32 * i, o);
                 tmem_ld_wait();
 #pragma unroll
-                for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * scale);
+                for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * inv * ref);   // inv ref may be subnormal
                 if (final) {
                     uint4 *to = reinterpret_cast<uint4 *>(line + 2 * (64 * half + 32 * i));
 #pragma unroll
@@ -857,7 +857,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 } else if (ri < R) {
                     const int64_t at = out_row(p, it.s, h, ri);
-                    const float inv = sum > 0.0f || sum != sum ? __fdividef(1.0f, sum) : 0.0f;
+                    const float inv = sum > 0.0f || sum != sum ? 1.0f / sum : 0.0f;
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
                         uint32_t w[4];

@@ -51,3 +51,26 @@ def test_scales_that_fall_again(V, form, name, softcap):
     c = _case_of_scales(FALLS[name], news, B, H, seed=201)
     Q = (R.rows(news * B, H, seed=202).float() * 0.05).to(torch.bfloat16)
     _check_attention(V, c, Q, causal=B == 1, softcap=softcap)
+
+
+@pytest.mark.parametrize("form", FORMS)
+def test_outputs_of_the_smallest_scale(V, form):
+    """All values equal, at the scale 2^-120, and softmax sums of 2^25 in units of
+    the reference maximum, which the first page's scores set 2^7.65 below the others':
+    the outputs are the value, to bf16 (2^-8), the probabilities' fp16 (2^-11) and
+    1,400 pages' eight additions of products (2^-23 each)."""
+    news, B, H = FORMS[form]
+    c = R.make_case([256], [0], H, seed=203)
+    first, other = c.table[0].tolist()
+    c.k8[first] = 0
+    c.k8[other] = torch.tensor(0.46875).to(torch.float8_e4m3fn).view(torch.uint8)
+    c.sk[:] = 1.0
+    c.v8[:] = torch.tensor(288.0).to(torch.float8_e4m3fn).view(torch.uint8)
+    c.sv[:] = 2.0 ** -120
+    c.table = torch.tensor([[first] + [other] * 1399] * B, dtype=torch.int32)
+    c.length = torch.full((B,), 1400 * 128 - 5, dtype=torch.int32)
+    c.start = torch.arange(B + 1, dtype=torch.int32) * news
+    cache, start = c.on(V)
+    out, _ = V.cache_attention(cache, torch.ones((news * B, H, 128), dtype=torch.bfloat16, device="cuda"), start, causal=False)
+    off = (out.double() / (288.0 * 2.0 ** -120) - 1.0).abs().max()
+    assert float(off) <= 2.0 ** -8 + 2.0 ** -11 + 1400 * 8 * 2.0 ** -23
