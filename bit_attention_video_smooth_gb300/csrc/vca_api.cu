@@ -43,12 +43,17 @@ bool query_sizes_ok(int T, int Hq, int H) {
 float scale_or_default(float softmax_scale) {
     return softmax_scale > 0.0f ? softmax_scale : static_cast<float>(1.0 / std::sqrt(128.0));
 }
-// The kernels scale by softmax_scale / softcap and by softcap, times 2 log2(e): a factor 4 to fp32's largest.
+// The kernels scale by softmax_scale, softmax_scale / softcap and softcap, times 2 log2(e): a factor 4 to fp32's largest.
 bool scores_ok(int causal, float softmax_scale, float softcap) {
     if ((causal != 0 && causal != 1) || !std::isfinite(softmax_scale) || !std::isfinite(softcap) || softcap < 0.0f) return false;
-    const double most = 8.5e37;
-    return softcap == 0.0f || (softcap < most && static_cast<double>(scale_or_default(softmax_scale)) / softcap < most);
+    const double most = 8.5e37, scale = scale_or_default(softmax_scale);
+    return scale < most && (softcap == 0.0f || (softcap < most && scale / softcap < most));
 }
+// The cap that the kernels get.  softcap tanh(s / softcap) is s to (s / softcap)^2 / 3:
+// from 2^40 on, to less than an fp32 rounding for scores below 2^28, and 0 (no cap)
+// it is.  Below 2^-40 all scores are 0 to 2^-40, as they are with a cap of 2^-40.
+// In between softmax_scale / softcap times a page scale stays a normal number.
+float cap_used(float softcap) { return softcap >= 0x1p40f ? 0.0f : softcap > 0.0f ? std::fmax(softcap, 0x1p-40f) : 0.0f; }
 
 int from_cuda(cudaError_t e) { return e == cudaSuccess ? VCA_OK : VCA_ERR_CUDA; }
 
@@ -191,7 +196,7 @@ int vca_cache_attention(const vca_cache *cache, const uint16_t *Q, int64_t q_tok
     const size_t need = vca::cache_attention_workspace(T, Hq, c.H, c.B, c.cols);
     if (need && (!ws || ws_bytes < need || !aligned16(ws))) return VCA_ERR_WORKSPACE;
     vca::CacheAttnArgs a{c, vca::CacheRows{Q, q_token, q_head}, start, T, Hq, causal, scale_or_default(softmax_scale),
-                         softcap, O, lse, ws, dev_status, g_wait_limit_ns};
+                         cap_used(softcap), O, lse, ws, dev_status, g_wait_limit_ns};
     return from_cuda(vca::launch_cache_attention(a, static_cast<cudaStream_t>(stream)));
 }
 
@@ -207,7 +212,7 @@ int vca_cache_weigh(const vca_cache *cache, const uint16_t *Q, int64_t q_token, 
     const size_t need = vca::cache_weigh_workspace(T, Hq, c.H, c.B, c.cols);
     if (need && (!ws || ws_bytes < need || !aligned16(ws))) return VCA_ERR_WORKSPACE;
     vca::CacheWeighArgs a{c, vca::CacheRows{Q, q_token, q_head}, start, T, Hq, causal, scale_or_default(softmax_scale),
-                          softcap, lse, weight, ws, dev_status, g_wait_limit_ns};
+                          cap_used(softcap), lse, weight, ws, dev_status, g_wait_limit_ns};
     return from_cuda(vca::launch_cache_weigh(a, static_cast<cudaStream_t>(stream)));
 }
 

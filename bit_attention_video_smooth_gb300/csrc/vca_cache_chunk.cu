@@ -697,7 +697,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             float m0, m1 = kNegInf;
             const float4 slot = sSlot[b % kSlots];
             s.edge = b >= full || slot.x < 0.0f;
-            s.c = fmaxf(__fmul_rn(f, slot.x), 0x1p-126f);      // above 0, so that -inf stays -inf
+            s.c = fmaxf(__fmul_rn(f, slot.x), 0x1p-149f);      // above 0, so that -inf stays -inf
             if constexpr (kCap) {
                 // loaded twice: the load's own maximum is cheaper than the thread's
                 load_scores<true>(tS + col0, X0, m0);

@@ -310,9 +310,10 @@ int vca_cache_append(const vca_cache *cache, const uint16_t *K, int64_t k_token,
  *   j visible to row i: j < len, and with causal = 1: j <= len - n + i
  *   O_i = sum_j softmax_j(s_ij) v_j sv,  lse_i = ln sum_j exp(s_ij)
  * A row that sees nothing gets O = 0 and lse = -inf.  softmax_scale <= 0 selects
- * 1/sqrt(d); softcap = 0 caps nothing, and softcap and softmax_scale / softcap have
- * to be below 8.5e37.  O is bf16 [T][Hq][d] and lse fp32 [T][Hq] (may be NULL), both
- * contiguous.  The products are exact but for query elements far below the
+ * 1/sqrt(d); softcap = 0 caps nothing, and softmax_scale, softcap and softmax_scale
+ * / softcap have to be below 8.5e37.  A cap of 2^40 or more counts as none (scores
+ * below 2^28 change by less than an fp32 rounding), one below 2^-40 as 2^-40.  O is
+ * bf16 [T][Hq][d] and lse fp32 [T][Hq] (may be NULL), both contiguous.  The products are exact but for query elements far below the
  * largest of their row (2^-30 of it) or of their 32 channels (2^-15, off by 2^-22 of
  * the largest, where a sequence has many rows); sums and statistics are fp32, the
  * probabilities enter the second product as fp16 (2^-12 relative, nothing below

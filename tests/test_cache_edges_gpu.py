@@ -6,7 +6,7 @@ import pytest
 import torch
 
 import cache_reference as R
-from test_cache_gpu import _check_attention
+from test_cache_gpu import _check_attention, _within
 
 pytestmark = pytest.mark.gpu
 
@@ -74,3 +74,41 @@ def test_outputs_of_the_smallest_scale(V, form):
     out, _ = V.cache_attention(cache, torch.ones((news * B, H, 128), dtype=torch.bfloat16, device="cuda"), start, causal=False)
     off = (out.double() / (288.0 * 2.0 ** -120) - 1.0).abs().max()
     assert float(off) <= 2.0 ** -8 + 2.0 ** -11 + 1400 * 8 * 2.0 ** -23
+
+
+def _check_weigh(V, c, Q, lse, **kw):
+    cache, start = c.on(V)
+    weight = torch.zeros((*c.sk.shape, 128), device="cuda")
+    V.cache_weigh(cache, Q.cuda(), start, lse, weight, **kw)
+    if "softmax_scale" in kw:
+        kw["scale"] = kw.pop("softmax_scale")
+    w, e = R.weigh(c, Q, lse.cpu(), torch.zeros(weight.shape), **kw)
+    _within(weight, w, e, "weight")
+
+
+# a token, middle rows, many rows: lengths, new rows, query heads, KV heads
+ROWS = {"tokens": ([700, 129], [1, 1], 6, 2), "middle": ([1500, 260], [5, 4], 10, 2), "many": ([900, 333], [150, 40], 4, 2)}
+
+
+@pytest.mark.parametrize("name", ROWS)
+@pytest.mark.parametrize("softcap", [1e-30, 2.0 ** -40, 2.0 ** 39, 2.0 ** 40, 1e20, 1e36, 8e37])
+def test_caps_at_the_ends_of_their_range(V, name, softcap):
+    """A cap of any accepted size: tiny ones leave no score, huge ones every score."""
+    lens, news, Hq, H = ROWS[name]
+    c = R.make_case(lens, news, H, seed=211)
+    Q = R.rows(sum(news), Hq, seed=212)
+    _, lse = _check_attention(V, c, Q, causal=True, softcap=softcap)
+    _check_weigh(V, c, Q, lse, softcap=softcap)
+
+
+@pytest.mark.parametrize("name", ROWS)
+@pytest.mark.parametrize("softcap", [1e-30, 30.0, 1e6, 2.0 ** 39, 1e30])
+@pytest.mark.parametrize("magnitude", [2.0 ** -50, 2.0 ** 50])
+def test_caps_of_queries_of_any_magnitude(V, name, softcap, magnitude):
+    """Page scales far from 1 against queries far from 1, with a cap."""
+    lens, news, Hq, H = ROWS[name]
+    c = R.make_case(lens, news, H, seed=213)
+    c.sk *= 1.0 / magnitude
+    Q = (R.rows(sum(news), Hq, seed=214).double() * magnitude).to(torch.bfloat16)
+    _, lse = _check_attention(V, c, Q, causal=True, softcap=softcap)
+    _check_weigh(V, c, Q, lse, softcap=softcap)
