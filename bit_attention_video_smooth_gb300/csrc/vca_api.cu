@@ -176,12 +176,19 @@ size_t vca_cache_workspace_bytes(int op, int T, int Hq, int H, int B, int cols) 
 
 int vca_cache_append(const vca_cache *cache, const uint16_t *K, int64_t k_token, int64_t k_head, const uint16_t *V,
                      int64_t v_token, int64_t v_head, const int32_t *start, int T, int32_t *dev_status, void *stream) {
+    return vca_cache_append_ex(cache, K, k_token, k_head, V, v_token, v_head, start, T, nullptr, dev_status, stream);
+}
+
+int vca_cache_append_ex(const vca_cache *cache, const uint16_t *K, int64_t k_token, int64_t k_head, const uint16_t *V,
+                        int64_t v_token, int64_t v_head, const int32_t *start, int T, float *weight, int32_t *dev_status,
+                        void *stream) {
     vca::CacheView c;
-    if (!cache_ok(cache, &c) || T < 0 || !start || !aligned4(start) || !aligned4(dev_status)) return VCA_ERR_INVALID_ARG;
+    if (!cache_ok(cache, &c) || T < 0 || !start || !aligned4(start) || !aligned16(weight) || !aligned4(dev_status))
+        return VCA_ERR_INVALID_ARG;
     if (T == 0) return VCA_OK;
     if (!rows_ok(K, k_token, k_head) || !rows_ok(V, v_token, v_head)) return VCA_ERR_INVALID_ARG;
     return from_cuda(vca::launch_cache_append(c, vca::CacheRows{K, k_token, k_head}, vca::CacheRows{V, v_token, v_head},
-                                              start, T, dev_status, static_cast<cudaStream_t>(stream)));
+                                              start, T, weight, dev_status, static_cast<cudaStream_t>(stream)));
 }
 
 int vca_cache_attention(const vca_cache *cache, const uint16_t *Q, int64_t q_token, int64_t q_head,

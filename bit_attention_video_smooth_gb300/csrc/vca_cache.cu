@@ -57,6 +57,7 @@ struct AppendParams {
     CacheRows k, v;
     const int32_t *start;
     int T;
+    float *weight;          // [pages][H][128] or null
     int32_t *dev_status;
 };
 
@@ -107,6 +108,9 @@ __global__ void __launch_bounds__(kThreads, 4) append_kernel(const AppendParams 
     float *scale = (is_v ? p.c.sv : p.c.sk) + static_cast<int64_t>(page) * p.c.H + h;
     const int lo = max(first - col * kBlk, 0), hi = min(p.c.len[b] - col * kBlk, kBlk);   // new slots of this page
     const int r = threadIdx.x >> 4, ch = (threadIdx.x & 15) * 8;
+    // a page that is used again holds another token's weights
+    if (p.weight && !is_v && static_cast<int>(threadIdx.x) >= lo && static_cast<int>(threadIdx.x) < hi)
+        p.weight[(static_cast<int64_t>(page) * p.c.H + h) * kBlk + threadIdx.x] = 0.0f;
 
     uint4 v[kPasses];
     uint32_t m = 0;
@@ -464,10 +468,10 @@ __global__ void __launch_bounds__(2 * kThreads, 3) move_kernel(const EvictParams
 }  // namespace
 
 cudaError_t launch_cache_append(const CacheView &c, const CacheRows &k, const CacheRows &v, const int32_t *start, int T,
-                                int32_t *dev_status, cudaStream_t st) {
+                                float *weight, int32_t *dev_status, cudaStream_t st) {
     // n rows touch at most n pages and at most (n - 1) / 128 + 2
     const int64_t bound = static_cast<int64_t>(T) / kBlk + 2ll * c.B;
-    const AppendParams p{c, k, v, start, T, dev_status};
+    const AppendParams p{c, k, v, start, T, weight, dev_status};
     append_kernel<<<dim3(static_cast<unsigned>(bound < T ? bound : T), c.H, 2), kThreads, 0, st>>>(p);
     return cudaGetLastError();
 }

@@ -82,7 +82,7 @@ struct CacheWeighArgs {
     uint64_t wait_limit_ns;
 };
 cudaError_t launch_cache_append(const CacheView &c, const CacheRows &k, const CacheRows &v, const int32_t *start, int T,
-                                int32_t *dev_status, cudaStream_t st);
+                                float *weight, int32_t *dev_status, cudaStream_t st);
 size_t cache_attention_workspace(int T, int Hq, int H, int B, int cols);
 cudaError_t launch_cache_attention(const CacheAttnArgs &a, cudaStream_t st);
 size_t cache_chunk_workspace(int T, int Hq, int H, int B, int cols);              // many rows

@@ -27,8 +27,8 @@ VCA_OP_CACHE_ATTENTION, VCA_OP_CACHE_WEIGH = 4, 5
 EXPORTS = ("vca_status_string", "vca_version", "vca_workspace_bytes", "vca_group", "vca_prep_quant",
            "vca_attention", "vca_expcast_codes", "vca_e4m3_encode_bits", "vca_selftest_timeout",
            "vca_set_wait_limit_ns", "vca_prep_quant_noalloc", "vca_prep_quant_ex",
-           "vca_cache_workspace_bytes", "vca_cache_append", "vca_cache_attention", "vca_cache_weigh",
-           "vca_cache_evict")
+           "vca_cache_workspace_bytes", "vca_cache_append", "vca_cache_append_ex", "vca_cache_attention",
+           "vca_cache_weigh", "vca_cache_evict")
 
 if not os.path.exists(LIB_PATH):
     raise ImportError(f"libvca.so is not built ({LIB_PATH}); run __graft_entry__.build() -- "
@@ -60,6 +60,7 @@ _SIGS = {
                                _P, _SZ, _P]),
     "vca_cache_workspace_bytes": (_SZ, [_I] * 6),
     "vca_cache_append": (_I, [_C, _P, _I64, _I64, _P, _I64, _I64, _P, _I, _P, _P]),
+    "vca_cache_append_ex": (_I, [_C, _P, _I64, _I64, _P, _I64, _I64, _P, _I, _P, _P, _P]),
     "vca_cache_attention": (_I, [_C, _P, _I64, _I64, _P, _I, _I, _I, _F, _F, _P, _P, _P, _SZ, _P, _P]),
     "vca_cache_weigh": (_I, [_C, _P, _I64, _I64, _P, _I, _I, _I, _F, _F, _P, _P, _P, _SZ, _P, _P]),
     "vca_cache_evict": (_I, [_C, _P, _P, _I, _I, _I, _P, _P, _P, _P]),
@@ -449,12 +450,13 @@ def _at(t: Optional[torch.Tensor]):
     return None if t is None else t.data_ptr()
 
 
-def vca_cache_append(cache: Cache, K, V, start, dev_status=None, stream=None) -> None:
+def vca_cache_append(cache: Cache, K, V, start, dev_status=None, stream=None, weight=None) -> None:
     H = cache.k8.shape[1] if cache.k8.dim() == 4 else 0
     s, dev = _cache_call("vca_cache_append", cache, (("K", K, H), ("V", V, H)),
-                         (("dev_status", dev_status, torch.int32, (1,)),), start)
-    _launch("vca_cache_append", dev, _lib.vca_cache_append, s, K.data_ptr(), K.stride(0), K.stride(1), V.data_ptr(),
-            V.stride(0), V.stride(1), start.data_ptr(), K.shape[0], _at(dev_status), stream=stream)
+                         (("weight", weight, torch.float32, (*cache.sk.shape, 128)),
+                          ("dev_status", dev_status, torch.int32, (1,))), start)
+    _launch("vca_cache_append", dev, _lib.vca_cache_append_ex, s, K.data_ptr(), K.stride(0), K.stride(1), V.data_ptr(),
+            V.stride(0), V.stride(1), start.data_ptr(), K.shape[0], _at(weight), _at(dev_status), stream=stream)
 
 
 def vca_cache_attention(cache: Cache, Q, start, causal: int, softmax_scale: float, softcap: float, O, lse, ws,
@@ -501,10 +503,11 @@ def _cache_ws(op, cache: Cache, Q, ws):
     return torch.empty(need, dtype=torch.uint8, device=cache.k8.device) if need else None
 
 
-def cache_append(cache: Cache, K, V, start, dev_status=None) -> None:
+def cache_append(cache: Cache, K, V, start, dev_status=None, weight: Optional[torch.Tensor] = None) -> None:
     """Quantises the new rows K, V [T, H, 128] into the cache's pages; sequence b
-    owns the rows start[b] .. start[b+1] - 1, its newest tokens."""
-    vca_cache_append(cache, K, V, start, dev_status)
+    owns the rows start[b] .. start[b+1] - 1, its newest tokens.  `weight`
+    [pages, H, 128], where the tokens are weighed: theirs becomes 0."""
+    vca_cache_append(cache, K, V, start, dev_status, weight=weight)
 
 
 def cache_attention(cache: Cache, Q, start, causal: bool = True, softmax_scale: float = 0.0, softcap: float = 0.0,
@@ -522,7 +525,8 @@ def cache_weigh(cache: Cache, Q, start, lse, weight, causal: bool = True, softma
                 softcap: float = 0.0, ws: Optional[torch.Tensor] = None,
                 dev_status: Optional[torch.Tensor] = None) -> None:
     """Adds to weight [pages, H, 128] the attention that each cached token gets
-    from Q; lse is cache_attention's."""
+    from Q; lse is cache_attention's.  cache_append(weight=...) makes a new
+    token's weight 0."""
     vca_cache_weigh(cache, Q, start, causal, softmax_scale, softcap, lse, weight,
                     _cache_ws(VCA_OP_CACHE_WEIGH, cache, Q, ws), dev_status)
 

@@ -304,6 +304,18 @@ int vca_cache_append(const vca_cache *cache, const uint16_t *K, int64_t k_token,
                      int64_t v_token, int64_t v_head, const int32_t *start, int T, int32_t *dev_status, void *stream);
 
 /*
+ * vca_cache_append_ex -- vca_cache_append that also clears the weights of the new
+ * tokens: weight[page][h][slot] = 0 (vca_cache_weigh's, 16-byte aligned; NULL clears
+ * nothing).  Who weighs and evicts in a pool whose pages are used again appends
+ * with it, or clears a page's weights before its first token (before
+ * vca_cache_evict, those of the pages it writes): else a new token starts with the
+ * weight of the token that its slot held before.
+ */
+int vca_cache_append_ex(const vca_cache *cache, const uint16_t *K, int64_t k_token, int64_t k_head, const uint16_t *V,
+                        int64_t v_token, int64_t v_head, const int32_t *start, int T, float *weight, int32_t *dev_status,
+                        void *stream);
+
+/*
  * vca_cache_attention -- attention of the rows Q [T][Hq][d] over the cache;
  * query heads h*G .. h*G + G - 1 read KV head h, G = Hq / H:
  *   s_ij = softmax_scale q_i . (k_j sk);  with softcap > 0: softcap tanh(s_ij / softcap)
@@ -333,7 +345,8 @@ int vca_cache_attention(const vca_cache *cache, const uint16_t *Q, int64_t q_tok
  * G query heads of KV head h, where the token is visible, of exp(s_ij - lse_i),
  * with s, visibility and lse [T][Hq] those of vca_cache_attention.  A key's sum
  * over the rows of one sequence has a fixed order and is added once (weight is
- * 16-byte aligned); sequences that share a page add to it in any order.
+ * 16-byte aligned); sequences that share a page add to it in any order.  A token's
+ * weight starts at what its slot holds: vca_cache_append_ex makes that 0.
  */
 int vca_cache_weigh(const vca_cache *cache, const uint16_t *Q, int64_t q_token, int64_t q_head, const int32_t *start,
                     int T, int Hq, int causal, float softmax_scale, float softcap, const float *lse, float *weight,
@@ -350,10 +363,10 @@ int vca_cache_weigh(const vca_cache *cache, const uint16_t *Q, int64_t q_token, 
  * are read, each named once and none a page that `table` names (the cached
  * pages are only read, so they may be shared with other sequences).  A written
  * page gets the scale of its own values, as in vca_cache_append; weights move
- * with their tokens.  Requires budget >= 1, 0 <= recent <= budget,
- * dst_cols*128 >= budget; new_len and dst_table are not the cache's own len and
- * table (refused).  `len` is the cache's as always; afterwards the
- * sequence is the cache with dst_table and new_len.
+ * with their tokens, and those of the slots behind the last one stay as they are.
+ * Requires budget >= 1, 0 <= recent <= budget, dst_cols*128 >= budget; new_len and
+ * dst_table are not the cache's own len and table (refused).  `len` is the cache's
+ * as always; afterwards the sequence is the cache with dst_table and new_len.
  */
 int vca_cache_evict(const vca_cache *cache, float *weight, const int32_t *dst_table, int dst_cols, int budget,
                     int recent, int32_t *new_len, int32_t *kept, int32_t *dev_status, void *stream);

@@ -112,3 +112,60 @@ def test_caps_of_queries_of_any_magnitude(V, name, softcap, magnitude):
     Q = (R.rows(sum(news), Hq, seed=214).double() * magnitude).to(torch.bfloat16)
     _, lse = _check_attention(V, c, Q, causal=True, softcap=softcap)
     _check_weigh(V, c, Q, lse, softcap=softcap)
+
+
+def test_pages_used_twice(V):
+    """Append, attend, weigh and evict in a pool whose pages, weights included, held
+    other tokens before: a new token's weight starts at 0, also in the slots behind
+    an eviction's last token, and other slots' weights stay."""
+    H, Hq, B, budget, recent = 2, 6, 2, 200, 20
+    c = R.make_case([0, 0], [0, 0], H, cols=4, seed=221, spare=12)
+    g = torch.Generator().manual_seed(222)
+    c.k8, c.v8 = R.random_codes(g, c.k8.shape), R.random_codes(g, c.v8.shape)
+    weight = torch.rand((*c.sk.shape, 128), generator=g) * 100.0
+    got = weight.cuda()
+    cache, _ = c.on(V)
+
+    def new_slots(news):
+        for b, n in enumerate(news):
+            for t in range(int(c.length[b]) - n, int(c.length[b])):
+                weight[int(c.table[b, t // 128]), :, t % 128] = 0.0
+
+    def step(news, seed):
+        nonlocal weight
+        c.length += torch.tensor(news, dtype=torch.int32)
+        c.start = torch.tensor([0, news[0], sum(news)], dtype=torch.int32)
+        K, W, Q = R.rows(sum(news), H, seed), R.rows(sum(news), H, seed + 1, outliers=False), R.rows(sum(news), Hq, seed + 2)
+        cache.length.copy_(c.length)
+        start = c.start.cuda()
+        V.cache_append(cache, K.cuda(), W.cuda(), start, weight=got)
+        R.append(c, K, W)
+        new_slots(news)
+        assert torch.equal(got.cpu(), weight)
+        out, lse = V.cache_attention(cache, Q.cuda(), start)
+        V.cache_weigh(cache, Q.cuda(), start, lse, got)
+        w, e = R.weigh(c, Q, lse.cpu(), weight)
+        _within(got, w, e, "weight")
+        weight = got.cpu()
+
+    def cut(pages):
+        dst = torch.tensor(pages, dtype=torch.int32).view(B, 2)
+        kept = torch.full((B, H, budget), -1, dtype=torch.int32)
+        new_len, got_kept = V.cache_evict(cache, got, dst.cuda(), budget, recent)
+        ref = R.evict(c, weight, dst, budget, recent, kept)
+        assert torch.equal(new_len.cpu(), ref) and torch.equal(got_kept.cpu(), kept) and torch.equal(got.cpu(), weight)
+        c.table = torch.cat([dst, torch.full((B, 2), -1, dtype=torch.int32)], 1)
+        c.length = ref.clone()
+        cache.table.copy_(c.table)
+
+    c.table = torch.tensor([[0, 1, 2, -1], [3, 4, 5, -1]], dtype=torch.int32)
+    cache.table.copy_(c.table)
+    step([300, 140], 230)
+    cut([6, 7, 8, 9])
+    step([1, 1], 240)
+    step([40, 100], 250)      # into the pages that the eviction filled in part, and one more of the first sequence's
+    c.table[:, 2] = torch.tensor([0, 3])      # pages of tokens that are gone
+    cache.table.copy_(c.table)
+    step([60, 30], 260)
+    cut([1, 2, 4, 5])
+    step([3, 2], 270)
