@@ -503,7 +503,8 @@ cudaError_t launch_cache_evict(const CacheView &c, float *weight, const int32_t 
     cfg.numAttrs = 1;
     e = cudaLaunchKernelEx(&cfg, kernel, p, keep);
     if (e != cudaSuccess) return e;
-    return launch_after(move_kernel, dim3((budget + kBlk - 1) / kBlk, c.H, c.B), 2 * kThreads, 0, st, p);
+    const int64_t most = budget < tokens ? budget : tokens;      // that stay
+    return launch_after(move_kernel, dim3(static_cast<unsigned>((most + kBlk - 1) / kBlk), c.H, c.B), 2 * kThreads, 0, st, p);
 }
 
 }  // namespace vca

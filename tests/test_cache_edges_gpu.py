@@ -6,7 +6,7 @@ import pytest
 import torch
 
 import cache_reference as R
-from test_cache_gpu import _check_attention, _within
+from test_cache_gpu import _check_attention, _same_codes, _within
 
 pytestmark = pytest.mark.gpu
 
@@ -169,3 +169,28 @@ def test_pages_used_twice(V):
     step([60, 30], 260)
     cut([1, 2, 4, 5])
     step([3, 2], 270)
+
+
+@pytest.mark.parametrize("budget", [1000, 2 ** 31 - 1])
+def test_budgets_beyond_the_cache(V, budget):
+    """A budget above every length, up to the largest int32: all tokens stay, in fresh pages."""
+    c = R.make_case([300, 129], [0, 0], 1, seed=231, spare=6)
+    used = set(c.table[c.table >= 0].tolist())
+    free = [p for p in range(len(c.sk)) if p not in used]
+    dst = torch.tensor([free[:3], free[3:6]], dtype=torch.int32)
+    cols = -(-budget // 128)
+    big = torch.full((2, cols), -1, dtype=torch.int32, device="cuda")
+    big[:, :3] = dst.cuda()
+    weight = torch.rand((*c.sk.shape, 128), generator=torch.Generator().manual_seed(232))
+    cache, _ = c.on(V)
+    got_w, got_kept = weight.cuda(), torch.full((2, 1, budget), -1, dtype=torch.int32, device="cuda")
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    new_len, _ = V.cache_evict(cache, got_w, big, budget, 7, kept=got_kept, dev_status=status)
+    torch.cuda.synchronize()
+    assert int(status) == 0 and new_len.tolist() == [300, 129]
+    kept = torch.full((2, 1, 400), -1, dtype=torch.int32)
+    R.evict(c, weight, dst, 400, 7, kept)
+    assert torch.equal(got_kept[..., :400].cpu(), kept) and not bool((got_kept[..., 400:] != -1).any())
+    _same_codes(cache.k8, c.k8)
+    _same_codes(cache.v8, c.v8)
+    assert torch.equal(cache.sk.cpu(), c.sk) and torch.equal(got_w.cpu(), weight)
