@@ -365,8 +365,18 @@ def alloc_cache(pages: int, H: int, B: int, cols: int, device="cuda") -> Cache:
                  torch.zeros((B,), dtype=torch.int32, device=device))
 
 
+_MOST = 2 ** 31 - 1      # the C interface's int; ctypes cuts larger numbers
+
+
 def vca_cache_workspace_bytes(op: int, T: int, Hq: int, H: int, B: int, cols: int) -> int:
+    if max(T, Hq, H, B, cols) > _MOST:
+        return 0
     return int(_lib.vca_cache_workspace_bytes(op, T, Hq, H, B, cols))
+
+
+def _ranks(where, cache: Cache):
+    if cache.k8.dim() != 4 or cache.table.dim() != 2:
+        raise ValueError(f"{where}: k8 must be [pages, H, 128, 128] and table [B, cols]")
 
 
 def _typed(where, name, t, dtype, shape):
@@ -376,6 +386,11 @@ def _typed(where, name, t, dtype, shape):
         raise ValueError(f"{where}: {name} must be contiguous")
 
 
+def _few_enough(where, name, t):
+    if max(t.shape[:2], default=0) > _MOST:
+        raise ValueError(f"{where}: {name} has more than {_MOST} rows or heads")
+
+
 def _cache_call(where, cache: Cache, rows, others, start=None, ws=None):
     """Checks a call's tensors and returns the C struct and the device: every
     tensor of the types and shapes of include/vca.h, all on one CUDA device.
@@ -383,8 +398,7 @@ def _cache_call(where, cache: Cache, rows, others, start=None, ws=None):
     channels, `others` (name, tensor, dtype, shape), the tensor None where it is
     not given; `ws` is a workspace or None."""
     k8, v8, sk, sv, table, length = cache.k8, cache.v8, cache.sk, cache.sv, cache.table, cache.length
-    if k8.dim() != 4 or table.dim() != 2:
-        raise ValueError(f"{where}: k8 must be [pages, H, 128, 128] and table [B, cols]")
+    _ranks(where, cache)
     pages, H = k8.shape[:2]
     B, cols = table.shape
     codes, scales = (pages, H, 128, 128), (pages, H)
@@ -401,6 +415,7 @@ def _cache_call(where, cache: Cache, rows, others, start=None, ws=None):
         ok = ok and t.dtype is dtype and t.shape == shape and t.get_device() == dev and t.is_contiguous()
     T = rows[0][1].shape[0] if rows and rows[0][1].dim() else 0
     for _, t, heads in rows:
+        ok = ok and T <= _MOST and heads <= _MOST
         ok = ok and t.dtype is torch.bfloat16 and t.shape == (T, heads, 128) and t.stride(2) == 1 and t.get_device() == dev
     if not ok:
         _refuse(where, k8, seen, rows, ws)
@@ -411,6 +426,8 @@ def _cache_call(where, cache: Cache, rows, others, start=None, ws=None):
 
 def _refuse(where, k8, seen, rows, ws):
     """Names the first tensor of a call that is not as it must be."""
+    for name, t, _ in rows:
+        _few_enough(where, name, t)
     for name, t, dtype, shape in seen:
         _typed(where, name, t, dtype, shape)
     if ws is not None and not ws.is_contiguous():
@@ -482,10 +499,16 @@ def vca_cache_weigh(cache: Cache, Q, start, causal: int, softmax_scale: float, s
             0 if ws is None else ws.numel() * ws.element_size(), _at(dev_status), stream=stream)
 
 
+def _cut(*sizes):
+    if any(not -_MOST <= x <= _MOST for x in sizes):
+        raise ValueError(f"vca_cache_evict: budget, recent and dst_cols must fit 32 bits, got {sizes}")
+
+
 def vca_cache_evict(cache: Cache, weight, dst_table, budget: int, recent: int, new_len, kept, dev_status=None,
                     stream=None) -> None:
     if dst_table.dim() != 2:
         raise ValueError("vca_cache_evict: dst_table must be [B, dst_cols]")
+    _cut(budget, recent, dst_table.shape[1])
     B, H = cache.table.shape[:1], cache.sk.shape[1:]
     s, dev = _cache_call("vca_cache_evict", cache, (),
                          (("weight", weight, torch.float32, (*cache.sk.shape, 128)),
@@ -496,7 +519,11 @@ def vca_cache_evict(cache: Cache, weight, dst_table, budget: int, recent: int, n
             dst_table.shape[1], budget, recent, new_len.data_ptr(), kept.data_ptr(), _at(dev_status), stream=stream)
 
 
-def _cache_ws(op, cache: Cache, Q, ws):
+def _cache_ws(where, op, cache: Cache, Q, ws):
+    _ranks(where, cache)
+    if Q.dim() != 3:
+        raise ValueError(f"{where}: Q must be bfloat16 [T, Hq, 128], got {Q.dtype} {tuple(Q.shape)}")
+    _few_enough(where, "Q", Q)
     if ws is not None:
         return ws
     need = vca_cache_workspace_bytes(op, Q.shape[0], Q.shape[1], cache.k8.shape[1], *cache.table.shape)
@@ -514,10 +541,10 @@ def cache_attention(cache: Cache, Q, start, causal: bool = True, softmax_scale: 
                     out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
                     ws: Optional[torch.Tensor] = None, dev_status: Optional[torch.Tensor] = None):
     """Attention of Q [T, Hq, 128] over the cache.  Returns (O [T, Hq, 128], lse [T, Hq])."""
+    ws = _cache_ws("vca_cache_attention", VCA_OP_CACHE_ATTENTION, cache, Q, ws)
     O = out if out is not None else torch.empty(Q.shape, dtype=torch.bfloat16, device=Q.device)
     lse = lse if lse is not None else torch.empty(Q.shape[:2], dtype=torch.float32, device=Q.device)
-    vca_cache_attention(cache, Q, start, causal, softmax_scale, softcap, O, lse,
-                        _cache_ws(VCA_OP_CACHE_ATTENTION, cache, Q, ws), dev_status)
+    vca_cache_attention(cache, Q, start, causal, softmax_scale, softcap, O, lse, ws, dev_status)
     return O, lse
 
 
@@ -528,7 +555,7 @@ def cache_weigh(cache: Cache, Q, start, lse, weight, causal: bool = True, softma
     from Q; lse is cache_attention's.  cache_append(weight=...) makes a new
     token's weight 0."""
     vca_cache_weigh(cache, Q, start, causal, softmax_scale, softcap, lse, weight,
-                    _cache_ws(VCA_OP_CACHE_WEIGH, cache, Q, ws), dev_status)
+                    _cache_ws("vca_cache_weigh", VCA_OP_CACHE_WEIGH, cache, Q, ws), dev_status)
 
 
 def cache_evict(cache: Cache, weight, dst_table, budget: int, recent: int, kept: Optional[torch.Tensor] = None,
@@ -536,7 +563,9 @@ def cache_evict(cache: Cache, weight, dst_table, budget: int, recent: int, kept:
     """Cuts every sequence to `budget` tokens per head into the pages of
     dst_table.  Returns (new_len [B], kept [B, H, budget]); the cut sequences are
     Cache(k8, v8, sk, sv, dst_table, new_len)."""
-    B, H = cache.length.shape[0], cache.k8.shape[1]
+    _ranks("vca_cache_evict", cache)
+    _cut(budget, recent)
+    B, H = cache.table.shape[0], cache.k8.shape[1]
     new_len = torch.empty((B,), dtype=torch.int32, device=cache.k8.device)
     if kept is None:
         kept = torch.full((B, H, budget), -1, dtype=torch.int32, device=cache.k8.device)
