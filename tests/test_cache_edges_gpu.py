@@ -1,5 +1,6 @@
-"""The 8-bit cache at the edges of what its documentation allows: page scales
-that fall again and again, against the 64-bit reference (cache_reference.py)."""
+"""The 8-bit cache at the edges of what its documentation allows -- page scales that
+fall again and again, caps and scales of any size, pages used twice, budgets
+beyond the cache -- against the 64-bit reference (cache_reference.py)."""
 import math
 
 import pytest
@@ -80,8 +81,6 @@ def _check_weigh(V, c, Q, lse, **kw):
     cache, start = c.on(V)
     weight = torch.zeros((*c.sk.shape, 128), device="cuda")
     V.cache_weigh(cache, Q.cuda(), start, lse, weight, **kw)
-    if "softmax_scale" in kw:
-        kw["scale"] = kw.pop("softmax_scale")
     w, e = R.weigh(c, Q, lse.cpu(), torch.zeros(weight.shape), **kw)
     _within(weight, w, e, "weight")
 
@@ -194,3 +193,23 @@ def test_budgets_beyond_the_cache(V, budget):
     _same_codes(cache.k8, c.k8)
     _same_codes(cache.v8, c.v8)
     assert torch.equal(cache.sk.cpu(), c.sk) and torch.equal(got_w.cpu(), weight)
+
+
+@pytest.mark.parametrize("name", ROWS)
+@pytest.mark.parametrize("softcap", [0.0, 4.0])
+@pytest.mark.parametrize("scale", [0.25, 0.011, 0.0, -3.0])
+def test_scales_of_scores(V, name, softcap, scale):
+    """softmax_scale as it is given; 1 / sqrt(128) where it is not above 0."""
+    lens, news, Hq, H = ROWS[name]
+    c = R.make_case(lens, news, H, seed=241)
+    Q = R.rows(sum(news), Hq, seed=242, outliers=False)
+    cache, start = c.on(V)
+    out, lse = V.cache_attention(cache, Q.cuda(), start, softmax_scale=scale, softcap=softcap)
+    used = scale if scale > 0 else 1.0 / math.sqrt(128.0)
+    o, z, eo, el = R.attention(c, Q, softcap=softcap, scale=used)
+    _within(out, o, eo, "O")
+    _within(lse, z, el, "lse")
+    weight = torch.zeros((*c.sk.shape, 128), device="cuda")
+    V.cache_weigh(cache, Q.cuda(), start, lse, weight, softmax_scale=scale, softcap=softcap)
+    w, e = R.weigh(c, Q, lse.cpu(), torch.zeros(weight.shape), softcap=softcap, scale=used)
+    _within(weight, w, e, "weight")
