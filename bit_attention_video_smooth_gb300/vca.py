@@ -398,7 +398,8 @@ def _cache_call(where, cache: Cache, rows, others, start=None, ws=None):
     channels, `others` (name, tensor, dtype, shape), the tensor None where it is
     not given; `ws` is a workspace or None."""
     k8, v8, sk, sv, table, length = cache.k8, cache.v8, cache.sk, cache.sv, cache.table, cache.length
-    _ranks(where, cache)
+    if k8.dim() != 4 or table.dim() != 2:
+        _ranks(where, cache)
     pages, H = k8.shape[:2]
     B, cols = table.shape
     codes, scales = (pages, H, 128, 128), (pages, H)
@@ -426,14 +427,9 @@ def _cache_call(where, cache: Cache, rows, others, start=None, ws=None):
 
 def _refuse(where, k8, seen, rows, ws):
     """Names the first tensor of a call that is not as it must be."""
-    for name, t, _ in rows:
-        _few_enough(where, name, t)
-    for name, t, dtype, shape in seen:
-        _typed(where, name, t, dtype, shape)
-    if ws is not None and not ws.is_contiguous():
-        raise ValueError(f"{where}: ws must be contiguous")
     T = None
     for name, t, heads in rows:
+        _few_enough(where, name, t)
         shape = t.shape
         if t.dtype != torch.bfloat16 or len(shape) != 3 or shape[1] != heads or shape[2] != 128:
             raise ValueError(f"{where}: {name} must be bfloat16 [T, {heads}, 128], got {t.dtype} {tuple(shape)}")
@@ -442,6 +438,10 @@ def _refuse(where, k8, seen, rows, ws):
         if T is not None and shape[0] != T:
             raise ValueError(f"{where}: {name} has {shape[0]} rows, not {T}")
         T = shape[0]
+    for name, t, dtype, shape in seen:
+        _typed(where, name, t, dtype, shape)
+    if ws is not None and not ws.is_contiguous():
+        raise ValueError(f"{where}: ws must be contiguous")
     named = [x[:2] for x in (*seen, *rows)] + ([("ws", ws)] if ws is not None else [])
     for name, t in named:
         if not t.is_cuda:
@@ -499,9 +499,9 @@ def vca_cache_weigh(cache: Cache, Q, start, causal: int, softmax_scale: float, s
             0 if ws is None else ws.numel() * ws.element_size(), _at(dev_status), stream=stream)
 
 
-def _cut(*sizes):
-    if any(not -_MOST <= x <= _MOST for x in sizes):
-        raise ValueError(f"vca_cache_evict: budget, recent and dst_cols must fit 32 bits, got {sizes}")
+def _cut(budget, recent, dst_cols):
+    if not (-_MOST <= budget <= _MOST and -_MOST <= recent <= _MOST and dst_cols <= _MOST):
+        raise ValueError(f"vca_cache_evict: budget {budget}, recent {recent} and dst_cols {dst_cols} must fit 32 bits")
 
 
 def vca_cache_evict(cache: Cache, weight, dst_table, budget: int, recent: int, new_len, kept, dev_status=None,
@@ -519,13 +519,11 @@ def vca_cache_evict(cache: Cache, weight, dst_table, budget: int, recent: int, n
             dst_table.shape[1], budget, recent, new_len.data_ptr(), kept.data_ptr(), _at(dev_status), stream=stream)
 
 
-def _cache_ws(where, op, cache: Cache, Q, ws):
+def _cache_ws(where, op, cache: Cache, Q):
     _ranks(where, cache)
     if Q.dim() != 3:
         raise ValueError(f"{where}: Q must be bfloat16 [T, Hq, 128], got {Q.dtype} {tuple(Q.shape)}")
     _few_enough(where, "Q", Q)
-    if ws is not None:
-        return ws
     need = vca_cache_workspace_bytes(op, Q.shape[0], Q.shape[1], cache.k8.shape[1], *cache.table.shape)
     return torch.empty(need, dtype=torch.uint8, device=cache.k8.device) if need else None
 
@@ -541,7 +539,8 @@ def cache_attention(cache: Cache, Q, start, causal: bool = True, softmax_scale: 
                     out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
                     ws: Optional[torch.Tensor] = None, dev_status: Optional[torch.Tensor] = None):
     """Attention of Q [T, Hq, 128] over the cache.  Returns (O [T, Hq, 128], lse [T, Hq])."""
-    ws = _cache_ws("vca_cache_attention", VCA_OP_CACHE_ATTENTION, cache, Q, ws)
+    if ws is None:
+        ws = _cache_ws("vca_cache_attention", VCA_OP_CACHE_ATTENTION, cache, Q)
     O = out if out is not None else torch.empty(Q.shape, dtype=torch.bfloat16, device=Q.device)
     lse = lse if lse is not None else torch.empty(Q.shape[:2], dtype=torch.float32, device=Q.device)
     vca_cache_attention(cache, Q, start, causal, softmax_scale, softcap, O, lse, ws, dev_status)
@@ -554,8 +553,9 @@ def cache_weigh(cache: Cache, Q, start, lse, weight, causal: bool = True, softma
     """Adds to weight [pages, H, 128] the attention that each cached token gets
     from Q; lse is cache_attention's.  cache_append(weight=...) makes a new
     token's weight 0."""
-    vca_cache_weigh(cache, Q, start, causal, softmax_scale, softcap, lse, weight,
-                    _cache_ws("vca_cache_weigh", VCA_OP_CACHE_WEIGH, cache, Q, ws), dev_status)
+    if ws is None:
+        ws = _cache_ws("vca_cache_weigh", VCA_OP_CACHE_WEIGH, cache, Q)
+    vca_cache_weigh(cache, Q, start, causal, softmax_scale, softcap, lse, weight, ws, dev_status)
 
 
 def cache_evict(cache: Cache, weight, dst_table, budget: int, recent: int, kept: Optional[torch.Tensor] = None,
@@ -564,10 +564,10 @@ def cache_evict(cache: Cache, weight, dst_table, budget: int, recent: int, kept:
     dst_table.  Returns (new_len [B], kept [B, H, budget]); the cut sequences are
     Cache(k8, v8, sk, sv, dst_table, new_len)."""
     _ranks("vca_cache_evict", cache)
-    _cut(budget, recent)
     B, H = cache.table.shape[0], cache.k8.shape[1]
     new_len = torch.empty((B,), dtype=torch.int32, device=cache.k8.device)
     if kept is None:
+        _cut(budget, recent, 0)
         kept = torch.full((B, H, budget), -1, dtype=torch.int32, device=cache.k8.device)
     vca_cache_evict(cache, weight, dst_table, budget, recent, new_len, kept, dev_status)
     return new_len, kept

@@ -43,6 +43,8 @@ def test_ranks_are_named(V):
     for bad in (Q[0, 0], Q[0], Q[None], Q[0, 0, 0]):
         refuses("Q must be", lambda: V.cache_attention(c, bad, start))
         refuses("Q must be", lambda: V.cache_weigh(c, bad, start, lse, w))
+        refuses("Q must be", lambda: V.cache_attention(c, bad, start, ws=w))
+        refuses("Q must be", lambda: V.cache_weigh(c, bad, start, lse, w, ws=w))
         refuses("K must be", lambda: V.cache_append(c, bad, bad, start))
     refuses("weight must be", lambda: V.cache_weigh(c, Q, start, lse, w[0]))
     refuses("dst_table must be", lambda: V.cache_evict(c, w, dst[0], 200, 10))
