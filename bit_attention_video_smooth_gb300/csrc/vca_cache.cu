@@ -6,7 +6,7 @@
 // grows: only values that become subnormal round again.
 //
 // Both are bound by the bytes they move.  Append reads 4 and writes 2 bytes a
-// channel of K and V: 17,664 rows of 40 heads 86 us, 6.3 TB/s.  Evict reads every
+// channel of K and V: 17,664 rows of 40 heads 87 us, 6.2 TB/s.  Evict reads every
 // weight once and moves what stays: 4 x 8 heads of up to 32,768 tokens cut to
 // 4,096 in 41 us, the selection 20 and the move 23 (they overlap); a thousand tokens
 // in 11 us.

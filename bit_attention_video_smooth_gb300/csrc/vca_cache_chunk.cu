@@ -39,17 +39,18 @@
 // largest so far: values whose page's scale is below 2^-95 of that lose bits.
 // Every wait is bounded, as in vca_attention.cu.
 //
-// 4,416 rows over 70,656 tokens, 8 heads: 955 us, 1,338 TFLOP/s, the tensor pipe
-// 56 % busy: 280 tiles on 152 SMs keep 8 % of them idle, and in a page's 1,650
-// cycles (1,056 in the pipe) QK(b + 2) waits for PV(b) and that for the softmax.
-// Prompts of 2,900 rows behind short prefixes, causal, 32 heads over 8: 271 us, 847
+// 4,416 rows over 70,656 tokens, 8 heads: 979 us, 1,305 TFLOP/s (957 us in a loop of
+// nothing else), the tensor pipe 56 % busy: 280 tiles on 152 SMs keep 8 % of them
+// idle, and in a page's 1,650 cycles (1,056 in the pipe) QK(b + 2) waits for PV(b)
+// and that for the softmax.
+// Prompts of 2,900 rows behind short prefixes, causal, 32 heads over 8: 270 us, 850
 // TFLOP/s: a tile has 17 pages on average and 7,500 cycles of its own.  A cap
-// costs the softmax warps seven multiply-adds a score: 961 -> 1,844 us.
+// costs the softmax warps seven multiply-adds a score: 957 -> 1,823 us.
 // Measured and not kept: P in columns of its own, with Q's lo in shared memory
 // (1,030 us); one persistent CTA per SM with equal runs of pages (1,016; prompts
 // 513); probabilities before the halves' maxima meet (1,236); one issuer (1,066
 // against 988 at the time).  Few rows: 8 sequences of up to 16,383 tokens, 5 rows
-// each, 40 heads over 8, capped: 63 us (92 in tiles of 128), 2.7 TB/s.
+// each, 40 heads over 8, capped: 62 us (92 in tiles of 128), 2.7 TB/s.
 #include "vca_attention_common.cuh"
 #include "vca_cache.cuh"
 

@@ -334,6 +334,10 @@ int vca_cache_append_ex(const vca_cache *cache, const uint16_t *K, int64_t k_tok
  * below 2^-104.  A slot behind len may hold any bytes; a NaN among the values of a
  * sequence may reach every row of that sequence, one in a query row, or an
  * infinity, only that row.  Equal calls give equal bits.
+ * The kernel is chosen on the host for the whole call, by its average of
+ * T (Hq / H) / B rows a sequence and KV head (vca_cache_weigh's too): a batch that
+ * mixes single tokens with prompts, or has many sequences without rows, is
+ * right, and faster as calls of their own for those with one row and with many.
  */
 int vca_cache_attention(const vca_cache *cache, const uint16_t *Q, int64_t q_token, int64_t q_head,
                         const int32_t *start, int T, int Hq, int causal, float softmax_scale, float softcap,
