@@ -52,7 +52,7 @@ bool scores_ok(int causal, float softmax_scale, float softcap) {
 // The cap that the kernels get.  softcap tanh(s / softcap) is s to (s / softcap)^2 / 3:
 // from 2^40 on, to less than an fp32 rounding for scores below 2^28, and 0 (no cap)
 // it is.  Below 2^-40 all scores are 0 to 2^-40, as they are with a cap of 2^-40.
-// In between softmax_scale / softcap times a page scale stays a normal number.
+// In between softmax_scale / softcap times a page scale above 2^-80 is a normal number.
 float cap_used(float softcap) { return softcap >= 0x1p40f ? 0.0f : softcap > 0.0f ? std::fmax(softcap, 0x1p-40f) : 0.0f; }
 
 int from_cuda(cudaError_t e) { return e == cudaSuccess ? VCA_OK : VCA_ERR_CUDA; }

@@ -325,15 +325,16 @@ int vca_cache_append_ex(const vca_cache *cache, const uint16_t *K, int64_t k_tok
  * 1/sqrt(d); softcap = 0 caps nothing, and softmax_scale, softcap and softmax_scale
  * / softcap have to be below 8.5e37.  A cap of 2^40 or more counts as none (scores
  * below 2^28 change by less than an fp32 rounding), one below 2^-40 as 2^-40.  O is
- * bf16 [T][Hq][d] and lse fp32 [T][Hq] (may be NULL), both contiguous.  The products are exact but for query elements far below the
- * largest of their row (2^-30 of it) or of their 32 channels (2^-15, off by 2^-22 of
- * the largest, where a sequence has many rows); sums and statistics are fp32, the
- * probabilities enter the second product as fp16 (2^-12 relative, nothing below
- * 2^-25 of the row's largest); where a sequence has many rows, values of pages
- * whose sv is below 2^-95 of the sequence's largest lose bits and count as 0
- * below 2^-104.  A slot behind len may hold any bytes; a NaN among the values of a
- * sequence may reach every row of that sequence, one in a query row, or an
- * infinity, only that row.  Equal calls give equal bits.
+ * bf16 [T][Hq][d] and lse fp32 [T][Hq] (may be NULL), both contiguous.  The products
+ * are exact but for query elements far below the largest of their row (2^-30 of it)
+ * or of their 32 channels (2^-15, off by 2^-22 of the largest, where a sequence has
+ * many rows); sums and statistics are fp32, the probabilities enter the second
+ * product as fp16 (2^-12 relative, nothing below 2^-25 of the row's largest); where
+ * a sequence has many rows, values of pages whose sv is below 2^-95 of the
+ * sequence's largest lose bits and count as 0 below 2^-104.  A slot behind len may
+ * hold any bytes; a NaN among the values of a sequence may reach every row of that
+ * sequence, one in a query row, or an infinity, only that row.  Equal calls give
+ * equal bits.
  * The kernel is chosen on the host for the whole call, by its average of
  * T (Hq / H) / B rows a sequence and KV head (vca_cache_weigh's too): a batch that
  * mixes single tokens with prompts, or has many sequences without rows, is
