@@ -15,7 +15,8 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(BUILD, "libvca.so")
 SOURCES = ["vca_api.cu", "vca_group.cu", "vca_prep.cu", "vca_attention.cu", "vca_attention_fp4.cu", "vca_noalloc.cu",
-           "vca_cache.cu", "vca_cache_attention.cu", "vca_cache_chunk.cu", "vca_cache_weigh.cu"]
+           "vca_cache.cu", "vca_cache_attention.cu", "vca_cache_chunk.cu", "vca_cache_weigh.cu",
+           "vca_prompt.cu", "vca_plan.cu"]
 HEADERS = ["vca_device.cuh", "vca_attention_common.cuh", "vca_cache.cuh", "vca_internal.h"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr"]

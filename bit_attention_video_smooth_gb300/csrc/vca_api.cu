@@ -37,6 +37,11 @@ bool cache_ok(const vca_cache *c, vca::CacheView *view) {
 bool rows_ok(const uint16_t *p, int64_t tok, int64_t head) {
     return p && aligned16(p) && (tok & 7) == 0 && (head & 7) == 0;
 }
+// Rows that tensor maps describe: a distance of 0 between heads makes them one, tokens are apart.
+bool mapped_rows_ok(const uint16_t *p, int64_t tok, int64_t head, int T, int H) {
+    const int64_t most = static_cast<int64_t>(1) << 39;      // 2^40 bytes
+    return rows_ok(p, tok, head) && (T < 2 || (tok > 0 && tok < most)) && (H < 2 || (head >= 0 && head < most));
+}
 bool query_sizes_ok(int T, int Hq, int H) {
     return T >= 0 && Hq >= 1 && H >= 1 && Hq % H == 0 && static_cast<int64_t>(T) * Hq <= (static_cast<int64_t>(1) << 31) - 1;
 }
@@ -55,6 +60,12 @@ bool scores_ok(int causal, float softmax_scale, float softcap) {
 // In between softmax_scale / softcap times a page scale above 2^-80 is a normal number.
 float cap_used(float softcap) { return softcap >= 0x1p40f ? 0.0f : softcap > 0.0f ? std::fmax(softcap, 0x1p-40f) : 0.0f; }
 
+// Sizes of a page table: slots (page * 128 + place) and lengths fit an int32.
+bool pages_ok(int pages, int B, int cols) {
+    const int64_t most = (static_cast<int64_t>(1) << 31) - 1;
+    return pages >= 1 && B >= 1 && B <= 65535 && cols >= 1 && pages <= most / 128 && cols <= most / 128;
+}
+
 int from_cuda(cudaError_t e) { return e == cudaSuccess ? VCA_OK : VCA_ERR_CUDA; }
 
 }  // namespace
@@ -69,6 +80,7 @@ const char *vca_status_string(int status) {
         case VCA_ERR_CUDA: return "CUDA error";
         case VCA_ERR_TIMEOUT: return "device wait timed out";
         case VCA_ERR_WORKSPACE: return "workspace missing or too small";
+        case VCA_ERR_FULL: return "too few free pages";
         default: return "unknown status";
     }
 }
@@ -237,6 +249,53 @@ int vca_cache_evict(const vca_cache *cache, float *weight, const int32_t *dst_ta
     if (new_len == c.len || dst_table == c.table) return VCA_ERR_INVALID_ARG;
     return from_cuda(vca::launch_cache_evict(c, weight, dst_table, dst_cols, budget, recent, new_len, kept, dev_status,
                                              static_cast<cudaStream_t>(stream)));
+}
+
+int vca_prompt_attention(const uint16_t *Q, int64_t q_token, int64_t q_head, const uint16_t *K, int64_t k_token,
+                         int64_t k_head, const uint16_t *V, int64_t v_token, int64_t v_head, const int32_t *start, int B,
+                         int T, int Hq, int H, int d, int causal, float softmax_scale, float softcap,
+                         const uint16_t *prior, const float *prior_lse, uint16_t *O, float *lse, int32_t *dev_status,
+                         void *stream) {
+    if (B < 1 || d != 128 || !query_sizes_ok(T, Hq, H) || static_cast<int64_t>(B) * H > 65535 ||
+        !scores_ok(causal, softmax_scale, softcap))
+        return VCA_ERR_INVALID_ARG;
+    if (!start || !aligned4(start) || !aligned4(lse) || !aligned4(dev_status) || !prior != !prior_lse || !aligned16(prior) ||
+        !aligned4(prior_lse))
+        return VCA_ERR_INVALID_ARG;
+    if (T == 0) return VCA_OK;
+    if (!rows_ok(Q, q_token, q_head) || !mapped_rows_ok(K, k_token, k_head, T, H) || !mapped_rows_ok(V, v_token, v_head, T, H) ||
+        !O || !aligned16(O))
+        return VCA_ERR_INVALID_ARG;
+    vca::PromptArgs a{vca::CacheRows{Q, q_token, q_head}, vca::CacheRows{K, k_token, k_head}, vca::CacheRows{V, v_token, v_head},
+                      start, B, T, Hq, H, causal, scale_or_default(softmax_scale), cap_used(softcap), prior, prior_lse, O, lse,
+                      dev_status, g_wait_limit_ns};
+    return from_cuda(vca::launch_prompt_attention(a, static_cast<cudaStream_t>(stream)));
+}
+
+int vca_cache_plan(int32_t *table, int32_t *len, int pages, int B, int cols, const int32_t *held, const int32_t *news,
+                   int32_t *start, int32_t *slot, int32_t *position, int T, int32_t *dev_status, void *stream) {
+    if (!pages_ok(pages, B, cols) || T < 0) return VCA_ERR_INVALID_ARG;
+    const void *ptrs[] = {table, len, held, news, start};
+    for (const void *p : ptrs)
+        if (!p || !aligned4(p)) return VCA_ERR_INVALID_ARG;
+    if (!aligned4(slot) || !aligned4(position) || !aligned4(dev_status)) return VCA_ERR_INVALID_ARG;
+    // read by some CTAs while others write
+    if (news == len || start == len || start == held || start == news) return VCA_ERR_INVALID_ARG;
+    vca::PlanArgs a{table, len, pages, B, cols, held, news, start, slot, position, T, nullptr, 0, 0, dev_status};
+    return from_cuda(vca::launch_cache_plan(a, static_cast<cudaStream_t>(stream)));
+}
+
+int vca_cache_fresh(const int32_t *table, const int32_t *len, int pages, int B, int cols, int budget, int32_t *dst_table,
+                    int dst_cols, int32_t *dev_status, void *stream) {
+    if (!pages_ok(pages, B, cols) || budget < 1 || dst_cols < 1 || static_cast<int64_t>(dst_cols) * 128 < budget)
+        return VCA_ERR_INVALID_ARG;
+    const void *ptrs[] = {table, len, dst_table};
+    for (const void *p : ptrs)
+        if (!p || !aligned4(p)) return VCA_ERR_INVALID_ARG;
+    if (!aligned4(dev_status) || dst_table == table || dst_table == len) return VCA_ERR_INVALID_ARG;
+    vca::PlanArgs a{const_cast<int32_t *>(table), nullptr, pages, B, cols, len, nullptr, nullptr, nullptr, nullptr, 0,
+                    dst_table, dst_cols, budget, dev_status};
+    return from_cuda(vca::launch_cache_plan(a, static_cast<cudaStream_t>(stream)));
 }
 
 int vca_expcast_codes(const float *s_raw, const float *c, const float *m, int64_t n, uint8_t *out, void *stream) {

@@ -92,6 +92,34 @@ cudaError_t launch_cache_weigh(const CacheWeighArgs &a, cudaStream_t st);
 cudaError_t launch_cache_evict(const CacheView &c, float *weight, const int32_t *dst_table, int dst_cols, int budget,
                                int recent, int32_t *new_len, int32_t *kept, int32_t *dev_status, cudaStream_t st);
 
+// Attention of packed prompts over their own keys and values.
+struct PromptArgs {
+    CacheRows q, k, v;                 // [T][Hq][128], [T][H][128] twice
+    const int32_t *start;
+    int B, T, Hq, H, causal;
+    float scale, softcap;
+    const uint16_t *prior;             // [T][Hq][128] or null
+    const float *prior_lse;            // [T][Hq]
+    uint16_t *O;                       // [T][Hq][128]
+    float *lse;                        // [T][Hq] or null
+    int32_t *dev_status;
+    uint64_t wait_limit_ns;
+};
+cudaError_t launch_prompt_attention(const PromptArgs &a, cudaStream_t st);
+
+// The cache's pages (vca_cache_plan, vca_cache_fresh of include/vca.h).
+struct PlanArgs {
+    int32_t *table, *len;              // plan: written too
+    int pages, B, cols;
+    const int32_t *held, *news;        // plan; fresh: held alone, the lengths
+    int32_t *start, *slot, *position;  // plan
+    int T;
+    int32_t *fresh;                    // fresh: [B][fresh_cols], null for a plan
+    int fresh_cols, budget;
+    int32_t *dev_status;
+};
+cudaError_t launch_cache_plan(const PlanArgs &a, cudaStream_t st);
+
 cudaError_t launch_expcast_codes(const float *s_raw, const float *c, const float *m, int64_t n, uint8_t *out,
                                  cudaStream_t st);
 cudaError_t launch_e4m3_encode_bits(uint32_t start, int64_t n, uint8_t *out, cudaStream_t st);

@@ -18,7 +18,7 @@ import torch
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "_build", "libvca.so")
 
-VCA_OK, VCA_ERR_INVALID_ARG, VCA_ERR_UNSUPPORTED, VCA_ERR_CUDA, VCA_ERR_TIMEOUT, VCA_ERR_WORKSPACE = range(6)
+VCA_OK, VCA_ERR_INVALID_ARG, VCA_ERR_UNSUPPORTED, VCA_ERR_CUDA, VCA_ERR_TIMEOUT, VCA_ERR_WORKSPACE, VCA_ERR_FULL = range(7)
 VCA_V_E4M3, VCA_V_NVFP4 = 0, 1
 VCA_OP_GROUP, VCA_OP_PREP, VCA_OP_ATTENTION, VCA_OP_PREP_KSMOOTH = 0, 1, 2, 3
 VCA_OP_CACHE_ATTENTION, VCA_OP_CACHE_WEIGH = 4, 5
@@ -28,7 +28,7 @@ EXPORTS = ("vca_status_string", "vca_version", "vca_workspace_bytes", "vca_group
            "vca_attention", "vca_expcast_codes", "vca_e4m3_encode_bits", "vca_selftest_timeout",
            "vca_set_wait_limit_ns", "vca_prep_quant_noalloc", "vca_prep_quant_ex",
            "vca_cache_workspace_bytes", "vca_cache_append", "vca_cache_append_ex", "vca_cache_attention",
-           "vca_cache_weigh", "vca_cache_evict")
+           "vca_cache_weigh", "vca_cache_evict", "vca_cache_plan", "vca_cache_fresh", "vca_prompt_attention")
 
 if not os.path.exists(LIB_PATH):
     raise ImportError(f"libvca.so is not built ({LIB_PATH}); run __graft_entry__.build() -- "
@@ -64,6 +64,10 @@ _SIGS = {
     "vca_cache_attention": (_I, [_C, _P, _I64, _I64, _P, _I, _I, _I, _F, _F, _P, _P, _P, _SZ, _P, _P]),
     "vca_cache_weigh": (_I, [_C, _P, _I64, _I64, _P, _I, _I, _I, _F, _F, _P, _P, _P, _SZ, _P, _P]),
     "vca_cache_evict": (_I, [_C, _P, _P, _I, _I, _I, _P, _P, _P, _P]),
+    "vca_cache_plan": (_I, [_P, _P, _I, _I, _I, _P, _P, _P, _P, _P, _I, _P, _P]),
+    "vca_cache_fresh": (_I, [_P, _P, _I, _I, _I, _I, _P, _I, _P, _P]),
+    "vca_prompt_attention": (_I, [_P, _I64, _I64, _P, _I64, _I64, _P, _I64, _I64, _P, _I, _I, _I, _I, _I, _I, _F, _F,
+                                  _P, _P, _P, _P, _P, _P]),
 }
 for _name, (_res, _args) in _SIGS.items():
     _fn = getattr(_lib, _name)
@@ -425,8 +429,8 @@ def _cache_call(where, cache: Cache, rows, others, start=None, ws=None):
     return s, dev
 
 
-def _refuse(where, k8, seen, rows, ws):
-    """Names the first tensor of a call that is not as it must be."""
+def _refuse(where, k8, seen, rows, ws, first="k8"):
+    """Names the first tensor of a call that is not as it must be; `k8`, named `first`, is on the call's device."""
     T = None
     for name, t, heads in rows:
         _few_enough(where, name, t)
@@ -447,7 +451,7 @@ def _refuse(where, k8, seen, rows, ws):
         if not t.is_cuda:
             raise ValueError(f"{where}: {name} is not a CUDA tensor")
         if t.device != k8.device:
-            raise ValueError(f"{where}: tensors on several devices: {name} on {t.device}, k8 on {k8.device}")
+            raise ValueError(f"{where}: tensors on several devices: {name} on {t.device}, {first} on {k8.device}")
     raise ValueError(f"{where}: tensors that do not fit together")
 
 
@@ -571,3 +575,126 @@ def cache_evict(cache: Cache, weight, dst_table, budget: int, recent: int, kept:
         kept = torch.full((B, H, budget), -1, dtype=torch.int32, device=cache.k8.device)
     vca_cache_evict(cache, weight, dst_table, budget, recent, new_len, kept, dev_status)
     return new_len, kept
+
+
+# ---------------------------------------------------------------------------
+# The cache's pages, and prompts on their way into it (include/vca.h)
+# ---------------------------------------------------------------------------
+def _ints_call(where, cache: Cache, ints):
+    """Checks that every tensor (name, tensor or None, shape) of a planning call is int32, contiguous, of its shape and on
+    one CUDA device, which is returned."""
+    if cache.table.dim() != 2 or cache.k8.dim() != 4 or max(cache.k8.shape[0], *cache.table.shape) > _MOST:
+        raise ValueError(f"{where}: k8 must be [pages, H, 128, 128] and table [B, cols]")
+    dev = cache.table.get_device()
+    ok = dev >= 0
+    for _, t, shape in ints:
+        ok = ok and (t is None or (t.dtype is torch.int32 and t.shape == shape and t.get_device() == dev and t.is_contiguous()))
+    if not ok:
+        given = [x for x in ints if x[1] is not None]
+        for name, t, shape in given:
+            _typed(where, name, t, torch.int32, shape)
+        for name, t, _ in given:
+            if not t.is_cuda:
+                raise ValueError(f"{where}: {name} is not a CUDA tensor")
+            if t.device != cache.table.device:
+                raise ValueError(f"{where}: tensors on several devices: {name} on {t.device}, table on {cache.table.device}")
+        raise ValueError(f"{where}: tensors that do not fit together")
+    return dev
+
+
+def vca_cache_plan(cache: Cache, held, news, T: int, start, slot, position, dev_status=None, stream=None) -> None:
+    if not 0 <= T <= _MOST:
+        raise ValueError(f"vca_cache_plan: T = {T} must be 0 .. {_MOST}")
+    B = cache.table.shape[0] if cache.table.dim() else 0
+    dev = _ints_call("vca_cache_plan", cache, (
+        ("table", cache.table, cache.table.shape), ("length", cache.length, (B,)), ("held", held, (B,)), ("news", news, (B,)),
+        ("start", start, (B + 1,)), ("slot", slot, (T,)), ("position", position, (T,)), ("dev_status", dev_status, (1,))))
+    _launch("vca_cache_plan", dev, _lib.vca_cache_plan, cache.table.data_ptr(), cache.length.data_ptr(), cache.k8.shape[0], B,
+            cache.table.shape[1], held.data_ptr(), news.data_ptr(), start.data_ptr(), _at(slot), _at(position), T,
+            _at(dev_status), stream=stream)
+
+
+def vca_cache_fresh(cache: Cache, budget: int, dst_table, dev_status=None, stream=None) -> None:
+    if dst_table.dim() != 2:
+        raise ValueError("vca_cache_fresh: dst_table must be [B, dst_cols]")
+    if not (-_MOST <= budget <= _MOST and dst_table.shape[1] <= _MOST):
+        raise ValueError(f"vca_cache_fresh: budget {budget} and dst_cols {dst_table.shape[1]} must fit 32 bits")
+    B = cache.table.shape[0] if cache.table.dim() else 0
+    dev = _ints_call("vca_cache_fresh", cache, (
+        ("table", cache.table, cache.table.shape), ("length", cache.length, (B,)),
+        ("dst_table", dst_table, (B, dst_table.shape[1])), ("dev_status", dev_status, (1,))))
+    _launch("vca_cache_fresh", dev, _lib.vca_cache_fresh, cache.table.data_ptr(), cache.length.data_ptr(), cache.k8.shape[0], B,
+            cache.table.shape[1], budget, dst_table.data_ptr(), dst_table.shape[1], _at(dev_status), stream=stream)
+
+
+def cache_plan(cache: Cache, news, T: int, held: Optional[torch.Tensor] = None, start: Optional[torch.Tensor] = None,
+               slot: Optional[torch.Tensor] = None, position: Optional[torch.Tensor] = None,
+               dev_status: Optional[torch.Tensor] = None):
+    """Pages, lengths and places for news [B] new tokens of each sequence behind
+    the held [B] ones (cache.length, which becomes their sum); T is how many rows the
+    call will have room for.  Returns (start [B + 1], slot [T], position [T]); slot
+    and position are -1 behind the last row where they are made here.  With too few
+    free pages (dev_status: VCA_ERR_FULL) start is 0 throughout and nothing changes."""
+    new = lambda n, fill: torch.full((n,), fill, dtype=torch.int32, device=cache.table.device)
+    if T < 0 or T > _MOST or cache.table.dim() != 2:
+        raise ValueError(f"vca_cache_plan: T = {T} must be 0 .. {_MOST} and table [B, cols]")
+    start = torch.empty((cache.table.shape[0] + 1,), dtype=torch.int32, device=cache.table.device) if start is None else start
+    slot = new(T, -1) if slot is None else slot
+    position = new(T, -1) if position is None else position
+    vca_cache_plan(cache, cache.length if held is None else held, news, T, start, slot, position, dev_status)
+    return start, slot, position
+
+
+def cache_fresh(cache: Cache, budget: int, out: Optional[torch.Tensor] = None, dev_status: Optional[torch.Tensor] = None):
+    """Free pages for cache_evict to `budget` tokens: its dst_table [B, ceil(budget / 128)],
+    -1 where a sequence needs none."""
+    if out is None:
+        if cache.table.dim() != 2 or not 1 <= budget <= _MOST:
+            raise ValueError(f"vca_cache_fresh: budget {budget} must be 1 .. {_MOST} and table [B, cols]")
+        out = torch.full((cache.table.shape[0], -(-budget // 128)), -1, dtype=torch.int32, device=cache.table.device)
+    vca_cache_fresh(cache, budget, out, dev_status)
+    return out
+
+
+def vca_prompt_attention(Q, K, V, start, causal: int, softmax_scale: float, softcap: float, prior, prior_lse, O, lse,
+                         dev_status=None, stream=None) -> None:
+    if Q.dim() != 3 or K.dim() != 3 or start.dim() != 1:
+        raise ValueError(f"vca_prompt_attention: Q must be bfloat16 [T, Hq, 128], K and V [T, H, 128] and start int32 [B + 1], "
+                         f"got {tuple(Q.shape)}, {tuple(K.shape)} and {tuple(start.shape)}")
+    (T, Hq, _), H, B = Q.shape, K.shape[1], start.shape[0] - 1
+    dev = Q.get_device()
+    rows = (("Q", Q, Hq), ("K", K, H), ("V", V, H))
+    seen = [("start", start, torch.int32, (B + 1,)), ("O", O, torch.bfloat16, (T, Hq, 128))]
+    if lse is not None:
+        seen.append(("lse", lse, torch.float32, (T, Hq)))
+    if prior is not None or prior_lse is not None:
+        if prior is None or prior_lse is None:
+            raise ValueError("vca_prompt_attention: prior and prior_lse are given together")
+        seen += [("prior", prior, torch.bfloat16, (T, Hq, 128)), ("prior_lse", prior_lse, torch.float32, (T, Hq))]
+    if dev_status is not None:
+        seen.append(("dev_status", dev_status, torch.int32, (1,)))
+    ok = dev >= 0 and max(T, Hq, H, B) <= _MOST
+    for _, t, dtype, shape in seen:
+        ok = ok and t.dtype is dtype and t.shape == shape and t.get_device() == dev and t.is_contiguous()
+    for _, t, heads in rows:
+        ok = ok and t.dtype is torch.bfloat16 and t.shape == (T, heads, 128) and t.stride(2) == 1 and t.get_device() == dev
+    if not ok:
+        _few_enough("vca_prompt_attention", "start", start)
+        _refuse("vca_prompt_attention", Q, seen, rows, None, "Q")
+    _launch("vca_prompt_attention", dev, _lib.vca_prompt_attention, Q.data_ptr(), Q.stride(0), Q.stride(1), K.data_ptr(),
+            K.stride(0), K.stride(1), V.data_ptr(), V.stride(0), V.stride(1), start.data_ptr(), B, T, Hq, H, 128, int(causal),
+            softmax_scale, softcap, _at(prior), _at(prior_lse), O.data_ptr(), _at(lse), _at(dev_status), stream=stream)
+
+
+def prompt_attention(Q, K, V, start, causal: bool = True, softmax_scale: float = 0.0, softcap: float = 0.0, prior=None,
+                     out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
+                     dev_status: Optional[torch.Tensor] = None):
+    """Attention of packed prompts Q [T, Hq, 128] over their own K, V [T, H, 128]; sequence
+    b owns the rows start[b] .. start[b+1] - 1.  `prior`, the (O, lse) of an attention
+    over what came before (cache_attention's), is joined in.  Returns (O [T, Hq, 128],
+    lse [T, Hq])."""
+    O = out if out is not None else torch.empty(Q.shape, dtype=torch.bfloat16, device=Q.device)
+    lse = lse if lse is not None else torch.empty(Q.shape[:2], dtype=torch.float32, device=Q.device)
+    before, before_lse = prior if prior is not None else (None, None)
+    vca_prompt_attention(Q, K, V, start, causal, softmax_scale, softcap, before, before_lse, O, lse, dev_status)
+    return O, lse

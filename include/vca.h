@@ -60,7 +60,8 @@ typedef enum {
     VCA_ERR_UNSUPPORTED = 2,   /* a combination the method does not define */
     VCA_ERR_CUDA = 3,          /* a CUDA runtime call or launch failed */
     VCA_ERR_TIMEOUT = 4,       /* a bounded device wait ran out (dev_status) */
-    VCA_ERR_WORKSPACE = 5      /* workspace missing or smaller than required */
+    VCA_ERR_WORKSPACE = 5,     /* workspace missing or smaller than required */
+    VCA_ERR_FULL = 6           /* too few free pages (dev_status of the cache's planning) */
 } vca_status;
 
 typedef enum { VCA_V_E4M3 = 0, VCA_V_NVFP4 = 1 } vca_vmode;
@@ -375,6 +376,74 @@ int vca_cache_weigh(const vca_cache *cache, const uint16_t *Q, int64_t q_token, 
  */
 int vca_cache_evict(const vca_cache *cache, float *weight, const int32_t *dst_table, int dst_cols, int budget,
                     int recent, int32_t *new_len, int32_t *kept, int32_t *dev_status, void *stream);
+
+/*
+ * vca_cache_plan -- places for the new tokens of the cache's next call, from the
+ * sequences' lengths: `held` int32 [B], the tokens of each sequence before (may be
+ * `len` itself), and `news` int32 [B], how many arrive.
+ *   table   the columns ceil(held / 128) .. ceil((held + news) / 128) - 1 of each
+ *           sequence get pages, the lowest free ones in the order of the
+ *           sequences and columns; other entries stay as they are
+ *   len     held + news
+ *   start   int32 [B + 1], the sums of news: it cuts the call's rows
+ *   slot, position (int32 [T], each may be NULL): row t = start[b] + i is token
+ *           position = held + i of its sequence, in slot = page * 128 + position
+ *           % 128 of the pool (-1 where the page does not exist); those of rows
+ *           behind start[B] stay as they are
+ * Free is a page that no live table entry names, live being the columns below
+ * ceil(held / 128): no list is kept, a length of 0 gives a sequence's pages back, and
+ * a page that sequences share is free when the last of them is gone.  A live
+ * entry outside 0 .. pages - 1 names none; it is reported where pages are given out.
+ * A plan is made whole or not at all: if held or news is negative or their sum
+ * above cols*128 anywhere, or the news sum up to more than T (dev_status =
+ * VCA_ERR_INVALID_ARG), or the free pages are too few (VCA_ERR_FULL), start becomes
+ * 0 throughout, so that its rows belong to nobody, and all else stays as it was.
+ * Sizes: B <= 65,535, pages*128 and cols*128 <= 2^31 - 1, T >= 0.  news is not len, and
+ * start none of len, held and news (refused).
+ */
+int vca_cache_plan(int32_t *table, int32_t *len, int pages, int B, int cols, const int32_t *held, const int32_t *news,
+                   int32_t *start, int32_t *slot, int32_t *position, int T, int32_t *dev_status, void *stream);
+
+/*
+ * vca_cache_fresh -- the pages that vca_cache_evict writes: columns 0 ..
+ * ceil(min(len, budget) / 128) - 1 of every row of dst_table int32 [B][dst_cols] get
+ * free pages, as in vca_cache_plan with held = len; other entries stay as they
+ * are.  Whole or not at all, likewise: dst_table is left as it was where a length
+ * is out of range or the free pages are too few.  Requires budget >= 1 and
+ * dst_cols*128 >= budget; dst_table is neither table nor len (refused).
+ */
+int vca_cache_fresh(const int32_t *table, const int32_t *len, int pages, int B, int cols, int budget, int32_t *dst_table,
+                    int dst_cols, int32_t *dev_status, void *stream);
+
+/*
+ * vca_prompt_attention -- attention of packed prompts over their own keys and
+ * values as they are, bf16, before they are quantised into the cache: Q [T][Hq][d],
+ * K and V [T][H][d], d = 128, all three cut by start[B + 1]; query heads h*G .. h*G + G - 1
+ * read KV head h, G = Hq / H.  Row i of a sequence's n:
+ *   s_ij = softmax_scale q_i . k_j;  with softcap > 0: softcap tanh(s_ij / softcap)
+ *   j visible to row i: j < n, and with causal = 1: j <= i
+ *   O_i = sum_j softmax_j(s_ij) v_j,  lse_i = ln sum_j exp(s_ij)
+ * With `prior` bf16 [T][Hq][d] and prior_lse fp32 [T][Hq], both contiguous (NULL:
+ * none), the result is joined with an attention of the same rows over other tokens,
+ * such as vca_cache_attention's over what the sequence held before the chunk:
+ *   lse_i = ln(sum_j exp(s_ij) + exp(prior_lse_i)),
+ *   O_i = (sum_j exp(s_ij) v_j + exp(prior_lse_i) prior_i) / exp(lse_i)
+ * in fp32 with one rounding of O; where prior_lse is -inf, prior is not read.  O may be
+ * prior, and lse prior_lse; other outputs must not overlap the inputs.
+ * Scale, cap, start, rows behind start[B], strides, O, lse, T = 0 and dev_status as in
+ * vca_cache_attention.  Where T > 1 the distance between tokens of K and V is above 0,
+ * and where H > 1 that between heads not below (0: all heads are one); below 2^39.
+ * B*H <= 65,535, T*Hq <= 2^31 - 1.
+ * The products of bf16 values are exact, sums and statistics fp32; the
+ * probabilities enter the second product as bf16 (2^-9 relative).  A NaN or an infinity
+ * among the values of a sequence may reach every row of that sequence, one in a
+ * key or query only the rows that see it.  Equal calls give equal bits.  No workspace.
+ */
+int vca_prompt_attention(const uint16_t *Q, int64_t q_token, int64_t q_head, const uint16_t *K, int64_t k_token,
+                         int64_t k_head, const uint16_t *V, int64_t v_token, int64_t v_head, const int32_t *start, int B,
+                         int T, int Hq, int H, int d, int causal, float softmax_scale, float softcap,
+                         const uint16_t *prior, const float *prior_lse, uint16_t *O, float *lse, int32_t *dev_status,
+                         void *stream);
 
 #ifdef __cplusplus
 }
