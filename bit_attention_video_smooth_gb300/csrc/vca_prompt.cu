@@ -10,9 +10,11 @@
 // smem).  While one tile's softmax runs the tensor core works for the other.
 // Warps:
 //   0      TMA producer: K and V blocks alternate in a ring of five
-//   1      MMA issuer, one thread: PV of a block and QK of the next, tile by tile.
-//          MMAs of one thread and shape run in order, so QK may write the scores
-//          over the probabilities that the PV before it reads
+//   1      MMA issuer: PV of a block and QK of the next, tile by tile.  MMAs of one
+//          thread and shape run in order, so QK may write the scores over the
+//          probabilities that the PV before it reads.  The whole warp waits and one
+//          thread of it, elected, issues: then the operands are in uniform registers,
+//          and an MMA takes 10 to 20 cycles to issue (46 from a branch on the lane)
 //   2      zeroes the rows of V behind the sequence's last token (they are another
 //          sequence's, and may hold NaN) and only then reports that block as full
 //   4-11   softmax, four warps a tile, a thread a row.  The reference maximum moves
@@ -37,7 +39,7 @@ constexpr uint32_t kTmemS = 0, kTmemO = 256, kTmemCols = 512;
 constexpr uint32_t kOffQ = 0;
 constexpr uint32_t kOffKV = kOffQ + kTiles * kBlock;
 constexpr uint32_t kOffBar = kOffKV + kStages * kBlock;
-constexpr int kNumBars = 2 * kStages + 4 * kTiles + 2;
+constexpr int kNumBars = 2 * kStages + 5 * kTiles + 2;
 constexpr uint32_t kOffMisc = kOffBar + kNumBars * 8;
 constexpr uint32_t kSmem = kOffMisc + 16 + 1024;
 static_assert(kSmem <= 232448, "shared memory budget");
@@ -63,6 +65,13 @@ __device__ __forceinline__ void tma_load_3d(void *smem_dst, const void *tmap, ui
             smem_u32(smem_dst)),
         "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
         : "memory");
+}
+
+// True in one thread of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}\n" : "=r"(r));
+    return r != 0;
 }
 
 // ---------------------------------------------------------------------------
@@ -226,13 +235,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     unsigned char *smem =
         reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint64_t *full = reinterpret_cast<uint64_t *>(smem + kOffBar), *empty = full + kStages;
-    uint64_t *q_full = empty + kStages, *s_full = q_full + kTiles, *p_full = s_full + kTiles, *o_full = p_full + kTiles;
+    uint64_t *q_full = empty + kStages, *s_full = q_full + kTiles, *p_full = s_full + kTiles, *o_full = p_full + 2 * kTiles;
     uint64_t *raw = o_full + kTiles, *drain = raw + 1;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + kOffMisc);
     int *abort_flag = reinterpret_cast<int *>(smem + kOffMisc + 4);
     int *first_fall = reinterpret_cast<int *>(smem + kOffMisc + 8);
 
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const int rank = static_cast<int>(blockIdx.x / p.H), h = static_cast<int>(blockIdx.x % p.H);
     Work w;
     // every warp finds the CTA's tile for itself
@@ -256,7 +265,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int t = 0; t < kTiles; ++t) {
             mbar_init(q_full + t, 4);
             mbar_init(s_full + t, 1);
-            mbar_init(p_full + t, 4);
+            mbar_init(p_full + 2 * t, 4);
+            mbar_init(p_full + 2 * t + 1, 4);
             mbar_init(o_full + t, 1);
         }
         mbar_init(raw, 1);
@@ -304,56 +314,70 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         } else if (warp == 1) {
             // -------------------------------------------------------- MMA issuer
-            if (lane == 0) {
-                constexpr uint32_t idesc_qk = make_idesc(128, 128, 1, 1), idesc_pv = make_idesc(128, 128, 1, 1, 0, 1);
-                const uint32_t base = smem_u32(smem);
-                auto qk = [&](int t, int st) {
-                    const uint64_t dq = sdesc_k_sw128(base + kOffQ + t * kBlock), dk = sdesc_k_sw128(base + kOffKV + st * kBlock);
+            constexpr uint32_t idesc_qk = make_idesc(128, 128, 1, 1), idesc_pv = make_idesc(128, 128, 1, 1, 0, 1);
+            const uint32_t base = smem_u32(smem);
+            const bool one = elect_one();
+            auto wait = [&](uint64_t *bar, int parity) {
+                const bool ok = __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, p.limit_ns));
+                tc_fence_after();
+                return ok;
+            };
+            auto qk = [&](int t, int st) {
+                const uint64_t dq = sdesc_k_sw128(base + kOffQ + t * kBlock), dk = sdesc_k_sw128(base + kOffKV + st * kBlock);
+                if (one) {
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
                         const uint32_t step = (i >> 2) * (kPanel >> 4) + 2 * (i & 3);
                         mma_f16(tmem + kTmemS + 128 * t, dq + step, dk + step, idesc_qk, i > 0);
                     }
                     tc_commit(s_full + t);
-                };
-                auto pv = [&](int t, int st, bool first) {
-                    const uint64_t dv = sdesc_mn_sw128(base + kOffKV + st * kBlock, kPanel);
+                }
+            };
+            auto pv = [&](int t, int st, int half, bool first) {      // of 64 keys
+                const uint64_t dv = sdesc_mn_sw128(base + kOffKV + st * kBlock, kPanel);
+                if (one) {
 #pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        mma_f16_ts(tmem + kTmemO + 128 * t, tmem + kTmemS + 128 * t + 8 * i, dv + (2048 >> 4) * i, idesc_pv,
-                                   !first || i > 0);
-                };
-                bool ok = mbar_wait(full, 0, abort_flag, p.limit_ns);
-                for (int t = 0; ok && t < kTiles; ++t) {
-                    if (t == 1 && nb1 == 0) break;
-                    ok = mbar_wait(q_full + t, 0, abort_flag, p.limit_ns);
-                    if (!ok) break;
-                    tc_fence_after();
-                    qk(t, 0);
+                    for (int i = 0; i < 4; ++i)
+                        mma_f16_ts(tmem + kTmemO + 128 * t, tmem + kTmemS + 128 * t + 32 * half + 8 * i,
+                                   dv + (2048 >> 4) * (4 * half + i), idesc_pv, !first || i > 0);
                 }
-                tc_commit(empty);
-                for (int j = 0; ok && j < nbs; ++j) {
-                    const int iv = 2 * j + 1, ik = 2 * j + 2, sv = iv % kStages, sk = ik % kStages;
-                    ok = mbar_wait(full + sv, (iv / kStages) & 1, abort_flag, p.limit_ns);
-                    if (ok && j + 1 < nbs) ok = mbar_wait(full + sk, (ik / kStages) & 1, abort_flag, p.limit_ns);
-                    for (int t = 0; ok && t < kTiles; ++t) {
-                        const int last = t ? nb1 : nb0;
-                        if (j >= last) continue;
-                        ok = mbar_wait(p_full + t, j & 1, abort_flag, p.limit_ns);
-                        if (!ok) break;
-                        tc_fence_after();
-                        pv(t, sv, j == 0);
-                        if (t == 1 || j >= nb1) tc_commit(empty + sv);
-                        if (j + 1 < last)
-                            qk(t, sk);
-                        else
-                            tc_commit(o_full + t);
-                    }
-                    if (ok && j + 1 < nbs) tc_commit(empty + sk);
-                }
-                tc_commit(drain);
-                drain_wait(drain, 0, p.limit_ns);
+            };
+            auto commit = [&](uint64_t *bar) {
+                if (one) tc_commit(bar);
+            };
+            bool ok = wait(full, 0);
+#pragma unroll
+            for (int t = 0; t < kTiles; ++t) {
+                if (!ok || (t == 1 && nb1 == 0)) break;
+                ok = wait(q_full + t, 0);
+                if (ok) qk(t, 0);
             }
+            commit(empty);
+            for (int j = 0; ok && j < nbs; ++j) {
+                const int iv = 2 * j + 1, ik = 2 * j + 2, sv = iv % kStages, sk = ik % kStages;
+                ok = wait(full + sv, (iv / kStages) & 1);
+                if (ok && j + 1 < nbs) ok = wait(full + sk, (ik / kStages) & 1);
+#pragma unroll
+                for (int t = 0; t < kTiles; ++t) {
+                    const int last = t ? nb1 : nb0;
+                    if (!ok || j >= last) continue;
+                    ok = wait(p_full + 2 * t, j & 1);
+                    if (!ok) break;
+                    pv(t, sv, 0, j == 0);
+                    ok = wait(p_full + 2 * t + 1, j & 1);
+                    if (!ok) break;
+                    pv(t, sv, 1, false);
+                    if (t == 1 || j >= nb1) commit(empty + sv);
+                    if (j + 1 < last)
+                        qk(t, sk);
+                    else
+                        commit(o_full + t);
+                }
+                if (ok && j + 1 < nbs) commit(empty + sk);
+            }
+            commit(drain);
+            if (one) drain_wait(drain, 0, p.limit_ns);
+            __syncwarp();
         } else if (warp == 2 && tail >= 0) {
             // -------------------------------------------------------- rows of V behind the sequence
             const int st = (2 * tail + 1) % kStages, live = w.n - tail * kBlk;
@@ -446,15 +470,18 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    uint32_t W[16];
-                    probabilities<kCap>(X[i], s, 32 * i, l2, W);
-                    VCA_TMEM_ST16(tS + 16 * i, W);
+                for (int half = 0; half < 2; ++half) {
+#pragma unroll
+                    for (int i = 2 * half; i < 2 * half + 2; ++i) {
+                        uint32_t W[16];
+                        probabilities<kCap>(X[i], s, 32 * i, l2, W);
+                        VCA_TMEM_ST16(tS + 16 * i, W);
+                    }
+                    tmem_st_wait();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(p_full + 2 * t + half);
                 }
-                tmem_st_wait();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(p_full + t);
             }
             // -------------------------------------------------------- epilogue
             if (ok) ok = __all_sync(0xffffffffu, mbar_wait(o_full + t, 0, abort_flag, p.limit_ns));
