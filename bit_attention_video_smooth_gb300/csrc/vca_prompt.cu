@@ -39,8 +39,10 @@ constexpr uint32_t kTmemS = 0, kTmemO = 256, kTmemCols = 512;
 constexpr uint32_t kOffQ = 0;
 constexpr uint32_t kOffKV = kOffQ + kTiles * kBlock;
 constexpr uint32_t kOffBar = kOffKV + kStages * kBlock;
-constexpr int kNumBars = 2 * kStages + 5 * kTiles + 2;
-constexpr uint32_t kOffMisc = kOffBar + kNumBars * 8;
+constexpr int kWorks = 2;                            // slots for what the CTA does now and next
+constexpr int kNumBars = 3 * kStages + 8 * kTiles + 2 * kWorks + 1;
+constexpr uint32_t kOffWork = (kOffBar + kNumBars * 8 + 15) / 16 * 16;
+constexpr uint32_t kOffMisc = kOffWork + kWorks * 16;
 constexpr uint32_t kSmem = kOffMisc + 16 + 1024;
 static_assert(kSmem <= 232448, "shared memory budget");
 
@@ -48,12 +50,14 @@ struct PromptParams {
     CacheRows q;
     const int32_t *start;
     int B, T, Hq, H, G, causal;
+    int64_t items;                          // (tile, head) pairs at most
     float scale_log2, cap_in, cap_out;      // as in AttnParams
     bool k_tokens, v_tokens;                // the tensor map's middle dimension: tokens, else heads
     int k_heads, v_heads;                   // 1, or 0: all heads are the same
     const uint16_t *prior;
     const float *prior_lse;
     uint16_t *O;
+    bool wide;                              // O is 32-byte aligned
     float *lse;
     int32_t *dev_status;
     uint64_t limit_ns;
@@ -67,6 +71,13 @@ __device__ __forceinline__ void tma_load_3d(void *smem_dst, const void *tmap, ui
         : "memory");
 }
 
+#define VCA_TMEM_LD16(taddr, r)                                                                                   \
+    asm volatile(                                                                                                 \
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"  \
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),         \
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])    \
+        : "r"(taddr))
+
 // True in one thread of a converged warp.
 __device__ __forceinline__ bool elect_one() {
     uint32_t r;
@@ -75,52 +86,60 @@ __device__ __forceinline__ bool elect_one() {
 }
 
 // ---------------------------------------------------------------------------
-// Which tile a CTA takes
+// Which tiles a CTA takes
 // ---------------------------------------------------------------------------
-// Rows [row0, row0 + n) of a sequence, and which 256 of its n G.
+// 256 of the rows of a (sequence, KV head): its tokens [row0, row0 + n), and which;
+// n = 0: there is no more work.
 struct Work {
-    int row0, n, tile;
+    int row0, n, tile, h;
 };
 __device__ __forceinline__ int tiles_of(int n, int G) {
     return static_cast<int>((static_cast<int64_t>(n) * G + kTileRows - 1) / kTileRows);
 }
 
-// Up to kSortable sequences: the tiles by their number of key blocks, most first,
-// so that the last wave's are short.  A causal tile's number grows with its
-// place in the sequence, another's is the sequence's.  F(c) tiles have a cost
-// above c; a warp evaluates it over sequences that it holds in registers.
+// Up to kSortable sequences: the tiles by their number of key blocks, most first.  A
+// causal tile's number grows with its place in the sequence, another's is the
+// sequence's.  The CTAs then take turns, there and back, and have done about the same at the
+// end.  A warp holds the sequences in registers.
 constexpr int kHeld = 8, kSortable = 32 * kHeld;
-__device__ bool find_sorted(const PromptParams &p, int rank, Work &w) {
+struct Sorted {
+    int lo[kHeld], n[kHeld], q[kHeld], most;
+};
+__device__ __forceinline__ void load_sorted(const PromptParams &p, Sorted &s) {
     const int lane = threadIdx.x & 31;
-    int q[kHeld], lo[kHeld], hi[kHeld], most = 0;
-    bool fell = false;
+    int hi[kHeld];
 #pragma unroll
     for (int k = 0; k < kHeld; ++k) {
         const int b = 32 * k + lane;
-        lo[k] = hi[k] = 0;
+        s.lo[k] = hi[k] = 0;
         if (b < p.B) {
-            lo[k] = p.start[b];
+            s.lo[k] = p.start[b];
             hi[k] = p.start[b + 1];
         }
     }
+    bool fell = false;
+    s.most = 0;
 #pragma unroll
     for (int k = 0; k < kHeld; ++k) {
-        const uint32_t falls = __ballot_sync(0xffffffffu, lo[k] < 0 || hi[k] < lo[k] || hi[k] > p.T);
-        if (fell || (falls & ((2u << lane) - 1u))) hi[k] = lo[k];
+        const uint32_t falls = __ballot_sync(0xffffffffu, s.lo[k] < 0 || hi[k] < s.lo[k] || hi[k] > p.T);
+        s.n[k] = fell || (falls & ((2u << lane) - 1u)) ? 0 : hi[k] - s.lo[k];
         fell = fell || falls != 0;
-        q[k] = tiles_of(hi[k] - lo[k], p.G);
-        most = max(most, q[k]);
+        s.q[k] = tiles_of(s.n[k], p.G);
+        s.most = max(s.most, s.q[k]);
     }
-    if (rank == 0 && blockIdx.x == 0 && lane == 0 && fell) report(p.dev_status, kErrInvalid);
-    most = __reduce_max_sync(0xffffffffu, most);
-    auto above = [&](int c) {
+    if (blockIdx.x == 0 && lane == 0 && fell) report(p.dev_status, kErrInvalid);
+    s.most = __reduce_max_sync(0xffffffffu, s.most);
+}
+__device__ __forceinline__ bool find_sorted(const PromptParams &p, const Sorted &s, int rank, Work &w) {
+    const int lane = threadIdx.x & 31;
+    auto above = [&](int c) {      // tiles of a cost above c
         int f = 0;
 #pragma unroll
-        for (int k = 0; k < kHeld; ++k) f += p.causal ? max(0, q[k] - c) : q[k] > c ? q[k] : 0;
+        for (int k = 0; k < kHeld; ++k) f += p.causal ? max(0, s.q[k] - c) : s.q[k] > c ? s.q[k] : 0;
         return static_cast<int>(__reduce_add_sync(0xffffffffu, f));
     };
     if (above(0) <= rank) return false;
-    int a = 0, z = most;      // F(a) > rank >= F(z)
+    int a = 0, z = s.most;      // above(a) > rank >= above(z)
     while (z - a > 1) {
         const int mid = a + (z - a) / 2;
         if (above(mid) > rank)
@@ -128,10 +147,10 @@ __device__ bool find_sorted(const PromptParams &p, int rank, Work &w) {
         else
             z = mid;
     }
-    int left = rank - above(z);      // among the tiles of cost a, in the sequences' order
+    int left = rank - above(z);      // among the tiles of cost a + 1, in the sequences' order
 #pragma unroll
     for (int k = 0; k < kHeld; ++k) {
-        const int has = p.causal ? (q[k] > a) : q[k] == a + 1 ? q[k] : 0;
+        const int has = p.causal ? (s.q[k] > a) : s.q[k] == a + 1 ? s.q[k] : 0;
         int incl = has;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -141,8 +160,8 @@ __device__ bool find_sorted(const PromptParams &p, int rank, Work &w) {
         const uint32_t hit = __ballot_sync(0xffffffffu, left < incl);
         if (hit) {
             const int l = __ffs(hit) - 1;
-            w.row0 = __shfl_sync(0xffffffffu, lo[k], l);
-            w.n = __shfl_sync(0xffffffffu, hi[k], l) - w.row0;
+            w.row0 = __shfl_sync(0xffffffffu, s.lo[k], l);
+            w.n = __shfl_sync(0xffffffffu, s.n[k], l);
             w.tile = p.causal ? a : left - __shfl_sync(0xffffffffu, incl - has, l);
             return true;
         }
@@ -152,32 +171,36 @@ __device__ bool find_sorted(const PromptParams &p, int rank, Work &w) {
 }
 
 // More sequences: sequence b's tiles are those from floor(start G / 256) + b on, which
-// leaves room for each sequence's and is found by search.  All threads; first checks
-// that start rises up to there, since nothing behind a fall has rows.
-__device__ bool find_searched(const PromptParams &p, int index, int *first_fall, Work &w) {
-    if (threadIdx.x == 0) *first_fall = p.B;
-    __syncthreads();
-    for (int b = threadIdx.x; b < p.B; b += kThreads) {
-        const int lo = p.start[b], hi = p.start[b + 1];
-        if (lo < 0 || hi < lo || hi > p.T) atomicMin(first_fall, b);
-    }
-    __syncthreads();
-    const int rise = *first_fall;      // sequences 0 .. rise - 1 are right
-    if (index == 0 && blockIdx.x == 0 && threadIdx.x == 0 && rise < p.B) report(p.dev_status, kErrInvalid);
+// leaves room for each sequence's and is found by search among the `rise` sequences
+// before the first whose start falls.  A warp's work; false where no tile is.
+__device__ __forceinline__ bool find_searched(const PromptParams &p, int rise, int index, Work &w) {
+    const int lane = threadIdx.x & 31;
     auto base = [&](int b) { return static_cast<int64_t>(p.start[b]) * p.G / kTileRows + b; };
-    if (rise == 0 || base(0) > index) return false;
     int a = 0, z = rise;      // base(a) <= index < base(z), or z = rise
     while (z - a > 1) {
-        const int mid = a + (z - a) / 2;
-        if (base(mid) <= index)
-            a = mid;
-        else
-            z = mid;
+        const int step = (z - a + 31) / 32, at = a + lane * step;
+        const int hits = __popc(__ballot_sync(0xffffffffu, at < z && base(at) <= index));
+        if (hits == 0) return false;
+        a += (hits - 1) * step;
+        z = min(z, a + step);
     }
+    if (rise == 0 || base(a) > index) return false;
     w.row0 = p.start[a];
     w.n = p.start[a + 1] - w.row0;
     w.tile = static_cast<int>(index - base(a));
     return w.tile < tiles_of(w.n, p.G);
+}
+
+// Key blocks that the rows of tile t see; 0: it has no rows.
+__device__ __forceinline__ int blocks_of(const PromptParams &p, const Work &w, int t) {
+    const int R = w.n * p.G, r0 = w.tile * kTileRows + t * kBlk;
+    if (r0 >= R) return 0;
+    const int last = min(R, r0 + kBlk) - 1;
+    return ((p.causal ? last / p.G + 1 : w.n) + kBlk - 1) / kBlk;
+}
+// The block that ends behind the sequence's last token, if it is among the first nbs; else -1.
+__device__ __forceinline__ int tail_of(const Work &w, int nbs) {
+    return w.n % kBlk && nbs == (w.n + kBlk - 1) / kBlk ? nbs - 1 : -1;
 }
 
 // ---------------------------------------------------------------------------
@@ -228,88 +251,133 @@ __device__ __forceinline__ float mask_scores(uint32_t (&X)[32], int col0, int li
     return m;
 }
 
+// 16 bytes global -> shared, zeros where there is nothing to read.
+__device__ __forceinline__ void copy16(void *smem_dst, const void *gmem_src, bool there) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(smem_dst)),
+                 "l"(reinterpret_cast<uint64_t>(gmem_src)), "r"(there ? 16u : 0u)
+                 : "memory");
+}
+// A row's 32 bytes (kWide: 32-byte aligned).
+template <bool kWide>
+__device__ __forceinline__ void store32(uint16_t *to, const uint32_t *w) {
+    if constexpr (kWide) {
+        asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(reinterpret_cast<uint64_t>(to)), "r"(w[0]), "r"(w[1]),
+                     "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                     : "memory");
+    } else {
+        reinterpret_cast<uint4 *>(to)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+        reinterpret_cast<uint4 *>(to)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+    }
+}
+
 template <bool kCap>
 __global__ void __launch_bounds__(kThreads, 1)
     prompt_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, const PromptParams p) {
     extern __shared__ unsigned char smem_raw[];
     unsigned char *smem =
         reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    uint64_t *full = reinterpret_cast<uint64_t *>(smem + kOffBar), *empty = full + kStages;
-    uint64_t *q_full = empty + kStages, *s_full = q_full + kTiles, *p_full = s_full + kTiles, *o_full = p_full + 2 * kTiles;
-    uint64_t *raw = o_full + kTiles, *drain = raw + 1;
+    uint64_t *full = reinterpret_cast<uint64_t *>(smem + kOffBar), *empty = full + kStages, *raw = empty + kStages;
+    uint64_t *q_full = raw + kStages, *q_free = q_full + kTiles, *s_full = q_free + kTiles, *p_full = s_full + kTiles;
+    uint64_t *o_full = p_full + 2 * kTiles, *o_free = o_full + kTiles, *w_full = o_free + kTiles, *w_free = w_full + kWorks;
+    uint64_t *drain = w_free + kWorks;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + kOffMisc);
     int *abort_flag = reinterpret_cast<int *>(smem + kOffMisc + 4);
     int *first_fall = reinterpret_cast<int *>(smem + kOffMisc + 8);
+    Work *works = reinterpret_cast<Work *>(smem + kOffWork);
 
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
-    const int rank = static_cast<int>(blockIdx.x / p.H), h = static_cast<int>(blockIdx.x % p.H);
-    Work w;
-    // every warp finds the CTA's tile for itself
-    if (!(p.B <= kSortable ? find_sorted(p, rank, w) : find_searched(p, rank, first_fall, w))) return;
-
-    const int R = w.n * p.G, r0 = w.tile * kTileRows;
-    // key blocks that each tile's rows see; none: the tile has no rows
-    auto blocks_of = [&](int t) {
-        if (r0 + t * kBlk >= R) return 0;
-        const int last = min(R, r0 + (t + 1) * kBlk) - 1;
-        return ((p.causal ? last / p.G + 1 : w.n) + kBlk - 1) / kBlk;
-    };
-    const int nb0 = blocks_of(0), nb1 = blocks_of(1), nbs = max(nb0, nb1);
-    const int tail = w.n % kBlk && nbs == (w.n + kBlk - 1) / kBlk ? nbs - 1 : -1;      // the block that ends behind the sequence
-
     if (threadIdx.x == 0) {
         for (int s = 0; s < kStages; ++s) {
             mbar_init(full + s, 1);
             mbar_init(empty + s, 1);
+            mbar_init(raw + s, 1);
         }
         for (int t = 0; t < kTiles; ++t) {
-            mbar_init(q_full + t, 4);
+            mbar_init(q_full + t, 1);
+            mbar_init(q_free + t, 1);
             mbar_init(s_full + t, 1);
             mbar_init(p_full + 2 * t, 4);
             mbar_init(p_full + 2 * t + 1, 4);
             mbar_init(o_full + t, 1);
+            mbar_init(o_free + t, 4);
         }
-        mbar_init(raw, 1);
+        for (int i = 0; i < kWorks; ++i) {
+            mbar_init(w_full + i, 1);
+            mbar_init(w_free + i, 3 + 4 * kTiles);
+        }
         mbar_init(drain, 1);
         *abort_flag = 0;
+        *first_fall = p.B;
         mbar_fence_init();
     }
     if (warp == 1) {
         tmem_alloc(tmem_slot, kTmemCols);
         tmem_relinquish();
     }
+    if (p.B > kSortable) {
+        __syncthreads();
+        for (int b = threadIdx.x; b < p.B; b += kThreads) {
+            const int lo = p.start[b], hi = p.start[b + 1];
+            if (lo < 0 || hi < lo || hi > p.T) atomicMin(first_fall, b);
+        }
+    }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
 
+    // The k-th work of this CTA, from its slot; false at the end, or where a wait gave up.
+    auto next_work = [&](int k, Work &w) {
+        const int i = k % kWorks;
+        if (!__all_sync(0xffffffffu, mbar_wait(w_full + i, (k / kWorks) & 1, abort_flag, p.limit_ns))) return false;
+        w = works[i];
+        return w.n > 0;
+    };
+    auto work_done = [&](int k) {      // a warp's
+        __syncwarp();
+        if (lane == 0) mbar_arrive(w_free + k % kWorks);
+    };
+
     // registers: 128 x 80 + 256 x 208 of the 384 x 168 at launch
     if (warp < kSoftWarp0) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
         if (warp == 0) {
-            // -------------------------------------------------------- producer
-            if (lane == 0) {
-                bool ok = true;
-                int i = 0;
-                for (; i < 2 * nbs; ++i) {      // K(0), V(0), K(1), V(1), ...
+            // -------------------------------------------------------- producer of K and V
+            Work w;
+            int i = 0;                  // copies issued: K(0), V(0), K(1), V(1), ... of one work after the other
+            uint32_t tails = 0;         // stages whose last copy `raw` counts,
+            uint32_t turns = 0;         // and the next phase of each stage's
+            bool ok = true;
+            for (int k = 0; ok && next_work(k, w); ++k) {
+                const int nbs = max(blocks_of(p, w, 0), blocks_of(p, w, 1)), tail = tail_of(w, nbs);
+                for (int j = 0; ok && j < 2 * nbs; ++j, ++i) {
                     const int st = i % kStages;
                     if (i >= kStages) ok = mbar_wait(empty + st, (i / kStages - 1) & 1, abort_flag, p.limit_ns);
+                    ok = __all_sync(0xffffffffu, ok);
                     if (!ok) break;
-                    const void *map = i & 1 ? &tmV : &tmK;
-                    const int token = w.row0 + (i >> 1) * kBlk, head = h * (i & 1 ? p.v_heads : p.k_heads);
-                    const bool tokens = i & 1 ? p.v_tokens : p.k_tokens;
-                    unsigned char *to = smem + kOffKV + st * kBlock;
-                    uint64_t *landed = i == 2 * tail + 1 ? raw : full + st;
-                    mbar_expect_tx(landed, kBlock);
-                    for (int c = 0; c < 2; ++c)
-                        tma_load_3d(to + c * kPanel, map, landed, 64 * c, tokens ? token : head, tokens ? head : token);
+                    const bool is_v = j & 1, is_tail = j == 2 * tail + 1;
+                    tails = is_tail ? tails | (1u << st) : tails & ~(1u << st);
+                    turns ^= is_tail ? 1u << st : 0u;
+                    if (lane == 0) {
+                        const int token = w.row0 + (j >> 1) * kBlk, head = w.h * (is_v ? p.v_heads : p.k_heads);
+                        const bool tokens = is_v ? p.v_tokens : p.k_tokens;
+                        unsigned char *to = smem + kOffKV + st * kBlock;
+                        uint64_t *landed = is_tail ? raw + st : full + st;
+                        mbar_expect_tx(landed, kBlock);
+                        for (int c = 0; c < 2; ++c)
+                            tma_load_3d(to + c * kPanel, is_v ? &tmV : &tmK, landed, 64 * c, tokens ? token : head, tokens ? head : token);
+                    }
                 }
-                // every copy issued has landed before the CTA can exit
+                work_done(k);
+            }
+            // every copy issued has landed before the CTA can exit
+            if (lane == 0) {
                 for (int j = max(0, i - kStages); j < i; ++j) {
-                    if (j == 2 * tail + 1)
-                        drain_wait(raw, 0, p.limit_ns);
+                    const int st = j % kStages;
+                    if ((tails >> st) & 1u)
+                        drain_wait(raw + st, ((turns >> st) & 1u) ^ 1u, p.limit_ns);
                     else
-                        drain_wait(full + j % kStages, (j / kStages) & 1, p.limit_ns);
+                        drain_wait(full + st, (j / kStages) & 1, p.limit_ns);
                 }
             }
         } else if (warp == 1) {
@@ -345,76 +413,152 @@ __global__ void __launch_bounds__(kThreads, 1)
             auto commit = [&](uint64_t *bar) {
                 if (one) tc_commit(bar);
             };
-            bool ok = wait(full, 0);
-#pragma unroll
-            for (int t = 0; t < kTiles; ++t) {
-                if (!ok || (t == 1 && nb1 == 0)) break;
-                ok = wait(q_full + t, 0);
-                if (ok) qk(t, 0);
-            }
-            commit(empty);
-            for (int j = 0; ok && j < nbs; ++j) {
-                const int iv = 2 * j + 1, ik = 2 * j + 2, sv = iv % kStages, sk = ik % kStages;
-                ok = wait(full + sv, (iv / kStages) & 1);
-                if (ok && j + 1 < nbs) ok = wait(full + sk, (ik / kStages) & 1);
+            Work w;
+            int i0 = 0;                         // the ring's copies before this work's
+            uint32_t blocks[kTiles] = {0, 0};   // of each tile so far
+            uint32_t had1 = 0;                  // works that had a second tile
+            bool ok = true;
+            for (int k = 0; ok && next_work(k, w); ++k) {
+                const int nb0 = blocks_of(p, w, 0), nb1 = blocks_of(p, w, 1), nbs = max(nb0, nb1);
+                ok = wait(full + i0 % kStages, (i0 / kStages) & 1);
 #pragma unroll
                 for (int t = 0; t < kTiles; ++t) {
-                    const int last = t ? nb1 : nb0;
-                    if (!ok || j >= last) continue;
-                    ok = wait(p_full + 2 * t, j & 1);
-                    if (!ok) break;
-                    pv(t, sv, 0, j == 0);
-                    ok = wait(p_full + 2 * t + 1, j & 1);
-                    if (!ok) break;
-                    pv(t, sv, 1, false);
-                    if (t == 1 || j >= nb1) commit(empty + sv);
-                    if (j + 1 < last)
-                        qk(t, sk);
-                    else
-                        commit(o_full + t);
+                    if (!ok || (t == 1 && nb1 == 0)) continue;
+                    ok = wait(q_full + t, (t ? had1 : k) & 1);
+                    if (!ok) continue;
+                    qk(t, i0 % kStages);
+                    if ((t ? nb1 : nb0) == 1) commit(q_free + t);
                 }
-                if (ok && j + 1 < nbs) commit(empty + sk);
+                commit(empty + i0 % kStages);
+                for (int j = 0; ok && j < nbs; ++j) {
+                    const int iv = i0 + 2 * j + 1, ik = iv + 1, sv = iv % kStages, sk = ik % kStages;
+                    ok = wait(full + sv, (iv / kStages) & 1);
+                    if (ok && j + 1 < nbs) ok = wait(full + sk, (ik / kStages) & 1);
+#pragma unroll
+                    for (int t = 0; t < kTiles; ++t) {
+                        const int last = t ? nb1 : nb0;
+                        if (!ok || j >= last) continue;
+                        const int turn = static_cast<int>(blocks[t]++) & 1, earlier = t ? static_cast<int>(had1) : k;
+                        // O's first product waits until the epilogue before has read it
+                        if (j == 0 && earlier > 0) ok = wait(o_free + t, (earlier - 1) & 1);
+                        if (ok) ok = wait(p_full + 2 * t, turn);
+                        if (!ok) continue;
+                        pv(t, sv, 0, j == 0);
+                        ok = wait(p_full + 2 * t + 1, turn);
+                        if (!ok) continue;
+                        pv(t, sv, 1, false);
+                        if (t == 1 || j >= nb1) commit(empty + sv);
+                        if (j + 1 < last) {
+                            qk(t, sk);
+                            if (j + 2 == last) commit(q_free + t);
+                        } else {
+                            commit(o_full + t);
+                        }
+                    }
+                    if (ok && j + 1 < nbs) commit(empty + sk);
+                }
+                i0 += 2 * nbs;
+                had1 += nb1 > 0;
+                work_done(k);
             }
             commit(drain);
             if (one) drain_wait(drain, 0, p.limit_ns);
             __syncwarp();
-        } else if (warp == 2 && tail >= 0) {
-            // -------------------------------------------------------- rows of V behind the sequence
-            const int st = (2 * tail + 1) % kStages, live = w.n - tail * kBlk;
-            if (__all_sync(0xffffffffu, mbar_wait(raw, 0, abort_flag, p.limit_ns))) {
-                uint4 *to = reinterpret_cast<uint4 *>(smem + kOffKV + st * kBlock);
-                for (int e = 8 * live + lane; e < 8 * kBlk; e += 32) to[e] = to[e + kPanel / 16] = make_uint4(0, 0, 0, 0);
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(full + st);
+        } else if (warp == 2) {
+            // -------------------------------------------------------- rows of V behind a sequence
+            Work w;
+            int i0 = 0;
+            uint32_t turns = 0;         // the phase of each stage's `raw`
+            bool ok = true;
+            for (int k = 0; ok && next_work(k, w); ++k) {
+                const int nbs = max(blocks_of(p, w, 0), blocks_of(p, w, 1)), tail = tail_of(w, nbs);
+                if (tail >= 0) {
+                    const int st = (i0 + 2 * tail + 1) % kStages, live = w.n - tail * kBlk;
+                    ok = __all_sync(0xffffffffu, mbar_wait(raw + st, (turns >> st) & 1, abort_flag, p.limit_ns));
+                    if (!ok) break;
+                    turns ^= 1u << st;
+                    uint4 *to = reinterpret_cast<uint4 *>(smem + kOffKV + st * kBlock);
+                    for (int e = 8 * live + lane; e < 8 * kBlk; e += 32) to[e] = to[e + kPanel / 16] = make_uint4(0, 0, 0, 0);
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(full + st);
+                }
+                i0 += 2 * nbs;
+                work_done(k);
             }
+        } else {
+            // -------------------------------------------------------- the CTA's work, and its queries
+            Sorted s;
+            const int rise = *first_fall;
+            if (p.B <= kSortable)
+                load_sorted(p, s);
+            else if (blockIdx.x == 0 && lane == 0 && rise < p.B)
+                report(p.dev_status, kErrInvalid);
+            const int ctas = static_cast<int>(gridDim.x), me = static_cast<int>(blockIdx.x);
+            int k = 0;
+            uint32_t had1 = 0;
+            bool ok = true;
+            for (int64_t turn = 0; ok; ++turn) {
+                const int64_t index = turn * ctas + (turn & 1 ? ctas - 1 - me : me);
+                Work w{0, 0, 0, 0};
+                const bool end = index >= p.items;
+                if (!end) {
+                    const int rank = static_cast<int>(index / p.H);
+                    w.h = static_cast<int>(index % p.H);
+                    if (!(p.B <= kSortable ? find_sorted(p, s, rank, w) : find_searched(p, rise, rank, w))) continue;
+                }
+                if (k >= kWorks) ok = __all_sync(0xffffffffu, mbar_wait(w_free + k % kWorks, (k / kWorks - 1) & 1, abort_flag, p.limit_ns));
+                if (!ok) break;
+                __syncwarp();
+                if (lane == 0) {
+                    if (end) w.n = 0;
+                    works[k % kWorks] = w;
+                    mbar_arrive(w_full + k % kWorks);
+                }
+                if (end) break;
+                const int R = w.n * p.G;
+#pragma unroll 1
+                for (int t = 0; ok && t < kTiles; ++t) {
+                    const int r0 = w.tile * kTileRows + t * kBlk, earlier = t ? static_cast<int>(had1) : k;
+                    if (r0 >= R) break;
+                    if (earlier > 0) ok = __all_sync(0xffffffffu, mbar_wait(q_free + t, (earlier - 1) & 1, abort_flag, p.limit_ns));
+                    if (!ok) break;
+                    // half a warp a row
+                    unsigned char *sQ = smem + kOffQ + t * kBlock;
+                    const int c = lane & 15;
+#pragma unroll 4
+                    for (int i = lane >> 4; i < kBlk; i += 2) {
+                        const int r = min(r0 + i, R - 1);
+                        copy16(sQ + (c >> 3) * kPanel + sw128_offset(i, c & 7),
+                               p.q.p + (w.row0 + r / p.G) * p.q.tok + (w.h * p.G + r % p.G) * p.q.head + 8 * c, r0 + i < R);
+                    }
+                    asm volatile("cp.async.wait_all;" ::: "memory");
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(q_full + t);
+                    had1 += t;
+                }
+                ++k;
+            }
+            asm volatile("cp.async.wait_all;" ::: "memory");
         }
     } else {
         // ------------------------------------------------------------ softmax
         asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
         const int t = (warp - kSoftWarp0) >> 2, quarter = warp & 3, row = quarter * 32 + lane;
-        const int n_blocks = t ? nb1 : nb0, rt = r0 + t * kBlk;
-        unsigned char *sQ = smem + kOffQ + t * kBlock;
-        if (n_blocks > 0) {
-            // the warp's rows of Q, half a warp a row
-#pragma unroll 4
-            for (int i = 0; i < 16; ++i) {
-                const int mine = quarter * 32 + 2 * i + (lane >> 4), r = rt + mine, c = lane & 15;
-                uint4 v = make_uint4(0, 0, 0, 0);
-                if (r < R)
-                    v = reinterpret_cast<const uint4 *>(p.q.p + (w.row0 + r / p.G) * p.q.tok + (h * p.G + r % p.G) * p.q.head)[c];
-                *reinterpret_cast<uint4 *>(sQ + (c >> 3) * kPanel + sw128_offset(mine, c & 7)) = v;
-            }
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(q_full + t);
-
-            const float kNegInf = __int_as_float(0xff800000);
-            const uint32_t tl = tmem + (static_cast<uint32_t>(quarter * 32) << 16), tS = tl + kTmemS + 128 * t,
-                           tO = tl + kTmemO + 128 * t;
-            const int r = rt + row;
+        const float kNegInf = __int_as_float(0xff800000);
+        const uint32_t tl = tmem + (static_cast<uint32_t>(quarter * 32) << 16), tS = tl + kTmemS + 128 * t,
+                       tO = tl + kTmemO + 128 * t;
+        Work w;
+        uint32_t blocks = 0, had = 0;      // of this tile so far, and works that had it
+        bool ok = true;
+        for (int k = 0; ok && next_work(k, w); ++k) {
+            const int n_blocks = blocks_of(p, w, t);
+            work_done(k);
+            if (n_blocks == 0) continue;
+            const int R = w.n * p.G, r = w.tile * kTileRows + t * kBlk + row;
             const bool real = r < R;
-            const int seen = real && p.causal ? r / p.G + 1 : w.n;
+            const int token = r / p.G, seen = real && p.causal ? token + 1 : w.n;
             const int whole = __reduce_min_sync(0xffffffffu, seen) / kBlk;      // blocks that every row of the warp sees all of
             BlockScore s;
             s.c = fmaxf(kCap ? p.cap_in : p.scale_log2, 0x1p-149f);
@@ -422,9 +566,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             s.bias = 0.0f;
             float m = kNegInf;
             uint64_t l2 = 0;
-            bool ok = true;
             for (int b = 0; b < n_blocks; ++b) {
-                ok = __all_sync(0xffffffffu, mbar_wait(s_full + t, b & 1, abort_flag, p.limit_ns));
+                ok = __all_sync(0xffffffffu, mbar_wait(s_full + t, blocks++ & 1, abort_flag, p.limit_ns));
                 if (!ok) break;
                 tc_fence_after();
                 uint32_t X[4][32];
@@ -458,10 +601,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
                         for (int i = 0; i < 8; ++i) {
                             uint32_t o[16];
-                            asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-                                         : "=r"(o[0]), "=r"(o[1]), "=r"(o[2]), "=r"(o[3]), "=r"(o[4]), "=r"(o[5]), "=r"(o[6]), "=r"(o[7]),
-                                           "=r"(o[8]), "=r"(o[9]), "=r"(o[10]), "=r"(o[11]), "=r"(o[12]), "=r"(o[13]), "=r"(o[14]), "=r"(o[15])
-                                         : "r"(tO + 16 * i));
+                            VCA_TMEM_LD16(tO + 16 * i, o);
                             tmem_ld_wait();
 #pragma unroll
                             for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__fmul_rn(__uint_as_float(o[e]), alpha));
@@ -483,70 +623,69 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (lane == 0) mbar_arrive(p_full + 2 * t + half);
                 }
             }
+            if (!ok) break;
             // -------------------------------------------------------- epilogue
-            if (ok) ok = __all_sync(0xffffffffu, mbar_wait(o_full + t, 0, abort_flag, p.limit_ns));
-            if (ok) {
-                tc_fence_after();
-                float l;
-                {
-                    float a, c;
-                    upk2(l2, a, c);
-                    l = __fadd_rn(a, c);
-                }
-                const int64_t at = static_cast<int64_t>(w.row0 + r / p.G) * p.Hq + h * p.G + r % p.G;
-                // joined with what came before: both sums to the larger maximum
-                float before = kNegInf, keep = 1.0f, add = 0.0f;
-                if (p.prior && real) before = p.prior_lse[at] * 1.4426950408889634f;
-                float M = m;
-                if (before != kNegInf) {
-                    M = m == kNegInf ? before : before != before ? before : fmaxf(m, before);
-                    keep = m == kNegInf ? 0.0f : ex2_approx(__fsub_rn(m, M));
-                    add = ex2_approx(__fsub_rn(before, M));
-                    l = __fadd_rn(__fmul_rn(l, keep), add);
-                }
-                const float inv = l > 0.0f || l != l ? 1.0f / l : 0.0f;
-                keep *= inv;
-                add *= inv;
-                const bool joins = before != kNegInf;
-                const uint4 *prior = reinterpret_cast<const uint4 *>(p.prior + at * kD);
-                // Q's place is free: rows of O through shared memory, half a warp a row to memory
-#pragma unroll 1
-                for (int i = 0; i < 4; ++i) {
-                    uint32_t o[32];
-                    VCA_TMEM_LD32(tO + 32 * i, o);
-                    tmem_ld_wait();
+            const int64_t at = static_cast<int64_t>(w.row0 + token) * p.Hq + w.h * p.G + r % p.G;
+            float l;
+            {
+                float a, c;
+                upk2(l2, a, c);
+                l = __fadd_rn(a, c);
+            }
+            // joined with what came before: both sums to the larger maximum
+            float before = kNegInf, keep = 1.0f, add = 0.0f, M = m;
+            if (p.prior && real) before = p.prior_lse[at] * 1.4426950408889634f;
+            const bool joins = before != kNegInf;
+            if (joins) {
+                M = before != before ? before : fmaxf(m, before);
+                keep = m == kNegInf ? 0.0f : ex2_approx(__fsub_rn(m, M));
+                add = ex2_approx(__fsub_rn(before, M));
+                l = __fadd_rn(__fmul_rn(l, keep), add);
+            }
+            const float inv = l > 0.0f || l != l ? 1.0f / l : 0.0f;
+            keep *= inv;
+            add *= inv;
+            ok = __all_sync(0xffffffffu, mbar_wait(o_full + t, had++ & 1, abort_flag, p.limit_ns));
+            if (!ok) break;
+            tc_fence_after();
+            const uint4 *prior = reinterpret_cast<const uint4 *>(p.prior + at * kD);
+            uint32_t y[kD / 2];
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__fmul_rn(__uint_as_float(o[e]), keep));
+            for (int i = 0; i < 4; ++i) {
+                uint32_t o[32];
+                VCA_TMEM_LD32(tO + 32 * i, o);
+                tmem_ld_wait();
+#pragma unroll
+                for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__fmul_rn(__uint_as_float(o[e]), keep));
+                if (joins) {
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        if (joins) {
-                            const uint4 x = prior[4 * i + e];
-                            const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
+                        const uint4 x = prior[4 * i + e];
+                        const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-                            for (int k = 0; k < 4; ++k) {
-                                o[8 * e + 2 * k] = __float_as_uint(fmaf(__uint_as_float(xs[k] << 16), add, __uint_as_float(o[8 * e + 2 * k])));
-                                o[8 * e + 2 * k + 1] =
-                                    __float_as_uint(fmaf(__uint_as_float(xs[k] & 0xffff0000u), add, __uint_as_float(o[8 * e + 2 * k + 1])));
-                            }
+                        for (int k2 = 0; k2 < 4; ++k2) {
+                            uint32_t &lo = o[8 * e + 2 * k2], &hi = o[8 * e + 2 * k2 + 1];
+                            lo = __float_as_uint(fmaf(__uint_as_float(xs[k2] << 16), add, __uint_as_float(lo)));
+                            hi = __float_as_uint(fmaf(__uint_as_float(xs[k2] & 0xffff0000u), add, __uint_as_float(hi)));
                         }
-                        uint32_t y[4];
+                    }
+                }
 #pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            y[k] = pack_bf16x2(__uint_as_float(o[8 * e + 2 * k]), __uint_as_float(o[8 * e + 2 * k + 1]));
-                        *reinterpret_cast<uint4 *>(sQ + row * 256 + (((4 * i + e) ^ (row & 15)) << 4)) = make_uint4(y[0], y[1], y[2], y[3]);
-                    }
+                for (int e = 0; e < 16; ++e) y[16 * i + e] = pack_bf16x2(__uint_as_float(o[2 * e]), __uint_as_float(o[2 * e + 1]));
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(o_free + t);
+            if (real) {
+                uint16_t *to = p.O + at * kD;
+                if (p.wide) {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) store32<true>(to + 16 * e, y + 8 * e);
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) store32<false>(to + 16 * e, y + 8 * e);
                 }
-                if (p.lse && real) p.lse[at] = (M == kNegInf ? 0.0f : M) * 0.6931471805599453f + logf(l);
-                __syncwarp();
-#pragma unroll 4
-                for (int i = 0; i < 16; ++i) {
-                    const int mine = quarter * 32 + 2 * i + (lane >> 4), ri = rt + mine, c = lane & 15;
-                    if (ri < R) {
-                        const int64_t to = static_cast<int64_t>(w.row0 + ri / p.G) * p.Hq + h * p.G + ri % p.G;
-                        reinterpret_cast<uint4 *>(p.O + to * kD)[c] =
-                            *reinterpret_cast<const uint4 *>(sQ + mine * 256 + ((c ^ (mine & 15)) << 4));
-                    }
-                }
+                if (p.lse) p.lse[at] = (M == kNegInf ? 0.0f : M) * 0.6931471805599453f + logf(l);
             }
         }
     }
@@ -607,10 +746,15 @@ cudaError_t launch_prompt_attention(const PromptArgs &a, cudaStream_t st) {
     p.dev_status = a.dev_status;
     p.limit_ns = a.wait_limit_ns;
     const auto kernel = a.softcap > 0.0f ? prompt_kernel<true> : prompt_kernel<false>;
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
     if (e != cudaSuccess) return e;
     const int64_t tiles = static_cast<int64_t>(a.T) * p.G / kTileRows + (a.B <= kSortable && a.T < a.B ? a.T : a.B);
-    kernel<<<static_cast<unsigned>(tiles * a.H), kThreads, kSmem, st>>>(mk, mv, p);
+    p.items = tiles * a.H;
+    p.wide = (reinterpret_cast<uintptr_t>(a.O) & 31u) == 0;
+    int device = 0, sms = 0;
+    if ((e = cudaGetDevice(&device)) != cudaSuccess) return e;
+    if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, device)) != cudaSuccess) return e;
+    kernel<<<static_cast<unsigned>(p.items < sms ? p.items : sms), kThreads, kSmem, st>>>(mk, mv, p);
     return cudaGetLastError();
 }
 
