@@ -37,10 +37,11 @@ bool cache_ok(const vca_cache *c, vca::CacheView *view) {
 bool rows_ok(const uint16_t *p, int64_t tok, int64_t head) {
     return p && aligned16(p) && (tok & 7) == 0 && (head & 7) == 0;
 }
-// Rows that tensor maps describe: a distance of 0 between heads makes them one, tokens are apart.
-bool mapped_rows_ok(const uint16_t *p, int64_t tok, int64_t head, int T, int H) {
+// Rows that tensor maps describe: tokens and heads are apart, or the heads (of keys and values) all one.
+bool mapped_rows_ok(const uint16_t *p, int64_t tok, int64_t head, int T, int H, bool one_head) {
     const int64_t most = static_cast<int64_t>(1) << 39;      // 2^40 bytes
-    return rows_ok(p, tok, head) && (T < 2 || (tok > 0 && tok < most)) && (H < 2 || (head >= 0 && head < most));
+    return rows_ok(p, tok, head) && (T < 2 || (tok > 0 && tok < most)) &&
+           (H < 2 || (head > 0 && head < most) || (one_head && head == 0));
 }
 bool query_sizes_ok(int T, int Hq, int H) {
     return T >= 0 && Hq >= 1 && H >= 1 && Hq % H == 0 && static_cast<int64_t>(T) * Hq <= (static_cast<int64_t>(1) << 31) - 1;
@@ -263,8 +264,8 @@ int vca_prompt_attention(const uint16_t *Q, int64_t q_token, int64_t q_head, con
         !aligned4(prior_lse))
         return VCA_ERR_INVALID_ARG;
     if (T == 0) return VCA_OK;
-    if (!rows_ok(Q, q_token, q_head) || !mapped_rows_ok(K, k_token, k_head, T, H) || !mapped_rows_ok(V, v_token, v_head, T, H) ||
-        !O || !aligned16(O))
+    if (!mapped_rows_ok(Q, q_token, q_head, T, Hq, false) || !mapped_rows_ok(K, k_token, k_head, T, H, true) ||
+        !mapped_rows_ok(V, v_token, v_head, T, H, true) || !O || !aligned16(O))
         return VCA_ERR_INVALID_ARG;
     vca::PromptArgs a{vca::CacheRows{Q, q_token, q_head}, vca::CacheRows{K, k_token, k_head}, vca::CacheRows{V, v_token, v_head},
                       start, B, T, Hq, H, causal, scale_or_default(softmax_scale), cap_used(softcap), prior, prior_lse, O, lse,

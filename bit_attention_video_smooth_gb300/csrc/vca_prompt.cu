@@ -31,7 +31,7 @@ namespace {
 using namespace attn;
 using namespace cache;
 
-constexpr int kTiles = 2, kTileRows = kTiles * kBlk;
+constexpr int kTiles = 2;
 constexpr int kStages = 5, kSoftWarp0 = 4, kThreads = 32 * (kSoftWarp0 + 4 * kTiles);
 constexpr uint32_t kPanel = kBlk * 128;              // 128 rows of 64 bf16 channels
 constexpr uint32_t kBlock = 2 * kPanel;              // Q, K or V: two panels
@@ -47,10 +47,11 @@ constexpr uint32_t kSmem = kOffMisc + 16 + 1024;
 static_assert(kSmem <= 232448, "shared memory budget");
 
 struct PromptParams {
-    CacheRows q;
     const int32_t *start;
-    int B, T, Hq, H, G, causal;
-    int64_t items;                          // (tile, head) pairs at most
+    int B, T, Hq, causal;
+    int G, tokens;                          // a tile: G query heads (of one KV head) of so many tokens
+    int groups, per_head;                   // of G query heads, and of those to a KV head
+    int64_t items;                          // (two tiles, group) at most
     float scale_log2, cap_in, cap_out;      // as in AttnParams
     bool k_tokens, v_tokens;                // the tensor map's middle dimension: tokens, else heads
     int k_heads, v_heads;                   // 1, or 0: all heads are the same
@@ -88,14 +89,12 @@ __device__ __forceinline__ bool elect_one() {
 // ---------------------------------------------------------------------------
 // Which tiles a CTA takes
 // ---------------------------------------------------------------------------
-// 256 of the rows of a (sequence, KV head): its tokens [row0, row0 + n), and which;
-// n = 0: there is no more work.
+// Two tiles of a (sequence, group of query heads): its tokens [row0, row0 + n), and
+// which pair; n = 0: there is no more work.
 struct Work {
-    int row0, n, tile, h;
+    int row0, n, tile, group;
 };
-__device__ __forceinline__ int tiles_of(int n, int G) {
-    return static_cast<int>((static_cast<int64_t>(n) * G + kTileRows - 1) / kTileRows);
-}
+__device__ __forceinline__ int tiles_of(const PromptParams &p, int n) { return (n + 2 * p.tokens - 1) / (2 * p.tokens); }
 
 // Up to kSortable sequences: the tiles by their number of key blocks, most first.  A
 // causal tile's number grows with its place in the sequence, another's is the
@@ -124,7 +123,7 @@ __device__ __forceinline__ void load_sorted(const PromptParams &p, Sorted &s) {
         const uint32_t falls = __ballot_sync(0xffffffffu, s.lo[k] < 0 || hi[k] < s.lo[k] || hi[k] > p.T);
         s.n[k] = fell || (falls & ((2u << lane) - 1u)) ? 0 : hi[k] - s.lo[k];
         fell = fell || falls != 0;
-        s.q[k] = tiles_of(s.n[k], p.G);
+        s.q[k] = tiles_of(p, s.n[k]);
         s.most = max(s.most, s.q[k]);
     }
     if (blockIdx.x == 0 && lane == 0 && fell) report(p.dev_status, kErrInvalid);
@@ -170,12 +169,12 @@ __device__ __forceinline__ bool find_sorted(const PromptParams &p, const Sorted 
     return false;
 }
 
-// More sequences: sequence b's tiles are those from floor(start G / 256) + b on, which
+// More sequences: sequence b's tiles are those from floor(start / tokens) + b on, which
 // leaves room for each sequence's and is found by search among the `rise` sequences
 // before the first whose start falls.  A warp's work; false where no tile is.
 __device__ __forceinline__ bool find_searched(const PromptParams &p, int rise, int index, Work &w) {
     const int lane = threadIdx.x & 31;
-    auto base = [&](int b) { return static_cast<int64_t>(p.start[b]) * p.G / kTileRows + b; };
+    auto base = [&](int b) { return static_cast<int64_t>(p.start[b] / (2 * p.tokens)) + b; };
     int a = 0, z = rise;      // base(a) <= index < base(z), or z = rise
     while (z - a > 1) {
         const int step = (z - a + 31) / 32, at = a + lane * step;
@@ -188,15 +187,14 @@ __device__ __forceinline__ bool find_searched(const PromptParams &p, int rise, i
     w.row0 = p.start[a];
     w.n = p.start[a + 1] - w.row0;
     w.tile = static_cast<int>(index - base(a));
-    return w.tile < tiles_of(w.n, p.G);
+    return w.tile < tiles_of(p, w.n);
 }
 
 // Key blocks that the rows of tile t see; 0: it has no rows.
 __device__ __forceinline__ int blocks_of(const PromptParams &p, const Work &w, int t) {
-    const int R = w.n * p.G, r0 = w.tile * kTileRows + t * kBlk;
-    if (r0 >= R) return 0;
-    const int last = min(R, r0 + kBlk) - 1;
-    return ((p.causal ? last / p.G + 1 : w.n) + kBlk - 1) / kBlk;
+    const int first = (2 * w.tile + t) * p.tokens;
+    if (first >= w.n) return 0;
+    return ((p.causal ? min(w.n, first + p.tokens) : w.n) + kBlk - 1) / kBlk;
 }
 // The block that ends behind the sequence's last token, if it is among the first nbs; else -1.
 __device__ __forceinline__ int tail_of(const Work &w, int nbs) {
@@ -251,12 +249,6 @@ __device__ __forceinline__ float mask_scores(uint32_t (&X)[32], int col0, int li
     return m;
 }
 
-// 16 bytes global -> shared, zeros where there is nothing to read.
-__device__ __forceinline__ void copy16(void *smem_dst, const void *gmem_src, bool there) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(smem_dst)),
-                 "l"(reinterpret_cast<uint64_t>(gmem_src)), "r"(there ? 16u : 0u)
-                 : "memory");
-}
 // A row's 32 bytes (kWide: 32-byte aligned).
 template <bool kWide>
 __device__ __forceinline__ void store32(uint16_t *to, const uint32_t *w) {
@@ -272,7 +264,8 @@ __device__ __forceinline__ void store32(uint16_t *to, const uint32_t *w) {
 
 template <bool kCap>
 __global__ void __launch_bounds__(kThreads, 1)
-    prompt_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, const PromptParams p) {
+    prompt_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                  const __grid_constant__ CUtensorMap tmV, const PromptParams p) {
     extern __shared__ unsigned char smem_raw[];
     unsigned char *smem =
         reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -359,7 +352,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     tails = is_tail ? tails | (1u << st) : tails & ~(1u << st);
                     turns ^= is_tail ? 1u << st : 0u;
                     if (lane == 0) {
-                        const int token = w.row0 + (j >> 1) * kBlk, head = w.h * (is_v ? p.v_heads : p.k_heads);
+                        const int token = w.row0 + (j >> 1) * kBlk, head = w.group / p.per_head * (is_v ? p.v_heads : p.k_heads);
                         const bool tokens = is_v ? p.v_tokens : p.k_tokens;
                         unsigned char *to = smem + kOffKV + st * kBlock;
                         uint64_t *landed = is_tail ? raw + st : full + st;
@@ -497,14 +490,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int ctas = static_cast<int>(gridDim.x), me = static_cast<int>(blockIdx.x);
             int k = 0;
             uint32_t had1 = 0;
+            int queries[kTiles] = {-1, -1};      // the last copy of each tile's
             bool ok = true;
             for (int64_t turn = 0; ok; ++turn) {
                 const int64_t index = turn * ctas + (turn & 1 ? ctas - 1 - me : me);
                 Work w{0, 0, 0, 0};
                 const bool end = index >= p.items;
                 if (!end) {
-                    const int rank = static_cast<int>(index / p.H);
-                    w.h = static_cast<int>(index % p.H);
+                    const int rank = static_cast<int>(index / p.groups);
+                    w.group = static_cast<int>(index % p.groups);
                     if (!(p.B <= kSortable ? find_sorted(p, s, rank, w) : find_searched(p, rise, rank, w))) continue;
                 }
                 if (k >= kWorks) ok = __all_sync(0xffffffffu, mbar_wait(w_free + k % kWorks, (k / kWorks - 1) & 1, abort_flag, p.limit_ns));
@@ -516,31 +510,31 @@ __global__ void __launch_bounds__(kThreads, 1)
                     mbar_arrive(w_full + k % kWorks);
                 }
                 if (end) break;
-                const int R = w.n * p.G;
 #pragma unroll 1
                 for (int t = 0; ok && t < kTiles; ++t) {
-                    const int r0 = w.tile * kTileRows + t * kBlk, earlier = t ? static_cast<int>(had1) : k;
-                    if (r0 >= R) break;
+                    const int token = (2 * w.tile + t) * p.tokens, earlier = t ? static_cast<int>(had1) : k;
+                    if (token >= w.n) break;
                     if (earlier > 0) ok = __all_sync(0xffffffffu, mbar_wait(q_free + t, (earlier - 1) & 1, abort_flag, p.limit_ns));
                     if (!ok) break;
-                    // half a warp a row
-                    unsigned char *sQ = smem + kOffQ + t * kBlock;
-                    const int c = lane & 15;
-#pragma unroll 4
-                    for (int i = lane >> 4; i < kBlk; i += 2) {
-                        const int r = min(r0 + i, R - 1);
-                        copy16(sQ + (c >> 3) * kPanel + sw128_offset(i, c & 7),
-                               p.q.p + (w.row0 + r / p.G) * p.q.tok + (w.h * p.G + r % p.G) * p.q.head + 8 * c, r0 + i < R);
+                    if (lane == 0) {
+                        unsigned char *sQ = smem + kOffQ + t * kBlock;
+                        mbar_expect_tx(q_full + t, 2 * 128 * p.G * p.tokens);
+                        for (int c = 0; c < 2; ++c) tma_load_3d(sQ + c * kPanel, &tmQ, q_full + t, 64 * c, w.group * p.G, w.row0 + token);
                     }
-                    asm volatile("cp.async.wait_all;" ::: "memory");
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(q_full + t);
                     had1 += t;
+                    if (t == 0)
+                        queries[0] = earlier;
+                    else
+                        queries[1] = earlier;
                 }
                 ++k;
             }
-            asm volatile("cp.async.wait_all;" ::: "memory");
+            // the last queries have landed before the CTA can exit
+            if (lane == 0) {
+#pragma unroll
+                for (int t = 0; t < kTiles; ++t)
+                    if (queries[t] >= 0) drain_wait(q_full + t, queries[t] & 1, p.limit_ns);
+            }
         }
     } else {
         // ------------------------------------------------------------ softmax
@@ -549,6 +543,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float kNegInf = __int_as_float(0xff800000);
         const uint32_t tl = tmem + (static_cast<uint32_t>(quarter * 32) << 16), tS = tl + kTmemS + 128 * t,
                        tO = tl + kTmemO + 128 * t;
+        const int row_token = row / p.G, row_head = row % p.G;
         Work w;
         uint32_t blocks = 0, had = 0;      // of this tile so far, and works that had it
         bool ok = true;
@@ -556,9 +551,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int n_blocks = blocks_of(p, w, t);
             work_done(k);
             if (n_blocks == 0) continue;
-            const int R = w.n * p.G, r = w.tile * kTileRows + t * kBlk + row;
-            const bool real = r < R;
-            const int token = r / p.G, seen = real && p.causal ? token + 1 : w.n;
+            const int token = (2 * w.tile + t) * p.tokens + row_token;
+            const bool real = row_token < p.tokens && token < w.n;
+            const int seen = real && p.causal ? token + 1 : w.n;
             const int whole = __reduce_min_sync(0xffffffffu, seen) / kBlk;      // blocks that every row of the warp sees all of
             BlockScore s;
             s.c = fmaxf(kCap ? p.cap_in : p.scale_log2, 0x1p-149f);
@@ -589,9 +584,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 const float pm = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * s.c;
                 const float bm = kCap ? capped(pm, p.cap_out) : pm;
-                if (__any_sync(0xffffffffu, bm > __fadd_rn(m, kLazyTau))) {
+                const bool rises = real && bm > __fadd_rn(m, kLazyTau);      // a row that is none may hold anything
+                if (__any_sync(0xffffffffu, rises)) {
                     float alpha = 1.0f;
-                    if (bm > __fadd_rn(m, kLazyTau)) {
+                    if (rises) {
                         alpha = ex2_approx(__fsub_rn(m, bm));
                         l2 = mul2(l2, pk2(__float_as_uint(alpha), __float_as_uint(alpha)));
                         m = bm;
@@ -625,7 +621,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             if (!ok) break;
             // -------------------------------------------------------- epilogue
-            const int64_t at = static_cast<int64_t>(w.row0 + token) * p.Hq + w.h * p.G + r % p.G;
+            const int64_t at = static_cast<int64_t>(w.row0 + token) * p.Hq + w.group * p.G + row_head;
             float l;
             {
                 float a, c;
@@ -699,39 +695,63 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (threadIdx.x == 0 && *reinterpret_cast<volatile int *>(abort_flag)) report(p.dev_status, kErrTimeout);
 }
 
-// bf16 rows [T][heads][128] as a 3-D matrix, its dimensions in the order of their
-// strides.  A dimension of one entry has no stride, and heads with stride 0 are one.
-bool make_rows_map(CUtensorMap *map, const CacheRows &x, int T, int H, bool *tokens_first, int *heads) {
+// bf16 rows as a 3-D matrix [z][y][128] and boxes of 64 channels.
+bool make_rows_map(CUtensorMap *map, const uint16_t *base, cuuint64_t y, cuuint64_t y_stride, cuuint64_t z, cuuint64_t z_stride,
+                   uint32_t box_y, uint32_t box_z) {
     EncodeTiledFn fn = encode_fn();
     if (!fn) return false;
-    *heads = H > 1 && x.head != 0 ? 1 : 0;
-    const cuuint64_t entries[2] = {static_cast<cuuint64_t>(T), *heads ? static_cast<cuuint64_t>(H) : 1u};
-    const cuuint64_t bytes[2] = {T > 1 ? static_cast<cuuint64_t>(x.tok) * 2 : 2u * kD, *heads ? static_cast<cuuint64_t>(x.head) * 2 : 2u * kD};
-    const int mid = bytes[0] < bytes[1] ? 0 : 1;
-    *tokens_first = mid == 0;
-    cuuint64_t dims[3] = {kD, entries[mid], entries[1 - mid]};
-    cuuint64_t strides[2] = {bytes[mid], bytes[1 - mid]};
-    cuuint32_t box[3] = {64, mid == 0 ? 128u : 1u, mid == 0 ? 1u : 128u};
+    cuuint64_t dims[3] = {kD, y, z};
+    cuuint64_t strides[2] = {2 * y_stride, 2 * z_stride};
+    cuuint32_t box[3] = {64, box_y, box_z};
     cuuint32_t estr[3] = {1, 1, 1};
-    return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<uint16_t *>(x.p), dims, strides, box, estr,
+    return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<uint16_t *>(base), dims, strides, box, estr,
               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+// Of K or V: 128 tokens of a head, dimensions in the order of their strides.  A
+// dimension of one entry has no stride, and heads with stride 0 are one.
+bool make_kv_map(CUtensorMap *map, const CacheRows &x, int T, int H, bool *tokens_first, int *heads) {
+    *heads = H > 1 && x.head != 0 ? 1 : 0;
+    const cuuint64_t tok = T > 1 ? x.tok : kD, head = *heads ? x.head : kD, n = *heads ? H : 1;
+    *tokens_first = tok < head;
+    return tok < head ? make_rows_map(map, x.p, T, tok, n, head, kBlk, 1) : make_rows_map(map, x.p, n, head, T, tok, 1, kBlk);
+}
+
+// Query heads of a tile: a divisor of G (they share a KV head).  More heads mean
+// fewer tokens, so fewer keys that only some rows see, and more of a short prompt's
+// rows in a tile; but whole tokens may not fill the tile's 128 rows.  The
+// least work by the average prompt's length is taken.
+int heads_of(int G, int causal, double length) {
+    int best = 1;
+    double least = 0.0;
+    for (int g = 1; g <= kBlk && g <= G; ++g) {
+        if (G % g) continue;
+        const double tokens = kBlk / g, work = kBlk / (g * tokens) * (1.0 + (causal ? 2.0 * tokens + kBlk : tokens) / length);
+        if (g == 1 || work <= least) {
+            best = g;
+            least = work;
+        }
+    }
+    return best;
 }
 
 }  // namespace
 
 cudaError_t launch_prompt_attention(const PromptArgs &a, cudaStream_t st) {
-    CUtensorMap mk, mv;
+    CUtensorMap mq, mk, mv;
     PromptParams p{};
-    if (!make_rows_map(&mk, a.k, a.T, a.H, &p.k_tokens, &p.k_heads) || !make_rows_map(&mv, a.v, a.T, a.H, &p.v_tokens, &p.v_heads))
+    const int G = a.Hq / a.H;
+    p.G = heads_of(G, a.causal, static_cast<double>(a.T) / a.B);
+    p.tokens = kBlk / p.G;
+    p.groups = a.Hq / p.G;
+    p.per_head = G / p.G;
+    if (!make_rows_map(&mq, a.q.p, a.Hq, a.Hq > 1 ? a.q.head : kD, a.T, a.T > 1 ? a.q.tok : kD, p.G, p.tokens) ||
+        !make_kv_map(&mk, a.k, a.T, a.H, &p.k_tokens, &p.k_heads) || !make_kv_map(&mv, a.v, a.T, a.H, &p.v_tokens, &p.v_heads))
         return cudaErrorInvalidValue;
-    p.q = a.q;
     p.start = a.start;
     p.B = a.B;
     p.T = a.T;
     p.Hq = a.Hq;
-    p.H = a.H;
-    p.G = a.Hq / a.H;
     p.causal = a.causal;
     CacheView heads{};
     heads.H = a.H;
@@ -748,13 +768,13 @@ cudaError_t launch_prompt_attention(const PromptArgs &a, cudaStream_t st) {
     const auto kernel = a.softcap > 0.0f ? prompt_kernel<true> : prompt_kernel<false>;
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
     if (e != cudaSuccess) return e;
-    const int64_t tiles = static_cast<int64_t>(a.T) * p.G / kTileRows + (a.B <= kSortable && a.T < a.B ? a.T : a.B);
-    p.items = tiles * a.H;
+    const int64_t tiles = a.T / (2 * p.tokens) + (a.B <= kSortable && a.T < a.B ? a.T : a.B);
+    p.items = tiles * p.groups;
     p.wide = (reinterpret_cast<uintptr_t>(a.O) & 31u) == 0;
     int device = 0, sms = 0;
     if ((e = cudaGetDevice(&device)) != cudaSuccess) return e;
     if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, device)) != cudaSuccess) return e;
-    kernel<<<static_cast<unsigned>(p.items < sms ? p.items : sms), kThreads, kSmem, st>>>(mk, mv, p);
+    kernel<<<static_cast<unsigned>(p.items < sms ? p.items : sms), kThreads, kSmem, st>>>(mq, mk, mv, p);
     return cudaGetLastError();
 }
 
