@@ -425,20 +425,31 @@ __global__ void __launch_bounds__(kThreads, 1)
                 commit(empty + i0 % kStages);
                 for (int j = 0; ok && j < nbs; ++j) {
                     const int iv = i0 + 2 * j + 1, ik = iv + 1, sv = iv % kStages, sk = ik % kStages;
-                    ok = wait(full + sv, (iv / kStages) & 1);
-                    if (ok && j + 1 < nbs) ok = wait(full + sk, (ik / kStages) & 1);
+                    const int pv_turn = (iv / kStages) & 1, pk_turn = (ik / kStages) & 1;
+                    // Several barriers are tested at once, before they are needed: one test after
+                    // the other, 130 cycles each, left the tensor core idle
+                    bool there = mbar_test_wait(full + sv, pv_turn) & (j + 1 >= nbs || mbar_test_wait(full + sk, pk_turn));
 #pragma unroll
                     for (int t = 0; t < kTiles; ++t) {
                         const int last = t ? nb1 : nb0;
                         if (!ok || j >= last) continue;
                         const int turn = static_cast<int>(blocks[t]++) & 1, earlier = t ? static_cast<int>(had1) : k;
+                        uint64_t *halves = p_full + 2 * t;
+                        const bool first = mbar_test_wait(halves, turn), second = mbar_test_wait(halves + 1, turn);
+                        if (!__all_sync(0xffffffffu, there)) {
+                            ok = wait(full + sv, pv_turn);
+                            if (ok && j + 1 < nbs) ok = wait(full + sk, pk_turn);
+                            there = true;
+                        }
                         // O's first product waits until the epilogue before has read it
-                        if (j == 0 && earlier > 0) ok = wait(o_free + t, (earlier - 1) & 1);
-                        if (ok) ok = wait(p_full + 2 * t, turn);
+                        if (ok && j == 0 && earlier > 0) ok = wait(o_free + t, (earlier - 1) & 1);
+                        if (ok && !__all_sync(0xffffffffu, first)) ok = wait(halves, turn);
                         if (!ok) continue;
+                        tc_fence_after();
                         pv(t, sv, 0, j == 0);
-                        ok = wait(p_full + 2 * t + 1, turn);
+                        if (!__all_sync(0xffffffffu, second)) ok = wait(halves + 1, turn);
                         if (!ok) continue;
+                        tc_fence_after();
                         pv(t, sv, 1, false);
                         if (t == 1 || j >= nb1) commit(empty + sv);
                         if (j + 1 < last) {
