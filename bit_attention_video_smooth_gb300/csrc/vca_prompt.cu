@@ -32,14 +32,16 @@ using namespace attn;
 using namespace cache;
 
 constexpr int kTiles = 2;
-constexpr int kStages = 5, kSoftWarp0 = 4, kThreads = 32 * (kSoftWarp0 + 4 * kTiles);
+constexpr int kStages = 4, kSoftWarp0 = 4, kOutWarp0 = kSoftWarp0 + 4 * kTiles, kThreads = 32 * (kOutWarp0 + 4);
 constexpr uint32_t kPanel = kBlk * 128;              // 128 rows of 64 bf16 channels
 constexpr uint32_t kBlock = 2 * kPanel;              // Q, K or V: two panels
 constexpr uint32_t kTmemS = 0, kTmemO = 256, kTmemCols = 512;
 constexpr uint32_t kOffQ = 0;
 constexpr uint32_t kOffKV = kOffQ + kTiles * kBlock;
-constexpr uint32_t kOffBar = kOffKV + kStages * kBlock;
-constexpr int kWorks = 2;                            // slots for what the CTA does now and next
+constexpr uint32_t kOffStat = kOffKV + kStages * kBlock;                  // fp32 [2][tile][max, sum][128], by turns
+constexpr uint32_t kOffSort = kOffStat + 2 * kTiles * 2 * kBlk * 4;           // Sorted, of at most 256 sequences
+constexpr uint32_t kOffBar = kOffSort + 3 * 256 * 4;
+constexpr int kWorks = 3;                            // slots for what the CTA does now and next
 constexpr int kNumBars = 3 * kStages + 8 * kTiles + 2 * kWorks + 1;
 constexpr uint32_t kOffWork = (kOffBar + kNumBars * 8 + 15) / 16 * 16;
 constexpr uint32_t kOffMisc = kOffWork + kWorks * 16;
@@ -99,46 +101,43 @@ __device__ __forceinline__ int tiles_of(const PromptParams &p, int n) { return (
 // Up to kSortable sequences: the tiles by their number of key blocks, most first.  A
 // causal tile's number grows with its place in the sequence, another's is the
 // sequence's.  The CTAs then take turns, there and back, and have done about the same at the
-// end.  A warp holds the sequences in registers.
-constexpr int kHeld = 8, kSortable = 32 * kHeld;
+// end.  A warp's work; the sequences' first tokens, tokens and tiles in shared memory.
+constexpr int kSortable = 256;
 struct Sorted {
-    int lo[kHeld], n[kHeld], q[kHeld], most;
+    int lo[kSortable], n[kSortable], q[kSortable];
 };
-__device__ __forceinline__ void load_sorted(const PromptParams &p, Sorted &s) {
+// Returns the most tiles of a sequence.
+__device__ __forceinline__ int load_sorted(const PromptParams &p, Sorted &s) {
     const int lane = threadIdx.x & 31;
-    int hi[kHeld];
-#pragma unroll
-    for (int k = 0; k < kHeld; ++k) {
-        const int b = 32 * k + lane;
-        s.lo[k] = hi[k] = 0;
-        if (b < p.B) {
-            s.lo[k] = p.start[b];
-            hi[k] = p.start[b + 1];
-        }
-    }
     bool fell = false;
-    s.most = 0;
-#pragma unroll
-    for (int k = 0; k < kHeld; ++k) {
-        const uint32_t falls = __ballot_sync(0xffffffffu, s.lo[k] < 0 || hi[k] < s.lo[k] || hi[k] > p.T);
-        s.n[k] = fell || (falls & ((2u << lane) - 1u)) ? 0 : hi[k] - s.lo[k];
+    int most = 0;
+    for (int b0 = 0; b0 < p.B; b0 += 32) {
+        const int b = b0 + lane;
+        int lo = 0, hi = 0;
+        if (b < p.B) {
+            lo = p.start[b];
+            hi = p.start[b + 1];
+        }
+        const uint32_t falls = __ballot_sync(0xffffffffu, lo < 0 || hi < lo || hi > p.T);
+        const int n = fell || (falls & ((2u << lane) - 1u)) ? 0 : hi - lo;
         fell = fell || falls != 0;
-        s.q[k] = tiles_of(p, s.n[k]);
-        s.most = max(s.most, s.q[k]);
+        s.lo[b] = lo;
+        s.n[b] = n;
+        s.q[b] = tiles_of(p, n);
+        most = max(most, s.q[b]);
     }
     if (blockIdx.x == 0 && lane == 0 && fell) report(p.dev_status, kErrInvalid);
-    s.most = __reduce_max_sync(0xffffffffu, s.most);
+    return __reduce_max_sync(0xffffffffu, most);
 }
-__device__ __forceinline__ bool find_sorted(const PromptParams &p, const Sorted &s, int rank, Work &w) {
+__device__ __forceinline__ bool find_sorted(const PromptParams &p, const Sorted &s, int most, int rank, Work &w) {
     const int lane = threadIdx.x & 31;
     auto above = [&](int c) {      // tiles of a cost above c
         int f = 0;
-#pragma unroll
-        for (int k = 0; k < kHeld; ++k) f += p.causal ? max(0, s.q[k] - c) : s.q[k] > c ? s.q[k] : 0;
+        for (int b = lane; b < p.B; b += 32) f += p.causal ? max(0, s.q[b] - c) : s.q[b] > c ? s.q[b] : 0;
         return static_cast<int>(__reduce_add_sync(0xffffffffu, f));
     };
     if (above(0) <= rank) return false;
-    int a = 0, z = s.most;      // above(a) > rank >= above(z)
+    int a = 0, z = most;      // above(a) > rank >= above(z)
     while (z - a > 1) {
         const int mid = a + (z - a) / 2;
         if (above(mid) > rank)
@@ -147,9 +146,8 @@ __device__ __forceinline__ bool find_sorted(const PromptParams &p, const Sorted 
             z = mid;
     }
     int left = rank - above(z);      // among the tiles of cost a + 1, in the sequences' order
-#pragma unroll
-    for (int k = 0; k < kHeld; ++k) {
-        const int has = p.causal ? (s.q[k] > a) : s.q[k] == a + 1 ? s.q[k] : 0;
+    for (int b0 = 0; b0 < p.B; b0 += 32) {
+        const int q = b0 + lane < p.B ? s.q[b0 + lane] : 0, has = p.causal ? (q > a) : q == a + 1 ? q : 0;
         int incl = has;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -159,8 +157,8 @@ __device__ __forceinline__ bool find_sorted(const PromptParams &p, const Sorted 
         const uint32_t hit = __ballot_sync(0xffffffffu, left < incl);
         if (hit) {
             const int l = __ffs(hit) - 1;
-            w.row0 = __shfl_sync(0xffffffffu, s.lo[k], l);
-            w.n = __shfl_sync(0xffffffffu, s.n[k], l);
+            w.row0 = s.lo[b0 + l];
+            w.n = s.n[b0 + l];
             w.tile = p.causal ? a : left - __shfl_sync(0xffffffffu, incl - has, l);
             return true;
         }
@@ -190,12 +188,12 @@ __device__ __forceinline__ bool find_searched(const PromptParams &p, int rise, i
     return w.tile < tiles_of(p, w.n);
 }
 
-// Key blocks that the rows of tile t see; 0: it has no rows.
-__device__ __forceinline__ int blocks_of(const PromptParams &p, const Work &w, int t) {
+// Keys that the rows of tile t see, and blocks of them; 0: it has no rows.
+__device__ __forceinline__ int seen_by(const PromptParams &p, const Work &w, int t) {
     const int first = (2 * w.tile + t) * p.tokens;
-    if (first >= w.n) return 0;
-    return ((p.causal ? min(w.n, first + p.tokens) : w.n) + kBlk - 1) / kBlk;
+    return first >= w.n ? 0 : p.causal ? min(w.n, first + p.tokens) : w.n;
 }
+__device__ __forceinline__ int blocks_of(const PromptParams &p, const Work &w, int t) { return (seen_by(p, w, t) + kBlk - 1) / kBlk; }
 // The block that ends behind the sequence's last token, if it is among the first nbs; else -1.
 __device__ __forceinline__ int tail_of(const Work &w, int nbs) {
     return w.n % kBlk && nbs == (w.n + kBlk - 1) / kBlk ? nbs - 1 : -1;
@@ -267,8 +265,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     prompt_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                   const __grid_constant__ CUtensorMap tmV, const PromptParams p) {
     extern __shared__ unsigned char smem_raw[];
-    unsigned char *smem =
-        reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    unsigned char *smem = smem_raw + (0u - smem_u32(smem_raw)) % 1024u;
     uint64_t *full = reinterpret_cast<uint64_t *>(smem + kOffBar), *empty = full + kStages, *raw = empty + kStages;
     uint64_t *q_full = raw + kStages, *q_free = q_full + kTiles, *s_full = q_free + kTiles, *p_full = s_full + kTiles;
     uint64_t *o_full = p_full + 2 * kTiles, *o_free = o_full + kTiles, *w_full = o_free + kTiles, *w_free = w_full + kWorks;
@@ -277,6 +274,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     int *abort_flag = reinterpret_cast<int *>(smem + kOffMisc + 4);
     int *first_fall = reinterpret_cast<int *>(smem + kOffMisc + 8);
     Work *works = reinterpret_cast<Work *>(smem + kOffWork);
+    float *stats = reinterpret_cast<float *>(smem + kOffStat);
 
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
@@ -291,12 +289,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(s_full + t, 1);
             mbar_init(p_full + 2 * t, 4);
             mbar_init(p_full + 2 * t + 1, 4);
-            mbar_init(o_full + t, 1);
+            mbar_init(o_full + t, 1 + 4);      // the last MMAs, and the softmax warps' statistics
             mbar_init(o_free + t, 4);
         }
         for (int i = 0; i < kWorks; ++i) {
             mbar_init(w_full + i, 1);
-            mbar_init(w_free + i, 3 + 4 * kTiles);
+            mbar_init(w_free + i, 3 + 4 * kTiles + 4);
         }
         mbar_init(drain, 1);
         *abort_flag = 0;
@@ -331,9 +329,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) mbar_arrive(w_free + k % kWorks);
     };
 
-    // registers: 128 x 80 + 256 x 208 of the 384 x 168 at launch
+    // registers: 128 x 72 + 256 x 184 + 128 x 72 = 512 x 128, those at launch
     if (warp < kSoftWarp0) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
         if (warp == 0) {
             // -------------------------------------------------------- producer of K and V
             Work w;
@@ -375,7 +373,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         } else if (warp == 1) {
             // -------------------------------------------------------- MMA issuer
-            constexpr uint32_t idesc_qk = make_idesc(128, 128, 1, 1), idesc_pv = make_idesc(128, 128, 1, 1, 0, 1);
             const uint32_t base = smem_u32(smem);
             const bool one = elect_one();
             auto wait = [&](uint64_t *bar, int parity) {
@@ -383,13 +380,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tc_fence_after();
                 return ok;
             };
-            auto qk = [&](int t, int st) {
+            // a block of which the tile sees 64 keys or fewer is half a block
+            auto qk = [&](int t, int st, bool half) {
                 const uint64_t dq = sdesc_k_sw128(base + kOffQ + t * kBlock), dk = sdesc_k_sw128(base + kOffKV + st * kBlock);
+                const uint32_t idesc = half ? make_idesc(128, 64, 1, 1) : make_idesc(128, 128, 1, 1);
                 if (one) {
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
                         const uint32_t step = (i >> 2) * (kPanel >> 4) + 2 * (i & 3);
-                        mma_f16(tmem + kTmemS + 128 * t, dq + step, dk + step, idesc_qk, i > 0);
+                        mma_f16(tmem + kTmemS + 128 * t, dq + step, dk + step, idesc, i > 0);
                     }
                     tc_commit(s_full + t);
                 }
@@ -400,7 +399,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
                         mma_f16_ts(tmem + kTmemO + 128 * t, tmem + kTmemS + 128 * t + 32 * half + 8 * i,
-                                   dv + (2048 >> 4) * (4 * half + i), idesc_pv, !first || i > 0);
+                                   dv + (2048 >> 4) * (4 * half + i), make_idesc(128, 128, 1, 1, 0, 1), !first || i > 0);
                 }
             };
             auto commit = [&](uint64_t *bar) {
@@ -409,61 +408,88 @@ __global__ void __launch_bounds__(kThreads, 1)
             Work w;
             int i0 = 0;                         // the ring's copies before this work's
             uint32_t blocks[kTiles] = {0, 0};   // of each tile so far
-            uint32_t had1 = 0;                  // works that had a second tile
-            bool ok = true;
-            for (int k = 0; ok && next_work(k, w); ++k) {
-                const int nb0 = blocks_of(p, w, 0), nb1 = blocks_of(p, w, 1), nbs = max(nb0, nb1);
-                ok = wait(full + i0 % kStages, (i0 / kStages) & 1);
+            uint32_t had[kTiles] = {0, 0};      // works that had the tile, the current one not among them
+            // a work's first QK, of tile t; its first block is in the ring's copy `at`
+            auto begin = [&](int t, int seen, int at) {
+                if (seen == 0) return true;
+                if (!wait(full + at % kStages, (at / kStages) & 1) || !wait(q_full + t, had[t] & 1)) return false;
+                qk(t, at % kStages, seen <= 64);
+                if (seen <= kBlk) commit(q_free + t);
+                return true;
+            };
+            bool ok = next_work(0, w);
+            int seen[kTiles] = {0, 0};
+            if (ok) {
 #pragma unroll
                 for (int t = 0; t < kTiles; ++t) {
-                    if (!ok || (t == 1 && nb1 == 0)) continue;
-                    ok = wait(q_full + t, (t ? had1 : k) & 1);
-                    if (!ok) continue;
-                    qk(t, i0 % kStages);
-                    if ((t ? nb1 : nb0) == 1) commit(q_free + t);
+                    seen[t] = seen_by(p, w, t);
+                    ok = ok && begin(t, seen[t], 0);
                 }
-                commit(empty + i0 % kStages);
+                commit(empty);
+            }
+            for (int k = 0; ok; ++k) {
+                const int nbs = (max(seen[0], seen[1]) + kBlk - 1) / kBlk, i1 = i0 + 2 * nbs;
+                Work next;
+                int sees[kTiles] = {0, 0};
+                bool more = false;
                 for (int j = 0; ok && j < nbs; ++j) {
                     const int iv = i0 + 2 * j + 1, ik = iv + 1, sv = iv % kStages, sk = ik % kStages;
                     const int pv_turn = (iv / kStages) & 1, pk_turn = (ik / kStages) & 1;
+                    const bool last = j + 1 == nbs;
                     // Several barriers are tested at once, before they are needed: one test after
                     // the other, 130 cycles each, left the tensor core idle
-                    bool there = mbar_test_wait(full + sv, pv_turn) & (j + 1 >= nbs || mbar_test_wait(full + sk, pk_turn));
+                    bool there = mbar_test_wait(full + sv, pv_turn) & (last || mbar_test_wait(full + sk, pk_turn));
+                    if (last) {
+                        // what follows: each tile goes on to its next work's first scores
+                        more = next_work(k + 1, next);
+#pragma unroll
+                        for (int t = 0; t < kTiles; ++t) sees[t] = more ? seen_by(p, next, t) : 0;
+                    }
 #pragma unroll
                     for (int t = 0; t < kTiles; ++t) {
-                        const int last = t ? nb1 : nb0;
-                        if (!ok || j >= last) continue;
-                        const int turn = static_cast<int>(blocks[t]++) & 1, earlier = t ? static_cast<int>(had1) : k;
-                        uint64_t *halves = p_full + 2 * t;
-                        const bool first = mbar_test_wait(halves, turn), second = mbar_test_wait(halves + 1, turn);
-                        if (!__all_sync(0xffffffffu, there)) {
-                            ok = wait(full + sv, pv_turn);
-                            if (ok && j + 1 < nbs) ok = wait(full + sk, pk_turn);
-                            there = true;
+                        const int left = seen[t] - j * kBlk;      // keys of this block and behind
+                        if (ok && left > 0) {
+                            const int turn = static_cast<int>(blocks[t]++) & 1;
+                            uint64_t *halves = p_full + 2 * t;
+                            const bool first = mbar_test_wait(halves, turn), second = mbar_test_wait(halves + 1, turn);
+                            if (!__all_sync(0xffffffffu, there)) {
+                                ok = wait(full + sv, pv_turn);
+                                if (ok && !last) ok = wait(full + sk, pk_turn);
+                                there = true;
+                            }
+                            // O's first product waits until the epilogue before has read it
+                            if (ok && j == 0 && had[t] > 0) ok = wait(o_free + t, (had[t] - 1) & 1);
+                            if (ok && !__all_sync(0xffffffffu, first)) ok = wait(halves, turn);
+                            if (!ok) continue;
+                            tc_fence_after();
+                            pv(t, sv, 0, j == 0);
+                            if (!__all_sync(0xffffffffu, second)) ok = wait(halves + 1, turn);
+                            if (!ok) continue;
+                            tc_fence_after();
+                            if (left > 64) pv(t, sv, 1, false);
+                            if (t == 1 || j * kBlk >= seen[1]) commit(empty + sv);
+                            if (left > kBlk) {
+                                qk(t, sk, left <= kBlk + 64);
+                                if (left <= 2 * kBlk) commit(q_free + t);
+                            } else {
+                                commit(o_full + t);
+                            }
                         }
-                        // O's first product waits until the epilogue before has read it
-                        if (ok && j == 0 && earlier > 0) ok = wait(o_free + t, (earlier - 1) & 1);
-                        if (ok && !__all_sync(0xffffffffu, first)) ok = wait(halves, turn);
-                        if (!ok) continue;
-                        tc_fence_after();
-                        pv(t, sv, 0, j == 0);
-                        if (!__all_sync(0xffffffffu, second)) ok = wait(halves + 1, turn);
-                        if (!ok) continue;
-                        tc_fence_after();
-                        pv(t, sv, 1, false);
-                        if (t == 1 || j >= nb1) commit(empty + sv);
-                        if (j + 1 < last) {
-                            qk(t, sk);
-                            if (j + 2 == last) commit(q_free + t);
-                        } else {
-                            commit(o_full + t);
+                        if (ok && last) {
+                            had[t] += seen[t] > 0;
+                            ok = begin(t, sees[t], i1);
                         }
                     }
-                    if (ok && j + 1 < nbs) commit(empty + sk);
+                    if (ok && !last) commit(empty + sk);
                 }
-                i0 += 2 * nbs;
-                had1 += nb1 > 0;
+                if (!ok) break;
                 work_done(k);
+                if (!more) break;
+                commit(empty + i1 % kStages);
+                w = next;
+                i0 = i1;
+                seen[0] = sees[0];
+                seen[1] = sees[1];
             }
             commit(drain);
             if (one) drain_wait(drain, 0, p.limit_ns);
@@ -492,10 +518,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         } else {
             // -------------------------------------------------------- the CTA's work, and its queries
-            Sorted s;
+            Sorted &s = *reinterpret_cast<Sorted *>(smem + kOffSort);
             const int rise = *first_fall;
+            int most = 0;
             if (p.B <= kSortable)
-                load_sorted(p, s);
+                most = load_sorted(p, s);
             else if (blockIdx.x == 0 && lane == 0 && rise < p.B)
                 report(p.dev_status, kErrInvalid);
             const int ctas = static_cast<int>(gridDim.x), me = static_cast<int>(blockIdx.x);
@@ -510,7 +537,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (!end) {
                     const int rank = static_cast<int>(index / p.groups);
                     w.group = static_cast<int>(index % p.groups);
-                    if (!(p.B <= kSortable ? find_sorted(p, s, rank, w) : find_searched(p, rise, rank, w))) continue;
+                    if (!(p.B <= kSortable ? find_sorted(p, s, most, rank, w) : find_searched(p, rise, rank, w))) continue;
                 }
                 if (k >= kWorks) ok = __all_sync(0xffffffffu, mbar_wait(w_free + k % kWorks, (k / kWorks - 1) & 1, abort_flag, p.limit_ns));
                 if (!ok) break;
@@ -547,19 +574,19 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (queries[t] >= 0) drain_wait(q_full + t, queries[t] & 1, p.limit_ns);
             }
         }
-    } else {
+    } else if (warp < kOutWarp0) {
         // ------------------------------------------------------------ softmax
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
         const int t = (warp - kSoftWarp0) >> 2, quarter = warp & 3, row = quarter * 32 + lane;
         const float kNegInf = __int_as_float(0xff800000);
         const uint32_t tl = tmem + (static_cast<uint32_t>(quarter * 32) << 16), tS = tl + kTmemS + 128 * t,
                        tO = tl + kTmemO + 128 * t;
-        const int row_token = row / p.G, row_head = row % p.G;
+        const int row_token = row / p.G;
         Work w;
         uint32_t blocks = 0, had = 0;      // of this tile so far, and works that had it
         bool ok = true;
         for (int k = 0; ok && next_work(k, w); ++k) {
-            const int n_blocks = blocks_of(p, w, t);
+            const int tile_sees = seen_by(p, w, t), n_blocks = (tile_sees + kBlk - 1) / kBlk;
             work_done(k);
             if (n_blocks == 0) continue;
             const int token = (2 * w.tile + t) * p.tokens + row_token;
@@ -579,19 +606,26 @@ __global__ void __launch_bounds__(kThreads, 1)
                 uint32_t X[4][32];
                 float mx[4];
                 s.edge = b >= whole;
+                const bool half_block = tile_sees - b * kBlk <= 64;
+                mx[2] = mx[3] = kNegInf;
                 if constexpr (kCap) {
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) VCA_TMEM_LDTOP32(tS + 32 * i, X[i], mx[i]);
+                    for (int i = 0; i < 4; ++i)
+                        if (i < 2 || !half_block) VCA_TMEM_LDTOP32(tS + 32 * i, X[i], mx[i]);
                     tmem_ld_wait();
                     s.near = __all_sync(0xffffffffu, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * s.c <= kTanhNear);
                 }
 #pragma unroll
-                for (int i = 0; i < 4; ++i) VCA_TMEM_LDMAX32(tS + 32 * i, X[i], mx[i]);
+                for (int i = 0; i < 4; ++i)
+                    if (i < 2 || !half_block) VCA_TMEM_LDMAX32(tS + 32 * i, X[i], mx[i]);
                 tmem_ld_wait();
+                s.lim = seen - b * kBlk;
                 if (s.edge) {
-                    s.lim = seen - b * kBlk;
+                    // 32 columns at a time: mostly all rows of the warp see them, or none
+                    const int least = __reduce_min_sync(0xffffffffu, s.lim);
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) mx[i] = mask_scores<kCap>(X[i], 32 * i, s.lim);
+                    for (int i = 0; i < 4; ++i)
+                        if (least < 32 * (i + 1) && (i < 2 || !half_block)) mx[i] = mask_scores<kCap>(X[i], 32 * i, s.lim);
                 }
                 const float pm = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * s.c;
                 const float bm = kCap ? capped(pm, p.cap_out) : pm;
@@ -618,82 +652,109 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
 #pragma unroll
                 for (int half = 0; half < 2; ++half) {
+                    if (half == 0 || !half_block) {
 #pragma unroll
-                    for (int i = 2 * half; i < 2 * half + 2; ++i) {
-                        uint32_t W[16];
-                        probabilities<kCap>(X[i], s, 32 * i, l2, W);
-                        VCA_TMEM_ST16(tS + 16 * i, W);
+                        for (int i = 2 * half; i < 2 * half + 2; ++i) {
+                            uint32_t W[16];
+                            probabilities<kCap>(X[i], s, 32 * i, l2, W);
+                            VCA_TMEM_ST16(tS + 16 * i, W);
+                        }
+                        tmem_st_wait();
                     }
-                    tmem_st_wait();
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(p_full + 2 * t + half);
                 }
             }
             if (!ok) break;
-            // -------------------------------------------------------- epilogue
-            const int64_t at = static_cast<int64_t>(w.row0 + token) * p.Hq + w.group * p.G + row_head;
-            float l;
-            {
-                float a, c;
-                upk2(l2, a, c);
-                l = __fadd_rn(a, c);
-            }
-            // joined with what came before: both sums to the larger maximum
-            float before = kNegInf, keep = 1.0f, add = 0.0f, M = m;
-            if (p.prior && real) before = p.prior_lse[at] * 1.4426950408889634f;
-            const bool joins = before != kNegInf;
-            if (joins) {
-                M = before != before ? before : fmaxf(m, before);
-                keep = m == kNegInf ? 0.0f : ex2_approx(__fsub_rn(m, M));
-                add = ex2_approx(__fsub_rn(before, M));
-                l = __fadd_rn(__fmul_rn(l, keep), add);
-            }
-            const float inv = l > 0.0f || l != l ? 1.0f / l : 0.0f;
-            keep *= inv;
-            add *= inv;
-            ok = __all_sync(0xffffffffu, mbar_wait(o_full + t, had++ & 1, abort_flag, p.limit_ns));
-            if (!ok) break;
-            tc_fence_after();
-            const uint4 *prior = reinterpret_cast<const uint4 *>(p.prior + at * kD);
-            uint32_t y[kD / 2];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                uint32_t o[32];
-                VCA_TMEM_LD32(tO + 32 * i, o);
-                tmem_ld_wait();
-#pragma unroll
-                for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__fmul_rn(__uint_as_float(o[e]), keep));
+            // the row's maximum and sum go to the epilogue.  By turns: before the scores of
+            // the work after next come, the epilogue has read O and these
+            float a, c;
+            upk2(l2, a, c);
+            float *mine = stats + ((had++ & 1) * kTiles + t) * 2 * kBlk + row;
+            mine[0] = m;
+            mine[kBlk] = __fadd_rn(a, c);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(o_full + t);
+        }
+    } else {
+        // ------------------------------------------------------------ epilogue
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+        const int quarter = warp & 3, row = quarter * 32 + lane, row_token = row / p.G, row_head = row % p.G;
+        const float kNegInf = __int_as_float(0xff800000);
+        Work w;
+        uint32_t had[kTiles] = {0, 0};
+        bool ok = true;
+        for (int k = 0; ok && next_work(k, w); ++k) {
+#pragma unroll 1
+            for (int t = 0; ok && t < kTiles; ++t) {
+                if (seen_by(p, w, t) == 0) break;
+                const int token = (2 * w.tile + t) * p.tokens + row_token;
+                const bool real = row_token < p.tokens && token < w.n;
+                const int64_t at = static_cast<int64_t>(w.row0 + token) * p.Hq + w.group * p.G + row_head;
+                float before = kNegInf, keep = 1.0f, add = 0.0f;
+                if (p.prior && real) before = p.prior_lse[at] * 1.4426950408889634f;
+                const uint32_t turn = t == 0 ? had[0]++ : had[1]++;
+                ok = __all_sync(0xffffffffu, mbar_wait(o_full + t, turn & 1, abort_flag, p.limit_ns));
+                if (!ok) break;
+                tc_fence_after();
+                const float *stat = stats + ((turn & 1) * kTiles + t) * 2 * kBlk + row;
+                float M = stat[0], l = stat[kBlk];
+                // joined with what came before: both sums to the larger maximum
+                const bool joins = before != kNegInf;
                 if (joins) {
+                    const float m = M;
+                    M = before != before ? before : fmaxf(m, before);
+                    keep = m == kNegInf ? 0.0f : ex2_approx(__fsub_rn(m, M));
+                    add = ex2_approx(__fsub_rn(before, M));
+                    l = __fadd_rn(__fmul_rn(l, keep), add);
+                }
+                const float inv = l > 0.0f || l != l ? 1.0f / l : 0.0f;
+                keep *= inv;
+                add *= inv;
+                const uint32_t tO = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + kTmemO + 128 * t;
+                const uint4 *prior = reinterpret_cast<const uint4 *>(p.prior + at * kD);
+                uint16_t *to = p.O + at * kD;
+#pragma unroll 1
+                for (int i = 0; i < 4; ++i) {
+                    uint32_t o[32];
+                    VCA_TMEM_LD32(tO + 32 * i, o);
+                    tmem_ld_wait();
+                    if (i == 3) {      // O is read
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(o_free + t);
+                    }
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const uint4 x = prior[4 * i + e];
-                        const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
+                    for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__fmul_rn(__uint_as_float(o[e]), keep));
+                    if (joins) {
 #pragma unroll
-                        for (int k2 = 0; k2 < 4; ++k2) {
-                            uint32_t &lo = o[8 * e + 2 * k2], &hi = o[8 * e + 2 * k2 + 1];
-                            lo = __float_as_uint(fmaf(__uint_as_float(xs[k2] << 16), add, __uint_as_float(lo)));
-                            hi = __float_as_uint(fmaf(__uint_as_float(xs[k2] & 0xffff0000u), add, __uint_as_float(hi)));
+                        for (int e = 0; e < 4; ++e) {
+                            const uint4 x = prior[4 * i + e];
+                            const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+                            for (int q = 0; q < 4; ++q) {
+                                uint32_t &lo = o[8 * e + 2 * q], &hi = o[8 * e + 2 * q + 1];
+                                lo = __float_as_uint(fmaf(__uint_as_float(xs[q] << 16), add, __uint_as_float(lo)));
+                                hi = __float_as_uint(fmaf(__uint_as_float(xs[q] & 0xffff0000u), add, __uint_as_float(hi)));
+                            }
+                        }
+                    }
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) o[e] = pack_bf16x2(__uint_as_float(o[2 * e]), __uint_as_float(o[2 * e + 1]));
+                    if (real) {
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            if (p.wide)
+                                store32<true>(to + 32 * i + 16 * e, o + 8 * e);
+                            else
+                                store32<false>(to + 32 * i + 16 * e, o + 8 * e);
                         }
                     }
                 }
-#pragma unroll
-                for (int e = 0; e < 16; ++e) y[16 * i + e] = pack_bf16x2(__uint_as_float(o[2 * e]), __uint_as_float(o[2 * e + 1]));
+                if (p.lse && real) p.lse[at] = (M == kNegInf ? 0.0f : M) * 0.6931471805599453f + logf(l);
             }
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(o_free + t);
-            if (real) {
-                uint16_t *to = p.O + at * kD;
-                if (p.wide) {
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) store32<true>(to + 16 * e, y + 8 * e);
-                } else {
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) store32<false>(to + 16 * e, y + 8 * e);
-                }
-                if (p.lse) p.lse[at] = (M == kNegInf ? 0.0f : M) * 0.6931471805599453f + logf(l);
-            }
+            work_done(k);
         }
     }
 
