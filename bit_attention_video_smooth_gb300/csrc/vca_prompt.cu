@@ -429,58 +429,62 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             for (int k = 0; ok; ++k) {
                 const int nbs = (max(seen[0], seen[1]) + kBlk - 1) / kBlk, i1 = i0 + 2 * nbs;
-                Work next;
-                int sees[kTiles] = {0, 0};
-                bool more = false;
-                for (int j = 0; ok && j < nbs; ++j) {
+                // Barriers are tested before they are needed, several at once, and V's and K's of the
+                // next block while the tensor core has the second tile's scores to do: a test takes 100
+                // cycles, and one after the other left it idle
+                auto landed = [&](int j) {      // V of block j, and K of the next
+                    const int iv = i0 + 2 * j + 1, ik = iv + 1;
+                    return mbar_test_wait(full + iv % kStages, (iv / kStages) & 1) &
+                           (j + 1 >= nbs || mbar_test_wait(full + ik % kStages, (ik / kStages) & 1));
+                };
+                bool there = landed(0);
+                // A block of tile t: its PV and, unless it is the work's last block, the next QK.
+                auto block = [&](int t, int j, bool last) {
+                    const int left = seen[t] - j * kBlk;      // keys of this block and behind
+                    if (left <= 0) return true;
                     const int iv = i0 + 2 * j + 1, ik = iv + 1, sv = iv % kStages, sk = ik % kStages;
-                    const int pv_turn = (iv / kStages) & 1, pk_turn = (ik / kStages) & 1;
-                    const bool last = j + 1 == nbs;
-                    // Several barriers are tested at once, before they are needed: one test after
-                    // the other, 130 cycles each, left the tensor core idle
-                    bool there = mbar_test_wait(full + sv, pv_turn) & (last || mbar_test_wait(full + sk, pk_turn));
-                    if (last) {
-                        // what follows: each tile goes on to its next work's first scores
-                        more = next_work(k + 1, next);
-#pragma unroll
-                        for (int t = 0; t < kTiles; ++t) sees[t] = more ? seen_by(p, next, t) : 0;
+                    const int turn = static_cast<int>(blocks[t]++) & 1;
+                    uint64_t *halves = p_full + 2 * t;
+                    const bool first = mbar_test_wait(halves, turn), second = mbar_test_wait(halves + 1, turn);
+                    if (!__all_sync(0xffffffffu, there)) {
+                        if (!wait(full + sv, (iv / kStages) & 1)) return false;
+                        if (!last && !wait(full + sk, (ik / kStages) & 1)) return false;
+                        there = true;
                     }
-#pragma unroll
-                    for (int t = 0; t < kTiles; ++t) {
-                        const int left = seen[t] - j * kBlk;      // keys of this block and behind
-                        if (ok && left > 0) {
-                            const int turn = static_cast<int>(blocks[t]++) & 1;
-                            uint64_t *halves = p_full + 2 * t;
-                            const bool first = mbar_test_wait(halves, turn), second = mbar_test_wait(halves + 1, turn);
-                            if (!__all_sync(0xffffffffu, there)) {
-                                ok = wait(full + sv, pv_turn);
-                                if (ok && !last) ok = wait(full + sk, pk_turn);
-                                there = true;
-                            }
-                            // O's first product waits until the epilogue before has read it
-                            if (ok && j == 0 && had[t] > 0) ok = wait(o_free + t, (had[t] - 1) & 1);
-                            if (ok && !__all_sync(0xffffffffu, first)) ok = wait(halves, turn);
-                            if (!ok) continue;
-                            tc_fence_after();
-                            pv(t, sv, 0, j == 0);
-                            if (!__all_sync(0xffffffffu, second)) ok = wait(halves + 1, turn);
-                            if (!ok) continue;
-                            tc_fence_after();
-                            if (left > 64) pv(t, sv, 1, false);
-                            if (t == 1 || j * kBlk >= seen[1]) commit(empty + sv);
-                            if (left > kBlk) {
-                                qk(t, sk, left <= kBlk + 64);
-                                if (left <= 2 * kBlk) commit(q_free + t);
-                            } else {
-                                commit(o_full + t);
-                            }
-                        }
-                        if (ok && last) {
-                            had[t] += seen[t] > 0;
-                            ok = begin(t, sees[t], i1);
-                        }
+                    // O's first product waits until the epilogue before has read it
+                    if (j == 0 && had[t] > 0 && !wait(o_free + t, (had[t] - 1) & 1)) return false;
+                    if (!__all_sync(0xffffffffu, first) && !wait(halves, turn)) return false;
+                    tc_fence_after();
+                    pv(t, sv, 0, j == 0);
+                    if (!__all_sync(0xffffffffu, second) && !wait(halves + 1, turn)) return false;
+                    tc_fence_after();
+                    if (left > 64) pv(t, sv, 1, false);
+                    if (t == 1 || j * kBlk >= seen[1]) {
+                        commit(empty + sv);
+                        there = last || landed(j + 1);
                     }
-                    if (ok && !last) commit(empty + sk);
+                    if (left > kBlk) {
+                        qk(t, sk, left <= kBlk + 64);
+                        if (left <= 2 * kBlk) commit(q_free + t);
+                    } else {
+                        commit(o_full + t);
+                    }
+                    return true;
+                };
+                for (int j = 0; ok && j + 1 < nbs; ++j) {
+                    ok = block(0, j, false) && block(1, j, false);
+                    if (ok) commit(empty + (i0 + 2 * j + 2) % kStages);
+                }
+                // the last one, after which each tile goes on to its next work's first scores
+                Work next;
+                const bool more = ok && next_work(k + 1, next);
+                int sees[kTiles] = {0, 0};
+#pragma unroll
+                for (int t = 0; t < kTiles; ++t) {
+                    sees[t] = more ? seen_by(p, next, t) : 0;
+                    ok = ok && block(t, nbs - 1, true);
+                    had[t] += seen[t] > 0;
+                    ok = ok && begin(t, sees[t], i1);
                 }
                 if (!ok) break;
                 work_done(k);
