@@ -81,6 +81,19 @@ __device__ __forceinline__ void tma_load_3d(void *smem_dst, const void *tmap, ui
           "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])    \
         : "r"(taddr))
 
+// mbar_wait in less code: the kernel's loops have to fit the instruction caches, and
+// a test suspends the thread for a thousand cycles anyway.
+__device__ __forceinline__ bool wait_phase(uint64_t *bar, uint32_t parity, int *abort, uint64_t limit_ns) {
+    if (mbar_try_wait(bar, parity)) return true;
+    const uint64_t t0 = globaltimer_ns();
+    do {
+        if (mbar_try_wait(bar, parity)) return true;
+        if (*reinterpret_cast<volatile int *>(abort)) return false;
+    } while (globaltimer_ns() - t0 <= limit_ns);
+    *reinterpret_cast<volatile int *>(abort) = 1;
+    return false;
+}
+
 // True in one thread of a converged warp.
 __device__ __forceinline__ bool elect_one() {
     uint32_t r;
@@ -320,7 +333,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // The k-th work of this CTA, from its slot; false at the end, or where a wait gave up.
     auto next_work = [&](int k, Work &w) {
         const int i = k % kWorks;
-        if (!__all_sync(0xffffffffu, mbar_wait(w_full + i, (k / kWorks) & 1, abort_flag, p.limit_ns))) return false;
+        if (!__all_sync(0xffffffffu, wait_phase(w_full + i, (k / kWorks) & 1, abort_flag, p.limit_ns))) return false;
         w = works[i];
         return w.n > 0;
     };
@@ -343,7 +356,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int nbs = max(blocks_of(p, w, 0), blocks_of(p, w, 1)), tail = tail_of(w, nbs);
                 for (int j = 0; ok && j < 2 * nbs; ++j, ++i) {
                     const int st = i % kStages;
-                    if (i >= kStages) ok = mbar_wait(empty + st, (i / kStages - 1) & 1, abort_flag, p.limit_ns);
+                    if (i >= kStages) ok = wait_phase(empty + st, (i / kStages - 1) & 1, abort_flag, p.limit_ns);
                     ok = __all_sync(0xffffffffu, ok);
                     if (!ok) break;
                     const bool is_v = j & 1, is_tail = j == 2 * tail + 1;
@@ -376,7 +389,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint32_t base = smem_u32(smem);
             const bool one = elect_one();
             auto wait = [&](uint64_t *bar, int parity) {
-                const bool ok = __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, p.limit_ns));
+                const bool ok = __all_sync(0xffffffffu, wait_phase(bar, parity, abort_flag, p.limit_ns));
                 tc_fence_after();
                 return ok;
             };
@@ -508,7 +521,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int nbs = max(blocks_of(p, w, 0), blocks_of(p, w, 1)), tail = tail_of(w, nbs);
                 if (tail >= 0) {
                     const int st = (i0 + 2 * tail + 1) % kStages, live = w.n - tail * kBlk;
-                    ok = __all_sync(0xffffffffu, mbar_wait(raw + st, (turns >> st) & 1, abort_flag, p.limit_ns));
+                    ok = __all_sync(0xffffffffu, wait_phase(raw + st, (turns >> st) & 1, abort_flag, p.limit_ns));
                     if (!ok) break;
                     turns ^= 1u << st;
                     uint4 *to = reinterpret_cast<uint4 *>(smem + kOffKV + st * kBlock);
@@ -543,7 +556,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     w.group = static_cast<int>(index % p.groups);
                     if (!(p.B <= kSortable ? find_sorted(p, s, most, rank, w) : find_searched(p, rise, rank, w))) continue;
                 }
-                if (k >= kWorks) ok = __all_sync(0xffffffffu, mbar_wait(w_free + k % kWorks, (k / kWorks - 1) & 1, abort_flag, p.limit_ns));
+                if (k >= kWorks) ok = __all_sync(0xffffffffu, wait_phase(w_free + k % kWorks, (k / kWorks - 1) & 1, abort_flag, p.limit_ns));
                 if (!ok) break;
                 __syncwarp();
                 if (lane == 0) {
@@ -556,7 +569,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int t = 0; ok && t < kTiles; ++t) {
                     const int token = (2 * w.tile + t) * p.tokens, earlier = t ? static_cast<int>(had1) : k;
                     if (token >= w.n) break;
-                    if (earlier > 0) ok = __all_sync(0xffffffffu, mbar_wait(q_free + t, (earlier - 1) & 1, abort_flag, p.limit_ns));
+                    if (earlier > 0) ok = __all_sync(0xffffffffu, wait_phase(q_free + t, (earlier - 1) & 1, abort_flag, p.limit_ns));
                     if (!ok) break;
                     if (lane == 0) {
                         unsigned char *sQ = smem + kOffQ + t * kBlock;
@@ -604,7 +617,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             float m = kNegInf;
             uint64_t l2 = 0;
             for (int b = 0; b < n_blocks; ++b) {
-                ok = __all_sync(0xffffffffu, mbar_wait(s_full + t, blocks++ & 1, abort_flag, p.limit_ns));
+                ok = __all_sync(0xffffffffu, wait_phase(s_full + t, blocks++ & 1, abort_flag, p.limit_ns));
                 if (!ok) break;
                 tc_fence_after();
                 uint32_t X[4][32];
@@ -699,7 +712,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 float before = kNegInf, keep = 1.0f, add = 0.0f;
                 if (p.prior && real) before = p.prior_lse[at] * 1.4426950408889634f;
                 const uint32_t turn = t == 0 ? had[0]++ : had[1]++;
-                ok = __all_sync(0xffffffffu, mbar_wait(o_full + t, turn & 1, abort_flag, p.limit_ns));
+                ok = __all_sync(0xffffffffu, wait_phase(o_full + t, turn & 1, abort_flag, p.limit_ns));
                 if (!ok) break;
                 tc_fence_after();
                 const float *stat = stats + ((turn & 1) * kTiles + t) * 2 * kBlk + row;
