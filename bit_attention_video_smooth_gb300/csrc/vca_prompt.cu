@@ -215,47 +215,64 @@ __device__ __forceinline__ int tail_of(const Work &w, int nbs) {
 // ---------------------------------------------------------------------------
 // Softmax pieces
 // ---------------------------------------------------------------------------
-struct BlockScore {
-    float c, bias;       // no cap: p = 2^(S c + bias); cap: p = 2^(cap tanh_half(S c) + bias)
-    float cap;
-    bool near;           // the polynomial of the cap's tanh will do for the warp
-    int lim;             // columns of the block that the row sees
-    bool edge;           // some row of the warp does not see all
-};
+__device__ __forceinline__ uint64_t both(float x) { return pk2(__float_as_uint(x), __float_as_uint(x)); }
+__device__ __forceinline__ uint64_t pk2f(float lo, float hi) { return pk2(__float_as_uint(lo), __float_as_uint(hi)); }
+__device__ __forceinline__ float rcp_approx(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
 
-// 32 raw scores -> words of bf16 pairs; the unrounded probabilities add to l2.
-template <bool kCap>
-__device__ __forceinline__ void probabilities(uint32_t (&X)[32], const BlockScore &s, int col0, uint64_t &l2,
-                                              uint32_t *W) {
-    const uint64_t c2 = pk2(__float_as_uint(s.c), __float_as_uint(s.c));
-    const uint64_t b2 = pk2(__float_as_uint(s.bias), __float_as_uint(s.bias));
-    if constexpr (kCap) cap_scores(X, s.c, s.cap, s.near, [&](int) { return b2; });
+// 32 raw scores -> words of bf16 pairs, p = 2^(S c + bias); the unrounded ones add to l2.
+__device__ __forceinline__ void probabilities(const uint32_t (&X)[32], float c, float bias, uint64_t &l2, uint32_t (&W)[16]) {
+    const uint64_t c2 = both(c), b2 = both(bias);
 #pragma unroll
     for (int k = 0; k < 16; ++k) {
-        float a = __uint_as_float(X[2 * k]), b = __uint_as_float(X[2 * k + 1]);
-        if constexpr (!kCap) upk2(fma2(pk2(X[2 * k], X[2 * k + 1]), c2, b2), a, b);
+        float a, b;
+        upk2(fma2(pk2(X[2 * k], X[2 * k + 1]), c2, b2), a, b);
         a = ex2_approx(a);
         b = ex2_approx(b);
-        if constexpr (kCap) {
-            if (s.edge) {
-                if (col0 + 2 * k >= s.lim) a = 0.0f;
-                if (col0 + 2 * k + 1 >= s.lim) b = 0.0f;
-            }
-        }
-        l2 = add2(l2, pk2(__float_as_uint(a), __float_as_uint(b)));
+        l2 = add2(l2, pk2f(a, b));
         W[k] = pack_bf16x2(a, b);
     }
 }
 
-// Scores of keys that the row does not see become -inf (0 where a cap follows);
+// The same of capped scores, p = 2^(cap tanh_half(S c) + bias), and 0 from column `lim`
+// on.  Near 0 (in all lanes: `near`) tanh_half is its polynomial alone; else also
+// 1 - 2 / (1 + 2^u), which has an absolute error of 2^-22 and is taken from |u| =
+// kTanhNear on, as in tanh_half, but for pairs and without branches.
+__device__ __forceinline__ void capped_probabilities(const uint32_t (&X)[32], float c, float cap, float bias, bool near, int lim,
+                                                     uint64_t &l2, uint32_t (&W)[16]) {
+    const uint64_t c2 = both(c), b2 = both(bias), one = both(1.0f), far_m = both(-2.0f * cap), far_b = both(__fadd_rn(cap, bias));
+    const uint64_t t0 = both(cap * kT0), t1 = both(cap * kT1), t2 = both(cap * kT2), t3 = both(cap * kT3), t4 = both(cap * kT4);
+#pragma unroll
+    for (int k = 0; k < 16; ++k) {
+        const uint64_t u = mul2(pk2(X[2 * k], X[2 * k + 1]), c2), w = mul2(u, u);
+        float a, b;
+        upk2(fma2(u, fma2(fma2(fma2(fma2(t4, w, t3), w, t2), w, t1), w, t0), b2), a, b);
+        if (!near) {
+            float ua, ub, ra, rb;
+            upk2(u, ua, ub);
+            upk2(add2(pk2f(ex2_approx(ua), ex2_approx(ub)), one), ra, rb);
+            upk2(fma2(pk2f(rcp_approx(ra), rcp_approx(rb)), far_m, far_b), ra, rb);
+            a = fabsf(ua) <= kTanhNear ? a : ra;
+            b = fabsf(ub) <= kTanhNear ? b : rb;
+        }
+        a = 2 * k < lim ? ex2_approx(a) : 0.0f;
+        b = 2 * k + 1 < lim ? ex2_approx(b) : 0.0f;
+        l2 = add2(l2, pk2f(a, b));
+        W[k] = pack_bf16x2(a, b);
+    }
+}
+
+// Scores of keys that the row does not see, from column `lim` on, become -inf;
 // returns the largest of the others.
-template <bool kCap>
-__device__ __forceinline__ float mask_scores(uint32_t (&X)[32], int col0, int lim) {
+__device__ __forceinline__ float mask_scores(uint32_t (&X)[32], int lim) {
     float m = __int_as_float(0xff800000);
 #pragma unroll
     for (int e = 0; e < 32; ++e) {
-        if (col0 + e < lim) m = fmaxf(m, __uint_as_float(X[e]));
-        else X[e] = kCap ? 0u : 0xff800000u;
+        if (e < lim) m = fmaxf(m, __uint_as_float(X[e]));
+        else X[e] = 0xff800000u;
     }
     return m;
 }
@@ -342,7 +359,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) mbar_arrive(w_free + k % kWorks);
     };
 
-    // registers: 128 x 72 + 256 x 184 + 128 x 72 = 512 x 128, those at launch
+    // registers: 128 x 72 + 256 x 168 + 128 x 104 = 512 x 128, those at launch
     if (warp < kSoftWarp0) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
         if (warp == 0) {
@@ -492,12 +509,21 @@ __global__ void __launch_bounds__(kThreads, 1)
                 Work next;
                 const bool more = ok && next_work(k + 1, next);
                 int sees[kTiles] = {0, 0};
+                bool early = false;
 #pragma unroll
                 for (int t = 0; t < kTiles; ++t) {
                     sees[t] = more ? seen_by(p, next, t) : 0;
                     ok = ok && block(t, nbs - 1, true);
                     had[t] += seen[t] > 0;
-                    ok = ok && begin(t, sees[t], i1);
+                    if (t == 0) {
+                        // not where tile 1's block would wait for what this needs
+                        early = __all_sync(0xffffffffu, mbar_test_wait(q_full, had[0] & 1) &
+                                                            mbar_test_wait(full + i1 % kStages, (i1 / kStages) & 1));
+                        if (early) ok = ok && begin(0, sees[0], i1);
+                    } else {
+                        if (!early) ok = ok && begin(0, sees[0], i1);
+                        ok = ok && begin(1, sees[1], i1);
+                    }
                 }
                 if (!ok) break;
                 work_done(k);
@@ -593,7 +619,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     } else if (warp < kOutWarp0) {
         // ------------------------------------------------------------ softmax
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 168;");
         const int t = (warp - kSoftWarp0) >> 2, quarter = warp & 3, row = quarter * 32 + lane;
         const float kNegInf = __int_as_float(0xff800000);
         const uint32_t tl = tmem + (static_cast<uint32_t>(quarter * 32) << 16), tS = tl + kTmemS + 128 * t,
@@ -610,42 +636,50 @@ __global__ void __launch_bounds__(kThreads, 1)
             const bool real = row_token < p.tokens && token < w.n;
             const int seen = real && p.causal ? token + 1 : w.n;
             const int whole = __reduce_min_sync(0xffffffffu, seen) / kBlk;      // blocks that every row of the warp sees all of
-            BlockScore s;
-            s.c = fmaxf(kCap ? p.cap_in : p.scale_log2, 0x1p-149f);
-            s.cap = p.cap_out;
-            s.bias = 0.0f;
+            const float c = fmaxf(kCap ? p.cap_in : p.scale_log2, 0x1p-149f);      // above 0, so that -inf stays -inf
+            float bias = 0.0f;
             float m = kNegInf;
             uint64_t l2 = 0;
             for (int b = 0; b < n_blocks; ++b) {
                 ok = __all_sync(0xffffffffu, wait_phase(s_full + t, blocks++ & 1, abort_flag, p.limit_ns));
                 if (!ok) break;
                 tc_fence_after();
-                uint32_t X[4][32];
-                float mx[4];
-                s.edge = b >= whole;
-                const bool half_block = tile_sees - b * kBlk <= 64;
-                mx[2] = mx[3] = kNegInf;
+                const bool edge = b >= whole, half_block = tile_sees - b * kBlk <= 64;
+                const int lim = seen - b * kBlk;      // columns of the block that the row sees
+                // 32 columns at a time: mostly all rows of the warp see them
+                const int least = edge ? __reduce_min_sync(0xffffffffu, lim) : kBlk;
+                uint32_t X[kCap ? 1 : 4][32];
+                float bm = kNegInf;
+                uint32_t near = 0;
                 if constexpr (kCap) {
+                    // scores are loaded again where they are needed: the code of 32 columns fits the
+                    // instruction caches, that of 128 does not
+#pragma unroll 1
+                    for (int i = 0; i < (half_block ? 2 : 4); ++i) {
+                        float top, mx;
+                        VCA_TMEM_LDTOP32(tS + 32 * i, X[0], top);
+                        tmem_ld_wait();
+                        VCA_TMEM_LDMAX32(tS + 32 * i, X[0], mx);
+                        tmem_ld_wait();
+                        near |= __all_sync(0xffffffffu, top * c <= kTanhNear) ? 1u << i : 0u;
+                        if (least < 32 * (i + 1)) mx = mask_scores(X[0], lim - 32 * i);
+                        bm = fmaxf(bm, mx);
+                    }
+                    bm = capped(bm * c, p.cap_out);
+                } else {
+                    float mx[4];
+                    mx[2] = mx[3] = kNegInf;
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
-                        if (i < 2 || !half_block) VCA_TMEM_LDTOP32(tS + 32 * i, X[i], mx[i]);
+                        if (i < 2 || !half_block) VCA_TMEM_LDMAX32(tS + 32 * i, X[i], mx[i]);
                     tmem_ld_wait();
-                    s.near = __all_sync(0xffffffffu, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * s.c <= kTanhNear);
-                }
+                    if (edge) {
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    if (i < 2 || !half_block) VCA_TMEM_LDMAX32(tS + 32 * i, X[i], mx[i]);
-                tmem_ld_wait();
-                s.lim = seen - b * kBlk;
-                if (s.edge) {
-                    // 32 columns at a time: mostly all rows of the warp see them, or none
-                    const int least = __reduce_min_sync(0xffffffffu, s.lim);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        if (least < 32 * (i + 1) && (i < 2 || !half_block)) mx[i] = mask_scores<kCap>(X[i], 32 * i, s.lim);
+                        for (int i = 0; i < 4; ++i)
+                            if (least < 32 * (i + 1) && (i < 2 || !half_block)) mx[i] = mask_scores(X[i], lim - 32 * i);
+                    }
+                    bm = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c;
                 }
-                const float pm = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * s.c;
-                const float bm = kCap ? capped(pm, p.cap_out) : pm;
                 const bool rises = real && bm > __fadd_rn(m, kLazyTau);      // a row that is none may hold anything
                 if (__any_sync(0xffffffffu, rises)) {
                     float alpha = 1.0f;
@@ -653,7 +687,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         alpha = ex2_approx(__fsub_rn(m, bm));
                         l2 = mul2(l2, pk2(__float_as_uint(alpha), __float_as_uint(alpha)));
                         m = bm;
-                        s.bias = -m;
+                        bias = -m;
                     }
                     if (b > 0) {
 #pragma unroll 1
@@ -667,36 +701,53 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                     }
                 }
-#pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                    if (half == 0 || !half_block) {
-#pragma unroll
-                        for (int i = 2 * half; i < 2 * half + 2; ++i) {
-                            uint32_t W[16];
-                            probabilities<kCap>(X[i], s, 32 * i, l2, W);
-                            VCA_TMEM_ST16(tS + 16 * i, W);
-                        }
-                        tmem_st_wait();
-                    }
+                auto hand_over = [&](int half) {
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(p_full + 2 * t + half);
+                };
+                if constexpr (kCap) {
+#pragma unroll 1
+                    for (int i = 0; i < (half_block ? 2 : 4); ++i) {
+                        uint32_t W[16];
+                        VCA_TMEM_LD32(tS + 32 * i, X[0]);
+                        tmem_ld_wait();
+                        capped_probabilities(X[0], c, p.cap_out, bias, (near >> i) & 1u, least < 32 * (i + 1) ? lim - 32 * i : 32, l2, W);
+                        VCA_TMEM_ST16(tS + 16 * i, W);      // over scores already read
+                        tmem_st_wait();
+                        if (i & 1) hand_over(i >> 1);
+                    }
+                    if (half_block) hand_over(1);
+                } else {
+#pragma unroll
+                    for (int half = 0; half < 2; ++half) {
+                        if (half == 0 || !half_block) {
+#pragma unroll
+                            for (int i = 2 * half; i < 2 * half + 2; ++i) {
+                                uint32_t W[16];
+                                probabilities(X[i], c, bias, l2, W);
+                                VCA_TMEM_ST16(tS + 16 * i, W);
+                            }
+                            tmem_st_wait();
+                        }
+                        hand_over(half);
+                    }
                 }
             }
             if (!ok) break;
             // the row's maximum and sum go to the epilogue.  By turns: before the scores of
             // the work after next come, the epilogue has read O and these
-            float a, c;
-            upk2(l2, a, c);
+            float even, odd;
+            upk2(l2, even, odd);
             float *mine = stats + ((had++ & 1) * kTiles + t) * 2 * kBlk + row;
             mine[0] = m;
-            mine[kBlk] = __fadd_rn(a, c);
+            mine[kBlk] = __fadd_rn(even, odd);
             __syncwarp();
             if (lane == 0) mbar_arrive(o_full + t);
         }
     } else {
         // ------------------------------------------------------------ epilogue
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
         const int quarter = warp & 3, row = quarter * 32 + lane, row_token = row / p.G, row_head = row % p.G;
         const float kNegInf = __int_as_float(0xff800000);
         Work w;
