@@ -237,10 +237,14 @@ __device__ __forceinline__ void probabilities(const uint32_t (&X)[32], float c, 
     }
 }
 
-// The same of capped scores, p = 2^(cap tanh_half(S c) + bias), and 0 from column `lim`
-// on.  Near 0 (in all lanes: `near`) tanh_half is its polynomial alone; else also
-// 1 - 2 / (1 + 2^u), which has an absolute error of 2^-22 and is taken from |u| =
-// kTanhNear on, as in tanh_half, but for pairs and without branches.
+// The same of capped scores, p = 2^(cap tanh_half(S c) + bias), and 0 from column
+// `lim` on.  tanh_half(u) = 1 - 2 / (1 + 2^u) has an absolute error of 2^-22: enough
+// for caps up to kSmallCap, whose scores are then right to 2e-5 (kCap = 1).  For
+// larger ones (kCap = 2) it is taken from |u| = kTanhNear on and the polynomial, with
+// its relative error, below, as in tanh_half; alone where all lanes are `near`.
+// 4 prompts of up to 2,900 tokens, 32 heads over 8, cap 30: 198 us, by kCap = 2 322.
+constexpr float kSmallCap = 64.0f;
+template <int kCap>
 __device__ __forceinline__ void capped_probabilities(const uint32_t (&X)[32], float c, float cap, float bias, bool near, int lim,
                                                      uint64_t &l2, uint32_t (&W)[16]) {
     const uint64_t c2 = both(c), b2 = both(bias), one = both(1.0f), far_m = both(-2.0f * cap), far_b = both(__fadd_rn(cap, bias));
@@ -248,15 +252,15 @@ __device__ __forceinline__ void capped_probabilities(const uint32_t (&X)[32], fl
 #pragma unroll
     for (int k = 0; k < 16; ++k) {
         const uint64_t u = mul2(pk2(X[2 * k], X[2 * k + 1]), c2), w = mul2(u, u);
-        float a, b;
-        upk2(fma2(u, fma2(fma2(fma2(fma2(t4, w, t3), w, t2), w, t1), w, t0), b2), a, b);
-        if (!near) {
+        float a = 0.0f, b = 0.0f;
+        if constexpr (kCap == 2) upk2(fma2(u, fma2(fma2(fma2(fma2(t4, w, t3), w, t2), w, t1), w, t0), b2), a, b);
+        if (kCap == 1 || !near) {
             float ua, ub, ra, rb;
             upk2(u, ua, ub);
             upk2(add2(pk2f(ex2_approx(ua), ex2_approx(ub)), one), ra, rb);
             upk2(fma2(pk2f(rcp_approx(ra), rcp_approx(rb)), far_m, far_b), ra, rb);
-            a = fabsf(ua) <= kTanhNear ? a : ra;
-            b = fabsf(ub) <= kTanhNear ? b : rb;
+            a = kCap == 2 && fabsf(ua) <= kTanhNear ? a : ra;
+            b = kCap == 2 && fabsf(ub) <= kTanhNear ? b : rb;
         }
         a = 2 * k < lim ? ex2_approx(a) : 0.0f;
         b = 2 * k + 1 < lim ? ex2_approx(b) : 0.0f;
@@ -290,7 +294,7 @@ __device__ __forceinline__ void store32(uint16_t *to, const uint32_t *w) {
     }
 }
 
-template <bool kCap>
+template <int kCap>      // 0: no cap, 1: a small one, 2: any
 __global__ void __launch_bounds__(kThreads, 1)
     prompt_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                   const __grid_constant__ CUtensorMap tmV, const PromptParams p) {
@@ -648,10 +652,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int lim = seen - b * kBlk;      // columns of the block that the row sees
                 // 32 columns at a time: mostly all rows of the warp see them
                 const int least = edge ? __reduce_min_sync(0xffffffffu, lim) : kBlk;
-                uint32_t X[kCap ? 1 : 4][32];
+                uint32_t X[kCap == 2 ? 1 : 4][32];
                 float bm = kNegInf;
                 uint32_t near = 0;
-                if constexpr (kCap) {
+                if constexpr (kCap == 2) {
                     // scores are loaded again where they are needed: the code of 32 columns fits the
                     // instruction caches, that of 128 does not
 #pragma unroll 1
@@ -679,6 +683,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             if (least < 32 * (i + 1) && (i < 2 || !half_block)) mx[i] = mask_scores(X[i], lim - 32 * i);
                     }
                     bm = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c;
+                    if constexpr (kCap == 1) bm = capped(bm, p.cap_out);
                 }
                 const bool rises = real && bm > __fadd_rn(m, kLazyTau);      // a row that is none may hold anything
                 if (__any_sync(0xffffffffu, rises)) {
@@ -706,13 +711,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                     __syncwarp();
                     if (lane == 0) mbar_arrive(p_full + 2 * t + half);
                 };
-                if constexpr (kCap) {
+                if constexpr (kCap == 2) {
 #pragma unroll 1
                     for (int i = 0; i < (half_block ? 2 : 4); ++i) {
                         uint32_t W[16];
                         VCA_TMEM_LD32(tS + 32 * i, X[0]);
                         tmem_ld_wait();
-                        capped_probabilities(X[0], c, p.cap_out, bias, (near >> i) & 1u, least < 32 * (i + 1) ? lim - 32 * i : 32, l2, W);
+                        capped_probabilities<2>(X[0], c, p.cap_out, bias, (near >> i) & 1u, least < 32 * (i + 1) ? lim - 32 * i : 32, l2, W);
                         VCA_TMEM_ST16(tS + 16 * i, W);      // over scores already read
                         tmem_st_wait();
                         if (i & 1) hand_over(i >> 1);
@@ -725,7 +730,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                             for (int i = 2 * half; i < 2 * half + 2; ++i) {
                                 uint32_t W[16];
-                                probabilities(X[i], c, bias, l2, W);
+                                if constexpr (kCap == 1)
+                                    capped_probabilities<1>(X[i], c, p.cap_out, bias, false, least < 32 * (i + 1) ? lim - 32 * i : 32, l2, W);
+                                else
+                                    probabilities(X[i], c, bias, l2, W);
                                 VCA_TMEM_ST16(tS + 16 * i, W);
                             }
                             tmem_st_wait();
@@ -905,7 +913,7 @@ cudaError_t launch_prompt_attention(const PromptArgs &a, cudaStream_t st) {
     p.lse = a.lse;
     p.dev_status = a.dev_status;
     p.limit_ns = a.wait_limit_ns;
-    const auto kernel = a.softcap > 0.0f ? prompt_kernel<true> : prompt_kernel<false>;
+    const auto kernel = a.softcap == 0.0f ? prompt_kernel<0> : a.softcap <= kSmallCap ? prompt_kernel<1> : prompt_kernel<2>;
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
     if (e != cudaSuccess) return e;
     const int64_t tiles = a.T / (2 * p.tokens) + (a.B <= kSortable && a.T < a.B ? a.T : a.B);
