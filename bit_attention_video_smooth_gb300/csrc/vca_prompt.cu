@@ -294,10 +294,16 @@ __device__ __forceinline__ void store32(uint16_t *to, const uint32_t *w) {
     }
 }
 
-template <int kCap>      // 0: no cap, 1: a small one, 2: any
+// kCap: 0 no cap, 1 a small one, 2 any.  kShort: the MMA issuer's code once for both
+// tiles, not twice.  It has to fit the instruction caches beside the softmax's, and a miss
+// leaves the tensor core idle; in long loops the addresses that are known then count more.
+// 32 prompts of 1,000 tokens, 40 heads over 8: 315 us once, 325 twice; one of 32,768: 6,644 and 6,328.
+constexpr int kShortTokens = 1024;      // of a prompt on average
+template <int kCap, bool kShort>
 __global__ void __launch_bounds__(kThreads, 1)
     prompt_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                   const __grid_constant__ CUtensorMap tmV, const PromptParams p) {
+    constexpr int kCopies = kShort ? 1 : kTiles;
     extern __shared__ unsigned char smem_raw[];
     unsigned char *smem = smem_raw + (0u - smem_u32(smem_raw)) % 1024u;
     uint64_t *full = reinterpret_cast<uint64_t *>(smem + kOffBar), *empty = full + kStages, *raw = empty + kStages;
@@ -443,10 +449,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             int i0 = 0;                         // the ring's copies before this work's
             uint32_t blocks[kTiles] = {0, 0};   // of each tile so far
             uint32_t had[kTiles] = {0, 0};      // works that had the tile, the current one not among them
+            auto of = [](const auto (&x)[kTiles], int t) { return t ? x[1] : x[0]; };
             // a work's first QK, of tile t; its first block is in the ring's copy `at`
             auto begin = [&](int t, int seen, int at) {
                 if (seen == 0) return true;
-                if (!wait(full + at % kStages, (at / kStages) & 1) || !wait(q_full + t, had[t] & 1)) return false;
+                if (!wait(full + at % kStages, (at / kStages) & 1) || !wait(q_full + t, of(had, t) & 1)) return false;
                 qk(t, at % kStages, seen <= 64);
                 if (seen <= kBlk) commit(q_free + t);
                 return true;
@@ -454,11 +461,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             bool ok = next_work(0, w);
             int seen[kTiles] = {0, 0};
             if (ok) {
-#pragma unroll
-                for (int t = 0; t < kTiles; ++t) {
-                    seen[t] = seen_by(p, w, t);
-                    ok = ok && begin(t, seen[t], 0);
-                }
+                seen[0] = seen_by(p, w, 0);
+                seen[1] = seen_by(p, w, 1);
+#pragma unroll 1
+                for (int t = 0; t < kTiles; ++t) ok = ok && begin(t, of(seen, t), 0);
                 commit(empty);
             }
             for (int k = 0; ok; ++k) {
@@ -474,10 +480,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                 bool there = landed(0);
                 // A block of tile t: its PV and, unless it is the work's last block, the next QK.
                 auto block = [&](int t, int j, bool last) {
-                    const int left = seen[t] - j * kBlk;      // keys of this block and behind
+                    const int left = of(seen, t) - j * kBlk;      // keys of this block and behind
                     if (left <= 0) return true;
                     const int iv = i0 + 2 * j + 1, ik = iv + 1, sv = iv % kStages, sk = ik % kStages;
-                    const int turn = static_cast<int>(blocks[t]++) & 1;
+                    const int turn = static_cast<int>(of(blocks, t)) & 1;
+                    blocks[0] += t == 0;
+                    blocks[1] += t == 1;
                     uint64_t *halves = p_full + 2 * t;
                     const bool first = mbar_test_wait(halves, turn), second = mbar_test_wait(halves + 1, turn);
                     if (!__all_sync(0xffffffffu, there)) {
@@ -486,7 +494,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         there = true;
                     }
                     // O's first product waits until the epilogue before has read it
-                    if (j == 0 && had[t] > 0 && !wait(o_free + t, (had[t] - 1) & 1)) return false;
+                    if (j == 0 && of(had, t) > 0 && !wait(o_free + t, (of(had, t) - 1) & 1)) return false;
                     if (!__all_sync(0xffffffffu, first) && !wait(halves, turn)) return false;
                     tc_fence_after();
                     pv(t, sv, 0, j == 0);
@@ -506,28 +514,24 @@ __global__ void __launch_bounds__(kThreads, 1)
                     return true;
                 };
                 for (int j = 0; ok && j + 1 < nbs; ++j) {
-                    ok = block(0, j, false) && block(1, j, false);
+#pragma unroll kCopies
+                    for (int t = 0; t < kTiles; ++t) ok = ok && block(t, j, false);
                     if (ok) commit(empty + (i0 + 2 * j + 2) % kStages);
                 }
                 // the last one, after which each tile goes on to its next work's first scores
                 Work next;
                 const bool more = ok && next_work(k + 1, next);
-                int sees[kTiles] = {0, 0};
-                bool early = false;
-#pragma unroll
+                const int sees[kTiles] = {more ? seen_by(p, next, 0) : 0, more ? seen_by(p, next, 1) : 0};
+                int begun = 0;
+#pragma unroll kCopies
                 for (int t = 0; t < kTiles; ++t) {
-                    sees[t] = more ? seen_by(p, next, t) : 0;
                     ok = ok && block(t, nbs - 1, true);
-                    had[t] += seen[t] > 0;
-                    if (t == 0) {
-                        // not where tile 1's block would wait for what this needs
-                        early = __all_sync(0xffffffffu, mbar_test_wait(q_full, had[0] & 1) &
-                                                            mbar_test_wait(full + i1 % kStages, (i1 / kStages) & 1));
-                        if (early) ok = ok && begin(0, sees[0], i1);
-                    } else {
-                        if (!early) ok = ok && begin(0, sees[0], i1);
-                        ok = ok && begin(1, sees[1], i1);
-                    }
+                    had[0] += t == 0;
+                    had[1] += t == 1 && seen[1] > 0;
+                    // tile 0 not where tile 1's block would wait for what this needs
+                    const bool now = t == 1 || __all_sync(0xffffffffu, mbar_test_wait(q_full, had[0] & 1) &
+                                                                           mbar_test_wait(full + i1 % kStages, (i1 / kStages) & 1));
+                    for (; now && begun <= t; ++begun) ok = ok && begin(begun, of(sees, begun), i1);
                 }
                 if (!ok) break;
                 work_done(k);
@@ -913,7 +917,10 @@ cudaError_t launch_prompt_attention(const PromptArgs &a, cudaStream_t st) {
     p.lse = a.lse;
     p.dev_status = a.dev_status;
     p.limit_ns = a.wait_limit_ns;
-    const auto kernel = a.softcap == 0.0f ? prompt_kernel<0> : a.softcap <= kSmallCap ? prompt_kernel<1> : prompt_kernel<2>;
+    const bool few = a.T <= static_cast<int64_t>(kShortTokens) * a.B;
+    const auto kernel = a.softcap == 0.0f        ? (few ? prompt_kernel<0, true> : prompt_kernel<0, false>)
+                        : a.softcap <= kSmallCap ? (few ? prompt_kernel<1, true> : prompt_kernel<1, false>)
+                                                 : (few ? prompt_kernel<2, true> : prompt_kernel<2, false>);
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
     if (e != cudaSuccess) return e;
     const int64_t tiles = a.T / (2 * p.tokens) + (a.B <= kSortable && a.T < a.B ? a.T : a.B);

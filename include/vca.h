@@ -435,7 +435,7 @@ int vca_cache_fresh(const int32_t *table, const int32_t *len, int pages, int B, 
  * and where H > 1 that between heads not below (0: all heads are one); below 2^39.
  * B*H <= 65,535, T*Hq <= 2^31 - 1.
  * The products of bf16 values are exact, sums and statistics fp32; the
- * probabilities enter the second product as bf16 (2^-9 relative).  A NaN or an infinity
+ * probabilities enter the second product as bf16 (2^-8 relative).  A NaN or an infinity
  * among the values of a sequence may reach every row of that sequence, one in a
  * key or query only the rows that see it.  Equal calls give equal bits.  No workspace.
  */
