@@ -356,7 +356,8 @@ __global__ void __launch_bounds__(kThreads, 1) plan_kernel(const PlanParams p) {
 template <bool kFresh, int kCluster, int kThreads>
 cudaError_t launch(const PlanParams &p, size_t smem, cudaStream_t st) {
     const auto kernel = plan_kernel<kFresh, kCluster, kThreads>;
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    // the most that any call needs: another thread's call may be between this and the launch
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
     if (e != cudaSuccess) return e;
     cudaLaunchAttribute at;
     at.id = cudaLaunchAttributeClusterDimension;

@@ -430,10 +430,10 @@ int vca_cache_fresh(const int32_t *table, const int32_t *len, int pages, int B, 
  *   O_i = (sum_j exp(s_ij) v_j + exp(prior_lse_i) prior_i) / exp(lse_i)
  * in fp32 with one rounding of O; where prior_lse is -inf, prior is not read.  O may be
  * prior, and lse prior_lse; other outputs must not overlap the inputs.
- * Scale, cap, start, rows behind start[B], strides, O, lse, T = 0 and dev_status as in
- * vca_cache_attention.  Where T > 1 the distance between tokens of K and V is above 0,
- * and where H > 1 that between heads not below (0: all heads are one); below 2^39.
- * B*H <= 65,535, T*Hq <= 2^31 - 1.
+ * Scale, cap, start, rows behind start[B], O, lse, T = 0 and dev_status as in
+ * vca_cache_attention.  Distances are multiples of 8 elements, above 0 and below 2^39,
+ * between tokens where T > 1 and between heads where there are several; 0 between
+ * the heads of K or V makes all of them one.  B*H <= 65,535, T*Hq <= 2^31 - 1.
  * The products of bf16 values are exact, sums and statistics fp32; the
  * probabilities enter the second product as bf16 (2^-8 relative).  A NaN or an infinity
  * among the values of a sequence may reach every row of that sequence, one in a
