@@ -1,26 +1,46 @@
 // vca_prompt.cu -- attention of packed prompts over their own keys and values
 // (bf16), bound by the tensor cores: 4 d flops for every visible pair.
 //
-// One CTA takes 256 query rows of a (sequence, KV head), two tiles of 128: rows
-// i G + g, so that the G query heads that share the KV head share its keys and
-// values, which pass through shared memory once for both tiles.  Per block of 128
+// One CTA an SM takes works in turn: 256 query rows of a (sequence, KV head), two tiles
+// of 128: G query heads of whole tokens, so that heads that share a KV head share its
+// keys and values, which pass through shared memory once for both tiles.  Per block of 128
 // keys and tile: S = Q K^T (smem x smem -> TMEM), the softmax takes S to P in its
-// place (bf16, the values' type, as the MMA wants it: 2^-9 relative a
-// probability, while the row sums take the unrounded ones in fp32), O += P V (TMEM x
-// smem).  While one tile's softmax runs the tensor core works for the other.
+// place (bf16, the values' type, as the MMA wants it: 2^-8 relative a probability,
+// while the row sums take the unrounded ones in fp32), O += P V (TMEM x smem).  While
+// one tile's softmax runs the tensor core works for the other.  TMEM: S0, S1, O0, O1, all of it.
 // Warps:
-//   0      TMA producer: K and V blocks alternate in a ring of five
-//   1      MMA issuer: PV of a block and QK of the next, tile by tile.  MMAs of one
-//          thread and shape run in order, so QK may write the scores over the
-//          probabilities that the PV before it reads.  The whole warp waits and one
+//   0      TMA producer: K and V blocks alternate in a ring of four
+//   1      MMA issuer: PV of a block and QK of the next, tile by tile.  One CTA's MMAs
+//          run in the order of their issue, so QK may write the scores over the
+//          probabilities that the PV before it reads (110,000 launches of random shapes, three
+//          of each, gave equal bits).  The whole warp waits and one
 //          thread of it, elected, issues: then the operands are in uniform registers,
-//          and an MMA takes 10 to 20 cycles to issue (46 from a branch on the lane)
+//          and an MMA takes 10 to 20 cycles to issue (46 from a branch on the lane,
+//          which the softmax's warps beside it make 95: 1,389 TFLOP/s against 1,605)
 //   2      zeroes the rows of V behind the sequence's last token (they are another
 //          sequence's, and may hold NaN) and only then reports that block as full
-//   4-11   softmax, four warps a tile, a thread a row.  The reference maximum moves
-//          only when a block's exceeds it by 8 (log2 units); O is rescaled in TMEM
-//          then: S(j) full means that PV(j - 1) is done too
+//   3      finds the CTA's works and loads their queries
+//   4-11   softmax, four warps a tile, a thread a row.  P goes over in halves of 64 keys.
+//          The reference maximum moves only when a block's exceeds it by 8 (log2
+//          units); O is rescaled in TMEM then: S(j) full means that PV(j - 1) is done too
+//   12-15  epilogue: O / sum, joined with what came before, while the tiles go on to
+//          their next work
 // Every wait is bounded, as in vca_attention.cu.
+//
+// What bounds it.  A block of both tiles is 2,048 cycles of the tensor core; it takes
+// 2,670, since a tile's chain (scores -> softmax 1,150 -> PV -> QK) is longer than the other
+// tile's 1,024 cycles of MMAs.  One prompt of 32,768 tokens, causal, 40 heads over 8: 6.33
+// ms, 1,737 TFLOP/s, 0.92 of cuBLAS's burst rate; 17,664 tokens both ways, 8 heads:
+// 770 us, 1,660 TFLOP/s (552 works on 152 SMs).  Short prompts are bound by what a
+// work costs beside its blocks, about 6,000 cycles: 32 of up to 1,000 tokens, 40 heads
+// over 8, 149 us, 860 TFLOP/s.  The code's size counts: all roles share the instruction
+// caches, and a loop that no longer fits costs 5 to 15 %.
+// Measured and not kept: an issuer for each tile (both tiles' MMAs then mix and their
+// softmaxes fall together: 8.7 ms), a ring of three (7.2) or of five, which
+// leaves no room for the statistics (6.24 against 6.39 at the time), O read into registers
+// at once before its stores (162 us for the 32 prompts against 155 at the time), the
+// queries prefetched into L2 (no change), a CTA for each work (886 us for 32 prompts of
+// 1,000 tokens, 315 now).
 #include "vca_attention_common.cuh"
 #include "vca_cache.cuh"
 
