@@ -580,38 +580,44 @@ def cache_evict(cache: Cache, weight, dst_table, budget: int, recent: int, kept:
 # ---------------------------------------------------------------------------
 # The cache's pages, and prompts on their way into it (include/vca.h)
 # ---------------------------------------------------------------------------
-def _ints_call(where, cache: Cache, ints):
-    """Checks that every tensor (name, tensor or None, shape) of a planning call is int32, contiguous, of its shape and on
-    one CUDA device, which is returned."""
+def _refuse_ints(where, cache: Cache, ints):
+    """Names the first tensor (name, tensor or None, shape) of a planning call that is not int32, contiguous, of its shape
+    and on the table's CUDA device."""
     if cache.table.dim() != 2 or cache.k8.dim() != 4 or max(cache.k8.shape[0], *cache.table.shape) > _MOST:
         raise ValueError(f"{where}: k8 must be [pages, H, 128, 128] and table [B, cols]")
-    dev = cache.table.get_device()
-    ok = dev >= 0
-    for _, t, shape in ints:
-        ok = ok and (t is None or (t.dtype is torch.int32 and t.shape == shape and t.get_device() == dev and t.is_contiguous()))
-    if not ok:
-        given = [x for x in ints if x[1] is not None]
-        for name, t, shape in given:
-            _typed(where, name, t, torch.int32, shape)
-        for name, t, _ in given:
-            if not t.is_cuda:
-                raise ValueError(f"{where}: {name} is not a CUDA tensor")
-            if t.device != cache.table.device:
-                raise ValueError(f"{where}: tensors on several devices: {name} on {t.device}, table on {cache.table.device}")
-        raise ValueError(f"{where}: tensors that do not fit together")
-    return dev
+    given = [x for x in ints if x[1] is not None]
+    for name, t, shape in given:
+        _typed(where, name, t, torch.int32, shape)
+    for name, t, _ in given:
+        if not t.is_cuda:
+            raise ValueError(f"{where}: {name} is not a CUDA tensor")
+        if t.device != cache.table.device:
+            raise ValueError(f"{where}: tensors on several devices: {name} on {t.device}, table on {cache.table.device}")
+    raise ValueError(f"{where}: tensors that do not fit together")
+
+
+def _is_ints(t, n, dev):
+    return t.dtype is torch.int32 and t.shape == n and t.get_device() == dev and t.is_contiguous()
 
 
 def vca_cache_plan(cache: Cache, held, news, T: int, start, slot, position, dev_status=None, stream=None) -> None:
     if not 0 <= T <= _MOST:
         raise ValueError(f"vca_cache_plan: T = {T} must be 0 .. {_MOST}")
-    B = cache.table.shape[0] if cache.table.dim() else 0
-    dev = _ints_call("vca_cache_plan", cache, (
-        ("table", cache.table, cache.table.shape), ("length", cache.length, (B,)), ("held", held, (B,)), ("news", news, (B,)),
-        ("start", start, (B + 1,)), ("slot", slot, (T,)), ("position", position, (T,)), ("dev_status", dev_status, (1,))))
-    _launch("vca_cache_plan", dev, _lib.vca_cache_plan, cache.table.data_ptr(), cache.length.data_ptr(), cache.k8.shape[0], B,
-            cache.table.shape[1], held.data_ptr(), news.data_ptr(), start.data_ptr(), _at(slot), _at(position), T,
-            _at(dev_status), stream=stream)
+    table, length = cache.table, cache.length
+    shape, pages, dev = table.shape, cache.k8.shape[0] if cache.k8.dim() == 4 else 0, table.get_device()
+    B = shape[0] if shape else 0
+    one, rows = (B,), (T,)
+    # all at once, and by name only where one fails, as in _cache_call
+    ok = (dev >= 0 and len(shape) == 2 and 0 < pages <= _MOST and max(shape) <= _MOST and _is_ints(table, shape, dev)
+          and _is_ints(length, one, dev) and (held is length or _is_ints(held, one, dev)) and _is_ints(news, one, dev)
+          and _is_ints(start, (B + 1,), dev) and (slot is None or _is_ints(slot, rows, dev))
+          and (position is None or _is_ints(position, rows, dev)) and (dev_status is None or _is_ints(dev_status, (1,), dev)))
+    if not ok:
+        _refuse_ints("vca_cache_plan", cache, (
+            ("table", table, shape), ("length", length, one), ("held", held, one), ("news", news, one), ("start", start, (B + 1,)),
+            ("slot", slot, rows), ("position", position, rows), ("dev_status", dev_status, (1,))))
+    _launch("vca_cache_plan", dev, _lib.vca_cache_plan, table.data_ptr(), length.data_ptr(), pages, B, shape[1], held.data_ptr(),
+            news.data_ptr(), start.data_ptr(), _at(slot), _at(position), T, _at(dev_status), stream=stream)
 
 
 def vca_cache_fresh(cache: Cache, budget: int, dst_table, dev_status=None, stream=None) -> None:
@@ -619,12 +625,17 @@ def vca_cache_fresh(cache: Cache, budget: int, dst_table, dev_status=None, strea
         raise ValueError("vca_cache_fresh: dst_table must be [B, dst_cols]")
     if not (-_MOST <= budget <= _MOST and dst_table.shape[1] <= _MOST):
         raise ValueError(f"vca_cache_fresh: budget {budget} and dst_cols {dst_table.shape[1]} must fit 32 bits")
-    B = cache.table.shape[0] if cache.table.dim() else 0
-    dev = _ints_call("vca_cache_fresh", cache, (
-        ("table", cache.table, cache.table.shape), ("length", cache.length, (B,)),
-        ("dst_table", dst_table, (B, dst_table.shape[1])), ("dev_status", dev_status, (1,))))
-    _launch("vca_cache_fresh", dev, _lib.vca_cache_fresh, cache.table.data_ptr(), cache.length.data_ptr(), cache.k8.shape[0], B,
-            cache.table.shape[1], budget, dst_table.data_ptr(), dst_table.shape[1], _at(dev_status), stream=stream)
+    table, length = cache.table, cache.length
+    shape, pages, dev = table.shape, cache.k8.shape[0] if cache.k8.dim() == 4 else 0, table.get_device()
+    B = shape[0] if shape else 0
+    dst = (B, dst_table.shape[1])
+    ok = (dev >= 0 and len(shape) == 2 and 0 < pages <= _MOST and max(shape) <= _MOST and _is_ints(table, shape, dev)
+          and _is_ints(length, (B,), dev) and _is_ints(dst_table, dst, dev) and (dev_status is None or _is_ints(dev_status, (1,), dev)))
+    if not ok:
+        _refuse_ints("vca_cache_fresh", cache, (("table", table, shape), ("length", length, (B,)), ("dst_table", dst_table, dst),
+                                                ("dev_status", dev_status, (1,))))
+    _launch("vca_cache_fresh", dev, _lib.vca_cache_fresh, table.data_ptr(), length.data_ptr(), pages, B, shape[1], budget,
+            dst_table.data_ptr(), dst_table.shape[1], _at(dev_status), stream=stream)
 
 
 def cache_plan(cache: Cache, news, T: int, held: Optional[torch.Tensor] = None, start: Optional[torch.Tensor] = None,
@@ -635,12 +646,15 @@ def cache_plan(cache: Cache, news, T: int, held: Optional[torch.Tensor] = None, 
     call will have room for.  Returns (start [B + 1], slot [T], position [T]); slot
     and position are -1 behind the last row where they are made here.  With too few
     free pages (dev_status: VCA_ERR_FULL) start is 0 throughout and nothing changes."""
-    new = lambda n, fill: torch.full((n,), fill, dtype=torch.int32, device=cache.table.device)
-    if T < 0 or T > _MOST or cache.table.dim() != 2:
+    table = cache.table
+    if T < 0 or T > _MOST or table.dim() != 2:
         raise ValueError(f"vca_cache_plan: T = {T} must be 0 .. {_MOST} and table [B, cols]")
-    start = torch.empty((cache.table.shape[0] + 1,), dtype=torch.int32, device=cache.table.device) if start is None else start
-    slot = new(T, -1) if slot is None else slot
-    position = new(T, -1) if position is None else position
+    if start is None:
+        start = torch.empty((table.shape[0] + 1,), dtype=torch.int32, device=table.device)
+    if slot is None:
+        slot = torch.full((T,), -1, dtype=torch.int32, device=table.device)
+    if position is None:
+        position = torch.full((T,), -1, dtype=torch.int32, device=table.device)
     vca_cache_plan(cache, cache.length if held is None else held, news, T, start, slot, position, dev_status)
     return start, slot, position
 
@@ -662,28 +676,27 @@ def vca_prompt_attention(Q, K, V, start, causal: int, softmax_scale: float, soft
         raise ValueError(f"vca_prompt_attention: Q must be bfloat16 [T, Hq, 128], K and V [T, H, 128] and start int32 [B + 1], "
                          f"got {tuple(Q.shape)}, {tuple(K.shape)} and {tuple(start.shape)}")
     (T, Hq, _), H, B = Q.shape, K.shape[1], start.shape[0] - 1
-    dev = Q.get_device()
-    rows = (("Q", Q, Hq), ("K", K, H), ("V", V, H))
-    seen = [("start", start, torch.int32, (B + 1,)), ("O", O, torch.bfloat16, (T, Hq, 128))]
-    if lse is not None:
-        seen.append(("lse", lse, torch.float32, (T, Hq)))
-    if prior is not None or prior_lse is not None:
-        if prior is None or prior_lse is None:
-            raise ValueError("vca_prompt_attention: prior and prior_lse are given together")
-        seen += [("prior", prior, torch.bfloat16, (T, Hq, 128)), ("prior_lse", prior_lse, torch.float32, (T, Hq))]
-    if dev_status is not None:
-        seen.append(("dev_status", dev_status, torch.int32, (1,)))
-    ok = dev >= 0 and max(T, Hq, H, B) <= _MOST
-    for _, t, dtype, shape in seen:
-        ok = ok and t.dtype is dtype and t.shape == shape and t.get_device() == dev and t.is_contiguous()
-    for _, t, heads in rows:
-        ok = ok and t.dtype is torch.bfloat16 and t.shape == (T, heads, 128) and t.stride(2) == 1 and t.get_device() == dev
+    dev, kv, wide, per_row, bf16, f32 = Q.get_device(), (T, H, 128), (T, Hq, 128), (T, Hq), torch.bfloat16, torch.float32
+    sq, sk, sv = Q.stride(), K.stride(), V.stride()
+    # a launch of a few microseconds waits for these checks: all at once, and by name only where one fails
+    ok = (dev >= 0 and Q.dtype is bf16 and Q.shape == wide and sq[2] == 1 and K.dtype is bf16 and K.shape == kv and sk[2] == 1
+          and V.dtype is bf16 and V.shape == kv and sv[2] == 1 and start.dtype is torch.int32 and start.is_contiguous()
+          and O.dtype is bf16 and O.shape == wide and O.is_contiguous() and (prior is None) == (prior_lse is None)
+          and K.get_device() == dev and V.get_device() == dev and start.get_device() == dev and O.get_device() == dev
+          and max(T, Hq, H, B) <= _MOST)
+    for t, dtype, shape in ((lse, f32, per_row), (prior, bf16, wide), (prior_lse, f32, per_row), (dev_status, torch.int32, (1,))):
+        if t is not None:
+            ok = ok and t.dtype is dtype and t.shape == shape and t.get_device() == dev and t.is_contiguous()
     if not ok:
+        if (prior is None) != (prior_lse is None):
+            raise ValueError("vca_prompt_attention: prior and prior_lse are given together")
         _few_enough("vca_prompt_attention", "start", start)
-        _refuse("vca_prompt_attention", Q, seen, rows, None, "Q")
-    _launch("vca_prompt_attention", dev, _lib.vca_prompt_attention, Q.data_ptr(), Q.stride(0), Q.stride(1), K.data_ptr(),
-            K.stride(0), K.stride(1), V.data_ptr(), V.stride(0), V.stride(1), start.data_ptr(), B, T, Hq, H, 128, int(causal),
-            softmax_scale, softcap, _at(prior), _at(prior_lse), O.data_ptr(), _at(lse), _at(dev_status), stream=stream)
+        seen = (("start", start, torch.int32, (B + 1,)), ("O", O, bf16, wide), ("lse", lse, f32, per_row), ("prior", prior, bf16, wide),
+                ("prior_lse", prior_lse, f32, per_row), ("dev_status", dev_status, torch.int32, (1,)))
+        _refuse("vca_prompt_attention", Q, [x for x in seen if x[1] is not None], (("Q", Q, Hq), ("K", K, H), ("V", V, H)), None, "Q")
+    _launch("vca_prompt_attention", dev, _lib.vca_prompt_attention, Q.data_ptr(), sq[0], sq[1], K.data_ptr(), sk[0], sk[1],
+            V.data_ptr(), sv[0], sv[1], start.data_ptr(), B, T, Hq, H, 128, int(causal), softmax_scale, softcap, _at(prior),
+            _at(prior_lse), O.data_ptr(), _at(lse), _at(dev_status), stream=stream)
 
 
 def prompt_attention(Q, K, V, start, causal: bool = True, softmax_scale: float = 0.0, softcap: float = 0.0, prior=None,
