@@ -17,9 +17,9 @@
 //          thread of it, elected, issues: then the operands are in uniform registers,
 //          and an MMA takes 10 to 20 cycles to issue (46 from a branch on the lane,
 //          which the softmax's warps beside it make 95: 1,389 TFLOP/s against 1,605)
-//   2      zeroes the rows of V behind the sequence's last token (they are another
-//          sequence's, and may hold NaN) and only then reports that block as full
-//   3      finds the CTA's works and loads their queries
+//   2      loads the queries; zeroes the rows of V behind the sequence's last token (they
+//          are another sequence's, and may hold NaN) and only then reports that block as full
+//   3      finds the CTA's works, some ahead of the others
 //   4-11   softmax, four warps a tile, a thread a row.  P goes over in halves of 64 keys.
 //          The reference maximum moves only when a block's exceeds it by 8 (log2
 //          units); O is rescaled in TMEM then: S(j) full means that PV(j - 1) is done too
@@ -566,14 +566,33 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (one) drain_wait(drain, 0, p.limit_ns);
             __syncwarp();
         } else if (warp == 2) {
-            // -------------------------------------------------------- rows of V behind a sequence
+            // -------------------------------------------------------- queries, and rows of V behind a sequence
             Work w;
             int i0 = 0;
-            uint32_t turns = 0;         // the phase of each stage's `raw`
+            uint32_t turns = 0;                  // the phase of each stage's `raw`
+            uint32_t had1 = 0;                   // works that had a second tile
+            int queries0 = -1, queries1 = -1;    // the last copy of each tile's
             bool ok = true;
             for (int k = 0; ok && next_work(k, w); ++k) {
+#pragma unroll 1
+                for (int t = 0; ok && t < kTiles; ++t) {
+                    const int token = (2 * w.tile + t) * p.tokens, earlier = t ? static_cast<int>(had1) : k;
+                    if (token >= w.n) break;
+                    if (earlier > 0) ok = __all_sync(0xffffffffu, wait_phase(q_free + t, (earlier - 1) & 1, abort_flag, p.limit_ns));
+                    if (!ok) break;
+                    if (lane == 0) {
+                        unsigned char *sQ = smem + kOffQ + t * kBlock;
+                        mbar_expect_tx(q_full + t, 2 * 128 * p.G * p.tokens);
+                        for (int c = 0; c < 2; ++c) tma_load_3d(sQ + c * kPanel, &tmQ, q_full + t, 64 * c, w.group * p.G, w.row0 + token);
+                    }
+                    had1 += t;
+                    if (t == 0)
+                        queries0 = earlier;
+                    else
+                        queries1 = earlier;
+                }
                 const int nbs = max(blocks_of(p, w, 0), blocks_of(p, w, 1)), tail = tail_of(w, nbs);
-                if (tail >= 0) {
+                if (ok && tail >= 0) {
                     const int st = (i0 + 2 * tail + 1) % kStages, live = w.n - tail * kBlk;
                     ok = __all_sync(0xffffffffu, wait_phase(raw + st, (turns >> st) & 1, abort_flag, p.limit_ns));
                     if (!ok) break;
@@ -587,8 +606,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                 i0 += 2 * nbs;
                 work_done(k);
             }
+            // the last queries have landed before the CTA can exit
+            if (lane == 0) {
+                if (queries0 >= 0) drain_wait(q_full, queries0 & 1, p.limit_ns);
+                if (queries1 >= 0) drain_wait(q_full + 1, queries1 & 1, p.limit_ns);
+            }
         } else {
-            // -------------------------------------------------------- the CTA's work, and its queries
+            // -------------------------------------------------------- the CTA's works, ahead of all others
             Sorted &s = *reinterpret_cast<Sorted *>(smem + kOffSort);
             const int rise = *first_fall;
             int most = 0;
@@ -598,8 +622,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                 report(p.dev_status, kErrInvalid);
             const int ctas = static_cast<int>(gridDim.x), me = static_cast<int>(blockIdx.x);
             int k = 0;
-            uint32_t had1 = 0;
-            int queries[kTiles] = {-1, -1};      // the last copy of each tile's
             bool ok = true;
             for (int64_t turn = 0; ok; ++turn) {
                 const int64_t index = turn * ctas + (turn & 1 ? ctas - 1 - me : me);
@@ -619,30 +641,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     mbar_arrive(w_full + k % kWorks);
                 }
                 if (end) break;
-#pragma unroll 1
-                for (int t = 0; ok && t < kTiles; ++t) {
-                    const int token = (2 * w.tile + t) * p.tokens, earlier = t ? static_cast<int>(had1) : k;
-                    if (token >= w.n) break;
-                    if (earlier > 0) ok = __all_sync(0xffffffffu, wait_phase(q_free + t, (earlier - 1) & 1, abort_flag, p.limit_ns));
-                    if (!ok) break;
-                    if (lane == 0) {
-                        unsigned char *sQ = smem + kOffQ + t * kBlock;
-                        mbar_expect_tx(q_full + t, 2 * 128 * p.G * p.tokens);
-                        for (int c = 0; c < 2; ++c) tma_load_3d(sQ + c * kPanel, &tmQ, q_full + t, 64 * c, w.group * p.G, w.row0 + token);
-                    }
-                    had1 += t;
-                    if (t == 0)
-                        queries[0] = earlier;
-                    else
-                        queries[1] = earlier;
-                }
                 ++k;
-            }
-            // the last queries have landed before the CTA can exit
-            if (lane == 0) {
-#pragma unroll
-                for (int t = 0; t < kTiles; ++t)
-                    if (queries[t] >= 0) drain_wait(q_full + t, queries[t] & 1, p.limit_ns);
             }
         }
     } else if (warp < kOutWarp0) {
