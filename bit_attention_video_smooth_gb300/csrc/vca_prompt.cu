@@ -52,7 +52,8 @@ using namespace attn;
 using namespace cache;
 
 constexpr int kTiles = 2;
-constexpr int kStages = 4, kSoftWarp0 = 4, kOutWarp0 = kSoftWarp0 + 4 * kTiles, kThreads = 32 * (kOutWarp0 + 4);
+constexpr int kStages = 4;      // a power of two: copies are counted modulo 2^32
+constexpr int kSoftWarp0 = 4, kOutWarp0 = kSoftWarp0 + 4 * kTiles, kThreads = 32 * (kOutWarp0 + 4);
 constexpr uint32_t kPanel = kBlk * 128;              // 128 rows of 64 bf16 channels
 constexpr uint32_t kBlock = 2 * kPanel;              // Q, K or V: two panels
 constexpr uint32_t kTmemS = 0, kTmemO = 256, kTmemCols = 512;
@@ -160,6 +161,7 @@ __device__ __forceinline__ int load_sorted(const PromptParams &p, Sorted &s) {
         most = max(most, s.q[b]);
     }
     if (blockIdx.x == 0 && lane == 0 && fell) report(p.dev_status, kErrInvalid);
+    __syncwarp();
     return __reduce_max_sync(0xffffffffu, most);
 }
 __device__ __forceinline__ bool find_sorted(const PromptParams &p, const Sorted &s, int most, int rank, Work &w) {
@@ -395,22 +397,24 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (warp == 0) {
             // -------------------------------------------------------- producer of K and V
             Work w;
-            int i = 0;                  // copies issued: K(0), V(0), K(1), V(1), ... of one work after the other
+            uint32_t i = 0;             // the next copy: K(0), V(0), K(1), V(1), ... of one work after the other, modulo 2^32
+            int issued = 0;             // copies, kStages at most
             uint32_t tails = 0;         // stages whose last copy `raw` counts,
             uint32_t turns = 0;         // and the next phase of each stage's
             bool ok = true;
             for (int k = 0; ok && next_work(k, w); ++k) {
-                const int nbs = max(blocks_of(p, w, 0), blocks_of(p, w, 1)), tail = tail_of(w, nbs);
+                const int nbs = max(blocks_of(p, w, 0), blocks_of(p, w, 1)), tail = tail_of(w, nbs), kv_head = w.group / p.per_head;
                 for (int j = 0; ok && j < 2 * nbs; ++j, ++i) {
-                    const int st = i % kStages;
-                    if (i >= kStages) ok = wait_phase(empty + st, (i / kStages - 1) & 1, abort_flag, p.limit_ns);
-                    ok = __all_sync(0xffffffffu, ok);
+                    const uint32_t st = i % kStages;
+                    // of a new barrier the phase before the first counts as complete
+                    ok = __all_sync(0xffffffffu, wait_phase(empty + st, (i / kStages - 1) & 1, abort_flag, p.limit_ns));
                     if (!ok) break;
+                    issued = min(issued + 1, kStages);
                     const bool is_v = j & 1, is_tail = j == 2 * tail + 1;
                     tails = is_tail ? tails | (1u << st) : tails & ~(1u << st);
                     turns ^= is_tail ? 1u << st : 0u;
                     if (lane == 0) {
-                        const int token = w.row0 + (j >> 1) * kBlk, head = w.group / p.per_head * (is_v ? p.v_heads : p.k_heads);
+                        const int token = w.row0 + (j >> 1) * kBlk, head = kv_head * (is_v ? p.v_heads : p.k_heads);
                         const bool tokens = is_v ? p.v_tokens : p.k_tokens;
                         unsigned char *to = smem + kOffKV + st * kBlock;
                         uint64_t *landed = is_tail ? raw + st : full + st;
@@ -423,8 +427,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             // every copy issued has landed before the CTA can exit
             if (lane == 0) {
-                for (int j = max(0, i - kStages); j < i; ++j) {
-                    const int st = j % kStages;
+                for (uint32_t j = i - issued; j != i; ++j) {
+                    const uint32_t st = j % kStages;
                     if ((tails >> st) & 1u)
                         drain_wait(raw + st, ((turns >> st) & 1u) ^ 1u, p.limit_ns);
                     else
@@ -441,7 +445,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 return ok;
             };
             // a block of which the tile sees 64 keys or fewer is half a block
-            auto qk = [&](int t, int st, bool half) {
+            auto qk = [&](int t, uint32_t st, bool half) {
                 const uint64_t dq = sdesc_k_sw128(base + kOffQ + t * kBlock), dk = sdesc_k_sw128(base + kOffKV + st * kBlock);
                 const uint32_t idesc = half ? make_idesc(128, 64, 1, 1) : make_idesc(128, 128, 1, 1);
                 if (one) {
@@ -453,7 +457,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     tc_commit(s_full + t);
                 }
             };
-            auto pv = [&](int t, int st, int half, bool first) {      // of 64 keys
+            auto pv = [&](int t, uint32_t st, int half, bool first) {      // of 64 keys
                 const uint64_t dv = sdesc_mn_sw128(base + kOffKV + st * kBlock, kPanel);
                 if (one) {
 #pragma unroll
@@ -466,12 +470,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (one) tc_commit(bar);
             };
             Work w;
-            int i0 = 0;                         // the ring's copies before this work's
+            uint32_t i0 = 0;                    // the ring's copies before this work's, modulo 2^32
             uint32_t blocks[kTiles] = {0, 0};   // of each tile so far
             uint32_t had[kTiles] = {0, 0};      // works that had the tile, the current one not among them
             auto of = [](const auto (&x)[kTiles], int t) { return t ? x[1] : x[0]; };
             // a work's first QK, of tile t; its first block is in the ring's copy `at`
-            auto begin = [&](int t, int seen, int at) {
+            auto begin = [&](int t, int seen, uint32_t at) {
                 if (seen == 0) return true;
                 if (!wait(full + at % kStages, (at / kStages) & 1) || !wait(q_full + t, of(had, t) & 1)) return false;
                 qk(t, at % kStages, seen <= 64);
@@ -488,12 +492,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                 commit(empty);
             }
             for (int k = 0; ok; ++k) {
-                const int nbs = (max(seen[0], seen[1]) + kBlk - 1) / kBlk, i1 = i0 + 2 * nbs;
+                const int nbs = (max(seen[0], seen[1]) + kBlk - 1) / kBlk;
+                const uint32_t i1 = i0 + 2 * nbs;
                 // Barriers are tested before they are needed, several at once, and V's and K's of the
                 // next block while the tensor core has the second tile's scores to do: a test takes 100
                 // cycles, and one after the other left it idle
                 auto landed = [&](int j) {      // V of block j, and K of the next
-                    const int iv = i0 + 2 * j + 1, ik = iv + 1;
+                    const uint32_t iv = i0 + 2 * j + 1, ik = iv + 1;
                     return mbar_test_wait(full + iv % kStages, (iv / kStages) & 1) &
                            (j + 1 >= nbs || mbar_test_wait(full + ik % kStages, (ik / kStages) & 1));
                 };
@@ -502,7 +507,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 auto block = [&](int t, int j, bool last) {
                     const int left = of(seen, t) - j * kBlk;      // keys of this block and behind
                     if (left <= 0) return true;
-                    const int iv = i0 + 2 * j + 1, ik = iv + 1, sv = iv % kStages, sk = ik % kStages;
+                    const uint32_t iv = i0 + 2 * j + 1, ik = iv + 1, sv = iv % kStages, sk = ik % kStages;
                     const int turn = static_cast<int>(of(blocks, t)) & 1;
                     blocks[0] += t == 0;
                     blocks[1] += t == 1;
@@ -568,7 +573,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         } else if (warp == 2) {
             // -------------------------------------------------------- queries, and rows of V behind a sequence
             Work w;
-            int i0 = 0;
+            uint32_t i0 = 0;
             uint32_t turns = 0;                  // the phase of each stage's `raw`
             uint32_t had1 = 0;                   // works that had a second tile
             int queries0 = -1, queries1 = -1;    // the last copy of each tile's
@@ -593,7 +598,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 const int nbs = max(blocks_of(p, w, 0), blocks_of(p, w, 1)), tail = tail_of(w, nbs);
                 if (ok && tail >= 0) {
-                    const int st = (i0 + 2 * tail + 1) % kStages, live = w.n - tail * kBlk;
+                    const uint32_t st = (i0 + 2 * tail + 1) % kStages;
+                    const int live = w.n - tail * kBlk;
                     ok = __all_sync(0xffffffffu, wait_phase(raw + st, (turns >> st) & 1, abort_flag, p.limit_ns));
                     if (!ok) break;
                     turns ^= 1u << st;
