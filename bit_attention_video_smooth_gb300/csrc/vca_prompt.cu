@@ -25,7 +25,8 @@
 //          units); O is rescaled in TMEM then: S(j) full means that PV(j - 1) is done too
 //   12-15  epilogue: O / sum, joined with what came before, while the tiles go on to
 //          their next work
-// Every wait is bounded, as in vca_attention.cu.
+// Every wait is bounded, as in vca_attention.cu; those that last as long as a work by as
+// many times the limit as it can have blocks.  Where one gives up all others do.
 //
 // What bounds it.  A block of both tiles is 2,048 cycles of the tensor core; it takes
 // 2,670, since a tile's chain (scores -> softmax 1,150 -> PV -> QK) is longer than the other
@@ -84,7 +85,7 @@ struct PromptParams {
     bool wide;                              // O is 32-byte aligned
     float *lse;
     int32_t *dev_status;
-    uint64_t limit_ns;
+    uint64_t limit_ns, work_limit_ns;       // of a wait for a block, and of one for a whole work
 };
 
 __device__ __forceinline__ void tma_load_3d(void *smem_dst, const void *tmap, uint64_t *bar, int x, int y, int z) {
@@ -382,7 +383,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // The k-th work of this CTA, from its slot; false at the end, or where a wait gave up.
     auto next_work = [&](int k, Work &w) {
         const int i = k % kWorks;
-        if (!__all_sync(0xffffffffu, wait_phase(w_full + i, (k / kWorks) & 1, abort_flag, p.limit_ns))) return false;
+        if (!__all_sync(0xffffffffu, wait_phase(w_full + i, (k / kWorks) & 1, abort_flag, p.work_limit_ns))) return false;
         w = works[i];
         return w.n > 0;
     };
@@ -583,7 +584,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int t = 0; ok && t < kTiles; ++t) {
                     const int token = (2 * w.tile + t) * p.tokens, earlier = t ? static_cast<int>(had1) : k;
                     if (token >= w.n) break;
-                    if (earlier > 0) ok = __all_sync(0xffffffffu, wait_phase(q_free + t, (earlier - 1) & 1, abort_flag, p.limit_ns));
+                    if (earlier > 0) ok = __all_sync(0xffffffffu, wait_phase(q_free + t, (earlier - 1) & 1, abort_flag, p.work_limit_ns));
                     if (!ok) break;
                     if (lane == 0) {
                         unsigned char *sQ = smem + kOffQ + t * kBlock;
@@ -600,7 +601,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (ok && tail >= 0) {
                     const uint32_t st = (i0 + 2 * tail + 1) % kStages;
                     const int live = w.n - tail * kBlk;
-                    ok = __all_sync(0xffffffffu, wait_phase(raw + st, (turns >> st) & 1, abort_flag, p.limit_ns));
+                    ok = __all_sync(0xffffffffu, wait_phase(raw + st, (turns >> st) & 1, abort_flag, p.work_limit_ns));
                     if (!ok) break;
                     turns ^= 1u << st;
                     uint4 *to = reinterpret_cast<uint4 *>(smem + kOffKV + st * kBlock);
@@ -638,7 +639,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     w.group = static_cast<int>(index % p.groups);
                     if (!(p.B <= kSortable ? find_sorted(p, s, most, rank, w) : find_searched(p, rise, rank, w))) continue;
                 }
-                if (k >= kWorks) ok = __all_sync(0xffffffffu, wait_phase(w_free + k % kWorks, (k / kWorks - 1) & 1, abort_flag, p.limit_ns));
+                if (k >= kWorks) ok = __all_sync(0xffffffffu, wait_phase(w_free + k % kWorks, (k / kWorks - 1) & 1, abort_flag, p.work_limit_ns));
                 if (!ok) break;
                 __syncwarp();
                 if (lane == 0) {
@@ -800,7 +801,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 float before = kNegInf, keep = 1.0f, add = 0.0f;
                 if (p.prior && real) before = p.prior_lse[at] * 1.4426950408889634f;
                 const uint32_t turn = t == 0 ? had[0]++ : had[1]++;
-                ok = __all_sync(0xffffffffu, wait_phase(o_full + t, turn & 1, abort_flag, p.limit_ns));
+                ok = __all_sync(0xffffffffu, wait_phase(o_full + t, turn & 1, abort_flag, p.work_limit_ns));
                 if (!ok) break;
                 tc_fence_after();
                 const float *stat = stats + ((turn & 1) * kTiles + t) * 2 * kBlk + row;
@@ -942,6 +943,7 @@ cudaError_t launch_prompt_attention(const PromptArgs &a, cudaStream_t st) {
     p.lse = a.lse;
     p.dev_status = a.dev_status;
     p.limit_ns = a.wait_limit_ns;
+    p.work_limit_ns = a.wait_limit_ns * (static_cast<uint64_t>(a.T) / kBlk + 2);      // a work has so many blocks at most
     const bool few = a.T <= static_cast<int64_t>(kShortTokens) * a.B;
     const auto kernel = a.softcap == 0.0f        ? (few ? prompt_kernel<0, true> : prompt_kernel<0, false>)
                         : a.softcap <= kSmallCap ? (few ? prompt_kernel<1, true> : prompt_kernel<1, false>)

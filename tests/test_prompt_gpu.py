@@ -251,6 +251,25 @@ def test_equal_calls_give_equal_bits(V):
         assert torch.equal(first[0], again[0]) and torch.equal(first[1], again[1])
 
 
+def test_a_work_may_last_longer_than_a_wait(V):
+    """The limit is that of waits for a block; 100,001 tokens are 782 of them in a row."""
+    n = 100001
+    Q, K, Val, start = _inputs([n], 1, 1, seed=69)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    V.vca_set_wait_limit_ns(400_000)
+    try:
+        out, lse = V.prompt_attention(Q, K, Val, start, causal=False, dev_status=status)
+        torch.cuda.synchronize()
+    finally:
+        V.vca_set_wait_limit_ns(2_000_000_000)
+    assert int(status) == 0
+    at = torch.tensor([0, 1, 777, n // 2, n - 1], device="cuda")
+    s = Q[at, 0].double() @ K[:, 0].double().T / math.sqrt(128)
+    assert torch.allclose(lse[at, 0].double(), torch.logsumexp(s, -1), rtol=1e-5)
+    o = torch.softmax(s, -1) @ Val[:, 0].double()
+    assert float((out[at, 0].double() - o).norm() / o.norm()) <= 2.0 ** -7      # P's and O's rounding, 2^-8 each at most
+
+
 def test_captured_and_on_other_streams(V):
     """One graph replayed over new inputs and lengths, beside calls on another stream."""
     lens, other = [300, 40, 500], [100, 640, 100]
