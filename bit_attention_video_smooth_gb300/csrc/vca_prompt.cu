@@ -86,6 +86,7 @@ struct PromptParams {
     float *lse;
     int32_t *dev_status;
     uint64_t limit_ns, work_limit_ns;       // of a wait for a block, and of one for a whole work
+    uint64_t drain_ns;                      // of the last wait for copies and MMAs under way, which outlive no CTA
 };
 
 __device__ __forceinline__ void tma_load_3d(void *smem_dst, const void *tmap, uint64_t *bar, int x, int y, int z) {
@@ -431,9 +432,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (uint32_t j = i - issued; j != i; ++j) {
                     const uint32_t st = j % kStages;
                     if ((tails >> st) & 1u)
-                        drain_wait(raw + st, ((turns >> st) & 1u) ^ 1u, p.limit_ns);
+                        drain_wait(raw + st, ((turns >> st) & 1u) ^ 1u, p.drain_ns);
                     else
-                        drain_wait(full + st, (j / kStages) & 1, p.limit_ns);
+                        drain_wait(full + st, (j / kStages) & 1, p.drain_ns);
                 }
             }
         } else if (warp == 1) {
@@ -569,7 +570,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 seen[1] = sees[1];
             }
             commit(drain);
-            if (one) drain_wait(drain, 0, p.limit_ns);
+            if (one) drain_wait(drain, 0, p.drain_ns);
             __syncwarp();
         } else if (warp == 2) {
             // -------------------------------------------------------- queries, and rows of V behind a sequence
@@ -615,8 +616,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             // the last queries have landed before the CTA can exit
             if (lane == 0) {
-                if (queries0 >= 0) drain_wait(q_full, queries0 & 1, p.limit_ns);
-                if (queries1 >= 0) drain_wait(q_full + 1, queries1 & 1, p.limit_ns);
+                if (queries0 >= 0) drain_wait(q_full, queries0 & 1, p.drain_ns);
+                if (queries1 >= 0) drain_wait(q_full + 1, queries1 & 1, p.drain_ns);
             }
         } else {
             // -------------------------------------------------------- the CTA's works, ahead of all others
@@ -943,6 +944,7 @@ cudaError_t launch_prompt_attention(const PromptArgs &a, cudaStream_t st) {
     p.lse = a.lse;
     p.dev_status = a.dev_status;
     p.limit_ns = a.wait_limit_ns;
+    p.drain_ns = a.wait_limit_ns > 100000000u ? a.wait_limit_ns : 100000000u;
     p.work_limit_ns = a.wait_limit_ns * (static_cast<uint64_t>(a.T) / kBlk + 2);      // a work has so many blocks at most
     const bool few = a.T <= static_cast<int64_t>(kShortTokens) * a.B;
     const auto kernel = a.softcap == 0.0f        ? (few ? prompt_kernel<0, true> : prompt_kernel<0, false>)

@@ -270,6 +270,23 @@ def test_a_work_may_last_longer_than_a_wait(V):
     assert float((out[at, 0].double() - o).norm() / o.norm()) <= 2.0 ** -7      # P's and O's rounding, 2^-8 each at most
 
 
+def test_waits_that_run_out(V):
+    """A limit shorter than a copy from memory: the call says so (or was quick enough), and the next is right."""
+    lens = [3000, 70]
+    Q, K, Val, start = _inputs(lens, 4, 2, seed=77)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    for _ in range(3):
+        V.vca_set_wait_limit_ns(1000)
+        try:
+            V.prompt_attention(Q, K, Val, start, dev_status=status)
+            torch.cuda.synchronize()
+        finally:
+            V.vca_set_wait_limit_ns(2_000_000_000)
+        assert int(status) in (0, V.VCA_ERR_TIMEOUT)
+        status.zero_()
+        _check(V, lens, Q, K, Val, start)
+
+
 def test_captured_and_on_other_streams(V):
     """One graph replayed over new inputs and lengths, beside calls on another stream."""
     lens, other = [300, 40, 500], [100, 640, 100]
