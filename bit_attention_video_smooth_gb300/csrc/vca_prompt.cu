@@ -801,6 +801,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int64_t at = static_cast<int64_t>(w.row0 + token) * p.Hq + w.group * p.G + row_head;
                 float before = kNegInf, keep = 1.0f, add = 0.0f;
                 if (p.prior && real) before = p.prior_lse[at] * 1.4426950408889634f;
+                const bool joins = before != kNegInf;
+                // the prior's row, 32 channels ahead: from here on the tile's next products wait for O
+                const uint4 *prior = reinterpret_cast<const uint4 *>(p.prior + at * kD);
+                uint4 ahead[4] = {};
+                if (joins) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) ahead[e] = prior[e];
+                }
                 const uint32_t turn = t == 0 ? had[0]++ : had[1]++;
                 ok = __all_sync(0xffffffffu, wait_phase(o_full + t, turn & 1, abort_flag, p.work_limit_ns));
                 if (!ok) break;
@@ -808,7 +816,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const float *stat = stats + ((turn & 1) * kTiles + t) * 2 * kBlk + row;
                 float M = stat[0], l = stat[kBlk];
                 // joined with what came before: both sums to the larger maximum
-                const bool joins = before != kNegInf;
                 if (joins) {
                     const float m = M;
                     M = before != before ? before : fmaxf(m, before);
@@ -820,7 +827,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                 keep *= inv;
                 add *= inv;
                 const uint32_t tO = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + kTmemO + 128 * t;
-                const uint4 *prior = reinterpret_cast<const uint4 *>(p.prior + at * kD);
                 uint16_t *to = p.O + at * kD;
 #pragma unroll 1
                 for (int i = 0; i < 4; ++i) {
@@ -837,7 +843,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (joins) {
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
-                            const uint4 x = prior[4 * i + e];
+                            const uint4 x = ahead[e];
+                            if (i < 3) ahead[e] = prior[4 * i + 4 + e];
                             const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
                             for (int q = 0; q < 4; ++q) {
