@@ -220,6 +220,21 @@ def test_more_sequences_than_are_sorted(V, causal):
     _check(V, lens, *_inputs(lens, 2, 2, seed=64), causal=causal)
 
 
+def test_as_many_sequences_as_there_can_be(V):
+    """Single tokens: O is the value, lse the score (two of 128 exact products and their sum's rounding)."""
+    B = 65535
+    lens = torch.arange(B) % 3 != 1
+    T = int(lens.sum())
+    start = torch.nn.functional.pad(torch.cumsum(lens, 0), (1, 0)).to(torch.int32).cuda()
+    Q, K, Val = R.rows(T, 3, 78), R.rows(T, 1, 79), R.rows(T, 1, 80)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    out, lse = V.prompt_attention(Q, K, Val, start, dev_status=status)
+    assert int(status) == 0 and torch.equal(out, Val.expand(-1, 3, -1))
+    s = (Q.double() * K.double()).sum(-1) / math.sqrt(128)
+    mag = (Q.double() * K.double()).abs().sum(-1) / math.sqrt(128)
+    R.within(lse, s, 2.0 ** -16 * mag + 2.0 ** -20 * (1 + s.abs()), "lse")
+
+
 def test_outputs_at_any_place(V):
     """O need not be 32-byte aligned, lse may be left out."""
     lens = [140, 33]
