@@ -12,7 +12,7 @@
 //   0      TMA producer: K and V blocks alternate in a ring of four
 //   1      MMA issuer: PV of a block and QK of the next, tile by tile.  One CTA's MMAs
 //          run in the order of their issue, so QK may write the scores over the
-//          probabilities that the PV before it reads (110,000 launches of random shapes, three
+//          probabilities that the PV before it reads (300,000 launches of random shapes, three
 //          of each, gave equal bits).  The whole warp waits and one
 //          thread of it, elected, issues: then the operands are in uniform registers,
 //          and an MMA takes 10 to 20 cycles to issue (46 from a branch on the lane,
