@@ -20,7 +20,7 @@
 //   2      loads the queries; zeroes the rows of V behind the sequence's last token (they
 //          are another sequence's, and may hold NaN) and only then reports that block as full
 //   3      finds the CTA's works, some ahead of the others
-//   4-11   softmax, four warps a tile, a thread a row.  P goes over in halves of 64 keys.
+//   4-11   softmax, four warps a tile, a thread a row.  P goes over in two parts.
 //          The reference maximum moves only when a block's exceeds it by 8 (log2
 //          units); O is rescaled in TMEM then: S(j) full means that PV(j - 1) is done too
 //   12-15  epilogue: O / sum, joined with what came before, while the tiles go on to
@@ -34,7 +34,7 @@
 // ms, 1,737 TFLOP/s, 0.92 of cuBLAS's burst rate; 17,664 tokens both ways, 8 heads:
 // 770 us, 1,660 TFLOP/s (552 works on 152 SMs).  Short prompts are bound by what a
 // work costs beside its blocks, about 6,000 cycles: 32 of up to 1,000 tokens, 40 heads
-// over 8, 149 us, 860 TFLOP/s.  The code's size counts: all roles share the instruction
+// over 8, 139 us, 920 TFLOP/s.  The code's size counts: all roles share the instruction
 // caches, and a loop that no longer fits costs 5 to 15 %.
 // Measured and not kept: an issuer for each tile (both tiles' MMAs then mix and their
 // softmaxes fall together: 8.7 ms), a ring of three (7.2) or of five, which
@@ -42,6 +42,8 @@
 // at once before its stores (162 us for the 32 prompts against 155 at the time), the
 // queries prefetched into L2 (no change), a CTA for each work (886 us for 32 prompts of
 // 1,000 tokens, 315 now).
+#include <type_traits>
+
 #include "vca_attention_common.cuh"
 #include "vca_cache.cuh"
 
@@ -266,7 +268,7 @@ __device__ __forceinline__ void probabilities(const uint32_t (&X)[32], float c, 
 // for caps up to kSmallCap, whose scores are then right to 2e-5 (kCap = 1).  For
 // larger ones (kCap = 2) it is taken from |u| = kTanhNear on and the polynomial, with
 // its relative error, below, as in tanh_half; alone where all lanes are `near`.
-// 4 prompts of up to 2,900 tokens, 32 heads over 8, cap 30: 198 us, by kCap = 2 322.
+// 4 prompts of up to 2,900 tokens, 32 heads over 8, cap 30: 189 us, by kCap = 2 322.
 constexpr float kSmallCap = 64.0f;
 template <int kCap>
 __device__ __forceinline__ void capped_probabilities(const uint32_t (&X)[32], float c, float cap, float bias, bool near, int lim,
@@ -319,15 +321,20 @@ __device__ __forceinline__ void store32(uint16_t *to, const uint32_t *w) {
 }
 
 // kCap: 0 no cap, 1 a small one, 2 any.  kShort: the MMA issuer's code once for both
-// tiles, not twice.  It has to fit the instruction caches beside the softmax's, and a miss
-// leaves the tensor core idle; in long loops the addresses that are known then count more.
-// 32 prompts of 1,000 tokens, 40 heads over 8: 315 us once, 325 twice; one of 32,768: 6,644 and 6,328.
-constexpr int kShortTokens = 1024;      // of a prompt on average
+// tiles, not twice, and P handed over in 96 and 32 keys, not 64 and 64.  The code has to
+// fit the instruction caches beside the softmax's, and a miss leaves the tensor core idle;
+// in long loops the addresses that are known then count more, and the larger first part
+// costs what the smaller second one brings.  Without a cap (us, kShort and not; 40 heads over 8
+// causal, 8 heads both ways): 32 prompts of 1,000 tokens 315 and 335, 16 of 1,500 295 and
+// 308, 12 of 2,000 363 and 368, 8 of 2,500 355 and 355, one of 32,768 6,400 and 6,280; both ways 64
+// of 256 93 and 111, 32 of 1,200 147 and 145, one of 17,664 781 and 767.  With one kShort
+// is the faster or the same: 8,192 tokens, 32 heads over 8, cap 30, 596 and 622.
+constexpr int kShortKeys = 1024;      // that a work sees on average
 template <int kCap, bool kShort>
 __global__ void __launch_bounds__(kThreads, 1)
     prompt_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                   const __grid_constant__ CUtensorMap tmV, const PromptParams p) {
-    constexpr int kCopies = kShort ? 1 : kTiles;
+    constexpr int kCopies = kShort ? 1 : kTiles, kFirst = kShort ? 3 : 2;
     extern __shared__ unsigned char smem_raw[];
     unsigned char *smem = smem_raw + (0u - smem_u32(smem_raw)) % 1024u;
     uint64_t *full = reinterpret_cast<uint64_t *>(smem + kOffBar), *empty = full + kStages, *raw = empty + kStages;
@@ -459,15 +466,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                     tc_commit(s_full + t);
                 }
             };
-            auto pv = [&](int t, uint32_t st, int half, bool first) {      // of 64 keys
+            auto pv = [&](int t, uint32_t st, auto from, auto to, bool first) {      // of keys 16 from .. 16 to - 1
                 const uint64_t dv = sdesc_mn_sw128(base + kOffKV + st * kBlock, kPanel);
                 if (one) {
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        mma_f16_ts(tmem + kTmemO + 128 * t, tmem + kTmemS + 128 * t + 32 * half + 8 * i,
-                                   dv + (2048 >> 4) * (4 * half + i), make_idesc(128, 128, 1, 1, 0, 1), !first || i > 0);
+                    for (int i = decltype(from)::value; i < decltype(to)::value; ++i)
+                        mma_f16_ts(tmem + kTmemO + 128 * t, tmem + kTmemS + 128 * t + 8 * i, dv + (2048 >> 4) * i,
+                                   make_idesc(128, 128, 1, 1, 0, 1), !first || i > 0);
                 }
             };
+            using std::integral_constant;
             auto commit = [&](uint64_t *bar) {
                 if (one) tc_commit(bar);
             };
@@ -513,8 +521,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const int turn = static_cast<int>(of(blocks, t)) & 1;
                     blocks[0] += t == 0;
                     blocks[1] += t == 1;
-                    uint64_t *halves = p_full + 2 * t;
-                    const bool first = mbar_test_wait(halves, turn), second = mbar_test_wait(halves + 1, turn);
+                    uint64_t *parts = p_full + 2 * t;
+                    const bool first = mbar_test_wait(parts, turn), second = mbar_test_wait(parts + 1, turn);
                     if (!__all_sync(0xffffffffu, there)) {
                         if (!wait(full + sv, (iv / kStages) & 1)) return false;
                         if (!last && !wait(full + sk, (ik / kStages) & 1)) return false;
@@ -522,12 +530,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     // O's first product waits until the epilogue before has read it
                     if (j == 0 && of(had, t) > 0 && !wait(o_free + t, (of(had, t) - 1) & 1)) return false;
-                    if (!__all_sync(0xffffffffu, first) && !wait(halves, turn)) return false;
+                    if (!__all_sync(0xffffffffu, first) && !wait(parts, turn)) return false;
                     tc_fence_after();
-                    pv(t, sv, 0, j == 0);
-                    if (!__all_sync(0xffffffffu, second) && !wait(halves + 1, turn)) return false;
+                    pv(t, sv, integral_constant<int, 0>{}, integral_constant<int, 4>{}, j == 0);
+                    if (kFirst > 2 && left > 64) pv(t, sv, integral_constant<int, 4>{}, integral_constant<int, 2 * kFirst>{}, false);
+                    if (!__all_sync(0xffffffffu, second) && !wait(parts + 1, turn)) return false;
                     tc_fence_after();
-                    if (left > 64) pv(t, sv, 1, false);
+                    if (left > 64) pv(t, sv, integral_constant<int, 2 * kFirst>{}, integral_constant<int, 8>{}, false);
                     if (t == 1 || j * kBlk >= seen[1]) {
                         commit(empty + sv);
                         there = last || landed(j + 1);
@@ -737,10 +746,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                     }
                 }
-                auto hand_over = [&](int half) {
+                // P of the first kFirst times 32 keys, and of the others
+                auto hand_over = [&](int part) {
                     tc_fence_before();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(p_full + 2 * t + half);
+                    if (lane == 0) mbar_arrive(p_full + 2 * t + part);
                 };
                 if constexpr (kCap == 2) {
 #pragma unroll 1
@@ -751,25 +761,28 @@ __global__ void __launch_bounds__(kThreads, 1)
                         capped_probabilities<2>(X[0], c, p.cap_out, bias, (near >> i) & 1u, least < 32 * (i + 1) ? lim - 32 * i : 32, l2, W);
                         VCA_TMEM_ST16(tS + 16 * i, W);      // over scores already read
                         tmem_st_wait();
-                        if (i & 1) hand_over(i >> 1);
+                        if (i == kFirst - 1) hand_over(0);
+                        if (i == 3) hand_over(1);
                     }
-                    if (half_block) hand_over(1);
+                    if (half_block) {
+                        if (kFirst > 2) hand_over(0);
+                        hand_over(1);
+                    }
                 } else {
 #pragma unroll
-                    for (int half = 0; half < 2; ++half) {
-                        if (half == 0 || !half_block) {
-#pragma unroll
-                            for (int i = 2 * half; i < 2 * half + 2; ++i) {
-                                uint32_t W[16];
-                                if constexpr (kCap == 1)
-                                    capped_probabilities<1>(X[i], c, p.cap_out, bias, false, least < 32 * (i + 1) ? lim - 32 * i : 32, l2, W);
-                                else
-                                    probabilities(X[i], c, bias, l2, W);
-                                VCA_TMEM_ST16(tS + 16 * i, W);
-                            }
-                            tmem_st_wait();
+                    for (int i = 0; i < 4; ++i) {
+                        if (i < 2 || !half_block) {
+                            uint32_t W[16];
+                            if constexpr (kCap == 1)
+                                capped_probabilities<1>(X[i], c, p.cap_out, bias, false, least < 32 * (i + 1) ? lim - 32 * i : 32, l2, W);
+                            else
+                                probabilities(X[i], c, bias, l2, W);
+                            VCA_TMEM_ST16(tS + 16 * i, W);
                         }
-                        hand_over(half);
+                        if (i == kFirst - 1 || i == 3) {
+                            tmem_st_wait();
+                            hand_over(i == 3);
+                        }
                     }
                 }
             }
@@ -953,10 +966,10 @@ cudaError_t launch_prompt_attention(const PromptArgs &a, cudaStream_t st) {
     p.limit_ns = a.wait_limit_ns;
     p.drain_ns = a.wait_limit_ns > 100000000u ? a.wait_limit_ns : 100000000u;
     p.work_limit_ns = a.wait_limit_ns * (static_cast<uint64_t>(a.T) / kBlk + 2);      // a work has so many blocks at most
-    const bool few = a.T <= static_cast<int64_t>(kShortTokens) * a.B;
+    const bool few = a.T <= static_cast<int64_t>(a.causal ? 2 * kShortKeys : kShortKeys) * a.B;
     const auto kernel = a.softcap == 0.0f        ? (few ? prompt_kernel<0, true> : prompt_kernel<0, false>)
-                        : a.softcap <= kSmallCap ? (few ? prompt_kernel<1, true> : prompt_kernel<1, false>)
-                                                 : (few ? prompt_kernel<2, true> : prompt_kernel<2, false>);
+                        : a.softcap <= kSmallCap ? prompt_kernel<1, true>
+                                                 : prompt_kernel<2, true>;
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
     if (e != cudaSuccess) return e;
     const int64_t tiles = a.T / (2 * p.tokens) + (a.B <= kSortable && a.T < a.B ? a.T : a.B);
