@@ -916,6 +916,15 @@ bool make_kv_map(CUtensorMap *map, const CacheRows &x, int T, int H, bool *token
     return tok < head ? make_rows_map(map, x.p, T, tok, n, head, kBlk, 1) : make_rows_map(map, x.p, n, head, T, tok, 1, kBlk);
 }
 
+// The limit of a wait for a whole work, which has T / 128 + 2 blocks at most.
+constexpr uint64_t work_limit(uint64_t limit_ns, int T) {
+    const uint64_t blocks = static_cast<uint64_t>(T) / kBlk + 2;
+    return limit_ns > ~0ull / blocks ? ~0ull : limit_ns * blocks;
+}
+static_assert(work_limit(2000000000ull, 1000) == 18000000000ull && work_limit(1ull << 63, 256) == ~0ull &&
+                  work_limit(~0ull, 1) == ~0ull && work_limit(0, 0x7fffffff) == 0,
+              "a limit of any length");
+
 // Query heads of a tile: a divisor of G (they share a KV head).  More heads mean
 // fewer tokens, so fewer keys that only some rows see, and more of a short prompt's
 // rows in a tile; but whole tokens may not fill the tile's 128 rows.  The
@@ -965,7 +974,7 @@ cudaError_t launch_prompt_attention(const PromptArgs &a, cudaStream_t st) {
     p.dev_status = a.dev_status;
     p.limit_ns = a.wait_limit_ns;
     p.drain_ns = a.wait_limit_ns > 100000000u ? a.wait_limit_ns : 100000000u;
-    p.work_limit_ns = a.wait_limit_ns * (static_cast<uint64_t>(a.T) / kBlk + 2);      // a work has so many blocks at most
+    p.work_limit_ns = work_limit(a.wait_limit_ns, a.T);
     const bool few = a.T <= static_cast<int64_t>(a.causal ? 2 * kShortKeys : kShortKeys) * a.B;
     const auto kernel = a.softcap == 0.0f        ? (few ? prompt_kernel<0, true> : prompt_kernel<0, false>)
                         : a.softcap <= kSmallCap ? prompt_kernel<1, true>

@@ -399,7 +399,8 @@ int vca_cache_evict(const vca_cache *cache, float *weight, const int32_t *dst_ta
  * VCA_ERR_INVALID_ARG), or the free pages are too few (VCA_ERR_FULL), start becomes
  * 0 throughout, so that its rows belong to nobody, and all else stays as it was.
  * Sizes: B <= 65,535, pages*128 and cols*128 <= 2^31 - 1, T >= 0.  news is not len, and
- * start none of len, held and news (refused).
+ * start none of len, held and news (refused);
+ * no two of the arrays overlap but held and len.
  */
 int vca_cache_plan(int32_t *table, int32_t *len, int pages, int B, int cols, const int32_t *held, const int32_t *news,
                    int32_t *start, int32_t *slot, int32_t *position, int T, int32_t *dev_status, void *stream);
