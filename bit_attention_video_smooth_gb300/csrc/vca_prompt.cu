@@ -66,7 +66,8 @@ constexpr uint32_t kOffStat = kOffKV + kStages * kBlock;                  // fp3
 constexpr uint32_t kOffSort = kOffStat + 2 * kTiles * 2 * kBlk * 4;           // Sorted, of at most 256 sequences
 constexpr uint32_t kOffBar = kOffSort + 3 * 256 * 4;
 constexpr int kWorks = 3;                            // slots for what the CTA does now and next
-constexpr int kNumBars = 3 * kStages + 8 * kTiles + 2 * kWorks + 1;
+constexpr int kTurns = 2;                            // o_full barriers a tile, by turns of its works
+constexpr int kNumBars = 3 * kStages + (6 + kTurns) * kTiles + 2 * kWorks + 1;
 constexpr uint32_t kOffWork = (kOffBar + kNumBars * 8 + 15) / 16 * 16;
 constexpr uint32_t kOffMisc = kOffWork + kWorks * 16;
 constexpr uint32_t kSmem = kOffMisc + 16 + 1024;
@@ -339,7 +340,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     unsigned char *smem = smem_raw + (0u - smem_u32(smem_raw)) % 1024u;
     uint64_t *full = reinterpret_cast<uint64_t *>(smem + kOffBar), *empty = full + kStages, *raw = empty + kStages;
     uint64_t *q_full = raw + kStages, *q_free = q_full + kTiles, *s_full = q_free + kTiles, *p_full = s_full + kTiles;
-    uint64_t *o_full = p_full + 2 * kTiles, *o_free = o_full + kTiles, *w_full = o_free + kTiles, *w_free = w_full + kWorks;
+    uint64_t *o_full = p_full + 2 * kTiles, *o_free = o_full + kTurns * kTiles, *w_full = o_free + kTiles, *w_free = w_full + kWorks;
     uint64_t *drain = w_free + kWorks;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + kOffMisc);
     int *abort_flag = reinterpret_cast<int *>(smem + kOffMisc + 4);
@@ -360,7 +361,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(s_full + t, 1);
             mbar_init(p_full + 2 * t, 4);
             mbar_init(p_full + 2 * t + 1, 4);
-            mbar_init(o_full + t, 1 + 4);      // the last MMAs, and the softmax warps' statistics
+            for (int i = 0; i < kTurns; ++i) mbar_init(o_full + kTurns * t + i, 1 + 4);      // the last MMAs, and the softmax warps' statistics
             mbar_init(o_free + t, 4);
         }
         for (int i = 0; i < kWorks; ++i) {
@@ -545,7 +546,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         qk(t, sk, left <= kBlk + 64);
                         if (left <= 2 * kBlk) commit(q_free + t);
                     } else {
-                        commit(o_full + t);
+                        commit(o_full + kTurns * t + (of(had, t) & 1));
                     }
                     return true;
                 };
@@ -787,15 +788,20 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             }
             if (!ok) break;
-            // the row's maximum and sum go to the epilogue.  By turns: before the scores of
-            // the work after next come, the epilogue has read O and these
+            // The row's maximum and sum go to the epilogue, by turns: before the scores of
+            // the work after next come, the epilogue has read O and these.  The barrier takes turns
+            // too: the next work's scores wait for this one's probabilities of all four warps,
+            // but not for their statistics, and a warp that is a work ahead must not arrive in
+            // a slower one's place.  The scores of the work after next wait for probabilities
+            // that each warp hands over behind this arrival.
             float even, odd;
             upk2(l2, even, odd);
-            float *mine = stats + ((had++ & 1) * kTiles + t) * 2 * kBlk + row;
+            const uint32_t turn = had++ & 1;
+            float *mine = stats + (turn * kTiles + t) * 2 * kBlk + row;
             mine[0] = m;
             mine[kBlk] = __fadd_rn(even, odd);
             __syncwarp();
-            if (lane == 0) mbar_arrive(o_full + t);
+            if (lane == 0) mbar_arrive(o_full + kTurns * t + turn);
         }
     } else {
         // ------------------------------------------------------------ epilogue
@@ -823,7 +829,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int e = 0; e < 4; ++e) ahead[e] = prior[e];
                 }
                 const uint32_t turn = t == 0 ? had[0]++ : had[1]++;
-                ok = __all_sync(0xffffffffu, wait_phase(o_full + t, turn & 1, abort_flag, p.work_limit_ns));
+                ok = __all_sync(0xffffffffu, wait_phase(o_full + kTurns * t + (turn & 1), (turn >> 1) & 1, abort_flag, p.work_limit_ns));
                 if (!ok) break;
                 tc_fence_after();
                 const float *stat = stats + ((turn & 1) * kTiles + t) * 2 * kBlk + row;
