@@ -26,7 +26,9 @@
 //   12-15  epilogue: O / sum, joined with what came before, while the tiles go on to
 //          their next work
 // Every wait is bounded, as in vca_attention.cu; those that last as long as a work by as
-// many times the limit as it can have blocks.  Where one gives up all others do.
+// many times the limit as it can have blocks, and a tile's first one, which may
+// come after works without that tile, by as many as the works at hand can.  Where one gives
+// up all others do.
 //
 // What bounds it.  A block of both tiles is 2,048 cycles of the tensor core; it takes
 // 2,670, since a tile's chain (scores -> softmax 1,150 -> PV -> QK) is longer than the other
@@ -89,6 +91,7 @@ struct PromptParams {
     float *lse;
     int32_t *dev_status;
     uint64_t limit_ns, work_limit_ns;       // of a wait for a block, and of one for a whole work
+    uint64_t works_limit_ns;                // of one for the works that a CTA has at hand
     uint64_t drain_ns;                      // of the last wait for copies and MMAs under way, which outlive no CTA
 };
 
@@ -686,7 +689,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             float m = kNegInf;
             uint64_t l2 = 0;
             for (int b = 0; b < n_blocks; ++b) {
-                ok = __all_sync(0xffffffffu, wait_phase(s_full + t, blocks++ & 1, abort_flag, p.limit_ns));
+                // where the works before have no such tile, their other one's blocks come first
+                ok = __all_sync(0xffffffffu, wait_phase(s_full + t, blocks++ & 1, abort_flag, b == 0 ? p.works_limit_ns : p.limit_ns));
                 if (!ok) break;
                 tc_fence_after();
                 const bool edge = b >= whole, half_block = tile_sees - b * kBlk <= 64;
@@ -922,13 +926,13 @@ bool make_kv_map(CUtensorMap *map, const CacheRows &x, int T, int H, bool *token
     return tok < head ? make_rows_map(map, x.p, T, tok, n, head, kBlk, 1) : make_rows_map(map, x.p, n, head, T, tok, 1, kBlk);
 }
 
-// The limit of a wait for a whole work, which has T / 128 + 2 blocks at most.
-constexpr uint64_t work_limit(uint64_t limit_ns, int T) {
-    const uint64_t blocks = static_cast<uint64_t>(T) / kBlk + 2;
+// The limit of a wait for so many whole works, of T / 128 + 2 blocks each at most.
+constexpr uint64_t work_limit(uint64_t limit_ns, int T, int works = 1) {
+    const uint64_t blocks = works * (static_cast<uint64_t>(T) / kBlk + 2);
     return limit_ns > ~0ull / blocks ? ~0ull : limit_ns * blocks;
 }
-static_assert(work_limit(2000000000ull, 1000) == 18000000000ull && work_limit(1ull << 63, 256) == ~0ull &&
-                  work_limit(~0ull, 1) == ~0ull && work_limit(0, 0x7fffffff) == 0,
+static_assert(work_limit(2000000000ull, 1000) == 18000000000ull && work_limit(2000000000ull, 1000, 3) == 54000000000ull &&
+                  work_limit(1ull << 63, 256) == ~0ull && work_limit(~0ull, 1) == ~0ull && work_limit(0, 0x7fffffff) == 0,
               "a limit of any length");
 
 // Query heads of a tile: a divisor of G (they share a KV head).  More heads mean
@@ -981,6 +985,7 @@ cudaError_t launch_prompt_attention(const PromptArgs &a, cudaStream_t st) {
     p.limit_ns = a.wait_limit_ns;
     p.drain_ns = a.wait_limit_ns > 100000000u ? a.wait_limit_ns : 100000000u;
     p.work_limit_ns = work_limit(a.wait_limit_ns, a.T);
+    p.works_limit_ns = work_limit(a.wait_limit_ns, a.T, kWorks);
     const bool few = a.T <= static_cast<int64_t>(a.causal ? 2 * kShortKeys : kShortKeys) * a.B;
     const auto kernel = a.softcap == 0.0f        ? (few ? prompt_kernel<0, true> : prompt_kernel<0, false>)
                         : a.softcap <= kSmallCap ? prompt_kernel<1, true>
