@@ -1,4 +1,4 @@
-"""Prompt attention's bounded waits that are as long as whole works."""
+"""Prompt attention's bounded waits: those that are as long as whole works, and those that run out."""
 import math
 
 import pytest
@@ -9,7 +9,7 @@ import prompt_reference as R
 pytestmark = pytest.mark.gpu
 
 
-def _call(V, lens, limit_ns, causal, seed):
+def _call(V, lens, limit_ns, causal, seed, softcap=0.0):
     T = sum(lens)
     Q, K, Val = R.rows(T, 1, seed), R.rows(T, 1, seed + 1), R.rows(T, 1, seed + 2, outliers=False)
     status = torch.zeros(1, dtype=torch.int32, device="cuda")
@@ -17,7 +17,7 @@ def _call(V, lens, limit_ns, causal, seed):
     torch.cuda.synchronize()
     V.vca_set_wait_limit_ns(limit_ns)
     try:
-        out, lse = V.prompt_attention(Q, K, Val, start, causal=causal, dev_status=status)
+        out, lse = V.prompt_attention(Q, K, Val, start, causal=causal, softcap=softcap, dev_status=status)
         torch.cuda.synchronize()
     finally:
         V.vca_set_wait_limit_ns(2_000_000_000)
@@ -48,3 +48,15 @@ def test_a_tile_without_rows_waits_for_whole_works(V, lens, causal):
     *tensors, status = _call(V, lens, 400_000, causal, 81)
     assert status == 0
     _some_rows(lens, causal, *tensors)
+
+
+def test_waits_that_cannot_but_run_out(V):
+    """Works of 782 blocks and the smallest limit there is, 1 us a block.  The softmax of a small cap has three operations of
+    the special function unit a score, 32 a cycle at most: 3,072 cycles a block of both tiles, 1.48 us at 2,070 MHz.
+    So the epilogue's wait for a work, 0.784 ms of 1.16, runs out, and the call says so; the next one is right."""
+    lens = [100001, 70]
+    for _ in range(2):
+        assert _call(V, lens, 1000, False, 84, softcap=64.0)[-1] == V.VCA_ERR_TIMEOUT
+        *tensors, status = _call(V, lens, 2_000_000_000, False, 84)
+        assert status == 0
+        _some_rows(lens, False, *tensors)
