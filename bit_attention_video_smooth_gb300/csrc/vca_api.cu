@@ -37,10 +37,11 @@ bool cache_ok(const vca_cache *c, vca::CacheView *view) {
 bool rows_ok(const uint16_t *p, int64_t tok, int64_t head) {
     return p && aligned16(p) && (tok & 7) == 0 && (head & 7) == 0;
 }
-// Rows that tensor maps describe: tokens and heads are apart, or the heads (of keys and values) all one.
+// Rows that tensor maps describe: tokens and heads are apart, or the heads (of keys and values) all one.  The
+// distance of a single token or head is never used.
 bool mapped_rows_ok(const uint16_t *p, int64_t tok, int64_t head, int T, int H, bool one_head) {
     const int64_t most = static_cast<int64_t>(1) << 39;      // 2^40 bytes
-    return rows_ok(p, tok, head) && (T < 2 || (tok > 0 && tok < most)) &&
+    return rows_ok(p, T < 2 ? 0 : tok, H < 2 ? 0 : head) && (T < 2 || (tok > 0 && tok < most)) &&
            (H < 2 || (head > 0 && head < most) || (one_head && head == 0));
 }
 bool query_sizes_ok(int T, int Hq, int H) {
