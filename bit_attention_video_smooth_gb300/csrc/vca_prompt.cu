@@ -21,8 +21,10 @@
 //          are another sequence's, and may hold NaN) and only then reports that block as full
 //   3      finds the CTA's works, some ahead of the others
 //   4-11   softmax, four warps a tile, a thread a row.  P goes over in two parts.
-//          The reference maximum moves only when a block's exceeds it by 8 (log2
-//          units); O is rescaled in TMEM then: S(j) full means that PV(j - 1) is done too
+//          The reference lies 8 (log2 units) above the maximum when it is set, and moves only
+//          when a block's maximum exceeds it; O is rescaled in TMEM then: S(j) full
+//          means that PV(j - 1) is done too.  So no probability is above 1, and O
+//          is finite where the sums of a sequence's values' magnitudes are
 //   12-15  epilogue: O / sum, joined with what came before, while the tiles go on to
 //          their next work
 // Every wait is bounded, as in vca_attention.cu; those that last as long as a work by as
@@ -67,6 +69,7 @@ constexpr uint32_t kOffKV = kOffQ + kTiles * kBlock;
 constexpr uint32_t kOffStat = kOffKV + kStages * kBlock;                  // fp32 [2][tile][max, sum][128], by turns
 constexpr uint32_t kOffSort = kOffStat + 2 * kTiles * 2 * kBlk * 4;           // Sorted, of at most 256 sequences
 constexpr uint32_t kOffBar = kOffSort + 3 * 256 * 4;
+constexpr float kAbove = 256.0f;                     // 2^kLazyTau
 constexpr int kWorks = 3;                            // slots for what the CTA does now and next
 constexpr int kTurns = 2;                            // o_full barriers a tile, by turns of its works
 constexpr int kNumBars = 3 * kStages + (6 + kTurns) * kTiles + 2 * kWorks + 1;
@@ -686,7 +689,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int whole = __reduce_min_sync(0xffffffffu, seen) / kBlk;      // blocks that every row of the warp sees all of
             const float c = fmaxf(kCap ? p.cap_in : p.scale_log2, 0x1p-149f);      // above 0, so that -inf stays -inf
             float bias = 0.0f;
-            float m = kNegInf;
+            float m = kNegInf;      // the reference
             uint64_t l2 = 0;
             for (int b = 0; b < n_blocks; ++b) {
                 // where the works before have no such tile, their other one's blocks come first
@@ -730,14 +733,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                     bm = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c;
                     if constexpr (kCap == 1) bm = capped(bm, p.cap_out);
                 }
-                const bool rises = real && bm > __fadd_rn(m, kLazyTau);      // a row that is none may hold anything
+                const bool rises = real && bm > m;      // a row that is none may hold anything
                 if (__any_sync(0xffffffffu, rises)) {
                     float alpha = 1.0f;
                     if (rises) {
-                        alpha = ex2_approx(__fsub_rn(m, bm));
+                        bias = -__fadd_rn(bm, kLazyTau);
+                        alpha = ex2_approx(__fadd_rn(m, bias));
                         l2 = mul2(l2, pk2(__float_as_uint(alpha), __float_as_uint(alpha)));
-                        m = bm;
-                        bias = -m;
+                        m = -bias;
                     }
                     if (b > 0) {
 #pragma unroll 1
@@ -802,8 +805,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             upk2(l2, even, odd);
             const uint32_t turn = had++ & 1;
             float *mine = stats + (turn * kTiles + t) * 2 * kBlk + row;
-            mine[0] = m;
-            mine[kBlk] = __fadd_rn(even, odd);
+            mine[0] = __fsub_rn(m, kLazyTau);      // as if the reference were the maximum that set it,
+            mine[kBlk] = __fmul_rn(__fadd_rn(even, odd), kAbove);      // which keeps the sum near 1 and lse its bits
             __syncwarp();
             if (lane == 0) mbar_arrive(o_full + kTurns * t + turn);
         }
@@ -847,7 +850,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     l = __fadd_rn(__fmul_rn(l, keep), add);
                 }
                 const float inv = l > 0.0f || l != l ? 1.0f / l : 0.0f;
-                keep *= inv;
+                keep *= inv * kAbove;
                 add *= inv;
                 const uint32_t tO = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + kTmemO + 128 * t;
                 uint16_t *to = p.O + at * kD;

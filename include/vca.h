@@ -436,7 +436,8 @@ int vca_cache_fresh(const int32_t *table, const int32_t *len, int pages, int B, 
  * between tokens where T > 1 and between heads where there are several; 0 between
  * the heads of K or V makes all of them one.  B*H <= 65,535, T*Hq <= 2^31 - 1.
  * The products of bf16 values are exact, sums and statistics fp32; the
- * probabilities enter the second product as bf16 (2^-8 relative).  A NaN or an infinity
+ * probabilities enter the second product as bf16 (2^-8 relative); the magnitudes of a
+ * sequence's values have to sum up to less than 2^128 a channel.  A NaN or an infinity
  * among the values of a sequence may reach every row of that sequence, one in a
  * key or query only the rows that see it.  Equal calls give equal bits.  No workspace.
  */
