@@ -10,13 +10,16 @@
 // one tile's softmax runs the tensor core works for the other.  TMEM: S0, S1, O0, O1, all of it.
 // Warps:
 //   0      TMA producer: K and V blocks alternate in a ring of four
-//   1      MMA issuer: PV of a block and QK of the next, tile by tile.  One CTA's MMAs
-//          run in the order of their issue, so QK may write the scores over the
-//          probabilities that the PV before it reads (300,000 launches of random shapes, three
-//          of each, gave equal bits).  The whole warp waits and one
-//          thread of it, elected, issues: then the operands are in uniform registers,
-//          and an MMA takes 10 to 20 cycles to issue (46 from a branch on the lane,
-//          which the softmax's warps beside it make 95: 1,389 TFLOP/s against 1,605)
+//   1      MMA issuer: PV of a block and QK of the next, tile by tile.  QK writes the scores
+//          over the probabilities that the PV before it reads.  That this needs no wait
+//          between them is observed, not guaranteed: PTX promises the order of issue for
+//          MMAs of one accumulator and shape, and these have two accumulators.  One thread's
+//          MMAs have run in their order in all that was measured (300,000 launches of random
+//          shapes, three of each, gave equal bits), and TMEM has no columns left for P.
+//          The whole warp waits and one thread of it, elected, issues: then the operands
+//          are in uniform registers, and an MMA takes 10.5 cycles to issue with A in TMEM
+//          and 40 with A in shared memory (46 from a branch on the lane, which the
+//          softmax's warps beside it make 95: 1,389 TFLOP/s against 1,605)
 //   2      loads the queries; zeroes the rows of V behind the sequence's last token (they
 //          are another sequence's, and may hold NaN) and only then reports that block as full
 //   3      finds the CTA's works, some ahead of the others
@@ -34,18 +37,19 @@
 //
 // What bounds it.  A block of both tiles is 2,048 cycles of the tensor core; it takes
 // 2,670, since a tile's chain (scores -> softmax 1,150 -> PV -> QK) is longer than the other
-// tile's 1,024 cycles of MMAs.  One prompt of 32,768 tokens, causal, 40 heads over 8: 6.33
-// ms, 1,737 TFLOP/s, 0.92 of cuBLAS's burst rate; 17,664 tokens both ways, 8 heads:
-// 770 us, 1,660 TFLOP/s (552 works on 152 SMs).  Short prompts are bound by what a
-// work costs beside its blocks, about 6,000 cycles: 32 of up to 1,000 tokens, 40 heads
-// over 8, 139 us, 920 TFLOP/s.  The code's size counts: all roles share the instruction
-// caches, and a loop that no longer fits costs 5 to 15 %.
-// Measured and not kept: an issuer for each tile (both tiles' MMAs then mix and their
-// softmaxes fall together: 8.7 ms), a ring of three (7.2) or of five, which
-// leaves no room for the statistics (6.24 against 6.39 at the time), O read into registers
-// at once before its stores (162 us for the 32 prompts against 155 at the time), the
-// queries prefetched into L2 (no change), a CTA for each work (886 us for 32 prompts of
-// 1,000 tokens, 315 now).
+// tile's 1,024 cycles of MMAs.  One prompt of 32,768 tokens, causal, 40 heads over 8, other
+// inputs in every call: 6.5 ms, 1,690 TFLOP/s, 0.90 of cuBLAS's burst rate; 17,664 tokens
+// both ways, 8 heads: 800 us, 1,590 TFLOP/s (552 works on 152 SMs).  Short prompts are
+// bound by what a work costs beside its blocks, about 6,000 cycles: 32 of up to 1,000
+// tokens, 40 heads over 8, 147 us, 870 TFLOP/s.  The code's size counts: all roles share
+// the instruction caches, and a loop that no longer fits costs 5 to 15 %.
+// The figures from here on are of loops over equal inputs, which are 3 to 5 % faster
+// (6.3 ms, 770 us, 139 us).  Measured and not kept: an issuer for each tile (both
+// tiles' MMAs then mix and their softmaxes fall together: 8.7 ms), a ring of three
+// (7.2) or of five, which leaves no room for the statistics (6.24 against 6.39 at the
+// time), O read into registers at once before its stores (162 us for the 32 prompts
+// against 155 at the time), the queries prefetched into L2 (no change), a CTA for each
+// work (886 us for 32 prompts of 1,000 tokens, 315 now).
 #include <type_traits>
 
 #include "vca_attention_common.cuh"
@@ -114,7 +118,8 @@ __device__ __forceinline__ void tma_load_3d(void *smem_dst, const void *tmap, ui
         : "r"(taddr))
 
 // mbar_wait in less code: the kernel's loops have to fit the instruction caches, and
-// a test suspends the thread for a thousand cycles anyway.
+// a test suspends the thread for up to 7,760 cycles (3.9 us, measured) anyway.  So a wait
+// gives up after two tests at the earliest, whatever its limit.
 __device__ __forceinline__ bool wait_phase(uint64_t *bar, uint32_t parity, int *abort, uint64_t limit_ns) {
     if (mbar_try_wait(bar, parity)) return true;
     const uint64_t t0 = globaltimer_ns();
@@ -147,6 +152,8 @@ __device__ __forceinline__ int tiles_of(const PromptParams &p, int n) { return (
 // causal tile's number grows with its place in the sequence, another's is the
 // sequence's.  The CTAs then take turns, there and back, and have done about the same at the
 // end.  A warp's work; the sequences' first tokens, tokens and tiles in shared memory.
+// Many short sequences are slower so than searched: 256 of 100 tokens, 40 heads over 8, take
+// 130 us, 257 of them, which are searched, 105.
 constexpr int kSortable = 256;
 struct Sorted {
     int lo[kSortable], n[kSortable], q[kSortable];
@@ -270,12 +277,13 @@ __device__ __forceinline__ void probabilities(const uint32_t (&X)[32], float c, 
     }
 }
 
-// The same of capped scores, p = 2^(cap tanh_half(S c) + bias), and 0 from column
-// `lim` on.  tanh_half(u) = 1 - 2 / (1 + 2^u) has an absolute error of 2^-22: enough
-// for caps up to kSmallCap, whose scores are then right to 2e-5 (kCap = 1).  For
-// larger ones (kCap = 2) it is taken from |u| = kTanhNear on and the polynomial, with
-// its relative error, below, as in tanh_half; alone where all lanes are `near`.
-// 4 prompts of up to 2,900 tokens, 32 heads over 8, cap 30: 189 us, by kCap = 2 322.
+// The same of capped scores, p = 2^(cap tanh_half(S c) + bias), and 0 from column `lim`
+// on.  tanh_half(u) = 1 - 2 / (1 + 2^u) has an absolute error, and with its roundings a
+// score is off by up to 2^-20 of the cap, however small the score is itself: 6e-5 at
+// kSmallCap, up to which this is all (kCap = 1).  For larger ones (kCap = 2) it is
+// taken from |u| = kTanhNear on and the polynomial, with its relative error, below, as
+// in tanh_half; alone where all lanes are `near`. 4 prompts of up to 2,900 tokens, 32
+// heads over 8, cap 30: 189 us, by kCap = 2 322.
 constexpr float kSmallCap = 64.0f;
 template <int kCap>
 __device__ __forceinline__ void capped_probabilities(const uint32_t (&X)[32], float c, float cap, float bias, bool near, int lim,

@@ -392,7 +392,10 @@ int vca_cache_evict(const vca_cache *cache, float *weight, const int32_t *dst_ta
  *           behind start[B] stay as they are
  * Free is a page that no live table entry names, live being the columns below
  * ceil(held / 128): no list is kept, a length of 0 gives a sequence's pages back, and
- * a page that sequences share is free when the last of them is gone.  A live
+ * a page that sequences share is free when the last of them is gone.  Only full
+ * pages may be shared by sequences with news: new tokens of two that share a partly
+ * filled last page get the same slots, which is not looked for (no page may be
+ * written twice in a call); copy such a page first.  A live
  * entry outside 0 .. pages - 1 names none; it is reported where pages are given out.
  * A plan is made whole or not at all: if held or news is negative or their sum
  * above cols*128 anywhere, or the news sum up to more than T (dev_status =
@@ -439,7 +442,12 @@ int vca_cache_fresh(const int32_t *table, const int32_t *len, int pages, int B, 
  * probabilities enter the second product as bf16 (2^-8 relative); the magnitudes of a
  * sequence's values have to sum up to less than 2^128 a channel.  A NaN or an infinity
  * among the values of a sequence may reach every row of that sequence, one in a
- * key or query only the rows that see it.  Equal calls give equal bits.  No workspace.
+ * key or query only the rows that see it.  A cap up to 64 adds an error of up to 2^-20 of
+ * the cap to a score; a larger one, and any in vca_cache_attention, 2^-20 of the score.
+ * Equal calls give equal bits.  No workspace.
+ * The kernel's form is chosen on the host for the whole call, by T / B: with many
+ * sequences without rows, or room for many more rows than there are, it is right and
+ * up to a few percent slower (a prompt of 32,768 tokens: 5 and 2 %).
  */
 int vca_prompt_attention(const uint16_t *Q, int64_t q_token, int64_t q_head, const uint16_t *K, int64_t k_token,
                          int64_t k_head, const uint16_t *V, int64_t v_token, int64_t v_head, const int32_t *start, int B,
