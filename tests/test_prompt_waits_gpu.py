@@ -52,7 +52,7 @@ def test_a_tile_without_rows_waits_for_whole_works(V, lens, causal):
 
 def test_waits_that_cannot_but_run_out(V):
     """Works of 782 blocks and the smallest limit there is, 1 us a block.  The softmax of a small cap has three operations of
-    the special function unit a score, 32 a cycle at most: 3,072 cycles a block of both tiles, 1.48 us at 2,070 MHz.
+    the special function unit a score, 32 a cycle at most: 1.48 us a block of both tiles (256 x 128 scores) at 2,070 MHz.
     So the epilogue's wait for a work, 0.784 ms of 1.16, runs out, and the call says so; the next one is right."""
     lens = [100001, 70]
     for _ in range(2):
